@@ -1,6 +1,8 @@
 /*
  * zeroadam.h -- C ABI of libzeroadam.so: the ZeRO stage-1/2 mixed-precision
- * Adam step and the ZeRO-3 unit gather on one GB300 (sm_103a).
+ * Adam step and the ZeRO-3 unit gather on one GB300 (sm_103a), and the rest of
+ * a training step around them: a unit's linear maps forward and backward, the
+ * global gradient norm, and AdamW over a list of tensors.
  *
  * The method is the one in "ZeRO and FSDP: partitioning the optimizer states,
  * the gradients and the parameters" (AI infra handbooks): the parameters are
@@ -21,9 +23,8 @@
  *     between calls is a per-device status word that a kernel sets only if one
  *     of its bounded waits gives up (see zero_device_status).  Faults inside a
  *     launched kernel surface, as for any CUDA work, at the caller's next sync.
- *   - Tracing: zero_adam_step, zero_adam_step_range, zero3_unit_gather,
- *     zero3_unit_gather_rows, zero3_unit_step and zero_device_status each
- *     open an NVTX range
+ *   - Tracing: every call that launches work, and zero_device_status,
+ *     opens an NVTX range
  *     named after the function for the duration of the call (visible to
  *     Nsight tools and any NVTX injection library; free when none is
  *     attached).
@@ -71,6 +72,7 @@ extern "C" {
 #define ZERO_E_SHAPE (-14)  /* zero3_unit_gather_rows: bad tensor count or shape    */
 #define ZERO_E_TIMEOUT (-15) /* a kernel gave up a bounded wait (zero_device_status) */
 #define ZERO_E_HOOK (-16)    /* a test hook was called without ZEROADAM_TEST_HOOKS=1 */
+#define ZERO_E_WORKSPACE (-17) /* the workspace is NULL, misaligned or too small     */
 
 /* Largest tensor count of one zero3_unit_gather_rows unit. */
 #define ZERO_MAX_UNIT_TENSORS 256
@@ -88,10 +90,22 @@ extern "C" {
 #define ZERO_GRAD_LAYOUT_MASK 0x0f
 #define ZERO_GRAD_F32 0x10 /* flag: gradient buffers hold fp32 (default: bf16) */
 #define ZERO_ACC_BF16 0x20 /* flag: round the running sum over ranks to bf16 after every addition */
+#define ZERO_GRAD_ACCUMULATE 0x40 /* zero_linear_backward: add to dw and dbias instead of writing them */
 
 /* param_layout */
 #define ZERO_PARAM_FULL 0  /* param_bf16: the whole flat parameter buffer (>= numel elements) */
 #define ZERO_PARAM_SHARD 1 /* param_bf16: this rank's shard only (shard elements; ZeRO-3); single rank only */
+
+/* act: the activation of a linear map's epilogue */
+#define ZERO_ACT_NONE 0
+#define ZERO_ACT_RELU 1 /* max(z, 0); its derivative at 0 is 0                          */
+#define ZERO_ACT_GELU 2 /* z/2 (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3))), the tanh form */
+#define ZERO_ACT_SILU 3 /* z / (1 + exp(-z))                                            */
+
+/* zero_adamw_step */
+#define ZERO_STATE_8BIT 0x80   /* flag: m and v are held as 8-bit codes with block scales */
+#define ZERO_MOMENT_BLOCK 256  /* elements that share one scale of an 8-bit moment        */
+#define ZERO_MAX_LIST 65536    /* largest number of tensors of one list                   */
 
 /* ------------------------------------------------------------------- plan */
 
@@ -276,6 +290,181 @@ int zero3_unit_step(const zero_plan_t* unit_plan, int32_t rank, const void* cons
                     void* full_bf16, const void* const* grad_ptrs, int32_t grad_layout,
                     float* master, float* m, float* v, void* param_bf16, int32_t param_layout,
                     double lr, double beta1, double beta2, double eps, int64_t t, void* stream);
+
+/* ------------------------------------------------------------- linear maps */
+
+/*
+ * Sizes of one linear map y = x W^T of `rows` tokens from `in` to `out`
+ * features, and the row pitches (leading dimensions, in elements) of its
+ * matrices.  Every matrix is row-major with unit column stride: x and dx are
+ * rows x in, W and dw out x in, y, dy, residual and pre rows x out, pre_in
+ * rows x in.  A pitch is at least the matrix's width; pitches of matrices that
+ * a call does not use are not read.  1 <= in, out; 0 <= rows; in, out and
+ * rows below 2^31.
+ */
+typedef struct {
+  int64_t rows, in, out;
+  int64_t ldx, ldw, ldy;      /* x, W, y (forward) or dy (backward)  */
+  int64_t ldr, ldp;           /* residual, pre                       */
+  int64_t ldpi, lddx, lddw;   /* pre_in, dx, dw                      */
+} zero_linear_t;
+
+/*
+ * Forward: with z = x W^T + bias (fp32 sums),
+ *   y   = bf16(act(z) + residual),   pre = bf16(z).
+ * A unit's maps on its gathered weights ("ZeRO-3 and FSDP": the complete
+ * parameters are used in the forward pass, then freed).  The activation and
+ * the residual take z in fp32; each output is rounded to bf16 once.
+ *
+ *   x, w        bf16, read.
+ *   bias        bf16, `out` elements, or NULL.
+ *   act         ZERO_ACT_*.
+ *   residual    bf16, or NULL.  It may be y itself (same pitch): in place.
+ *   pre         bf16, written, or NULL: what the backward pass takes.
+ *   y           bf16, written.
+ *   workspace   device memory of zero_linear_workspace(shape, 0) bytes,
+ *               16-byte aligned (NULL where that is 0), free again once the
+ *               call's work has run.
+ * rows = 0 is valid and launches nothing (matrices of no rows may be NULL).  Any alignment of 2 bytes and any
+ * pitch is taken; matrices whose base is 16-byte aligned and whose pitch is a
+ * multiple of 8 are read in place by the TMA engine, others are laid out anew
+ * in the workspace first.  Results do not depend on the run: every sum has a
+ * fixed order for given sizes.
+ * Errors: ZERO_E_NULLPTR, ZERO_E_SHAPE, ZERO_E_LAYOUT (unknown act),
+ * ZERO_E_ALIGN, ZERO_E_ALIAS (y or pre overlaps another matrix),
+ * ZERO_E_WORKSPACE, ZERO_E_LAUNCH, ZERO_E_DEVICE.
+ */
+int zero_linear_forward(const zero_linear_t* shape, const void* x, const void* w,
+                        const void* bias, int32_t act, const void* residual, void* pre, void* y,
+                        void* workspace, int64_t workspace_bytes, void* stream);
+
+/*
+ * Backward of y = act(x W^T + bias): with dz = dy * act'(pre),
+ *   dx    = bf16((dz W) * act_in'(pre_in)),
+ *   dw    = dz^T x          (added to dw with ZERO_GRAD_ACCUMULATE),
+ *   dbias = sum over rows of dz (likewise),
+ * in fp32 sums.  act_in / pre_in are the activation that made x, and what it
+ * was given: dx is then the gradient of the map before it, ready to be that
+ * map's dy with act NONE.  A residual's gradient is dy itself.
+ *
+ *   dy          bf16, read.
+ *   act, pre    the map's activation and the `pre` its forward wrote (NULL
+ *               with ZERO_ACT_NONE).  With an activation dz is rounded to
+ *               bf16 before the products (the tensor cores' operand type);
+ *               dbias sums it unrounded.
+ *   act_in, pre_in  as above; ZERO_ACT_NONE and NULL to leave dx as it is.
+ *   x, w        bf16, read (x only for dw, w only for dx; else may be NULL).
+ *   dx, dw, dbias  each written, or NULL to skip it.  dw and dbias are bf16,
+ *               or fp32 with ZERO_GRAD_F32: a tensor's place in a rank's flat
+ *               gradient buffer can be passed as it is.
+ *   flags       ZERO_GRAD_F32, ZERO_GRAD_ACCUMULATE.
+ *   workspace   zero_linear_workspace(shape, 1) bytes.
+ * rows = 0 writes zeros to dw and dbias (or leaves them, accumulating).
+ * Errors: as zero_linear_forward (ZERO_E_LAYOUT also for unknown flags).
+ */
+int zero_linear_backward(const zero_linear_t* shape, const void* dy, const void* x, const void* w,
+                         int32_t act, const void* pre, int32_t act_in, const void* pre_in,
+                         void* dx, void* dw, void* dbias, int32_t flags, void* workspace,
+                         int64_t workspace_bytes, void* stream);
+
+/* Bytes of workspace that suffice for zero_linear_forward (backward = 0) or
+ * zero_linear_backward (1) of this shape, whatever its matrices' alignment;
+ * negative: the ZERO_E_* code of a bad shape.  Host only. */
+int64_t zero_linear_workspace(const zero_linear_t* shape, int32_t backward);
+
+/* ------------------------------------------------- AdamW over a list of tensors */
+
+/*
+ * Global norm of a list of gradients, and the factor that clips it:
+ *   out[0] = sqrt(sum over tensors and elements of g^2)
+ *   out[1] = min(1, max_norm / (out[0] + 1e-6))   (NaN if the norm is NaN)
+ * Squares and each thread's run of up to 64 of them are summed in fp32, all
+ * else in fp64; the order is fixed, so equal inputs give equal bits.
+ *
+ *   grads, numels  host arrays of ntensors device pointers and sizes (>= 0).
+ *   flags       ZERO_GRAD_F32 for fp32 gradients (default bf16).
+ *   out         device, two fp32.
+ *   workspace   device memory of zero_grad_norm_workspace() bytes, 16-byte
+ *               aligned.  Set to zero once before its first use; every call
+ *               leaves it ready for the next.  One call at a time may use it.
+ * Errors: ZERO_E_SHAPE (ntensors not in [0, ZERO_MAX_LIST], or a size < 0),
+ * ZERO_E_NULLPTR, ZERO_E_LAYOUT, ZERO_E_ALIGN, ZERO_E_HPARAM (max_norm not
+ * finite or < 0), ZERO_E_WORKSPACE, ZERO_E_LAUNCH, ZERO_E_DEVICE.
+ */
+int zero_grad_norm(int32_t ntensors, const void* const* grads, const int64_t* numels,
+                   int32_t flags, double max_norm, float* out, void* workspace,
+                   int64_t workspace_bytes, void* stream);
+int64_t zero_grad_norm_workspace(void);
+
+/* One tensor of an AdamW list.  m_scale and v_scale are used with
+ * ZERO_STATE_8BIT only (ceil(numel / ZERO_MOMENT_BLOCK) fp32 each). */
+typedef struct {
+  int64_t numel;        /* >= 0                                              */
+  const void* grad;     /* bf16, or fp32 with ZERO_GRAD_F32                   */
+  float* master;        /* fp32 weights, in place                            */
+  void* param_bf16;     /* bf16 copy of the new weights, written; or NULL     */
+  void* m;              /* fp32, or 8-bit codes; in place                    */
+  void* v;
+  float* m_scale;
+  float* v_scale;
+  double weight_decay;  /* >= 0, finite                                      */
+} zero_adamw_tensor_t;
+
+/*
+ * One AdamW step (Adam with bias correction and decoupled weight decay) over a
+ * list of tensors: the optimizer of FSDP2-style shards, where a rank holds a
+ * block of rows of every tensor instead of a slice of one flat vector.  With
+ * c = *grad_scale (1 if NULL), for every element:
+ *   g = c * grad
+ *   m = m*b1 + (1-b1)*g ;  v = v*b2 + ((1-b2)*g)*g
+ *   w = w*(1 - lr*weight_decay) - (lr/(1-b1^t)) * m / (sqrt(v)/sqrt(1-b2^t) + eps)
+ *   p = bf16 round-to-nearest-even of w
+ * m and v are computed in binary32, one rounding per operation, exactly as
+ * zero_adam_step does; the update of w takes them before they are encoded, and
+ * its square root and quotient are good to a few ulp of binary32.
+ *
+ * 8-bit moments (ZERO_STATE_8BIT): a tensor's elements are cut into blocks of
+ * ZERO_MOMENT_BLOCK from its first one.  A block's scale is the power of two
+ * 2^e of its largest magnitude after that is rounded up to 4 significant bits
+ * (e in [-126, 126]).  Codes keep 3 mantissa bits with gradual underflow, f
+ * the low 3 bits and x the exponent bits above them:
+ *   |value| = scale * (1 + f/8) 2^(x-top), or scale * f/8 2^(1-top) for x = 0;
+ *   m: sign in bit 7, 4 exponent bits (top = 15); v: 5 (top = 31), no sign.
+ * Rounding is stochastic: 16 random bits r of each element are added to the
+ * dropped 20 (as 16 r + 8) before the cut, so the expected value is the moment
+ * itself; a moving average that moves less than half a step at a time would
+ * stand still under rounding to nearest.  The scales are powers of two so that
+ * a value that has not changed is held exactly.  r comes from a hash: with
+ * h the 32-bit permuted congruential generator's step, k = h(h(seed) + index
+ * in the list) and u = h(k + element), m takes u >> 16 and v takes u & 0xffff
+ * (element counted within the tensor; beyond 2^32 of them k adds
+ * 0x9E3779B9 per 2^32).  A new seed every step; the same seed, the same bits.
+ * A block with an infinity or NaN gets the scale NaN and codes 0: it reads as
+ * NaN from then on.  All-zero codes and scales are zero moments.
+ *
+ *   tensors     host array, read before the call returns.
+ *   flags       ZERO_GRAD_F32, ZERO_STATE_8BIT.
+ *   grad_scale  device fp32 (zero_grad_norm's out + 1, say), or NULL.
+ *   seed        of the rounding; unused with fp32 moments.
+ * Lists of any length take one launch per 384 tensors.  Tensors of no elements
+ * are skipped.  Any alignment of the element type is taken; tensors whose
+ * buffers are all 16-byte aligned (8 for 8-bit codes) go in 16-byte accesses.
+ * Errors: ZERO_E_SHAPE, ZERO_E_NULLPTR, ZERO_E_LAYOUT (unknown flags),
+ * ZERO_E_HPARAM, ZERO_E_STEP, ZERO_E_ALIGN, ZERO_E_ALIAS (within a tensor:
+ * master, m, v, param, grad or scales overlap), ZERO_E_LAUNCH, ZERO_E_DEVICE.
+ */
+int zero_adamw_step(int32_t ntensors, const zero_adamw_tensor_t* tensors, int32_t flags,
+                    double lr, double beta1, double beta2, double eps, int64_t t,
+                    const float* grad_scale, uint32_t seed, void* stream);
+
+/*
+ * The values of 8-bit moments, as fp32 (for a checkpoint, or to go on with
+ * fp32 moments): m_out[i] and v_out[i] are device buffers of tensors[i].numel
+ * fp32, written; either array may be NULL.  Only numel, m, v and the scales of
+ * each tensor are read.  Errors: as zero_adamw_step.
+ */
+int zero_adamw_state_f32(int32_t ntensors, const zero_adamw_tensor_t* tensors,
+                         float* const* m_out, float* const* v_out, void* stream);
 
 /* ------------------------------------------------------------------ misc */
 

@@ -1,0 +1,292 @@
+"""Linear maps, forward and backward, on the GPU against products in 64 bits."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import train_oracle as o
+import zero_partitioned_mixed_adam_gb300 as za
+
+pytestmark = pytest.mark.gpu
+
+BF, F32, F64 = torch.bfloat16, torch.float32, torch.float64
+
+
+def normal(shape, sigma, seed, pitch=0, offset=0):
+    """A bf16 matrix; pitch: extra elements between rows; offset: elements before the first."""
+    gen = torch.Generator("cuda").manual_seed(seed)
+    rows, cols = shape
+    flat = torch.empty(offset + rows * (cols + pitch), device="cuda").normal_(0, sigma, generator=gen).to(BF)
+    return flat[offset:].view(rows, cols + pitch)[:, :cols]
+
+
+def empty(shape, dtype=BF, pitch=0, offset=0):
+    flat = torch.full((offset + shape[0] * (shape[1] + pitch),), 7.0, dtype=dtype, device="cuda")
+    return flat[offset:].view(shape[0], shape[1] + pitch)[:, :shape[1]]
+
+
+def host(t):
+    return t.double().cpu().numpy()
+
+
+def product_error(a, b, depth):
+    """Bound of an fp32 product's error: sums of 16 products or more at a time, each of the
+    depth/16 + 2 additions good to 2^-22 of the sum of magnitudes so far."""
+    return (depth / 16 + 2) * 2.0 ** -22 * host(a.double().abs() @ b.double().abs())
+
+
+def check(got, want, tol, what):
+    got = host(got)
+    assert np.isfinite(got).all(), what
+    bad = np.abs(got - want) > tol
+    assert not bad.any(), (what, int(bad.sum()), float((np.abs(got - want) - tol).max()))
+
+
+# sizes: one row and one feature; around the tiles of 16 to 256; odd; longer
+SHAPES = [(1, 1, 1), (1, 64, 64), (1, 4096, 1000), (2, 100, 72), (3, 1027, 515), (5, 768, 2304),
+          (8, 512, 256), (16, 256, 4096), (17, 130, 70), (31, 2048, 96), (64, 640, 384),
+          (65, 192, 136), (127, 128, 129), (128, 128, 256), (129, 64, 257), (255, 72, 264),
+          (256, 256, 256), (257, 320, 512), (300, 775, 1031), (777, 768, 2304), (1024, 1024, 1024),
+          (2000, 520, 296), (4100, 136, 72)]
+
+
+@pytest.mark.parametrize("shape", SHAPES)
+@pytest.mark.parametrize("act", ["none", "relu", "gelu", "silu"])
+def test_forward(shape, act):
+    m, k, n = shape
+    x, w = normal((m, k), 1.0, 1), normal((n, k), 1.0 / math.sqrt(k), 2)
+    bias, res = normal((1, n), 0.5, 3)[0], normal((m, n), 1.0, 4)
+    plain = act == "none"
+    y, pre = empty((m, n)), empty((m, n))
+    za.zero_linear_forward(x, w, y, bias=None if plain else bias, act=o.ACTS[act],
+                           residual=None if act == "relu" else res, pre=None if plain else pre)
+    z = host(x) @ host(w).T + (0.0 if plain else host(bias))
+    ez = product_error(x, w.t(), k) + 2.0 ** -22 * np.abs(z)
+    want = o.act(z, act) + (0.0 if act == "relu" else host(res))
+    # the sum's error through the slope, the exponential's and the quotients' few ulp, and
+    # the one rounding to bf16
+    tol = o.SLOPE[act] * ez + 2.0 ** -18 * np.abs(z) + 2.0 ** -8 * np.abs(want) + 1e-30
+    check(y, want, tol, "y")
+    if not plain:
+        check(pre, z, ez + 2.0 ** -8 * np.abs(z) + 1e-30, "pre")
+
+
+@pytest.mark.parametrize("shape", SHAPES)
+@pytest.mark.parametrize("act,act_in,dtype,add", [("none", "none", F32, False), ("none", "silu", F32, True),
+                                                  ("gelu", "none", BF, False), ("silu", "gelu", BF, True),
+                                                  ("relu", "relu", F32, True)])
+def test_backward(shape, act, act_in, dtype, add):
+    m, k, n = shape
+    x, w, dy = normal((m, k), 1.0, 1), normal((n, k), 1.0 / math.sqrt(k), 2), normal((m, n), 1.0, 3)
+    pre = normal((m, n), 1.0, 4) if act != "none" else None
+    pre_in = normal((m, k), 1.0, 5) if act_in != "none" else None
+    dw = normal((n, k), 1.0, 6).to(dtype) if add else empty((n, k), dtype)
+    db = normal((1, n), 1.0, 7)[0].to(dtype) if add else empty((1, n), dtype)[0]
+    dx, dw0, db0 = empty((m, k)), host(dw), host(db)
+    za.zero_linear_backward(dy, x, w, dx=dx, dw=dw, dbias=db, act=o.ACTS[act], pre=pre,
+                            act_in=o.ACTS[act_in], pre_in=pre_in, accumulate=add)
+    s = np.ones((m, n)) if pre is None else o.slope(host(pre), act)
+    dz = host(dy) * s
+    adz = torch.from_numpy(np.abs(dz)).cuda()
+    # dz as the products take it: the slope's few ulp, then rounded to bf16
+    edz = 0.0 if pre is None else 2.0 ** -8
+    s_in = np.ones((m, k)) if pre_in is None else o.slope(host(pre_in), act_in)
+    want = (dz @ host(w)) * s_in
+    tol = (product_error(adz, w, n) + edz * host(adz @ w.double().abs())) * np.abs(s_in)
+    tol = tol + 2.0 ** -17 * np.abs(dz @ host(w)) + 2.0 ** -8 * np.abs(want) + 1e-30
+    check(dx, want, tol, "dx")
+    keep = 1.0 if add else 0.0
+    last = 2.0 ** -8 if dtype == BF else 2.0 ** -23
+    want = dz.T @ host(x) + keep * dw0
+    tol = product_error(adz.t(), x, m) + edz * host(adz.t() @ x.double().abs()) + last * np.abs(want)
+    check(dw, want, tol + 2.0 ** -23 * np.abs(keep * dw0) + 1e-30, "dw")
+    want = dz.sum(0) + keep * db0
+    tol = (m + 2) * 2.0 ** -23 * np.abs(dz).sum(0) + 2.0 ** -17 * np.abs(dz).sum(0) * (pre is not None)
+    check(db, want, tol + last * np.abs(want) + 2.0 ** -23 * np.abs(keep * db0) + 1e-30, "dbias")
+
+
+@pytest.mark.parametrize("pitch,offset", [(8, 0), (1, 0), (0, 1), (3, 5), (64, 8)])
+@pytest.mark.parametrize("shape", [(1, 256, 128), (7, 96, 264), (130, 200, 136), (300, 264, 520)])
+def test_pitches_and_offsets(shape, pitch, offset):
+    """Views: any row pitch, any 2-byte address; what lies between the rows is not touched."""
+    m, k, n = shape
+    kw = dict(pitch=pitch, offset=offset)
+    x, w = normal((m, k), 1.0, 1, **kw), normal((n, k), 0.1, 2, **kw)
+    res, y, pre = normal((m, n), 1.0, 3, **kw), empty((m, n), **kw), empty((m, n), **kw)
+    bias = normal((1, n), 1.0, 4, offset=offset)[0]
+    za.zero_linear_forward(x, w, y, bias=bias, act=3, residual=res, pre=pre)
+    y2, pre2 = empty((m, n)), empty((m, n))
+    za.zero_linear_forward(x.contiguous(), w.contiguous(), y2, bias=bias.clone(), act=3,
+                           residual=res.contiguous(), pre=pre2)
+    assert torch.equal(y, y2) and torch.equal(pre, pre2)
+    dy = normal((m, n), 1.0, 5, **kw)
+    out = [empty((m, k), **kw), empty((n, k), F32, **kw), empty((1, n), F32, offset=offset)[0]]
+    out2 = [empty((m, k)), empty((n, k), F32), empty((1, n), F32)[0]]
+    za.zero_linear_backward(dy, x, w, dx=out[0], dw=out[1], dbias=out[2], act=2, pre=pre)
+    za.zero_linear_backward(dy.contiguous(), x.contiguous(), w.contiguous(), dx=out2[0], dw=out2[1],
+                            dbias=out2[2], act=2, pre=pre2)
+    for a, b in zip(out, out2):
+        assert torch.equal(a, b)
+    for t in (y, pre, *out):
+        if t.dim() == 2 and pitch:
+            whole = t.as_strided((t.shape[0] - 1, pitch), (t.stride(0), 1), t.storage_offset() + t.shape[1])
+            assert bool((whole == 7.0).all())
+        assert bool((t.as_strided((offset,), (1,), 0) == 7.0).all())
+
+
+def test_each_output_alone():
+    m, k, n = 70, 130, 90
+    x, w, dy, pre = (normal(s, 1.0, i) for i, s in enumerate([(m, k), (n, k), (m, n), (m, n)]))
+    dx, dw, db = empty((m, k)), empty((n, k)), empty((1, n))[0]
+    za.zero_linear_backward(dy, x, w, dx=dx, dw=dw, dbias=db, act=2, pre=pre)
+    for name, full, kw in (("dx", dx, dict(x=None, w=w)), ("dw", dw, dict(x=x, w=None)),
+                           ("dbias", db, dict(x=None, w=None))):
+        alone = torch.empty_like(full)
+        za.zero_linear_backward(dy, kw["x"], kw["w"], act=2, pre=pre, **{name: alone})
+        assert torch.equal(alone, full), name
+    za.zero_linear_backward(dy, None, None, act=2, pre=pre)      # nothing wanted
+
+
+def test_no_rows():
+    x, w, y = empty((0, 64)), normal((32, 64), 1.0, 1), empty((0, 32))
+    za.zero_linear_forward(x, w, y)
+    dw, db = empty((32, 64), F32), empty((1, 32), F32)[0]
+    za.zero_linear_backward(y, x, w, dx=empty((0, 64)), dw=dw, dbias=db, accumulate=True)
+    assert bool((dw == 7.0).all()) and bool((db == 7.0).all())
+    za.zero_linear_backward(y, x, w, dx=empty((0, 64)), dw=dw, dbias=db)
+    assert not dw.any() and not db.any()
+
+
+def test_residual_in_place_and_side_by_side():
+    m, d = 200, 128
+    qkv = normal((m, 3 * d), 1.0, 1)
+    w, before = normal((d, d), 0.1, 2), qkv.clone()
+    za.zero_linear_forward(qkv[:, :d], w, qkv[:, d:2 * d], residual=qkv[:, d:2 * d])
+    want = host(before[:, :d]) @ host(w).T + host(before[:, d:2 * d])
+    assert np.abs(host(qkv[:, d:2 * d]) - want).max() <= 2.0 ** -7 * np.abs(want).max()
+    assert torch.equal(qkv[:, :d], before[:, :d]) and torch.equal(qkv[:, 2 * d:], before[:, 2 * d:])
+    with pytest.raises(za.ZeroError):
+        za.zero_linear_forward(qkv[:, :d], w, qkv[:, d // 2:d // 2 + d])
+
+
+@pytest.mark.parametrize("shape", [(1, 512, 256), (100, 192, 320), (300, 256, 512)])
+def test_infinities_and_nan_stay_in_their_row(shape):
+    """A row of x that is not finite reaches its own row of y and of dx, and no other; padding
+    that the kernels read past an edge never does."""
+    m, k, n = shape
+    x, w = normal((m, k), 1.0, 1), normal((n, k), 0.1, 2)
+    y0, y = empty((m, n)), empty((m, n))
+    za.zero_linear_forward(x, w, y0, act=2)
+    for bad in (float("nan"), float("inf")):
+        x2 = x.clone()
+        x2[m // 2, k - 1] = bad
+        za.zero_linear_forward(x2, w, y, act=2)
+        rows = torch.ones(m, dtype=torch.bool, device="cuda")
+        rows[m // 2] = False
+        assert torch.equal(y[rows], y0[rows])
+        if math.isnan(bad):
+            assert bool(y[m // 2].isnan().all())
+        else:
+            # gelu of +inf is inf, of -inf 0
+            want = torch.where(w[:, k - 1] > 0, float("inf"), 0.0).to(BF)
+            assert torch.equal(y[m // 2], want)
+
+
+def test_activations_at_extremes():
+    z = torch.tensor([0.0, -0.0, 1e-30, -1e-30, 5.0, -5.0, 60.0, -60.0, 150.0, -150.0, 1e20, -1e20, 3e38, -3e38,
+                      float("inf"), float("-inf"), float("nan")], device="cuda").to(BF)
+    for name, act in o.ACTS.items():
+        if act == 0:
+            continue
+        dx = empty((1, len(z)))
+        # act_in's slope at z, times 1: a map of one feature
+        za.zero_linear_backward(torch.ones(1, 1, dtype=BF, device="cuda"), None,
+                                torch.ones(1, len(z), dtype=BF, device="cuda"), dx=dx, act_in=act, pre_in=z[None])
+        got = host(dx)[0]
+        want = o.slope(np.clip(host(z), -200, 200), name)
+        assert np.isnan(got[-1]) or name == "relu"
+        assert (np.abs(got[:-1] - want[:-1]) <= 2.0 ** -8 * np.abs(want[:-1]) + 2.0 ** -17).all(), (name, got)
+
+
+@pytest.mark.parametrize("act", ["relu", "gelu", "silu"])
+def test_gradient_against_differences(act):
+    """<gradient, direction> against central differences of sum(dy * act(x w^T + b)) in 64 bits,
+    along random directions of x, w and b together."""
+    m, k, n = 96, 80, 72
+    x, w, b, dy = normal((m, k), 1.0, 1), normal((n, k), 0.2, 2), normal((1, n), 0.5, 3)[0], normal((m, n), 1.0, 4)
+    y, pre = empty((m, n)), empty((m, n))
+    za.zero_linear_forward(x, w, y, bias=b, act=o.ACTS[act], pre=pre)
+    dx, dw, db = empty((m, k)), empty((n, k), F32), empty((1, n), F32)[0]
+    za.zero_linear_backward(dy, x, w, dx=dx, dw=dw, dbias=db, act=o.ACTS[act], pre=pre)
+    hx, hw, hb, hy = host(x), host(w), host(b), host(dy)
+    rng = np.random.default_rng(0)
+    for _ in range(4):
+        ux, uw, ub = rng.normal(size=hx.shape), rng.normal(size=hw.shape), rng.normal(size=hb.shape)
+
+        def loss(e):
+            return (hy * o.act((hx + e * ux) @ (hw + e * uw).T + hb + e * ub, act)).sum()
+
+        h = 1e-5
+        want = (loss(h) - loss(-h)) / (2 * h)
+        parts = [(host(dx), ux), (host(dw), uw), (host(db), ub)]
+        got = sum((g * u).sum() for g, u in parts)
+        # bf16 roundings of pre, dz and dx: each good to 2^-8 of its element, independent
+        size = math.sqrt(sum(((g * u) ** 2).sum() for g, u in parts))
+        assert abs(got - want) <= 6 * 2.0 ** -7 * size
+
+
+def test_same_bits_every_time_on_any_stream():
+    m, k, n = 300, 520, 264
+    x, w, dy, pre = (normal(s, 1.0, i) for i, s in enumerate([(m, k), (n, k), (m, n), (m, n)]))
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    got = []
+    for stream in (None, None, side, side.cuda_stream):
+        y, dx, dw, db = empty((m, n)), empty((m, k)), empty((n, k), F32), empty((1, n), F32)[0]
+        side.wait_stream(torch.cuda.current_stream())
+        za.zero_linear_forward(x, w, y, act=2, stream=stream)
+        za.zero_linear_backward(dy, x, w, dx=dx, dw=dw, dbias=db, act=3, pre=pre, stream=stream)
+        torch.cuda.synchronize()
+        got.append((y, dx, dw, db))
+    for other in got[1:]:
+        assert all(torch.equal(a, b) for a, b in zip(got[0], other))
+    assert za.device_status() == za.ZERO_OK
+
+
+def test_in_a_graph():
+    m, k, n = 128, 256, 512
+    x, w, dy, pre = (normal(s, 1.0, i) for i, s in enumerate([(m, k), (n, k), (m, n), (m, n)]))
+    y, dx, dw = empty((m, n)), empty((m, k)), empty((n, k))
+    ws = torch.empty(za.zero_linear_workspace(m, k, n, True), dtype=torch.uint8, device="cuda")
+
+    def both():
+        za.zero_linear_forward(x, w, y, act=2, workspace=ws)
+        za.zero_linear_backward(dy, x, w, dx=dx, dw=dw, act=3, pre=pre, workspace=ws)
+
+    both()
+    torch.cuda.synchronize()
+    want = [t.clone() for t in (y, dx, dw)]
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        both()
+    for t in (y, dx, dw):
+        t.zero_()
+    graph.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(want, (y, dx, dw)))
+
+
+def test_offsets_past_32_bits():
+    """Rows whose element offset passes 2^31: the last rows of a 2.2e9-element x and y."""
+    m, k, n = 1100, 64, 64
+    pitch = 2_000_000
+    big = torch.empty((m - 1) * pitch + k, dtype=BF, device="cuda")
+    x = big.as_strided((m, k), (pitch, 1))
+    x.copy_(normal((m, k), 1.0, 1))
+    w = normal((n, k), 0.1, 2)
+    y2 = empty((m, n))
+    za.zero_linear_forward(x.contiguous(), w, y2)
+    out = torch.empty((m - 1) * pitch + n, dtype=BF, device="cuda").as_strided((m, n), (pitch, 1))
+    za.zero_linear_forward(x, w, out)
+    assert torch.equal(out, y2)

@@ -7,7 +7,10 @@ fallback: importing this package fails loudly when the library is missing.
 
 The method: "ZeRO and FSDP: partitioning the optimizer states, the gradients
 and the parameters" (AI infra handbooks), "Implementing ZeRO's Adam from
-scratch" (ZeroAdam) and "ZeRO-3 and FSDP" (unit all-gather).
+scratch" (ZeroAdam) and "ZeRO-3 and FSDP" (unit all-gather).  Around it, the rest
+of a training step (train_ops.py): zero_linear_forward and zero_linear_backward (a
+unit's linear maps), zero_grad_norm, and zero_adamw_step (AdamW over a list of
+tensors, with moments in 32 or 8 bits).
 """
 from __future__ import annotations
 
@@ -22,7 +25,11 @@ ZERO_ALL_RANKS = -1
 ZERO_GRAD_FULL, ZERO_GRAD_SHARD, ZERO_GRAD_WINDOW = 0, 1, 2
 ZERO_GRAD_LAYOUT_MASK = 0x0F
 ZERO_GRAD_F32, ZERO_ACC_BF16 = 0x10, 0x20
+ZERO_GRAD_ACCUMULATE, ZERO_STATE_8BIT = 0x40, 0x80
 ZERO_PARAM_FULL, ZERO_PARAM_SHARD = 0, 1
+ZERO_ACT_NONE, ZERO_ACT_RELU, ZERO_ACT_GELU, ZERO_ACT_SILU = 0, 1, 2, 3
+ZERO_MOMENT_BLOCK = 256
+ZERO_MAX_LIST = 65536
 ZERO_MAX_WORLD = 1024
 ZERO_MAX_UNIT_TENSORS = 256
 
@@ -31,12 +38,16 @@ ERRORS = {
     -5: "ZERO_E_STEP", -6: "ZERO_E_ALIGN", -7: "ZERO_E_HPARAM", -8: "ZERO_E_LAYOUT",
     -9: "ZERO_E_PLAN", -10: "ZERO_E_ALIAS", -11: "ZERO_E_LAUNCH", -12: "ZERO_E_DEVICE",
     -13: "ZERO_E_RANGE", -14: "ZERO_E_SHAPE", -15: "ZERO_E_TIMEOUT", -16: "ZERO_E_HOOK",
+    -17: "ZERO_E_WORKSPACE",
 }
 
 # Every symbol include/zeroadam.h declares.
 EXPORTS = ("zero_plan", "zero_adam_step", "zero_adam_step_range", "zero3_unit_gather",
            "zero3_unit_gather_rows", "zero3_unit_step", "zero_device_status",
-           "zero_test_withhold_copies", "zero_strerror", "zero_version")
+           "zero_test_withhold_copies", "zero_strerror", "zero_version",
+           "zero_linear_forward", "zero_linear_backward", "zero_linear_workspace",
+           "zero_grad_norm", "zero_grad_norm_workspace", "zero_adamw_step",
+           "zero_adamw_state_f32")
 
 
 class ZeroError(RuntimeError):
@@ -287,10 +298,15 @@ def raw_lib() -> ctypes.CDLL:
     return _lib
 
 
+from . import train_ops  # noqa: E402  (it takes the loaded library from here)
+from .train_ops import *  # noqa: E402,F401,F403
+
 __all__ = ["zero_plan", "zero_adam_step", "zero_adam_step_range", "zero3_unit_gather",
            "zero3_unit_gather_rows", "pointer_array", "PointerArray", "zero3_unit_step", "rows_layout", "device_status",
            "check_device", "test_withhold_copies",
            "ZeroPlan", "ZeroError", "strerror", "version", "raw_lib", "ZERO_ALL_RANKS",
            "ZERO_GRAD_FULL", "ZERO_GRAD_SHARD", "ZERO_GRAD_WINDOW", "ZERO_GRAD_F32",
            "ZERO_ACC_BF16", "ZERO_PARAM_FULL", "ZERO_PARAM_SHARD", "ZERO_MAX_WORLD",
-           "ZERO_MAX_UNIT_TENSORS", "EXPORTS", "LIB_PATH"]
+           "ZERO_MAX_UNIT_TENSORS", "EXPORTS", "LIB_PATH", "ZERO_GRAD_ACCUMULATE",
+           "ZERO_STATE_8BIT", "ZERO_ACT_NONE", "ZERO_ACT_RELU", "ZERO_ACT_GELU", "ZERO_ACT_SILU",
+           "ZERO_MOMENT_BLOCK", "ZERO_MAX_LIST"] + train_ops.__all__

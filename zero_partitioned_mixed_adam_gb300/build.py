@@ -15,8 +15,10 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 OUT = os.path.join(HERE, "libzeroadam.so")
 OBJ_DIR = os.path.join(ROOT, "_build", "zeroadam")
-SOURCES = ["capi.cpp", "adam_step.cu", "unit_gather.cu"]
-HEADERS = ([os.path.join(CSRC, h) for h in sorted(os.listdir(CSRC)) if h.endswith(".h")]
+SOURCES = ["capi.cpp", "capi_train.cpp", "adam_step.cu", "unit_gather.cu", "adamw_tensors.cu",
+           "linear.cu"]
+HEADERS = ([os.path.join(CSRC, h) for h in sorted(os.listdir(CSRC))
+            if h.endswith((".h", ".hpp", ".cuh"))]
            + [os.path.join(ROOT, "include", "zeroadam.h")])
 ARCH = "sm_103a"
 

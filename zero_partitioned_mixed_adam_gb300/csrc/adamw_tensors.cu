@@ -1,0 +1,647 @@
+// adamw_tensors.cu -- AdamW over a list of tensors, its 8-bit moments, and the
+// global gradient norm, on sm_103a.
+//
+// All three stream every element once and do little with it, so they are bound
+// by HBM bandwidth; what a list adds is that a block has to find its tensor.
+// The tensors' descriptors travel in the kernel's arguments (constant memory:
+// no table in device memory to lay out, nothing to free, captured by a graph as
+// they are), and a launch covers as many tensors as fit there.
+#include <cuda_bf16.h>
+
+#include <cmath>
+
+#include "internal.h"
+#include "train_ops.cuh"
+
+namespace zeroadam {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kTile = kThreads * 8;  // elements of one tile: 8 moment blocks, one per warp
+
+__device__ __forceinline__ float bf16_value(uint32_t h) { return __uint_as_float(h << 16); }
+__device__ __forceinline__ uint32_t bf16_bits(float x) {
+  return __bfloat16_as_ushort(__float2bfloat16_rn(x));
+}
+
+// One step of O'Neill's 32-bit permuted congruential generator (RXS-M-XS),
+// used as a hash (Jarzynski and Olano, "Hash Functions for GPU Rendering").
+__host__ __device__ __forceinline__ uint32_t pcg_hash(uint32_t x) {
+  x = x * 747796405u + 2891336453u;
+  x = ((x >> ((x >> 28) + 4)) ^ x) * 277803737u;
+  return (x >> 22) ^ x;
+}
+
+// Index of the tensor that holds `tile`: the last with tile0 <= tile.
+template <typename Desc>
+__device__ __forceinline__ int find_tensor(const Desc* t, int count, int tile, int low) {
+  int high = count;  // t[low].tile0 <= tile < t[high].tile0
+  while (high - low > 1) {
+    const int mid = (low + high) / 2;
+    if (t[mid].tile0 <= tile) low = mid; else high = mid;
+  }
+  return low;
+}
+
+// 8 consecutive elements, or with VEC = false the 8 elements i + 32 j, of which
+// those from n on do not exist (0 stands in for them).
+template <bool VEC>
+__device__ __forceinline__ void load_f32(const float* p, int64_t i, int64_t n, float x[8]) {
+  if (VEC) {
+    const float4 a = __ldcs(reinterpret_cast<const float4*>(p + i));
+    const float4 b = __ldcs(reinterpret_cast<const float4*>(p + i) + 1);
+    x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
+    x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) x[j] = i + 32 * j < n ? __ldcs(p + i + 32 * j) : 0.0f;
+  }
+}
+
+template <bool VEC>
+__device__ __forceinline__ void store_f32(float* p, int64_t i, int64_t n, const float x[8]) {
+  if (VEC) {
+    __stcs(reinterpret_cast<float4*>(p + i), make_float4(x[0], x[1], x[2], x[3]));
+    __stcs(reinterpret_cast<float4*>(p + i) + 1, make_float4(x[4], x[5], x[6], x[7]));
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (i + 32 * j < n) __stcs(p + i + 32 * j, x[j]);
+  }
+}
+
+template <bool VEC, bool GF32>
+__device__ __forceinline__ void load_grad(const void* p, int64_t i, int64_t n, float x[8]) {
+  if (GF32) {
+    load_f32<VEC>(static_cast<const float*>(p), i, n, x);
+  } else if (VEC) {
+    const uint4 r = __ldcs(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p) + i));
+    const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      x[2 * j] = __uint_as_float(w[j] << 16);
+      x[2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
+    }
+  } else {
+    const uint16_t* q = static_cast<const uint16_t*>(p);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) x[j] = i + 32 * j < n ? bf16_value(__ldcs(q + i + 32 * j)) : 0.0f;
+  }
+}
+
+template <bool VEC>
+__device__ __forceinline__ void store_bf16(uint16_t* p, int64_t i, int64_t n, const float x[8]) {
+  if (VEC) {
+    uint32_t w[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) w[j] = bf16_bits(x[2 * j]) | (bf16_bits(x[2 * j + 1]) << 16);
+    __stcs(reinterpret_cast<uint4*>(p + i), make_uint4(w[0], w[1], w[2], w[3]));
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (i + 32 * j < n)
+        __stcs(reinterpret_cast<unsigned short*>(p) + i + 32 * j,
+               static_cast<unsigned short>(bf16_bits(x[j])));
+  }
+}
+
+template <bool VEC>
+__device__ __forceinline__ void load_codes(const uint8_t* p, int64_t i, int64_t n, uint32_t c[8]) {
+  if (VEC) {
+    const uint2 r = __ldcs(reinterpret_cast<const uint2*>(p + i));
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      c[j] = (r.x >> (8 * j)) & 0xffu;
+      c[4 + j] = (r.y >> (8 * j)) & 0xffu;
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) c[j] = i + 32 * j < n ? __ldcs(p + i + 32 * j) : 0;
+  }
+}
+
+template <bool VEC>
+__device__ __forceinline__ void store_codes(uint8_t* p, int64_t i, int64_t n, const uint32_t c[8]) {
+  if (VEC) {
+    __stcs(reinterpret_cast<uint2*>(p + i),
+           make_uint2(c[0] | (c[1] << 8) | (c[2] << 16) | (c[3] << 24),
+                      c[4] | (c[5] << 8) | (c[6] << 16) | (c[7] << 24)));
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (i + 32 * j < n)
+        __stcs(reinterpret_cast<unsigned char*>(p) + i + 32 * j, static_cast<unsigned char>(c[j]));
+  }
+}
+
+// ------------------------------------------------------------ 8-bit moments
+//
+// A code's bits, put 20 places up, are the bits of a binary32 number whose
+// exponent field is the code's own: for m (4 exponent bits, top 15) that number
+// is the value over 2^112 times the block's scale, for v (5 bits, top 31) over
+// 2^96, and gradual underflow comes with binary32's own denormals.  So decoding
+// is a shift and two exact products with powers of two, and encoding two such
+// products, an integer addition of the random bits (whose carry is the rounding
+// up) and a shift.
+constexpr float kMUp = 0x1p112f, kMDown = 0x1p-112f;
+constexpr float kVUp = 0x1p96f, kVDown = 0x1p-96f;
+
+__device__ __forceinline__ float decode_m(uint32_t c, float scale) {
+  const float a = __uint_as_float(((c & 0x80u) << 24) | ((c & 0x7fu) << 20));
+  return __fmul_rn(__fmul_rn(a, kMUp), scale);
+}
+__device__ __forceinline__ float decode_v(uint32_t c, float scale) {
+  return __fmul_rn(__fmul_rn(__uint_as_float(c << 20), kVUp), scale);
+}
+
+// A block's scale from the bits of its largest magnitude: the exponent after
+// rounding up to 4 significant bits, so that no code overflows by rounding up.
+struct BlockScale {
+  float scale, inverse;
+  bool fine;  // false: an infinity or NaN among the block's values
+};
+__device__ __forceinline__ BlockScale block_scale(uint32_t top) {
+  uint32_t e = (top + 0xfffffu) >> 23;
+  e = e < 1u ? 1u : e > 253u ? 253u : e;
+  BlockScale b;
+  b.fine = top < 0x7f800000u;
+  b.scale = b.fine ? __uint_as_float(e << 23) : __uint_as_float(0x7fffffffu);
+  b.inverse = __uint_as_float((254u - e) << 23);
+  return b;
+}
+
+__device__ __forceinline__ uint32_t encode_magnitude(uint32_t bits, float inverse, float down,
+                                                     uint32_t r, uint32_t most) {
+  const float t = __fmul_rn(__fmul_rn(__uint_as_float(bits), inverse), down);
+  const uint32_t c = (__float_as_uint(t) + (r * 16u + 8u)) >> 20;
+  return c < most ? c : most;
+}
+
+struct AdamwDesc {
+  const void* grad;
+  float* master;
+  uint16_t* param;
+  void* m;
+  void* v;
+  float* m_scale;
+  float* v_scale;
+  int64_t numel;
+  float keep;     // 1 - lr * weight_decay
+  uint32_t key;   // of the random bits
+  int32_t tile0;  // first tile of this tensor in the launch
+  int32_t vec;    // every buffer allows vector accesses
+};
+
+template <int CAP>
+struct AdamwArgs {
+  AdamwDesc t[CAP];
+  AdamwScalars s;
+  const float* grad_scale;
+  int32_t count, tiles;
+};
+
+// One element; the sums and products that m and v are made of are rounded one
+// by one, as the flat step's are, so that codes and moments have one value.
+__device__ __forceinline__ void adamw_element(float g, const AdamwScalars& s, float keep, float& w,
+                                              float& m, float& v) {
+  m = __fadd_rn(__fmul_rn(m, s.b1), __fmul_rn(s.omb1, g));
+  v = __fadd_rn(__fmul_rn(v, s.b2), __fmul_rn(__fmul_rn(s.omb2, g), g));
+  const float denom = __fsqrt_rn(v) * s.inv_root + s.eps;
+  w = w * keep - __fdiv_rn(s.size * m, denom);
+}
+
+// 8 elements per thread; one warp's 256 are one moment block.
+template <bool VEC, bool GF32, bool EIGHT>
+__device__ __forceinline__ void adamw_tile(const AdamwDesc& t, const AdamwScalars& s, float clip,
+                                           bool clipped, int64_t base, int lane) {
+  const int64_t n = t.numel;
+  const int64_t i = base + (VEC ? 8 * lane : lane);
+  constexpr int step = VEC ? 1 : 32;
+  float g[8], w[8], m[8], v[8];
+  load_grad<VEC, GF32>(t.grad, i, n, g);
+  load_f32<VEC>(t.master, i, n, w);
+  if constexpr (EIGHT) {
+    const int64_t block = base / ZERO_MOMENT_BLOCK;
+    uint32_t mc[8], vc[8];
+    load_codes<VEC>(static_cast<const uint8_t*>(t.m), i, n, mc);
+    load_codes<VEC>(static_cast<const uint8_t*>(t.v), i, n, vc);
+    const float ms = t.m_scale[block], vs = t.v_scale[block];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      m[j] = decode_m(mc[j], ms);
+      v[j] = decode_v(vc[j], vs);
+    }
+  } else {
+    load_f32<VEC>(static_cast<const float*>(t.m), i, n, m);
+    load_f32<VEC>(static_cast<const float*>(t.v), i, n, v);
+  }
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    if (clipped) g[j] = __fmul_rn(g[j], clip);
+    adamw_element(g[j], s, t.keep, w[j], m[j], v[j]);
+  }
+  store_f32<VEC>(t.master, i, n, w);
+  if (t.param != nullptr) store_bf16<VEC>(t.param, i, n, w);
+  if constexpr (EIGHT) {
+    const int64_t block = base / ZERO_MOMENT_BLOCK;
+    uint32_t mtop = 0, vtop = 0;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      if (!VEC && i + step * j >= n) m[j] = v[j] = 0.0f;  // no element: no part in the scale
+      const uint32_t a = __float_as_uint(m[j]) & 0x7fffffffu;
+      const uint32_t b = __float_as_uint(v[j]) & 0x7fffffffu;
+      mtop = a > mtop ? a : mtop;
+      vtop = b > vtop ? b : vtop;
+    }
+    mtop = __reduce_max_sync(0xffffffffu, mtop);
+    vtop = __reduce_max_sync(0xffffffffu, vtop);
+    const BlockScale mb = block_scale(mtop), vb = block_scale(vtop);
+    const uint32_t key = t.key + static_cast<uint32_t>(i >> 32) * 0x9E3779B9u;
+    uint32_t mc[8], vc[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const uint32_t u = pcg_hash(static_cast<uint32_t>(i) + step * j + key);
+      const uint32_t bits = __float_as_uint(m[j]);
+      mc[j] = mb.fine ? (encode_magnitude(bits & 0x7fffffffu, mb.inverse, kMDown, u >> 16, 127u) |
+                         ((bits >> 24) & 0x80u))
+                      : 0u;
+      vc[j] = vb.fine ? encode_magnitude(__float_as_uint(v[j]) & 0x7fffffffu, vb.inverse, kVDown,
+                                         u & 0xffffu, 255u)
+                      : 0u;
+    }
+    store_codes<VEC>(static_cast<uint8_t*>(t.m), i, n, mc);
+    store_codes<VEC>(static_cast<uint8_t*>(t.v), i, n, vc);
+    if (lane == 0) {
+      t.m_scale[block] = mb.scale;
+      t.v_scale[block] = vb.scale;
+    }
+  } else {
+    store_f32<VEC>(static_cast<float*>(t.m), i, n, m);
+    store_f32<VEC>(static_cast<float*>(t.v), i, n, v);
+  }
+}
+
+template <int CAP, bool GF32, bool EIGHT>
+__global__ void __launch_bounds__(kThreads)
+    adamw_tensors_kernel(const __grid_constant__ AdamwArgs<CAP> a) {
+  const bool clipped = a.grad_scale != nullptr;
+  const float clip = clipped ? *a.grad_scale : 1.0f;
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  int ti = 0;
+  for (int tile = blockIdx.x; tile < a.tiles; tile += gridDim.x) {
+    ti = find_tensor(a.t, a.count, tile, ti);
+    const AdamwDesc& t = a.t[ti];
+    const int64_t base = static_cast<int64_t>(tile - t.tile0) * kTile + 256 * warp;
+    if (base >= t.numel) continue;  // the same for the whole warp
+    if (t.vec && base + 256 <= t.numel)
+      adamw_tile<true, GF32, EIGHT>(t, a.s, clip, clipped, base, lane);
+    else
+      adamw_tile<false, GF32, EIGHT>(t, a.s, clip, clipped, base, lane);
+  }
+}
+
+struct MomentsDesc {
+  const uint8_t* codes;
+  const float* scale;
+  float* out;
+  int64_t numel;
+  int32_t tile0;
+  int32_t is_m;
+};
+
+template <int CAP>
+struct MomentsArgs {
+  MomentsDesc t[CAP];
+  int32_t count, tiles;
+};
+
+template <int CAP>
+__global__ void __launch_bounds__(kThreads)
+    adamw_moments_kernel(const __grid_constant__ MomentsArgs<CAP> a) {
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  int ti = 0;
+  for (int tile = blockIdx.x; tile < a.tiles; tile += gridDim.x) {
+    ti = find_tensor(a.t, a.count, tile, ti);
+    const MomentsDesc& t = a.t[ti];
+    const int64_t base = static_cast<int64_t>(tile - t.tile0) * kTile + 256 * warp;
+    if (base >= t.numel) continue;
+    const float scale = t.scale[base / ZERO_MOMENT_BLOCK];
+    uint32_t c[8];
+    float x[8];
+    load_codes<false>(t.codes, base + lane, t.numel, c);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) x[j] = t.is_m ? decode_m(c[j], scale) : decode_v(c[j], scale);
+    store_f32<false>(t.out, base + lane, t.numel, x);
+  }
+}
+
+// ------------------------------------------------------------------- norm
+
+struct NormDesc {
+  const void* grad;
+  int64_t numel;
+  int32_t tile0;
+  int32_t shift;  // elements between the 16-byte boundary before the tensor and its start
+};
+
+constexpr int kNormTile = kThreads * 64;  // elements
+
+template <int CAP>
+struct NormArgs {
+  NormDesc t[CAP];
+  int32_t count, tiles;
+  int32_t slot0, slots;  // this launch's first place in the workspace; places of all launches
+  float max_norm;
+  float* out;
+  uint32_t* ticket;
+  double* partial;
+};
+
+// The sum of a thread's up to 64 squares in fp32, its tiles and all else in
+// fp64.  Vectors are counted from the 16-byte boundary at or before the
+// tensor's start, so each is aligned whatever the tensor's address; the
+// elements of the first and the last that are not the tensor's are left out.
+template <int CAP, bool GF32>
+__global__ void __launch_bounds__(kThreads)
+    grad_norm_kernel(const __grid_constant__ NormArgs<CAP> a) {
+  constexpr int V = GF32 ? 4 : 8;  // elements of a 16-byte vector
+  double sum = 0.0;
+  int ti = 0;
+  for (int tile = blockIdx.x; tile < a.tiles; tile += gridDim.x) {
+    ti = find_tensor(a.t, a.count, tile, ti);
+    const NormDesc& t = a.t[ti];
+    const int64_t first = static_cast<int64_t>(tile - t.tile0) * kNormTile;
+    const int64_t end = t.numel + t.shift;
+    const char* p = static_cast<const char*>(t.grad) - t.shift * (GF32 ? 4 : 2);
+    float acc = 0.0f;
+    if (first >= t.shift && first + kNormTile <= end) {
+      const uint4* q = reinterpret_cast<const uint4*>(p) + first / V;
+#pragma unroll
+      for (int r = 0; r < 64 / V; r += 8) {
+        uint4 x[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) x[j] = __ldcs(q + (r + j) * kThreads + threadIdx.x);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const uint32_t w[4] = {x[j].x, x[j].y, x[j].z, x[j].w};
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            if (GF32) {
+              const float f = __uint_as_float(w[k]);
+              acc = fmaf(f, f, acc);
+            } else {
+              const float lo = __uint_as_float(w[k] << 16), hi = __uint_as_float(w[k] & 0xffff0000u);
+              acc = fmaf(lo, lo, acc);
+              acc = fmaf(hi, hi, acc);
+            }
+          }
+        }
+      }
+    } else {
+      int64_t e = first + threadIdx.x;
+      const int64_t stop = end < first + kNormTile ? end : first + kNormTile;
+      for (; e < stop; e += kThreads) {
+        if (e < t.shift) continue;
+        const float f = GF32 ? __ldcs(reinterpret_cast<const float*>(p) + e)
+                             : bf16_value(__ldcs(reinterpret_cast<const uint16_t*>(p) + e));
+        acc = fmaf(f, f, acc);
+      }
+    }
+    sum += static_cast<double>(acc);
+  }
+
+  __shared__ double part[kThreads / 32];
+  __shared__ bool last;
+  auto block_sum = [&](double x) {
+#pragma unroll
+    for (int d = 16; d > 0; d /= 2) x += __shfl_down_sync(0xffffffffu, x, d);
+    if (threadIdx.x % 32 == 0) part[threadIdx.x / 32] = x;
+    __syncthreads();
+    x = 0.0;
+#pragma unroll
+    for (int k = 0; k < kThreads / 32; ++k) x += part[k];
+    return x;
+  };
+  sum = block_sum(sum);
+  if (threadIdx.x == 0) {
+    a.partial[a.slot0 + blockIdx.x] = sum;
+    __threadfence();
+    last = atomicAdd(a.ticket, 1u) == static_cast<uint32_t>(a.slots - 1);
+  }
+  __syncthreads();
+  if (!last) return;
+  __threadfence();
+  sum = 0.0;
+  for (int k = threadIdx.x; k < a.slots; k += kThreads) sum += __ldcg(a.partial + k);
+  sum = block_sum(sum);
+  if (threadIdx.x == 0) {
+    const float norm = static_cast<float>(sqrt(sum));
+    const float c = a.max_norm / (norm + 1e-6f);
+    a.out[0] = norm;
+    a.out[1] = c > 1.0f ? 1.0f : c;  // a NaN stays one
+    *a.ticket = 0;
+  }
+}
+
+int grid_of(int64_t tiles, int per_sm) {
+  int sms = 0;
+  if (device_sm_count(&sms) != 0) return 0;
+  const int64_t most = static_cast<int64_t>(sms) * per_sm;
+  return static_cast<int>(tiles < most ? tiles : most);
+}
+
+template <typename T>
+bool aligned(const T* p, uintptr_t k) {
+  return (reinterpret_cast<uintptr_t>(p) & (k - 1)) == 0;
+}
+
+// Kernel arguments hold at most 32,764 bytes.
+constexpr int kAdamwMost = 384;
+
+template <int CAP>
+cudaError_t launch_adamw_chunk(const AdamwLaunch& L, const int32_t* index, int count) {
+  AdamwArgs<CAP> a;
+  static_assert(sizeof(a) <= 32764, "kernel arguments");
+  int64_t tiles = 0;
+  const uint32_t seed = pcg_hash(L.seed);
+  for (int k = 0; k < count; ++k) {
+    const zero_adamw_tensor_t& x = L.tensors[index[k]];
+    AdamwDesc& t = a.t[k];
+    t.grad = x.grad;
+    t.master = x.master;
+    t.param = static_cast<uint16_t*>(x.param_bf16);
+    t.m = x.m;
+    t.v = x.v;
+    t.m_scale = x.m_scale;
+    t.v_scale = x.v_scale;
+    t.numel = x.numel;
+    t.keep = static_cast<float>(1.0 - L.lr * x.weight_decay);
+    t.key = pcg_hash(seed + static_cast<uint32_t>(index[k]));
+    t.tile0 = static_cast<int32_t>(tiles);
+    const uintptr_t code = L.eight ? 8 : 16;
+    t.vec = aligned(t.grad, 16) && aligned(t.master, 16) && aligned(t.param, 16) &&
+            aligned(t.m, code) && aligned(t.v, code);
+    tiles += (x.numel + kTile - 1) / kTile;
+  }
+  if (tiles > INT32_MAX) return cudaErrorInvalidValue;
+  a.s = L.s;
+  a.grad_scale = L.grad_scale;
+  a.count = count;
+  a.tiles = static_cast<int32_t>(tiles);
+  const int grid = grid_of(tiles, 8);
+  if (grid == 0) return cudaErrorNoDevice;
+  if (L.grad_f32) {
+    if (L.eight)
+      adamw_tensors_kernel<CAP, true, true><<<grid, kThreads, 0, L.stream>>>(a);
+    else
+      adamw_tensors_kernel<CAP, true, false><<<grid, kThreads, 0, L.stream>>>(a);
+  } else {
+    if (L.eight)
+      adamw_tensors_kernel<CAP, false, true><<<grid, kThreads, 0, L.stream>>>(a);
+    else
+      adamw_tensors_kernel<CAP, false, false><<<grid, kThreads, 0, L.stream>>>(a);
+  }
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_adamw(const AdamwLaunch& L) {
+  (void)cudaGetLastError();
+  int32_t index[kAdamwMost];
+  for (int32_t i = 0; i < L.ntensors;) {
+    int count = 0;
+    for (; i < L.ntensors && count < kAdamwMost; ++i)
+      if (L.tensors[i].numel > 0) index[count++] = i;
+    if (count == 0) break;
+    const cudaError_t e = count <= 16    ? launch_adamw_chunk<16>(L, index, count)
+                          : count <= 160 ? launch_adamw_chunk<160>(L, index, count)
+                                         : launch_adamw_chunk<kAdamwMost>(L, index, count);
+    if (e != cudaSuccess) return e;
+  }
+  return cudaSuccess;
+}
+
+cudaError_t launch_adamw_moments(const MomentsLaunch& L) {
+  constexpr int kCap = 512;
+  (void)cudaGetLastError();
+  MomentsArgs<kCap> a;
+  static_assert(sizeof(a) <= 32764, "kernel arguments");
+  a.count = 0;
+  int64_t tiles = 0;
+  auto flush = [&]() -> cudaError_t {
+    if (a.count == 0) return cudaSuccess;
+    if (tiles > INT32_MAX) return cudaErrorInvalidValue;
+    a.tiles = static_cast<int32_t>(tiles);
+    const int grid = grid_of(tiles, 8);
+    if (grid == 0) return cudaErrorNoDevice;
+    adamw_moments_kernel<kCap><<<grid, kThreads, 0, L.stream>>>(a);
+    a.count = 0;
+    tiles = 0;
+    return cudaGetLastError();
+  };
+  for (int32_t i = 0; i < L.ntensors; ++i) {
+    const zero_adamw_tensor_t& x = L.tensors[i];
+    if (x.numel == 0) continue;
+    for (int which = 0; which < 2; ++which) {
+      float* const* out = which == 0 ? L.m_out : L.v_out;
+      if (out == nullptr) continue;
+      MomentsDesc& t = a.t[a.count++];
+      t.codes = static_cast<const uint8_t*>(which == 0 ? x.m : x.v);
+      t.scale = which == 0 ? x.m_scale : x.v_scale;
+      t.out = out[i];
+      t.numel = x.numel;
+      t.tile0 = static_cast<int32_t>(tiles);
+      t.is_m = which == 0;
+      tiles += (x.numel + kTile - 1) / kTile;
+      if (a.count == kCap || tiles > INT32_MAX / 2) {
+        const cudaError_t e = flush();
+        if (e != cudaSuccess) return e;
+      }
+    }
+  }
+  return flush();
+}
+
+namespace {
+
+template <int CAP>
+cudaError_t launch_norm_chunk(const NormLaunch& L, const int32_t* index, int count, int slot0,
+                              int slots, int grid) {
+  NormArgs<CAP> a;
+  static_assert(sizeof(a) <= 32764, "kernel arguments");
+  int64_t tiles = 0;
+  for (int k = 0; k < count; ++k) {
+    NormDesc& t = a.t[k];
+    t.grad = L.grads[index[k]];
+    t.numel = L.numels[index[k]];
+    t.tile0 = static_cast<int32_t>(tiles);
+    t.shift = static_cast<int32_t>((reinterpret_cast<uintptr_t>(t.grad) & 15u) /
+                                   (L.grad_f32 ? 4u : 2u));
+    tiles += (t.numel + t.shift + kNormTile - 1) / kNormTile;
+  }
+  if (tiles > INT32_MAX) return cudaErrorInvalidValue;
+  a.count = count;
+  a.tiles = static_cast<int32_t>(tiles);
+  a.slot0 = slot0;
+  a.slots = slots;
+  a.max_norm = L.max_norm;
+  a.out = L.out;
+  a.ticket = static_cast<uint32_t*>(L.workspace);
+  a.partial = reinterpret_cast<double*>(static_cast<char*>(L.workspace) + 16);
+  if (L.grad_f32)
+    grad_norm_kernel<CAP, true><<<grid, kThreads, 0, L.stream>>>(a);
+  else
+    grad_norm_kernel<CAP, false><<<grid, kThreads, 0, L.stream>>>(a);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_grad_norm(const NormLaunch& L) {
+  constexpr int kMost = 1024;
+  (void)cudaGetLastError();
+  // The blocks of each launch are settled first: the last block of all, whichever
+  // launch it is in, adds up every block's part.
+  int32_t left = 0;
+  for (int32_t i = 0; i < L.ntensors; ++i) left += L.numels[i] > 0;
+  const int launches = left == 0 ? 1 : (left + kMost - 1) / kMost;
+  int grids[(ZERO_MAX_LIST + kMost - 1) / kMost];
+  int64_t tiles = 0;
+  int slots = 0;
+  int launch = 0, count = 0;
+  auto close = [&]() {
+    int g = grid_of(tiles < 1 ? 1 : tiles, 4);
+    if (g > kNormSlots / launches) g = static_cast<int>(kNormSlots / launches);
+    grids[launch++] = g;
+    slots += g;
+    tiles = 0;
+    count = 0;
+  };
+  for (int32_t i = 0; i < L.ntensors; ++i) {
+    if (L.numels[i] == 0) continue;
+    const int64_t shift = static_cast<int64_t>((reinterpret_cast<uintptr_t>(L.grads[i]) & 15u) /
+                                               (L.grad_f32 ? 4u : 2u));
+    tiles += (L.numels[i] + shift + kNormTile - 1) / kNormTile;
+    if (++count == kMost) close();
+  }
+  if (count > 0 || launch == 0) close();
+  if (grids[0] == 0) return cudaErrorNoDevice;
+  int32_t index[kMost];
+  int32_t i = 0;
+  int slot0 = 0;
+  for (int k = 0; k < launch; ++k) {
+    count = 0;
+    for (; i < L.ntensors && count < kMost; ++i)
+      if (L.numels[i] > 0) index[count++] = i;
+    const cudaError_t e =
+        count <= 16    ? launch_norm_chunk<16>(L, index, count, slot0, slots, grids[k])
+        : count <= 160 ? launch_norm_chunk<160>(L, index, count, slot0, slots, grids[k])
+                       : launch_norm_chunk<kMost>(L, index, count, slot0, slots, grids[k]);
+    if (e != cudaSuccess) return e;
+    slot0 += grids[k];
+  }
+  return cudaSuccess;
+}
+
+}  // namespace zeroadam

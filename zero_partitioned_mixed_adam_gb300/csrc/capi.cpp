@@ -4,7 +4,6 @@
 // named after itself for its whole duration (a no-op unless a profiler or
 // another NVTX tool is attached).
 #include <cuda_runtime.h>
-#include <nvtx3/nvToolsExt.h>
 
 #include <atomic>
 #include <cmath>
@@ -15,8 +14,9 @@
 #include <mutex>
 #include <string>
 
-#include "zeroadam.h"
+#include "capi_common.hpp"
 #include "internal.h"
+#include "zeroadam.h"
 
 namespace zeroadam {
 
@@ -45,14 +45,6 @@ int device_sm_count(int* sms) {
 
 namespace {
 
-// Scoped NVTX range.
-struct Trace {
-  explicit Trace(const char* name) { nvtxRangePushA(name); }
-  ~Trace() { nvtxRangePop(); }
-  Trace(const Trace&) = delete;
-  Trace& operator=(const Trace&) = delete;
-};
-
 // zero_test_withhold_copies: read by every step launch (relaxed; a test sets it
 // between launches).
 std::atomic<int> g_withhold{0};
@@ -66,11 +58,15 @@ int device_error(cudaError_t e) {
   return ZERO_E_DEVICE;
 }
 
+}  // namespace
+
 int launch_status(cudaError_t e) {
   if (e == cudaSuccess) return ZERO_OK;
   t_last_cuda = e;
   return e == cudaErrorNoDevice ? ZERO_E_DEVICE : ZERO_E_LAUNCH;
 }
+
+namespace {
 
 // Shard layout: ceil(numel/world) elements per rank, zero pad at the end
 // ("Implementing ZeRO's Adam from scratch": shard size and _flatten).
@@ -123,16 +119,6 @@ int check_plan(const zero_plan_t* plan) {
 }
 
 bool is_finite(double x) { return std::isfinite(x); }
-
-struct Range {
-  uintptr_t lo, hi;
-};
-bool overlap(Range a, Range b) { return a.lo < b.hi && b.lo < a.hi; }
-Range bytes_of(const void* p, int64_t first, int64_t count, int esize) {
-  const uintptr_t b = reinterpret_cast<uintptr_t>(p) + static_cast<uintptr_t>(first) * esize;
-  return {b, b + static_cast<uintptr_t>(count) * esize};
-}
-bool nonempty(Range r) { return r.hi > r.lo; }
 
 // A step over [begin, end), checked: its launch and the byte ranges it
 // touches (for the unit step's checks across its two parts).
@@ -452,6 +438,7 @@ const char* zero_strerror(int status) {
     case ZERO_E_SHAPE: return "ntensors in [1, ZERO_MAX_UNIT_TENSORS] and sizes >= 1 required";
     case ZERO_E_TIMEOUT: return "a kernel gave up a bounded wait; that step's outputs are incomplete";
     case ZERO_E_HOOK: return "test hooks are off: they need ZEROADAM_TEST_HOOKS=1 in the environment";
+    case ZERO_E_WORKSPACE: return "the workspace is NULL, not 16-byte aligned or too small";
     case ZERO_E_LAUNCH:
       t_msg = std::string("kernel launch failed: ") + cudaGetErrorString(t_last_cuda);
       return t_msg.c_str();
