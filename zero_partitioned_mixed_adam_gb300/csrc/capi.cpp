@@ -16,6 +16,7 @@
 
 #include "capi_common.hpp"
 #include "internal.h"
+#include "train_ops.cuh"
 #include "zeroadam.h"
 
 namespace zeroadam {
@@ -59,6 +60,8 @@ int device_error(cudaError_t e) {
 }
 
 }  // namespace
+
+int withhold_copies() { return g_withhold.load(std::memory_order_relaxed); }
 
 int launch_status(cudaError_t e) {
   if (e == cudaSuccess) return ZERO_OK;
@@ -411,10 +414,11 @@ int zero_device_status(void) {
   if (e != cudaSuccess) return device_error(e);
   static std::mutex mu;  // one caller at a time takes the words
   std::lock_guard<std::mutex> lock(mu);
-  int step = 0, gather = 0;
+  int step = 0, gather = 0, linear = 0;
   if (read_and_clear_step_status(&step) != 0) return device_error(cudaGetLastError());
   if (read_and_clear_gather_status(&gather) != 0) return device_error(cudaGetLastError());
-  return step == 0 && gather == 0 ? ZERO_OK : ZERO_E_TIMEOUT;
+  if (read_and_clear_linear_status(&linear) != 0) return device_error(cudaGetLastError());
+  return step == 0 && gather == 0 && linear == 0 ? ZERO_OK : ZERO_E_TIMEOUT;
 }
 
 const char* zero_strerror(int status) {

@@ -17,6 +17,9 @@ struct Trace {
   Trace& operator=(const Trace&) = delete;
 };
 
+// Whether zero_test_withhold_copies is on.
+int withhold_copies();
+
 // The status of a launch, keeping its CUDA error for zero_strerror.
 int launch_status(cudaError_t e);
 

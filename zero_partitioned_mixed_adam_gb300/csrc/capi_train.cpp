@@ -126,6 +126,7 @@ int zero_linear_forward(const zero_linear_t* shape, const void* x, const void* w
   L.y = static_cast<uint16_t*>(y);
   L.workspace = workspace;
   L.stream = static_cast<cudaStream_t>(stream);
+  L.withhold = withhold_copies();
   return launch_status(launch_linear_forward(L));
 }
 
@@ -179,6 +180,7 @@ int zero_linear_backward(const zero_linear_t* shape, const void* dy, const void*
   L.accumulate = (flags & ZERO_GRAD_ACCUMULATE) ? 1 : 0;
   L.workspace = workspace;
   L.stream = static_cast<cudaStream_t>(stream);
+  L.withhold = withhold_copies();
   return launch_status(launch_linear_backward(L));
 }
 

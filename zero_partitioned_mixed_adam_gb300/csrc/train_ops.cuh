@@ -68,6 +68,7 @@ struct LinearForwardLaunch {
   uint16_t *pre, *y;
   void* workspace;
   cudaStream_t stream;
+  int32_t withhold;  // test hook of the bounded waits (zero_test_withhold_copies)
 };
 
 struct LinearBackwardLaunch {
@@ -79,10 +80,14 @@ struct LinearBackwardLaunch {
   int32_t grad_f32, accumulate;
   void* workspace;
   cudaStream_t stream;
+  int32_t withhold;
 };
 
 int64_t linear_workspace(const zero_linear_t& s, bool backward);
 cudaError_t launch_linear_forward(const LinearForwardLaunch& L);
 cudaError_t launch_linear_backward(const LinearBackwardLaunch& L);
+// Status word of the products' bounded waits on the current device (0 = every
+// wait completed); read and cleared.  Returns -1 if CUDA fails.
+int read_and_clear_linear_status(int* status);
 
 }  // namespace zeroadam
