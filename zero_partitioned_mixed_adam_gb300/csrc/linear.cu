@@ -87,6 +87,118 @@ __device__ __forceinline__ Tile tile_of(const ProductArgs& a, int t) {
   return r;
 }
 
+// Which epilogue a product has, settled when the kernel is compiled.
+enum Kind {
+  kForward,   // bias, pre, activation, residual; bf16
+  kGradient,  // times an activation's slope, or added to what is there; bf16
+  kFloat,     // fp32, alone or added to what is there
+};
+
+// A warp's 32 x 32 part of D from shared memory, where row r's 16-byte piece q
+// (columns 4q to 4q+3) lies at piece q ^ (r & 7): bank conflicts neither where a
+// lane writes its row nor where 4 or 8 lanes read one.
+__device__ __forceinline__ int staged(int r, int q) { return r * 32 + ((q ^ (r & 7)) * 4); }
+
+// Any layout, and the edges: a lane takes one column, row after row.
+__device__ __noinline__ void epilogue_scalar(const Epilogue& e, const float* mine, int64_t row0,
+                                             int64_t col0, int64_t rows, int64_t cols, int lane) {
+  const int64_t j = col0 + lane;
+  if (j >= cols) return;
+  const int n = rows - row0 < 32 ? static_cast<int>(rows - row0) : 32;
+#pragma unroll 4
+  for (int r = 0; r < n; ++r)
+    epilogue_element(e, row0 + r, j, mine[staged(r, lane / 4) + lane % 4]);
+}
+
+// What the epilogue reads of a 32 x 32 part, asked for before the sums are there.
+template <Kind KIND>
+struct EpilogueReads {
+  uint4 x[KIND == kFloat ? 8 : 4];
+  __device__ __forceinline__ void issue(const Epilogue& e, int64_t row0, int64_t col0, int lane) {
+    if constexpr (KIND == kFloat) {
+      if (!e.accumulate) return;
+      const float* p = static_cast<const float*>(e.out) + (row0 + lane / 8) * e.ldo + col0 + 4 * (lane % 8);
+#pragma unroll
+      for (int q = 0; q < 8; ++q) x[q] = *reinterpret_cast<const uint4*>(p + 4 * q * e.ldo);
+    } else {
+      const uint16_t* p;
+      int64_t ld;
+      if constexpr (KIND == kForward) {
+        p = e.residual;
+        ld = e.ldr;
+      } else {
+        p = e.accumulate ? static_cast<const uint16_t*>(e.out) : e.slope_of;
+        ld = e.accumulate ? e.ldo : e.lds;
+      }
+      if (p == nullptr) return;
+      p += (row0 + lane / 4) * ld + col0 + 8 * (lane % 4);
+#pragma unroll
+      for (int q = 0; q < 4; ++q) x[q] = *reinterpret_cast<const uint4*>(p + 8 * q * ld);
+    }
+  }
+};
+
+// A whole 32 x 32 part in 16-byte accesses: 4 lanes take a row's 32 columns of
+// bf16, 8 lanes of fp32.
+template <Kind KIND>
+__device__ __forceinline__ void epilogue_vector(const Epilogue& e, const float* mine, int64_t row0,
+                                                int64_t col0, int lane,
+                                                const EpilogueReads<KIND>& reads) {
+  if constexpr (KIND == kFloat) {
+    float* p = static_cast<float*>(e.out) + (row0 + lane / 8) * e.ldo + col0 + 4 * (lane % 8);
+#pragma unroll
+    for (int q = 0; q < 8; ++q) {
+      float4 v = *reinterpret_cast<const float4*>(mine + staged(4 * q + lane / 8, lane % 8));
+      if (e.accumulate) {
+        v.x += __uint_as_float(reads.x[q].x);
+        v.y += __uint_as_float(reads.x[q].y);
+        v.z += __uint_as_float(reads.x[q].z);
+        v.w += __uint_as_float(reads.x[q].w);
+      }
+      *reinterpret_cast<float4*>(p + 4 * q * e.ldo) = v;
+    }
+  } else {
+    const int64_t row = row0 + lane / 4, col = col0 + 8 * (lane % 4);
+    uint16_t* p = static_cast<uint16_t*>(e.out) + row * e.ldo + col;
+    float bias[8];
+    if constexpr (KIND == kForward) {
+      if (e.bias != nullptr) bf16x8(*reinterpret_cast<const uint4*>(e.bias + col), bias);
+    }
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const int r = 8 * q + lane / 4;
+      float x[8];
+      const float4 u = *reinterpret_cast<const float4*>(mine + staged(r, 2 * (lane % 4)));
+      const float4 v = *reinterpret_cast<const float4*>(mine + staged(r, 2 * (lane % 4) + 1));
+      x[0] = u.x; x[1] = u.y; x[2] = u.z; x[3] = u.w;
+      x[4] = v.x; x[5] = v.y; x[6] = v.z; x[7] = v.w;
+      if constexpr (KIND == kForward) {
+        if (e.bias != nullptr) {
+#pragma unroll
+          for (int c = 0; c < 8; ++c) x[c] += bias[c];
+        }
+        if (e.pre != nullptr)
+          *reinterpret_cast<uint4*>(e.pre + (row + 8 * q) * e.ldp + col) = to_bf16x8(x);
+        act_value8(x, e.act);
+        if (e.residual != nullptr) {
+          float y[8];
+          bf16x8(reads.x[q], y);
+#pragma unroll
+          for (int c = 0; c < 8; ++c) x[c] += y[c];
+        }
+      } else if (e.accumulate) {
+        float y[8];
+        bf16x8(reads.x[q], y);
+#pragma unroll
+        for (int c = 0; c < 8; ++c) x[c] += y[c];
+      } else if (e.slope_of != nullptr) {
+        times_slope8(x, reads.x[q], e.slope_act);
+      }
+      *reinterpret_cast<uint4*>(p + 8 * q * e.ldo) = to_bf16x8(x);
+    }
+  }
+}
+
 // Persistent and specialised by warp.  Warp 0 brings the operands' tiles into a
 // ring of stages; warp 1 of the tile's first CTA issues the matrix
 // instructions, accumulating in one half of tensor memory while the other
@@ -97,7 +209,7 @@ __device__ __forceinline__ Tile tile_of(const ProductArgs& a, int t) {
 // first CTA) when every epilogue warp has read it.
 // Every wait is bounded; one that gives up sets g_linear_status and ends its
 // warp's loop, and the others' waits then run out too.
-template <int CG, int BN, bool A_MN, bool B_MN>
+template <int CG, int BN, bool A_MN, bool B_MN, Kind KIND>
 __global__ void __launch_bounds__(kProductThreads, 1)
     linear_product_kernel(const __grid_constant__ ProductArgs a) {
   using Shape = ProductShape<CG, BN>;
@@ -239,11 +351,14 @@ __global__ void __launch_bounds__(kProductThreads, 1)
       tc_fence_after();
       const int64_t row0 = tile.row + rank * kBlockRows + quarter * 32;
       Epilogue e = a.e;
-      e.out = e.out_f32 ? static_cast<void*>(static_cast<float*>(e.out) + tile.split * a.split_stride)
-                        : e.out;
+      if constexpr (KIND == kFloat) e.out = static_cast<float*>(e.out) + tile.split * a.split_stride;
 #pragma unroll 1
       for (int c = 0; c < BN / 2; c += 32) {
         const int at = half * (BN / 2) + c;
+        const int64_t col0 = tile.col + at;
+        const bool whole = e.vec && row0 + 32 <= a.rows && col0 + 32 <= a.cols;
+        EpilogueReads<KIND> reads;
+        if (whole) reads.issue(e, row0, col0, lane);
         uint32_t x[32];
         tmem_load32(tmem + (static_cast<uint32_t>(quarter * 32) << 16) + b * BN + at, x);
         tmem_load_wait();
@@ -255,35 +370,14 @@ __global__ void __launch_bounds__(kProductThreads, 1)
             else mbar_arrive(&free_[b]);
           }
         }
-        // Through shared memory into rows: a lane holds 32 columns of one row, and
-        // takes 4 columns of 8 rows, so that 8 lanes cover a row's 32.  The 16-byte
-        // pieces of a row are permuted by its number, against bank conflicts.
-        __syncwarp();
+        __syncwarp();  // the part before has been read
 #pragma unroll
         for (int q = 0; q < 8; ++q)
-          *reinterpret_cast<uint4*>(mine + lane * 32 + ((q ^ (lane & 7)) * 4)) =
+          *reinterpret_cast<uint4*>(mine + staged(lane, q)) =
               make_uint4(x[4 * q], x[4 * q + 1], x[4 * q + 2], x[4 * q + 3]);
         __syncwarp();
-        const int64_t j = tile.col + at + 4 * (lane % 8);
-        const int cols = a.cols - j < 4 ? (a.cols > j ? static_cast<int>(a.cols - j) : 0) : 4;
-#pragma unroll
-        for (int g = 0; g < 2; ++g) {
-          EpilogueInputs in[4];
-          float d[4][4];
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            const int r = (4 * g + q) * 4 + lane / 8;
-            const float4 v = *reinterpret_cast<const float4*>(
-                mine + r * 32 + (((lane % 8) ^ (r & 7)) * 4));
-            d[q][0] = v.x; d[q][1] = v.y; d[q][2] = v.z; d[q][3] = v.w;
-            if (cols > 0 && row0 + r < a.rows) epilogue_load4(e, row0 + r, j, cols, in[q]);
-          }
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            const int r = (4 * g + q) * 4 + lane / 8;
-            if (cols > 0 && row0 + r < a.rows) epilogue_store4(e, row0 + r, j, cols, in[q], d[q]);
-          }
-        }
+        if (whole) epilogue_vector<KIND>(e, mine, row0, col0, lane, reads);
+        else epilogue_scalar(e, mine, row0, col0, a.rows, a.cols, lane);
       }
     }
   }
@@ -307,15 +401,14 @@ __global__ void __launch_bounds__(256) linear_join_kernel(const __grid_constant_
   for (int64_t q = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; q < a.rows * quads;
        q += static_cast<int64_t>(gridDim.x) * blockDim.x) {
     const int64_t i = q / quads, j = (q - i * quads) * 4;
-    const int n = a.cols - j < 4 ? static_cast<int>(a.cols - j) : 4;
-    EpilogueInputs in;
-    epilogue_load4(a.e, i, j, n, in);
     float x[4] = {};
     for (int s = 0; s < a.splits; ++s) {
       const float4 v = __ldcg(reinterpret_cast<const float4*>(a.parts + s * a.stride + i * a.ld + j));
       x[0] += v.x; x[1] += v.y; x[2] += v.z; x[3] += v.w;
     }
-    epilogue_store4(a.e, i, j, n, in, x);
+#pragma unroll
+    for (int c = 0; c < 4; ++c)
+      if (j + c < a.cols) epilogue_element(a.e, i, j + c, x[c]);
   }
 }
 
@@ -465,10 +558,10 @@ int64_t parts_bytes(const Plan& p, int64_t rows, int64_t cols) {
   return p.splits > 1 ? round_up(p.splits * rows * round_up(cols, 4) * 4, 256) : 0;
 }
 
-template <int CG, int BN, bool A_MN, bool B_MN>
+template <int CG, int BN, bool A_MN, bool B_MN, Kind KIND>
 cudaError_t launch_shape(const Product& p, const Plan& plan, ProductArgs& a, cudaStream_t stream) {
   using Shape = ProductShape<CG, BN>;
-  auto kernel = linear_product_kernel<CG, BN, A_MN, B_MN>;
+  auto kernel = linear_product_kernel<CG, BN, A_MN, B_MN, KIND>;
   static std::mutex mu;
   static bool configured[64] = {false};
   int dev = 0, sms = 0;
@@ -506,19 +599,20 @@ cudaError_t launch_shape(const Product& p, const Plan& plan, ProductArgs& a, cud
   return cudaLaunchKernelEx(&config, kernel, a);
 }
 
-template <bool A_MN, bool B_MN>
-cudaError_t launch_majors(const Product& p, const Plan& plan, ProductArgs& a, cudaStream_t stream) {
-  if (plan.cg == 2 && plan.bn == 256) return launch_shape<2, 256, A_MN, B_MN>(p, plan, a, stream);
-  if (plan.cg == 2) return launch_shape<2, 128, A_MN, B_MN>(p, plan, a, stream);
-  return launch_shape<1, 128, A_MN, B_MN>(p, plan, a, stream);
+template <bool A_MN, bool B_MN, Kind KIND>
+cudaError_t launch_kind(const Product& p, const Plan& plan, ProductArgs& a, cudaStream_t stream) {
+  if (plan.cg == 2 && plan.bn == 256)
+    return launch_shape<2, 256, A_MN, B_MN, KIND>(p, plan, a, stream);
+  if (plan.cg == 2) return launch_shape<2, 128, A_MN, B_MN, KIND>(p, plan, a, stream);
+  return launch_shape<1, 128, A_MN, B_MN, KIND>(p, plan, a, stream);
 }
 
 void set_vec(Epilogue* e) {
-  auto ok = [](const void* p, int64_t ld, uintptr_t bytes) {
-    return p == nullptr || (aligned(p, bytes) && ld % 4 == 0);
+  auto ok = [](const void* p, int64_t ld, int bytes) {
+    return p == nullptr || (aligned(p, 16) && ld * bytes % 16 == 0);
   };
-  e->vec = ok(e->bias, 0, 8) && ok(e->pre, e->ldp, 8) && ok(e->residual, e->ldr, 8) &&
-           ok(e->slope_of, e->lds, 8) && ok(e->out, e->ldo, e->out_f32 ? 16 : 8);
+  e->vec = ok(e->bias, 0, 2) && ok(e->pre, e->ldp, 2) && ok(e->residual, e->ldr, 2) &&
+           ok(e->slope_of, e->lds, 2) && ok(e->out, e->ldo, e->out_f32 ? 4 : 2);
 }
 
 cudaError_t launch_product(Product p, Space space, int withhold, cudaStream_t stream) {
@@ -551,9 +645,16 @@ cudaError_t launch_product(Product p, Space space, int withhold, cudaStream_t st
     a.e.vec = 1;
     a.split_stride = join.stride;
   }
-  err = p.a_mn   ? launch_majors<true, true>(p, plan, a, stream)
-        : p.b_mn ? launch_majors<false, true>(p, plan, a, stream)
-                 : launch_majors<false, false>(p, plan, a, stream);
+  const bool f32 = a.e.out_f32 != 0;
+  if (p.a_mn)
+    err = f32 ? launch_kind<true, true, kFloat>(p, plan, a, stream)
+              : launch_kind<true, true, kGradient>(p, plan, a, stream);
+  else if (p.b_mn)
+    err = f32 ? launch_kind<false, true, kFloat>(p, plan, a, stream)
+              : launch_kind<false, true, kGradient>(p, plan, a, stream);
+  else
+    err = f32 ? launch_kind<false, false, kFloat>(p, plan, a, stream)
+              : launch_kind<false, false, kForward>(p, plan, a, stream);
   if (err != cudaSuccess || plan.splits == 1) return err;
   const int64_t blocks = (p.rows * (join.ld / 4) + 255) / 256;
   linear_join_kernel<<<static_cast<unsigned>(blocks < 4096 ? blocks : 4096), 256, 0, stream>>>(join);
@@ -566,33 +667,87 @@ int64_t product_bytes(const Stored& a, const Stored& b, int64_t rows, int64_t co
 }
 
 // dz = bf16(dy * act'(pre)), and each column's sum of it before the rounding.
-// A block takes 32 columns and all rows, 8 at a time.
+// One pass over dy and pre, bound by HBM bandwidth: a warp takes 256 columns of
+// a row, 8 a lane, and a block 8 warps' rows in turn over kSlopeRows of them.
+// The block's column sums go to the workspace and linear_dbias_kernel adds them
+// in the blocks' order.
+constexpr int kSlopeRows = 128, kSlopeCols = 256;
+
 struct SlopeArgs {
   const uint16_t *dy, *pre;
   int64_t ldy, ldp, rows, cols;
   int32_t act;
+  int32_t vec;   // 16-byte accesses
   uint16_t* dz;  // NULL: sums only
   int64_t ldz;
-  void* dbias;   // NULL: dz only
-  int32_t out_f32, accumulate;
+  float* sums;   // [row blocks][cols], NULL: dz only
 };
 
 __global__ void __launch_bounds__(256) linear_slope_kernel(const __grid_constant__ SlopeArgs a) {
+  __shared__ float part[8][kSlopeCols];
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int64_t j0 = static_cast<int64_t>(blockIdx.x) * kSlopeCols;
+  const int64_t first = static_cast<int64_t>(blockIdx.y) * kSlopeRows;
+  const int64_t last = first + kSlopeRows < a.rows ? first + kSlopeRows : a.rows;
+  float sum[8] = {};
+  if (a.vec && j0 + kSlopeCols <= a.cols) {
+    const int64_t j = j0 + 8 * lane;
+#pragma unroll 4
+    for (int64_t i = first + warp; i < last; i += 8) {
+      float x[8];
+      bf16x8(__ldcs(reinterpret_cast<const uint4*>(a.dy + i * a.ldy + j)), x);
+      if (a.act != ZERO_ACT_NONE)
+        times_slope8(x, __ldcs(reinterpret_cast<const uint4*>(a.pre + i * a.ldp + j)), a.act);
+      if (a.dz != nullptr) *reinterpret_cast<uint4*>(a.dz + i * a.ldz + j) = to_bf16x8(x);
+#pragma unroll
+      for (int c = 0; c < 8; ++c) sum[c] += x[c];
+    }
+#pragma unroll
+    for (int c = 0; c < 8; ++c) part[warp][8 * lane + c] = sum[c];
+  } else {
+    for (int64_t i = first + warp; i < last; i += 8) {
+#pragma unroll
+      for (int c = 0; c < 8; ++c) {
+        const int64_t j = j0 + 32 * c + lane;
+        if (j >= a.cols) continue;
+        float x = bf16_at(a.dy + i * a.ldy + j);
+        if (a.act != ZERO_ACT_NONE) x *= act_slope(bf16_at(a.pre + i * a.ldp + j), a.act);
+        if (a.dz != nullptr) a.dz[i * a.ldz + j] = to_bf16(x);
+        sum[c] += x;
+      }
+    }
+#pragma unroll
+    for (int c = 0; c < 8; ++c) part[warp][32 * c + lane] = sum[c];
+  }
+  if (a.sums == nullptr) return;
+  __syncthreads();
+  const int64_t j = j0 + threadIdx.x;
+  if (j >= a.cols) return;
+  float s = 0.0f;
+#pragma unroll
+  for (int k = 0; k < 8; ++k) s += part[k][threadIdx.x];
+  a.sums[blockIdx.y * a.cols + j] = s;
+}
+
+struct DbiasArgs {
+  const float* sums;
+  int64_t cols;
+  int32_t blocks;
+  void* dbias;
+  int32_t out_f32, accumulate;
+};
+
+// 32 columns a block, 8 runs of row blocks each.
+__global__ void __launch_bounds__(256) linear_dbias_kernel(const __grid_constant__ DbiasArgs a) {
   __shared__ float part[8][32];
   const int64_t j = static_cast<int64_t>(blockIdx.x) * 32 + threadIdx.x % 32;
   const int r = threadIdx.x / 32;
   float sum = 0.0f;
-  if (j < a.cols) {
-    for (int64_t i = r; i < a.rows; i += 8) {
-      float x = bf16_at(a.dy + i * a.ldy + j);
-      if (a.act != ZERO_ACT_NONE) x *= act_slope(bf16_at(a.pre + i * a.ldp + j), a.act);
-      if (a.dz != nullptr) a.dz[i * a.ldz + j] = to_bf16(x);
-      sum += x;
-    }
-  }
+  if (j < a.cols)
+    for (int k = r; k < a.blocks; k += 8) sum += __ldcg(a.sums + k * a.cols + j);
   part[r][threadIdx.x % 32] = sum;
   __syncthreads();
-  if (r != 0 || j >= a.cols || a.dbias == nullptr) return;
+  if (r != 0 || j >= a.cols) return;
 #pragma unroll
   for (int k = 1; k < 8; ++k) sum += part[k][threadIdx.x];
   if (a.out_f32) {
@@ -603,6 +758,8 @@ __global__ void __launch_bounds__(256) linear_slope_kernel(const __grid_constant
     *o = to_bf16(a.accumulate ? bf16_at(o) + sum : sum);
   }
 }
+
+int64_t slope_blocks(int64_t rows) { return (rows + kSlopeRows - 1) / kSlopeRows; }
 
 }  // namespace
 
@@ -621,7 +778,7 @@ int64_t linear_workspace(const zero_linear_t& s, bool backward) {
   // dz is laid out once and taken by both products, one after the other
   const int64_t dx = product_bytes(none, w, s.rows, s.in, s.out);
   const int64_t dw = product_bytes(none, x, s.out, s.in, s.rows);
-  return copy_bytes(z) + (dx > dw ? dx : dw);
+  return copy_bytes(z) + round_up(slope_blocks(s.rows) * s.out * 4, 256) + (dx > dw ? dx : dw);
 }
 
 cudaError_t launch_linear_forward(const LinearForwardLaunch& L) {
@@ -650,15 +807,41 @@ cudaError_t launch_linear_backward(const LinearBackwardLaunch& L) {
   Stored dz{L.dy, s.rows, s.out, s.ldy};
   Space space{static_cast<char*>(L.workspace)};
   if (L.act != ZERO_ACT_NONE || L.dbias != nullptr) {
-    SlopeArgs a{L.dy, L.pre, s.ldy, s.ldp, s.rows, s.out, L.act, nullptr, 0, L.dbias,
-                L.grad_f32, L.accumulate};
+    SlopeArgs a{};
+    a.dy = L.dy;
+    a.pre = L.pre;
+    a.ldy = s.ldy;
+    a.ldp = s.ldp;
+    a.rows = s.rows;
+    a.cols = s.out;
+    a.act = L.act;
     if (L.act != ZERO_ACT_NONE && (L.dx != nullptr || L.dw != nullptr)) {
       a.dz = static_cast<uint16_t*>(space.take(copy_bytes(dz)));
       a.ldz = round_up(s.out, 8);
-      dz.p = a.dz;
-      dz.ld = a.ldz;
+      dz = Stored(a.dz, s.rows, s.out, a.ldz);
     }
-    linear_slope_kernel<<<static_cast<unsigned>((s.out + 31) / 32), 256, 0, L.stream>>>(a);
+    const int64_t blocks = slope_blocks(s.rows);
+    if (L.dbias != nullptr) a.sums = static_cast<float*>(space.take(blocks * s.out * 4));
+    a.vec = tileable(Stored(L.dy, s.rows, s.out, s.ldy)) &&
+            (L.act == ZERO_ACT_NONE || tileable(Stored(L.pre, s.rows, s.out, s.ldp)));
+    const int64_t across = (s.out + kSlopeCols - 1) / kSlopeCols;
+    // the grid's y side ends at 65535
+    for (int64_t k = 0; k < blocks; k += 65535) {
+      SlopeArgs part = a;
+      const int64_t skip = k * kSlopeRows;
+      part.dy += skip * s.ldy;
+      part.pre += L.act != ZERO_ACT_NONE ? skip * s.ldp : 0;
+      part.dz += a.dz != nullptr ? skip * a.ldz : 0;
+      part.sums += a.sums != nullptr ? k * s.out : 0;
+      part.rows -= skip;
+      const int64_t high = blocks - k < 65535 ? blocks - k : 65535;
+      linear_slope_kernel<<<dim3(static_cast<unsigned>(across), static_cast<unsigned>(high)), 256, 0,
+                            L.stream>>>(part);
+    }
+    if (L.dbias != nullptr) {
+      const DbiasArgs d{a.sums, s.out, static_cast<int32_t>(blocks), L.dbias, L.grad_f32, L.accumulate};
+      linear_dbias_kernel<<<static_cast<unsigned>((s.out + 31) / 32), 256, 0, L.stream>>>(d);
+    }
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
   }

@@ -65,97 +65,69 @@ struct Epilogue {
   void* out;                 // bf16, or fp32
   int64_t ldo;
   int32_t out_f32, accumulate;
-  int32_t vec;               // 4 columns at a time: every matrix's base and pitch allow it
+  int32_t vec;               // 16-byte accesses: every matrix's base and pitch allow them
 };
 
-__device__ __forceinline__ float4 bf16x4(const uint2 r) {
-  return make_float4(__uint_as_float(r.x << 16), __uint_as_float(r.x & 0xffff0000u),
-                     __uint_as_float(r.y << 16), __uint_as_float(r.y & 0xffff0000u));
-}
-__device__ __forceinline__ uint2 to_bf16x4(const float x[4]) {
-  return make_uint2(to_bf16(x[0]) | (static_cast<uint32_t>(to_bf16(x[1])) << 16),
-                    to_bf16(x[2]) | (static_cast<uint32_t>(to_bf16(x[3])) << 16));
-}
+// ---- one element, any layout
 
-// What the epilogue reads of 4 columns (j a multiple of 4) of row i.
-struct EpilogueInputs {
-  float bias[4], residual[4], slope_of[4], old[4];
-};
-
-// n: how many of the 4 columns exist.
-__device__ __forceinline__ void epilogue_load4(const Epilogue& e, int64_t i, int64_t j, int n,
-                                               EpilogueInputs& in) {
-  auto take = [&](const uint16_t* p, float x[4]) {
-    if (e.vec && n == 4) {
-      const float4 v = bf16x4(*reinterpret_cast<const uint2*>(p));
-      x[0] = v.x; x[1] = v.y; x[2] = v.z; x[3] = v.w;
-    } else {
-#pragma unroll
-      for (int c = 0; c < 4; ++c) x[c] = c < n ? bf16_at(p + c) : 0.0f;
-    }
-  };
-  if (e.bias != nullptr) take(e.bias + j, in.bias);
-  if (e.residual != nullptr) take(e.residual + i * e.ldr + j, in.residual);
-  if (e.slope_of != nullptr) take(e.slope_of + i * e.lds + j, in.slope_of);
-  if (e.accumulate) {
-    if (!e.out_f32) {
-      take(static_cast<const uint16_t*>(e.out) + i * e.ldo + j, in.old);
-    } else {
-      const float* p = static_cast<const float*>(e.out) + i * e.ldo + j;
-      if (e.vec && n == 4) {
-        const float4 v = *reinterpret_cast<const float4*>(p);
-        in.old[0] = v.x; in.old[1] = v.y; in.old[2] = v.z; in.old[3] = v.w;
-      } else {
-#pragma unroll
-        for (int c = 0; c < 4; ++c) in.old[c] = c < n ? p[c] : 0.0f;
-      }
-    }
-  }
-}
-
-__device__ __forceinline__ void epilogue_store4(const Epilogue& e, int64_t i, int64_t j, int n,
-                                                const EpilogueInputs& in, float x[4]) {
-  auto put = [&](uint16_t* p) {
-    if (e.vec && n == 4) {
-      *reinterpret_cast<uint2*>(p) = to_bf16x4(x);
-    } else {
-#pragma unroll
-      for (int c = 0; c < 4; ++c)
-        if (c < n) p[c] = to_bf16(x[c]);
-    }
-  };
-  if (e.bias != nullptr) {
-#pragma unroll
-    for (int c = 0; c < 4; ++c) x[c] += in.bias[c];
-  }
-  if (e.pre != nullptr) put(e.pre + i * e.ldp + j);
-  if (e.act != ZERO_ACT_NONE) {
-#pragma unroll
-    for (int c = 0; c < 4; ++c) x[c] = act_value(x[c], e.act);
-  }
-  if (e.residual != nullptr) {
-#pragma unroll
-    for (int c = 0; c < 4; ++c) x[c] += in.residual[c];
-  }
-  if (e.slope_of != nullptr) {
-#pragma unroll
-    for (int c = 0; c < 4; ++c) x[c] *= act_slope(in.slope_of[c], e.slope_act);
-  }
-  if (e.accumulate) {
-#pragma unroll
-    for (int c = 0; c < 4; ++c) x[c] += in.old[c];
-  }
-  if (!e.out_f32) {
-    put(static_cast<uint16_t*>(e.out) + i * e.ldo + j);
+__device__ __forceinline__ void epilogue_element(const Epilogue& e, int64_t i, int64_t j, float x) {
+  if (e.bias != nullptr) x += bf16_at(e.bias + j);
+  if (e.pre != nullptr) e.pre[i * e.ldp + j] = to_bf16(x);
+  x = act_value(x, e.act);
+  if (e.residual != nullptr) x += bf16_at(e.residual + i * e.ldr + j);
+  if (e.slope_of != nullptr) x *= act_slope(bf16_at(e.slope_of + i * e.lds + j), e.slope_act);
+  if (e.out_f32) {
+    float* o = static_cast<float*>(e.out) + i * e.ldo + j;
+    *o = e.accumulate ? *o + x : x;
   } else {
-    float* p = static_cast<float*>(e.out) + i * e.ldo + j;
-    if (e.vec && n == 4) {
-      *reinterpret_cast<float4*>(p) = make_float4(x[0], x[1], x[2], x[3]);
-    } else {
+    uint16_t* o = static_cast<uint16_t*>(e.out) + i * e.ldo + j;
+    *o = to_bf16(e.accumulate ? bf16_at(o) + x : x);
+  }
+}
+
+// ---- 8 columns as one 16-byte vector of bf16
+
+__device__ __forceinline__ void bf16x8(const uint4 r, float x[8]) {
+  const uint32_t w[4] = {r.x, r.y, r.z, r.w};
 #pragma unroll
-      for (int c = 0; c < 4; ++c)
-        if (c < n) p[c] = x[c];
-    }
+  for (int c = 0; c < 4; ++c) {
+    x[2 * c] = __uint_as_float(w[c] << 16);
+    x[2 * c + 1] = __uint_as_float(w[c] & 0xffff0000u);
+  }
+}
+__device__ __forceinline__ uint32_t bf16x2_bits(float lo, float hi) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ uint4 to_bf16x8(const float x[8]) {
+  return make_uint4(bf16x2_bits(x[0], x[1]), bf16x2_bits(x[2], x[3]), bf16x2_bits(x[4], x[5]),
+                    bf16x2_bits(x[6], x[7]));
+}
+// One branch for the 8 of them.
+__device__ __forceinline__ void act_value8(float x[8], int act) {
+  if (act == ZERO_ACT_GELU) {
+#pragma unroll
+    for (int c = 0; c < 8; ++c) x[c] = act_value(x[c], ZERO_ACT_GELU);
+  } else if (act == ZERO_ACT_SILU) {
+#pragma unroll
+    for (int c = 0; c < 8; ++c) x[c] = act_value(x[c], ZERO_ACT_SILU);
+  } else if (act == ZERO_ACT_RELU) {
+#pragma unroll
+    for (int c = 0; c < 8; ++c) x[c] = act_value(x[c], ZERO_ACT_RELU);
+  }
+}
+__device__ __forceinline__ void times_slope8(float x[8], const uint4 at, int act) {
+  float z[8];
+  bf16x8(at, z);
+  if (act == ZERO_ACT_GELU) {
+#pragma unroll
+    for (int c = 0; c < 8; ++c) x[c] *= act_slope(z[c], ZERO_ACT_GELU);
+  } else if (act == ZERO_ACT_SILU) {
+#pragma unroll
+    for (int c = 0; c < 8; ++c) x[c] *= act_slope(z[c], ZERO_ACT_SILU);
+  } else if (act == ZERO_ACT_RELU) {
+#pragma unroll
+    for (int c = 0; c < 8; ++c) x[c] *= act_slope(z[c], ZERO_ACT_RELU);
   }
 }
 
