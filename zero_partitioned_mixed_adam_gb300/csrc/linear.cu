@@ -26,7 +26,9 @@ __global__ void take_linear_status_kernel() {
   g_linear_status_taken = atomicExch(&g_linear_status, 0);
 }
 
-constexpr int kDepth = 64;         // steps of the reduction in one stage: 128 bytes of bf16
+constexpr int kDepth = 64;         // steps of the reduction in one swizzled tile: 128 bytes
+constexpr int kSub = 2;            // such tiles of each operand in one stage
+constexpr int kStep = kSub * kDepth;
 constexpr int kBlockRows = 128;    // rows of D per CTA: the lanes of tensor memory
 constexpr int kEpilogueWarps = 8;  // two per quarter of the lanes
 constexpr int kProductThreads = 64 + 32 * kEpilogueWarps;
@@ -40,13 +42,14 @@ struct ProductShape {
   static constexpr int kBRows = BN / CG;
   static constexpr int kABytes = kBlockRows * kDepth * 2;
   static constexpr int kBBytes = kBRows * kDepth * 2;
-  static constexpr int kStage = kABytes + kBBytes;
+  static constexpr int kPair = kABytes + kBBytes;
+  static constexpr int kStage = kSub * kPair;
   static constexpr int kStaging = kEpilogueWarps * 32 * 32 * 4;
   static constexpr int kBarriers = 512;
   static constexpr int kStages = (227 * 1024 - 1024 - kStaging - kBarriers) / kStage;
   static constexpr int kSmem = kStages * kStage + kStaging + kBarriers + 1024;
   static constexpr int kColumns = 2 * BN < 32 ? 32 : 2 * BN;  // of tensor memory: two tiles
-  static_assert(kStages >= 3 && 2 * kStages + 5 <= kBarriers / 8, "stages");
+  static_assert(kStages >= 2 && 2 * kStages + 5 <= kBarriers / 8, "stages");
   static_assert(kColumns <= 512 && BN % 64 == 0, "tensor memory");
 };
 
@@ -199,6 +202,19 @@ __device__ __forceinline__ void epilogue_vector(const Epilogue& e, const float* 
   }
 }
 
+// Place in the ring of stages: the stage, and the parity of its barriers' phase.
+template <int STAGES>
+struct Place {
+  int s = 0;
+  uint32_t phase = 0;
+  __device__ __forceinline__ void next() {
+    if (++s == STAGES) {
+      s = 0;
+      phase ^= 1;
+    }
+  }
+};
+
 // Persistent and specialised by warp.  Warp 0 brings the operands' tiles into a
 // ring of stages; warp 1 of the tile's first CTA issues the matrix
 // instructions, accumulating in one half of tensor memory while the other
@@ -251,49 +267,60 @@ __global__ void __launch_bounds__(kProductThreads, 1)
 
   if (warp == 0) {
     if (lane == 0) {
-      int64_t k = 0;  // stages issued
+      Place<kStages> at;
+      int issued = 0;  // stages, up to the ring's
       bool ok = true;
       for (int t = unit; t < tiles && ok; t += units) {
         const Tile tile = tile_of<BM, BN>(a, t);
         const int ra = static_cast<int>(tile.row) + rank * kBlockRows;
         const int rb = static_cast<int>(tile.col) + rank * Shape::kBRows;
-        for (int step = tile.first; step < tile.last; ++step, ++k) {
-          const int s = static_cast<int>(k % kStages);
-          if (k >= kStages && !mbar_wait(&empty[s], static_cast<uint32_t>((k / kStages - 1) & 1))) {
-            ok = false;
-            break;
+        for (int step = tile.first; step < tile.last; ++step, at.next()) {
+          if (issued == kStages) {
+            if (!mbar_wait(&empty[at.s], at.phase ^ 1)) {
+              ok = false;
+              break;
+            }
+          } else {
+            ++issued;
           }
           if (a.withhold) continue;
-          uint8_t* sa = ring + s * Shape::kStage;
-          uint8_t* sb = sa + Shape::kABytes;
-          const uint32_t bar = CG == 2 ? peer_addr(&full[s], 0) : smem_addr(&full[s]);
-          if (rank == 0) mbar_expect_tx(&full[s], CG * Shape::kStage);
-          const int x = step * kDepth;
-          if constexpr (A_MN) {
+          const uint32_t bar = CG == 2 ? peer_addr(&full[at.s], 0) : smem_addr(&full[at.s]);
+          if (rank == 0) mbar_expect_tx(&full[at.s], CG * Shape::kStage);
 #pragma unroll
-            for (int c = 0; c < kBlockRows / 64; ++c)
-              tile_load<CG>(sa + c * 64 * kDepth * 2, &a.a, ra + 64 * c, x, bar);
-          } else {
-            tile_load<CG>(sa, &a.a, x, ra, bar);
-          }
-          if constexpr (B_MN) {
+          for (int h = 0; h < kSub; ++h) {
+            uint8_t* sa = ring + at.s * Shape::kStage + h * Shape::kPair;
+            uint8_t* sb = sa + Shape::kABytes;
+            const int x = step * kStep + h * kDepth;
+            if constexpr (A_MN) {
 #pragma unroll
-            for (int c = 0; c < Shape::kBRows / 64; ++c)
-              tile_load<CG>(sb + c * 64 * kDepth * 2, &a.b, rb + 64 * c, x, bar);
-          } else {
-            tile_load<CG>(sb, &a.b, x, rb, bar);
+              for (int c = 0; c < kBlockRows / 64; ++c)
+                tile_load<CG>(sa + c * 64 * kDepth * 2, &a.a, ra + 64 * c, x, bar);
+            } else {
+              tile_load<CG>(sa, &a.a, x, ra, bar);
+            }
+            if constexpr (B_MN) {
+#pragma unroll
+              for (int c = 0; c < Shape::kBRows / 64; ++c)
+                tile_load<CG>(sb + c * 64 * kDepth * 2, &a.b, rb + 64 * c, x, bar);
+            } else {
+              tile_load<CG>(sb, &a.b, x, rb, bar);
+            }
           }
         }
       }
       if (!ok) atomicExch(&g_linear_status, 1);
       // No CTA ends while loads into it, or arrivals on its barriers, are under
       // way: the products that read the last stages are waited for.
-      if (!a.withhold)
-        for (int64_t j = k > kStages ? k - kStages : 0; j < k; ++j)
-          mbar_wait(&empty[j % kStages], static_cast<uint32_t>((j / kStages) & 1));
-      if (!ok && rank == 0 && !a.withhold)
-        for (int64_t j = k > kStages ? k - kStages : 0; j < k; ++j)
-          mbar_wait(&full[j % kStages], static_cast<uint32_t>((j / kStages) & 1));
+      if (!a.withhold) {
+        if (issued < kStages) at = Place<kStages>();
+        for (int j = 0; j < issued; ++j, at.next()) {
+          // stage at.s was filled last in the phase before this place's, or, in a
+          // ring not yet full, in its first
+          const uint32_t phase = issued < kStages ? at.phase : at.phase ^ 1;
+          mbar_wait(&empty[at.s], phase);
+          if (!ok && rank == 0) mbar_wait(&full[at.s], phase);
+        }
+      }
     }
   } else if (warp == 1) {
     if (rank == 0 && lane == 0) {
@@ -302,8 +329,9 @@ __global__ void __launch_bounds__(kProductThreads, 1)
       // smem_desc, along each operand's rows
       constexpr uint32_t step_a = A_MN ? 16 * 128 : 32, step_b = B_MN ? 16 * 128 : 32;
       constexpr uint32_t lead = 64 * kDepth * 2, stride = 1024;
-      int64_t k = 0;
-      int n = 0;  // tiles begun
+      Place<kStages> at;
+      int used = 0;  // stages, up to the ring's
+      int n = 0;     // tiles begun
       bool ok = true;
       for (int t = unit; t < tiles && ok; t += units, ++n) {
         const Tile tile = tile_of<BM, BN>(a, t);
@@ -313,28 +341,33 @@ __global__ void __launch_bounds__(kProductThreads, 1)
           break;
         }
         tc_fence_after();
-        for (int step = tile.first; step < tile.last; ++step, ++k) {
-          const int s = static_cast<int>(k % kStages);
-          if (!mbar_wait(&full[s], static_cast<uint32_t>((k / kStages) & 1))) {
+        for (int step = tile.first; step < tile.last; ++step, at.next()) {
+          if (!mbar_wait(&full[at.s], at.phase)) {
             ok = false;
             break;
           }
           tc_fence_after();
-          const uint32_t sa = smem_addr(ring + s * Shape::kStage), sb = sa + Shape::kABytes;
-          const uint64_t da = smem_desc(sa, lead, stride), db = smem_desc(sb, lead, stride);
+          if (used < kStages) ++used;
 #pragma unroll
-          for (int q = 0; q < kDepth / 16; ++q)
-            mma_bf16<CG>(tmem + b * BN, da + q * (step_a >> 4), db + q * (step_b >> 4), desc,
-                         step > tile.first || q > 0);
-          mma_commit<CG>(&empty[s]);
+          for (int h = 0; h < kSub; ++h) {
+            const uint32_t sa = smem_addr(ring) + at.s * Shape::kStage + h * Shape::kPair;
+            const uint64_t da = smem_desc(sa, lead, stride);
+            const uint64_t db = smem_desc(sa + Shape::kABytes, lead, stride);
+#pragma unroll
+            for (int q = 0; q < kDepth / 16; ++q)
+              mma_bf16<CG>(tmem + b * BN, da + q * (step_a >> 4), db + q * (step_b >> 4), desc,
+                           step > tile.first || q > 0 || h > 0);
+          }
+          mma_commit<CG>(&empty[at.s]);
         }
         if (ok) mma_commit<CG>(&done[b]);
       }
       if (!ok) {
         // products already issued end before tensor memory is freed
         atomicExch(&g_linear_status, 2);
-        for (int64_t j = k > kStages ? k - kStages : 0; j < k; ++j)
-          mbar_wait(&empty[j % kStages], static_cast<uint32_t>((j / kStages) & 1));
+        if (used < kStages) at = Place<kStages>();
+        for (int j = 0; j < used; ++j, at.next())
+          mbar_wait(&empty[at.s], used < kStages ? at.phase : at.phase ^ 1);
       }
     }
   } else {
@@ -527,7 +560,7 @@ struct Plan {
 };
 
 Plan plan_product(int64_t rows, int64_t cols, int64_t depth) {
-  const int64_t steps = (depth + kDepth - 1) / kDepth;
+  const int64_t steps = (depth + kStep - 1) / kStep;
   Plan best{2, 256, 1};
   if (rows < 1 || cols < 1) return best;
   double least = 1e300;
@@ -544,7 +577,7 @@ Plan plan_product(int64_t rows, int64_t cols, int64_t depth) {
       int64_t splits = 1;
       if (tiles * 2 <= units) {  // most SMs would idle: the reduction is cut
         splits = units / tiles;
-        if (splits > steps / 4) splits = steps / 4;
+        if (splits > steps / 2) splits = steps / 2;
         if (splits > 16) splits = 16;
         if (splits < 1) splits = 1;
       }
@@ -626,7 +659,7 @@ cudaError_t launch_product(Product p, Space space, int withhold, cudaStream_t st
   a.rows = p.rows;
   a.cols = p.cols;
   a.splits = plan.splits;
-  a.steps = static_cast<int32_t>((p.depth + kDepth - 1) / kDepth);
+  a.steps = static_cast<int32_t>((p.depth + kStep - 1) / kStep);
   a.withhold = withhold;
   JoinArgs join{};
   if (plan.splits > 1) {
