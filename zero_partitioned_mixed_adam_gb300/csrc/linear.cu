@@ -113,94 +113,95 @@ __device__ __noinline__ void epilogue_scalar(const Epilogue& e, const float* min
     epilogue_element(e, row0 + r, j, mine[staged(r, lane / 4) + lane % 4]);
 }
 
-// What the epilogue reads of a 32 x 32 part, asked for before the sums are there.
+// A whole 32 x 32 part in 16-byte accesses: 4 lanes take a row's 32 columns of
+// bf16 (8 rows at a time), 8 lanes of fp32 (4 rows).
 template <Kind KIND>
-struct EpilogueReads {
-  uint4 x[KIND == kFloat ? 8 : 4];
-  __device__ __forceinline__ void issue(const Epilogue& e, int64_t row0, int64_t col0, int lane) {
+struct EpilogueVector {
+  static constexpr int kLanes = KIND == kFloat ? 8 : 4, kHeight = 32 / kLanes, kTimes = kLanes;
+  // What it reads: the residual, the slope's argument or the old value, 16 bytes
+  // a lane and time; asked for one part ahead of its use.
+  uint4 in[kTimes];
+  const char* from;   // NULL: nothing is read
+  int64_t from_pitch;  // bytes
+
+  __device__ __forceinline__ void begin(const Epilogue& e) {
     if constexpr (KIND == kFloat) {
-      if (!e.accumulate) return;
-      const float* p = static_cast<const float*>(e.out) + (row0 + lane / 8) * e.ldo + col0 + 4 * (lane % 8);
-#pragma unroll
-      for (int q = 0; q < 8; ++q) x[q] = *reinterpret_cast<const uint4*>(p + 4 * q * e.ldo);
+      from = e.accumulate ? static_cast<const char*>(e.out) : nullptr;
+      from_pitch = 4 * e.ldo;
+    } else if constexpr (KIND == kForward) {
+      from = reinterpret_cast<const char*>(e.residual);
+      from_pitch = 2 * e.ldr;
     } else {
-      const uint16_t* p;
-      int64_t ld;
-      if constexpr (KIND == kForward) {
-        p = e.residual;
-        ld = e.ldr;
-      } else {
-        p = e.accumulate ? static_cast<const uint16_t*>(e.out) : e.slope_of;
-        ld = e.accumulate ? e.ldo : e.lds;
-      }
-      if (p == nullptr) return;
-      p += (row0 + lane / 4) * ld + col0 + 8 * (lane % 4);
+      from = e.accumulate ? static_cast<const char*>(e.out)
+                          : reinterpret_cast<const char*>(e.slope_of);
+      from_pitch = 2 * (e.accumulate ? e.ldo : e.lds);
+    }
+  }
+  __device__ __forceinline__ void ask(int64_t row0, int64_t col0, int lane) {
+    if (from == nullptr) return;
+    const char* p = from + (row0 + lane / kLanes) * from_pitch + col0 * (KIND == kFloat ? 4 : 2) +
+                    16 * (lane % kLanes);
 #pragma unroll
-      for (int q = 0; q < 4; ++q) x[q] = *reinterpret_cast<const uint4*>(p + 8 * q * ld);
+    for (int q = 0; q < kTimes; ++q)
+      in[q] = *reinterpret_cast<const uint4*>(p + kHeight * q * from_pitch);
+  }
+  __device__ __forceinline__ void put(const Epilogue& e, const float* mine, int64_t row0,
+                                      int64_t col0, int lane) {
+    const int64_t row = row0 + lane / kLanes, col = col0 + (32 / kLanes) * (lane % kLanes);
+    if constexpr (KIND == kFloat) {
+      float* p = static_cast<float*>(e.out) + row * e.ldo + col;
+#pragma unroll
+      for (int q = 0; q < kTimes; ++q) {
+        float4 v = *reinterpret_cast<const float4*>(mine + staged(kHeight * q + lane / 8, lane % 8));
+        if (e.accumulate) {
+          v.x += __uint_as_float(in[q].x);
+          v.y += __uint_as_float(in[q].y);
+          v.z += __uint_as_float(in[q].z);
+          v.w += __uint_as_float(in[q].w);
+        }
+        *reinterpret_cast<float4*>(p) = v;
+        p += kHeight * e.ldo;
+      }
+    } else {
+      uint16_t* p = static_cast<uint16_t*>(e.out) + row * e.ldo + col;
+      uint16_t* pre = nullptr;
+      float bias[8] = {};
+      if constexpr (KIND == kForward) {
+        if (e.bias != nullptr) bf16x8(*reinterpret_cast<const uint4*>(e.bias + col), bias);
+        if (e.pre != nullptr) pre = e.pre + row * e.ldp + col;
+      }
+#pragma unroll
+      for (int q = 0; q < kTimes; ++q) {
+        const int r = kHeight * q + lane / 4;
+        float x[8], y[8];
+        const float4 u = *reinterpret_cast<const float4*>(mine + staged(r, 2 * (lane % 4)));
+        const float4 v = *reinterpret_cast<const float4*>(mine + staged(r, 2 * (lane % 4) + 1));
+        x[0] = u.x; x[1] = u.y; x[2] = u.z; x[3] = u.w;
+        x[4] = v.x; x[5] = v.y; x[6] = v.z; x[7] = v.w;
+        if constexpr (KIND == kForward) {
+#pragma unroll
+          for (int c = 0; c < 8; ++c) x[c] += bias[c];
+          if (e.pre != nullptr) {
+            *reinterpret_cast<uint4*>(pre) = to_bf16x8(x);
+            pre += kHeight * e.ldp;
+          }
+          act_value8(x, e.act);
+        }
+        if (from != nullptr) {
+          if (KIND == kForward || e.accumulate) {
+            bf16x8(in[q], y);
+#pragma unroll
+            for (int c = 0; c < 8; ++c) x[c] += y[c];
+          } else {
+            times_slope8(x, in[q], e.slope_act);
+          }
+        }
+        *reinterpret_cast<uint4*>(p) = to_bf16x8(x);
+        p += kHeight * e.ldo;
+      }
     }
   }
 };
-
-// A whole 32 x 32 part in 16-byte accesses: 4 lanes take a row's 32 columns of
-// bf16, 8 lanes of fp32.
-template <Kind KIND>
-__device__ __forceinline__ void epilogue_vector(const Epilogue& e, const float* mine, int64_t row0,
-                                                int64_t col0, int lane,
-                                                const EpilogueReads<KIND>& reads) {
-  if constexpr (KIND == kFloat) {
-    float* p = static_cast<float*>(e.out) + (row0 + lane / 8) * e.ldo + col0 + 4 * (lane % 8);
-#pragma unroll
-    for (int q = 0; q < 8; ++q) {
-      float4 v = *reinterpret_cast<const float4*>(mine + staged(4 * q + lane / 8, lane % 8));
-      if (e.accumulate) {
-        v.x += __uint_as_float(reads.x[q].x);
-        v.y += __uint_as_float(reads.x[q].y);
-        v.z += __uint_as_float(reads.x[q].z);
-        v.w += __uint_as_float(reads.x[q].w);
-      }
-      *reinterpret_cast<float4*>(p + 4 * q * e.ldo) = v;
-    }
-  } else {
-    const int64_t row = row0 + lane / 4, col = col0 + 8 * (lane % 4);
-    uint16_t* p = static_cast<uint16_t*>(e.out) + row * e.ldo + col;
-    float bias[8];
-    if constexpr (KIND == kForward) {
-      if (e.bias != nullptr) bf16x8(*reinterpret_cast<const uint4*>(e.bias + col), bias);
-    }
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      const int r = 8 * q + lane / 4;
-      float x[8];
-      const float4 u = *reinterpret_cast<const float4*>(mine + staged(r, 2 * (lane % 4)));
-      const float4 v = *reinterpret_cast<const float4*>(mine + staged(r, 2 * (lane % 4) + 1));
-      x[0] = u.x; x[1] = u.y; x[2] = u.z; x[3] = u.w;
-      x[4] = v.x; x[5] = v.y; x[6] = v.z; x[7] = v.w;
-      if constexpr (KIND == kForward) {
-        if (e.bias != nullptr) {
-#pragma unroll
-          for (int c = 0; c < 8; ++c) x[c] += bias[c];
-        }
-        if (e.pre != nullptr)
-          *reinterpret_cast<uint4*>(e.pre + (row + 8 * q) * e.ldp + col) = to_bf16x8(x);
-        act_value8(x, e.act);
-        if (e.residual != nullptr) {
-          float y[8];
-          bf16x8(reads.x[q], y);
-#pragma unroll
-          for (int c = 0; c < 8; ++c) x[c] += y[c];
-        }
-      } else if (e.accumulate) {
-        float y[8];
-        bf16x8(reads.x[q], y);
-#pragma unroll
-        for (int c = 0; c < 8; ++c) x[c] += y[c];
-      } else if (e.slope_of != nullptr) {
-        times_slope8(x, reads.x[q], e.slope_act);
-      }
-      *reinterpret_cast<uint4*>(p + 8 * q * e.ldo) = to_bf16x8(x);
-    }
-  }
-}
 
 // Place in the ring of stages: the stage, and the parity of its barriers' phase.
 template <int STAGES>
@@ -385,17 +386,27 @@ __global__ void __launch_bounds__(kProductThreads, 1)
       const int64_t row0 = tile.row + rank * kBlockRows + quarter * 32;
       Epilogue e = a.e;
       if constexpr (KIND == kFloat) e.out = static_cast<float*>(e.out) + tile.split * a.split_stride;
+      const int64_t left = tile.col + half * (BN / 2);
+      const uint32_t from = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + b * BN + half * (BN / 2);
+      const auto whole = [&](int c) {
+        return e.vec && row0 + 32 <= a.rows && left + c + 32 <= a.cols;
+      };
+      EpilogueVector<KIND> vec;
+      vec.begin(e);
+      uint32_t x[32];
+      tmem_load32(from, x);
+      if (whole(0)) vec.ask(row0, left, lane);
 #pragma unroll 1
       for (int c = 0; c < BN / 2; c += 32) {
-        const int at = half * (BN / 2) + c;
-        const int64_t col0 = tile.col + at;
-        const bool whole = e.vec && row0 + 32 <= a.rows && col0 + 32 <= a.cols;
-        EpilogueReads<KIND> reads;
-        if (whole) reads.issue(e, row0, col0, lane);
-        uint32_t x[32];
-        tmem_load32(tmem + (static_cast<uint32_t>(quarter * 32) << 16) + b * BN + at, x);
         tmem_load_wait();
-        if (c + 32 >= BN / 2) {  // the warp has read its part: this half may be written again
+        __syncwarp();  // the part before has been read
+#pragma unroll
+        for (int q = 0; q < 8; ++q)
+          *reinterpret_cast<uint4*>(mine + staged(lane, q)) =
+              make_uint4(x[4 * q], x[4 * q + 1], x[4 * q + 2], x[4 * q + 3]);
+        if (c + 32 < BN / 2) {
+          tmem_load32(from + c + 32, x);
+        } else {  // the warp has read its part: this half may be written again
           tc_fence_before();
           __syncwarp();
           if (lane == 0) {
@@ -403,14 +414,13 @@ __global__ void __launch_bounds__(kProductThreads, 1)
             else mbar_arrive(&free_[b]);
           }
         }
-        __syncwarp();  // the part before has been read
-#pragma unroll
-        for (int q = 0; q < 8; ++q)
-          *reinterpret_cast<uint4*>(mine + staged(lane, q)) =
-              make_uint4(x[4 * q], x[4 * q + 1], x[4 * q + 2], x[4 * q + 3]);
         __syncwarp();
-        if (whole) epilogue_vector<KIND>(e, mine, row0, col0, lane, reads);
-        else epilogue_scalar(e, mine, row0, col0, a.rows, a.cols, lane);
+        if (whole(c)) {
+          vec.put(e, mine, row0, left + c, lane);
+          if (c + 32 < BN / 2 && whole(c + 32)) vec.ask(row0, left + c + 32, lane);
+        } else {
+          epilogue_scalar(e, mine, row0, left + c, a.rows, a.cols, lane);
+        }
       }
     }
   }

@@ -17,36 +17,118 @@ __device__ __forceinline__ uint16_t to_bf16(float x) {
   return __bfloat16_as_ushort(__float2bfloat16_rn(x));
 }
 
-// 1 / (1 + exp(-x)); exp(-x) = inf gives 0.
-__device__ __forceinline__ float logistic(float x) { return __fdividef(1.0f, 1.0f + __expf(-x)); }
-
-constexpr float kGelu2C = 1.5957691216057308f;  // 2 sqrt(2/pi)
-constexpr float kGeluA = 0.044715f;
-
-// gelu's tanh form is z times the logistic function of 2u, u = sqrt(2/pi) (z + a z^3),
-// since (1 + tanh u) / 2 = 1 / (1 + exp(-2u)).
-//
-// Past kActFlat the logistic function is 0 or 1 to the last bit of fp32, so the
-// value is 0 or z and the slope 0 or 1; taking them as such also keeps infinite
-// and huge z from meeting 0 * inf.  A NaN fails both comparisons and stays one.
-constexpr float kActFlat = 104.0f;
-
-__device__ __forceinline__ float act_value(float z, int act) {
-  if (act == ZERO_ACT_NONE) return z;
-  if (act == ZERO_ACT_RELU) return z < 0.0f ? 0.0f : z;
-  if (fabsf(z) > kActFlat) return z > 0.0f ? z : 0.0f;
-  return z * logistic(act == ZERO_ACT_GELU ? kGelu2C * (z + kGeluA * z * z * z) : z);
+// 2^x and 1/x of the special-function unit: 2 ulp and 1 ulp; results below the
+// least normal number are 0, 1/inf is 0.
+__device__ __forceinline__ float fast_exp2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float fast_inverse(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
 }
 
-__device__ __forceinline__ float act_slope(float z, int act) {
-  if (act == ZERO_ACT_NONE) return 1.0f;
-  if (act == ZERO_ACT_RELU || fabsf(z) > kActFlat) return z > 0.0f ? 1.0f : 0.0f;
-  if (act == ZERO_ACT_GELU) {
-    const float p = logistic(kGelu2C * (z + kGeluA * z * z * z));
-    return p + z * p * (1.0f - p) * (kGelu2C * (1.0f + 3.0f * kGeluA * z * z));
+// Two fp32 operations at a time.
+struct Pair {
+  uint64_t v;
+};
+__device__ __forceinline__ Pair pair(float lo, float hi) {
+  Pair p;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(p.v) : "f"(lo), "f"(hi));
+  return p;
+}
+__device__ __forceinline__ void split(Pair p, float& lo, float& hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(p.v));
+}
+__device__ __forceinline__ Pair operator*(Pair a, Pair b) {
+  Pair d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d.v) : "l"(a.v), "l"(b.v));
+  return d;
+}
+__device__ __forceinline__ Pair operator+(Pair a, Pair b) {
+  Pair d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d.v) : "l"(a.v), "l"(b.v));
+  return d;
+}
+__device__ __forceinline__ Pair fma2(Pair a, Pair b, Pair c) {
+  Pair d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+  return d;
+}
+
+// gelu's tanh form is z times the logistic function of 2u, u = sqrt(2/pi) (z + a z^3),
+// since (1 + tanh u) / 2 = 1 / (1 + exp(-2u)); silu is z times that of z.  Both as
+// p = 1 / (1 + 2^t), t = z (k0 + k1 z^2) with log2(e) and the sign in k0 and k1.
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kGelu2C = 1.5957691216057308f;  // 2 sqrt(2/pi)
+constexpr float kGeluA = 0.044715f;
+constexpr float kGeluT0 = -kLog2e * kGelu2C, kGeluT1 = -kLog2e * kGelu2C * kGeluA;
+// Where 2^t is inf or 0, p is 0 or 1 and z p (1 - p) is 0 for finite z.  An
+// infinite z is kept from meeting 0 by these bounds, past which p is flat to the
+// last bit of fp32; a NaN comes through p.
+constexpr float kActMost = 3.402823466e38f, kActFlat = 104.0f;
+
+template <int ACT>
+__device__ __forceinline__ void logistic2(float z0, float z1, Pair& p) {
+  const Pair z = pair(z0, z1);
+  Pair t;
+  if constexpr (ACT == ZERO_ACT_GELU)
+    t = z * fma2(z * z, pair(kGeluT1, kGeluT1), pair(kGeluT0, kGeluT0));
+  else
+    t = z * pair(-kLog2e, -kLog2e);
+  float t0, t1;
+  split(t, t0, t1);
+  split(pair(fast_exp2(t0), fast_exp2(t1)) + pair(1.0f, 1.0f), t0, t1);
+  p = pair(fast_inverse(t0), fast_inverse(t1));
+}
+
+// act of two sums, in place.
+template <int ACT>
+__device__ __forceinline__ void act_value2(float& z0, float& z1) {
+  if constexpr (ACT == ZERO_ACT_RELU) {
+    z0 = z0 < 0.0f ? 0.0f : z0;
+    z1 = z1 < 0.0f ? 0.0f : z1;
+  } else if constexpr (ACT != ZERO_ACT_NONE) {
+    Pair p;
+    logistic2<ACT>(z0, z1, p);
+    split(pair(fmaxf(z0, -kActMost), fmaxf(z1, -kActMost)) * p, z0, z1);
   }
-  const float p = logistic(z);
-  return p * (1.0f + z * (1.0f - p));
+}
+
+// x0 and x1 times act' at z0 and z1:
+//   silu' = p + z (p - p^2),  gelu' = p + z (p - p^2) 2 sqrt(2/pi) (1 + 3 a z^2)
+template <int ACT>
+__device__ __forceinline__ void times_slope2(float& x0, float& x1, float z0, float z1) {
+  if constexpr (ACT == ZERO_ACT_RELU) {
+    x0 *= z0 > 0.0f ? 1.0f : 0.0f;
+    x1 *= z1 > 0.0f ? 1.0f : 0.0f;
+  } else if constexpr (ACT != ZERO_ACT_NONE) {
+    Pair p;
+    logistic2<ACT>(z0, z1, p);
+    Pair z = pair(fminf(fmaxf(z0, -kActFlat), kActFlat), fminf(fmaxf(z1, -kActFlat), kActFlat));
+    if constexpr (ACT == ZERO_ACT_GELU)
+      z = z * fma2(z * z, pair(3.0f * kGeluA * kGelu2C, 3.0f * kGeluA * kGelu2C),
+                   pair(kGelu2C, kGelu2C));
+    const Pair flat = fma2(p * pair(-1.0f, -1.0f), p, p);  // p - p^2
+    split(pair(x0, x1) * fma2(z, flat, p), x0, x1);
+  }
+}
+
+__device__ __forceinline__ float act_value(float z, int act) {
+  float unused = 0.0f;
+  if (act == ZERO_ACT_GELU) act_value2<ZERO_ACT_GELU>(z, unused);
+  else if (act == ZERO_ACT_SILU) act_value2<ZERO_ACT_SILU>(z, unused);
+  else if (act == ZERO_ACT_RELU) act_value2<ZERO_ACT_RELU>(z, unused);
+  return z;
+}
+__device__ __forceinline__ float act_slope(float z, int act) {
+  float slope = 1.0f, unused = 0.0f;
+  if (act == ZERO_ACT_GELU) times_slope2<ZERO_ACT_GELU>(slope, unused, z, 0.0f);
+  else if (act == ZERO_ACT_SILU) times_slope2<ZERO_ACT_SILU>(slope, unused, z, 0.0f);
+  else if (act == ZERO_ACT_RELU) times_slope2<ZERO_ACT_RELU>(slope, unused, z, 0.0f);
+  return slope;
 }
 
 // The epilogue of a product D[rows, cols]: what is added to, made of and
@@ -107,13 +189,13 @@ __device__ __forceinline__ uint4 to_bf16x8(const float x[8]) {
 __device__ __forceinline__ void act_value8(float x[8], int act) {
   if (act == ZERO_ACT_GELU) {
 #pragma unroll
-    for (int c = 0; c < 8; ++c) x[c] = act_value(x[c], ZERO_ACT_GELU);
+    for (int c = 0; c < 8; c += 2) act_value2<ZERO_ACT_GELU>(x[c], x[c + 1]);
   } else if (act == ZERO_ACT_SILU) {
 #pragma unroll
-    for (int c = 0; c < 8; ++c) x[c] = act_value(x[c], ZERO_ACT_SILU);
+    for (int c = 0; c < 8; c += 2) act_value2<ZERO_ACT_SILU>(x[c], x[c + 1]);
   } else if (act == ZERO_ACT_RELU) {
 #pragma unroll
-    for (int c = 0; c < 8; ++c) x[c] = act_value(x[c], ZERO_ACT_RELU);
+    for (int c = 0; c < 8; c += 2) act_value2<ZERO_ACT_RELU>(x[c], x[c + 1]);
   }
 }
 __device__ __forceinline__ void times_slope8(float x[8], const uint4 at, int act) {
@@ -121,13 +203,13 @@ __device__ __forceinline__ void times_slope8(float x[8], const uint4 at, int act
   bf16x8(at, z);
   if (act == ZERO_ACT_GELU) {
 #pragma unroll
-    for (int c = 0; c < 8; ++c) x[c] *= act_slope(z[c], ZERO_ACT_GELU);
+    for (int c = 0; c < 8; c += 2) times_slope2<ZERO_ACT_GELU>(x[c], x[c + 1], z[c], z[c + 1]);
   } else if (act == ZERO_ACT_SILU) {
 #pragma unroll
-    for (int c = 0; c < 8; ++c) x[c] *= act_slope(z[c], ZERO_ACT_SILU);
+    for (int c = 0; c < 8; c += 2) times_slope2<ZERO_ACT_SILU>(x[c], x[c + 1], z[c], z[c + 1]);
   } else if (act == ZERO_ACT_RELU) {
 #pragma unroll
-    for (int c = 0; c < 8; ++c) x[c] *= act_slope(z[c], ZERO_ACT_RELU);
+    for (int c = 0; c < 8; c += 2) times_slope2<ZERO_ACT_RELU>(x[c], x[c + 1], z[c], z[c + 1]);
   }
 }
 
