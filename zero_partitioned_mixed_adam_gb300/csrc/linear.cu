@@ -55,38 +55,49 @@ struct ProductShape {
 
 struct ProductArgs {
   CUtensorMap a, b;
+  CUtensorMap out, pre;  // D and pre, where e.vec
+  CUtensorMap parts;     // [tail tile * parts + part][rows of a tile][columns of a tile], fp32
   Epilogue e;
   int64_t rows, cols;
-  int64_t split_stride;  // elements of D between two parts of a split reduction
-  int32_t tiles_m, tiles_n, splits;
+  int32_t tiles_m, tiles_n;
+  int32_t whole;         // tiles done in one piece
+  int32_t splits;        // parts of the reduction of each tile after those
   int32_t steps;         // stages of the whole reduction
   int32_t withhold;      // test hook: no loads are issued, so every wait runs out
 };
 
 struct Tile {
-  int64_t row, col;   // of the tile's first element
-  int first, last;    // stages
-  int split;
+  int64_t row, col;  // of the tile's first element
+  int first, last;   // stages
+  int part;          // place in the parts, or -1: the whole reduction
 };
 
-// Tiles in the order CTAs take them: the parts of the reduction apart, and in
-// each part columns of up to 8 tiles of rows, so that the tiles in flight at
-// one time share their operands in L2.
+// Item t of the work: the tiles in columns of up to 8 tiles of rows, so that the
+// tiles in flight at one time share their operands in L2; after the first
+// `whole` of them each tile is `splits` items, one for each part of the
+// reduction, so that the last round of tiles keeps every SM busy.
 template <int BM, int BN>
 __device__ __forceinline__ Tile tile_of(const ProductArgs& a, int t) {
   constexpr int kGroup = 8;
-  const int per = a.tiles_m * a.tiles_n;
   Tile r;
-  r.split = t / per;
-  t -= r.split * per;
+  r.part = -1;
+  r.first = 0;
+  r.last = a.steps;
+  if (t >= a.whole) {
+    const int u = t - a.whole, part = u % a.splits;
+    t = a.whole + u / a.splits;
+    if (a.splits > 1) {
+      r.part = u;
+      r.first = static_cast<int>(static_cast<int64_t>(a.steps) * part / a.splits);
+      r.last = static_cast<int>(static_cast<int64_t>(a.steps) * (part + 1) / a.splits);
+    }
+  }
   const int group = t / (kGroup * a.tiles_n);
   const int m0 = group * kGroup;
   const int height = a.tiles_m - m0 < kGroup ? a.tiles_m - m0 : kGroup;
   const int in = t - group * kGroup * a.tiles_n;
   r.row = static_cast<int64_t>(m0 + in % height) * BM;
   r.col = static_cast<int64_t>(in / height) * BN;
-  r.first = static_cast<int>(static_cast<int64_t>(a.steps) * r.split / a.splits);
-  r.last = static_cast<int>(static_cast<int64_t>(a.steps) * (r.split + 1) / a.splits);
   return r;
 }
 
@@ -113,81 +124,94 @@ __device__ __noinline__ void epilogue_scalar(const Epilogue& e, const float* min
     epilogue_element(e, row0 + r, j, mine[staged(r, lane / 4) + lane % 4]);
 }
 
-// A whole 32 x 32 part in 16-byte accesses: 4 lanes take a row's 32 columns of
-// bf16 (8 rows at a time), 8 lanes of fp32 (4 rows).
+// A 32 x 32 part, a row a lane, through shared memory and out by TMA: plain
+// stores of the same sectors took 12 of 160 us from the matrix instructions at
+// 8192 x 2048 x 8192.  A warp has 4 KB: two slots of bf16, or one of fp32, in
+// TMA's swizzle, which keeps the lanes' 16-byte writes off each other's banks.
+// fp32 gradients are added to what is there by the copy itself.
 template <Kind KIND>
-struct EpilogueVector {
-  static constexpr int kLanes = KIND == kFloat ? 8 : 4, kHeight = 32 / kLanes, kTimes = kLanes;
-  // What it reads: the residual, the slope's argument or the old value, 16 bytes
-  // a lane and time; asked for one part ahead of its use.
-  uint4 in[kTimes];
-  const char* from;   // NULL: nothing is read
-  int64_t from_pitch;  // bytes
+struct EpiloguePart {
+  uint4 in[4];     // the residual, the slope's argument or the old value of the lane's row
+  uint4 bias[4];
+  int slot = 0;
 
-  __device__ __forceinline__ void begin(const Epilogue& e) {
-    if constexpr (KIND == kFloat) {
-      from = e.accumulate ? static_cast<const char*>(e.out) : nullptr;
-      from_pitch = 4 * e.ldo;
-    } else if constexpr (KIND == kForward) {
-      from = reinterpret_cast<const char*>(e.residual);
-      from_pitch = 2 * e.ldr;
-    } else {
-      from = e.accumulate ? static_cast<const char*>(e.out)
-                          : reinterpret_cast<const char*>(e.slope_of);
-      from_pitch = 2 * (e.accumulate ? e.ldo : e.lds);
+  // Asks for what the part reads, before its sums are there.
+  __device__ __forceinline__ void ask(const Epilogue& e, int64_t row, int64_t col, bool mine) {
+    if constexpr (KIND != kFloat) {
+      const uint16_t* p = KIND == kForward ? e.residual
+                          : e.accumulate   ? static_cast<const uint16_t*>(e.out)
+                                           : e.slope_of;
+      const int64_t ld = KIND == kForward ? e.ldr : e.accumulate ? e.ldo : e.lds;
+      if (p != nullptr && mine) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          in[q] = *reinterpret_cast<const uint4*>(p + row * ld + col + 8 * q);
+      }
+      if (KIND == kForward && e.bias != nullptr) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          bias[q] = __ldg(reinterpret_cast<const uint4*>(e.bias + col + 8 * q));
+      }
     }
   }
-  __device__ __forceinline__ void ask(int64_t row0, int64_t col0, int lane) {
-    if (from == nullptr) return;
-    const char* p = from + (row0 + lane / kLanes) * from_pitch + col0 * (KIND == kFloat ? 4 : 2) +
-                    16 * (lane % kLanes);
+  // 32 columns of bf16 into a slot and off.
+  __device__ __forceinline__ void send(const CUtensorMap* map, uint8_t* staging, const uint4 v[4],
+                                       int x, int y, int lane) {
+    if (lane == 0) bulk_wait_read<1>();  // the copy before the last has left this slot
+    __syncwarp();
+    uint8_t* to = staging + 2048 * slot;
+    slot ^= 1;
 #pragma unroll
-    for (int q = 0; q < kTimes; ++q)
-      in[q] = *reinterpret_cast<const uint4*>(p + kHeight * q * from_pitch);
+    for (int q = 0; q < 4; ++q)
+      *reinterpret_cast<uint4*>(to + lane * 64 + ((q ^ ((lane >> 1) & 3)) * 16)) = v[q];
+    fence_async_shared();
+    __syncwarp();
+    if (lane == 0) {
+      tile_store(map, to, x, y, 0, false);
+      bulk_commit();
+    }
   }
-  __device__ __forceinline__ void put(const Epilogue& e, const float* mine, int64_t row0,
-                                      int64_t col0, int lane) {
-    const int64_t row = row0 + lane / kLanes, col = col0 + (32 / kLanes) * (lane % kLanes);
+  // 32 columns of fp32 as they are.
+  __device__ __forceinline__ void send_sums(const CUtensorMap* map, uint8_t* staging,
+                                            const uint32_t sums[32], int x, int y, int z, bool add,
+                                            int lane) {
+    if (lane == 0) bulk_wait_read<0>();
+    __syncwarp();
+#pragma unroll
+    for (int q = 0; q < 8; ++q)
+      *reinterpret_cast<uint4*>(staging + 4 * staged(lane, q)) =
+          make_uint4(sums[4 * q], sums[4 * q + 1], sums[4 * q + 2], sums[4 * q + 3]);
+    fence_async_shared();
+    __syncwarp();
+    if (lane == 0) {
+      tile_store(map, staging, x, y, z, add);
+      bulk_commit();
+    }
+  }
+  __device__ __forceinline__ void put(const ProductArgs& a, uint8_t* staging,
+                                      const uint32_t sums[32], int64_t row0, int64_t col, int lane) {
+    const Epilogue& e = a.e;
+    const int x0 = static_cast<int>(col), y0 = static_cast<int>(row0);
     if constexpr (KIND == kFloat) {
-      float* p = static_cast<float*>(e.out) + row * e.ldo + col;
-#pragma unroll
-      for (int q = 0; q < kTimes; ++q) {
-        float4 v = *reinterpret_cast<const float4*>(mine + staged(kHeight * q + lane / 8, lane % 8));
-        if (e.accumulate) {
-          v.x += __uint_as_float(in[q].x);
-          v.y += __uint_as_float(in[q].y);
-          v.z += __uint_as_float(in[q].z);
-          v.w += __uint_as_float(in[q].w);
-        }
-        *reinterpret_cast<float4*>(p) = v;
-        p += kHeight * e.ldo;
-      }
+      send_sums(&a.out, staging, sums, x0, y0, 0, e.accumulate != 0, lane);
     } else {
-      uint16_t* p = static_cast<uint16_t*>(e.out) + row * e.ldo + col;
-      uint16_t* pre = nullptr;
-      float bias[8] = {};
-      if constexpr (KIND == kForward) {
-        if (e.bias != nullptr) bf16x8(*reinterpret_cast<const uint4*>(e.bias + col), bias);
-        if (e.pre != nullptr) pre = e.pre + row * e.ldp + col;
-      }
+      uint4 v[4], pre[4];
+      const bool reads = KIND == kForward ? e.residual != nullptr : e.accumulate || e.slope_of != nullptr;
 #pragma unroll
-      for (int q = 0; q < kTimes; ++q) {
-        const int r = kHeight * q + lane / 4;
+      for (int q = 0; q < 4; ++q) {
         float x[8], y[8];
-        const float4 u = *reinterpret_cast<const float4*>(mine + staged(r, 2 * (lane % 4)));
-        const float4 v = *reinterpret_cast<const float4*>(mine + staged(r, 2 * (lane % 4) + 1));
-        x[0] = u.x; x[1] = u.y; x[2] = u.z; x[3] = u.w;
-        x[4] = v.x; x[5] = v.y; x[6] = v.z; x[7] = v.w;
-        if constexpr (KIND == kForward) {
 #pragma unroll
-          for (int c = 0; c < 8; ++c) x[c] += bias[c];
-          if (e.pre != nullptr) {
-            *reinterpret_cast<uint4*>(pre) = to_bf16x8(x);
-            pre += kHeight * e.ldp;
+        for (int c = 0; c < 8; ++c) x[c] = __uint_as_float(sums[8 * q + c]);
+        if constexpr (KIND == kForward) {
+          if (e.bias != nullptr) {
+            bf16x8(bias[q], y);
+#pragma unroll
+            for (int c = 0; c < 8; ++c) x[c] += y[c];
           }
+          if (e.pre != nullptr) pre[q] = to_bf16x8(x);
           act_value8(x, e.act);
         }
-        if (from != nullptr) {
+        if (reads) {
           if (KIND == kForward || e.accumulate) {
             bf16x8(in[q], y);
 #pragma unroll
@@ -196,9 +220,10 @@ struct EpilogueVector {
             times_slope8(x, in[q], e.slope_act);
           }
         }
-        *reinterpret_cast<uint4*>(p) = to_bf16x8(x);
-        p += kHeight * e.ldo;
+        v[q] = to_bf16x8(x);
       }
+      if (KIND == kForward && e.pre != nullptr) send(&a.pre, staging, pre, x0, y0, lane);
+      send(&a.out, staging, v, x0, y0, lane);
     }
   }
 };
@@ -244,7 +269,7 @@ __global__ void __launch_bounds__(kProductThreads, 1)
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const uint32_t rank = CG == 2 ? cluster_rank() : 0u;
   const int unit = blockIdx.x / CG, units = gridDim.x / CG;
-  const int tiles = a.tiles_m * a.tiles_n * a.splits;
+  const int tiles = a.whole + (a.tiles_m * a.tiles_n - a.whole) * a.splits;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
@@ -374,6 +399,7 @@ __global__ void __launch_bounds__(kProductThreads, 1)
   } else {
     const int quarter = warp % 4, half = (warp - 2) / 4;
     float* mine = staging + (warp - 2) * 32 * 32;
+    EpiloguePart<KIND> part;
     int n = 0;
     for (int t = unit; t < tiles; t += units, ++n) {
       const Tile tile = tile_of<BM, BN>(a, t);
@@ -384,29 +410,21 @@ __global__ void __launch_bounds__(kProductThreads, 1)
       }
       tc_fence_after();
       const int64_t row0 = tile.row + rank * kBlockRows + quarter * 32;
-      Epilogue e = a.e;
-      if constexpr (KIND == kFloat) e.out = static_cast<float*>(e.out) + tile.split * a.split_stride;
       const int64_t left = tile.col + half * (BN / 2);
-      const uint32_t from = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + b * BN + half * (BN / 2);
-      const auto whole = [&](int c) {
-        return e.vec && row0 + 32 <= a.rows && left + c + 32 <= a.cols;
-      };
-      EpilogueVector<KIND> vec;
-      vec.begin(e);
-      uint32_t x[32];
-      tmem_load32(from, x);
-      if (whole(0)) vec.ask(row0, left, lane);
+      const uint32_t from =
+          tmem + (static_cast<uint32_t>(quarter * 32) << 16) + b * BN + half * (BN / 2);
 #pragma unroll 1
       for (int c = 0; c < BN / 2; c += 32) {
+        const int64_t col0 = left + c;
+        const bool any = row0 < a.rows && col0 < a.cols;
+        const bool split = tile.part >= 0;
+        // (rows past the end are left out)
+        const bool whole = any && a.e.vec && !split && col0 + 32 <= a.cols;
+        uint32_t x[32];
+        tmem_load32(from + c, x);
+        if (whole) part.ask(a.e, row0 + lane, col0, row0 + lane < a.rows);
         tmem_load_wait();
-        __syncwarp();  // the part before has been read
-#pragma unroll
-        for (int q = 0; q < 8; ++q)
-          *reinterpret_cast<uint4*>(mine + staged(lane, q)) =
-              make_uint4(x[4 * q], x[4 * q + 1], x[4 * q + 2], x[4 * q + 3]);
-        if (c + 32 < BN / 2) {
-          tmem_load32(from + c + 32, x);
-        } else {  // the warp has read its part: this half may be written again
+        if (c + 32 >= BN / 2) {  // the warp has read its part: this half may be written again
           tc_fence_before();
           __syncwarp();
           if (lane == 0) {
@@ -414,15 +432,27 @@ __global__ void __launch_bounds__(kProductThreads, 1)
             else mbar_arrive(&free_[b]);
           }
         }
-        __syncwarp();
-        if (whole(c)) {
-          vec.put(e, mine, row0, left + c, lane);
-          if (c + 32 < BN / 2 && whole(c + 32)) vec.ask(row0, left + c + 32, lane);
-        } else {
-          epilogue_scalar(e, mine, row0, left + c, a.rows, a.cols, lane);
+        if (whole) {
+          part.put(a, reinterpret_cast<uint8_t*>(mine), x, row0, col0, lane);
+        } else if (split) {
+          if (any)
+            part.send_sums(&a.parts, reinterpret_cast<uint8_t*>(mine), x,
+                           half * (BN / 2) + c, static_cast<int>(row0 - tile.row), tile.part, false,
+                           lane);
+        } else if (any) {
+          if (lane == 0) bulk_wait_read<0>();
+          __syncwarp();
+#pragma unroll
+          for (int q = 0; q < 8; ++q)
+            *reinterpret_cast<uint4*>(mine + staged(lane, q)) =
+                make_uint4(x[4 * q], x[4 * q + 1], x[4 * q + 2], x[4 * q + 3]);
+          __syncwarp();
+          epilogue_scalar(a.e, mine, row0, col0, a.rows, a.cols, lane);
+          __syncwarp();
         }
       }
     }
+    if (lane == 0) bulk_wait_all();
   }
   __syncwarp();
   __syncthreads();
@@ -430,29 +460,51 @@ __global__ void __launch_bounds__(kProductThreads, 1)
   if (warp == 1) tmem_free<CG>(tmem, Shape::kColumns);
 }
 
-// The parts of a split reduction, added in their order, and the epilogue.
-struct JoinArgs {
-  const float* parts;
-  int64_t ld, stride;
-  int32_t splits;
-  int64_t rows, cols;
-  Epilogue e;
-};
-
-__global__ void __launch_bounds__(256) linear_join_kernel(const __grid_constant__ JoinArgs a) {
-  const int64_t quads = (a.cols + 3) / 4;
-  for (int64_t q = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; q < a.rows * quads;
-       q += static_cast<int64_t>(gridDim.x) * blockDim.x) {
-    const int64_t i = q / quads, j = (q - i * quads) * 4;
-    float x[4] = {};
-    for (int s = 0; s < a.splits; ++s) {
-      const float4 v = __ldcg(reinterpret_cast<const float4*>(a.parts + s * a.stride + i * a.ld + j));
-      x[0] += v.x; x[1] += v.y; x[2] += v.z; x[3] += v.w;
-    }
-#pragma unroll
-    for (int c = 0; c < 4; ++c)
-      if (j + c < a.cols) epilogue_element(a.e, i, j + c, x[c]);
+// The parts of the tiles whose reduction was split, added in their order, and the
+// epilogue: 8 columns a thread.
+template <int BM, int BN>
+__global__ void __launch_bounds__(256) linear_join_kernel(const __grid_constant__ ProductArgs a,
+                                                          const float* parts) {
+  constexpr int kPerTile = BM * BN / 8;
+  const int64_t q = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+  const int u = static_cast<int>(q / kPerTile);  // of the tiles split
+  const int in = static_cast<int>(q % kPerTile);
+  const Tile tile = tile_of<BM, BN>(a, a.whole + u * a.splits);
+  const int r = in / (BN / 8), c = in % (BN / 8) * 8;
+  const int64_t i = tile.row + r, j = tile.col + c;
+  if (i >= a.rows || j >= a.cols) return;
+  const Epilogue& e = a.e;
+  const bool vec = e.vec && j + 8 <= a.cols;
+  float x[8] = {};
+  const float* p = parts + (static_cast<int64_t>(u) * a.splits * BM + r) * BN + c;
+#pragma unroll 4
+  for (int s = 0; s < a.splits; ++s, p += BM * BN) {
+    const float4 v = __ldcg(reinterpret_cast<const float4*>(p));
+    const float4 w = __ldcg(reinterpret_cast<const float4*>(p) + 1);
+    x[0] += v.x; x[1] += v.y; x[2] += v.z; x[3] += v.w;
+    x[4] += w.x; x[5] += w.y; x[6] += w.z; x[7] += w.w;
   }
+  if (!vec || e.out_f32) {
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+      if (j + k < a.cols) epilogue_element(e, i, j + k, x[k]);
+    return;
+  }
+  float y[8];
+  auto add = [&](const uint16_t* from) {
+    bf16x8(*reinterpret_cast<const uint4*>(from), y);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) x[k] += y[k];
+  };
+  if (e.bias != nullptr) add(e.bias + j);
+  if (e.pre != nullptr) *reinterpret_cast<uint4*>(e.pre + i * e.ldp + j) = to_bf16x8(x);
+  act_value8(x, e.act);
+  if (e.residual != nullptr) add(e.residual + i * e.ldr + j);
+  if (e.slope_of != nullptr)
+    times_slope8(x, *reinterpret_cast<const uint4*>(e.slope_of + i * e.lds + j), e.slope_act);
+  uint16_t* o = static_cast<uint16_t*>(e.out) + i * e.ldo + j;
+  if (e.accumulate) add(o);
+  *reinterpret_cast<uint4*>(o) = to_bf16x8(x);
 }
 
 // ------------------------------------------------------------------ layouts
@@ -550,6 +602,26 @@ cudaError_t make_map(CUtensorMap* map, const Stored& m, int box_rows) {
              : cudaErrorInvalidValue;
 }
 
+// D or pre as `parts` matrices of rows x cols one after the other, in boxes of
+// 32 x 32.
+cudaError_t make_out_map(CUtensorMap* map, const void* p, int64_t rows, int64_t cols, int64_t ld,
+                         int64_t parts, int64_t stride, bool f32) {
+  const EncodeTiled encode = encode_tiled();
+  if (encode == nullptr) return cudaErrorNotSupported;
+  const int size = f32 ? 4 : 2;
+  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows),
+                              static_cast<cuuint64_t>(parts)};
+  const cuuint64_t pitch[2] = {static_cast<cuuint64_t>(ld * size),
+                               static_cast<cuuint64_t>(stride * size)};
+  const cuuint32_t box[3] = {32, 32, 1}, unit[3] = {1, 1, 1};
+  return encode(map, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3,
+                const_cast<void*>(p), dims, pitch, box, unit, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                f32 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
+             ? cudaSuccess
+             : cudaErrorInvalidValue;
+}
+
 // ----------------------------------------------------------------- products
 
 // D[rows, cols] over `depth`; a_mn / b_mn: the operand is stored [depth, rows]
@@ -566,43 +638,52 @@ struct Product {
 constexpr int kSms = 152;
 
 struct Plan {
-  int cg, bn, splits;
+  int cg, bn;
+  int whole, splits;  // as in ProductArgs
+  int tail;           // tiles split
+  int64_t part_bytes() const {
+    return splits > 1 ? int64_t{4} * tail * splits * cg * kBlockRows * bn : 0;
+  }
 };
 
+// The shape of the tiles, and how the last round of them is spread: with T tiles
+// on U units (pairs of SMs, or SMs) the tiles past the last multiple of U would
+// leave most units idle, so their reduction is cut into parts.  Costs are in
+// stages of a 256 x 256 tile on two SMs (0.65 us): a narrower tile feeds the
+// tensor cores less well, and joining the parts is one more launch (4 us) and
+// two passes over them.
 Plan plan_product(int64_t rows, int64_t cols, int64_t depth) {
   const int64_t steps = (depth + kStep - 1) / kStep;
-  Plan best{2, 256, 1};
+  Plan best{2, 256, 0, 1, 0};
   if (rows < 1 || cols < 1) return best;
   double least = 1e300;
-  const struct { int cg, bn; double rate; } shapes[] = {{2, 256, 1.0}, {2, 128, 0.85}, {1, 128, 0.7}};
+  const struct { int cg, bn; double step; } shapes[] = {{2, 256, 1.0}, {2, 128, 0.6}, {1, 128, 0.6}};
   for (const auto& s : shapes) {
-    const int64_t tiles = ((rows + 128 * s.cg - 1) / (128 * s.cg)) * ((cols + s.bn - 1) / s.bn);
-    const int64_t units = kSms / s.cg;
-    const int64_t waves = (tiles + units - 1) / units;
-    const double cost = waves * (128.0 * s.bn) / s.rate;
-    if (cost < least) {
-      least = cost;
-      best.cg = s.cg;
-      best.bn = s.bn;
-      int64_t splits = 1;
-      if (tiles * 2 <= units) {  // most SMs would idle: the reduction is cut
-        splits = units / tiles;
-        if (splits > steps / 2) splits = steps / 2;
-        if (splits > 16) splits = 16;
-        if (splits < 1) splits = 1;
+    const int64_t tm = (rows + 128 * s.cg - 1) / (128 * s.cg), tn = (cols + s.bn - 1) / s.bn;
+    const int64_t tiles = tm * tn, units = kSms / s.cg, rest = tiles % units;
+    const int64_t whole = tiles - rest;
+    if (tiles > INT32_MAX / 64) continue;
+    for (int parts = 1; parts <= 16 && (parts == 1 || (rest > 0 && parts * 2 <= steps)); ++parts) {
+      const int64_t rounds = (rest * parts + units - 1) / units;
+      const Plan p{s.cg, s.bn, static_cast<int>(parts > 1 ? whole : tiles), parts,
+                   static_cast<int>(parts > 1 ? rest : 0)};
+      // a round's end: filling the ring, and the last tile's epilogue
+      const double ends = 4.0;
+      double cost = s.step * (whole / units * steps + rounds * ((steps + parts - 1) / parts)) + ends;
+      if (parts > 1) cost += 6.0 + p.part_bytes() * 2 / 3.0e6;
+      if (p.part_bytes() > (int64_t{64} << 20)) continue;
+      if (cost < least) {
+        least = cost;
+        best = p;
       }
-      best.splits = static_cast<int>(splits);
     }
   }
   return best;
 }
 
-int64_t parts_bytes(const Plan& p, int64_t rows, int64_t cols) {
-  return p.splits > 1 ? round_up(p.splits * rows * round_up(cols, 4) * 4, 256) : 0;
-}
-
 template <int CG, int BN, bool A_MN, bool B_MN, Kind KIND>
-cudaError_t launch_shape(const Product& p, const Plan& plan, ProductArgs& a, cudaStream_t stream) {
+cudaError_t launch_shape(const Product& p, const Plan& plan, ProductArgs& a, float* parts,
+                         cudaStream_t stream) {
   using Shape = ProductShape<CG, BN>;
   auto kernel = linear_product_kernel<CG, BN, A_MN, B_MN, KIND>;
   static std::mutex mu;
@@ -623,10 +704,17 @@ cudaError_t launch_shape(const Product& p, const Plan& plan, ProductArgs& a, cud
   if (e == cudaSuccess) e = make_map(&a.b, p.b, B_MN ? kDepth : Shape::kBRows);
   if (e != cudaSuccess) return e;
   const int64_t tm = (p.rows + CG * kBlockRows - 1) / (CG * kBlockRows), tn = (p.cols + BN - 1) / BN;
-  if (tm * tn * plan.splits > INT32_MAX) return cudaErrorInvalidValue;
+  if (tm * tn > INT32_MAX / 64) return cudaErrorInvalidValue;
   a.tiles_m = static_cast<int32_t>(tm);
   a.tiles_n = static_cast<int32_t>(tn);
-  const int64_t units = sms / CG, tiles = tm * tn * plan.splits;
+  a.whole = plan.whole;
+  a.splits = plan.splits;
+  if (plan.splits > 1) {
+    e = make_out_map(&a.parts, parts, CG * kBlockRows, BN, BN, plan.tail * plan.splits,
+                     CG * kBlockRows * BN, true);
+    if (e != cudaSuccess) return e;
+  }
+  const int64_t units = sms / CG, tiles = plan.whole + int64_t{plan.tail} * plan.splits;
   cudaLaunchConfig_t config = {};
   config.gridDim = dim3(static_cast<unsigned>(CG * (tiles < units ? tiles : units)));
   config.blockDim = dim3(kProductThreads);
@@ -639,20 +727,26 @@ cudaError_t launch_shape(const Product& p, const Plan& plan, ProductArgs& a, cud
   attr[0].val.clusterDim.z = 1;
   config.attrs = attr;
   config.numAttrs = 1;
-  return cudaLaunchKernelEx(&config, kernel, a);
+  e = cudaLaunchKernelEx(&config, kernel, a);
+  if (e != cudaSuccess || plan.splits == 1) return e;
+  linear_join_kernel<CG * kBlockRows, BN>
+      <<<plan.tail * (CG * kBlockRows * BN / 8 / 256), 256, 0, stream>>>(a, parts);
+  return cudaGetLastError();
 }
 
 template <bool A_MN, bool B_MN, Kind KIND>
-cudaError_t launch_kind(const Product& p, const Plan& plan, ProductArgs& a, cudaStream_t stream) {
+cudaError_t launch_kind(const Product& p, const Plan& plan, ProductArgs& a, float* parts,
+                        cudaStream_t stream) {
   if (plan.cg == 2 && plan.bn == 256)
-    return launch_shape<2, 256, A_MN, B_MN, KIND>(p, plan, a, stream);
-  if (plan.cg == 2) return launch_shape<2, 128, A_MN, B_MN, KIND>(p, plan, a, stream);
-  return launch_shape<1, 128, A_MN, B_MN, KIND>(p, plan, a, stream);
+    return launch_shape<2, 256, A_MN, B_MN, KIND>(p, plan, a, parts, stream);
+  if (plan.cg == 2) return launch_shape<2, 128, A_MN, B_MN, KIND>(p, plan, a, parts, stream);
+  return launch_shape<1, 128, A_MN, B_MN, KIND>(p, plan, a, parts, stream);
 }
 
-void set_vec(Epilogue* e) {
-  auto ok = [](const void* p, int64_t ld, int bytes) {
-    return p == nullptr || (aligned(p, 16) && ld * bytes % 16 == 0);
+void set_vec(Epilogue* e, int64_t rows) {
+  // (the pitch of a matrix of one row is not looked at)
+  auto ok = [&](const void* p, int64_t ld, int bytes) {
+    return p == nullptr || (aligned(p, 16) && (rows == 1 || ld * bytes % 16 == 0));
   };
   e->vec = ok(e->bias, 0, 2) && ok(e->pre, e->ldp, 2) && ok(e->residual, e->ldr, 2) &&
            ok(e->slope_of, e->lds, 2) && ok(e->out, e->ldo, e->out_f32 ? 4 : 2);
@@ -662,51 +756,35 @@ cudaError_t launch_product(Product p, Space space, int withhold, cudaStream_t st
   cudaError_t err = make_tileable(&p.a, &space, stream);
   if (err == cudaSuccess) err = make_tileable(&p.b, &space, stream);
   if (err != cudaSuccess) return err;
-  set_vec(&p.e);
+  set_vec(&p.e, p.rows);
   const Plan plan = plan_product(p.rows, p.cols, p.depth);
   ProductArgs a{};
   a.e = p.e;
   a.rows = p.rows;
   a.cols = p.cols;
-  a.splits = plan.splits;
   a.steps = static_cast<int32_t>((p.depth + kStep - 1) / kStep);
   a.withhold = withhold;
-  JoinArgs join{};
-  if (plan.splits > 1) {
-    join.ld = round_up(p.cols, 4);
-    join.stride = p.rows * join.ld;
-    float* parts = static_cast<float*>(space.take(parts_bytes(plan, p.rows, p.cols)));
-    join.parts = parts;
-    join.splits = plan.splits;
-    join.rows = p.rows;
-    join.cols = p.cols;
-    join.e = p.e;
-    a.e = Epilogue{};
-    a.e.out = parts;
-    a.e.ldo = join.ld;
-    a.e.out_f32 = 1;
-    a.e.vec = 1;
-    a.split_stride = join.stride;
-  }
+  float* parts = static_cast<float*>(space.take(plan.part_bytes()));
   const bool f32 = a.e.out_f32 != 0;
+  if (a.e.vec) {
+    // a matrix of one row has any pitch
+    const int64_t one = round_up(p.cols, 8);
+    const int64_t stride = p.rows > 1 ? p.rows * a.e.ldo : one;
+    err = make_out_map(&a.out, a.e.out, p.rows, p.cols, p.rows > 1 ? a.e.ldo : one, 1, stride, f32);
+    if (err == cudaSuccess && a.e.pre != nullptr)
+      err = make_out_map(&a.pre, a.e.pre, p.rows, p.cols, p.rows > 1 ? a.e.ldp : one, 1, stride, false);
+    if (err != cudaSuccess) return err;
+  }
   if (p.a_mn)
-    err = f32 ? launch_kind<true, true, kFloat>(p, plan, a, stream)
-              : launch_kind<true, true, kGradient>(p, plan, a, stream);
-  else if (p.b_mn)
-    err = f32 ? launch_kind<false, true, kFloat>(p, plan, a, stream)
-              : launch_kind<false, true, kGradient>(p, plan, a, stream);
-  else
-    err = f32 ? launch_kind<false, false, kFloat>(p, plan, a, stream)
-              : launch_kind<false, false, kForward>(p, plan, a, stream);
-  if (err != cudaSuccess || plan.splits == 1) return err;
-  const int64_t blocks = (p.rows * (join.ld / 4) + 255) / 256;
-  linear_join_kernel<<<static_cast<unsigned>(blocks < 4096 ? blocks : 4096), 256, 0, stream>>>(join);
-  return cudaGetLastError();
+    return f32 ? launch_kind<true, true, kFloat>(p, plan, a, parts, stream)
+               : launch_kind<true, true, kGradient>(p, plan, a, parts, stream);
+  if (p.b_mn) return launch_kind<false, true, kGradient>(p, plan, a, parts, stream);
+  return launch_kind<false, false, kForward>(p, plan, a, parts, stream);
 }
 
 // Workspace of a product whose operands may both have to be laid out anew.
 int64_t product_bytes(const Stored& a, const Stored& b, int64_t rows, int64_t cols, int64_t depth) {
-  return copy_bytes(a) + copy_bytes(b) + parts_bytes(plan_product(rows, cols, depth), rows, cols);
+  return copy_bytes(a) + copy_bytes(b) + round_up(plan_product(rows, cols, depth).part_bytes(), 256);
 }
 
 // dz = bf16(dy * act'(pre)), and each column's sum of it before the rounding.

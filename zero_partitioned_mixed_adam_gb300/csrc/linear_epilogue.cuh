@@ -147,7 +147,7 @@ struct Epilogue {
   void* out;                 // bf16, or fp32
   int64_t ldo;
   int32_t out_f32, accumulate;
-  int32_t vec;               // 16-byte accesses: every matrix's base and pitch allow them
+  int32_t vec;               // every matrix's base and pitch are multiples of 16 bytes
 };
 
 // ---- one element, any layout

@@ -58,6 +58,22 @@ __device__ __forceinline__ void tile_load(void* dst, const CUtensorMap* m, int x
         : "memory");
 }
 
+// Box from shared memory into (x, y, z) of a tensor, what lies past its edges
+// left out; with `add` it is added in place, in L2.  Tracked by bulk groups.
+__device__ __forceinline__ void tile_store(const CUtensorMap* m, const void* src, int x, int y,
+                                           int z, bool add) {
+  if (add)
+    asm volatile(
+        "cp.reduce.async.bulk.tensor.3d.global.shared::cta.add.tile.bulk_group [%0, {%1, %2, %3}], "
+        "[%4];" ::"l"(m), "r"(x), "r"(y), "r"(z), "r"(smem_addr(src))
+        : "memory");
+  else
+    asm volatile(
+        "cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(
+            m), "r"(x), "r"(y), "r"(z), "r"(smem_addr(src))
+        : "memory");
+}
+
 // ---------------------------------------------------------------- tensor memory
 
 template <int CG>
