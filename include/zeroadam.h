@@ -102,6 +102,11 @@ extern "C" {
 #define ZERO_ACT_GELU 2 /* z/2 (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3))), the tanh form */
 #define ZERO_ACT_SILU 3 /* z / (1 + exp(-z))                                            */
 
+/* zero_linear_workspace */
+#define ZERO_LINEAR_BACKWARD 1
+#define ZERO_LINEAR_ALIGNED 2
+#define ZERO_LINEAR_PLAIN 4
+
 /* zero_adamw_step */
 #define ZERO_STATE_8BIT 0x80   /* flag: m and v are held as 8-bit codes with block scales */
 #define ZERO_MOMENT_BLOCK 256  /* elements that share one scale of an 8-bit moment        */
@@ -322,7 +327,7 @@ typedef struct {
  *   residual    bf16, or NULL.  It may be y itself (same pitch): in place.
  *   pre         bf16, written, or NULL: what the backward pass takes.
  *   y           bf16, written.
- *   workspace   device memory of zero_linear_workspace(shape, 0) bytes,
+ *   workspace   device memory of zero_linear_workspace bytes,
  *               16-byte aligned (NULL where that is 0), free again once the
  *               call's work has run.
  * rows = 0 is valid and launches nothing (matrices of no rows may be NULL).  Any alignment of 2 bytes and any
@@ -358,7 +363,7 @@ int zero_linear_forward(const zero_linear_t* shape, const void* x, const void* w
  *               or fp32 with ZERO_GRAD_F32: a tensor's place in a rank's flat
  *               gradient buffer can be passed as it is.
  *   flags       ZERO_GRAD_F32, ZERO_GRAD_ACCUMULATE.
- *   workspace   zero_linear_workspace(shape, 1) bytes.
+ *   workspace   zero_linear_workspace bytes with ZERO_LINEAR_BACKWARD.
  * rows = 0 writes zeros to dw and dbias (or leaves them, accumulating).
  * Errors: as zero_linear_forward (ZERO_E_LAYOUT also for unknown flags).
  */
@@ -367,10 +372,14 @@ int zero_linear_backward(const zero_linear_t* shape, const void* dy, const void*
                          void* dx, void* dw, void* dbias, int32_t flags, void* workspace,
                          int64_t workspace_bytes, void* stream);
 
-/* Bytes of workspace that suffice for zero_linear_forward (backward = 0) or
- * zero_linear_backward (1) of this shape, whatever its matrices' alignment;
- * negative: the ZERO_E_* code of a bad shape.  Host only. */
-int64_t zero_linear_workspace(const zero_linear_t* shape, int32_t backward);
+/* Bytes of workspace that suffice for zero_linear_forward, or with
+ * ZERO_LINEAR_BACKWARD for zero_linear_backward, of this shape; 0 for a forward
+ * of at most 16 rows.  ZERO_LINEAR_ALIGNED: every matrix's base will be on a
+ * 16-byte boundary and every pitch a multiple of 8, so none is laid out anew
+ * (a call whose matrices are not so needs the figure without it).
+ * ZERO_LINEAR_PLAIN: a backward with ZERO_ACT_NONE.  Negative: the ZERO_E_* code
+ * of a bad shape or flag.  Host only. */
+int64_t zero_linear_workspace(const zero_linear_t* shape, int32_t flags);
 
 /* ------------------------------------------------- AdamW over a list of tensors */
 

@@ -74,8 +74,11 @@ def test_backward_refusals():
     assert backward(db=at(6)) == CODES["ZERO_E_ALIAS"]
     assert backward(ws=None) == CODES["ZERO_E_WORKSPACE"]
     assert backward(ws=at(9) + 8) == CODES["ZERO_E_WORKSPACE"]
-    need = za.zero_linear_workspace(64, 128, 96, True)
+    need = za.zero_linear_workspace(64, 128, 96, True, aligned=True)
     assert need > 0 and backward(nbytes=need - 1) == CODES["ZERO_E_WORKSPACE"]
+    most = za.zero_linear_workspace(64, 128, 96, True)
+    assert most > need and backward(dy=at(1) + 2, nbytes=most - 1) == CODES["ZERO_E_WORKSPACE"]
+    assert LIB.zero_linear_workspace(ctypes.byref(shape()), 8) == CODES["ZERO_E_LAYOUT"]
     assert backward(ws=at(7)) == CODES["ZERO_E_ALIAS"]
     with pytest.raises(za.ZeroError) as e:
         za.zero_linear_workspace(1, 0, 1)

@@ -28,6 +28,7 @@ ZERO_GRAD_F32, ZERO_ACC_BF16 = 0x10, 0x20
 ZERO_GRAD_ACCUMULATE, ZERO_STATE_8BIT = 0x40, 0x80
 ZERO_PARAM_FULL, ZERO_PARAM_SHARD = 0, 1
 ZERO_ACT_NONE, ZERO_ACT_RELU, ZERO_ACT_GELU, ZERO_ACT_SILU = 0, 1, 2, 3
+ZERO_LINEAR_BACKWARD, ZERO_LINEAR_ALIGNED, ZERO_LINEAR_PLAIN = 1, 2, 4
 ZERO_MOMENT_BLOCK = 256
 ZERO_MAX_LIST = 65536
 ZERO_MAX_WORLD = 1024
@@ -157,11 +158,20 @@ def _ptrs(buffers):
     return (ctypes.c_void_p * len(buffers))(*[_addr(b) for b in buffers])
 
 
+def _current_stream() -> int:
+    """The current stream's handle, without building a stream object where PyTorch can."""
+    import torch
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    device = getattr(torch._C, "_cuda_getDevice", None)
+    if raw is None or device is None:
+        return int(torch.cuda.current_stream().cuda_stream)
+    return int(raw(device()))
+
+
 def _stream_handle(stream) -> int:
     if stream is None:
         try:
-            import torch
-            return int(torch.cuda.current_stream().cuda_stream)
+            return _current_stream()
         except Exception:
             return 0
     if isinstance(stream, int):
@@ -309,4 +319,5 @@ __all__ = ["zero_plan", "zero_adam_step", "zero_adam_step_range", "zero3_unit_ga
            "ZERO_ACC_BF16", "ZERO_PARAM_FULL", "ZERO_PARAM_SHARD", "ZERO_MAX_WORLD",
            "ZERO_MAX_UNIT_TENSORS", "EXPORTS", "LIB_PATH", "ZERO_GRAD_ACCUMULATE",
            "ZERO_STATE_8BIT", "ZERO_ACT_NONE", "ZERO_ACT_RELU", "ZERO_ACT_GELU", "ZERO_ACT_SILU",
-           "ZERO_MOMENT_BLOCK", "ZERO_MAX_LIST"] + train_ops.__all__
+           "ZERO_LINEAR_BACKWARD", "ZERO_LINEAR_ALIGNED", "ZERO_LINEAR_PLAIN", "ZERO_MOMENT_BLOCK",
+           "ZERO_MAX_LIST"] + train_ops.__all__

@@ -61,6 +61,11 @@ int check_matrix(const Matrix& m) {
   return misaligned(m.base, static_cast<uintptr_t>(m.esize)) ? ZERO_E_ALIGN : ZERO_OK;
 }
 
+// Whether the TMA engine can read a matrix where it lies (ZERO_LINEAR_ALIGNED).
+bool in_place(const Matrix& m) {
+  return m.base == nullptr || (!misaligned(m.base, 16) && (m.rows <= 1 || m.ld % 8 == 0));
+}
+
 bool known_act(int32_t act) { return act >= ZERO_ACT_NONE && act <= ZERO_ACT_SILU; }
 
 int check_workspace(const void* p, int64_t have, int64_t need) {
@@ -85,10 +90,12 @@ using namespace zeroadam;
 
 extern "C" {
 
-int64_t zero_linear_workspace(const zero_linear_t* shape, int32_t backward) {
+int64_t zero_linear_workspace(const zero_linear_t* shape, int32_t flags) {
   const int rc = check_shape(shape);
   if (rc != ZERO_OK) return rc;
-  return linear_workspace(*shape, backward != 0);
+  if ((flags & ~(ZERO_LINEAR_BACKWARD | ZERO_LINEAR_ALIGNED | ZERO_LINEAR_PLAIN)) != 0)
+    return ZERO_E_LAYOUT;
+  return linear_workspace(*shape, flags);
 }
 
 int zero_linear_forward(const zero_linear_t* shape, const void* x, const void* w,
@@ -109,7 +116,7 @@ int zero_linear_forward(const zero_linear_t* shape, const void* x, const void* w
     if (share(my, *m) || share(mp, *m)) return ZERO_E_ALIAS;
   if (share(my, mp) || share(mp, mr)) return ZERO_E_ALIAS;
   if (!(residual == y && s.ldr == s.ldy) && share(my, mr)) return ZERO_E_ALIAS;
-  const int64_t need = linear_workspace(s, false);
+  const int64_t need = linear_workspace(s, in_place(mx) && in_place(mw) ? ZERO_LINEAR_ALIGNED : 0);
   if ((rc = check_workspace(workspace, workspace_bytes, need)) != ZERO_OK) return rc;
   const Matrix ms{need > 0 ? workspace : nullptr, 1, need, need, 1};
   for (const Matrix* m : {&mx, &mw, &mb, &mr, &mp, &my})
@@ -159,7 +166,9 @@ int zero_linear_backward(const zero_linear_t* shape, const void* dy, const void*
     for (const Matrix* m : {&mdy, &mx, &mw, &mp, &mi})
       if (share(*o, *m)) return ZERO_E_ALIAS;
   if (share(mdx, mdw) || share(mdx, mdb) || share(mdw, mdb)) return ZERO_E_ALIAS;
-  const int64_t need = linear_workspace(s, true);
+  const int64_t need = linear_workspace(
+      s, ZERO_LINEAR_BACKWARD | (act == ZERO_ACT_NONE ? ZERO_LINEAR_PLAIN : 0) |
+             (in_place(mdy) && in_place(mx) && in_place(mw) ? ZERO_LINEAR_ALIGNED : 0));
   if ((rc = check_workspace(workspace, workspace_bytes, need)) != ZERO_OK) return rc;
   const Matrix ms{need > 0 ? workspace : nullptr, 1, need, need, 1};
   for (const Matrix* m : {&mdy, &mx, &mw, &mp, &mi, &mdx, &mdw, &mdb})

@@ -782,9 +782,151 @@ cudaError_t launch_product(Product p, Space space, int withhold, cudaStream_t st
   return launch_kind<false, false, kForward>(p, plan, a, parts, stream);
 }
 
-// Workspace of a product whose operands may both have to be laid out anew.
-int64_t product_bytes(const Stored& a, const Stored& b, int64_t rows, int64_t cols, int64_t depth) {
-  return copy_bytes(a) + copy_bytes(b) + round_up(plan_product(rows, cols, depth).part_bytes(), 256);
+// Workspace of a product; `moved`: of its operands, where they have to be laid
+// out anew.
+int64_t product_bytes(int64_t moved, int64_t rows, int64_t cols, int64_t depth) {
+  return moved + round_up(plan_product(rows, cols, depth).part_bytes(), 256);
+}
+
+// --------------------------------------------------------------- a few rows
+//
+// y for at most 16 rows of x (tokens of generation): W is read once and nothing
+// else counts, so this is bound by HBM bandwidth.  A warp takes 16 rows of W, a
+// block's 8 warps share out the columns, and the warp-level matrix instruction
+// (16 rows of W by 8 rows of x, 16 steps) adds up: tcgen05's tiles of 128 rows
+// of x, brought through shared memory, took 33 us where this takes 21 (32 x 4096
+// x 11008).  A lane's 16-byte load is 8 neighbours of one row; which steps of
+// the reduction an instruction's operands belong to does not matter as long as
+// W's and x's agree, so the vectors are its operands as they are.  All loads of
+// 256 (128) columns are in flight at once; x comes from L1.  The shares are
+// added through shared memory in their order.
+
+constexpr int kFewRows = 16, kFewWarps = 8;
+
+struct FewArgs {
+  const uint16_t *x, *w;
+  int64_t ldx, ldw;
+  int64_t cols;   // of D: rows of W
+  int32_t depth, rows;
+  int32_t share;  // warps that share out the columns of 16 rows of W: 1, 2, 4 or 8
+  Epilogue e;
+};
+
+// 8 elements from p[j] on; those from n on are 0.
+template <bool VEC, bool STREAM>
+__device__ __forceinline__ uint4 few_load(const uint16_t* p, int j, int n) {
+  if (VEC && j + 8 <= n) {
+    uint4 v;
+    if (STREAM)
+      asm volatile("ld.global.nc.L1::no_allocate.v4.b32 {%0, %1, %2, %3}, [%4];"
+                   : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                   : "l"(p + j));
+    else
+      v = __ldg(reinterpret_cast<const uint4*>(p + j));
+    return v;
+  }
+  uint32_t w[4] = {};
+#pragma unroll
+  for (int c = 0; c < 8; ++c)
+    if (j + c < n) w[c / 2] |= static_cast<uint32_t>(__ldg(p + j + c)) << (16 * (c & 1));
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// d += the product of 16 rows (a) and 8 rows (b) over 16 steps.
+__device__ __forceinline__ void warp_mma(float d[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                         uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+      "{%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// NT: groups of 8 rows of x.
+template <int NT, bool VEC>
+__global__ void __launch_bounds__(32 * kFewWarps)
+    linear_few_rows_kernel(const __grid_constant__ FewArgs a) {
+  constexpr int U = NT == 1 ? 8 : 4;     // loads of each row in flight
+  constexpr int kSpan = 32 * U;          // columns a warp takes at a time
+  __shared__ float part[kFewWarps][16 * 8 * NT];
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, g = lane / 4, t = lane % 4;
+  const int share = a.share, mine = warp % share;
+  const int64_t row0 = (static_cast<int64_t>(blockIdx.x) * (kFewWarps / share) + warp / share) * 16;
+  float acc[NT][4] = {};
+  if (row0 < a.cols) {
+    // rows past the end read the last one; nothing is made of them
+    const int64_t top = row0 + g, low = row0 + g + 8, end = a.cols - 1;
+    const uint16_t* w0 = a.w + (top < end ? top : end) * a.ldw;
+    const uint16_t* w1 = a.w + (low < end ? low : end) * a.ldw;
+    const uint16_t* x[NT];  // rows past the end: row 0's, in sums that are not stored
+#pragma unroll
+    for (int n = 0; n < NT; ++n) x[n] = a.x + (8 * n + g < a.rows ? 8 * n + g : 0) * a.ldx;
+    for (int k0 = kSpan * mine; k0 < a.depth; k0 += kSpan * share) {
+      const int j = k0 + 8 * t;
+      uint4 u[U], v[U];
+#pragma unroll
+      for (int q = 0; q < U; ++q) {
+        u[q] = few_load<VEC, true>(w0, j + 32 * q, a.depth);
+        v[q] = few_load<VEC, true>(w1, j + 32 * q, a.depth);
+      }
+#pragma unroll
+      for (int q = 0; q < U; ++q) {
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          const uint4 y = few_load<VEC, false>(x[n], j + 32 * q, a.depth);
+          warp_mma(acc[n], u[q].x, v[q].x, u[q].y, v[q].y, y.x, y.y);
+          warp_mma(acc[n], u[q].z, v[q].z, u[q].w, v[q].w, y.z, y.w);
+        }
+      }
+    }
+  }
+  // (row of W, row of x) of a lane's sums: (g, 2t), (g, 2t + 1), and g + 8 alike
+#pragma unroll
+  for (int n = 0; n < NT; ++n)
+#pragma unroll
+    for (int c = 0; c < 4; ++c)
+      part[warp][(8 * n + 2 * t + c % 2) * 16 + g + 8 * (c / 2)] = acc[n][c];
+  __syncthreads();
+  // one thread an output, neighbours along W's rows
+  for (int q = threadIdx.x; q < (kFewWarps / share) * 128 * NT; q += 32 * kFewWarps) {
+    const int group = q / (128 * NT), in = q % (128 * NT), m = in / 16;
+    const int64_t j = (static_cast<int64_t>(blockIdx.x) * (kFewWarps / share) + group) * 16 + in % 16;
+    if (j >= a.cols || m >= a.rows) continue;
+    float sum = 0.0f;
+    for (int s = 0; s < share; ++s) sum += part[group * share + s][in];
+    epilogue_element(a.e, m, j, sum);
+  }
+}
+
+template <int NT>
+cudaError_t launch_few_groups(FewArgs& a, bool vec, cudaStream_t stream) {
+  // The columns are shared out until there are 16 warps an SM, or a warp's part
+  // is one step.
+  const int64_t groups = (a.cols + 15) / 16;
+  a.share = 1;
+  while (a.share < kFewWarps && groups * a.share < int64_t{32} * kSms && a.depth > 128 * a.share)
+    a.share *= 2;
+  const int64_t blocks = (groups + kFewWarps / a.share - 1) / (kFewWarps / a.share);
+  if (blocks > INT32_MAX) return cudaErrorInvalidValue;
+  if (vec)
+    linear_few_rows_kernel<NT, true><<<static_cast<unsigned>(blocks), 32 * kFewWarps, 0, stream>>>(a);
+  else
+    linear_few_rows_kernel<NT, false><<<static_cast<unsigned>(blocks), 32 * kFewWarps, 0, stream>>>(a);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_few_rows(const Product& p, cudaStream_t stream) {
+  FewArgs a{};
+  a.x = p.a.p;
+  a.ldx = p.a.ld;
+  a.w = p.b.p;
+  a.ldw = p.b.ld;
+  a.rows = static_cast<int32_t>(p.rows);
+  a.cols = p.cols;
+  a.depth = static_cast<int32_t>(p.depth);
+  a.e = p.e;
+  const bool vec = tileable(p.a) && tileable(p.b);
+  return p.rows <= 8 ? launch_few_groups<1>(a, vec, stream) : launch_few_groups<2>(a, vec, stream);
 }
 
 // dz = bf16(dy * act'(pre)), and each column's sum of it before the rounding.
@@ -893,13 +1035,17 @@ int read_and_clear_linear_status(int* status) {
   return 0;
 }
 
-int64_t linear_workspace(const zero_linear_t& s, bool backward) {
-  const Stored x{nullptr, s.rows, s.in, 0}, w{nullptr, s.out, s.in, 0}, z{nullptr, s.rows, s.out, 0}, none{nullptr, 0, 0, 0};
-  if (!backward) return product_bytes(x, w, s.rows, s.out, s.in);
+int64_t linear_workspace(const zero_linear_t& s, int32_t flags) {
+  const bool in_place = (flags & ZERO_LINEAR_ALIGNED) != 0;
+  const int64_t x = in_place ? 0 : copy_bytes(Stored(nullptr, s.rows, s.in, 0));
+  const int64_t w = in_place ? 0 : copy_bytes(Stored(nullptr, s.out, s.in, 0));
+  if ((flags & ZERO_LINEAR_BACKWARD) == 0)
+    return s.rows <= kFewRows ? 0 : product_bytes(x + w, s.rows, s.out, s.in);
   // dz is laid out once and taken by both products, one after the other
-  const int64_t dx = product_bytes(none, w, s.rows, s.in, s.out);
-  const int64_t dw = product_bytes(none, x, s.out, s.in, s.rows);
-  return copy_bytes(z) + round_up(slope_blocks(s.rows) * s.out * 4, 256) + (dx > dw ? dx : dw);
+  const bool dz = !in_place || (flags & ZERO_LINEAR_PLAIN) == 0;
+  const int64_t dx = product_bytes(w, s.rows, s.in, s.out), dw = product_bytes(x, s.out, s.in, s.rows);
+  return (dz ? copy_bytes(Stored(nullptr, s.rows, s.out, 0)) : 0) +
+         round_up(slope_blocks(s.rows) * s.out * 4, 256) + (dx > dw ? dx : dw);
 }
 
 cudaError_t launch_linear_forward(const LinearForwardLaunch& L) {
@@ -919,6 +1065,7 @@ cudaError_t launch_linear_forward(const LinearForwardLaunch& L) {
   p.e.ldr = s.ldr;
   p.e.out = L.y;
   p.e.ldo = s.ldy;
+  if (s.rows <= kFewRows) return launch_few_rows(p, L.stream);
   return launch_product(p, {static_cast<char*>(L.workspace)}, L.withhold, L.stream);
 }
 

@@ -83,7 +83,8 @@ struct LinearBackwardLaunch {
   int32_t withhold;
 };
 
-int64_t linear_workspace(const zero_linear_t& s, bool backward);
+// flags: ZERO_LINEAR_*
+int64_t linear_workspace(const zero_linear_t& s, int32_t flags);
 cudaError_t launch_linear_forward(const LinearForwardLaunch& L);
 cudaError_t launch_linear_backward(const LinearBackwardLaunch& L);
 // Status word of the products' bounded waits on the current device (0 = every

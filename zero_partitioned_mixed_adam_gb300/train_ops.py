@@ -10,8 +10,9 @@ import ctypes
 
 import torch
 
-from . import (ZERO_ACT_NONE, ZERO_GRAD_ACCUMULATE, ZERO_GRAD_F32, ZERO_MOMENT_BLOCK, ZERO_OK,
-               ZERO_STATE_8BIT, ZeroError, _addr, _lib, _ptrs, _stream_handle)
+from . import (ZERO_ACT_NONE, ZERO_GRAD_ACCUMULATE, ZERO_GRAD_F32, ZERO_LINEAR_ALIGNED,
+               ZERO_LINEAR_BACKWARD, ZERO_LINEAR_PLAIN, ZERO_MOMENT_BLOCK, ZERO_OK, ZERO_STATE_8BIT,
+               ZeroError, _addr, _lib, _ptrs, _stream_handle)
 
 
 class ZeroLinear(ctypes.Structure):
@@ -63,9 +64,10 @@ def _matrix(name, t, rows, cols, dtypes=_BF16):
         raise ValueError(f"{name}: expected {rows} x {cols}, got {tuple(t.shape)}")
     if t.dtype not in dtypes:
         raise ValueError(f"{name}: expected one of {dtypes}, got {t.dtype}")
-    if cols > 1 and t.stride(1) != 1:
-        raise ValueError(f"{name}: its columns are not contiguous (stride {t.stride(1)})")
-    return t.stride(0) if rows > 1 else max(cols, t.stride(0))
+    pitch, step = t.stride()
+    if cols > 1 and step != 1:
+        raise ValueError(f"{name}: its columns are not contiguous (stride {step})")
+    return pitch if rows > 1 else max(cols, pitch)
 
 
 def _vector(name, t, n, dtypes=_BF16):
@@ -73,26 +75,32 @@ def _vector(name, t, n, dtypes=_BF16):
         raise ValueError(f"{name}: expected {n} contiguous elements of one of {dtypes}")
 
 
-def _linear_workspace(shape, backward, workspace, device, stream):
+def _linear_workspace(shape, flags, bases, pitches, workspace, device, stream):
     """The caller's workspace, or one from PyTorch's allocator that is kept from reuse
-    until `stream` is past the call; and its bytes."""
-    if workspace is None:
-        need = _lib.zero_linear_workspace(ctypes.byref(shape), backward)
-        if need < 0:
-            raise ZeroError(need, "zero_linear_workspace")
-        if need == 0:
-            return None, 0
-        workspace = torch.empty(need, dtype=torch.uint8, device=device)
-        if stream is not None:
-            workspace.record_stream(stream if not isinstance(stream, int)
-                                    else torch.cuda.ExternalStream(stream, device))
-    return workspace, workspace.numel() * workspace.element_size()
+    until `stream` is past the call; and its bytes.  bases, pitches: those of the matrices
+    that the products read, or-ed together."""
+    if workspace is not None:
+        return workspace, workspace.numel() * workspace.element_size()
+    if bases % 16 == 0 and pitches % 8 == 0:
+        flags |= ZERO_LINEAR_ALIGNED
+    need = _lib.zero_linear_workspace(ctypes.byref(shape), flags)
+    if need < 0:
+        raise ZeroError(need, "zero_linear_workspace")
+    if need == 0:
+        return None, 0
+    workspace = torch.empty(need, dtype=torch.uint8, device=device)
+    if stream is not None:
+        workspace.record_stream(stream if not isinstance(stream, int)
+                                else torch.cuda.ExternalStream(stream, device))
+    return workspace, need
 
 
-def zero_linear_workspace(rows: int, width_in: int, width_out: int, backward: bool = False) -> int:
-    """Bytes of workspace that suffice for a linear map of these sizes."""
-    rc = _lib.zero_linear_workspace(ctypes.byref(ZeroLinear(rows, width_in, width_out)),
-                                    int(backward))
+def zero_linear_workspace(rows: int, width_in: int, width_out: int, backward: bool = False,
+                          aligned: bool = False) -> int:
+    """Bytes of workspace that suffice for a linear map of these sizes; aligned: of matrices
+    that all start on 16-byte boundaries and have pitches that are multiples of 8."""
+    flags = (ZERO_LINEAR_BACKWARD if backward else 0) | (ZERO_LINEAR_ALIGNED if aligned else 0)
+    rc = _lib.zero_linear_workspace(ctypes.byref(ZeroLinear(rows, width_in, width_out)), flags)
     if rc < 0:
         raise ZeroError(rc, "zero_linear_workspace")
     return rc
@@ -118,8 +126,9 @@ def zero_linear_forward(x, w, y, *, bias=None, act: int = ZERO_ACT_NONE, residua
         s.ldr = _matrix("residual", residual, rows, out)
     if pre is not None:
         s.ldp = _matrix("pre", pre, rows, out)
-    workspace, nbytes = _linear_workspace(s, 0, workspace, y.device, stream)
-    rc = _lib.zero_linear_forward(ctypes.byref(s), _addr(x), _addr(w), _addr(bias), act,
+    px, pw = x.data_ptr(), w.data_ptr()
+    workspace, nbytes = _linear_workspace(s, 0, px | pw, s.ldx | s.ldw, workspace, y.device, stream)
+    rc = _lib.zero_linear_forward(ctypes.byref(s), px, pw, _addr(bias), act,
                                   _addr(residual), _addr(pre), _addr(y), _addr(workspace), nbytes,
                                   _stream_handle(stream))
     if rc != ZERO_OK:
@@ -164,7 +173,9 @@ def zero_linear_backward(dy, x, w, *, dx=None, dw=None, dbias=None, act: int = Z
     flags = ZERO_GRAD_F32 if g is not None and g.dtype == torch.float32 else 0
     if accumulate:
         flags |= ZERO_GRAD_ACCUMULATE
-    workspace, nbytes = _linear_workspace(s, 1, workspace, dy.device, stream)
+    workspace, nbytes = _linear_workspace(
+        s, ZERO_LINEAR_BACKWARD | (ZERO_LINEAR_PLAIN if act == ZERO_ACT_NONE else 0),
+        _addr(dy) | _addr(x) | _addr(w), s.ldy | s.ldx | s.ldw, workspace, dy.device, stream)
     rc = _lib.zero_linear_backward(ctypes.byref(s), _addr(dy), _addr(x), _addr(w), act, _addr(pre),
                                    act_in, _addr(pre_in), _addr(dx), _addr(dw), _addr(dbias),
                                    flags, _addr(workspace), nbytes, _stream_handle(stream))
