@@ -33,33 +33,41 @@ constexpr int kBlockRows = 128;    // rows of D per CTA: the lanes of tensor mem
 constexpr int kEpilogueWarps = 8;  // two per quarter of the lanes
 constexpr int kProductThreads = 64 + 32 * kEpilogueWarps;
 
-// One tile of D is CG * 128 rows by BN columns, made by CG CTAs: each brings
-// its own 128 rows of A and BN/CG rows of B, the tensor cores read both CTAs'
-// B (half the shared-memory traffic of two tiles of their own), and each CTA's
-// tensor memory ends up with its 128 rows.
-template <int CG, int BN>
+// One tile of D is CG * 128 rows by bn columns (a multiple of 32, 256 or 128 at
+// most), made by CG CTAs: each brings its own 128 rows of A and bn/CG rows of B,
+// the tensor cores read both CTAs' B (half the shared-memory traffic of two
+// tiles of their own), and each CTA's tensor memory ends up with its 128 rows.
+// The ring has as many stages as fit.  Where D has fewer rows than a tile, only
+// a_rows of A (a multiple of 8) are brought and given room: the tensor cores read
+// on into whatever lies behind, and nothing is made of those rows of D.
+constexpr int kStaging = kEpilogueWarps * 32 * 32 * 4;
+constexpr int kMaxStages = 8;
+constexpr int kBarriers = 256;
+constexpr int kSmem = 227 * 1024;
+static_assert((2 * kMaxStages + 5) * 8 <= kBarriers, "barriers");
+
+template <int CG>
 struct ProductShape {
-  static constexpr int kBRows = BN / CG;
-  static constexpr int kABytes = kBlockRows * kDepth * 2;
-  static constexpr int kBBytes = kBRows * kDepth * 2;
-  static constexpr int kPair = kABytes + kBBytes;
-  static constexpr int kStage = kSub * kPair;
-  static constexpr int kStaging = kEpilogueWarps * 32 * 32 * 4;
-  static constexpr int kBarriers = 512;
-  static constexpr int kStages = (227 * 1024 - 1024 - kStaging - kBarriers) / kStage;
-  static constexpr int kSmem = kStages * kStage + kStaging + kBarriers + 1024;
-  static constexpr int kColumns = 2 * BN < 32 ? 32 : 2 * BN;  // of tensor memory: two tiles
-  static_assert(kStages >= 2 && 2 * kStages + 5 <= kBarriers / 8, "stages");
-  static_assert(kColumns <= 512 && BN % 64 == 0, "tensor memory");
+  static constexpr int kMaxCols = CG == 2 ? 256 : 128;
+  static constexpr int kColumns = 2 * kMaxCols;  // of tensor memory: two tiles
 };
+// Bytes of kDepth steps of one CTA's rows of A and B, and stages of the ring.
+__host__ __device__ constexpr int pair_bytes(int a_rows, int b_rows) {
+  return (a_rows + b_rows) * kDepth * 2;
+}
+__host__ __device__ constexpr int ring_stages(int a_rows, int b_rows) {
+  const int n = (kSmem - 1024 - kStaging - kBarriers) / (kSub * pair_bytes(a_rows, b_rows));
+  return n < kMaxStages ? n : kMaxStages;
+}
+static_assert(kStaging >= kBlockRows * kDepth * 2, "reads behind the last stage's A end in it");
 
 struct ProductArgs {
   CUtensorMap a, b;
   CUtensorMap out, pre;  // D and pre, where e.vec
-  CUtensorMap parts;     // [tail tile * parts + part][rows of a tile][columns of a tile], fp32
+  CUtensorMap parts;     // [tail tile * splits + part][rows of a tile][bn], fp32
   Epilogue e;
   int64_t rows, cols;
-  int32_t tiles_m, tiles_n;
+  int32_t tiles_m, tiles_n, bn, a_rows;
   int32_t whole;         // tiles done in one piece
   int32_t splits;        // parts of the reduction of each tile after those
   int32_t steps;         // stages of the whole reduction
@@ -76,7 +84,7 @@ struct Tile {
 // tiles in flight at one time share their operands in L2; after the first
 // `whole` of them each tile is `splits` items, one for each part of the
 // reduction, so that the last round of tiles keeps every SM busy.
-template <int BM, int BN>
+template <int BM>
 __device__ __forceinline__ Tile tile_of(const ProductArgs& a, int t) {
   constexpr int kGroup = 8;
   Tile r;
@@ -97,7 +105,7 @@ __device__ __forceinline__ Tile tile_of(const ProductArgs& a, int t) {
   const int height = a.tiles_m - m0 < kGroup ? a.tiles_m - m0 : kGroup;
   const int in = t - group * kGroup * a.tiles_n;
   r.row = static_cast<int64_t>(m0 + in % height) * BM;
-  r.col = static_cast<int64_t>(in / height) * BN;
+  r.col = static_cast<int64_t>(in / height) * a.bn;
   return r;
 }
 
@@ -229,12 +237,13 @@ struct EpiloguePart {
 };
 
 // Place in the ring of stages: the stage, and the parity of its barriers' phase.
-template <int STAGES>
 struct Place {
+  int stages;
   int s = 0;
   uint32_t phase = 0;
+  __device__ __forceinline__ explicit Place(int n) : stages(n) {}
   __device__ __forceinline__ void next() {
-    if (++s == STAGES) {
+    if (++s == stages) {
       s = 0;
       phase ^= 1;
     }
@@ -251,18 +260,19 @@ struct Place {
 // first CTA) when every epilogue warp has read it.
 // Every wait is bounded; one that gives up sets g_linear_status and ends its
 // warp's loop, and the others' waits then run out too.
-template <int CG, int BN, bool A_MN, bool B_MN, Kind KIND>
+template <int CG, bool A_MN, bool B_MN, Kind KIND>
 __global__ void __launch_bounds__(kProductThreads, 1)
     linear_product_kernel(const __grid_constant__ ProductArgs a) {
-  using Shape = ProductShape<CG, BN>;
-  constexpr int kStages = Shape::kStages;
+  using Shape = ProductShape<CG>;
   constexpr int BM = CG * kBlockRows;
+  const int b_rows = a.bn / CG, pair = pair_bytes(a.a_rows, b_rows), stage = kSub * pair;
+  const int stages = ring_stages(a.a_rows, b_rows), a_bytes = a.a_rows * kDepth * 2;
   extern __shared__ uint8_t raw[];
   uint8_t* ring = raw + ((1024u - (smem_addr(raw) & 1023u)) & 1023u);
-  float* staging = reinterpret_cast<float*>(ring + kStages * Shape::kStage);
-  uint64_t* full = reinterpret_cast<uint64_t*>(ring + kStages * Shape::kStage + Shape::kStaging);
-  uint64_t* empty = full + kStages;
-  uint64_t* done = empty + kStages;
+  float* staging = reinterpret_cast<float*>(ring + stages * stage);
+  uint64_t* full = reinterpret_cast<uint64_t*>(ring + stages * stage + kStaging);
+  uint64_t* empty = full + kMaxStages;
+  uint64_t* done = empty + kMaxStages;
   uint64_t* free_ = done + 2;
   uint32_t* tmem_at = reinterpret_cast<uint32_t*>(free_ + 2);
 
@@ -272,7 +282,7 @@ __global__ void __launch_bounds__(kProductThreads, 1)
   const int tiles = a.whole + (a.tiles_m * a.tiles_n - a.whole) * a.splits;
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < kStages; ++s) {
+    for (int s = 0; s < stages; ++s) {
       mbar_init(&full[s], 1);
       mbar_init(&empty[s], 1);
     }
@@ -290,18 +300,19 @@ __global__ void __launch_bounds__(kProductThreads, 1)
   if constexpr (CG == 2) cluster_sync();
   tc_fence_after();
   const uint32_t tmem = *tmem_at;
+  if (a.splits > 1) launch_dependents();
 
   if (warp == 0) {
     if (lane == 0) {
-      Place<kStages> at;
+      Place at(stages);
       int issued = 0;  // stages, up to the ring's
       bool ok = true;
       for (int t = unit; t < tiles && ok; t += units) {
-        const Tile tile = tile_of<BM, BN>(a, t);
+        const Tile tile = tile_of<BM>(a, t);
         const int ra = static_cast<int>(tile.row) + rank * kBlockRows;
-        const int rb = static_cast<int>(tile.col) + rank * Shape::kBRows;
+        const int rb = static_cast<int>(tile.col) + rank * b_rows;
         for (int step = tile.first; step < tile.last; ++step, at.next()) {
-          if (issued == kStages) {
+          if (issued == stages) {
             if (!mbar_wait(&empty[at.s], at.phase ^ 1)) {
               ok = false;
               break;
@@ -311,11 +322,11 @@ __global__ void __launch_bounds__(kProductThreads, 1)
           }
           if (a.withhold) continue;
           const uint32_t bar = CG == 2 ? peer_addr(&full[at.s], 0) : smem_addr(&full[at.s]);
-          if (rank == 0) mbar_expect_tx(&full[at.s], CG * Shape::kStage);
+          if (rank == 0) mbar_expect_tx(&full[at.s], CG * stage);
 #pragma unroll
           for (int h = 0; h < kSub; ++h) {
-            uint8_t* sa = ring + at.s * Shape::kStage + h * Shape::kPair;
-            uint8_t* sb = sa + Shape::kABytes;
+            uint8_t* sa = ring + at.s * stage + h * pair;
+            uint8_t* sb = sa + a_bytes;
             const int x = step * kStep + h * kDepth;
             if constexpr (A_MN) {
 #pragma unroll
@@ -325,8 +336,7 @@ __global__ void __launch_bounds__(kProductThreads, 1)
               tile_load<CG>(sa, &a.a, x, ra, bar);
             }
             if constexpr (B_MN) {
-#pragma unroll
-              for (int c = 0; c < Shape::kBRows / 64; ++c)
+              for (int c = 0; c < b_rows / 64; ++c)
                 tile_load<CG>(sb + c * 64 * kDepth * 2, &a.b, rb + 64 * c, x, bar);
             } else {
               tile_load<CG>(sb, &a.b, x, rb, bar);
@@ -338,11 +348,11 @@ __global__ void __launch_bounds__(kProductThreads, 1)
       // No CTA ends while loads into it, or arrivals on its barriers, are under
       // way: the products that read the last stages are waited for.
       if (!a.withhold) {
-        if (issued < kStages) at = Place<kStages>();
+        if (issued < stages) at = Place(stages);
         for (int j = 0; j < issued; ++j, at.next()) {
           // stage at.s was filled last in the phase before this place's, or, in a
           // ring not yet full, in its first
-          const uint32_t phase = issued < kStages ? at.phase : at.phase ^ 1;
+          const uint32_t phase = issued < stages ? at.phase : at.phase ^ 1;
           mbar_wait(&empty[at.s], phase);
           if (!ok && rank == 0) mbar_wait(&full[at.s], phase);
         }
@@ -350,17 +360,17 @@ __global__ void __launch_bounds__(kProductThreads, 1)
     }
   } else if (warp == 1) {
     if (rank == 0 && lane == 0) {
-      constexpr uint32_t desc = mma_desc(BM, BN, A_MN, B_MN);
+      const uint32_t desc = mma_desc(BM, a.bn, A_MN, B_MN);
       // bytes between two steps of 16 of the reduction, and the distances of
       // smem_desc, along each operand's rows
       constexpr uint32_t step_a = A_MN ? 16 * 128 : 32, step_b = B_MN ? 16 * 128 : 32;
       constexpr uint32_t lead = 64 * kDepth * 2, stride = 1024;
-      Place<kStages> at;
+      Place at(stages);
       int used = 0;  // stages, up to the ring's
       int n = 0;     // tiles begun
       bool ok = true;
       for (int t = unit; t < tiles && ok; t += units, ++n) {
-        const Tile tile = tile_of<BM, BN>(a, t);
+        const Tile tile = tile_of<BM>(a, t);
         const int b = n & 1;
         if (n >= 2 && !mbar_wait(&free_[b], static_cast<uint32_t>((n / 2 - 1) & 1))) {
           ok = false;
@@ -373,15 +383,15 @@ __global__ void __launch_bounds__(kProductThreads, 1)
             break;
           }
           tc_fence_after();
-          if (used < kStages) ++used;
+          if (used < stages) ++used;
 #pragma unroll
           for (int h = 0; h < kSub; ++h) {
-            const uint32_t sa = smem_addr(ring) + at.s * Shape::kStage + h * Shape::kPair;
+            const uint32_t sa = smem_addr(ring) + at.s * stage + h * pair;
             const uint64_t da = smem_desc(sa, lead, stride);
-            const uint64_t db = smem_desc(sa + Shape::kABytes, lead, stride);
+            const uint64_t db = smem_desc(sa + a_bytes, lead, stride);
 #pragma unroll
             for (int q = 0; q < kDepth / 16; ++q)
-              mma_bf16<CG>(tmem + b * BN, da + q * (step_a >> 4), db + q * (step_b >> 4), desc,
+              mma_bf16<CG>(tmem + b * Shape::kMaxCols, da + q * (step_a >> 4), db + q * (step_b >> 4), desc,
                            step > tile.first || q > 0 || h > 0);
           }
           mma_commit<CG>(&empty[at.s]);
@@ -391,9 +401,9 @@ __global__ void __launch_bounds__(kProductThreads, 1)
       if (!ok) {
         // products already issued end before tensor memory is freed
         atomicExch(&g_linear_status, 2);
-        if (used < kStages) at = Place<kStages>();
+        if (used < stages) at = Place(stages);
         for (int j = 0; j < used; ++j, at.next())
-          mbar_wait(&empty[at.s], used < kStages ? at.phase : at.phase ^ 1);
+          mbar_wait(&empty[at.s], used < stages ? at.phase : at.phase ^ 1);
       }
     }
   } else {
@@ -402,7 +412,7 @@ __global__ void __launch_bounds__(kProductThreads, 1)
     EpiloguePart<KIND> part;
     int n = 0;
     for (int t = unit; t < tiles; t += units, ++n) {
-      const Tile tile = tile_of<BM, BN>(a, t);
+      const Tile tile = tile_of<BM>(a, t);
       const int b = n & 1;
       if (!mbar_wait(&done[b], static_cast<uint32_t>((n / 2) & 1))) {
         if (lane == 0) atomicExch(&g_linear_status, 3);
@@ -410,12 +420,18 @@ __global__ void __launch_bounds__(kProductThreads, 1)
       }
       tc_fence_after();
       const int64_t row0 = tile.row + rank * kBlockRows + quarter * 32;
-      const int64_t left = tile.col + half * (BN / 2);
       const uint32_t from =
-          tmem + (static_cast<uint32_t>(quarter * 32) << 16) + b * BN + half * (BN / 2);
+          tmem + (static_cast<uint32_t>(quarter * 32) << 16) + b * Shape::kMaxCols;
+      if (32 * half >= a.bn) {  // nothing of a tile this narrow is this warp's
+        __syncwarp();
+        if (lane == 0) {
+          if constexpr (CG == 2) mbar_arrive_peer(peer_addr(&free_[b], 0));
+          else mbar_arrive(&free_[b]);
+        }
+      }
 #pragma unroll 1
-      for (int c = 0; c < BN / 2; c += 32) {
-        const int64_t col0 = left + c;
+      for (int c = 32 * half; c < a.bn; c += 64) {
+        const int64_t col0 = tile.col + c;
         const bool any = row0 < a.rows && col0 < a.cols;
         const bool split = tile.part >= 0;
         // (rows past the end are left out)
@@ -424,7 +440,7 @@ __global__ void __launch_bounds__(kProductThreads, 1)
         tmem_load32(from + c, x);
         if (whole) part.ask(a.e, row0 + lane, col0, row0 + lane < a.rows);
         tmem_load_wait();
-        if (c + 32 >= BN / 2) {  // the warp has read its part: this half may be written again
+        if (c + 64 >= a.bn) {  // the warp has read its part: this half may be written again
           tc_fence_before();
           __syncwarp();
           if (lane == 0) {
@@ -436,9 +452,8 @@ __global__ void __launch_bounds__(kProductThreads, 1)
           part.put(a, reinterpret_cast<uint8_t*>(mine), x, row0, col0, lane);
         } else if (split) {
           if (any)
-            part.send_sums(&a.parts, reinterpret_cast<uint8_t*>(mine), x,
-                           half * (BN / 2) + c, static_cast<int>(row0 - tile.row), tile.part, false,
-                           lane);
+            part.send_sums(&a.parts, reinterpret_cast<uint8_t*>(mine), x, c,
+                           static_cast<int>(row0 - tile.row), tile.part, false, lane);
         } else if (any) {
           if (lane == 0) bulk_wait_read<0>();
           __syncwarp();
@@ -462,23 +477,23 @@ __global__ void __launch_bounds__(kProductThreads, 1)
 
 // The parts of the tiles whose reduction was split, added in their order, and the
 // epilogue: 8 columns a thread.
-template <int BM, int BN>
+template <int BM>
 __global__ void __launch_bounds__(256) linear_join_kernel(const __grid_constant__ ProductArgs a,
                                                           const float* parts) {
-  constexpr int kPerTile = BM * BN / 8;
-  const int64_t q = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
-  const int u = static_cast<int>(q / kPerTile);  // of the tiles split
-  const int in = static_cast<int>(q % kPerTile);
-  const Tile tile = tile_of<BM, BN>(a, a.whole + u * a.splits);
-  const int r = in / (BN / 8), c = in % (BN / 8) * 8;
+  const int per_row = a.bn / 8;
+  const int u = blockIdx.y;  // of the tiles split
+  const Tile tile = tile_of<BM>(a, a.whole + u * a.splits);
+  const int in = blockIdx.x * 256 + threadIdx.x;
+  const int r = in / per_row, c = in % per_row * 8;
   const int64_t i = tile.row + r, j = tile.col + c;
-  if (i >= a.rows || j >= a.cols) return;
+  wait_for_predecessor();
+  if (r >= BM || i >= a.rows || j >= a.cols) return;
   const Epilogue& e = a.e;
   const bool vec = e.vec && j + 8 <= a.cols;
   float x[8] = {};
-  const float* p = parts + (static_cast<int64_t>(u) * a.splits * BM + r) * BN + c;
+  const float* p = parts + (static_cast<int64_t>(u) * a.splits * BM + r) * a.bn + c;
 #pragma unroll 4
-  for (int s = 0; s < a.splits; ++s, p += BM * BN) {
+  for (int s = 0; s < a.splits; ++s, p += BM * a.bn) {
     const float4 v = __ldcg(reinterpret_cast<const float4*>(p));
     const float4 w = __ldcg(reinterpret_cast<const float4*>(p) + 1);
     x[0] += v.x; x[1] += v.y; x[2] += v.z; x[3] += v.w;
@@ -637,6 +652,11 @@ struct Product {
 // the workspace follow from the sizes alone.
 constexpr int kSms = 152;
 
+// Rows of A that a CTA brings.
+int a_rows_of(int64_t rows, int cg, bool a_mn) {
+  return cg == 1 && !a_mn && rows < kBlockRows ? static_cast<int>(round_up(rows, 8)) : kBlockRows;
+}
+
 struct Plan {
   int cg, bn;
   int whole, splits;  // as in ProductArgs
@@ -648,44 +668,62 @@ struct Plan {
 
 // The shape of the tiles, and how the last round of them is spread: with T tiles
 // on U units (pairs of SMs, or SMs) the tiles past the last multiple of U would
-// leave most units idle, so their reduction is cut into parts.  Costs are in
-// stages of a 256 x 256 tile on two SMs (0.65 us): a narrower tile feeds the
-// tensor cores less well, and joining the parts is one more launch (4 us) and
-// two passes over them.
-Plan plan_product(int64_t rows, int64_t cols, int64_t depth) {
+// leave most units idle, so their reduction may be cut into parts, which are
+// joined by one more launch and two passes over them.  The least estimate in
+// microseconds is taken, from what was measured: a stage of 256 x 256 on two SMs
+// takes 0.65, of 128 x 128 on one 0.35, and narrower tiles feed the tensor cores
+// less well; a stage's distinct rows of A and B come from HBM at 6.5 TB/s at
+// best and 1.3 after they are asked for, a ring ahead, which is what counts for a
+// few rows; 3 for a round's end (filling the ring, the last epilogue), 3 for the
+// join.
+Plan plan_product(int64_t rows, int64_t cols, int64_t depth, bool a_mn, bool b_mn) {
   const int64_t steps = (depth + kStep - 1) / kStep;
   Plan best{2, 256, 0, 1, 0};
   if (rows < 1 || cols < 1) return best;
   double least = 1e300;
-  const struct { int cg, bn; double step; } shapes[] = {{2, 256, 1.0}, {2, 128, 0.6}, {1, 128, 0.6}};
-  for (const auto& s : shapes) {
-    const int64_t tm = (rows + 128 * s.cg - 1) / (128 * s.cg), tn = (cols + s.bn - 1) / s.bn;
-    const int64_t tiles = tm * tn, units = kSms / s.cg, rest = tiles % units;
-    const int64_t whole = tiles - rest;
-    if (tiles > INT32_MAX / 64) continue;
-    for (int parts = 1; parts <= 16 && (parts == 1 || (rest > 0 && parts * 2 <= steps)); ++parts) {
-      const int64_t rounds = (rest * parts + units - 1) / units;
-      const Plan p{s.cg, s.bn, static_cast<int>(parts > 1 ? whole : tiles), parts,
-                   static_cast<int>(parts > 1 ? rest : 0)};
-      // a round's end: filling the ring, and the last tile's epilogue
-      const double ends = 4.0;
-      double cost = s.step * (whole / units * steps + rounds * ((steps + parts - 1) / parts)) + ends;
-      if (parts > 1) cost += 6.0 + p.part_bytes() * 2 / 3.0e6;
-      if (p.part_bytes() > (int64_t{64} << 20)) continue;
-      if (cost < least) {
-        least = cost;
-        best = p;
+  for (int cg = 2; cg >= 1; --cg) {
+    const int most = cg == 2 ? 256 : 128;
+    // MN-major operands come in columns of 64 per CTA
+    const int unit = b_mn ? 64 * cg : 32;
+    const int64_t units = kSms / cg, tm = (rows + 128 * cg - 1) / (128 * cg);
+    for (int bn = most; bn >= unit; bn -= unit) {
+      const int64_t tn = (cols + bn - 1) / bn;
+      if (tm * tn > INT32_MAX / 64) continue;
+      const int64_t tiles = tm * tn, rest = tiles % units, whole = tiles - rest;
+      const double mma = cg == 2 ? 0.65 * (0.2 + 0.8 * bn / 256) : 0.35 * (0.3 + 0.7 * bn / 128);
+      const auto stage = [&](int64_t active) {
+        const double distinct = static_cast<double>(active < tn ? active : tn) * bn +
+                                static_cast<double>(active < tm ? active : tm) * 128 * cg;
+        const double read = distinct * (2 * kStep) / 6.5e6;
+        const double wait = 1.3 / ring_stages(a_rows_of(rows, cg, a_mn), bn / cg);
+        return mma > read && mma > wait ? mma : read > wait ? read : wait;
+      };
+      double cost = whole / units * steps * (whole > 0 ? stage(units) : 0.0) + 3.0;
+      const double before = cost;
+      for (int parts = 1; parts <= 16; ++parts) {
+        if (parts > 1 && (rest == 0 || parts * 2 > steps)) break;
+        const Plan p{cg, bn, static_cast<int>(parts > 1 ? whole : tiles), parts,
+                     static_cast<int>(parts > 1 ? rest : 0)};
+        if (p.part_bytes() > (int64_t{64} << 20)) break;
+        const int64_t items = rest * parts, rounds = (items + units - 1) / units;
+        const int64_t deep = (steps + parts - 1) / parts;
+        cost = before + rounds * deep * (items > 0 ? stage(items < units ? items : units) : 0.0);
+        if (parts > 1) cost += 3.0 + p.part_bytes() * 2 / 5.0e6;
+        if (cost < least) {
+          least = cost;
+          best = p;
+        }
       }
     }
   }
   return best;
 }
 
-template <int CG, int BN, bool A_MN, bool B_MN, Kind KIND>
+template <int CG, bool A_MN, bool B_MN, Kind KIND>
 cudaError_t launch_shape(const Product& p, const Plan& plan, ProductArgs& a, float* parts,
                          cudaStream_t stream) {
-  using Shape = ProductShape<CG, BN>;
-  auto kernel = linear_product_kernel<CG, BN, A_MN, B_MN, KIND>;
+  const int bn = plan.bn;
+  auto kernel = linear_product_kernel<CG, A_MN, B_MN, KIND>;
   static std::mutex mu;
   static bool configured[64] = {false};
   int dev = 0, sms = 0;
@@ -695,30 +733,32 @@ cudaError_t launch_shape(const Product& p, const Plan& plan, ProductArgs& a, flo
   {
     std::lock_guard<std::mutex> lock(mu);
     if (!configured[dev]) {
-      e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Shape::kSmem);
+      e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
       if (e != cudaSuccess) return e;
       configured[dev] = true;
     }
   }
-  e = make_map(&a.a, p.a, A_MN ? kDepth : kBlockRows);
-  if (e == cudaSuccess) e = make_map(&a.b, p.b, B_MN ? kDepth : Shape::kBRows);
+  a.a_rows = a_rows_of(p.rows, CG, A_MN);
+  e = make_map(&a.a, p.a, A_MN ? kDepth : a.a_rows);
+  if (e == cudaSuccess) e = make_map(&a.b, p.b, B_MN ? kDepth : bn / CG);
   if (e != cudaSuccess) return e;
-  const int64_t tm = (p.rows + CG * kBlockRows - 1) / (CG * kBlockRows), tn = (p.cols + BN - 1) / BN;
+  const int64_t tm = (p.rows + CG * kBlockRows - 1) / (CG * kBlockRows), tn = (p.cols + bn - 1) / bn;
   if (tm * tn > INT32_MAX / 64) return cudaErrorInvalidValue;
   a.tiles_m = static_cast<int32_t>(tm);
   a.tiles_n = static_cast<int32_t>(tn);
+  a.bn = bn;
   a.whole = plan.whole;
   a.splits = plan.splits;
   if (plan.splits > 1) {
-    e = make_out_map(&a.parts, parts, CG * kBlockRows, BN, BN, plan.tail * plan.splits,
-                     CG * kBlockRows * BN, true);
+    e = make_out_map(&a.parts, parts, CG * kBlockRows, bn, bn, plan.tail * plan.splits,
+                     CG * kBlockRows * bn, true);
     if (e != cudaSuccess) return e;
   }
   const int64_t units = sms / CG, tiles = plan.whole + int64_t{plan.tail} * plan.splits;
   cudaLaunchConfig_t config = {};
   config.gridDim = dim3(static_cast<unsigned>(CG * (tiles < units ? tiles : units)));
   config.blockDim = dim3(kProductThreads);
-  config.dynamicSmemBytes = Shape::kSmem;
+  config.dynamicSmemBytes = kSmem;
   config.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -729,18 +769,21 @@ cudaError_t launch_shape(const Product& p, const Plan& plan, ProductArgs& a, flo
   config.numAttrs = 1;
   e = cudaLaunchKernelEx(&config, kernel, a);
   if (e != cudaSuccess || plan.splits == 1) return e;
-  linear_join_kernel<CG * kBlockRows, BN>
-      <<<plan.tail * (CG * kBlockRows * BN / 8 / 256), 256, 0, stream>>>(a, parts);
-  return cudaGetLastError();
+  const int64_t high = p.rows < CG * kBlockRows ? p.rows : CG * kBlockRows;
+  config.gridDim = dim3(static_cast<unsigned>((high * (bn / 8) + 255) / 256), plan.tail);
+  config.blockDim = dim3(256);
+  config.dynamicSmemBytes = 0;
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  return cudaLaunchKernelEx(&config, linear_join_kernel<CG * kBlockRows>, a,
+                            static_cast<const float*>(parts));
 }
 
 template <bool A_MN, bool B_MN, Kind KIND>
 cudaError_t launch_kind(const Product& p, const Plan& plan, ProductArgs& a, float* parts,
                         cudaStream_t stream) {
-  if (plan.cg == 2 && plan.bn == 256)
-    return launch_shape<2, 256, A_MN, B_MN, KIND>(p, plan, a, parts, stream);
-  if (plan.cg == 2) return launch_shape<2, 128, A_MN, B_MN, KIND>(p, plan, a, parts, stream);
-  return launch_shape<1, 128, A_MN, B_MN, KIND>(p, plan, a, parts, stream);
+  return plan.cg == 2 ? launch_shape<2, A_MN, B_MN, KIND>(p, plan, a, parts, stream)
+                      : launch_shape<1, A_MN, B_MN, KIND>(p, plan, a, parts, stream);
 }
 
 void set_vec(Epilogue* e, int64_t rows) {
@@ -757,7 +800,7 @@ cudaError_t launch_product(Product p, Space space, int withhold, cudaStream_t st
   if (err == cudaSuccess) err = make_tileable(&p.b, &space, stream);
   if (err != cudaSuccess) return err;
   set_vec(&p.e, p.rows);
-  const Plan plan = plan_product(p.rows, p.cols, p.depth);
+  const Plan plan = plan_product(p.rows, p.cols, p.depth, p.a_mn, p.b_mn);
   ProductArgs a{};
   a.e = p.e;
   a.rows = p.rows;
@@ -784,8 +827,9 @@ cudaError_t launch_product(Product p, Space space, int withhold, cudaStream_t st
 
 // Workspace of a product; `moved`: of its operands, where they have to be laid
 // out anew.
-int64_t product_bytes(int64_t moved, int64_t rows, int64_t cols, int64_t depth) {
-  return moved + round_up(plan_product(rows, cols, depth).part_bytes(), 256);
+int64_t product_bytes(int64_t moved, int64_t rows, int64_t cols, int64_t depth, bool a_mn,
+                      bool b_mn) {
+  return moved + round_up(plan_product(rows, cols, depth, a_mn, b_mn).part_bytes(), 256);
 }
 
 // --------------------------------------------------------------- a few rows
@@ -798,7 +842,7 @@ int64_t product_bytes(int64_t moved, int64_t rows, int64_t cols, int64_t depth) 
 // x 11008).  A lane's 16-byte load is 8 neighbours of one row; which steps of
 // the reduction an instruction's operands belong to does not matter as long as
 // W's and x's agree, so the vectors are its operands as they are.  All loads of
-// 256 (128) columns are in flight at once; x comes from L1.  The shares are
+// 64 or 128 columns are in flight at once; x comes from L1.  The shares are
 // added through shared memory in their order.
 
 constexpr int kFewRows = 16, kFewWarps = 8;
@@ -818,7 +862,7 @@ __device__ __forceinline__ uint4 few_load(const uint16_t* p, int j, int n) {
   if (VEC && j + 8 <= n) {
     uint4 v;
     if (STREAM)
-      asm volatile("ld.global.nc.L1::no_allocate.v4.b32 {%0, %1, %2, %3}, [%4];"
+      asm volatile("ld.global.nc.L1::no_allocate.L2::256B.v4.b32 {%0, %1, %2, %3}, [%4];"
                    : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
                    : "l"(p + j));
     else
@@ -842,11 +886,10 @@ __device__ __forceinline__ void warp_mma(float d[4], uint32_t a0, uint32_t a1, u
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// NT: groups of 8 rows of x.
-template <int NT, bool VEC>
-__global__ void __launch_bounds__(32 * kFewWarps)
+// NT: groups of 8 rows of x; U: loads of each row in flight.
+template <int NT, int U, bool VEC>
+__global__ void __launch_bounds__(32 * kFewWarps, U == 2 ? 5 : 3)
     linear_few_rows_kernel(const __grid_constant__ FewArgs a) {
-  constexpr int U = NT == 1 ? 8 : 4;     // loads of each row in flight
   constexpr int kSpan = 32 * U;          // columns a warp takes at a time
   __shared__ float part[kFewWarps][16 * 8 * NT];
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, g = lane / 4, t = lane % 4;
@@ -908,10 +951,17 @@ cudaError_t launch_few_groups(FewArgs& a, bool vec, cudaStream_t stream) {
     a.share *= 2;
   const int64_t blocks = (groups + kFewWarps / a.share - 1) / (kFewWarps / a.share);
   if (blocks > INT32_MAX) return cudaErrorInvalidValue;
-  if (vec)
-    linear_few_rows_kernel<NT, true><<<static_cast<unsigned>(blocks), 32 * kFewWarps, 0, stream>>>(a);
-  else
-    linear_few_rows_kernel<NT, false><<<static_cast<unsigned>(blocks), 32 * kFewWarps, 0, stream>>>(a);
+  // Many blocks: few registers, 5 blocks an SM; few: more in flight by each warp
+  // (1 x 4096 x 11008, 688 blocks: 16.2 us against 19.5 with the 4 loads that 1 x
+  // 11008 x 4096, 256 blocks, wants: 18.5 against 25.1).
+  const unsigned grid = static_cast<unsigned>(blocks), threads = 32 * kFewWarps;
+  if (blocks >= 3 * kSms) {
+    if (vec) linear_few_rows_kernel<NT, 2, true><<<grid, threads, 0, stream>>>(a);
+    else linear_few_rows_kernel<NT, 2, false><<<grid, threads, 0, stream>>>(a);
+  } else {
+    if (vec) linear_few_rows_kernel<NT, 4, true><<<grid, threads, 0, stream>>>(a);
+    else linear_few_rows_kernel<NT, 4, false><<<grid, threads, 0, stream>>>(a);
+  }
   return cudaGetLastError();
 }
 
@@ -1040,10 +1090,11 @@ int64_t linear_workspace(const zero_linear_t& s, int32_t flags) {
   const int64_t x = in_place ? 0 : copy_bytes(Stored(nullptr, s.rows, s.in, 0));
   const int64_t w = in_place ? 0 : copy_bytes(Stored(nullptr, s.out, s.in, 0));
   if ((flags & ZERO_LINEAR_BACKWARD) == 0)
-    return s.rows <= kFewRows ? 0 : product_bytes(x + w, s.rows, s.out, s.in);
+    return s.rows <= kFewRows ? 0 : product_bytes(x + w, s.rows, s.out, s.in, false, false);
   // dz is laid out once and taken by both products, one after the other
   const bool dz = !in_place || (flags & ZERO_LINEAR_PLAIN) == 0;
-  const int64_t dx = product_bytes(w, s.rows, s.in, s.out), dw = product_bytes(x, s.out, s.in, s.rows);
+  const int64_t dx = product_bytes(w, s.rows, s.in, s.out, false, true);
+  const int64_t dw = product_bytes(x, s.out, s.in, s.rows, true, true);
   return (dz ? copy_bytes(Stored(nullptr, s.rows, s.out, 0)) : 0) +
          round_up(slope_blocks(s.rows) * s.out * 4, 256) + (dx > dw ? dx : dw);
 }

@@ -135,6 +135,15 @@ __device__ __forceinline__ uint64_t smem_desc(uint32_t addr, uint32_t lead, uint
          (uint64_t{2} << 61);   // 128-byte swizzle
 }
 
+// The next kernel of the stream, launched as a programmatic dependent, may begin;
+// and: this one's predecessor is complete and its writes are visible.
+__device__ __forceinline__ void launch_dependents() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+__device__ __forceinline__ void wait_for_predecessor() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
 // Instruction descriptor of kind::f16: bf16 operands, fp32 accumulators.
 __host__ __device__ constexpr uint32_t mma_desc(int m, int n, bool a_mn, bool b_mn) {
   return (1u << 4) | (1u << 7) | (1u << 10) | (a_mn ? 1u << 15 : 0u) | (b_mn ? 1u << 16 : 0u) |
