@@ -137,33 +137,54 @@ __device__ __noinline__ void epilogue_scalar(const Epilogue& e, const float* min
 // 8192 x 2048 x 8192.  A warp has 4 KB: two slots of bf16, or one of fp32, in
 // TMA's swizzle, which keeps the lanes' 16-byte writes off each other's banks.
 // fp32 gradients are added to what is there by the copy itself.
+//
+// The parameters are taken into registers once, and each step is one branch
+// around its 32 columns: a warp runs a part alone, with nothing to hide a
+// branch or a constant's load behind (a branch for each 8 columns, its pointer
+// loaded anew, made a part 2,400 cycles).
 template <Kind KIND>
 struct EpiloguePart {
-  uint4 in[4];     // the residual, the slope's argument or the old value of the lane's row
-  uint4 bias[4];
+  const uint16_t *from, *bias_from;  // what it reads; NULL: nothing
+  int64_t from_pitch;
+  int32_t act;       // of the sum, or whose slope it is multiplied with
+  bool pre, add;     // pre is written; what is read is added
   int slot = 0;
+  uint4 in[4], bias[4];
 
+  __device__ __forceinline__ explicit EpiloguePart(const Epilogue& e)
+      : from(nullptr), bias_from(nullptr), from_pitch(0), act(ZERO_ACT_NONE), pre(false), add(true) {
+    if constexpr (KIND == kForward) {
+      from = e.residual;
+      from_pitch = e.ldr;
+      bias_from = e.bias;
+      act = e.act;
+      pre = e.pre != nullptr;
+    } else if constexpr (KIND == kGradient) {
+      add = e.accumulate != 0;
+      from = add ? static_cast<const uint16_t*>(e.out) : e.slope_of;
+      from_pitch = add ? e.ldo : e.lds;
+      act = e.slope_act;
+    } else {
+      add = e.accumulate != 0;
+    }
+  }
   // Asks for what the part reads, before its sums are there.
-  __device__ __forceinline__ void ask(const Epilogue& e, int64_t row, int64_t col, bool mine) {
+  __device__ __forceinline__ void ask(int64_t row, int64_t col, bool mine) {
     if constexpr (KIND != kFloat) {
-      const uint16_t* p = KIND == kForward ? e.residual
-                          : e.accumulate   ? static_cast<const uint16_t*>(e.out)
-                                           : e.slope_of;
-      const int64_t ld = KIND == kForward ? e.ldr : e.accumulate ? e.ldo : e.lds;
-      if (p != nullptr && mine) {
+      if (from != nullptr && mine) {
+        const uint4* p = reinterpret_cast<const uint4*>(from + row * from_pitch + col);
 #pragma unroll
-        for (int q = 0; q < 4; ++q)
-          in[q] = *reinterpret_cast<const uint4*>(p + row * ld + col + 8 * q);
+        for (int q = 0; q < 4; ++q) in[q] = p[q];
       }
-      if (KIND == kForward && e.bias != nullptr) {
+      if (KIND == kForward && bias_from != nullptr) {
+        const uint4* p = reinterpret_cast<const uint4*>(bias_from + col);
 #pragma unroll
-        for (int q = 0; q < 4; ++q)
-          bias[q] = __ldg(reinterpret_cast<const uint4*>(e.bias + col + 8 * q));
+        for (int q = 0; q < 4; ++q) bias[q] = __ldg(p + q);
       }
     }
   }
   // 32 columns of bf16 into a slot and off.
-  __device__ __forceinline__ void send(const CUtensorMap* map, uint8_t* staging, const uint4 v[4],
+  __device__ __forceinline__ void send(const CUtensorMap* map, uint8_t* staging, const float v[32],
                                        int x, int y, int lane) {
     if (lane == 0) bulk_wait_read<1>();  // the copy before the last has left this slot
     __syncwarp();
@@ -171,7 +192,7 @@ struct EpiloguePart {
     slot ^= 1;
 #pragma unroll
     for (int q = 0; q < 4; ++q)
-      *reinterpret_cast<uint4*>(to + lane * 64 + ((q ^ ((lane >> 1) & 3)) * 16)) = v[q];
+      *reinterpret_cast<uint4*>(to + lane * 64 + ((q ^ ((lane >> 1) & 3)) * 16)) = to_bf16x8(v + 8 * q);
     fence_async_shared();
     __syncwarp();
     if (lane == 0) {
@@ -181,57 +202,65 @@ struct EpiloguePart {
   }
   // 32 columns of fp32 as they are.
   __device__ __forceinline__ void send_sums(const CUtensorMap* map, uint8_t* staging,
-                                            const uint32_t sums[32], int x, int y, int z, bool add,
+                                            const float v[32], int x, int y, int z, bool sum,
                                             int lane) {
     if (lane == 0) bulk_wait_read<0>();
     __syncwarp();
 #pragma unroll
     for (int q = 0; q < 8; ++q)
-      *reinterpret_cast<uint4*>(staging + 4 * staged(lane, q)) =
-          make_uint4(sums[4 * q], sums[4 * q + 1], sums[4 * q + 2], sums[4 * q + 3]);
+      *reinterpret_cast<float4*>(staging + 4 * staged(lane, q)) =
+          make_float4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
     fence_async_shared();
     __syncwarp();
     if (lane == 0) {
-      tile_store(map, staging, x, y, z, add);
+      tile_store(map, staging, x, y, z, sum);
       bulk_commit();
     }
   }
-  __device__ __forceinline__ void put(const ProductArgs& a, uint8_t* staging,
-                                      const uint32_t sums[32], int64_t row0, int64_t col, int lane) {
-    const Epilogue& e = a.e;
-    const int x0 = static_cast<int>(col), y0 = static_cast<int>(row0);
+  __device__ __forceinline__ static void plus(float v[32], const uint4 w[4]) {
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      float y[8];
+      bf16x8(w[q], y);
+#pragma unroll
+      for (int c = 0; c < 8; ++c) v[8 * q + c] += y[c];
+    }
+  }
+  template <int ACT>
+  __device__ __forceinline__ void times_slope(float v[32]) {
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      float z[8];
+      bf16x8(in[q], z);
+#pragma unroll
+      for (int c = 0; c < 8; c += 2)
+        times_slope2<ACT>(v[8 * q + c], v[8 * q + c + 1], z[c], z[c + 1]);
+    }
+  }
+  template <int ACT>
+  __device__ __forceinline__ static void activate(float v[32]) {
+#pragma unroll
+    for (int c = 0; c < 32; c += 2) act_value2<ACT>(v[c], v[c + 1]);
+  }
+  __device__ __forceinline__ void put(const ProductArgs& a, uint8_t* staging, float v[32], int row,
+                                      int col, int lane) {
     if constexpr (KIND == kFloat) {
-      send_sums(&a.out, staging, sums, x0, y0, 0, e.accumulate != 0, lane);
+      send_sums(&a.out, staging, v, col, row, 0, add, lane);
     } else {
-      uint4 v[4], pre[4];
-      const bool reads = KIND == kForward ? e.residual != nullptr : e.accumulate || e.slope_of != nullptr;
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        float x[8], y[8];
-#pragma unroll
-        for (int c = 0; c < 8; ++c) x[c] = __uint_as_float(sums[8 * q + c]);
-        if constexpr (KIND == kForward) {
-          if (e.bias != nullptr) {
-            bf16x8(bias[q], y);
-#pragma unroll
-            for (int c = 0; c < 8; ++c) x[c] += y[c];
-          }
-          if (e.pre != nullptr) pre[q] = to_bf16x8(x);
-          act_value8(x, e.act);
-        }
-        if (reads) {
-          if (KIND == kForward || e.accumulate) {
-            bf16x8(in[q], y);
-#pragma unroll
-            for (int c = 0; c < 8; ++c) x[c] += y[c];
-          } else {
-            times_slope8(x, in[q], e.slope_act);
-          }
-        }
-        v[q] = to_bf16x8(x);
+      if constexpr (KIND == kForward) {
+        if (bias_from != nullptr) plus(v, bias);
+        if (pre) send(&a.pre, staging, v, col, row, lane);
+        if (act == ZERO_ACT_GELU) activate<ZERO_ACT_GELU>(v);
+        else if (act == ZERO_ACT_SILU) activate<ZERO_ACT_SILU>(v);
+        else if (act == ZERO_ACT_RELU) activate<ZERO_ACT_RELU>(v);
       }
-      if (KIND == kForward && e.pre != nullptr) send(&a.pre, staging, pre, x0, y0, lane);
-      send(&a.out, staging, v, x0, y0, lane);
+      if (from != nullptr) {
+        if (KIND == kForward || add) plus(v, in);
+        else if (act == ZERO_ACT_GELU) times_slope<ZERO_ACT_GELU>(v);
+        else if (act == ZERO_ACT_SILU) times_slope<ZERO_ACT_SILU>(v);
+        else if (act == ZERO_ACT_RELU) times_slope<ZERO_ACT_RELU>(v);
+      }
+      send(&a.out, staging, v, col, row, lane);
     }
   }
 };
@@ -409,7 +438,10 @@ __global__ void __launch_bounds__(kProductThreads, 1)
   } else {
     const int quarter = warp % 4, half = (warp - 2) / 4;
     float* mine = staging + (warp - 2) * 32 * 32;
-    EpiloguePart<KIND> part;
+    EpiloguePart<KIND> part(a.e);
+    const bool vec = a.e.vec != 0;
+    const int bn = a.bn;
+    const int64_t rows = a.rows, cols = a.cols;
     int n = 0;
     for (int t = unit; t < tiles; t += units, ++n) {
       const Tile tile = tile_of<BM>(a, t);
@@ -422,25 +454,32 @@ __global__ void __launch_bounds__(kProductThreads, 1)
       const int64_t row0 = tile.row + rank * kBlockRows + quarter * 32;
       const uint32_t from =
           tmem + (static_cast<uint32_t>(quarter * 32) << 16) + b * Shape::kMaxCols;
-      if (32 * half >= a.bn) {  // nothing of a tile this narrow is this warp's
+      // (rows past the end are left out by the copy)
+      const bool any = row0 < rows;
+      const bool fast = any && vec && tile.part < 0 && tile.col + bn <= cols;
+      const bool mine_in = row0 + lane < rows;
+      if (32 * half >= bn) {  // nothing of a tile this narrow is this warp's
         __syncwarp();
         if (lane == 0) {
           if constexpr (CG == 2) mbar_arrive_peer(peer_addr(&free_[b], 0));
           else mbar_arrive(&free_[b]);
         }
       }
+      uint32_t bits[32];
+      if (32 * half < bn) {
+        tmem_load32(from + 32 * half, bits);
+        if (fast) part.ask(row0 + lane, tile.col + 32 * half, mine_in);
+      }
 #pragma unroll 1
-      for (int c = 32 * half; c < a.bn; c += 64) {
+      for (int c = 32 * half; c < bn; c += 64) {
         const int64_t col0 = tile.col + c;
-        const bool any = row0 < a.rows && col0 < a.cols;
-        const bool split = tile.part >= 0;
-        // (rows past the end are left out)
-        const bool whole = any && a.e.vec && !split && col0 + 32 <= a.cols;
-        uint32_t x[32];
-        tmem_load32(from + c, x);
-        if (whole) part.ask(a.e, row0 + lane, col0, row0 + lane < a.rows);
+        float x[32];
         tmem_load_wait();
-        if (c + 64 >= a.bn) {  // the warp has read its part: this half may be written again
+#pragma unroll
+        for (int q = 0; q < 32; ++q) x[q] = __uint_as_float(bits[q]);
+        if (c + 64 < bn) {  // the next part's sums come while this one's are worked on
+          tmem_load32(from + c + 64, bits);
+        } else {  // the warp has read its part: this half may be written again
           tc_fence_before();
           __syncwarp();
           if (lane == 0) {
@@ -448,21 +487,29 @@ __global__ void __launch_bounds__(kProductThreads, 1)
             else mbar_arrive(&free_[b]);
           }
         }
-        if (whole) {
-          part.put(a, reinterpret_cast<uint8_t*>(mine), x, row0, col0, lane);
-        } else if (split) {
-          if (any)
-            part.send_sums(&a.parts, reinterpret_cast<uint8_t*>(mine), x, c,
-                           static_cast<int>(row0 - tile.row), tile.part, false, lane);
-        } else if (any) {
+        if (fast) {
+          part.put(a, reinterpret_cast<uint8_t*>(mine), x, static_cast<int>(row0),
+                   static_cast<int>(col0), lane);
+          if (c + 64 < bn) part.ask(row0 + lane, col0 + 64, mine_in);
+          continue;
+        }
+        if (!any || col0 >= cols) continue;
+        if (tile.part >= 0) {
+          part.send_sums(&a.parts, reinterpret_cast<uint8_t*>(mine), x, c,
+                         static_cast<int>(row0 - tile.row), tile.part, false, lane);
+        } else if (vec && col0 + 32 <= cols) {
+          part.ask(row0 + lane, col0, mine_in);
+          part.put(a, reinterpret_cast<uint8_t*>(mine), x, static_cast<int>(row0),
+                   static_cast<int>(col0), lane);
+        } else {
           if (lane == 0) bulk_wait_read<0>();
           __syncwarp();
 #pragma unroll
           for (int q = 0; q < 8; ++q)
-            *reinterpret_cast<uint4*>(mine + staged(lane, q)) =
-                make_uint4(x[4 * q], x[4 * q + 1], x[4 * q + 2], x[4 * q + 3]);
+            *reinterpret_cast<float4*>(mine + staged(lane, q)) =
+                make_float4(x[4 * q], x[4 * q + 1], x[4 * q + 2], x[4 * q + 3]);
           __syncwarp();
-          epilogue_scalar(a.e, mine, row0, col0, a.rows, a.cols, lane);
+          epilogue_scalar(a.e, mine, row0, col0, rows, cols, lane);
           __syncwarp();
         }
       }
@@ -538,7 +585,11 @@ struct Stored {
 
 // Whether TMA can read it in place.
 bool tileable(const Stored& m) { return aligned(m.p, 16) && m.ld % 8 == 0; }
-int64_t copy_bytes(const Stored& m) { return round_up(m.rows * round_up(m.cols, 8) * 2, 256); }
+// Pitch and bytes of a copy: rows on 128-byte boundaries, one swizzled row of
+// TMA's each (with rows on odd multiples of 16 bytes its loads take twice the
+// time: 1003 x 776 x 2312 backward 21 to 26 us a product).
+int64_t copy_pitch(int64_t cols) { return round_up(cols, 64); }
+int64_t copy_bytes(const Stored& m) { return round_up(m.rows * copy_pitch(m.cols) * 2, 256); }
 
 struct CopyArgs {
   const uint16_t* src;
@@ -574,7 +625,7 @@ struct Space {
 cudaError_t make_tileable(Stored* m, Space* space, cudaStream_t stream) {
   if (tileable(*m)) return cudaSuccess;
   CopyArgs a{m->p, static_cast<uint16_t*>(space->take(copy_bytes(*m))), m->rows, m->cols, m->ld,
-             round_up(m->cols, 8)};
+             copy_pitch(m->cols)};
   const int64_t blocks = (m->rows * (a.ldd / 8) + 255) / 256;
   linear_copy_kernel<<<static_cast<unsigned>(blocks < 4096 ? blocks : 4096), 256, 0, stream>>>(a);
   m->p = a.dst;
@@ -670,12 +721,12 @@ struct Plan {
 // on U units (pairs of SMs, or SMs) the tiles past the last multiple of U would
 // leave most units idle, so their reduction may be cut into parts, which are
 // joined by one more launch and two passes over them.  The least estimate in
-// microseconds is taken, from what was measured: a stage of 256 x 256 on two SMs
-// takes 0.65, of 128 x 128 on one 0.35, and narrower tiles feed the tensor cores
-// less well; a stage's distinct rows of A and B come from HBM at 6.5 TB/s at
-// best and 1.3 after they are asked for, a ring ahead, which is what counts for a
-// few rows; 3 for a round's end (filling the ring, the last epilogue), 3 for the
-// join.
+// microseconds is taken, fitted to a sweep of 20 shapes: a stage of 256 x 256 on
+// two SMs takes 0.65, of 256 x 128 0.47, of 128 x 128 on one SM 0.47, and no
+// narrower tile less than 0.42; a stage's distinct rows of A and B come from HBM
+// at 6.5 TB/s at best and 1.3 after they are asked for, a ring ahead, which is
+// what counts for a few rows; 3 for a kernel's beginning and end, 0.9 for each 64
+// columns of its last epilogue, 3 for the join's launch.
 Plan plan_product(int64_t rows, int64_t cols, int64_t depth, bool a_mn, bool b_mn) {
   const int64_t steps = (depth + kStep - 1) / kStep;
   Plan best{2, 256, 0, 1, 0};
@@ -690,7 +741,8 @@ Plan plan_product(int64_t rows, int64_t cols, int64_t depth, bool a_mn, bool b_m
       const int64_t tn = (cols + bn - 1) / bn;
       if (tm * tn > INT32_MAX / 64) continue;
       const int64_t tiles = tm * tn, rest = tiles % units, whole = tiles - rest;
-      const double mma = cg == 2 ? 0.65 * (0.2 + 0.8 * bn / 256) : 0.35 * (0.3 + 0.7 * bn / 128);
+      const double share = static_cast<double>(bn) / most;
+      const double mma = cg == 2 ? 0.40 + 0.25 * share * share : 0.42 + 0.055 * share * share;
       const auto stage = [&](int64_t active) {
         const double distinct = static_cast<double>(active < tn ? active : tn) * bn +
                                 static_cast<double>(active < tm ? active : tm) * 128 * cg;
@@ -698,7 +750,7 @@ Plan plan_product(int64_t rows, int64_t cols, int64_t depth, bool a_mn, bool b_m
         const double wait = 1.3 / ring_stages(a_rows_of(rows, cg, a_mn), bn / cg);
         return mma > read && mma > wait ? mma : read > wait ? read : wait;
       };
-      double cost = whole / units * steps * (whole > 0 ? stage(units) : 0.0) + 3.0;
+      double cost = whole / units * steps * (whole > 0 ? stage(units) : 0.0) + 3.0 + 0.9 * bn / 64;
       const double before = cost;
       for (int parts = 1; parts <= 16; ++parts) {
         if (parts > 1 && (rest == 0 || parts * 2 > steps)) break;
@@ -1136,7 +1188,7 @@ cudaError_t launch_linear_backward(const LinearBackwardLaunch& L) {
     a.act = L.act;
     if (L.act != ZERO_ACT_NONE && (L.dx != nullptr || L.dw != nullptr)) {
       a.dz = static_cast<uint16_t*>(space.take(copy_bytes(dz)));
-      a.ldz = round_up(s.out, 8);
+      a.ldz = copy_pitch(s.out);
       dz = Stored(a.dz, s.rows, s.out, a.ldz);
     }
     const int64_t blocks = slope_blocks(s.rows);

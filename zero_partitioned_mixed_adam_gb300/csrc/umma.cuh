@@ -19,8 +19,13 @@ __device__ __forceinline__ uint32_t cluster_rank() {
   asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
   return r;
 }
+// Every thread of the cluster is here.  No thread's writes are waited for (a
+// release at cluster scope drains its global stores, over 1,000 cycles): what
+// the kernels pass on goes by barriers of its own, whose initialisation
+// mbar_init_fence publishes.
 __device__ __forceinline__ void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.aligned;\n barrier.cluster.wait.aligned;" ::: "memory");
+  asm volatile("barrier.cluster.arrive.relaxed.aligned;\n barrier.cluster.wait.aligned;" ::
+                   : "memory");
 }
 // The address, in the cluster's shared window, of CTA `rank`'s copy of `p`.
 __device__ __forceinline__ uint32_t peer_addr(const void* p, uint32_t rank) {
@@ -28,8 +33,10 @@ __device__ __forceinline__ uint32_t peer_addr(const void* p, uint32_t rank) {
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_addr(p)), "r"(rank));
   return a;
 }
+// Passes on no writes of this thread (relaxed, as above); reads of tensor memory
+// are ordered by tc_fence_before.
 __device__ __forceinline__ void mbar_arrive_peer(uint32_t addr) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(addr)
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(addr)
                : "memory");
 }
 
