@@ -390,7 +390,12 @@ __device__ __forceinline__ void moments_tile(const MomentsDesc& t, int64_t base,
     x[j] = __fmul_rn(t.is_m ? __fmul_rn(bits_of_m(w, j % 4), kMUp) : __fmul_rn(bits_of_v(w, j % 4), kVUp),
                      scale);
   }
-  store_f32<VEC>(t.out, i, t.numel, x);
+  if (VEC)  // a lane's 32 bytes at once: two halves took 1,331 us where this takes 1,211 (8e8)
+    asm volatile("st.global.v8.f32 [%8], {%0, %1, %2, %3, %4, %5, %6, %7};" ::"f"(x[0]), "f"(x[1]),
+                 "f"(x[2]), "f"(x[3]), "f"(x[4]), "f"(x[5]), "f"(x[6]), "f"(x[7]), "l"(t.out + i)
+                 : "memory");
+  else
+    store_f32<false>(t.out, i, t.numel, x);
 }
 
 // A block a tile, in the order of memory.
@@ -621,7 +626,7 @@ cudaError_t launch_adamw_moments(const MomentsLaunch& L) {
       t.numel = x.numel;
       t.tile0 = static_cast<int32_t>(tiles);
       t.is_m = which == 0;
-      t.vec = aligned(t.codes, 8) && aligned(t.out, 16);
+      t.vec = aligned(t.codes, 8) && aligned(t.out, 32);
       tiles += (x.numel + kTile - 1) / kTile;
       if (a.count == kCap || tiles > INT32_MAX / 2) {
         const cudaError_t e = flush();

@@ -121,15 +121,64 @@ enum Kind {
 // lane writes its row nor where 4 or 8 lanes read one.
 __device__ __forceinline__ int staged(int r, int q) { return r * 32 + ((q ^ (r & 7)) * 4); }
 
-// Any layout, and the edges: a lane takes one column, row after row.
+// Any layout, and the edges: a lane takes one column, 8 rows at a time so that
+// their loads are under way together.
+template <Kind KIND>
 __device__ __noinline__ void epilogue_scalar(const Epilogue& e, const float* mine, int64_t row0,
                                              int64_t col0, int64_t rows, int64_t cols, int lane) {
   const int64_t j = col0 + lane;
   if (j >= cols) return;
   const int n = rows - row0 < 32 ? static_cast<int>(rows - row0) : 32;
-#pragma unroll 4
-  for (int r = 0; r < n; ++r)
-    epilogue_element(e, row0 + r, j, mine[staged(r, lane / 4) + lane % 4]);
+  const uint16_t* from = nullptr;
+  int64_t from_pitch = 0;
+  float bias = 0.0f;
+  const bool add = KIND == kForward || e.accumulate;
+  if constexpr (KIND == kForward) {
+    from = e.residual;
+    from_pitch = e.ldr;
+    if (e.bias != nullptr) bias = bf16_at(e.bias + j);
+  } else if constexpr (KIND == kGradient) {
+    from = e.accumulate ? static_cast<const uint16_t*>(e.out) : e.slope_of;
+    from_pitch = e.accumulate ? e.ldo : e.lds;
+  }
+  if (from != nullptr) from += row0 * from_pitch + j;
+  float* out32 = static_cast<float*>(e.out) + row0 * e.ldo + j;
+  uint16_t* out16 = static_cast<uint16_t*>(e.out) + row0 * e.ldo + j;
+  uint16_t* pre = KIND == kForward && e.pre != nullptr ? e.pre + row0 * e.ldp + j : nullptr;
+#pragma unroll 1
+  for (int r = 0; r < n; r += 8) {
+    float x[8], y[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      y[k] = 0.0f;
+      if (r + k < n) {
+        if (KIND == kFloat && e.accumulate) y[k] = out32[(r + k) * e.ldo];
+        if (KIND != kFloat && from != nullptr) y[k] = bf16_at(from + (r + k) * from_pitch);
+      }
+      x[k] = mine[staged(r + k, lane / 4) + lane % 4] + bias;
+    }
+    if (KIND == kForward) {
+      if (pre != nullptr) {
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          if (r + k < n) pre[(r + k) * e.ldp] = to_bf16(x[k]);
+      }
+      act_value8(x, e.act);
+    }
+    if (KIND == kGradient && !add && from != nullptr) {
+#pragma unroll
+      for (int k = 0; k < 8; ++k) x[k] *= act_slope(y[k], e.slope_act);
+    } else if (KIND == kFloat || from != nullptr) {
+#pragma unroll
+      for (int k = 0; k < 8; ++k) x[k] += y[k];
+    }
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      if (r + k >= n) break;
+      if (KIND == kFloat) out32[(r + k) * e.ldo] = x[k];
+      else out16[(r + k) * e.ldo] = to_bf16(x[k]);
+    }
+  }
 }
 
 // A 32 x 32 part, a row a lane, through shared memory and out by TMA: plain
@@ -509,7 +558,7 @@ __global__ void __launch_bounds__(kProductThreads, 1)
             *reinterpret_cast<float4*>(mine + staged(lane, q)) =
                 make_float4(x[4 * q], x[4 * q + 1], x[4 * q + 2], x[4 * q + 3]);
           __syncwarp();
-          epilogue_scalar(a.e, mine, row0, col0, rows, cols, lane);
+          epilogue_scalar<KIND>(a.e, mine, row0, col0, rows, cols, lane);
           __syncwarp();
         }
       }
@@ -571,7 +620,8 @@ __global__ void __launch_bounds__(256) linear_join_kernel(const __grid_constant_
 
 // ------------------------------------------------------------------ layouts
 
-int64_t round_up(int64_t x, int64_t k) { return (x + k - 1) / k * k; }
+__host__ __device__ constexpr int64_t round_up(int64_t x, int64_t k) { return (x + k - 1) / k * k; }
+__host__ __device__ constexpr int64_t round_up4(int64_t x) { return round_up(x, 4); }
 bool aligned(const void* p, uintptr_t k) { return (reinterpret_cast<uintptr_t>(p) & (k - 1)) == 0; }
 
 // A bf16 matrix as it lies in memory.  A single row has no pitch.
@@ -596,19 +646,26 @@ struct CopyArgs {
   uint16_t* dst;
   int64_t rows, cols, lds, ldd;
 };
+struct Copies {
+  CopyArgs of[3];
+};
 
-// A matrix laid out anew with rows on 16-byte boundaries: 8 elements a thread.
-__global__ void __launch_bounds__(256) linear_copy_kernel(const __grid_constant__ CopyArgs a) {
-  const int64_t per = (a.cols + 7) / 8;
-  for (int64_t q = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; q < a.rows * per;
-       q += static_cast<int64_t>(gridDim.x) * blockDim.x) {
-    const int64_t i = q / per, j = (q - i * per) * 8;
-    const uint16_t* s = a.src + i * a.lds + j;
-    uint32_t w[4] = {};
+// Matrices laid out anew with rows on 128-byte boundaries: 8 elements a thread,
+// read one by one and 64 bytes of a row by each warp at a time.
+__global__ void __launch_bounds__(256) linear_copy_kernel(const __grid_constant__ Copies all) {
+  const CopyArgs& a = all.of[blockIdx.y];
+  const int64_t per = (a.cols + 255) / 256;  // warps a row
+  const int lane = threadIdx.x % 32;
+  for (int64_t q = static_cast<int64_t>(blockIdx.x) * 8 + threadIdx.x / 32; q < a.rows * per;
+       q += static_cast<int64_t>(gridDim.x) * 8) {
+    const int64_t i = q / per, j0 = (q - i * per) * 256;
+    const uint16_t* s = a.src + i * a.lds + j0 + lane;
+    uint16_t x[8];
+#pragma unroll
+    for (int c = 0; c < 8; ++c) x[c] = j0 + 32 * c + lane < a.cols ? __ldg(s + 32 * c) : 0;
 #pragma unroll
     for (int c = 0; c < 8; ++c)
-      if (j + c < a.cols) w[c / 2] |= static_cast<uint32_t>(__ldg(s + c)) << (16 * (c & 1));
-    *reinterpret_cast<uint4*>(a.dst + i * a.ldd + j) = make_uint4(w[0], w[1], w[2], w[3]);
+      if (j0 + 32 * c + lane < a.cols) a.dst[i * a.ldd + j0 + 32 * c + lane] = x[c];
   }
 }
 
@@ -622,14 +679,26 @@ struct Space {
   }
 };
 
-cudaError_t make_tileable(Stored* m, Space* space, cudaStream_t stream) {
-  if (tileable(*m)) return cudaSuccess;
-  CopyArgs a{m->p, static_cast<uint16_t*>(space->take(copy_bytes(*m))), m->rows, m->cols, m->ld,
-             copy_pitch(m->cols)};
-  const int64_t blocks = (m->rows * (a.ldd / 8) + 255) / 256;
-  linear_copy_kernel<<<static_cast<unsigned>(blocks < 4096 ? blocks : 4096), 256, 0, stream>>>(a);
-  m->p = a.dst;
-  m->ld = a.ldd;
+// Lays the matrices that TMA cannot read where they are out anew, in one launch.
+cudaError_t make_tileable(Stored* const* matrices, int count, Space* space, cudaStream_t stream) {
+  Copies all{};
+  int n = 0;
+  int64_t most = 0;
+  for (int k = 0; k < count; ++k) {
+    Stored& m = *matrices[k];
+    if (m.p == nullptr || tileable(m)) continue;
+    const int64_t pitch = copy_pitch(m.cols);
+    CopyArgs& a = all.of[n++];
+    a = {m.p, static_cast<uint16_t*>(space->take(copy_bytes(m))), m.rows, m.cols, m.ld, pitch};
+    m.p = a.dst;
+    m.ld = pitch;
+    const int64_t warps = m.rows * ((m.cols + 255) / 256);
+    most = warps > most ? warps : most;
+  }
+  if (n == 0) return cudaSuccess;
+  const int64_t blocks = (most + 7) / 8;
+  const dim3 grid(static_cast<unsigned>(blocks < 16 * 152 ? blocks : 16 * 152), n);
+  linear_copy_kernel<<<grid, 256, 0, stream>>>(all);
   return cudaGetLastError();
 }
 
@@ -848,9 +917,7 @@ void set_vec(Epilogue* e, int64_t rows) {
 }
 
 cudaError_t launch_product(Product p, Space space, int withhold, cudaStream_t stream) {
-  cudaError_t err = make_tileable(&p.a, &space, stream);
-  if (err == cudaSuccess) err = make_tileable(&p.b, &space, stream);
-  if (err != cudaSuccess) return err;
+  cudaError_t err = cudaSuccess;
   set_vec(&p.e, p.rows);
   const Plan plan = plan_product(p.rows, p.cols, p.depth, p.a_mn, p.b_mn);
   ProductArgs a{};
@@ -1032,66 +1099,83 @@ cudaError_t launch_few_rows(const Product& p, cudaStream_t stream) {
 }
 
 // dz = bf16(dy * act'(pre)), and each column's sum of it before the rounding.
-// One pass over dy and pre, bound by HBM bandwidth: a warp takes 256 columns of
-// a row, 8 a lane, and a block 8 warps' rows in turn over kSlopeRows of them.
-// The block's column sums go to the workspace and linear_dbias_kernel adds them
-// in the blocks' order.
-constexpr int kSlopeRows = 128, kSlopeCols = 256;
+// One pass over dy and pre, bound by HBM bandwidth.  A warp takes 256 columns of
+// every row of its block's, 8 a lane, and the block's 4 warps lie side by side, so
+// that a row is read 2 KB at a time; its column sums, a thread's own, go to the
+// workspace, and linear_dbias_kernel adds the blocks' in their order.
+constexpr int kSlopeWarps = 4, kSlopeCols = 256 * kSlopeWarps;
 
 struct SlopeArgs {
   const uint16_t *dy, *pre;
   int64_t ldy, ldp, rows, cols;
   int32_t act;
-  int32_t vec;   // 16-byte accesses
-  uint16_t* dz;  // NULL: sums only
+  int32_t vec;     // 16-byte accesses
+  int32_t height;  // rows of a block
+  uint16_t* dz;    // NULL: sums only
   int64_t ldz;
-  float* sums;   // [row blocks][cols], NULL: dz only
+  float* sums;     // [row blocks][cols], NULL: dz only
 };
 
-__global__ void __launch_bounds__(256) linear_slope_kernel(const __grid_constant__ SlopeArgs a) {
-  __shared__ float part[8][kSlopeCols];
+__global__ void __launch_bounds__(32 * kSlopeWarps)
+    linear_slope_kernel(const __grid_constant__ SlopeArgs a) {
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  const int64_t j0 = static_cast<int64_t>(blockIdx.x) * kSlopeCols;
-  const int64_t first = static_cast<int64_t>(blockIdx.y) * kSlopeRows;
-  const int64_t last = first + kSlopeRows < a.rows ? first + kSlopeRows : a.rows;
+  const int64_t j0 = static_cast<int64_t>(blockIdx.x) * kSlopeCols + 256 * warp;
+  if (j0 >= a.cols) return;
+  const int64_t first = static_cast<int64_t>(blockIdx.y) * a.height;
+  const int n = static_cast<int>(a.rows - first < a.height ? a.rows - first : a.height);
   float sum[8] = {};
-  if (a.vec && j0 + kSlopeCols <= a.cols) {
+  if (a.vec && j0 + 256 <= a.cols) {
     const int64_t j = j0 + 8 * lane;
+    const uint16_t* dy = a.dy + first * a.ldy + j;
+    const uint16_t* pre = a.act != ZERO_ACT_NONE ? a.pre + first * a.ldp + j : dy;
+    uint16_t* dz = a.dz != nullptr ? a.dz + first * a.ldz + j : nullptr;
 #pragma unroll 4
-    for (int64_t i = first + warp; i < last; i += 8) {
+    for (int i = 0; i < n; ++i) {
       float x[8];
-      bf16x8(__ldcs(reinterpret_cast<const uint4*>(a.dy + i * a.ldy + j)), x);
-      if (a.act != ZERO_ACT_NONE)
-        times_slope8(x, __ldcs(reinterpret_cast<const uint4*>(a.pre + i * a.ldp + j)), a.act);
-      if (a.dz != nullptr) *reinterpret_cast<uint4*>(a.dz + i * a.ldz + j) = to_bf16x8(x);
+      bf16x8(__ldcs(reinterpret_cast<const uint4*>(dy)), x);
+      dy += a.ldy;
+      if (a.act != ZERO_ACT_NONE) {
+        times_slope8(x, __ldcs(reinterpret_cast<const uint4*>(pre)), a.act);
+        pre += a.ldp;
+      }
+      if (dz != nullptr) {
+        *reinterpret_cast<uint4*>(dz) = to_bf16x8(x);
+        dz += a.ldz;
+      }
 #pragma unroll
       for (int c = 0; c < 8; ++c) sum[c] += x[c];
     }
-#pragma unroll
-    for (int c = 0; c < 8; ++c) part[warp][8 * lane + c] = sum[c];
+    if (a.sums != nullptr) {
+      float4* s = reinterpret_cast<float4*>(a.sums + blockIdx.y * round_up4(a.cols) + j);
+      s[0] = make_float4(sum[0], sum[1], sum[2], sum[3]);
+      s[1] = make_float4(sum[4], sum[5], sum[6], sum[7]);
+    }
   } else {
-    for (int64_t i = first + warp; i < last; i += 8) {
+#pragma unroll 2
+    for (int i = 0; i < n; ++i) {
+      float x[8], z[8];
 #pragma unroll
       for (int c = 0; c < 8; ++c) {
         const int64_t j = j0 + 32 * c + lane;
-        if (j >= a.cols) continue;
-        float x = bf16_at(a.dy + i * a.ldy + j);
-        if (a.act != ZERO_ACT_NONE) x *= act_slope(bf16_at(a.pre + i * a.ldp + j), a.act);
-        if (a.dz != nullptr) a.dz[i * a.ldz + j] = to_bf16(x);
-        sum[c] += x;
+        x[c] = j < a.cols ? bf16_at(a.dy + (first + i) * a.ldy + j) : 0.0f;
+        if (a.act != ZERO_ACT_NONE) z[c] = j < a.cols ? bf16_at(a.pre + (first + i) * a.ldp + j) : 0.0f;
+      }
+#pragma unroll
+      for (int c = 0; c < 8; ++c) {
+        const int64_t j = j0 + 32 * c + lane;
+        if (a.act != ZERO_ACT_NONE) x[c] *= act_slope(z[c], a.act);
+        if (a.dz != nullptr && j < a.cols) a.dz[(first + i) * a.ldz + j] = to_bf16(x[c]);
+        sum[c] += x[c];
       }
     }
+    if (a.sums != nullptr) {
 #pragma unroll
-    for (int c = 0; c < 8; ++c) part[warp][32 * c + lane] = sum[c];
+      for (int c = 0; c < 8; ++c) {
+        const int64_t j = j0 + 32 * c + lane;
+        if (j < a.cols) a.sums[blockIdx.y * round_up4(a.cols) + j] = sum[c];
+      }
+    }
   }
-  if (a.sums == nullptr) return;
-  __syncthreads();
-  const int64_t j = j0 + threadIdx.x;
-  if (j >= a.cols) return;
-  float s = 0.0f;
-#pragma unroll
-  for (int k = 0; k < 8; ++k) s += part[k][threadIdx.x];
-  a.sums[blockIdx.y * a.cols + j] = s;
 }
 
 struct DbiasArgs {
@@ -1109,7 +1193,7 @@ __global__ void __launch_bounds__(256) linear_dbias_kernel(const __grid_constant
   const int r = threadIdx.x / 32;
   float sum = 0.0f;
   if (j < a.cols)
-    for (int k = r; k < a.blocks; k += 8) sum += __ldcg(a.sums + k * a.cols + j);
+    for (int k = r; k < a.blocks; k += 8) sum += __ldcg(a.sums + k * round_up4(a.cols) + j);
   part[r][threadIdx.x % 32] = sum;
   __syncthreads();
   if (r != 0 || j >= a.cols) return;
@@ -1124,7 +1208,16 @@ __global__ void __launch_bounds__(256) linear_dbias_kernel(const __grid_constant
   }
 }
 
-int64_t slope_blocks(int64_t rows) { return (rows + kSlopeRows - 1) / kSlopeRows; }
+// Rows of a block: 8 blocks an SM, 8 to 64 rows.
+int64_t slope_height(int64_t rows, int64_t cols) {
+  const int64_t across = (cols + kSlopeCols - 1) / kSlopeCols;
+  const int64_t h = rows * across / (8 * kSms);
+  return h < 8 ? 8 : h > 64 ? 64 : h;
+}
+int64_t slope_blocks(int64_t rows, int64_t cols) {
+  const int64_t h = slope_height(rows, cols);
+  return (rows + h - 1) / h;
+}
 
 }  // namespace
 
@@ -1143,12 +1236,12 @@ int64_t linear_workspace(const zero_linear_t& s, int32_t flags) {
   const int64_t w = in_place ? 0 : copy_bytes(Stored(nullptr, s.out, s.in, 0));
   if ((flags & ZERO_LINEAR_BACKWARD) == 0)
     return s.rows <= kFewRows ? 0 : product_bytes(x + w, s.rows, s.out, s.in, false, false);
-  // dz is laid out once and taken by both products, one after the other
+  // dz, W and x are there for both products, the parts for one after the other
   const bool dz = !in_place || (flags & ZERO_LINEAR_PLAIN) == 0;
-  const int64_t dx = product_bytes(w, s.rows, s.in, s.out, false, true);
-  const int64_t dw = product_bytes(x, s.out, s.in, s.rows, true, true);
-  return (dz ? copy_bytes(Stored(nullptr, s.rows, s.out, 0)) : 0) +
-         round_up(slope_blocks(s.rows) * s.out * 4, 256) + (dx > dw ? dx : dw);
+  const int64_t dx = product_bytes(0, s.rows, s.in, s.out, false, true);
+  const int64_t dw = product_bytes(0, s.out, s.in, s.rows, true, true);
+  return (dz ? copy_bytes(Stored(nullptr, s.rows, s.out, 0)) : 0) + w + x +
+         round_up(slope_blocks(s.rows, s.out) * round_up4(s.out) * 4, 256) + (dx > dw ? dx : dw);
 }
 
 cudaError_t launch_linear_forward(const LinearForwardLaunch& L) {
@@ -1169,7 +1262,10 @@ cudaError_t launch_linear_forward(const LinearForwardLaunch& L) {
   p.e.out = L.y;
   p.e.ldo = s.ldy;
   if (s.rows <= kFewRows) return launch_few_rows(p, L.stream);
-  return launch_product(p, {static_cast<char*>(L.workspace)}, L.withhold, L.stream);
+  Space space{static_cast<char*>(L.workspace)};
+  Stored* const both[2] = {&p.a, &p.b};
+  const cudaError_t e = make_tileable(both, 2, &space, L.stream);
+  return e == cudaSuccess ? launch_product(p, space, L.withhold, L.stream) : e;
 }
 
 cudaError_t launch_linear_backward(const LinearBackwardLaunch& L) {
@@ -1191,23 +1287,25 @@ cudaError_t launch_linear_backward(const LinearBackwardLaunch& L) {
       a.ldz = copy_pitch(s.out);
       dz = Stored(a.dz, s.rows, s.out, a.ldz);
     }
-    const int64_t blocks = slope_blocks(s.rows);
-    if (L.dbias != nullptr) a.sums = static_cast<float*>(space.take(blocks * s.out * 4));
+    const int64_t blocks = slope_blocks(s.rows, s.out);
+    a.height = static_cast<int32_t>(slope_height(s.rows, s.out));
+    if (L.dbias != nullptr)
+      a.sums = static_cast<float*>(space.take(blocks * round_up4(s.out) * 4));
     a.vec = tileable(Stored(L.dy, s.rows, s.out, s.ldy)) &&
             (L.act == ZERO_ACT_NONE || tileable(Stored(L.pre, s.rows, s.out, s.ldp)));
     const int64_t across = (s.out + kSlopeCols - 1) / kSlopeCols;
     // the grid's y side ends at 65535
     for (int64_t k = 0; k < blocks; k += 65535) {
       SlopeArgs part = a;
-      const int64_t skip = k * kSlopeRows;
+      const int64_t skip = k * a.height;
       part.dy += skip * s.ldy;
       part.pre += L.act != ZERO_ACT_NONE ? skip * s.ldp : 0;
       part.dz += a.dz != nullptr ? skip * a.ldz : 0;
-      part.sums += a.sums != nullptr ? k * s.out : 0;
+      part.sums += a.sums != nullptr ? k * round_up4(s.out) : 0;
       part.rows -= skip;
       const int64_t high = blocks - k < 65535 ? blocks - k : 65535;
-      linear_slope_kernel<<<dim3(static_cast<unsigned>(across), static_cast<unsigned>(high)), 256, 0,
-                            L.stream>>>(part);
+      linear_slope_kernel<<<dim3(static_cast<unsigned>(across), static_cast<unsigned>(high)),
+                            32 * kSlopeWarps, 0, L.stream>>>(part);
     }
     if (L.dbias != nullptr) {
       const DbiasArgs d{a.sums, s.out, static_cast<int32_t>(blocks), L.dbias, L.grad_f32, L.accumulate};
@@ -1221,14 +1319,17 @@ cudaError_t launch_linear_backward(const LinearBackwardLaunch& L) {
     return cudaMemset2DAsync(L.dw, s.lddw * (L.grad_f32 ? 4 : 2), 0, s.in * (L.grad_f32 ? 4 : 2),
                              s.out, L.stream);
   }
+  Stored w(L.dx != nullptr ? L.w : nullptr, s.out, s.in, s.ldw);
+  Stored x(L.dw != nullptr ? L.x : nullptr, s.rows, s.in, s.ldx);
   if (L.dx != nullptr || L.dw != nullptr) {
-    const cudaError_t e = make_tileable(&dz, &space, L.stream);
+    Stored* const all[3] = {&dz, &w, &x};
+    const cudaError_t e = make_tileable(all, 3, &space, L.stream);
     if (e != cudaSuccess) return e;
   }
   if (L.dx != nullptr) {
     Product p{};
     p.a = dz;
-    p.b = {L.w, s.out, s.in, s.ldw};
+    p.b = w;
     p.b_mn = true;
     p.rows = s.rows;
     p.cols = s.in;
@@ -1245,7 +1346,7 @@ cudaError_t launch_linear_backward(const LinearBackwardLaunch& L) {
     Product p{};
     p.a = dz;
     p.a_mn = true;
-    p.b = {L.x, s.rows, s.in, s.ldx};
+    p.b = x;
     p.b_mn = true;
     p.rows = s.out;
     p.cols = s.in;
