@@ -72,6 +72,7 @@ struct ProductArgs {
   int32_t splits;        // parts of the reduction of each tile after those
   int32_t steps;         // stages of the whole reduction
   int32_t withhold;      // test hook: no loads are issued, so every wait runs out
+  int32_t late;          // its inputs were there before its predecessor began
 };
 
 struct Tile {
@@ -373,12 +374,13 @@ __global__ void __launch_bounds__(kProductThreads, 1)
     prefetch_map(&a.b);
   }
   if (warp == 1) tmem_alloc<CG>(tmem_at, Shape::kColumns);
+  if (!a.late) wait_for_predecessor();
+  launch_dependents();
   tc_fence_before();
   __syncthreads();
   if constexpr (CG == 2) cluster_sync();
   tc_fence_after();
   const uint32_t tmem = *tmem_at;
-  if (a.splits > 1) launch_dependents();
 
   if (warp == 0) {
     if (lane == 0) {
@@ -569,6 +571,8 @@ __global__ void __launch_bounds__(kProductThreads, 1)
   __syncthreads();
   if constexpr (CG == 2) cluster_sync();
   if (warp == 1) tmem_free<CG>(tmem, Shape::kColumns);
+  // what follows this kernel follows its predecessor too
+  if (a.late) wait_for_predecessor();
 }
 
 // The parts of the tiles whose reduction was split, added in their order, and the
@@ -583,6 +587,7 @@ __global__ void __launch_bounds__(256) linear_join_kernel(const __grid_constant_
   const int r = in / per_row, c = in % per_row * 8;
   const int64_t i = tile.row + r, j = tile.col + c;
   wait_for_predecessor();
+  launch_dependents();
   if (r >= BM || i >= a.rows || j >= a.cols) return;
   const Epilogue& e = a.e;
   const bool vec = e.vec && j + 8 <= a.cols;
@@ -646,14 +651,24 @@ struct CopyArgs {
   uint16_t* dst;
   int64_t rows, cols, lds, ldd;
 };
-struct Copies {
-  CopyArgs of[3];
+// dbias from the column sums of `blocks` blocks of rows.
+struct DbiasArgs {
+  const float* sums;  // [blocks][cols rounded up to 4]
+  int64_t cols;
+  int32_t blocks;
+  void* dbias;        // NULL: not wanted
+  int32_t out_f32, accumulate;
 };
 
-// Matrices laid out anew with rows on 128-byte boundaries: 8 elements a thread,
+struct PrepareArgs {
+  CopyArgs copy[3];
+  int32_t copies;
+  DbiasArgs dbias;
+};
+
+// A matrix laid out anew with rows on 128-byte boundaries: 8 elements a thread,
 // read one by one and 64 bytes of a row by each warp at a time.
-__global__ void __launch_bounds__(256) linear_copy_kernel(const __grid_constant__ Copies all) {
-  const CopyArgs& a = all.of[blockIdx.y];
+__device__ __forceinline__ void copy_rows(const CopyArgs& a) {
   const int64_t per = (a.cols + 255) / 256;  // warps a row
   const int lane = threadIdx.x % 32;
   for (int64_t q = static_cast<int64_t>(blockIdx.x) * 8 + threadIdx.x / 32; q < a.rows * per;
@@ -669,6 +684,42 @@ __global__ void __launch_bounds__(256) linear_copy_kernel(const __grid_constant_
   }
 }
 
+// 32 columns of dbias at a time, 8 runs of row blocks each.
+__device__ __forceinline__ void add_dbias(const DbiasArgs& a) {
+  __shared__ float part[8][32];
+  const int r = threadIdx.x / 32, lane = threadIdx.x % 32;
+  for (int64_t j0 = static_cast<int64_t>(blockIdx.x) * 32; j0 < a.cols;
+       j0 += static_cast<int64_t>(gridDim.x) * 32) {
+    const int64_t j = j0 + lane;
+    float sum = 0.0f;
+    if (j < a.cols) {
+#pragma unroll 8
+      for (int k = r; k < a.blocks; k += 8) sum += __ldcg(a.sums + k * round_up4(a.cols) + j);
+    }
+    __syncthreads();
+    part[r][lane] = sum;
+    __syncthreads();
+    if (r != 0 || j >= a.cols) continue;
+#pragma unroll
+    for (int k = 1; k < 8; ++k) sum += part[k][lane];
+    if (a.out_f32) {
+      float* o = static_cast<float*>(a.dbias) + j;
+      *o = a.accumulate ? *o + sum : sum;
+    } else {
+      uint16_t* o = static_cast<uint16_t*>(a.dbias) + j;
+      *o = to_bf16(a.accumulate ? bf16_at(o) + sum : sum);
+    }
+  }
+}
+
+// What is left to do before (or beside) the products: a row of blocks a job.
+__global__ void __launch_bounds__(256) linear_prepare_kernel(const __grid_constant__ PrepareArgs a) {
+  wait_for_predecessor();
+  launch_dependents();
+  if (blockIdx.y < a.copies) copy_rows(a.copy[blockIdx.y]);
+  else add_dbias(a.dbias);
+}
+
 // Takes pieces of the workspace in order.
 struct Space {
   char* at;
@@ -679,27 +730,67 @@ struct Space {
   }
 };
 
-// Lays the matrices that TMA cannot read where they are out anew, in one launch.
-cudaError_t make_tileable(Stored* const* matrices, int count, Space* space, cudaStream_t stream) {
-  Copies all{};
-  int n = 0;
+// The kernels of one call.  All but the first are launched as programmatic
+// dependents: they begin while their predecessor ends, and wait for it
+// (wait_for_predecessor) before they read what it wrote.
+struct Chain {
+  cudaStream_t stream;
+  bool begun = false;
+
+  template <typename... Params, typename... Args>
+  cudaError_t launch(void (*kernel)(Params...), dim3 grid, int threads, int smem, int cluster,
+                     Args&&... args) {
+    cudaLaunchConfig_t config = {};
+    config.gridDim = grid;
+    config.blockDim = dim3(threads);
+    config.dynamicSmemBytes = smem;
+    config.stream = stream;
+    cudaLaunchAttribute attr[2];
+    config.attrs = attr;
+    if (cluster > 1) {
+      cudaLaunchAttribute& a = attr[config.numAttrs++];
+      a.id = cudaLaunchAttributeClusterDimension;
+      a.val.clusterDim.x = cluster;
+      a.val.clusterDim.y = 1;
+      a.val.clusterDim.z = 1;
+    }
+    if (begun) {
+      cudaLaunchAttribute& a = attr[config.numAttrs++];
+      a.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+      a.val.programmaticStreamSerializationAllowed = 1;
+    }
+    begun = true;
+    return cudaLaunchKernelEx(&config, kernel, static_cast<Params>(args)...);
+  }
+};
+
+// Lays the matrices that TMA cannot read where they are out anew, and adds up
+// dbias where it is wanted, in one launch.
+cudaError_t prepare(Stored* const* matrices, int count, const DbiasArgs& dbias, Space* space,
+                    Chain* chain) {
+  PrepareArgs all{};
   int64_t most = 0;
   for (int k = 0; k < count; ++k) {
     Stored& m = *matrices[k];
     if (m.p == nullptr || tileable(m)) continue;
     const int64_t pitch = copy_pitch(m.cols);
-    CopyArgs& a = all.of[n++];
+    CopyArgs& a = all.copy[all.copies++];
     a = {m.p, static_cast<uint16_t*>(space->take(copy_bytes(m))), m.rows, m.cols, m.ld, pitch};
     m.p = a.dst;
     m.ld = pitch;
-    const int64_t warps = m.rows * ((m.cols + 255) / 256);
-    most = warps > most ? warps : most;
+    const int64_t blocks = (m.rows * ((m.cols + 255) / 256) + 7) / 8;
+    most = blocks > most ? blocks : most;
   }
-  if (n == 0) return cudaSuccess;
-  const int64_t blocks = (most + 7) / 8;
-  const dim3 grid(static_cast<unsigned>(blocks < 16 * 152 ? blocks : 16 * 152), n);
-  linear_copy_kernel<<<grid, 256, 0, stream>>>(all);
-  return cudaGetLastError();
+  int jobs = all.copies;
+  if (dbias.dbias != nullptr) {
+    all.dbias = dbias;
+    const int64_t blocks = (dbias.cols + 31) / 32;
+    most = blocks > most ? blocks : most;
+    ++jobs;
+  }
+  if (jobs == 0) return cudaSuccess;
+  const dim3 grid(static_cast<unsigned>(most < 2432 ? most : 2432), jobs);
+  return chain->launch(linear_prepare_kernel, grid, 256, 0, 1, all);
 }
 
 using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
@@ -796,39 +887,52 @@ struct Plan {
 // at 6.5 TB/s at best and 1.3 after they are asked for, a ring ahead, which is
 // what counts for a few rows; 3 for a kernel's beginning and end, 0.9 for each 64
 // columns of its last epilogue, 3 for the join's launch.
-Plan plan_product(int64_t rows, int64_t cols, int64_t depth, bool a_mn, bool b_mn) {
-  const int64_t steps = (depth + kStep - 1) / kStep;
+//
+// follows: the tiles of a product that is launched just before and does not have
+// to end first, so that this one's fill its last round; split: whether tiles past
+// the last whole round may be.
+Plan plan_product(int64_t rows, int64_t cols, int64_t depth, bool a_mn, bool b_mn,
+                  const Plan* follows = nullptr, bool split = true) {
   Plan best{2, 256, 0, 1, 0};
   if (rows < 1 || cols < 1) return best;
+  const int steps = static_cast<int>((depth + kStep - 1) / kStep);
   double least = 1e300;
   for (int cg = 2; cg >= 1; --cg) {
     const int most = cg == 2 ? 256 : 128;
     // MN-major operands come in columns of 64 per CTA
     const int unit = b_mn ? 64 * cg : 32;
-    const int64_t units = kSms / cg, tm = (rows + 128 * cg - 1) / (128 * cg);
+    const int units = kSms / cg, a_rows = a_rows_of(rows, cg, a_mn);
+    const int64_t tm = (rows + 128 * cg - 1) / (128 * cg);
     for (int bn = most; bn >= unit; bn -= unit) {
-      const int64_t tn = (cols + bn - 1) / bn;
-      if (tm * tn > INT32_MAX / 64) continue;
-      const int64_t tiles = tm * tn, rest = tiles % units, whole = tiles - rest;
+      const int64_t tn = (cols + bn - 1) / bn, tiles = tm * tn;
+      if (tiles > INT32_MAX / 64) continue;
+      const int before = follows != nullptr && follows->cg == cg ? follows->whole % units : 0;
+      int rest = static_cast<int>((tiles + before) % units);
+      if (rest > tiles) rest = static_cast<int>(tiles);
+      const int whole = static_cast<int>(tiles) - rest;
       const double share = static_cast<double>(bn) / most;
       const double mma = cg == 2 ? 0.40 + 0.25 * share * share : 0.42 + 0.055 * share * share;
-      const auto stage = [&](int64_t active) {
+      const double wait = 1.3 / ring_stages(a_rows, bn / cg);
+      const double floor = mma > wait ? mma : wait;
+      const auto stage = [&](int active) {
         const double distinct = static_cast<double>(active < tn ? active : tn) * bn +
                                 static_cast<double>(active < tm ? active : tm) * 128 * cg;
         const double read = distinct * (2 * kStep) / 6.5e6;
-        const double wait = 1.3 / ring_stages(a_rows_of(rows, cg, a_mn), bn / cg);
-        return mma > read && mma > wait ? mma : read > wait ? read : wait;
+        return floor > read ? floor : read;
       };
-      double cost = whole / units * steps * (whole > 0 ? stage(units) : 0.0) + 3.0 + 0.9 * bn / 64;
-      const double before = cost;
+      const double before_us =
+          (whole > 0 ? whole / units * steps * stage(units) : 0.0) + 3.0 + 0.9 * bn / 64;
       for (int parts = 1; parts <= 16; ++parts) {
-        if (parts > 1 && (rest == 0 || parts * 2 > steps)) break;
-        const Plan p{cg, bn, static_cast<int>(parts > 1 ? whole : tiles), parts,
-                     static_cast<int>(parts > 1 ? rest : 0)};
+        // (past two rounds of parts nothing was ever gained)
+        if (parts > 1 && (rest == 0 || parts * 2 > steps || rest * parts > 2 * units ||
+                          (!split && whole > 0)))
+          break;
+        const Plan p{cg, bn, parts > 1 ? whole : static_cast<int>(tiles), parts, parts > 1 ? rest : 0};
         if (p.part_bytes() > (int64_t{64} << 20)) break;
-        const int64_t items = rest * parts, rounds = (items + units - 1) / units;
-        const int64_t deep = (steps + parts - 1) / parts;
-        cost = before + rounds * deep * (items > 0 ? stage(items < units ? items : units) : 0.0);
+        const int items = rest * parts, rounds = (items + units - 1) / units;
+        const int deep = (steps + parts - 1) / parts;
+        double cost = before_us;
+        if (items > 0) cost += rounds * deep * stage(items < units ? items : units);
         if (parts > 1) cost += 3.0 + p.part_bytes() * 2 / 5.0e6;
         if (cost < least) {
           least = cost;
@@ -840,9 +944,18 @@ Plan plan_product(int64_t rows, int64_t cols, int64_t depth, bool a_mn, bool b_m
   return best;
 }
 
+// A product under way: what its join needs, where its reduction is split.
+struct Pending {
+  ProductArgs a;
+  Plan plan;
+  int64_t rows;
+  float* parts;
+};
+
 template <int CG, bool A_MN, bool B_MN, Kind KIND>
-cudaError_t launch_shape(const Product& p, const Plan& plan, ProductArgs& a, float* parts,
-                         cudaStream_t stream) {
+cudaError_t launch_shape(const Product& p, Pending* w, Chain* chain) {
+  ProductArgs& a = w->a;
+  const Plan& plan = w->plan;
   const int bn = plan.bn;
   auto kernel = linear_product_kernel<CG, A_MN, B_MN, KIND>;
   static std::mutex mu;
@@ -871,40 +984,27 @@ cudaError_t launch_shape(const Product& p, const Plan& plan, ProductArgs& a, flo
   a.whole = plan.whole;
   a.splits = plan.splits;
   if (plan.splits > 1) {
-    e = make_out_map(&a.parts, parts, CG * kBlockRows, bn, bn, plan.tail * plan.splits,
+    e = make_out_map(&a.parts, w->parts, CG * kBlockRows, bn, bn, plan.tail * plan.splits,
                      CG * kBlockRows * bn, true);
     if (e != cudaSuccess) return e;
   }
   const int64_t units = sms / CG, tiles = plan.whole + int64_t{plan.tail} * plan.splits;
-  cudaLaunchConfig_t config = {};
-  config.gridDim = dim3(static_cast<unsigned>(CG * (tiles < units ? tiles : units)));
-  config.blockDim = dim3(kProductThreads);
-  config.dynamicSmemBytes = kSmem;
-  config.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = CG;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  config.attrs = attr;
-  config.numAttrs = 1;
-  e = cudaLaunchKernelEx(&config, kernel, a);
-  if (e != cudaSuccess || plan.splits == 1) return e;
-  const int64_t high = p.rows < CG * kBlockRows ? p.rows : CG * kBlockRows;
-  config.gridDim = dim3(static_cast<unsigned>((high * (bn / 8) + 255) / 256), plan.tail);
-  config.blockDim = dim3(256);
-  config.dynamicSmemBytes = 0;
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  return cudaLaunchKernelEx(&config, linear_join_kernel<CG * kBlockRows>, a,
-                            static_cast<const float*>(parts));
+  const unsigned grid = static_cast<unsigned>(CG * (tiles < units ? tiles : units));
+  return chain->launch(kernel, dim3(grid), kProductThreads, kSmem, CG, a);
+}
+
+cudaError_t launch_join(const Pending& w, Chain* chain) {
+  if (w.plan.splits == 1) return cudaSuccess;
+  const int64_t high = w.rows < w.plan.cg * kBlockRows ? w.rows : w.plan.cg * kBlockRows;
+  const dim3 grid(static_cast<unsigned>((high * (w.plan.bn / 8) + 255) / 256), w.plan.tail);
+  return w.plan.cg == 2 ? chain->launch(linear_join_kernel<256>, grid, 256, 0, 1, w.a, w.parts)
+                        : chain->launch(linear_join_kernel<128>, grid, 256, 0, 1, w.a, w.parts);
 }
 
 template <bool A_MN, bool B_MN, Kind KIND>
-cudaError_t launch_kind(const Product& p, const Plan& plan, ProductArgs& a, float* parts,
-                        cudaStream_t stream) {
-  return plan.cg == 2 ? launch_shape<2, A_MN, B_MN, KIND>(p, plan, a, parts, stream)
-                      : launch_shape<1, A_MN, B_MN, KIND>(p, plan, a, parts, stream);
+cudaError_t launch_kind(const Product& p, Pending* w, Chain* chain) {
+  return w->plan.cg == 2 ? launch_shape<2, A_MN, B_MN, KIND>(p, w, chain)
+                         : launch_shape<1, A_MN, B_MN, KIND>(p, w, chain);
 }
 
 void set_vec(Epilogue* e, int64_t rows) {
@@ -916,39 +1016,37 @@ void set_vec(Epilogue* e, int64_t rows) {
            ok(e->slope_of, e->lds, 2) && ok(e->out, e->ldo, e->out_f32 ? 4 : 2);
 }
 
-cudaError_t launch_product(Product p, Space space, int withhold, cudaStream_t stream) {
-  cudaError_t err = cudaSuccess;
+// late: see ProductArgs.  The join is left to the caller.
+cudaError_t launch_product(Product p, const Plan& plan, bool late, Space* space, int withhold,
+                           Chain* chain, Pending* w) {
   set_vec(&p.e, p.rows);
-  const Plan plan = plan_product(p.rows, p.cols, p.depth, p.a_mn, p.b_mn);
-  ProductArgs a{};
+  *w = Pending{};
+  w->plan = plan;
+  w->rows = p.rows;
+  w->parts = static_cast<float*>(space->take(plan.part_bytes()));
+  ProductArgs& a = w->a;
   a.e = p.e;
   a.rows = p.rows;
   a.cols = p.cols;
   a.steps = static_cast<int32_t>((p.depth + kStep - 1) / kStep);
   a.withhold = withhold;
-  float* parts = static_cast<float*>(space.take(plan.part_bytes()));
+  a.late = late;
   const bool f32 = a.e.out_f32 != 0;
   if (a.e.vec) {
     // a matrix of one row has any pitch
     const int64_t one = round_up(p.cols, 8);
     const int64_t stride = p.rows > 1 ? p.rows * a.e.ldo : one;
-    err = make_out_map(&a.out, a.e.out, p.rows, p.cols, p.rows > 1 ? a.e.ldo : one, 1, stride, f32);
-    if (err == cudaSuccess && a.e.pre != nullptr)
-      err = make_out_map(&a.pre, a.e.pre, p.rows, p.cols, p.rows > 1 ? a.e.ldp : one, 1, stride, false);
-    if (err != cudaSuccess) return err;
+    cudaError_t e =
+        make_out_map(&a.out, a.e.out, p.rows, p.cols, p.rows > 1 ? a.e.ldo : one, 1, stride, f32);
+    if (e == cudaSuccess && a.e.pre != nullptr)
+      e = make_out_map(&a.pre, a.e.pre, p.rows, p.cols, p.rows > 1 ? a.e.ldp : one, 1, stride, false);
+    if (e != cudaSuccess) return e;
   }
   if (p.a_mn)
-    return f32 ? launch_kind<true, true, kFloat>(p, plan, a, parts, stream)
-               : launch_kind<true, true, kGradient>(p, plan, a, parts, stream);
-  if (p.b_mn) return launch_kind<false, true, kGradient>(p, plan, a, parts, stream);
-  return launch_kind<false, false, kForward>(p, plan, a, parts, stream);
-}
-
-// Workspace of a product; `moved`: of its operands, where they have to be laid
-// out anew.
-int64_t product_bytes(int64_t moved, int64_t rows, int64_t cols, int64_t depth, bool a_mn,
-                      bool b_mn) {
-  return moved + round_up(plan_product(rows, cols, depth, a_mn, b_mn).part_bytes(), 256);
+    return f32 ? launch_kind<true, true, kFloat>(p, w, chain)
+               : launch_kind<true, true, kGradient>(p, w, chain);
+  if (p.b_mn) return launch_kind<false, true, kGradient>(p, w, chain);
+  return launch_kind<false, false, kForward>(p, w, chain);
 }
 
 // --------------------------------------------------------------- a few rows
@@ -1102,13 +1200,12 @@ cudaError_t launch_few_rows(const Product& p, cudaStream_t stream) {
 // One pass over dy and pre, bound by HBM bandwidth.  A warp takes 256 columns of
 // every row of its block's, 8 a lane, and the block's 4 warps lie side by side, so
 // that a row is read 2 KB at a time; its column sums, a thread's own, go to the
-// workspace, and linear_dbias_kernel adds the blocks' in their order.
+// workspace, and add_dbias adds the blocks' in their order.
 constexpr int kSlopeWarps = 4, kSlopeCols = 256 * kSlopeWarps;
 
 struct SlopeArgs {
   const uint16_t *dy, *pre;
   int64_t ldy, ldp, rows, cols;
-  int32_t act;
   int32_t vec;     // 16-byte accesses
   int32_t height;  // rows of a block
   uint16_t* dz;    // NULL: sums only
@@ -1116,9 +1213,12 @@ struct SlopeArgs {
   float* sums;     // [row blocks][cols], NULL: dz only
 };
 
-__global__ void __launch_bounds__(32 * kSlopeWarps)
+template <int ACT>
+__global__ void __launch_bounds__(32 * kSlopeWarps, 6)
     linear_slope_kernel(const __grid_constant__ SlopeArgs a) {
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  wait_for_predecessor();
+  launch_dependents();
   const int64_t j0 = static_cast<int64_t>(blockIdx.x) * kSlopeCols + 256 * warp;
   if (j0 >= a.cols) return;
   const int64_t first = static_cast<int64_t>(blockIdx.y) * a.height;
@@ -1127,23 +1227,31 @@ __global__ void __launch_bounds__(32 * kSlopeWarps)
   if (a.vec && j0 + 256 <= a.cols) {
     const int64_t j = j0 + 8 * lane;
     const uint16_t* dy = a.dy + first * a.ldy + j;
-    const uint16_t* pre = a.act != ZERO_ACT_NONE ? a.pre + first * a.ldp + j : dy;
+    const uint16_t* pre = ACT != ZERO_ACT_NONE ? a.pre + first * a.ldp + j : dy;
     uint16_t* dz = a.dz != nullptr ? a.dz + first * a.ldz + j : nullptr;
-#pragma unroll 4
-    for (int i = 0; i < n; ++i) {
-      float x[8];
-      bf16x8(__ldcs(reinterpret_cast<const uint4*>(dy)), x);
-      dy += a.ldy;
-      if (a.act != ZERO_ACT_NONE) {
-        times_slope8(x, __ldcs(reinterpret_cast<const uint4*>(pre)), a.act);
-        pre += a.ldp;
-      }
-      if (dz != nullptr) {
-        *reinterpret_cast<uint4*>(dz) = to_bf16x8(x);
-        dz += a.ldz;
+    // 4 rows' loads at a time: one row's are too few to cover HBM's latency
+#pragma unroll 1
+    for (int i = 0; i < n; i += 4) {
+      uint4 u[4], w[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        if (i + k >= n) break;
+        u[k] = __ldcs(reinterpret_cast<const uint4*>(dy + k * a.ldy));
+        if (ACT != ZERO_ACT_NONE) w[k] = __ldcs(reinterpret_cast<const uint4*>(pre + k * a.ldp));
       }
 #pragma unroll
-      for (int c = 0; c < 8; ++c) sum[c] += x[c];
+      for (int k = 0; k < 4; ++k) {
+        if (i + k >= n) break;
+        float x[8];
+        bf16x8(u[k], x);
+        if (ACT != ZERO_ACT_NONE) times_slope8(x, w[k], ACT);
+        if (dz != nullptr) *reinterpret_cast<uint4*>(dz + k * a.ldz) = to_bf16x8(x);
+#pragma unroll
+        for (int c = 0; c < 8; ++c) sum[c] += x[c];
+      }
+      dy += 4 * a.ldy;
+      pre += 4 * a.ldp;
+      if (dz != nullptr) dz += 4 * a.ldz;
     }
     if (a.sums != nullptr) {
       float4* s = reinterpret_cast<float4*>(a.sums + blockIdx.y * round_up4(a.cols) + j);
@@ -1151,22 +1259,29 @@ __global__ void __launch_bounds__(32 * kSlopeWarps)
       s[1] = make_float4(sum[4], sum[5], sum[6], sum[7]);
     }
   } else {
-#pragma unroll 2
-    for (int i = 0; i < n; ++i) {
-      float x[8], z[8];
+#pragma unroll 1
+    for (int i = 0; i < n; i += 2) {  // 2 rows' loads at a time
+      float x[2][8], z[2][8];
 #pragma unroll
-      for (int c = 0; c < 8; ++c) {
-        const int64_t j = j0 + 32 * c + lane;
-        x[c] = j < a.cols ? bf16_at(a.dy + (first + i) * a.ldy + j) : 0.0f;
-        if (a.act != ZERO_ACT_NONE) z[c] = j < a.cols ? bf16_at(a.pre + (first + i) * a.ldp + j) : 0.0f;
-      }
+      for (int k = 0; k < 2; ++k)
 #pragma unroll
-      for (int c = 0; c < 8; ++c) {
-        const int64_t j = j0 + 32 * c + lane;
-        if (a.act != ZERO_ACT_NONE) x[c] *= act_slope(z[c], a.act);
-        if (a.dz != nullptr && j < a.cols) a.dz[(first + i) * a.ldz + j] = to_bf16(x[c]);
-        sum[c] += x[c];
-      }
+        for (int c = 0; c < 8; ++c) {
+          const int64_t j = j0 + 32 * c + lane;
+          const bool in = j < a.cols && i + k < n;
+          x[k][c] = in ? bf16_at(a.dy + (first + i + k) * a.ldy + j) : 0.0f;
+          if (ACT != ZERO_ACT_NONE) z[k][c] = in ? bf16_at(a.pre + (first + i + k) * a.ldp + j) : 0.0f;
+        }
+#pragma unroll
+      for (int k = 0; k < 2; ++k)
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+          const int64_t j = j0 + 32 * c + lane;
+          if (ACT != ZERO_ACT_NONE && c % 2 == 0)
+            times_slope2<ACT>(x[k][c], x[k][c + 1], z[k][c], z[k][c + 1]);
+          if (a.dz != nullptr && j < a.cols && i + k < n)
+            a.dz[(first + i + k) * a.ldz + j] = to_bf16(x[k][c]);
+          sum[c] += x[k][c];
+        }
     }
     if (a.sums != nullptr) {
 #pragma unroll
@@ -1178,41 +1293,11 @@ __global__ void __launch_bounds__(32 * kSlopeWarps)
   }
 }
 
-struct DbiasArgs {
-  const float* sums;
-  int64_t cols;
-  int32_t blocks;
-  void* dbias;
-  int32_t out_f32, accumulate;
-};
-
-// 32 columns a block, 8 runs of row blocks each.
-__global__ void __launch_bounds__(256) linear_dbias_kernel(const __grid_constant__ DbiasArgs a) {
-  __shared__ float part[8][32];
-  const int64_t j = static_cast<int64_t>(blockIdx.x) * 32 + threadIdx.x % 32;
-  const int r = threadIdx.x / 32;
-  float sum = 0.0f;
-  if (j < a.cols)
-    for (int k = r; k < a.blocks; k += 8) sum += __ldcg(a.sums + k * round_up4(a.cols) + j);
-  part[r][threadIdx.x % 32] = sum;
-  __syncthreads();
-  if (r != 0 || j >= a.cols) return;
-#pragma unroll
-  for (int k = 1; k < 8; ++k) sum += part[k][threadIdx.x];
-  if (a.out_f32) {
-    float* o = static_cast<float*>(a.dbias) + j;
-    *o = a.accumulate ? *o + sum : sum;
-  } else {
-    uint16_t* o = static_cast<uint16_t*>(a.dbias) + j;
-    *o = to_bf16(a.accumulate ? bf16_at(o) + sum : sum);
-  }
-}
-
-// Rows of a block: 8 blocks an SM, 8 to 64 rows.
+// Rows of a block: 8 blocks an SM, 4 to 64 rows.
 int64_t slope_height(int64_t rows, int64_t cols) {
   const int64_t across = (cols + kSlopeCols - 1) / kSlopeCols;
   const int64_t h = rows * across / (8 * kSms);
-  return h < 8 ? 8 : h > 64 ? 64 : h;
+  return h < 4 ? 4 : h > 64 ? 64 : h;
 }
 int64_t slope_blocks(int64_t rows, int64_t cols) {
   const int64_t h = slope_height(rows, cols);
@@ -1230,18 +1315,40 @@ int read_and_clear_linear_status(int* status) {
   return 0;
 }
 
+namespace {
+
+Plan plan_forward(const zero_linear_t& s) {
+  return plan_product(s.rows, s.out, s.in, false, false);
+}
+
+// dw's tiles fill dx's last round, so dx is split only where it has less than one.
+struct BackwardPlan {
+  Plan dx, dw;
+};
+BackwardPlan plan_backward(const zero_linear_t& s, bool dx, bool dw) {
+  BackwardPlan p{{2, 256, 0, 1, 0}, {2, 256, 0, 1, 0}};
+  if (dx) p.dx = plan_product(s.rows, s.in, s.out, false, true, nullptr, !dw);
+  if (dw) p.dw = plan_product(s.out, s.in, s.rows, true, true, dx ? &p.dx : nullptr);
+  return p;
+}
+
+}  // namespace
+
 int64_t linear_workspace(const zero_linear_t& s, int32_t flags) {
   const bool in_place = (flags & ZERO_LINEAR_ALIGNED) != 0;
   const int64_t x = in_place ? 0 : copy_bytes(Stored(nullptr, s.rows, s.in, 0));
   const int64_t w = in_place ? 0 : copy_bytes(Stored(nullptr, s.out, s.in, 0));
   if ((flags & ZERO_LINEAR_BACKWARD) == 0)
-    return s.rows <= kFewRows ? 0 : product_bytes(x + w, s.rows, s.out, s.in, false, false);
-  // dz, W and x are there for both products, the parts for one after the other
+    return s.rows <= kFewRows ? 0 : x + w + round_up(plan_forward(s).part_bytes(), 256);
   const bool dz = !in_place || (flags & ZERO_LINEAR_PLAIN) == 0;
-  const int64_t dx = product_bytes(0, s.rows, s.in, s.out, false, true);
-  const int64_t dw = product_bytes(0, s.out, s.in, s.rows, true, true);
+  // the two products' parts, side by side; either may be wanted alone
+  const BackwardPlan both = plan_backward(s, true, true), one = plan_backward(s, true, false),
+                     two = plan_backward(s, false, true);
+  auto most = [](int64_t x, int64_t y) { return x > y ? x : y; };
   return (dz ? copy_bytes(Stored(nullptr, s.rows, s.out, 0)) : 0) + w + x +
-         round_up(slope_blocks(s.rows, s.out) * round_up4(s.out) * 4, 256) + (dx > dw ? dx : dw);
+         round_up(slope_blocks(s.rows, s.out) * round_up4(s.out) * 4, 256) +
+         most(both.dx.part_bytes() + both.dw.part_bytes(),
+              most(one.dx.part_bytes(), two.dw.part_bytes())) + 512;
 }
 
 cudaError_t launch_linear_forward(const LinearForwardLaunch& L) {
@@ -1263,9 +1370,13 @@ cudaError_t launch_linear_forward(const LinearForwardLaunch& L) {
   p.e.ldo = s.ldy;
   if (s.rows <= kFewRows) return launch_few_rows(p, L.stream);
   Space space{static_cast<char*>(L.workspace)};
+  Chain chain{L.stream};
   Stored* const both[2] = {&p.a, &p.b};
-  const cudaError_t e = make_tileable(both, 2, &space, L.stream);
-  return e == cudaSuccess ? launch_product(p, space, L.withhold, L.stream) : e;
+  cudaError_t e = prepare(both, 2, DbiasArgs{}, &space, &chain);
+  Pending w;
+  if (e == cudaSuccess)
+    e = launch_product(p, plan_forward(s), false, &space, L.withhold, &chain, &w);
+  return e == cudaSuccess ? launch_join(w, &chain) : e;
 }
 
 cudaError_t launch_linear_backward(const LinearBackwardLaunch& L) {
@@ -1273,7 +1384,10 @@ cudaError_t launch_linear_backward(const LinearBackwardLaunch& L) {
   const zero_linear_t& s = L.s;
   Stored dz{L.dy, s.rows, s.out, s.ldy};
   Space space{static_cast<char*>(L.workspace)};
-  if (L.act != ZERO_ACT_NONE || L.dbias != nullptr) {
+  Chain chain{L.stream};
+  DbiasArgs dbias{};
+  cudaError_t e = cudaSuccess;
+  if (s.rows > 0 && (L.act != ZERO_ACT_NONE || L.dbias != nullptr)) {
     SlopeArgs a{};
     a.dy = L.dy;
     a.pre = L.pre;
@@ -1281,7 +1395,6 @@ cudaError_t launch_linear_backward(const LinearBackwardLaunch& L) {
     a.ldp = s.ldp;
     a.rows = s.rows;
     a.cols = s.out;
-    a.act = L.act;
     if (L.act != ZERO_ACT_NONE && (L.dx != nullptr || L.dw != nullptr)) {
       a.dz = static_cast<uint16_t*>(space.take(copy_bytes(dz)));
       a.ldz = copy_pitch(s.out);
@@ -1289,13 +1402,19 @@ cudaError_t launch_linear_backward(const LinearBackwardLaunch& L) {
     }
     const int64_t blocks = slope_blocks(s.rows, s.out);
     a.height = static_cast<int32_t>(slope_height(s.rows, s.out));
-    if (L.dbias != nullptr)
+    if (L.dbias != nullptr) {
       a.sums = static_cast<float*>(space.take(blocks * round_up4(s.out) * 4));
+      dbias.blocks = static_cast<int32_t>(blocks);
+    }
     a.vec = tileable(Stored(L.dy, s.rows, s.out, s.ldy)) &&
             (L.act == ZERO_ACT_NONE || tileable(Stored(L.pre, s.rows, s.out, s.ldp)));
+    auto kernel = L.act == ZERO_ACT_GELU   ? linear_slope_kernel<ZERO_ACT_GELU>
+                  : L.act == ZERO_ACT_SILU ? linear_slope_kernel<ZERO_ACT_SILU>
+                  : L.act == ZERO_ACT_RELU ? linear_slope_kernel<ZERO_ACT_RELU>
+                                           : linear_slope_kernel<ZERO_ACT_NONE>;
     const int64_t across = (s.out + kSlopeCols - 1) / kSlopeCols;
     // the grid's y side ends at 65535
-    for (int64_t k = 0; k < blocks; k += 65535) {
+    for (int64_t k = 0; k < blocks && e == cudaSuccess; k += 65535) {
       SlopeArgs part = a;
       const int64_t skip = k * a.height;
       part.dy += skip * s.ldy;
@@ -1304,28 +1423,33 @@ cudaError_t launch_linear_backward(const LinearBackwardLaunch& L) {
       part.sums += a.sums != nullptr ? k * round_up4(s.out) : 0;
       part.rows -= skip;
       const int64_t high = blocks - k < 65535 ? blocks - k : 65535;
-      linear_slope_kernel<<<dim3(static_cast<unsigned>(across), static_cast<unsigned>(high)),
-                            32 * kSlopeWarps, 0, L.stream>>>(part);
+      const dim3 grid(static_cast<unsigned>(across), static_cast<unsigned>(high));
+      e = chain.launch(kernel, grid, 32 * kSlopeWarps, 0, 1, part);
     }
-    if (L.dbias != nullptr) {
-      const DbiasArgs d{a.sums, s.out, static_cast<int32_t>(blocks), L.dbias, L.grad_f32, L.accumulate};
-      linear_dbias_kernel<<<static_cast<unsigned>((s.out + 31) / 32), 256, 0, L.stream>>>(d);
-    }
-    const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
+    dbias.sums = a.sums;
   }
-  if (s.rows == 0) {
-    if (L.dw == nullptr || L.accumulate) return cudaSuccess;
+  if (L.dbias != nullptr) {
+    dbias.cols = s.out;
+    dbias.dbias = L.dbias;
+    dbias.out_f32 = L.grad_f32;
+    dbias.accumulate = L.accumulate;
+  }
+  if (s.rows == 0) {  // sums of nothing
+    e = prepare(nullptr, 0, dbias, &space, &chain);
+    if (e != cudaSuccess || L.dw == nullptr || L.accumulate) return e;
     return cudaMemset2DAsync(L.dw, s.lddw * (L.grad_f32 ? 4 : 2), 0, s.in * (L.grad_f32 ? 4 : 2),
                              s.out, L.stream);
   }
   Stored w(L.dx != nullptr ? L.w : nullptr, s.out, s.in, s.ldw);
   Stored x(L.dw != nullptr ? L.x : nullptr, s.rows, s.in, s.ldx);
-  if (L.dx != nullptr || L.dw != nullptr) {
-    Stored* const all[3] = {&dz, &w, &x};
-    const cudaError_t e = make_tileable(all, 3, &space, L.stream);
-    if (e != cudaSuccess) return e;
-  }
+  if (L.dx == nullptr && L.dw == nullptr) dz.p = nullptr;
+  Stored* const all[3] = {&dz, &w, &x};
+  e = prepare(all, 3, dbias, &space, &chain);
+  if (e != cudaSuccess) return e;
+  const BackwardPlan plan = plan_backward(s, L.dx != nullptr, L.dw != nullptr);
+  Pending dx{}, dw{};
+  dx.plan.splits = dw.plan.splits = 1;
   if (L.dx != nullptr) {
     Product p{};
     p.a = dz;
@@ -1339,7 +1463,7 @@ cudaError_t launch_linear_backward(const LinearBackwardLaunch& L) {
     p.e.lds = s.ldpi;
     p.e.out = L.dx;
     p.e.ldo = s.lddx;
-    const cudaError_t e = launch_product(p, space, L.withhold, L.stream);
+    e = launch_product(p, plan.dx, false, &space, L.withhold, &chain, &dx);
     if (e != cudaSuccess) return e;
   }
   if (L.dw != nullptr) {
@@ -1355,9 +1479,12 @@ cudaError_t launch_linear_backward(const LinearBackwardLaunch& L) {
     p.e.ldo = s.lddw;
     p.e.out_f32 = L.grad_f32;
     p.e.accumulate = L.accumulate;
-    return launch_product(p, space, L.withhold, L.stream);
+    // dx's product has waited for all that this one reads before it let it begin
+    e = launch_product(p, plan.dw, L.dx != nullptr, &space, L.withhold, &chain, &dw);
+    if (e != cudaSuccess) return e;
   }
-  return cudaSuccess;
+  e = launch_join(dx, &chain);
+  return e == cudaSuccess ? launch_join(dw, &chain) : e;
 }
 
 }  // namespace zeroadam
