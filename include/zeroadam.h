@@ -501,9 +501,10 @@ int zero_device_status(void);
  * While `on` is nonzero, every step launch that uses a TMA-staged kernel
  * (world >= 5, bf16 gradients, fp32 sum, all buffers 16-byte aligned at the
  * stepped range's first element), every zero3_unit_gather or
- * zero3_unit_gather_rows that uses the TMA copy (see those calls), and every
- * zero3_unit_step that runs as a single launch tells its producers to issue
- * no copies.  Every wait then runs out after its limit (about one second),
+ * zero3_unit_gather_rows that uses the TMA copy (see those calls), every
+ * zero3_unit_step that runs as a single launch, and every product of
+ * zero_linear_forward (more than 16 rows) and zero_linear_backward tells its
+ * producers to issue no copies.  Every wait then runs out after its limit (about one second),
  * the outputs of the parts that wait are not written (at world <= 4 the
  * unit step's step part reads its gradients without staging and completes),
  * and zero_device_status reports ZERO_E_TIMEOUT; the device and its context

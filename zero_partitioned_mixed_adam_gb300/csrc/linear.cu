@@ -329,6 +329,25 @@ struct Place {
   }
 };
 
+// Stages that are summed in tensor memory before the sum is taken over in fp32.
+// The tensor cores cut off what does not fit a sum's 24 bits, so a chain of
+// additions comes out too small by 1e-9 of itself for each step of the reduction
+// (1e-6 over 1,024 steps, 4e-6 over 4,096).  fp32 gradients are worth more than
+// that: their chains end after 768 steps, and the epilogue's warps add them up in
+// registers, rounding to nearest.  Results in bf16 keep one chain: its loss is
+// below a hundredth of their rounding up to 16,384 steps.
+template <Kind KIND>
+constexpr int kChain = KIND == kFloat ? 768 / kStep : INT32_MAX;
+
+// A wait for a chain, which may take `stages` stages: 1 s, and 10 us for each.
+__device__ __forceinline__ bool wait_for_chain(uint64_t* bar, uint32_t parity, int stages) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const uint64_t limit = kWaitLimitNs + static_cast<uint64_t>(stages) * 10000u, t0 = global_ns();
+  while (!mbar_try_wait(bar, parity))
+    if (global_ns() - t0 > limit) return false;
+  return true;
+}
+
 // Persistent and specialised by warp.  Warp 0 brings the operands' tiles into a
 // ring of stages; warp 1 of the tile's first CTA issues the matrix
 // instructions, accumulating in one half of tensor memory while the other
@@ -447,36 +466,40 @@ __global__ void __launch_bounds__(kProductThreads, 1)
       constexpr uint32_t lead = 64 * kDepth * 2, stride = 1024;
       Place at(stages);
       int used = 0;  // stages, up to the ring's
-      int n = 0;     // tiles begun
+      int n = 0;     // chains begun
       bool ok = true;
-      for (int t = unit; t < tiles && ok; t += units, ++n) {
+      for (int t = unit; t < tiles && ok; t += units) {
         const Tile tile = tile_of<BM>(a, t);
-        const int b = n & 1;
-        if (n >= 2 && !mbar_wait(&free_[b], static_cast<uint32_t>((n / 2 - 1) & 1))) {
-          ok = false;
-          break;
-        }
-        tc_fence_after();
-        for (int step = tile.first; step < tile.last; ++step, at.next()) {
-          if (!mbar_wait(&full[at.s], at.phase)) {
+        for (int step = tile.first; step < tile.last && ok; ++n) {
+          const int first = step;
+          const int last = tile.last - step > kChain<KIND> ? step + kChain<KIND> : tile.last;
+          const int b = n & 1;
+          if (n >= 2 && !mbar_wait(&free_[b], static_cast<uint32_t>((n / 2 - 1) & 1))) {
             ok = false;
             break;
           }
           tc_fence_after();
-          if (used < stages) ++used;
+          for (; step < last; ++step, at.next()) {
+            if (!mbar_wait(&full[at.s], at.phase)) {
+              ok = false;
+              break;
+            }
+            tc_fence_after();
+            if (used < stages) ++used;
 #pragma unroll
-          for (int h = 0; h < kSub; ++h) {
-            const uint32_t sa = smem_addr(ring) + at.s * stage + h * pair;
-            const uint64_t da = smem_desc(sa, lead, stride);
-            const uint64_t db = smem_desc(sa + a_bytes, lead, stride);
+            for (int h = 0; h < kSub; ++h) {
+              const uint32_t sa = smem_addr(ring) + at.s * stage + h * pair;
+              const uint64_t da = smem_desc(sa, lead, stride);
+              const uint64_t db = smem_desc(sa + a_bytes, lead, stride);
 #pragma unroll
-            for (int q = 0; q < kDepth / 16; ++q)
-              mma_bf16<CG>(tmem + b * Shape::kMaxCols, da + q * (step_a >> 4), db + q * (step_b >> 4), desc,
-                           step > tile.first || q > 0 || h > 0);
+              for (int q = 0; q < kDepth / 16; ++q)
+                mma_bf16<CG>(tmem + b * Shape::kMaxCols, da + q * (step_a >> 4),
+                             db + q * (step_b >> 4), desc, step > first || q > 0 || h > 0);
+            }
+            mma_commit<CG>(&empty[at.s]);
           }
-          mma_commit<CG>(&empty[at.s]);
+          if (ok) mma_commit<CG>(&done[b]);
         }
-        if (ok) mma_commit<CG>(&done[b]);
       }
       if (!ok) {
         // products already issued end before tensor memory is freed
@@ -493,58 +516,34 @@ __global__ void __launch_bounds__(kProductThreads, 1)
     const bool vec = a.e.vec != 0;
     const int bn = a.bn;
     const int64_t rows = a.rows, cols = a.cols;
-    int n = 0;
-    for (int t = unit; t < tiles; t += units, ++n) {
-      const Tile tile = tile_of<BM>(a, t);
-      const int b = n & 1;
-      if (!mbar_wait(&done[b], static_cast<uint32_t>((n / 2) & 1))) {
-        if (lane == 0) atomicExch(&g_linear_status, 3);
-        break;
+    const uint32_t lanes = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
+    // This half of tensor memory has been read by the warp and may be written again.
+    const auto release = [&](int b) {
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        if constexpr (CG == 2) mbar_arrive_peer(peer_addr(&free_[b], 0));
+        else mbar_arrive(&free_[b]);
       }
-      tc_fence_after();
+    };
+    int n = 0;
+    bool ok = true;
+    for (int t = unit; t < tiles && ok; t += units) {
+      const Tile tile = tile_of<BM>(a, t);
       const int64_t row0 = tile.row + rank * kBlockRows + quarter * 32;
-      const uint32_t from =
-          tmem + (static_cast<uint32_t>(quarter * 32) << 16) + b * Shape::kMaxCols;
       // (rows past the end are left out by the copy)
       const bool any = row0 < rows;
       const bool fast = any && vec && tile.part < 0 && tile.col + bn <= cols;
       const bool mine_in = row0 + lane < rows;
-      if (32 * half >= bn) {  // nothing of a tile this narrow is this warp's
-        __syncwarp();
-        if (lane == 0) {
-          if constexpr (CG == 2) mbar_arrive_peer(peer_addr(&free_[b], 0));
-          else mbar_arrive(&free_[b]);
-        }
-      }
-      uint32_t bits[32];
-      if (32 * half < bn) {
-        tmem_load32(from + 32 * half, bits);
-        if (fast) part.ask(row0 + lane, tile.col + 32 * half, mine_in);
-      }
-#pragma unroll 1
-      for (int c = 32 * half; c < bn; c += 64) {
+      // 32 columns from c on are summed up: on their way.
+      const auto finish = [&](float x[32], int c) {
         const int64_t col0 = tile.col + c;
-        float x[32];
-        tmem_load_wait();
-#pragma unroll
-        for (int q = 0; q < 32; ++q) x[q] = __uint_as_float(bits[q]);
-        if (c + 64 < bn) {  // the next part's sums come while this one's are worked on
-          tmem_load32(from + c + 64, bits);
-        } else {  // the warp has read its part: this half may be written again
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) {
-            if constexpr (CG == 2) mbar_arrive_peer(peer_addr(&free_[b], 0));
-            else mbar_arrive(&free_[b]);
-          }
-        }
         if (fast) {
           part.put(a, reinterpret_cast<uint8_t*>(mine), x, static_cast<int>(row0),
                    static_cast<int>(col0), lane);
-          if (c + 64 < bn) part.ask(row0 + lane, col0 + 64, mine_in);
-          continue;
+          return;
         }
-        if (!any || col0 >= cols) continue;
+        if (!any || col0 >= cols) return;
         if (tile.part >= 0) {
           part.send_sums(&a.parts, reinterpret_cast<uint8_t*>(mine), x, c,
                          static_cast<int>(row0 - tile.row), tile.part, false, lane);
@@ -563,8 +562,69 @@ __global__ void __launch_bounds__(kProductThreads, 1)
           epilogue_scalar<KIND>(a.e, mine, row0, col0, rows, cols, lane);
           __syncwarp();
         }
+      };
+      if constexpr (KIND == kFloat) {
+        constexpr int kParts = Shape::kMaxCols / 64;
+        float sum[kParts][32];
+        for (int step = tile.first; step < tile.last; step += kChain<KIND>, ++n) {
+          const int b = n & 1;
+          ok = wait_for_chain(&done[b], static_cast<uint32_t>((n / 2) & 1), kChain<KIND>);
+          if (!ok) break;
+          tc_fence_after();
+#pragma unroll
+          for (int i = 0; i < kParts; ++i) {
+            const int c = 32 * half + 64 * i;
+            if (c >= bn) break;
+#pragma unroll
+            for (int h = 0; h < 32; h += 16) {  // 16 at a time: 128 registers hold the sums
+              uint32_t bits[16];
+              tmem_load16(lanes + b * Shape::kMaxCols + c + h, bits);
+              tmem_load_wait();
+              if (step == tile.first) {
+#pragma unroll
+                for (int q = 0; q < 16; ++q) sum[i][h + q] = __uint_as_float(bits[q]);
+              } else {
+#pragma unroll
+                for (int q = 0; q < 16; ++q) sum[i][h + q] += __uint_as_float(bits[q]);
+              }
+            }
+          }
+          release(b);
+        }
+        if (ok) {
+#pragma unroll
+          for (int i = 0; i < kParts; ++i)
+            if (32 * half + 64 * i < bn) finish(sum[i], 32 * half + 64 * i);
+        }
+      } else {
+        const int b = n & 1;
+        ok = wait_for_chain(&done[b], static_cast<uint32_t>((n / 2) & 1), tile.last - tile.first);
+        ++n;
+        if (!ok) break;
+        tc_fence_after();
+        const uint32_t from = lanes + b * Shape::kMaxCols;
+        uint32_t bits[32];
+        if (32 * half < bn) {
+          tmem_load32(from + 32 * half, bits);
+          if (fast) part.ask(row0 + lane, tile.col + 32 * half, mine_in);
+        } else {
+          release(b);  // nothing of a tile this narrow is this warp's
+        }
+#pragma unroll 1
+        for (int c = 32 * half; c < bn; c += 64) {
+          float x[32];
+          tmem_load_wait();
+#pragma unroll
+          for (int q = 0; q < 32; ++q) x[q] = __uint_as_float(bits[q]);
+          // the next part's sums come while this one's are worked on
+          if (c + 64 < bn) tmem_load32(from + c + 64, bits);
+          else release(b);
+          finish(x, c);
+          if (fast && c + 64 < bn) part.ask(row0 + lane, tile.col + c + 64, mine_in);
+        }
       }
     }
+    if (!ok && lane == 0) atomicExch(&g_linear_status, 3);
     if (lane == 0) bulk_wait_all();
   }
   __syncwarp();

@@ -122,6 +122,16 @@ __device__ __forceinline__ void tmem_load32(uint32_t addr, uint32_t x[32]) {
         "=r"(x[28]), "=r"(x[29]), "=r"(x[30]), "=r"(x[31])
       : "r"(addr));
 }
+// The same with 16 columns.
+__device__ __forceinline__ void tmem_load16(uint32_t addr, uint32_t x[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+      : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3]), "=r"(x[4]), "=r"(x[5]), "=r"(x[6]),
+        "=r"(x[7]), "=r"(x[8]), "=r"(x[9]), "=r"(x[10]), "=r"(x[11]), "=r"(x[12]), "=r"(x[13]),
+        "=r"(x[14]), "=r"(x[15])
+      : "r"(addr));
+}
 __device__ __forceinline__ void tmem_load_wait() {
   asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 }

@@ -13,6 +13,11 @@ ceil(numel/world), zero-padded tail); the differences are GB300-first:
 - step() is one zero_adam_step launch on the current stream (no collectives:
   the ranks are buffers in this GPU's memory).
 
+TensorAdamW is the same surface over a list of tensors that keep their own
+storage (a rank's FSDP2-style row shards, or a whole model on one card): AdamW
+with decoupled weight decay, clipping by the global norm, and moments in 32 or
+8 bits.
+
 This module only allocates (through PyTorch) and marshals; the arithmetic runs
 in libzeroadam.so.
 """
@@ -20,7 +25,9 @@ from __future__ import annotations
 
 import torch
 
-from . import ZERO_ALL_RANKS, check_device, pointer_array, zero_adam_step, zero_plan
+from . import (ZERO_ALL_RANKS, ZERO_MOMENT_BLOCK, adamw_tensors, check_device,
+               grad_norm_workspace, pointer_array, zero_adam_step, zero_adamw_state_f32,
+               zero_adamw_step, zero_grad_norm, zero_plan)
 
 
 class ZeroAdam:
@@ -84,3 +91,82 @@ class ZeroAdam:
     def state_bytes(self):
         """fp32 master + m + v bytes one rank holds (12 x shard)."""
         return 3 * 4 * self.shard
+
+
+class TensorAdamW:
+    """AdamW over a list of bf16 CUDA tensors: one norm (with max_norm) and one step launch
+    per 384 tensors.
+
+    Each parameter has an fp32 master copy and fp32 moments, or with eight_bit=True
+    8-bit ones (2 + 8/256 bytes a parameter instead of 8).  weight_decay is applied to
+    tensors of two or more dimensions.  Gradients are bf16 or fp32 tensors of the
+    parameters' sizes: those of `grads`, filled by the caller, or else each
+    parameter's .grad at step()."""
+
+    def __init__(self, params, lr, betas=(0.9, 0.999), eps=1e-8, weight_decay=0.0, max_norm=None,
+                 eight_bit=False, grads=None, seed=0):
+        self.params = list(params)
+        if not self.params or any(p.device.type != "cuda" for p in self.params):
+            raise ValueError("TensorAdamW keeps its state in GPU memory: give it CUDA parameters")
+        if any(p.dtype != torch.bfloat16 or not p.is_contiguous() for p in self.params):
+            raise ValueError("the parameters are contiguous bf16 tensors")
+        self.lr, self.betas, self.eps, self.max_norm, self.t = lr, betas, eps, max_norm, 0
+        self.decay = [weight_decay if p.dim() > 1 else 0.0 for p in self.params]
+        self.eight_bit, self.seed, self.grads = eight_bit, seed, grads
+        dev = self.params[0].device
+        like = dict(dtype=torch.uint8 if eight_bit else torch.float32, device=dev)
+        self.master = [p.detach().float() for p in self.params]
+        self.m = [torch.zeros(p.shape, **like) for p in self.params]
+        self.v = [torch.zeros(p.shape, **like) for p in self.params]
+        self.m_scale = self.v_scale = None
+        if eight_bit:
+            blocks = [-(-p.numel() // ZERO_MOMENT_BLOCK) for p in self.params]
+            self.m_scale = [torch.zeros(b, dtype=torch.float32, device=dev) for b in blocks]
+            self.v_scale = [torch.zeros(b, dtype=torch.float32, device=dev) for b in blocks]
+        self.norm = torch.zeros(2, dtype=torch.float32, device=dev)  # of the last step, and its clip
+        self._workspace = grad_norm_workspace(dev)
+        self._list = None
+
+    def _tensors(self):
+        grads = self.grads if self.grads is not None else [p.grad for p in self.params]
+        if any(g is None for g in grads):
+            raise ValueError("a parameter has no gradient")
+        known = self._list
+        if known is None or any(a is not b or a.data_ptr() != p for a, b, p in
+                                zip(grads, known.grads.buffers, known.grads.ptrs)):
+            self._list = adamw_tensors(grads, self.master, self.m, self.v, params=self.params,
+                                       m_scale=self.m_scale, v_scale=self.v_scale,
+                                       weight_decay=self.decay)
+        return self._list
+
+    def step(self, stream=None):
+        """One step: the gradients' global norm and its clip (with max_norm), then AdamW."""
+        tensors = self._tensors()
+        self.t += 1
+        scale = None
+        if self.max_norm is not None:
+            zero_grad_norm(tensors, self.norm, max_norm=self.max_norm, workspace=self._workspace,
+                           stream=stream)
+            scale = self.norm[1:]
+        b1, b2 = self.betas
+        zero_adamw_step(tensors, lr=self.lr, beta1=b1, beta2=b2, eps=self.eps, t=self.t,
+                        grad_scale=scale, seed=self.seed + self.t, stream=stream)
+
+    def zero_grad(self):
+        for g in self.grads if self.grads is not None else [p.grad for p in self.params]:
+            if g is not None:
+                g.zero_()
+
+    def moments(self):
+        """(m, v) of every parameter as fp32, for a checkpoint."""
+        if not self.eight_bit:
+            return self.m, self.v
+        out = [[torch.empty(p.shape, dtype=torch.float32, device=p.device) for p in self.params]
+               for _ in range(2)]
+        zero_adamw_state_f32(self._tensors(), *out)
+        return out[0], out[1]
+
+    def state_bytes(self):
+        """Bytes of master weights and moments."""
+        lists = (self.master, self.m, self.v, self.m_scale or [], self.v_scale or [])
+        return sum(t.numel() * t.element_size() for x in lists for t in x)
