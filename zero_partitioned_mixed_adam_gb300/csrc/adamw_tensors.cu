@@ -32,13 +32,14 @@ __host__ __device__ __forceinline__ uint32_t pcg_hash(uint32_t x) {
   return (x >> 22) ^ x;
 }
 
-// Index of the tensor that holds `tile`: the last with tile0 <= tile.
-template <typename Desc>
-__device__ __forceinline__ int find_tensor(const Desc* t, int count, int tile, int low) {
-  int high = count;  // t[low].tile0 <= tile < t[high].tile0
+// Index of the tensor that holds `tile`: the last with tile0 <= tile, from `low`
+// on.  The tensors' first tiles are an array of their own, which stays in the
+// constant cache where the descriptors around them would not.
+__device__ __forceinline__ int find_tensor(const int32_t* tile0, int count, int tile, int low) {
+  int high = count;  // tile0[low] <= tile < tile0[high]
   while (high - low > 1) {
     const int mid = (low + high) / 2;
-    if (t[mid].tile0 <= tile) low = mid; else high = mid;
+    if (tile0[mid] <= tile) low = mid; else high = mid;
   }
   return low;
 }
@@ -256,14 +257,14 @@ struct AdamwDesc {
   float* m_scale;
   float* v_scale;
   int64_t numel;
-  float keep;     // 1 - lr * weight_decay
-  uint32_t key;   // of the random bits
-  int32_t tile0;  // first tile of this tensor in the launch
-  int32_t vec;    // every buffer allows vector accesses
+  float keep;    // 1 - lr * weight_decay
+  uint32_t key;  // of the random bits
+  int64_t vec;   // every buffer allows vector accesses
 };
 
 template <int CAP>
 struct AdamwArgs {
+  int32_t tile0[CAP];  // first tile of each tensor
   AdamwDesc t[CAP];
   AdamwScalars s;
   const float* grad_scale;
@@ -352,9 +353,9 @@ __global__ void __launch_bounds__(kThreads, EIGHT ? 4 : 3)
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   int ti = 0;
   for (int tile = blockIdx.x; tile < a.tiles; tile += gridDim.x) {
-    ti = find_tensor(a.t, a.count, tile, ti);
+    ti = find_tensor(a.tile0, a.count, tile, ti);
     const AdamwDesc& t = a.t[ti];
-    const int64_t base = static_cast<int64_t>(tile - t.tile0) * kTile + 256 * warp;
+    const int64_t base = static_cast<int64_t>(tile - a.tile0[ti]) * kTile + 256 * warp;
     if (base >= t.numel) continue;  // the same for the whole warp
     if (t.vec && base + 256 <= t.numel)
       adamw_tile<true, GF32, EIGHT>(t, a.s, clip, clipped, base, lane);
@@ -368,12 +369,12 @@ struct MomentsDesc {
   const float* scale;
   float* out;
   int64_t numel;
-  int32_t tile0;
-  int16_t is_m, vec;
+  int32_t is_m, vec;
 };
 
 template <int CAP>
 struct MomentsArgs {
+  int32_t tile0[CAP];
   MomentsDesc t[CAP];
   int32_t count, tiles;
 };
@@ -403,8 +404,9 @@ template <int CAP>
 __global__ void __launch_bounds__(kThreads)
     adamw_moments_kernel(const __grid_constant__ MomentsArgs<CAP> a) {
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, tile = blockIdx.x;
-  const MomentsDesc& t = a.t[find_tensor(a.t, a.count, tile, 0)];
-  const int64_t base = static_cast<int64_t>(tile - t.tile0) * kTile + 256 * warp;
+  const int ti = find_tensor(a.tile0, a.count, tile, 0);
+  const MomentsDesc& t = a.t[ti];
+  const int64_t base = static_cast<int64_t>(tile - a.tile0[ti]) * kTile + 256 * warp;
   if (base >= t.numel) return;
   if (t.vec && base + 256 <= t.numel) moments_tile<true>(t, base, lane);
   else moments_tile<false>(t, base, lane);
@@ -415,14 +417,14 @@ __global__ void __launch_bounds__(kThreads)
 struct NormDesc {
   const void* grad;
   int64_t numel;
-  int32_t tile0;
-  int32_t shift;  // elements between the 16-byte boundary before the tensor and its start
+  int64_t shift;  // elements between the 16-byte boundary before the tensor and its start
 };
 
 constexpr int kNormTile = kThreads * 64;  // elements
 
 template <int CAP>
 struct NormArgs {
+  int32_t tile0[CAP];
   NormDesc t[CAP];
   int32_t count, tiles;
   int32_t slot0, slots;  // this launch's first place in the workspace; places of all launches
@@ -443,9 +445,9 @@ __global__ void __launch_bounds__(kThreads)
   double sum = 0.0;
   int ti = 0;
   for (int tile = blockIdx.x; tile < a.tiles; tile += gridDim.x) {
-    ti = find_tensor(a.t, a.count, tile, ti);
+    ti = find_tensor(a.tile0, a.count, tile, ti);
     const NormDesc& t = a.t[ti];
-    const int64_t first = static_cast<int64_t>(tile - t.tile0) * kNormTile;
+    const int64_t first = static_cast<int64_t>(tile - a.tile0[ti]) * kNormTile;
     const int64_t end = t.numel + t.shift;
     const char* p = static_cast<const char*>(t.grad) - t.shift * (GF32 ? 4 : 2);
     float acc = 0.0f;
@@ -552,7 +554,7 @@ cudaError_t launch_adamw_chunk(const AdamwLaunch& L, const int32_t* index, int c
     t.numel = x.numel;
     t.keep = static_cast<float>(1.0 - L.lr * x.weight_decay);
     t.key = pcg_hash(seed + static_cast<uint32_t>(index[k]));
-    t.tile0 = static_cast<int32_t>(tiles);
+    a.tile0[k] = static_cast<int32_t>(tiles);
     const uintptr_t code = L.eight ? 8 : 16;
     t.vec = aligned(t.grad, 16) && aligned(t.master, 16) && aligned(t.param, 16) &&
             aligned(t.m, code) && aligned(t.v, code);
@@ -619,12 +621,12 @@ cudaError_t launch_adamw_moments(const MomentsLaunch& L) {
     for (int which = 0; which < 2; ++which) {
       float* const* out = which == 0 ? L.m_out : L.v_out;
       if (out == nullptr) continue;
+      a.tile0[a.count] = static_cast<int32_t>(tiles);
       MomentsDesc& t = a.t[a.count++];
       t.codes = static_cast<const uint8_t*>(which == 0 ? x.m : x.v);
       t.scale = which == 0 ? x.m_scale : x.v_scale;
       t.out = out[i];
       t.numel = x.numel;
-      t.tile0 = static_cast<int32_t>(tiles);
       t.is_m = which == 0;
       t.vec = aligned(t.codes, 8) && aligned(t.out, 32);
       tiles += (x.numel + kTile - 1) / kTile;
@@ -649,8 +651,8 @@ cudaError_t launch_norm_chunk(const NormLaunch& L, const int32_t* index, int cou
     NormDesc& t = a.t[k];
     t.grad = L.grads[index[k]];
     t.numel = L.numels[index[k]];
-    t.tile0 = static_cast<int32_t>(tiles);
-    t.shift = static_cast<int32_t>((reinterpret_cast<uintptr_t>(t.grad) & 15u) /
+    a.tile0[k] = static_cast<int32_t>(tiles);
+    t.shift = static_cast<int64_t>((reinterpret_cast<uintptr_t>(t.grad) & 15u) /
                                    (L.grad_f32 ? 4u : 2u));
     tiles += (t.numel + t.shift + kNormTile - 1) / kNormTile;
   }
