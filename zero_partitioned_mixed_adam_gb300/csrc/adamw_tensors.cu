@@ -17,7 +17,10 @@ namespace zeroadam {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kTile = kThreads * 8;  // elements of one tile: 8 moment blocks, one per warp
+// Elements of a tile: each warp's, one moment block of 256 or several in a row,
+// so that finding the tensor (10 to 50 instructions a warp) does not count.
+constexpr int kBlocksOfWarp32 = 1, kBlocksOfWarp8 = 1, kBlocksOfWarpMoments = 2;
+__host__ __device__ constexpr int tile_of_blocks(int blocks) { return kThreads * 8 * blocks; }
 
 __device__ __forceinline__ float bf16_value(uint32_t h) { return __uint_as_float(h << 16); }
 __device__ __forceinline__ uint32_t bf16_bits(float x) {
@@ -277,11 +280,14 @@ __device__ __forceinline__ void adamw_element(float g, const AdamwScalars& s, fl
                                               float& m, float& v) {
   m = __fadd_rn(__fmul_rn(m, s.b1), __fmul_rn(s.omb1, g));
   v = __fadd_rn(__fmul_rn(v, s.b2), __fmul_rn(__fmul_rn(s.omb2, g), g));
-  // the root and the quotient of the special-function unit, 2 ulp each: the
-  // correctly rounded ones took a quarter of the 8-bit step's time
-  float root;
+  // the root and the inverse of the special-function unit, 1 to 2 ulp each: the
+  // correctly rounded ones took a quarter of the 8-bit step's time.  (The inverse
+  // takes denominators below the least normal number, which only eps = 0 and v = 0
+  // give, as 0, and is 0 past 2^126.)
+  float root, inverse;
   asm("sqrt.approx.f32 %0, %1;" : "=f"(root) : "f"(v));
-  w = w * keep - __fdividef(s.size * m, root * s.inv_root + s.eps);
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inverse) : "f"(root * s.inv_root + s.eps));
+  w = w * keep - s.size * m * inverse;
 }
 
 // 8 elements per thread; one warp's 256 are one moment block.
@@ -346,21 +352,25 @@ __device__ __forceinline__ void adamw_tile(const AdamwDesc& t, const AdamwScalar
 constexpr int kBlocksPerSm = 64;
 
 template <int CAP, bool GF32, bool EIGHT>
-__global__ void __launch_bounds__(kThreads, EIGHT ? 4 : 3)
+__global__ void __launch_bounds__(kThreads, EIGHT ? 6 : 3)
     adamw_tensors_kernel(const __grid_constant__ AdamwArgs<CAP> a) {
   const bool clipped = a.grad_scale != nullptr;
   const float clip = clipped ? *a.grad_scale : 1.0f;
+  constexpr int kBlocks = EIGHT ? kBlocksOfWarp8 : kBlocksOfWarp32;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   int ti = 0;
   for (int tile = blockIdx.x; tile < a.tiles; tile += gridDim.x) {
     ti = find_tensor(a.tile0, a.count, tile, ti);
     const AdamwDesc& t = a.t[ti];
-    const int64_t base = static_cast<int64_t>(tile - a.tile0[ti]) * kTile + 256 * warp;
-    if (base >= t.numel) continue;  // the same for the whole warp
-    if (t.vec && base + 256 <= t.numel)
-      adamw_tile<true, GF32, EIGHT>(t, a.s, clip, clipped, base, lane);
-    else
-      adamw_tile<false, GF32, EIGHT>(t, a.s, clip, clipped, base, lane);
+    int64_t base = static_cast<int64_t>(tile - a.tile0[ti]) * tile_of_blocks(kBlocks) + 256 * warp;
+#pragma unroll 1
+    for (int k = 0; k < kBlocks; ++k, base += tile_of_blocks(1)) {
+      if (base >= t.numel) break;  // the same for the whole warp
+      if (t.vec && base + 256 <= t.numel)
+        adamw_tile<true, GF32, EIGHT>(t, a.s, clip, clipped, base, lane);
+      else
+        adamw_tile<false, GF32, EIGHT>(t, a.s, clip, clipped, base, lane);
+    }
   }
 }
 
@@ -406,10 +416,14 @@ __global__ void __launch_bounds__(kThreads)
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, tile = blockIdx.x;
   const int ti = find_tensor(a.tile0, a.count, tile, 0);
   const MomentsDesc& t = a.t[ti];
-  const int64_t base = static_cast<int64_t>(tile - a.tile0[ti]) * kTile + 256 * warp;
-  if (base >= t.numel) return;
-  if (t.vec && base + 256 <= t.numel) moments_tile<true>(t, base, lane);
-  else moments_tile<false>(t, base, lane);
+  int64_t base = static_cast<int64_t>(tile - a.tile0[ti]) * tile_of_blocks(kBlocksOfWarpMoments) +
+                 256 * warp;
+#pragma unroll 1
+  for (int k = 0; k < kBlocksOfWarpMoments; ++k, base += tile_of_blocks(1)) {
+    if (base >= t.numel) return;
+    if (t.vec && base + 256 <= t.numel) moments_tile<true>(t, base, lane);
+    else moments_tile<false>(t, base, lane);
+  }
 }
 
 // ------------------------------------------------------------------- norm
@@ -558,7 +572,8 @@ cudaError_t launch_adamw_chunk(const AdamwLaunch& L, const int32_t* index, int c
     const uintptr_t code = L.eight ? 8 : 16;
     t.vec = aligned(t.grad, 16) && aligned(t.master, 16) && aligned(t.param, 16) &&
             aligned(t.m, code) && aligned(t.v, code);
-    tiles += (x.numel + kTile - 1) / kTile;
+    const int64_t per = tile_of_blocks(L.eight ? kBlocksOfWarp8 : kBlocksOfWarp32);
+    tiles += (x.numel + per - 1) / per;
   }
   if (tiles > INT32_MAX) return cudaErrorInvalidValue;
   a.s = L.s;
@@ -629,7 +644,8 @@ cudaError_t launch_adamw_moments(const MomentsLaunch& L) {
       t.numel = x.numel;
       t.is_m = which == 0;
       t.vec = aligned(t.codes, 8) && aligned(t.out, 32);
-      tiles += (x.numel + kTile - 1) / kTile;
+      constexpr int kPer = tile_of_blocks(kBlocksOfWarpMoments);
+      tiles += (x.numel + kPer - 1) / kPer;
       if (a.count == kCap || tiles > INT32_MAX / 2) {
         const cudaError_t e = flush();
         if (e != cudaSuccess) return e;
