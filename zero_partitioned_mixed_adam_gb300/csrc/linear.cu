@@ -726,42 +726,76 @@ struct PrepareArgs {
   DbiasArgs dbias;
 };
 
-// A matrix laid out anew with rows on 128-byte boundaries: 8 elements a thread,
-// read one by one and 64 bytes of a row by each warp at a time.
+// A matrix laid out anew with rows on 128-byte boundaries.  A lane writes 16
+// bytes of a row; it reads the aligned 16 bytes in which they begin, takes those
+// in which they end from its neighbour, and shifts.  Vectors that lie partly
+// outside the matrix's memory are read element by element.
+__device__ __forceinline__ uint4 aligned_load(const char* p, const char* begin, const char* end) {
+  if (p >= begin && p + 16 <= end) return __ldg(reinterpret_cast<const uint4*>(p));
+  uint32_t w[4] = {};
+#pragma unroll
+  for (int c = 0; c < 8; ++c)
+    if (p + 2 * c >= begin && p + 2 * c < end)
+      w[c / 2] |= static_cast<uint32_t>(__ldg(reinterpret_cast<const uint16_t*>(p + 2 * c)))
+                  << (16 * (c & 1));
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
 __device__ __forceinline__ void copy_rows(const CopyArgs& a) {
   const int64_t per = (a.cols + 255) / 256;  // warps a row
   const int lane = threadIdx.x % 32;
+  const char* begin = reinterpret_cast<const char*>(a.src);
+  const char* end = begin + 2 * ((a.rows - 1) * a.lds + a.cols);
   for (int64_t q = static_cast<int64_t>(blockIdx.x) * 8 + threadIdx.x / 32; q < a.rows * per;
        q += static_cast<int64_t>(gridDim.x) * 8) {
     const int64_t i = q / per, j0 = (q - i * per) * 256;
-    const uint16_t* s = a.src + i * a.lds + j0 + lane;
-    uint16_t x[8];
+    const char* s = begin + 2 * (i * a.lds + j0);
+    const uint32_t off = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(s)) & 15u;
+    s += 16 * lane - static_cast<int>(off);
+    const uint4 u = aligned_load(s, begin, end);
+    uint32_t w[9] = {u.x, u.y, u.z, u.w, 0, 0, 0, 0, 0};
 #pragma unroll
-    for (int c = 0; c < 8; ++c) x[c] = j0 + 32 * c + lane < a.cols ? __ldg(s + 32 * c) : 0;
+    for (int k = 0; k < 4; ++k) w[4 + k] = __shfl_down_sync(0xffffffffu, w[k], 1);
+    if (lane == 31 && off != 0) {
+      const uint4 v = aligned_load(s + 16, begin, end);
+      w[4] = v.x; w[5] = v.y; w[6] = v.z; w[7] = v.w;
+    }
+    if (off & 8u) {
 #pragma unroll
-    for (int c = 0; c < 8; ++c)
-      if (j0 + 32 * c + lane < a.cols) a.dst[i * a.ldd + j0 + 32 * c + lane] = x[c];
+      for (int k = 0; k < 6; ++k) w[k] = w[k + 2];
+    }
+    if (off & 4u) {
+#pragma unroll
+      for (int k = 0; k < 5; ++k) w[k] = w[k + 1];
+    }
+    if (off & 2u) {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) w[k] = __funnelshift_r(w[k], w[k + 1], 16);
+    }
+    const int64_t j = j0 + 8 * lane;
+    if (j < a.cols)
+      *reinterpret_cast<uint4*>(a.dst + i * a.ldd + j) = make_uint4(w[0], w[1], w[2], w[3]);
   }
 }
 
-// 32 columns of dbias at a time, 8 runs of row blocks each.
+// 8 columns of dbias at a time, 32 runs of row blocks each.
 __device__ __forceinline__ void add_dbias(const DbiasArgs& a) {
-  __shared__ float part[8][32];
-  const int r = threadIdx.x / 32, lane = threadIdx.x % 32;
-  for (int64_t j0 = static_cast<int64_t>(blockIdx.x) * 32; j0 < a.cols;
-       j0 += static_cast<int64_t>(gridDim.x) * 32) {
-    const int64_t j = j0 + lane;
+  __shared__ float part[32][9];
+  const int r = threadIdx.x / 8, c = threadIdx.x % 8;
+  for (int64_t j0 = static_cast<int64_t>(blockIdx.x) * 8; j0 < a.cols;
+       j0 += static_cast<int64_t>(gridDim.x) * 8) {
+    const int64_t j = j0 + c;
     float sum = 0.0f;
     if (j < a.cols) {
 #pragma unroll 8
-      for (int k = r; k < a.blocks; k += 8) sum += __ldcg(a.sums + k * round_up4(a.cols) + j);
+      for (int k = r; k < a.blocks; k += 32) sum += __ldcg(a.sums + k * round_up4(a.cols) + j);
     }
     __syncthreads();
-    part[r][lane] = sum;
+    part[r][c] = sum;
     __syncthreads();
     if (r != 0 || j >= a.cols) continue;
 #pragma unroll
-    for (int k = 1; k < 8; ++k) sum += part[k][lane];
+    for (int k = 1; k < 32; ++k) sum += part[k][c];
     if (a.out_f32) {
       float* o = static_cast<float*>(a.dbias) + j;
       *o = a.accumulate ? *o + sum : sum;
@@ -844,7 +878,7 @@ cudaError_t prepare(Stored* const* matrices, int count, const DbiasArgs& dbias, 
   int jobs = all.copies;
   if (dbias.dbias != nullptr) {
     all.dbias = dbias;
-    const int64_t blocks = (dbias.cols + 31) / 32;
+    const int64_t blocks = (dbias.cols + 7) / 8;
     most = blocks > most ? blocks : most;
     ++jobs;
   }
