@@ -85,22 +85,23 @@ struct Tile {
 // tiles in flight at one time share their operands in L2; after the first
 // `whole` of them each tile is `splits` items, one for each part of the
 // reduction, so that the last round of tiles keeps every SM busy.
+__device__ __forceinline__ void part_of(const ProductArgs& a, int t, Tile& r) {
+  r.part = -1;
+  r.first = 0;
+  r.last = a.steps;
+  if (t >= a.whole && a.splits > 1) {
+    r.part = t - a.whole;
+    const int part = r.part % a.splits;
+    r.first = static_cast<int>(static_cast<int64_t>(a.steps) * part / a.splits);
+    r.last = static_cast<int>(static_cast<int64_t>(a.steps) * (part + 1) / a.splits);
+  }
+}
 template <int BM>
 __device__ __forceinline__ Tile tile_of(const ProductArgs& a, int t) {
   constexpr int kGroup = 8;
   Tile r;
-  r.part = -1;
-  r.first = 0;
-  r.last = a.steps;
-  if (t >= a.whole) {
-    const int u = t - a.whole, part = u % a.splits;
-    t = a.whole + u / a.splits;
-    if (a.splits > 1) {
-      r.part = u;
-      r.first = static_cast<int>(static_cast<int64_t>(a.steps) * part / a.splits);
-      r.last = static_cast<int>(static_cast<int64_t>(a.steps) * (part + 1) / a.splits);
-    }
-  }
+  part_of(a, t, r);
+  if (t >= a.whole) t = a.whole + (t - a.whole) / a.splits;
   const int group = t / (kGroup * a.tiles_n);
   const int m0 = group * kGroup;
   const int height = a.tiles_m - m0 < kGroup ? a.tiles_m - m0 : kGroup;
@@ -406,8 +407,9 @@ __global__ void __launch_bounds__(kProductThreads, 1)
       Place at(stages);
       int issued = 0;  // stages, up to the ring's
       bool ok = true;
+      Tile next = tile_of<BM>(a, unit);
       for (int t = unit; t < tiles && ok; t += units) {
-        const Tile tile = tile_of<BM>(a, t);
+        const Tile tile = next;
         const int ra = static_cast<int>(tile.row) + rank * kBlockRows;
         const int rb = static_cast<int>(tile.col) + rank * b_rows;
         for (int step = tile.first; step < tile.last; ++step, at.next()) {
@@ -419,7 +421,10 @@ __global__ void __launch_bounds__(kProductThreads, 1)
           } else {
             ++issued;
           }
-          if (a.withhold) continue;
+          if (a.withhold) {
+            if (step == tile.first && t + units < tiles) next = tile_of<BM>(a, t + units);
+            continue;
+          }
           const uint32_t bar = CG == 2 ? peer_addr(&full[at.s], 0) : smem_addr(&full[at.s]);
           if (rank == 0) mbar_expect_tx(&full[at.s], CG * stage);
 #pragma unroll
@@ -441,6 +446,8 @@ __global__ void __launch_bounds__(kProductThreads, 1)
               tile_load<CG>(sb, &a.b, x, rb, bar);
             }
           }
+          // (off the path from one tile's last loads to the next one's first)
+          if (step == tile.first && t + units < tiles) next = tile_of<BM>(a, t + units);
         }
       }
       if (!ok) atomicExch(&g_linear_status, 1);
@@ -469,7 +476,8 @@ __global__ void __launch_bounds__(kProductThreads, 1)
       int n = 0;     // chains begun
       bool ok = true;
       for (int t = unit; t < tiles && ok; t += units) {
-        const Tile tile = tile_of<BM>(a, t);
+        Tile tile;
+        part_of(a, t, tile);
         for (int step = tile.first; step < tile.last && ok; ++n) {
           const int first = step;
           const int last = tile.last - step > kChain<KIND> ? step + kChain<KIND> : tile.last;
