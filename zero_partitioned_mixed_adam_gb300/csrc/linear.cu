@@ -183,11 +183,12 @@ __device__ __noinline__ void epilogue_scalar(const Epilogue& e, const float* min
   }
 }
 
-// A 32 x 32 part, a row a lane, through shared memory and out by TMA: plain
-// stores of the same sectors took 12 of 160 us from the matrix instructions at
-// 8192 x 2048 x 8192.  A warp has 4 KB: two slots of bf16, or one of fp32, in
-// TMA's swizzle, which keeps the lanes' 16-byte writes off each other's banks.
-// fp32 gradients are added to what is there by the copy itself.
+// A 32 x 32 part, a row a lane, through shared memory and out by TMA, which takes
+// the addresses and the edges off the lanes and adds fp32 gradients to what is
+// there itself, in L2 (128 x 8192 x 8192 fp32: 64 us with stores by the lanes, 56
+// so; accumulating 138 and 115; what both come to below 2^-126 is 0 there).  A
+// warp has 4 KB: two slots of bf16, or one of fp32, in TMA's swizzle, which keeps
+// the lanes' 16-byte writes off each other's banks.
 //
 // The parameters are taken into registers once, and each step is one branch
 // around its 32 columns: a warp runs a part alone, with nothing to hide a
@@ -359,6 +360,10 @@ __device__ __forceinline__ bool wait_for_chain(uint64_t* bar, uint32_t parity, i
 // first CTA) when every epilogue warp has read it.
 // Every wait is bounded; one that gives up sets g_linear_status and ends its
 // warp's loop, and the others' waits then run out too.
+// What bounds it is the tensor cores: at 8192^3 a stage takes 1,039 cycles where
+// its matrix instructions alone are 1,024 (1,922 TFLOP/s, 572 us); at 8192 x 2048
+// x 8192, 154 us, 14 rounds of tiles where 13.47 are needed, and 8 us of beginning
+// and end.
 template <int CG, bool A_MN, bool B_MN, Kind KIND>
 __global__ void __launch_bounds__(kProductThreads, 1)
     linear_product_kernel(const __grid_constant__ ProductArgs a) {
@@ -390,6 +395,8 @@ __global__ void __launch_bounds__(kProductThreads, 1)
       mbar_init(&free_[b], kEpilogueWarps * CG);
     }
     mbar_init_fence();
+  }
+  if (threadIdx.x == 64) {
     prefetch_map(&a.a);
     prefetch_map(&a.b);
   }
@@ -1156,9 +1163,11 @@ cudaError_t launch_product(Product p, const Plan& plan, bool late, Space* space,
 // y for at most 16 rows of x (tokens of generation): W is read once and nothing
 // else counts, so this is bound by HBM bandwidth.  A warp takes 16 rows of W, a
 // block's 8 warps share out the columns, and the warp-level matrix instruction
-// (16 rows of W by 8 rows of x, 16 steps) adds up: tcgen05's tiles of 128 rows
-// of x, brought through shared memory, took 33 us where this takes 21 (32 x 4096
-// x 11008).  A lane's 16-byte load is 8 neighbours of one row; which steps of
+// (16 rows of W by 8 rows of x, 16 steps) adds up.  4096 x 11008, calls in a row
+// over cold weights: 1 row 16.2 us (5.6 TB/s; fp32 multiply-adds instead of
+// matrix instructions were level there and 7 times slower at 8), 8 rows 17.8, 16
+// rows 21.2; tcgen05's tiles, brought through shared memory, 21.3 for any number
+// up to 32, so they take over at 17.  A lane's 16-byte load is 8 neighbours of one row; which steps of
 // the reduction an instruction's operands belong to does not matter as long as
 // W's and x's agree, so the vectors are its operands as they are.  All loads of
 // 64 or 128 columns are in flight at once; x comes from L1.  The shares are
