@@ -457,7 +457,9 @@ typedef struct {
  *   seed        of the rounding; unused with fp32 moments.
  * Lists of any length take one launch per 384 tensors.  Tensors of no elements
  * are skipped.  Any alignment of the element type is taken; tensors whose
- * buffers are all 16-byte aligned (8 for 8-bit codes) go in 16-byte accesses.
+ * buffers all begin the same number of elements (0 to 7) past a 16-byte boundary,
+ * as where all are packed in flat vectors alike, go in 16-byte accesses (8-bit
+ * codes that begin on an 8-byte boundary, at a lower rate unless that number is 0).
  * Errors: ZERO_E_SHAPE, ZERO_E_NULLPTR, ZERO_E_LAYOUT (unknown flags),
  * ZERO_E_HPARAM, ZERO_E_STEP, ZERO_E_ALIGN, ZERO_E_ALIAS (within a tensor:
  * master, m, v, param, grad or scales overlap), ZERO_E_LAUNCH, ZERO_E_DEVICE.

@@ -19,7 +19,8 @@ def cut(flat, sizes):
 
 class Case:
     """A list of tensors on the host and the GPU; flat=True packs every buffer (so that
-    tensors start at any element), else each has an allocation of its own."""
+    tensors start at any element), "codes apart" all but the codes, else each has an
+    allocation of its own."""
 
     def __init__(self, sizes, eight, f32, flat, seed=0, params=True):
         rng = np.random.default_rng(seed)
@@ -41,10 +42,10 @@ class Case:
             self.m = np.concatenate([o.decode(*q, 4) for q in self.mq] or [np.zeros(0, np.float32)])
             self.v = np.concatenate([o.decode(*q, 5) for q in self.vq] or [np.zeros(0, np.float32)])
 
-        def dev(x, dtype=None):
+        def dev(x, dtype=None, packed=bool(flat)):
             t = torch.from_numpy(np.ascontiguousarray(x)).cuda()
             t = t if dtype is None else t.to(dtype)
-            return cut(t, sizes) if flat else [p.clone() for p in cut(t, sizes)]
+            return cut(t, sizes) if packed else [p.clone() for p in cut(t, sizes)]
 
         self.dg = dev(self.g, None if f32 else torch.bfloat16)
         self.dw = dev(self.w)
@@ -52,7 +53,8 @@ class Case:
         kw = {}
         if eight:
             cat = lambda q, k, z: np.concatenate([x[k] for x in q] or [np.zeros(0, z)])  # noqa: E731
-            self.dm, self.dv = dev(cat(self.mq, 0, np.uint8)), dev(cat(self.vq, 0, np.uint8))
+            self.dm, self.dv = (dev(cat(q, 0, np.uint8), packed=flat is True)
+                                for q in (self.mq, self.vq))
             self.dms = [torch.from_numpy(s).cuda() for _, s in self.mq]
             self.dvs = [torch.from_numpy(s).cuda() for _, s in self.vq]
             kw = dict(m_scale=self.dms, v_scale=self.dvs)
@@ -110,6 +112,21 @@ def test_steps(eight, f32, flat):
     case = Case(SIZES, eight, f32, flat)
     case.step(t=7, seed=123)
     case.step(t=8, seed=2 ** 32 - 1, scale=0.37)
+
+
+@pytest.mark.parametrize("eight", [False, True])
+@pytest.mark.parametrize("f32", [False, True])
+def test_every_start_within_16_bytes(eight, f32):
+    """Tensors that begin 0 to 7 elements past a 16-byte boundary, from shorter than that to
+    several tiles."""
+    sizes = [2049] * 9 + [1, 6, 7, 257, 255, 1025, 513, 33, 4099]
+    starts = np.cumsum([0] + sizes)
+    assert set(starts[:9] % 8) == set(range(8))
+    case = Case(sizes, eight, f32, "codes apart")
+    case.step(t=7, seed=9)
+    case.step(t=8, seed=10, scale=0.37)
+    case = Case(sizes, eight, f32, "codes apart", params=False)
+    case.step(t=7, seed=9)
 
 
 @pytest.mark.parametrize("eight", [False, True])
