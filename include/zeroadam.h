@@ -330,10 +330,10 @@ typedef struct {
  *   workspace   device memory of zero_linear_workspace bytes,
  *               16-byte aligned (NULL where that is 0), free again once the
  *               call's work has run.
- * rows = 0 is valid and launches nothing (matrices of no rows may be NULL).  Any alignment of 2 bytes and any
- * pitch is taken; matrices whose base is 16-byte aligned and whose pitch is a
- * multiple of 8 are read in place by the TMA engine, others are laid out anew
- * in the workspace first.  Results do not depend on the run: every sum has a
+ * rows = 0 is valid and launches nothing (matrices of no rows may be NULL).  Any
+ * alignment of 2 bytes and any pitch is taken; x and w whose base is 16-byte
+ * aligned and whose pitch is a multiple of 8, and a bias on a 16-byte boundary,
+ * are read in place, others are laid out anew in the workspace first.  Results do not depend on the run: every sum has a
  * fixed order for given sizes.
  * Errors: ZERO_E_NULLPTR, ZERO_E_SHAPE, ZERO_E_LAYOUT (unknown act),
  * ZERO_E_ALIGN, ZERO_E_ALIAS (y or pre overlaps another matrix),
@@ -374,8 +374,9 @@ int zero_linear_backward(const zero_linear_t* shape, const void* dy, const void*
 
 /* Bytes of workspace that suffice for zero_linear_forward, or with
  * ZERO_LINEAR_BACKWARD for zero_linear_backward, of this shape; 0 for a forward
- * of at most 16 rows.  ZERO_LINEAR_ALIGNED: every matrix's base will be on a
- * 16-byte boundary and every pitch a multiple of 8, so none is laid out anew
+ * of at most 16 rows.  ZERO_LINEAR_ALIGNED: every matrix's base, and a
+ * forward's bias, will be on a 16-byte boundary and every pitch a multiple of 8,
+ * so none is laid out anew
  * (a call whose matrices are not so needs the figure without it).
  * ZERO_LINEAR_PLAIN: a backward with ZERO_ACT_NONE.  Negative: the ZERO_E_* code
  * of a bad shape or flag.  Host only. */

@@ -135,6 +135,24 @@ def test_pitches_and_offsets(shape, pitch, offset):
         assert bool((t.as_strided((offset,), (1,), 0) == 7.0).all())
 
 
+@pytest.mark.parametrize("shape", [(3, 128, 64), (200, 128, 264), (260, 72, 131)])
+def test_a_bias_at_any_address(shape):
+    """The bias alone is off a 16-byte boundary (a vector among others in a flat one); the
+    workspace holds its copy and no more."""
+    m, k, n = shape
+    x, w, res = normal((m, k), 1.0, 1), normal((n, k), 0.1, 2), normal((m, n), 1.0, 3)
+    moved = normal((1, n), 1.0, 4, offset=3)[0]
+    bias = moved.clone()
+    assert moved.data_ptr() % 16 == 6 and bias.data_ptr() % 16 == 0
+    y, pre, y2, pre2 = (empty((m, n)) for _ in range(4))
+    za.zero_linear_forward(x, w, y, bias=bias, act=2, residual=res, pre=pre)
+    need = za.zero_linear_workspace(m, k, n)
+    ws = torch.full((need + 256,), 77, dtype=torch.uint8, device="cuda")
+    za.zero_linear_forward(x, w, y2, bias=moved, act=2, residual=res, pre=pre2, workspace=ws[:need])
+    assert torch.equal(y, y2) and torch.equal(pre, pre2)
+    assert bool((ws[need:] == 77).all())
+
+
 def test_each_output_alone():
     m, k, n = 70, 130, 90
     x, w, dy, pre = (normal(s, 1.0, i) for i, s in enumerate([(m, k), (n, k), (m, n), (m, n)]))

@@ -61,7 +61,7 @@ int check_matrix(const Matrix& m) {
   return misaligned(m.base, static_cast<uintptr_t>(m.esize)) ? ZERO_E_ALIGN : ZERO_OK;
 }
 
-// Whether the TMA engine can read a matrix where it lies (ZERO_LINEAR_ALIGNED).
+// Whether the kernel can read a matrix, or a bias, where it lies (ZERO_LINEAR_ALIGNED).
 bool in_place(const Matrix& m) {
   return m.base == nullptr || (!misaligned(m.base, 16) && (m.rows <= 1 || m.ld % 8 == 0));
 }
@@ -116,7 +116,8 @@ int zero_linear_forward(const zero_linear_t* shape, const void* x, const void* w
     if (share(my, *m) || share(mp, *m)) return ZERO_E_ALIAS;
   if (share(my, mp) || share(mp, mr)) return ZERO_E_ALIAS;
   if (!(residual == y && s.ldr == s.ldy) && share(my, mr)) return ZERO_E_ALIAS;
-  const int64_t need = linear_workspace(s, in_place(mx) && in_place(mw) ? ZERO_LINEAR_ALIGNED : 0);
+  const int64_t need = linear_workspace(
+      s, in_place(mx) && in_place(mw) && in_place(mb) ? ZERO_LINEAR_ALIGNED : 0);
   if ((rc = check_workspace(workspace, workspace_bytes, need)) != ZERO_OK) return rc;
   const Matrix ms{need > 0 ? workspace : nullptr, 1, need, need, 1};
   for (const Matrix* m : {&mx, &mw, &mb, &mr, &mp, &my})

@@ -252,7 +252,8 @@ struct EpiloguePart {
       bulk_commit();
     }
   }
-  // 32 columns of fp32 as they are.
+  // 32 columns of fp32 as they are, in the room of both slots: no send() may
+  // follow (fp32 outputs have none, and split tiles are a unit's last).
   __device__ __forceinline__ void send_sums(const CUtensorMap* map, uint8_t* staging,
                                             const float v[32], int x, int y, int z, bool sum,
                                             int lane) {
@@ -1449,8 +1450,9 @@ int64_t linear_workspace(const zero_linear_t& s, int32_t flags) {
   const bool in_place = (flags & ZERO_LINEAR_ALIGNED) != 0;
   const int64_t x = in_place ? 0 : copy_bytes(Stored(nullptr, s.rows, s.in, 0));
   const int64_t w = in_place ? 0 : copy_bytes(Stored(nullptr, s.out, s.in, 0));
+  const int64_t bias = in_place ? 0 : copy_bytes(Stored(nullptr, 1, s.out, 0));
   if ((flags & ZERO_LINEAR_BACKWARD) == 0)
-    return s.rows <= kFewRows ? 0 : x + w + round_up(plan_forward(s).part_bytes(), 256);
+    return s.rows <= kFewRows ? 0 : x + w + bias + round_up(plan_forward(s).part_bytes(), 256);
   const bool dz = !in_place || (flags & ZERO_LINEAR_PLAIN) == 0;
   // the two products' parts, side by side; either may be wanted alone
   const BackwardPlan both = plan_backward(s, true, true), one = plan_backward(s, true, false),
@@ -1482,8 +1484,12 @@ cudaError_t launch_linear_forward(const LinearForwardLaunch& L) {
   if (s.rows <= kFewRows) return launch_few_rows(p, L.stream);
   Space space{static_cast<char*>(L.workspace)};
   Chain chain{L.stream};
-  Stored* const both[2] = {&p.a, &p.b};
-  cudaError_t e = prepare(both, 2, DbiasArgs{}, &space, &chain);
+  // (where only the bias is out of place, its copy costs a launch; taken element by
+  // element it would take the whole epilogue with it)
+  Stored bias{L.bias, 1, s.out, 0};
+  Stored* const all[3] = {&p.a, &p.b, &bias};
+  cudaError_t e = prepare(all, 3, DbiasArgs{}, &space, &chain);
+  p.e.bias = bias.p;
   Pending w;
   if (e == cudaSuccess)
     e = launch_product(p, plan_forward(s), false, &space, L.withhold, &chain, &w);

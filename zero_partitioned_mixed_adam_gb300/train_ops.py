@@ -78,7 +78,7 @@ def _vector(name, t, n, dtypes=_BF16):
 def _linear_workspace(shape, flags, bases, pitches, workspace, device, stream):
     """The caller's workspace, or one from PyTorch's allocator that is kept from reuse
     until `stream` is past the call; and its bytes.  bases, pitches: those of the matrices
-    that the products read, or-ed together."""
+    (and the bias) that the products read, or-ed together."""
     if workspace is not None:
         return workspace, workspace.numel() * workspace.element_size()
     if bases % 16 == 0 and pitches % 8 == 0:
@@ -98,7 +98,7 @@ def _linear_workspace(shape, flags, bases, pitches, workspace, device, stream):
 def zero_linear_workspace(rows: int, width_in: int, width_out: int, backward: bool = False,
                           aligned: bool = False) -> int:
     """Bytes of workspace that suffice for a linear map of these sizes; aligned: of matrices
-    that all start on 16-byte boundaries and have pitches that are multiples of 8."""
+    (and a bias) that all start on 16-byte boundaries and have pitches that are multiples of 8."""
     flags = (ZERO_LINEAR_BACKWARD if backward else 0) | (ZERO_LINEAR_ALIGNED if aligned else 0)
     rc = _lib.zero_linear_workspace(ctypes.byref(ZeroLinear(rows, width_in, width_out)), flags)
     if rc < 0:
@@ -126,9 +126,10 @@ def zero_linear_forward(x, w, y, *, bias=None, act: int = ZERO_ACT_NONE, residua
         s.ldr = _matrix("residual", residual, rows, out)
     if pre is not None:
         s.ldp = _matrix("pre", pre, rows, out)
-    px, pw = x.data_ptr(), w.data_ptr()
-    workspace, nbytes = _linear_workspace(s, 0, px | pw, s.ldx | s.ldw, workspace, y.device, stream)
-    rc = _lib.zero_linear_forward(ctypes.byref(s), px, pw, _addr(bias), act,
+    px, pw, pb = x.data_ptr(), w.data_ptr(), _addr(bias)
+    workspace, nbytes = _linear_workspace(s, 0, px | pw | (pb or 0), s.ldx | s.ldw, workspace,
+                                          y.device, stream)
+    rc = _lib.zero_linear_forward(ctypes.byref(s), px, pw, pb, act,
                                   _addr(residual), _addr(pre), _addr(y), _addr(workspace), nbytes,
                                   _stream_handle(stream))
     if rc != ZERO_OK:
