@@ -135,6 +135,46 @@ def test_pitches_and_offsets(shape, pitch, offset):
         assert bool((t.as_strided((offset,), (1,), 0) == 7.0).all())
 
 
+@pytest.mark.parametrize("n", [17, 23, 39, 40, 41, 65, 71, 103, 135, 161, 255, 259, 263, 519])
+@pytest.mark.parametrize("gap,offset", [(1, 0), (2, 3), (8, 5)])
+def test_rows_at_any_address(n, gap, offset):
+    """Outputs and what is added to them, in place too, at every distance from 16-byte
+    boundaries, a warp's columns ending anywhere: the aligned matrices' results, and what
+    lies around the rows untouched."""
+    m, k = 165, 72
+    kw = dict(pitch=n + gap, offset=offset)
+
+    def moved(t):
+        out = torch.full((t.shape[0] * kw["pitch"] + 64,), 7.0, dtype=t.dtype, device="cuda")
+        view = out.as_strided(t.shape, (kw["pitch"], 1), offset)
+        view.copy_(t)
+        return out, view
+
+    def untouched(out, view):
+        keep = torch.ones(out.shape, dtype=torch.bool, device="cuda")
+        keep.as_strided(view.shape, view.stride(), offset).fill_(False)
+        return bool((out[keep] == 7.0).all())
+
+    x, w = normal((m, k), 1.0, 1), normal((n, k), 0.1, 2)
+    even = dict(pitch=-n % 8)
+    y, pre, bias = normal((m, n), 1.0, 3, **even), empty((m, n), **even), normal((1, n), 1.0, 5)[0]
+    (ybuf, yv), (pbuf, pv) = moved(y), moved(pre)
+    za.zero_linear_forward(x, w, y, bias=bias, act=2, residual=y, pre=pre)
+    za.zero_linear_forward(x, w, yv, bias=bias, act=2, residual=yv, pre=pv)
+    assert torch.equal(yv, y) and torch.equal(pv, pre)
+    assert untouched(ybuf, yv) and untouched(pbuf, pv)
+    # n as the width in: dx times a slope, dw added to what is there
+    dy, wt, xt = normal((m, k), 1.0, 6), normal((k, n), 0.1, 7, **even), normal((m, n), 1.0, 8, **even)
+    for dtype in (BF, F32):
+        dx, dw = empty((m, n), **even), empty((k, n), dtype, **even)
+        dw.copy_(normal((k, n), 1.0, 9))
+        (dxbuf, dxv), (dwbuf, dwv), (_, before) = moved(dx), moved(dw), moved(xt)
+        za.zero_linear_backward(dy, xt, wt, dx=dx, dw=dw, act_in=2, pre_in=xt, accumulate=True)
+        za.zero_linear_backward(dy, xt, wt, dx=dxv, dw=dwv, act_in=2, pre_in=before, accumulate=True)
+        assert torch.equal(dxv, dx) and torch.equal(dwv, dw), dtype
+        assert untouched(dxbuf, dxv) and untouched(dwbuf, dwv)
+
+
 @pytest.mark.parametrize("shape", [(3, 128, 64), (200, 128, 264), (260, 72, 131)])
 def test_a_bias_at_any_address(shape):
     """The bias alone is off a 16-byte boundary (a vector among others in a flat one); the

@@ -8,6 +8,7 @@
 // The tensor cores take either way (K-major, MN-major) from tiles that TMA
 // brings into shared memory, so no operand is transposed in memory.
 #include <mutex>
+#include <type_traits>
 
 #include "internal.h"
 #include "linear_epilogue.cuh"
@@ -124,64 +125,91 @@ enum Kind {
 __device__ __forceinline__ int staged(int r, int q) { return r * 32 + ((q ^ (r & 7)) * 4); }
 
 // Any layout, and the edges: a lane takes one column, 8 rows at a time so that
-// their loads are under way together.
+// their loads are under way together; whole eights have code of their own, without
+// a predicate a row (fp32 dw of 8192 x 2047, 4096 rows: 150 us, else 173).
 template <Kind KIND>
 __device__ __noinline__ void epilogue_scalar(const Epilogue& e, const float* mine, int64_t row0,
                                              int64_t col0, int64_t rows, int64_t cols, int lane) {
   const int64_t j = col0 + lane;
   if (j >= cols) return;
   const int n = rows - row0 < 32 ? static_cast<int>(rows - row0) : 32;
+  const bool accumulate = e.accumulate != 0;
+  const int act = KIND == kForward ? e.act : e.slope_act;
+  const int64_t ldo = e.ldo, ldp = e.ldp;
   const uint16_t* from = nullptr;
   int64_t from_pitch = 0;
   float bias = 0.0f;
-  const bool add = KIND == kForward || e.accumulate;
   if constexpr (KIND == kForward) {
     from = e.residual;
     from_pitch = e.ldr;
     if (e.bias != nullptr) bias = bf16_at(e.bias + j);
   } else if constexpr (KIND == kGradient) {
-    from = e.accumulate ? static_cast<const uint16_t*>(e.out) : e.slope_of;
-    from_pitch = e.accumulate ? e.ldo : e.lds;
+    from = accumulate ? static_cast<const uint16_t*>(e.out) : e.slope_of;
+    from_pitch = accumulate ? ldo : e.lds;
   }
   if (from != nullptr) from += row0 * from_pitch + j;
-  float* out32 = static_cast<float*>(e.out) + row0 * e.ldo + j;
-  uint16_t* out16 = static_cast<uint16_t*>(e.out) + row0 * e.ldo + j;
-  uint16_t* pre = KIND == kForward && e.pre != nullptr ? e.pre + row0 * e.ldp + j : nullptr;
-#pragma unroll 1
-  for (int r = 0; r < n; r += 8) {
-    float x[8], y[8];
+  float* out32 = static_cast<float*>(e.out) + row0 * ldo + j;
+  uint16_t* out16 = static_cast<uint16_t*>(e.out) + row0 * ldo + j;
+  uint16_t* pre = KIND == kForward && e.pre != nullptr ? e.pre + row0 * ldp + j : nullptr;
+  const auto rows8 = [&](int r, auto all) {  // all: the 8 rows are there
+    const auto each = [&](auto* p, int64_t pitch, auto f) {
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      y[k] = 0.0f;
-      if (r + k < n) {
-        if (KIND == kFloat && e.accumulate) y[k] = out32[(r + k) * e.ldo];
-        if (KIND != kFloat && from != nullptr) y[k] = bf16_at(from + (r + k) * from_pitch);
-      }
-      x[k] = mine[staged(r + k, lane / 4) + lane % 4] + bias;
-    }
+      for (int k = 0; k < 8; ++k, p += pitch)
+        if (all.value || r + k < n) f(k, p);
+    };
+    float x[8], y[8] = {};
+    if (KIND == kFloat && accumulate) each(out32, ldo, [&](int k, float* p) { y[k] = *p; });
+    if (KIND != kFloat && from != nullptr)
+      each(from, from_pitch, [&](int k, const uint16_t* p) { y[k] = bf16_at(p); });
+#pragma unroll
+    for (int k = 0; k < 8; ++k) x[k] = mine[32 * r + staged(k, lane / 4) + lane % 4] + bias;
     if (KIND == kForward) {
-      if (pre != nullptr) {
-#pragma unroll
-        for (int k = 0; k < 8; ++k)
-          if (r + k < n) pre[(r + k) * e.ldp] = to_bf16(x[k]);
-      }
-      act_value8(x, e.act);
+      if (pre != nullptr) each(pre, ldp, [&](int k, uint16_t* p) { *p = to_bf16(x[k]); });
+      act_value8(x, act);
     }
-    if (KIND == kGradient && !add && from != nullptr) {
+    if (KIND == kGradient && !accumulate && from != nullptr) {
 #pragma unroll
-      for (int k = 0; k < 8; ++k) x[k] *= act_slope(y[k], e.slope_act);
-    } else if (KIND == kFloat || from != nullptr) {
+      for (int k = 0; k < 8; k += 2) {
+        if (act == ZERO_ACT_GELU) times_slope2<ZERO_ACT_GELU>(x[k], x[k + 1], y[k], y[k + 1]);
+        else if (act == ZERO_ACT_SILU) times_slope2<ZERO_ACT_SILU>(x[k], x[k + 1], y[k], y[k + 1]);
+        else if (act == ZERO_ACT_RELU) times_slope2<ZERO_ACT_RELU>(x[k], x[k + 1], y[k], y[k + 1]);
+      }
+    } else if (KIND == kFloat ? accumulate : from != nullptr) {
 #pragma unroll
       for (int k = 0; k < 8; ++k) x[k] += y[k];
     }
-#pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      if (r + k >= n) break;
-      if (KIND == kFloat) out32[(r + k) * e.ldo] = x[k];
-      else out16[(r + k) * e.ldo] = to_bf16(x[k]);
-    }
+    if (KIND == kFloat) each(out32, ldo, [&](int k, float* p) { *p = x[k]; });
+    else each(out16, ldo, [&](int k, uint16_t* p) { *p = to_bf16(x[k]); });
+    out32 += 8 * ldo;
+    out16 += 8 * ldo;
+    if (pre != nullptr) pre += 8 * ldp;
+    if (from != nullptr) from += 8 * from_pitch;
+  };
+#pragma unroll 1
+  for (int r = 0; r < n; r += 8) {
+    if (r + 8 <= n) rows8(r, std::true_type{});
+    else rows8(r, std::false_type{});
   }
 }
+
+// 32 columns of fp32 as they are, in the room of both slots: no send() may
+  // follow (fp32 outputs have none, and split tiles are a unit's last).
+  __device__ __forceinline__ void send_sums(const CUtensorMap* map, uint8_t* staging,
+                                            const float v[32], int x, int y, int z, bool sum,
+                                            int lane) {
+    if (lane == 0) bulk_wait_read<0>();
+    __syncwarp();
+#pragma unroll
+    for (int q = 0; q < 8; ++q)
+      *reinterpret_cast<float4*>(staging + 4 * staged(lane, q)) =
+          make_float4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
+    fence_async_shared();
+    __syncwarp();
+    if (lane == 0) {
+      tile_store(map, staging, x, y, z, sum);
+      bulk_commit();
+    }
+  }
 
 // A 32 x 32 part, a row a lane, through shared memory and out by TMA, which takes
 // the addresses and the edges off the lanes and adds fp32 gradients to what is
@@ -252,24 +280,6 @@ struct EpiloguePart {
       bulk_commit();
     }
   }
-  // 32 columns of fp32 as they are, in the room of both slots: no send() may
-  // follow (fp32 outputs have none, and split tiles are a unit's last).
-  __device__ __forceinline__ void send_sums(const CUtensorMap* map, uint8_t* staging,
-                                            const float v[32], int x, int y, int z, bool sum,
-                                            int lane) {
-    if (lane == 0) bulk_wait_read<0>();
-    __syncwarp();
-#pragma unroll
-    for (int q = 0; q < 8; ++q)
-      *reinterpret_cast<float4*>(staging + 4 * staged(lane, q)) =
-          make_float4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
-    fence_async_shared();
-    __syncwarp();
-    if (lane == 0) {
-      tile_store(map, staging, x, y, z, sum);
-      bulk_commit();
-    }
-  }
   __device__ __forceinline__ static void plus(float v[32], const uint4 w[4]) {
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
@@ -315,6 +325,183 @@ struct EpiloguePart {
       }
       send(&a.out, staging, v, col, row, lane);
     }
+  }
+};
+
+// The same for bf16 matrices that TMA cannot write: rows begin anywhere (odd
+// pitches, offsets).  A lane's row begins s elements (0 to 7) past a 16-byte
+// boundary in every part of a tile, as parts are 32 columns and a warp's lie side
+// by side; so a part is moved up by s, behind the last s columns of the part to
+// its left, and goes in aligned vectors, 4 lanes a row.  What is left at both ends
+// of a warp's columns goes in pieces of 2, 4 and 8 bytes.  8192 x 768 -> 50257: 462
+// us (50304 columns, by TMA: 376; a column a lane, 2 bytes at a time: 909); with
+// bias and residual 895 (2,562 so); what bounds it is the warps' instructions, some
+// 250 a part.
+template <Kind KIND>
+struct RowsPart {
+  const uint16_t *from, *bias;
+  uint16_t *out, *pre;
+  int64_t from_pitch, out_pitch, pre_pitch;
+  int32_t act;
+  bool add;
+  uint32_t in[20];  // what the part reads, from the vector on that its first column is in
+  float b;          // the lane's column's bias
+  uint4 before_out, before_pre;  // the part to the left: its last 8 columns
+
+  __device__ __forceinline__ explicit RowsPart(const Epilogue& e)
+      : from(nullptr), bias(nullptr), out(static_cast<uint16_t*>(e.out)), pre(nullptr),
+        from_pitch(0), out_pitch(e.ldo), pre_pitch(0), act(ZERO_ACT_NONE), add(true), b(0.0f) {
+    if constexpr (KIND == kForward) {
+      from = e.residual;
+      from_pitch = e.ldr;
+      bias = e.bias;
+      act = e.act;
+      pre = e.pre;
+      pre_pitch = e.ldp;
+    } else {
+      add = e.accumulate != 0;
+      from = add ? out : e.slope_of;
+      from_pitch = add ? out_pitch : e.lds;
+      act = e.slope_act;
+    }
+  }
+  // Elements from the 16-byte boundary before p to it.
+  __device__ __forceinline__ static int past(const uint16_t* p) {
+    return static_cast<int>(reinterpret_cast<uintptr_t>(p) / 2 % 8);
+  }
+  // o: elements `first` (0 to 8) on of v.
+  template <int N, int M>
+  __device__ __forceinline__ static void moved(uint32_t (&v)[N], int first, uint32_t (&o)[M]) {
+#pragma unroll
+    for (int k = 4; k >= 1; k /= 2)
+#pragma unroll
+      for (int i = 0; i < M + k && i + k < N; ++i) v[i] = (first / 2) & k ? v[i + k] : v[i];
+#pragma unroll
+    for (int i = 0; i < M; ++i)
+      o[i] = __funnelshift_r(v[i], i + 1 < N ? v[i + 1] : 0u, 16 * (first & 1));
+  }
+  // Asks for what the part at `col` reads; the warp's columns are [first, end).
+  __device__ __forceinline__ void ask(int64_t row, int64_t col, bool mine, int64_t first,
+                                      int64_t end, int lane) {
+    if (KIND == kForward && bias != nullptr)
+      b = col + lane < end ? bf16_at(bias + col + lane) : 0.0f;
+    if (from == nullptr || !mine) return;
+    const uint16_t* at = from + row * from_pitch + col;
+    const int s = past(at);
+    at -= s;
+    const int low = static_cast<int>(first - col) + s, high = static_cast<int>(end - col) + s;
+    const int stop = high < 32 + s ? high : 32 + s;
+#pragma unroll
+    for (int k = 0; k < 5; ++k) {
+      uint4 x = make_uint4(0, 0, 0, 0);
+      if (8 * k >= low && 8 * k + 8 <= high) {
+        x = *reinterpret_cast<const uint4*>(at + 8 * k);
+      } else if (8 * k < stop) {
+        uint32_t w[4] = {0, 0, 0, 0};
+#pragma unroll
+        for (int q = 0; q < 8; ++q)
+          if (8 * k + q >= low && 8 * k + q < stop)
+            w[q / 2] |= static_cast<uint32_t>(at[8 * k + q]) << (16 * (q % 2));
+        x = make_uint4(w[0], w[1], w[2], w[3]);
+      }
+      in[4 * k] = x.x; in[4 * k + 1] = x.y; in[4 * k + 2] = x.z; in[4 * k + 3] = x.w;
+    }
+  }
+  // 32 columns into rows of p, from `col` on.
+  __device__ __forceinline__ void send(uint16_t* p, int64_t pitch, uint4& before, uint4* staging,
+                                       const float x[32], int64_t row0, int64_t rows, int64_t col,
+                                       int64_t first, int64_t end, int lane) {
+    uint16_t* at = p + (row0 + lane) * pitch + col;
+    const int s = past(at);
+    uint32_t v[25], o[20];
+    v[0] = before.x; v[1] = before.y; v[2] = before.z; v[3] = before.w;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) v[4 + i] = bf16x2_bits(x[2 * i], x[2 * i + 1]);
+#pragma unroll
+    for (int i = 20; i < 25; ++i) v[i] = 0;
+    before = make_uint4(v[16], v[17], v[18], v[19]);
+    moved(v, 8 - s, o);
+    __syncwarp();  // the part before has been read
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+      staging[lane * 4 + (q ^ (lane / 2 % 4))] =
+          make_uint4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
+    __syncwarp();
+    const int low = static_cast<int>(first - col), high = static_cast<int>(end - col);
+    const int i0 = lane / 4, q = lane % 4, n = rows - row0 < 32 ? static_cast<int>(rows - row0) : 32;
+    uint16_t* to = p + (row0 + i0) * pitch + col + 8 * q;
+#pragma unroll
+    for (int k = 0; k < 4; ++k, to += 8 * pitch) {
+      const int c = 8 * q - past(to);
+      if (8 * k + i0 < n && c >= low && c + 8 <= high)
+        *reinterpret_cast<uint4*>(to - past(to)) = staging[(8 * k + i0) * 4 + (q ^ (i0 / 2 % 4))];
+    }
+    if (lane >= n) return;
+    at -= s;
+    if (low == 0 && s > 0) {
+      int j = s;
+      if (j & 1) {
+        const uint32_t w = j == 1 ? o[0] : j == 3 ? o[1] : j == 5 ? o[2] : o[3];
+        at[j++] = static_cast<uint16_t>(w >> 16);
+      }
+      if (j & 2) {
+        *reinterpret_cast<uint32_t*>(at + j) = j == 2 ? o[1] : o[3];
+        j += 2;
+      }
+      if (j & 4) *reinterpret_cast<uint2*>(at + 4) = make_uint2(o[2], o[3]);
+    }
+    const int left = (s + high) % 8;
+    if (high <= 32 && left > 0) {
+      const int k = (s + high) / 8;
+      const uint4 w = k < 4 ? staging[lane * 4 + (k ^ (lane / 2 % 4))]
+                            : make_uint4(o[16], o[17], o[18], o[19]);
+      at += 8 * k;
+      if (left & 4) *reinterpret_cast<uint2*>(at) = make_uint2(w.x, w.y);
+      if (left & 2) *reinterpret_cast<uint32_t*>(at + (left & 4)) = left & 4 ? w.z : w.x;
+      if (left & 1)
+        at[left - 1] = static_cast<uint16_t>(left == 1 ? w.x : left == 3 ? w.y : left == 5 ? w.z : w.w);
+    }
+  }
+  template <typename F>
+  __device__ __forceinline__ static void pairs(float x[32], const uint32_t w[16], F f) {
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+      f(x[2 * i], x[2 * i + 1], __uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
+  }
+  // At least 8 columns are the warp's.
+  __device__ __forceinline__ void put(float* mine, float x[32], int64_t row0, int64_t rows,
+                                      int64_t col, int64_t first, int64_t end, int lane) {
+    uint4* staging = reinterpret_cast<uint4*>(mine);
+    if constexpr (KIND == kForward) {
+      if (bias != nullptr) {
+#pragma unroll
+        for (int i = 0; i < 32; ++i) x[i] += __shfl_sync(0xffffffffu, b, i);
+      }
+      if (pre != nullptr)
+        send(pre, pre_pitch, before_pre, staging, x, row0, rows, col, first, end, lane);
+      if (act == ZERO_ACT_GELU) EpiloguePart<KIND>::template activate<ZERO_ACT_GELU>(x);
+      else if (act == ZERO_ACT_SILU) EpiloguePart<KIND>::template activate<ZERO_ACT_SILU>(x);
+      else if (act == ZERO_ACT_RELU) EpiloguePart<KIND>::template activate<ZERO_ACT_RELU>(x);
+    }
+    if (from != nullptr) {
+      uint32_t w[16];
+      moved(in, past(from + (row0 + lane) * from_pitch + col), w);
+      if (add)
+        pairs(x, w, [](float& a, float& b, float c, float d) { a += c; b += d; });
+      else if (act == ZERO_ACT_GELU)
+        pairs(x, w, [](float& a, float& b, float c, float d) {
+          times_slope2<ZERO_ACT_GELU>(a, b, c, d);
+        });
+      else if (act == ZERO_ACT_SILU)
+        pairs(x, w, [](float& a, float& b, float c, float d) {
+          times_slope2<ZERO_ACT_SILU>(a, b, c, d);
+        });
+      else if (act == ZERO_ACT_RELU)
+        pairs(x, w, [](float& a, float& b, float c, float d) {
+          times_slope2<ZERO_ACT_RELU>(a, b, c, d);
+        });
+    }
+    send(out, out_pitch, before_out, staging, x, row0, rows, col, first, end, lane);
   }
 };
 
@@ -365,7 +552,8 @@ __device__ __forceinline__ bool wait_for_chain(uint64_t* bar, uint32_t parity, i
 // its matrix instructions alone are 1,024 (1,922 TFLOP/s, 572 us); at 8192 x 2048
 // x 8192, 154 us, 14 rounds of tiles where 13.47 are needed, and 8 us of beginning
 // and end.
-template <int CG, bool A_MN, bool B_MN, Kind KIND>
+// ROWS: D, pre or what is read with them lies where TMA cannot take it.
+template <int CG, bool A_MN, bool B_MN, Kind KIND, bool ROWS>
 __global__ void __launch_bounds__(kProductThreads, 1)
     linear_product_kernel(const __grid_constant__ ProductArgs a) {
   using Shape = ProductShape<CG>;
@@ -528,9 +716,17 @@ __global__ void __launch_bounds__(kProductThreads, 1)
   } else {
     const int quarter = warp % 4, half = (warp - 2) / 4;
     float* mine = staging + (warp - 2) * 32 * 32;
-    EpiloguePart<KIND> part(a.e);
+    std::conditional_t<ROWS, RowsPart<KIND>, EpiloguePart<KIND>> part(a.e);
     const bool vec = a.e.vec != 0;
     const int bn = a.bn;
+    // The columns of a tile that are this warp's, 32 at a time: every other 32, or half
+    // of all.  Halves are what RowsPart needs; with them the gradient's reads of what
+    // is there are faster (8192 x 8192 x 128 times a slope: 99 us, else 121), the
+    // forward's writes slower (8192 x 128 x 8192: 58, else 52; plus a residual 105, 93).
+    constexpr bool kBeside = ROWS || KIND == kGradient;
+    const int c_first = 32 * half * (kBeside ? (bn / 32 + 1) / 2 : 1);
+    const int c_end = kBeside && half == 0 ? (bn / 32 + 1) / 2 * 32 : bn;
+    constexpr int c_step = kBeside ? 32 : 64;
     const int64_t rows = a.rows, cols = a.cols;
     const uint32_t lanes = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
     // This half of tensor memory has been read by the warp and may be written again.
@@ -549,25 +745,45 @@ __global__ void __launch_bounds__(kProductThreads, 1)
       const int64_t row0 = tile.row + rank * kBlockRows + quarter * 32;
       // (rows past the end are left out by the copy)
       const bool any = row0 < rows;
-      const bool fast = any && vec && tile.part < 0 && tile.col + bn <= cols;
+      const int64_t first = tile.col + c_first, end = tile.col + c_end < cols ? tile.col + c_end : cols;
+      const bool fast = any && tile.part < 0 &&
+                        (ROWS ? end - first >= 8 : vec && tile.col + bn <= cols);
       const bool mine_in = row0 + lane < rows;
+      const auto ask = [&](int c) {
+        if constexpr (ROWS) {
+          if (tile.col + c < end) part.ask(row0 + lane, tile.col + c, mine_in, first, end, lane);
+        } else {
+          part.ask(row0 + lane, tile.col + c, mine_in);
+        }
+      };
       // 32 columns from c on are summed up: on their way.
       const auto finish = [&](float x[32], int c) {
         const int64_t col0 = tile.col + c;
-        if (fast) {
+        if constexpr (ROWS) {
+          if (fast) {
+            if (col0 < end) part.put(mine, x, row0, rows, col0, first, end, lane);
+            return;
+          }
+        } else if (fast) {
           part.put(a, reinterpret_cast<uint8_t*>(mine), x, static_cast<int>(row0),
                    static_cast<int>(col0), lane);
           return;
         }
         if (!any || col0 >= cols) return;
         if (tile.part >= 0) {
-          part.send_sums(&a.parts, reinterpret_cast<uint8_t*>(mine), x, c,
-                         static_cast<int>(row0 - tile.row), tile.part, false, lane);
-        } else if (vec && col0 + 32 <= cols) {
-          part.ask(row0 + lane, col0, mine_in);
-          part.put(a, reinterpret_cast<uint8_t*>(mine), x, static_cast<int>(row0),
-                   static_cast<int>(col0), lane);
-        } else {
+          send_sums(&a.parts, reinterpret_cast<uint8_t*>(mine), x, c,
+                    static_cast<int>(row0 - tile.row), tile.part, false, lane);
+          return;
+        }
+        if constexpr (!ROWS) {
+          if (vec && col0 + 32 <= cols) {
+            part.ask(row0 + lane, col0, mine_in);
+            part.put(a, reinterpret_cast<uint8_t*>(mine), x, static_cast<int>(row0),
+                     static_cast<int>(col0), lane);
+            return;
+          }
+        }
+        {
           if (lane == 0) bulk_wait_read<0>();
           __syncwarp();
 #pragma unroll
@@ -589,8 +805,8 @@ __global__ void __launch_bounds__(kProductThreads, 1)
           tc_fence_after();
 #pragma unroll
           for (int i = 0; i < kParts; ++i) {
-            const int c = 32 * half + 64 * i;
-            if (c >= bn) break;
+            const int c = c_first + c_step * i;
+            if (c >= c_end) break;
 #pragma unroll
             for (int h = 0; h < 32; h += 16) {  // 16 at a time: 128 registers hold the sums
               uint32_t bits[16];
@@ -610,7 +826,7 @@ __global__ void __launch_bounds__(kProductThreads, 1)
         if (ok) {
 #pragma unroll
           for (int i = 0; i < kParts; ++i)
-            if (32 * half + 64 * i < bn) finish(sum[i], 32 * half + 64 * i);
+            if (c_first + c_step * i < c_end) finish(sum[i], c_first + c_step * i);
         }
       } else {
         const int b = n & 1;
@@ -620,23 +836,23 @@ __global__ void __launch_bounds__(kProductThreads, 1)
         tc_fence_after();
         const uint32_t from = lanes + b * Shape::kMaxCols;
         uint32_t bits[32];
-        if (32 * half < bn) {
-          tmem_load32(from + 32 * half, bits);
-          if (fast) part.ask(row0 + lane, tile.col + 32 * half, mine_in);
+        if (c_first < c_end) {
+          tmem_load32(from + c_first, bits);
+          if (fast) ask(c_first);
         } else {
           release(b);  // nothing of a tile this narrow is this warp's
         }
 #pragma unroll 1
-        for (int c = 32 * half; c < bn; c += 64) {
+        for (int c = c_first; c < c_end; c += c_step) {
           float x[32];
           tmem_load_wait();
 #pragma unroll
           for (int q = 0; q < 32; ++q) x[q] = __uint_as_float(bits[q]);
           // the next part's sums come while this one's are worked on
-          if (c + 64 < bn) tmem_load32(from + c + 64, bits);
+          if (c + c_step < c_end) tmem_load32(from + c + c_step, bits);
           else release(b);
           finish(x, c);
-          if (fast && c + 64 < bn) part.ask(row0 + lane, tile.col + c + 64, mine_in);
+          if (fast && c + c_step < c_end) ask(c + c_step);
         }
       }
     }
@@ -1062,12 +1278,12 @@ struct Pending {
   float* parts;
 };
 
-template <int CG, bool A_MN, bool B_MN, Kind KIND>
+template <int CG, bool A_MN, bool B_MN, Kind KIND, bool ROWS>
 cudaError_t launch_shape(const Product& p, Pending* w, Chain* chain) {
   ProductArgs& a = w->a;
   const Plan& plan = w->plan;
   const int bn = plan.bn;
-  auto kernel = linear_product_kernel<CG, A_MN, B_MN, KIND>;
+  auto kernel = linear_product_kernel<CG, A_MN, B_MN, KIND, ROWS>;
   static std::mutex mu;
   static bool configured[64] = {false};
   int dev = 0, sms = 0;
@@ -1113,8 +1329,12 @@ cudaError_t launch_join(const Pending& w, Chain* chain) {
 
 template <bool A_MN, bool B_MN, Kind KIND>
 cudaError_t launch_kind(const Product& p, Pending* w, Chain* chain) {
-  return w->plan.cg == 2 ? launch_shape<2, A_MN, B_MN, KIND>(p, w, chain)
-                         : launch_shape<1, A_MN, B_MN, KIND>(p, w, chain);
+  if constexpr (KIND != kFloat)
+    if (!w->a.e.vec)
+      return w->plan.cg == 2 ? launch_shape<2, A_MN, B_MN, KIND, true>(p, w, chain)
+                             : launch_shape<1, A_MN, B_MN, KIND, true>(p, w, chain);
+  return w->plan.cg == 2 ? launch_shape<2, A_MN, B_MN, KIND, false>(p, w, chain)
+                         : launch_shape<1, A_MN, B_MN, KIND, false>(p, w, chain);
 }
 
 void set_vec(Epilogue* e, int64_t rows) {
