@@ -335,10 +335,11 @@ def test_in_a_graph():
     assert all(torch.equal(a, b) for a, b in zip(want, (y, dx, dw)))
 
 
-def test_offsets_past_32_bits():
-    """Rows whose element offset passes 2^31: the last rows of a 2.2e9-element x and y."""
+@pytest.mark.parametrize("pitch", [2_000_000, 4_000_001])
+def test_offsets_past_32_bits(pitch):
+    """Rows whose element offset passes 2^31, or 2^32: the last rows of a 2.2e9-element x and
+    y, and of 4.4e9 with rows on odd addresses."""
     m, k, n = 1100, 64, 64
-    pitch = 2_000_000
     big = torch.empty((m - 1) * pitch + k, dtype=BF, device="cuda")
     x = big.as_strided((m, k), (pitch, 1))
     x.copy_(normal((m, k), 1.0, 1))
