@@ -74,6 +74,20 @@ struct ProductArgs {
   int32_t steps;         // stages of the whole reduction
   int32_t withhold;      // test hook: no loads are issued, so every wait runs out
   int32_t late;          // its inputs were there before its predecessor began
+  int32_t early_units;   // units that the predecessor leaves idle in its last round,
+  int32_t early_tiles;   // and tiles they do meanwhile
+};
+
+// The items of a unit (a CTA, or a pair): the early ones go round among the units that
+// are there early, the rest among all.
+struct Turns {
+  int early_units, early_tiles, units;
+  __device__ __forceinline__ int first(int unit) const {
+    return unit < early_units ? unit : early_tiles + unit;
+  }
+  __device__ __forceinline__ int after(int t) const {
+    return t + (t < early_tiles ? early_units : units);
+  }
 };
 
 struct Tile {
@@ -571,7 +585,8 @@ __global__ void __launch_bounds__(kProductThreads, 1)
 
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const uint32_t rank = CG == 2 ? cluster_rank() : 0u;
-  const int unit = blockIdx.x / CG, units = gridDim.x / CG;
+  const int unit = blockIdx.x / CG;
+  const Turns turns{a.early_units, a.early_tiles, static_cast<int>(gridDim.x) / CG};
   const int tiles = a.whole + (a.tiles_m * a.tiles_n - a.whole) * a.splits;
 
   if (threadIdx.x == 0) {
@@ -603,8 +618,8 @@ __global__ void __launch_bounds__(kProductThreads, 1)
       Place at(stages);
       int issued = 0;  // stages, up to the ring's
       bool ok = true;
-      Tile next = tile_of<BM>(a, unit);
-      for (int t = unit; t < tiles && ok; t += units) {
+      Tile next = tile_of<BM>(a, turns.first(unit));
+      for (int t = turns.first(unit); t < tiles && ok; t = turns.after(t)) {
         const Tile tile = next;
         const int ra = static_cast<int>(tile.row) + rank * kBlockRows;
         const int rb = static_cast<int>(tile.col) + rank * b_rows;
@@ -618,7 +633,7 @@ __global__ void __launch_bounds__(kProductThreads, 1)
             ++issued;
           }
           if (a.withhold) {
-            if (step == tile.first && t + units < tiles) next = tile_of<BM>(a, t + units);
+            if (step == tile.first && turns.after(t) < tiles) next = tile_of<BM>(a, turns.after(t));
             continue;
           }
           const uint32_t bar = CG == 2 ? peer_addr(&full[at.s], 0) : smem_addr(&full[at.s]);
@@ -643,7 +658,7 @@ __global__ void __launch_bounds__(kProductThreads, 1)
             }
           }
           // (off the path from one tile's last loads to the next one's first)
-          if (step == tile.first && t + units < tiles) next = tile_of<BM>(a, t + units);
+          if (step == tile.first && turns.after(t) < tiles) next = tile_of<BM>(a, turns.after(t));
         }
       }
       if (!ok) atomicExch(&g_linear_status, 1);
@@ -671,7 +686,7 @@ __global__ void __launch_bounds__(kProductThreads, 1)
       int used = 0;  // stages, up to the ring's
       int n = 0;     // chains begun
       bool ok = true;
-      for (int t = unit; t < tiles && ok; t += units) {
+      for (int t = turns.first(unit); t < tiles && ok; t = turns.after(t)) {
         Tile tile;
         part_of(a, t, tile);
         for (int step = tile.first; step < tile.last && ok; ++n) {
@@ -740,7 +755,7 @@ __global__ void __launch_bounds__(kProductThreads, 1)
     };
     int n = 0;
     bool ok = true;
-    for (int t = unit; t < tiles && ok; t += units) {
+    for (int t = turns.first(unit); t < tiles && ok; t = turns.after(t)) {
       const Tile tile = tile_of<BM>(a, t);
       const int64_t row0 = tile.row + rank * kBlockRows + quarter * 32;
       // (rows past the end are left out by the copy)
@@ -1198,6 +1213,10 @@ struct Plan {
   int cg, bn;
   int whole, splits;  // as in ProductArgs
   int tail;           // tiles split
+  int early_units, early_tiles;  // as in ProductArgs
+  double us;          // the estimate, with the wait for what it follows
+  double last_us;     // of the last round, where that has whole tiles only
+  int last_tiles;     // tiles of that round
   int64_t part_bytes() const {
     return splits > 1 ? int64_t{4} * tail * splits * cg * kBlockRows * bn : 0;
   }
@@ -1214,15 +1233,17 @@ struct Plan {
 // what counts for a few rows; 3 for a kernel's beginning and end, 0.9 for each 64
 // columns of its last epilogue, 3 for the join's launch.
 //
-// follows: the tiles of a product that is launched just before and does not have
-// to end first, so that this one's fill its last round; split: whether tiles past
-// the last whole round may be.
+// follows: the product that is launched just before and does not have to end
+// first, so that this one's tiles fill its last round: units without a tile there
+// take theirs early, as many as they can do meanwhile (the first blocks of a grid
+// get the first units that are free).  split: whether tiles past the last whole
+// round may be.
 Plan plan_product(int64_t rows, int64_t cols, int64_t depth, bool a_mn, bool b_mn,
                   const Plan* follows = nullptr, bool split = true) {
-  Plan best{2, 256, 0, 1, 0};
+  Plan best{2, 256, 0, 1, 0, 0, 0, 0.0, 0.0, 0};
   if (rows < 1 || cols < 1) return best;
   const int steps = static_cast<int>((depth + kStep - 1) / kStep);
-  double least = 1e300;
+  best.us = 1e300;
   for (int cg = 2; cg >= 1; --cg) {
     const int most = cg == 2 ? 256 : 128;
     // MN-major operands come in columns of 64 per CTA
@@ -1230,12 +1251,9 @@ Plan plan_product(int64_t rows, int64_t cols, int64_t depth, bool a_mn, bool b_m
     const int units = kSms / cg, a_rows = a_rows_of(rows, cg, a_mn);
     const int64_t tm = (rows + 128 * cg - 1) / (128 * cg);
     for (int bn = most; bn >= unit; bn -= unit) {
-      const int64_t tn = (cols + bn - 1) / bn, tiles = tm * tn;
-      if (tiles > INT32_MAX / 64) continue;
-      const int before = follows != nullptr && follows->cg == cg ? follows->whole % units : 0;
-      int rest = static_cast<int>((tiles + before) % units);
-      if (rest > tiles) rest = static_cast<int>(tiles);
-      const int whole = static_cast<int>(tiles) - rest;
+      const int64_t tn = (cols + bn - 1) / bn;
+      if (tm * tn > INT32_MAX / 64) continue;
+      const int tiles = static_cast<int>(tm * tn);
       const double share = static_cast<double>(bn) / most;
       const double mma = cg == 2 ? 0.40 + 0.25 * share * share : 0.42 + 0.055 * share * share;
       const double wait = 1.3 / ring_stages(a_rows, bn / cg);
@@ -1246,23 +1264,38 @@ Plan plan_product(int64_t rows, int64_t cols, int64_t depth, bool a_mn, bool b_m
         const double read = distinct * (2 * kStep) / 6.5e6;
         return floor > read ? floor : read;
       };
-      const double before_us =
-          (whole > 0 ? whole / units * steps * stage(units) : 0.0) + 3.0 + 0.9 * bn / 64;
-      for (int parts = 1; parts <= 16; ++parts) {
-        // (past two rounds of parts nothing was ever gained)
-        if (parts > 1 && (rest == 0 || parts * 2 > steps || rest * parts > 2 * units ||
-                          (!split && whole > 0)))
-          break;
-        const Plan p{cg, bn, parts > 1 ? whole : static_cast<int>(tiles), parts, parts > 1 ? rest : 0};
-        if (p.part_bytes() > (int64_t{64} << 20)) break;
-        const int items = rest * parts, rounds = (items + units - 1) / units;
-        const int deep = (steps + parts - 1) / parts;
-        double cost = before_us;
-        if (items > 0) cost += rounds * deep * stage(items < units ? items : units);
-        if (parts > 1) cost += 3.0 + p.part_bytes() * 2 / 5.0e6;
-        if (cost < least) {
-          least = cost;
-          best = p;
+      const double tile = steps * stage(units), ends = 3.0 + 0.9 * bn / 64;
+      const int taken = follows != nullptr ? follows->last_tiles * follows->cg : 0;  // SMs
+      const int free = (kSms - taken) / cg;
+      const bool fills = taken > 0 && free > 0;
+      const double begin = follows != nullptr ? follows->last_us : 0.0;
+      const int ahead = fills ? static_cast<int>(begin / tile) : 0;
+      for (int turn = ahead; turn <= ahead + (fills ? 1 : 0); ++turn) {
+        if (turn > 0 && turn > tiles / free) break;
+        const int early = turn * free, rest = (tiles - early) % units;
+        const int whole = tiles - rest;
+        const double rounds_us = (whole - early) / units * tile;
+        const double late_us = begin + rounds_us, early_us = turn * tile + rounds_us;
+        const double all_us = late_us > early_us ? late_us : early_us;
+        for (int parts = 1; parts <= 16; ++parts) {
+          // (past two rounds of parts nothing was ever gained)
+          if (parts > 1 && (rest == 0 || parts * 2 > steps || rest * parts > 2 * units ||
+                            (!split && whole > 0)))
+            break;
+          Plan p{cg, bn, parts > 1 ? whole : tiles, parts, parts > 1 ? rest : 0,
+                 fills ? free : 0, early, 0.0, 0.0, 0};
+          if (p.part_bytes() > (int64_t{64} << 20)) break;
+          const int items = rest * parts, rounds = (items + units - 1) / units;
+          const double last =
+              items > 0 ? rounds * ((steps + parts - 1) / parts) * stage(items < units ? items : units) : 0.0;
+          if (parts == 1) {
+            p.last_us = rest > 0 ? last : 0.0;
+            p.last_tiles = rest;
+          }
+          const double end = fills && items <= free ? early_us + last : all_us + last;
+          p.us = (end > late_us ? end : late_us) + ends;
+          if (parts > 1) p.us += 3.0 + p.part_bytes() * 2 / 5.0e6;
+          if (p.us < best.us) best = p;
         }
       }
     }
@@ -1309,6 +1342,8 @@ cudaError_t launch_shape(const Product& p, Pending* w, Chain* chain) {
   a.bn = bn;
   a.whole = plan.whole;
   a.splits = plan.splits;
+  a.early_units = plan.early_units;
+  a.early_tiles = plan.early_tiles;
   if (plan.splits > 1) {
     e = make_out_map(&a.parts, w->parts, CG * kBlockRows, bn, bn, plan.tail * plan.splits,
                      CG * kBlockRows * bn, true);
@@ -1653,15 +1688,23 @@ Plan plan_forward(const zero_linear_t& s) {
   return plan_product(s.rows, s.out, s.in, false, false);
 }
 
-// dw's tiles fill dx's last round, so dx is split only where it has less than one.
+// dw's tiles fill dx's last round, or dx's last round is split.
 struct BackwardPlan {
   Plan dx, dw;
 };
 BackwardPlan plan_backward(const zero_linear_t& s, bool dx, bool dw) {
-  BackwardPlan p{{2, 256, 0, 1, 0}, {2, 256, 0, 1, 0}};
-  if (dx) p.dx = plan_product(s.rows, s.in, s.out, false, true, nullptr, !dw);
-  if (dw) p.dw = plan_product(s.out, s.in, s.rows, true, true, dx ? &p.dx : nullptr);
-  return p;
+  const auto first = [&](bool split) {
+    return plan_product(s.rows, s.in, s.out, false, true, nullptr, split);
+  };
+  const auto second = [&](const Plan* follows) {
+    return plan_product(s.out, s.in, s.rows, true, true, follows);
+  };
+  if (!dw) return {first(true), Plan{2, 256, 0, 1, 0, 0, 0, 0.0, 0.0, 0}};
+  if (!dx) return {Plan{2, 256, 0, 1, 0, 0, 0, 0.0, 0.0, 0}, second(nullptr)};
+  BackwardPlan filled{first(false), {}}, split{first(true), second(nullptr)};
+  filled.dw = second(&filled.dx);
+  return filled.dx.us - filled.dx.last_us + filled.dw.us <= split.dx.us + split.dw.us ? filled
+                                                                                      : split;
 }
 
 }  // namespace
