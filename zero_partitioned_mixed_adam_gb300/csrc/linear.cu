@@ -1053,7 +1053,7 @@ __device__ __forceinline__ void add_dbias(const DbiasArgs& a) {
   }
 }
 
-// What is left to do before (or beside) the products: a row of blocks a job.
+// Copies, a row of blocks each, or dbias (beside the products: it lets them begin).
 __global__ void __launch_bounds__(256) linear_prepare_kernel(const __grid_constant__ PrepareArgs a) {
   wait_for_predecessor();
   launch_dependents();
@@ -1105,10 +1105,8 @@ struct Chain {
   }
 };
 
-// Lays the matrices that TMA cannot read where they are out anew, and adds up
-// dbias where it is wanted, in one launch.
-cudaError_t prepare(Stored* const* matrices, int count, const DbiasArgs& dbias, Space* space,
-                    Chain* chain) {
+// Lays the matrices that TMA cannot read where they are out anew.
+cudaError_t lay_out(Stored* const* matrices, int count, Space* space, Chain* chain) {
   PrepareArgs all{};
   int64_t most = 0;
   for (int k = 0; k < count; ++k) {
@@ -1122,16 +1120,17 @@ cudaError_t prepare(Stored* const* matrices, int count, const DbiasArgs& dbias, 
     const int64_t blocks = (m.rows * ((m.cols + 255) / 256) + 7) / 8;
     most = blocks > most ? blocks : most;
   }
-  int jobs = all.copies;
-  if (dbias.dbias != nullptr) {
-    all.dbias = dbias;
-    const int64_t blocks = (dbias.cols + 7) / 8;
-    most = blocks > most ? blocks : most;
-    ++jobs;
-  }
-  if (jobs == 0) return cudaSuccess;
-  const dim3 grid(static_cast<unsigned>(most < 2432 ? most : 2432), jobs);
+  if (all.copies == 0) return cudaSuccess;
+  const dim3 grid(static_cast<unsigned>(most < 2432 ? most : 2432), all.copies);
   return chain->launch(linear_prepare_kernel, grid, 256, 0, 1, all);
+}
+
+cudaError_t launch_dbias(const DbiasArgs& dbias, Chain* chain) {
+  PrepareArgs all{};
+  all.dbias = dbias;
+  const int64_t blocks = (dbias.cols + 7) / 8;
+  return chain->launch(linear_prepare_kernel, dim3(static_cast<unsigned>(blocks < 2432 ? blocks : 2432)),
+                       256, 0, 1, all);
 }
 
 using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
@@ -1578,16 +1577,11 @@ struct SlopeArgs {
   uint16_t* dz;    // NULL: sums only
   int64_t ldz;
   float* sums;     // [row blocks][cols], NULL: dz only
+  int32_t late;    // as in ProductArgs
 };
 
 template <int ACT>
-__global__ void __launch_bounds__(32 * kSlopeWarps, 6)
-    linear_slope_kernel(const __grid_constant__ SlopeArgs a) {
-  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  wait_for_predecessor();
-  launch_dependents();
-  const int64_t j0 = static_cast<int64_t>(blockIdx.x) * kSlopeCols + 256 * warp;
-  if (j0 >= a.cols) return;
+__device__ __forceinline__ void slope_rows(const SlopeArgs& a, int64_t j0, int lane) {
   const int64_t first = static_cast<int64_t>(blockIdx.y) * a.height;
   const int n = static_cast<int>(a.rows - first < a.height ? a.rows - first : a.height);
   float sum[8] = {};
@@ -1658,6 +1652,17 @@ __global__ void __launch_bounds__(32 * kSlopeWarps, 6)
       }
     }
   }
+}
+
+template <int ACT>
+__global__ void __launch_bounds__(32 * kSlopeWarps, 6)
+    linear_slope_kernel(const __grid_constant__ SlopeArgs a) {
+  if (!a.late) wait_for_predecessor();
+  launch_dependents();
+  const int64_t j0 =
+      static_cast<int64_t>(blockIdx.x) * kSlopeCols + 256 * static_cast<int>(threadIdx.x / 32);
+  if (j0 < a.cols) slope_rows<ACT>(a, j0, threadIdx.x % 32);
+  if (a.late) wait_for_predecessor();
 }
 
 // Rows of a block: 8 blocks an SM, 4 to 64 rows.
@@ -1751,7 +1756,7 @@ cudaError_t launch_linear_forward(const LinearForwardLaunch& L) {
   // element it would take the whole epilogue with it)
   Stored bias{L.bias, 1, s.out, 0};
   Stored* const all[3] = {&p.a, &p.b, &bias};
-  cudaError_t e = prepare(all, 3, DbiasArgs{}, &space, &chain);
+  cudaError_t e = lay_out(all, 3, &space, &chain);
   p.e.bias = bias.p;
   Pending w;
   if (e == cudaSuccess)
@@ -1766,28 +1771,46 @@ cudaError_t launch_linear_backward(const LinearBackwardLaunch& L) {
   Space space{static_cast<char*>(L.workspace)};
   Chain chain{L.stream};
   DbiasArgs dbias{};
-  cudaError_t e = cudaSuccess;
-  if (s.rows > 0 && (L.act != ZERO_ACT_NONE || L.dbias != nullptr)) {
-    SlopeArgs a{};
+  dbias.cols = s.out;
+  dbias.dbias = L.dbias;
+  dbias.out_f32 = L.grad_f32;
+  dbias.accumulate = L.accumulate;
+  if (s.rows == 0) {  // sums of nothing
+    const cudaError_t e = L.dbias != nullptr ? launch_dbias(dbias, &chain) : cudaSuccess;
+    if (e != cudaSuccess || L.dw == nullptr || L.accumulate) return e;
+    return cudaMemset2DAsync(L.dw, s.lddw * (L.grad_f32 ? 4 : 2), 0, s.in * (L.grad_f32 ? 4 : 2),
+                             s.out, L.stream);
+  }
+  const bool products = L.dx != nullptr || L.dw != nullptr;
+  SlopeArgs a{};
+  if (L.act != ZERO_ACT_NONE && products) {
+    a.dz = static_cast<uint16_t*>(space.take(copy_bytes(dz)));
+    a.ldz = copy_pitch(s.out);
+    dz = Stored(a.dz, s.rows, s.out, a.ldz);
+  }
+  if (!products) dz.p = nullptr;
+  Stored w(L.dx != nullptr ? L.w : nullptr, s.out, s.in, s.ldw);
+  Stored x(L.dw != nullptr ? L.x : nullptr, s.rows, s.in, s.ldx);
+  Stored* const all[3] = {&dz, &w, &x};
+  cudaError_t e = lay_out(all, 3, &space, &chain);
+  if (e != cudaSuccess) return e;
+  if (a.dz != nullptr || L.dbias != nullptr) {
     a.dy = L.dy;
     a.pre = L.pre;
     a.ldy = s.ldy;
     a.ldp = s.ldp;
     a.rows = s.rows;
     a.cols = s.out;
-    if (L.act != ZERO_ACT_NONE && (L.dx != nullptr || L.dw != nullptr)) {
-      a.dz = static_cast<uint16_t*>(space.take(copy_bytes(dz)));
-      a.ldz = copy_pitch(s.out);
-      dz = Stored(a.dz, s.rows, s.out, a.ldz);
-    }
     const int64_t blocks = slope_blocks(s.rows, s.out);
     a.height = static_cast<int32_t>(slope_height(s.rows, s.out));
     if (L.dbias != nullptr) {
       a.sums = static_cast<float*>(space.take(blocks * round_up4(s.out) * 4));
+      dbias.sums = a.sums;
       dbias.blocks = static_cast<int32_t>(blocks);
     }
     a.vec = tileable(Stored(L.dy, s.rows, s.out, s.ldy)) &&
             (L.act == ZERO_ACT_NONE || tileable(Stored(L.pre, s.rows, s.out, s.ldp)));
+    a.late = chain.begun;  // beside the copies
     auto kernel = L.act == ZERO_ACT_GELU   ? linear_slope_kernel<ZERO_ACT_GELU>
                   : L.act == ZERO_ACT_SILU ? linear_slope_kernel<ZERO_ACT_SILU>
                   : L.act == ZERO_ACT_RELU ? linear_slope_kernel<ZERO_ACT_RELU>
@@ -1802,31 +1825,14 @@ cudaError_t launch_linear_backward(const LinearBackwardLaunch& L) {
       part.dz += a.dz != nullptr ? skip * a.ldz : 0;
       part.sums += a.sums != nullptr ? k * round_up4(s.out) : 0;
       part.rows -= skip;
+      part.late = a.late && k == 0;
       const int64_t high = blocks - k < 65535 ? blocks - k : 65535;
       const dim3 grid(static_cast<unsigned>(across), static_cast<unsigned>(high));
       e = chain.launch(kernel, grid, 32 * kSlopeWarps, 0, 1, part);
     }
+    if (e == cudaSuccess && L.dbias != nullptr) e = launch_dbias(dbias, &chain);
     if (e != cudaSuccess) return e;
-    dbias.sums = a.sums;
   }
-  if (L.dbias != nullptr) {
-    dbias.cols = s.out;
-    dbias.dbias = L.dbias;
-    dbias.out_f32 = L.grad_f32;
-    dbias.accumulate = L.accumulate;
-  }
-  if (s.rows == 0) {  // sums of nothing
-    e = prepare(nullptr, 0, dbias, &space, &chain);
-    if (e != cudaSuccess || L.dw == nullptr || L.accumulate) return e;
-    return cudaMemset2DAsync(L.dw, s.lddw * (L.grad_f32 ? 4 : 2), 0, s.in * (L.grad_f32 ? 4 : 2),
-                             s.out, L.stream);
-  }
-  Stored w(L.dx != nullptr ? L.w : nullptr, s.out, s.in, s.ldw);
-  Stored x(L.dw != nullptr ? L.x : nullptr, s.rows, s.in, s.ldx);
-  if (L.dx == nullptr && L.dw == nullptr) dz.p = nullptr;
-  Stored* const all[3] = {&dz, &w, &x};
-  e = prepare(all, 3, dbias, &space, &chain);
-  if (e != cudaSuccess) return e;
   const BackwardPlan plan = plan_backward(s, L.dx != nullptr, L.dw != nullptr);
   Pending dx{}, dw{};
   dx.plan.splits = dw.plan.splits = 1;
@@ -1843,7 +1849,8 @@ cudaError_t launch_linear_backward(const LinearBackwardLaunch& L) {
     p.e.lds = s.ldpi;
     p.e.out = L.dx;
     p.e.ldo = s.lddx;
-    e = launch_product(p, plan.dx, false, &space, L.withhold, &chain, &dx);
+    // dbias's kernel has waited for all that this one reads before it let it begin
+    e = launch_product(p, plan.dx, L.dbias != nullptr, &space, L.withhold, &chain, &dx);
     if (e != cudaSuccess) return e;
   }
   if (L.dw != nullptr) {
@@ -1859,8 +1866,8 @@ cudaError_t launch_linear_backward(const LinearBackwardLaunch& L) {
     p.e.ldo = s.lddw;
     p.e.out_f32 = L.grad_f32;
     p.e.accumulate = L.accumulate;
-    // dx's product has waited for all that this one reads before it let it begin
-    e = launch_product(p, plan.dw, L.dx != nullptr, &space, L.withhold, &chain, &dw);
+    // (and so have dx's product, or what came before that)
+    e = launch_product(p, plan.dw, L.dbias != nullptr || L.dx != nullptr, &space, L.withhold, &chain, &dw);
     if (e != cudaSuccess) return e;
   }
   e = launch_join(dx, &chain);
