@@ -1071,9 +1071,9 @@ struct Space {
   }
 };
 
-// The kernels of one call.  All but the first are launched as programmatic
-// dependents: they begin while their predecessor ends, and wait for it
-// (wait_for_predecessor) before they read what it wrote.
+// The kernels of one call, launched as programmatic dependents: they begin while
+// their predecessor ends, and wait for it (wait_for_predecessor) before they read
+// what it wrote; the first one so after whatever the stream held before.
 struct Chain {
   cudaStream_t stream;
   bool begun = false;
@@ -1095,11 +1095,9 @@ struct Chain {
       a.val.clusterDim.y = 1;
       a.val.clusterDim.z = 1;
     }
-    if (begun) {
-      cudaLaunchAttribute& a = attr[config.numAttrs++];
-      a.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-      a.val.programmaticStreamSerializationAllowed = 1;
-    }
+    cudaLaunchAttribute& a = attr[config.numAttrs++];
+    a.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    a.val.programmaticStreamSerializationAllowed = 1;
     begun = true;
     return cudaLaunchKernelEx(&config, kernel, static_cast<Params>(args)...);
   }
@@ -1475,6 +1473,8 @@ __global__ void __launch_bounds__(32 * kFewWarps, U == 2 ? 5 : 3)
     linear_few_rows_kernel(const __grid_constant__ FewArgs a) {
   constexpr int kSpan = 32 * U;          // columns a warp takes at a time
   __shared__ float part[kFewWarps][16 * 8 * NT];
+  wait_for_predecessor();
+  launch_dependents();
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, g = lane / 4, t = lane % 4;
   const int share = a.share, mine = warp % share;
   const int64_t row0 = (static_cast<int64_t>(blockIdx.x) * (kFewWarps / share) + warp / share) * 16;
@@ -1525,7 +1525,7 @@ __global__ void __launch_bounds__(32 * kFewWarps, U == 2 ? 5 : 3)
 }
 
 template <int NT>
-cudaError_t launch_few_groups(FewArgs& a, bool vec, cudaStream_t stream) {
+cudaError_t launch_few_groups(FewArgs& a, bool vec, Chain* chain) {
   // The columns are shared out until there are 16 warps an SM, or a warp's part
   // is one step.
   const int64_t groups = (a.cols + 15) / 16;
@@ -1538,17 +1538,13 @@ cudaError_t launch_few_groups(FewArgs& a, bool vec, cudaStream_t stream) {
   // (1 x 4096 x 11008, 688 blocks: 16.2 us against 19.5 with the 4 loads that 1 x
   // 11008 x 4096, 256 blocks, wants: 18.5 against 25.1).
   const unsigned grid = static_cast<unsigned>(blocks), threads = 32 * kFewWarps;
-  if (blocks >= 3 * kSms) {
-    if (vec) linear_few_rows_kernel<NT, 2, true><<<grid, threads, 0, stream>>>(a);
-    else linear_few_rows_kernel<NT, 2, false><<<grid, threads, 0, stream>>>(a);
-  } else {
-    if (vec) linear_few_rows_kernel<NT, 4, true><<<grid, threads, 0, stream>>>(a);
-    else linear_few_rows_kernel<NT, 4, false><<<grid, threads, 0, stream>>>(a);
-  }
-  return cudaGetLastError();
+  const auto kernel = blocks >= 3 * kSms ? (vec ? linear_few_rows_kernel<NT, 2, true>
+                                                : linear_few_rows_kernel<NT, 2, false>)
+                                         : (vec ? linear_few_rows_kernel<NT, 4, true>
+                                                : linear_few_rows_kernel<NT, 4, false>);
+  return chain->launch(kernel, dim3(grid), threads, 0, 1, a);
 }
-
-cudaError_t launch_few_rows(const Product& p, cudaStream_t stream) {
+cudaError_t launch_few_rows(const Product& p, Chain* chain) {
   FewArgs a{};
   a.x = p.a.p;
   a.ldx = p.a.ld;
@@ -1559,7 +1555,7 @@ cudaError_t launch_few_rows(const Product& p, cudaStream_t stream) {
   a.depth = static_cast<int32_t>(p.depth);
   a.e = p.e;
   const bool vec = tileable(p.a) && tileable(p.b);
-  return p.rows <= 8 ? launch_few_groups<1>(a, vec, stream) : launch_few_groups<2>(a, vec, stream);
+  return p.rows <= 8 ? launch_few_groups<1>(a, vec, chain) : launch_few_groups<2>(a, vec, chain);
 }
 
 // dz = bf16(dy * act'(pre)), and each column's sum of it before the rounding.
@@ -1749,9 +1745,9 @@ cudaError_t launch_linear_forward(const LinearForwardLaunch& L) {
   p.e.ldr = s.ldr;
   p.e.out = L.y;
   p.e.ldo = s.ldy;
-  if (s.rows <= kFewRows) return launch_few_rows(p, L.stream);
-  Space space{static_cast<char*>(L.workspace)};
   Chain chain{L.stream};
+  if (s.rows <= kFewRows) return launch_few_rows(p, &chain);
+  Space space{static_cast<char*>(L.workspace)};
   // (where only the bias is out of place, its copy costs a launch; taken element by
   // element it would take the whole epilogue with it)
   Stored bias{L.bias, 1, s.out, 0};
