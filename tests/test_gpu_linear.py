@@ -364,6 +364,56 @@ def test_fp32_gradients_keep_their_precision(rows):
     assert np.linalg.norm(host(db) - want) <= 1e-6 * np.linalg.norm(want)
 
 
+@pytest.mark.parametrize("captured", [False, True])
+@pytest.mark.parametrize("m", [4, 200])
+def test_order_among_streams(m, captured):
+    """Calls begin while their stream's last kernel ends: what another stream wrote before an
+    event is read, and what is overwritten after one has been read, run or captured."""
+    k, n = 512, 768
+    x, w, dy = normal((m, k), 1.0, 1), normal((n, k), 0.1, 2), normal((m, n), 1.0, 3)
+    y, dx, dw, db = empty((m, n)), empty((m, k)), empty((n, k)), empty((1, n))[0]
+    want = [torch.empty_like(t) for t in (y, dx, dw, db)]
+    za.zero_linear_forward(x, w, want[0])
+    za.zero_linear_backward(dy, x, w, dx=want[1], dw=want[2], dbias=want[3], act=2, pre=want[0])
+    inputs, late = (x, w, dy), [torch.zeros_like(t) for t in (x, w, dy)]
+    copies = [torch.empty_like(t) for t in want]
+    tiny = torch.zeros(1, device="cuda")
+    a, b = torch.cuda.Stream(), torch.cuda.Stream()
+
+    def work(a, b):
+        b.wait_stream(a)
+        with torch.cuda.stream(b):
+            torch.cuda._sleep(2_000_000)
+            for t, s in zip(late, inputs):
+                t.copy_(s)
+        with torch.cuda.stream(a):
+            tiny.add_(1.0)               # a kernel right before the call, beside the event
+            a.wait_stream(b)
+            za.zero_linear_forward(late[0], late[1], y)
+            za.zero_linear_backward(late[2], late[0], late[1], dx=dx, dw=dw, dbias=db, act=2, pre=y)
+        b.wait_stream(a)
+        with torch.cuda.stream(b):
+            for t, s in zip(copies, (y, dx, dw, db)):
+                t.copy_(s)
+            for t in (*late, y, dx, dw, db):
+                t.zero_()
+        a.wait_stream(b)
+
+    torch.cuda.synchronize()
+    if captured:
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=a):
+            work(a, b)
+        for _ in range(3):
+            graph.replay()
+    else:
+        for _ in range(3):
+            work(a, b)
+    torch.cuda.synchronize()
+    for got, t in zip(copies, want):
+        assert torch.equal(got, t)
+
+
 def test_a_wait_that_runs_out_is_reported():
     """With no tile loaded every wait of the product gives up after about a second, nothing
     is written, the status says so, and the next call is as if nothing had been."""
