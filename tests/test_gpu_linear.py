@@ -135,6 +135,22 @@ def test_pitches_and_offsets(shape, pitch, offset):
         assert bool((t.as_strided((offset,), (1,), 0) == 7.0).all())
 
 
+@pytest.mark.parametrize("shape", [(17, 2048, 96), (64, 4096, 256), (100, 3000, 1031), (128, 2048, 130),
+                                   (128, 4096, 4096), (250, 2304, 761), (256, 2304, 768),
+                                   (300, 4096, 1024), (513, 1900, 200)])
+def test_few_tiles_and_long_sums(shape):
+    """Products whose reduction is shared out: forward, and with the widths changed over the
+    gradient of x times a slope."""
+    m, k, n = shape
+    test_forward(shape, "gelu")
+    dy, w, pre = normal((m, k), 1.0, 1), normal((k, n), 1.0 / math.sqrt(k), 2), normal((m, n), 1.0, 3)
+    dx = empty((m, n))
+    za.zero_linear_backward(dy, None, w, dx=dx, act_in=o.ACTS["relu"], pre_in=pre)
+    want = (host(dy) @ host(w)) * (host(pre) > 0)
+    tol = product_error(dy, w, k) + 2.0 ** -8 * np.abs(want) + 1e-30
+    check(dx, want, tol, "dx")
+
+
 @pytest.mark.parametrize("n", [17, 23, 39, 40, 41, 65, 71, 103, 135, 161, 255, 259, 263, 519])
 @pytest.mark.parametrize("gap,offset", [(1, 0), (2, 3), (8, 5)])
 def test_rows_at_any_address(n, gap, offset):
@@ -431,6 +447,11 @@ def test_a_wait_that_runs_out_is_reported():
         torch.cuda.synchronize()
         assert za.device_status() == -15
         assert bool((dx == 7.0).all()) and bool((dw == 7.0).all())
+        x2, w2, y2 = normal((128, 2048), 1.0, 4), normal((256, 2048), 0.1, 5), empty((128, 256))
+        za.zero_linear_forward(x2, w2, y2)    # a reduction shared out in a cluster
+        torch.cuda.synchronize()
+        assert za.device_status() == -15
+        assert bool((y2 == 7.0).all())
     finally:
         za.test_withhold_copies(was)
     assert za.device_status() == za.ZERO_OK

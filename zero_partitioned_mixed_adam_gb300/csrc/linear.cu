@@ -45,7 +45,7 @@ constexpr int kStaging = kEpilogueWarps * 32 * 32 * 4;
 constexpr int kMaxStages = 8;
 constexpr int kBarriers = 256;
 constexpr int kSmem = 227 * 1024;
-static_assert((2 * kMaxStages + 5) * 8 <= kBarriers, "barriers");
+static_assert((2 * kMaxStages + 5) * 8 <= kBarriers, "barriers, and two words");
 
 template <int CG>
 struct ProductShape {
@@ -567,7 +567,16 @@ __device__ __forceinline__ bool wait_for_chain(uint64_t* bar, uint32_t parity, i
 // x 8192, 154 us, 14 rounds of tiles where 13.47 are needed, and 8 us of beginning
 // and end.
 // ROWS: D, pre or what is read with them lies where TMA cannot take it.
-template <int CG, bool A_MN, bool B_MN, Kind KIND, bool ROWS>
+//
+// GATHER: a cluster's CTAs have a part of one tile's reduction each, and no other
+// item.  They leave their sums in the ring, which nothing is loaded into any more,
+// and each adds up every splits-th 32 columns of all, in the parts' order.  For few
+// tiles: an SM takes in some 60 bytes a cycle whatever the tile, so more SMs with
+// less of the reduction each are faster, by more than the exchange costs (256 x 4096
+// -> 4096 17.4 -> 14.8 us, 300 x 4096 -> 1024 12.6 -> 11.1, 64 x 11008 -> 4096 23.5 ->
+// 21.6; 128 x 4096 -> 4096 with the parts through global memory and joined by a
+// launch 14.7, 13.7 so).
+template <int CG, bool A_MN, bool B_MN, Kind KIND, bool ROWS, bool GATHER>
 __global__ void __launch_bounds__(kProductThreads, 1)
     linear_product_kernel(const __grid_constant__ ProductArgs a) {
   using Shape = ProductShape<CG>;
@@ -582,6 +591,7 @@ __global__ void __launch_bounds__(kProductThreads, 1)
   uint64_t* done = empty + kMaxStages;
   uint64_t* free_ = done + 2;
   uint32_t* tmem_at = reinterpret_cast<uint32_t*>(free_ + 2);
+  uint32_t* failed = tmem_at + 1;  // GATHER: this CTA's sums are not there
 
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const uint32_t rank = CG == 2 ? cluster_rank() : 0u;
@@ -590,6 +600,7 @@ __global__ void __launch_bounds__(kProductThreads, 1)
   const int tiles = a.whole + (a.tiles_m * a.tiles_n - a.whole) * a.splits;
 
   if (threadIdx.x == 0) {
+    *failed = 0;
     for (int s = 0; s < stages; ++s) {
       mbar_init(&full[s], 1);
       mbar_init(&empty[s], 1);
@@ -774,6 +785,14 @@ __global__ void __launch_bounds__(kProductThreads, 1)
       // 32 columns from c on are summed up: on their way.
       const auto finish = [&](float x[32], int c) {
         const int64_t col0 = tile.col + c;
+        if constexpr (GATHER) {
+          float* to = reinterpret_cast<float*>(ring) + (c / 32 * 4 + quarter) * 32 * 32;
+#pragma unroll
+          for (int q = 0; q < 8; ++q)
+            *reinterpret_cast<float4*>(to + staged(lane, q)) =
+                make_float4(x[4 * q], x[4 * q + 1], x[4 * q + 2], x[4 * q + 3]);
+          return;
+        }
         if constexpr (ROWS) {
           if (fast) {
             if (col0 < end) part.put(mine, x, row0, rows, col0, first, end, lane);
@@ -871,12 +890,79 @@ __global__ void __launch_bounds__(kProductThreads, 1)
         }
       }
     }
-    if (!ok && lane == 0) atomicExch(&g_linear_status, 3);
-    if (lane == 0) bulk_wait_all();
+    if (!ok && lane == 0) {
+      atomicExch(&g_linear_status, 3);
+      if (GATHER) *failed = 1;
+    }
+    if (!GATHER && lane == 0) bulk_wait_all();
   }
   __syncwarp();
+  if constexpr (GATHER) {
+    cluster_sync_writes();
+    if (warp >= 2) {
+      const int quarter = warp % 4, half = (warp - 2) / 4, mine_of = static_cast<int>(cluster_rank());
+      float* mine = staging + (warp - 2) * 32 * 32;
+      bool ok = true;
+      for (int s = 0; s < a.splits; ++s)
+        ok = ok && peer_load_u32(peer_addr(failed, s)) == 0;
+      const Tile tile = tile_of<BM>(a, unit);
+      const int64_t row0 = tile.row + quarter * 32;
+      std::conditional_t<ROWS, RowsPart<KIND>, EpiloguePart<KIND>> part(a.e);
+      for (int c = 32 * (mine_of + a.splits * half); c < a.bn; c += 64 * a.splits) {
+        const int64_t col0 = tile.col + c;
+        if (!ok || row0 >= a.rows || col0 >= a.cols) break;
+        const int64_t end = a.cols < col0 + 32 ? a.cols : col0 + 32;
+        const bool whole = ROWS ? end - col0 >= 8 : a.e.vec && col0 + 32 <= a.cols;
+        if (whole) {
+          if constexpr (ROWS) part.ask(row0 + lane, col0, row0 + lane < a.rows, col0, end, lane);
+          else part.ask(row0 + lane, col0, row0 + lane < a.rows);
+        }
+        const float* from = reinterpret_cast<const float*>(ring) + (c / 32 * 4 + quarter) * 32 * 32;
+        // A load takes 4 whole rows, two parts at a time (16 bytes of 32 rows, a row a
+        // lane, made the kernel 22 us instead of 16 at 128 x 4096 -> 4096).
+        float4 sum[8] = {};
+#pragma unroll 1
+        for (int s = 0; s < a.splits; s += 2) {
+          float4 y[16];
+#pragma unroll
+          for (int q = 0; q < 16; ++q)
+            y[q] = peer_load(peer_addr(from, s + q / 8) + 4 * staged(4 * (q % 8) + lane / 8, lane % 8));
+#pragma unroll
+          for (int q = 0; q < 16; ++q) {
+            float4& t = sum[q % 8];
+            t.x += y[q].x; t.y += y[q].y; t.z += y[q].z; t.w += y[q].w;
+          }
+        }
+        if (lane == 0) bulk_wait_read<0>();
+        __syncwarp();
+#pragma unroll
+        for (int q = 0; q < 8; ++q)
+          *reinterpret_cast<float4*>(mine + staged(4 * q + lane / 8, lane % 8)) = sum[q];
+        __syncwarp();
+        if (whole) {
+          float x[32];
+#pragma unroll
+          for (int q = 0; q < 8; ++q) {
+            const float4 y = *reinterpret_cast<const float4*>(mine + staged(lane, q));
+            x[4 * q] = y.x; x[4 * q + 1] = y.y; x[4 * q + 2] = y.z; x[4 * q + 3] = y.w;
+          }
+          __syncwarp();
+          if constexpr (ROWS)
+            part.put(mine, x, row0, a.rows, col0, col0, end, lane);
+          else
+            part.put(a, reinterpret_cast<uint8_t*>(mine), x, static_cast<int>(row0),
+                     static_cast<int>(col0), lane);
+        } else {
+          epilogue_scalar<KIND>(a.e, mine, row0, col0, a.rows, a.cols, lane);
+          __syncwarp();
+        }
+      }
+      if (lane == 0) bulk_wait_all();
+      __syncwarp();
+    }
+  }
   __syncthreads();
-  if constexpr (CG == 2) cluster_sync();
+  if constexpr (CG == 2 || GATHER) cluster_sync();
   if (warp == 1) tmem_free<CG>(tmem, Shape::kColumns);
   // what follows this kernel follows its predecessor too
   if (a.late) wait_for_predecessor();
@@ -1210,12 +1296,13 @@ struct Plan {
   int cg, bn;
   int whole, splits;  // as in ProductArgs
   int tail;           // tiles split
+  bool gather;        // the parts are a cluster's
   int early_units, early_tiles;  // as in ProductArgs
   double us;          // the estimate, with the wait for what it follows
   double last_us;     // of the last round, where that has whole tiles only
   int last_tiles;     // tiles of that round
   int64_t part_bytes() const {
-    return splits > 1 ? int64_t{4} * tail * splits * cg * kBlockRows * bn : 0;
+    return splits > 1 && !gather ? int64_t{4} * tail * splits * cg * kBlockRows * bn : 0;
   }
 };
 
@@ -1237,7 +1324,7 @@ struct Plan {
 // round may be.
 Plan plan_product(int64_t rows, int64_t cols, int64_t depth, bool a_mn, bool b_mn,
                   const Plan* follows = nullptr, bool split = true) {
-  Plan best{2, 256, 0, 1, 0, 0, 0, 0.0, 0.0, 0};
+  Plan best{2, 256, 0, 1, 0, false, 0, 0, 0.0, 0.0, 0};
   if (rows < 1 || cols < 1) return best;
   const int steps = static_cast<int>((depth + kStep - 1) / kStep);
   best.us = 1e300;
@@ -1279,7 +1366,7 @@ Plan plan_product(int64_t rows, int64_t cols, int64_t depth, bool a_mn, bool b_m
           if (parts > 1 && (rest == 0 || parts * 2 > steps || rest * parts > 2 * units ||
                             (!split && whole > 0)))
             break;
-          Plan p{cg, bn, parts > 1 ? whole : tiles, parts, parts > 1 ? rest : 0,
+          Plan p{cg, bn, parts > 1 ? whole : tiles, parts, parts > 1 ? rest : 0, false,
                  fills ? free : 0, early, 0.0, 0.0, 0};
           if (p.part_bytes() > (int64_t{64} << 20)) break;
           const int items = rest * parts, rounds = (items + units - 1) / units;
@@ -1293,6 +1380,12 @@ Plan plan_product(int64_t rows, int64_t cols, int64_t depth, bool a_mn, bool b_m
           p.us = (end > late_us ? end : late_us) + ends;
           if (parts > 1) p.us += 3.0 + p.part_bytes() * 2 / 5.0e6;
           if (p.us < best.us) best = p;
+          // A cluster's parts: 2.5 for the exchange.  (36 clusters of 4 fit.)
+          if (cg == 1 && !a_mn && whole == 0 && ((parts == 2 && items <= 152) || (parts == 4 && items <= 144))) {
+            p.gather = true;
+            p.us = end + ends + 2.5;
+            if (p.us < best.us) best = p;
+          }
         }
       }
     }
@@ -1308,12 +1401,12 @@ struct Pending {
   float* parts;
 };
 
-template <int CG, bool A_MN, bool B_MN, Kind KIND, bool ROWS>
+template <int CG, bool A_MN, bool B_MN, Kind KIND, bool ROWS, bool GATHER = false>
 cudaError_t launch_shape(const Product& p, Pending* w, Chain* chain) {
   ProductArgs& a = w->a;
   const Plan& plan = w->plan;
   const int bn = plan.bn;
-  auto kernel = linear_product_kernel<CG, A_MN, B_MN, KIND, ROWS>;
+  auto kernel = linear_product_kernel<CG, A_MN, B_MN, KIND, ROWS, GATHER>;
   static std::mutex mu;
   static bool configured[64] = {false};
   int dev = 0, sms = 0;
@@ -1341,18 +1434,20 @@ cudaError_t launch_shape(const Product& p, Pending* w, Chain* chain) {
   a.splits = plan.splits;
   a.early_units = plan.early_units;
   a.early_tiles = plan.early_tiles;
-  if (plan.splits > 1) {
+  if (plan.splits > 1 && !GATHER) {
     e = make_out_map(&a.parts, w->parts, CG * kBlockRows, bn, bn, plan.tail * plan.splits,
                      CG * kBlockRows * bn, true);
     if (e != cudaSuccess) return e;
   }
   const int64_t units = sms / CG, tiles = plan.whole + int64_t{plan.tail} * plan.splits;
   const unsigned grid = static_cast<unsigned>(CG * (tiles < units ? tiles : units));
+  if (GATHER)  // a CTA for each item
+    return chain->launch(kernel, dim3(static_cast<unsigned>(tiles)), kProductThreads, kSmem, plan.splits, a);
   return chain->launch(kernel, dim3(grid), kProductThreads, kSmem, CG, a);
 }
 
 cudaError_t launch_join(const Pending& w, Chain* chain) {
-  if (w.plan.splits == 1) return cudaSuccess;
+  if (w.plan.splits == 1 || w.plan.gather) return cudaSuccess;
   const int64_t high = w.rows < w.plan.cg * kBlockRows ? w.rows : w.plan.cg * kBlockRows;
   const dim3 grid(static_cast<unsigned>((high * (w.plan.bn / 8) + 255) / 256), w.plan.tail);
   return w.plan.cg == 2 ? chain->launch(linear_join_kernel<256>, grid, 256, 0, 1, w.a, w.parts)
@@ -1361,6 +1456,10 @@ cudaError_t launch_join(const Pending& w, Chain* chain) {
 
 template <bool A_MN, bool B_MN, Kind KIND>
 cudaError_t launch_kind(const Product& p, Pending* w, Chain* chain) {
+  if constexpr (!A_MN)
+    if (w->plan.gather)
+      return w->a.e.vec ? launch_shape<1, A_MN, B_MN, KIND, false, true>(p, w, chain)
+                        : launch_shape<1, A_MN, B_MN, KIND, true, true>(p, w, chain);
   if constexpr (KIND != kFloat)
     if (!w->a.e.vec)
       return w->plan.cg == 2 ? launch_shape<2, A_MN, B_MN, KIND, true>(p, w, chain)
@@ -1700,8 +1799,8 @@ BackwardPlan plan_backward(const zero_linear_t& s, bool dx, bool dw) {
   const auto second = [&](const Plan* follows) {
     return plan_product(s.out, s.in, s.rows, true, true, follows);
   };
-  if (!dw) return {first(true), Plan{2, 256, 0, 1, 0, 0, 0, 0.0, 0.0, 0}};
-  if (!dx) return {Plan{2, 256, 0, 1, 0, 0, 0, 0.0, 0.0, 0}, second(nullptr)};
+  if (!dw) return {first(true), Plan{2, 256, 0, 1, 0, false, 0, 0, 0.0, 0.0, 0}};
+  if (!dx) return {Plan{2, 256, 0, 1, 0, false, 0, 0, 0.0, 0.0, 0}, second(nullptr)};
   BackwardPlan filled{first(false), {}}, split{first(true), second(nullptr)};
   filled.dw = second(&filled.dx);
   return filled.dx.us - filled.dx.last_us + filled.dw.us <= split.dx.us + split.dw.us ? filled
