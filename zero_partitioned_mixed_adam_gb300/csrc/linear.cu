@@ -12,6 +12,7 @@
 
 #include "internal.h"
 #include "linear_epilogue.cuh"
+#include "linear_plan.hpp"
 #include "train_ops.cuh"
 #include "umma.cuh"
 
@@ -27,41 +28,6 @@ __global__ void take_linear_status_kernel() {
   g_linear_status_taken = atomicExch(&g_linear_status, 0);
 }
 
-constexpr int kDepth = 64;         // steps of the reduction in one swizzled tile: 128 bytes
-constexpr int kSub = 2;            // such tiles of each operand in one stage
-constexpr int kStep = kSub * kDepth;
-constexpr int kBlockRows = 128;    // rows of D per CTA: the lanes of tensor memory
-constexpr int kEpilogueWarps = 8;  // two per quarter of the lanes
-constexpr int kProductThreads = 64 + 32 * kEpilogueWarps;
-
-// One tile of D is CG * 128 rows by bn columns (a multiple of 32, 256 or 128 at
-// most), made by CG CTAs: each brings its own 128 rows of A and bn/CG rows of B,
-// the tensor cores read both CTAs' B (half the shared-memory traffic of two
-// tiles of their own), and each CTA's tensor memory ends up with its 128 rows.
-// The ring has as many stages as fit.  Where D has fewer rows than a tile, only
-// a_rows of A (a multiple of 8) are brought and given room: the tensor cores read
-// on into whatever lies behind, and nothing is made of those rows of D.
-constexpr int kStaging = kEpilogueWarps * 32 * 32 * 4;
-constexpr int kMaxStages = 8;
-constexpr int kBarriers = 256;
-constexpr int kSmem = 227 * 1024;
-static_assert((2 * kMaxStages + 5) * 8 <= kBarriers, "barriers, and two words");
-
-template <int CG>
-struct ProductShape {
-  static constexpr int kMaxCols = CG == 2 ? 256 : 128;
-  static constexpr int kColumns = 2 * kMaxCols;  // of tensor memory: two tiles
-};
-// Bytes of kDepth steps of one CTA's rows of A and B, and stages of the ring.
-__host__ __device__ constexpr int pair_bytes(int a_rows, int b_rows) {
-  return (a_rows + b_rows) * kDepth * 2;
-}
-__host__ __device__ constexpr int ring_stages(int a_rows, int b_rows) {
-  const int n = (kSmem - 1024 - kStaging - kBarriers) / (kSub * pair_bytes(a_rows, b_rows));
-  return n < kMaxStages ? n : kMaxStages;
-}
-static_assert(kStaging >= kBlockRows * kDepth * 2, "reads behind the last stage's A end in it");
-
 struct ProductArgs {
   CUtensorMap a, b;
   CUtensorMap out, pre;  // D and pre, where e.vec
@@ -76,18 +42,6 @@ struct ProductArgs {
   int32_t late;          // its inputs were there before its predecessor began
   int32_t early_units;   // units that the predecessor leaves idle in its last round,
   int32_t early_tiles;   // and tiles they do meanwhile
-};
-
-// The items of a unit (a CTA, or a pair): the early ones go round among the units that
-// are there early, the rest among all.
-struct Turns {
-  int early_units, early_tiles, units;
-  __device__ __forceinline__ int first(int unit) const {
-    return unit < early_units ? unit : early_tiles + unit;
-  }
-  __device__ __forceinline__ int after(int t) const {
-    return t + (t < early_tiles ? early_units : units);
-  }
 };
 
 struct Tile {
@@ -1018,8 +972,6 @@ __global__ void __launch_bounds__(256) linear_join_kernel(const __grid_constant_
 
 // ------------------------------------------------------------------ layouts
 
-__host__ __device__ constexpr int64_t round_up(int64_t x, int64_t k) { return (x + k - 1) / k * k; }
-__host__ __device__ constexpr int64_t round_up4(int64_t x) { return round_up(x, 4); }
 bool aligned(const void* p, uintptr_t k) { return (reinterpret_cast<uintptr_t>(p) & (k - 1)) == 0; }
 
 // A bf16 matrix as it lies in memory.  A single row has no pitch.
@@ -1283,116 +1235,6 @@ struct Product {
   Epilogue e;
 };
 
-// Planned for the part's 152 SMs wherever it runs, so that the sums' order and
-// the workspace follow from the sizes alone.
-constexpr int kSms = 152;
-
-// Rows of A that a CTA brings.
-int a_rows_of(int64_t rows, int cg, bool a_mn) {
-  return cg == 1 && !a_mn && rows < kBlockRows ? static_cast<int>(round_up(rows, 8)) : kBlockRows;
-}
-
-struct Plan {
-  int cg, bn;
-  int whole, splits;  // as in ProductArgs
-  int tail;           // tiles split
-  bool gather;        // the parts are a cluster's
-  int early_units, early_tiles;  // as in ProductArgs
-  double us;          // the estimate, with the wait for what it follows
-  double last_us;     // of the last round, where that has whole tiles only
-  int last_tiles;     // tiles of that round
-  int64_t part_bytes() const {
-    return splits > 1 && !gather ? int64_t{4} * tail * splits * cg * kBlockRows * bn : 0;
-  }
-};
-
-// The shape of the tiles, and how the last round of them is spread: with T tiles
-// on U units (pairs of SMs, or SMs) the tiles past the last multiple of U would
-// leave most units idle, so their reduction may be cut into parts, which are
-// joined by one more launch and two passes over them.  The least estimate in
-// microseconds is taken, fitted to a sweep of 20 shapes: a stage of 256 x 256 on
-// two SMs takes 0.65, of 256 x 128 0.47, of 128 x 128 on one SM 0.47, and no
-// narrower tile less than 0.42; a stage's distinct rows of A and B come from HBM
-// at 6.5 TB/s at best and 1.3 after they are asked for, a ring ahead, which is
-// what counts for a few rows; 3 for a kernel's beginning and end, 0.9 for each 64
-// columns of its last epilogue, 3 for the join's launch.
-//
-// follows: the product that is launched just before and does not have to end
-// first, so that this one's tiles fill its last round: units without a tile there
-// take theirs early, as many as they can do meanwhile (the first blocks of a grid
-// get the first units that are free).  split: whether tiles past the last whole
-// round may be.
-Plan plan_product(int64_t rows, int64_t cols, int64_t depth, bool a_mn, bool b_mn,
-                  const Plan* follows = nullptr, bool split = true) {
-  Plan best{2, 256, 0, 1, 0, false, 0, 0, 0.0, 0.0, 0};
-  if (rows < 1 || cols < 1) return best;
-  const int steps = static_cast<int>((depth + kStep - 1) / kStep);
-  best.us = 1e300;
-  for (int cg = 2; cg >= 1; --cg) {
-    const int most = cg == 2 ? 256 : 128;
-    // MN-major operands come in columns of 64 per CTA
-    const int unit = b_mn ? 64 * cg : 32;
-    const int units = kSms / cg, a_rows = a_rows_of(rows, cg, a_mn);
-    const int64_t tm = (rows + 128 * cg - 1) / (128 * cg);
-    for (int bn = most; bn >= unit; bn -= unit) {
-      const int64_t tn = (cols + bn - 1) / bn;
-      if (tm * tn > INT32_MAX / 64) continue;
-      const int tiles = static_cast<int>(tm * tn);
-      const double share = static_cast<double>(bn) / most;
-      const double mma = cg == 2 ? 0.40 + 0.25 * share * share : 0.42 + 0.055 * share * share;
-      const double wait = 1.3 / ring_stages(a_rows, bn / cg);
-      const double floor = mma > wait ? mma : wait;
-      const auto stage = [&](int active) {
-        const double distinct = static_cast<double>(active < tn ? active : tn) * bn +
-                                static_cast<double>(active < tm ? active : tm) * 128 * cg;
-        const double read = distinct * (2 * kStep) / 6.5e6;
-        return floor > read ? floor : read;
-      };
-      const double tile = steps * stage(units), ends = 3.0 + 0.9 * bn / 64;
-      const int taken = follows != nullptr ? follows->last_tiles * follows->cg : 0;  // SMs
-      const int free = (kSms - taken) / cg;
-      const bool fills = taken > 0 && free > 0;
-      const double begin = follows != nullptr ? follows->last_us : 0.0;
-      const int ahead = fills ? static_cast<int>(begin / tile) : 0;
-      for (int turn = ahead; turn <= ahead + (fills ? 1 : 0); ++turn) {
-        if (turn > 0 && turn > tiles / free) break;
-        const int early = turn * free, rest = (tiles - early) % units;
-        const int whole = tiles - rest;
-        const double rounds_us = (whole - early) / units * tile;
-        const double late_us = begin + rounds_us, early_us = turn * tile + rounds_us;
-        const double all_us = late_us > early_us ? late_us : early_us;
-        for (int parts = 1; parts <= 16; ++parts) {
-          // (past two rounds of parts nothing was ever gained)
-          if (parts > 1 && (rest == 0 || parts * 2 > steps || rest * parts > 2 * units ||
-                            (!split && whole > 0)))
-            break;
-          Plan p{cg, bn, parts > 1 ? whole : tiles, parts, parts > 1 ? rest : 0, false,
-                 fills ? free : 0, early, 0.0, 0.0, 0};
-          if (p.part_bytes() > (int64_t{64} << 20)) break;
-          const int items = rest * parts, rounds = (items + units - 1) / units;
-          const double last =
-              items > 0 ? rounds * ((steps + parts - 1) / parts) * stage(items < units ? items : units) : 0.0;
-          if (parts == 1) {
-            p.last_us = rest > 0 ? last : 0.0;
-            p.last_tiles = rest;
-          }
-          const double end = fills && items <= free ? early_us + last : all_us + last;
-          p.us = (end > late_us ? end : late_us) + ends;
-          if (parts > 1) p.us += 3.0 + p.part_bytes() * 2 / 5.0e6;
-          if (p.us < best.us) best = p;
-          // A cluster's parts: 2.5 for the exchange.  (36 clusters of 4 fit.)
-          if (cg == 1 && !a_mn && whole == 0 && ((parts == 2 && items <= 152) || (parts == 4 && items <= 144))) {
-            p.gather = true;
-            p.us = end + ends + 2.5;
-            if (p.us < best.us) best = p;
-          }
-        }
-      }
-    }
-  }
-  return best;
-}
-
 // A product under way: what its join needs, where its reduction is split.
 struct Pending {
   ProductArgs a;
@@ -1432,18 +1274,18 @@ cudaError_t launch_shape(const Product& p, Pending* w, Chain* chain) {
   a.bn = bn;
   a.whole = plan.whole;
   a.splits = plan.splits;
-  a.early_units = plan.early_units;
+  const int64_t units = grid_units(plan, sms);
+  a.early_units = early_units_on(plan, units);
   a.early_tiles = plan.early_tiles;
   if (plan.splits > 1 && !GATHER) {
     e = make_out_map(&a.parts, w->parts, CG * kBlockRows, bn, bn, plan.tail * plan.splits,
                      CG * kBlockRows * bn, true);
     if (e != cudaSuccess) return e;
   }
-  const int64_t units = sms / CG, tiles = plan.whole + int64_t{plan.tail} * plan.splits;
-  const unsigned grid = static_cast<unsigned>(CG * (tiles < units ? tiles : units));
   if (GATHER)  // a CTA for each item
-    return chain->launch(kernel, dim3(static_cast<unsigned>(tiles)), kProductThreads, kSmem, plan.splits, a);
-  return chain->launch(kernel, dim3(grid), kProductThreads, kSmem, CG, a);
+    return chain->launch(kernel, dim3(static_cast<unsigned>(plan.tail * plan.splits)), kProductThreads,
+                         kSmem, plan.splits, a);
+  return chain->launch(kernel, dim3(static_cast<unsigned>(CG * units)), kProductThreads, kSmem, CG, a);
 }
 
 cudaError_t launch_join(const Pending& w, Chain* chain) {
@@ -1781,33 +1623,6 @@ int read_and_clear_linear_status(int* status) {
   *status = v;
   return 0;
 }
-
-namespace {
-
-Plan plan_forward(const zero_linear_t& s) {
-  return plan_product(s.rows, s.out, s.in, false, false);
-}
-
-// dw's tiles fill dx's last round, or dx's last round is split.
-struct BackwardPlan {
-  Plan dx, dw;
-};
-BackwardPlan plan_backward(const zero_linear_t& s, bool dx, bool dw) {
-  const auto first = [&](bool split) {
-    return plan_product(s.rows, s.in, s.out, false, true, nullptr, split);
-  };
-  const auto second = [&](const Plan* follows) {
-    return plan_product(s.out, s.in, s.rows, true, true, follows);
-  };
-  if (!dw) return {first(true), Plan{2, 256, 0, 1, 0, false, 0, 0, 0.0, 0.0, 0}};
-  if (!dx) return {Plan{2, 256, 0, 1, 0, false, 0, 0, 0.0, 0.0, 0}, second(nullptr)};
-  BackwardPlan filled{first(false), {}}, split{first(true), second(nullptr)};
-  filled.dw = second(&filled.dx);
-  return filled.dx.us - filled.dx.last_us + filled.dw.us <= split.dx.us + split.dw.us ? filled
-                                                                                      : split;
-}
-
-}  // namespace
 
 int64_t linear_workspace(const zero_linear_t& s, int32_t flags) {
   const bool in_place = (flags & ZERO_LINEAR_ALIGNED) != 0;
