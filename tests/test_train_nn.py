@@ -1,0 +1,54 @@
+"""nn.linear's autograd function on the host: the two library calls are replaced by products in
+64 bits that take their arguments as the library does."""
+import pytest
+import torch
+
+from zero_partitioned_mixed_adam_gb300 import nn, train_ops
+
+
+def as_the_library(*matrices):
+    for t in matrices:
+        if t is not None and train_ops._matrix("matrix", t, *t.shape) < t.shape[1]:
+            raise RuntimeError("a pitch below the width")
+
+
+def forward(x, w, y, *, bias=None, act=0, residual=None, pre=None):
+    as_the_library(x, w, y, residual, pre)
+    assert act == 0 and pre is None
+    z = x.double() @ w.double().t()
+    if bias is not None:
+        train_ops._vector("bias", bias, w.shape[0])
+        z = z + bias.double()
+    y.copy_(z if residual is None else z + residual.double())
+
+
+def backward(dy, x, w, *, dx=None, dw=None, dbias=None, act=0, pre=None):
+    as_the_library(dy, x, w, dx, dw)
+    for out, value in ((dx, lambda: dy.double() @ w.double()),
+                       (dw, lambda: dy.double().t() @ x.double()),
+                       (dbias, lambda: dy.double().sum(0))):
+        if out is not None:
+            out.copy_(value())
+
+
+@pytest.fixture(autouse=True)
+def on_the_host(monkeypatch):
+    monkeypatch.setattr(nn, "zero_linear_forward", torch.no_grad()(forward))
+    monkeypatch.setattr(nn, "zero_linear_backward", torch.no_grad()(backward))
+
+
+def leaf(*shape, seed=0):
+    gen = torch.Generator().manual_seed(seed)
+    return torch.randn(*shape, generator=gen).bfloat16().requires_grad_()
+
+
+def test_second_order_gradients_are_refused():
+    """A gradient penalty needs the backward pass's own gradient, which the library does not
+    have: asking for it is an error, not a gradient without the penalty's part."""
+    x, w = leaf(5, 8, seed=1), leaf(6, 8, seed=2)
+    y = nn.linear(x, w)
+    dx, = torch.autograd.grad(y.float().square().sum(), x, create_graph=True)
+    with pytest.raises(RuntimeError):
+        (dx.float().square().sum() + y.float().sum()).backward()
+    first = torch.autograd.grad(nn.linear(x, w).float().sum(), (x, w), create_graph=True)
+    assert [g.shape for g in first] == [x.shape, w.shape]     # the first order is there as ever

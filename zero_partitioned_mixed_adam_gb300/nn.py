@@ -1,11 +1,13 @@
 """Linear maps for PyTorch's autograd, over zero_linear_forward and zero_linear_backward.
 
-linear(x, weight, bias, act, residual) is act(x weight^T + bias) + residual in one launch,
-and its backward pass the library's.  Everything is bf16 on the GPU with fp32 sums.
+linear(x, weight, bias, act, residual) is act(x weight^T + bias) + residual in one launch, and
+its backward pass the library's; a gradient of that (a second order) is refused.
+Everything is bf16 on the GPU with fp32 sums.
 """
 from __future__ import annotations
 
 import torch
+from torch.autograd.function import once_differentiable
 
 from . import (ZERO_ACT_GELU, ZERO_ACT_NONE, ZERO_ACT_RELU, ZERO_ACT_SILU, zero_linear_backward,
                zero_linear_forward)
@@ -36,6 +38,7 @@ class _Linear(torch.autograd.Function):
         return y.view(*x.shape[:-1], out)
 
     @staticmethod
+    @once_differentiable  # the gradients of dx, dw and dbias are not the library's: no second order
     def backward(ctx, grad):
         rows, w, pre = ctx.saved_tensors
         need_x, need_w, need_b, _, need_r = ctx.needs_input_grad
