@@ -52,3 +52,44 @@ def test_second_order_gradients_are_refused():
         (dx.float().square().sum() + y.float().sum()).backward()
     first = torch.autograd.grad(nn.linear(x, w).float().sum(), (x, w), create_graph=True)
     assert [g.shape for g in first] == [x.shape, w.shape]     # the first order is there as ever
+
+
+def reference(x, w, b=None, r=None):
+    x, w, b, r = (t if t is None else t.detach().double().requires_grad_() for t in (x, w, b, r))
+    z = x @ w.t()
+    z = z if b is None else z + b
+    return (z if r is None else z + r), (x, w, b, r)
+
+
+def near(got, want):
+    assert got.shape == want.shape
+    assert (got.double() - want).abs().max() <= 2.0 ** -7 * want.abs().max()
+
+
+@pytest.mark.parametrize("out", [1, 6])
+def test_expanded_gradients(out):
+    """The gradient of a sum over rows has the row stride 0; that of a whole sum, both."""
+    x, w, c = leaf(5, 8, seed=1), leaf(out, 8, seed=2), leaf(out, seed=3).detach()
+    for loss in (lambda y: (y.sum(0) * c.to(y.dtype)).sum(), lambda y: y.sum()):
+        x.grad = w.grad = None
+        loss(nn.linear(x, w)).backward()
+        z, (rx, rw, _, _) = reference(x, w)
+        loss(z).backward()
+        near(x.grad, rx.grad)
+        near(w.grad, rw.grad)
+
+
+@pytest.mark.parametrize("width", [1, 8])
+def test_expanded_and_overlapping_inputs(width):
+    w, b, r = leaf(6, width, seed=2), leaf(1, seed=3).expand(6), leaf(6, seed=4).expand(5, 6)
+    rows = leaf(width + 4, seed=1)
+    for x in (leaf(width, seed=1).expand(5, width), rows.unfold(0, width, 1)):
+        y = nn.linear(x, w, b, residual=r)
+        near(y, reference(x, w, b, r)[0])
+    v = leaf(width, seed=1)
+    nn.linear(v.expand(5, width), w).sum().backward()
+    want, (rx, _, _, _) = reference(v.expand(5, width), w)
+    want.sum().backward()
+    near(v.grad, rx.grad.sum(0))
+    row = leaf(width, seed=5)
+    near(nn.linear(leaf(5, width), row.expand(6, width)), reference(leaf(5, width), row.expand(6, width))[0])

@@ -17,9 +17,11 @@ ACTS = {None: ZERO_ACT_NONE, "none": ZERO_ACT_NONE, "relu": ZERO_ACT_RELU, "gelu
 
 
 def _rows(x, width):
-    """x as a matrix with contiguous columns (a copy only where it has to be)."""
+    """x as a matrix with contiguous columns and rows that do not overlap (a copy only where
+    it has to be: of columns apart, and of expanded tensors, whose strides are 0)."""
     x = x.reshape(-1, width)
-    return x if width == 1 or x.stride(1) == 1 else x.contiguous()
+    rows, pitch, step = x.shape[0], *x.stride()
+    return x if (width == 1 or step == 1) and (rows <= 1 or pitch >= width) else x.contiguous()
 
 
 class _Linear(torch.autograd.Function):
@@ -31,7 +33,8 @@ class _Linear(torch.autograd.Function):
         y = torch.empty((rows.shape[0], out), dtype=torch.bfloat16, device=x.device)
         keep = act != ZERO_ACT_NONE and any(ctx.needs_input_grad[:3])
         pre = torch.empty_like(y) if keep else None
-        zero_linear_forward(rows, w, y, bias=bias, act=act, pre=pre,
+        zero_linear_forward(rows, w, y, act=act, pre=pre,
+                            bias=None if bias is None else bias.contiguous(),
                             residual=None if residual is None else _rows(residual, out))
         ctx.save_for_backward(rows, w, pre)
         ctx.act, ctx.shape, ctx.has_bias = act, x.shape, bias is not None
