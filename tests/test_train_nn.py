@@ -93,3 +93,16 @@ def test_expanded_and_overlapping_inputs(width):
     near(v.grad, rx.grad.sum(0))
     row = leaf(width, seed=5)
     near(nn.linear(leaf(5, width), row.expand(6, width)), reference(leaf(5, width), row.expand(6, width))[0])
+
+
+@pytest.mark.parametrize("lead", [(5,), (2, 3), ()])
+def test_in_place_on_the_output(lead):
+    """The output is a tensor of its own, which may be written in place like any other."""
+    x, w = leaf(*lead, 8, seed=1), leaf(6, 8, seed=2)
+    y = nn.linear(x, w)
+    near(y.mul_(2.0).add_(1.0), 2 * reference(x, w)[0] + 1)
+    y.sum().backward()
+    z, (rx, rw, _, _) = reference(x, w)
+    (2 * z).sum().backward()
+    near(x.grad, rx.grad)
+    near(w.grad, rw.grad)

@@ -30,15 +30,17 @@ class _Linear(torch.autograd.Function):
         out, width = weight.shape
         rows = _rows(x, width)
         w = _rows(weight, width)
-        y = torch.empty((rows.shape[0], out), dtype=torch.bfloat16, device=x.device)
+        # of x's shape from the start: a view made here could not be written in place
+        y = torch.empty((*x.shape[:-1], out), dtype=torch.bfloat16, device=x.device)
+        flat = y.view(-1, out)
         keep = act != ZERO_ACT_NONE and any(ctx.needs_input_grad[:3])
-        pre = torch.empty_like(y) if keep else None
-        zero_linear_forward(rows, w, y, act=act, pre=pre,
+        pre = torch.empty_like(flat) if keep else None
+        zero_linear_forward(rows, w, flat, act=act, pre=pre,
                             bias=None if bias is None else bias.contiguous(),
                             residual=None if residual is None else _rows(residual, out))
         ctx.save_for_backward(rows, w, pre)
         ctx.act, ctx.shape, ctx.has_bias = act, x.shape, bias is not None
-        return y.view(*x.shape[:-1], out)
+        return y
 
     @staticmethod
     @once_differentiable  # the gradients of dx, dw and dbias are not the library's: no second order
