@@ -459,3 +459,17 @@ def test_a_wait_that_runs_out_is_reported():
     want = host(x) @ host(w).T
     assert np.abs(host(y) - want).max() <= 2.0 ** -7 * np.abs(want).max()
     assert za.device_status() == za.ZERO_OK
+
+
+def test_few_rows_of_the_greatest_width():
+    """in = 2^31 - 2, the largest taken: the columns past the last whole round are counted
+    without overflow.  Zeros but for ones at both ends and in between, so sums are exact."""
+    k = 2 ** 31 - 2
+    x = torch.zeros(2, k + 2, dtype=BF, device="cuda")[:, :k]
+    w = torch.zeros(3, k + 2, dtype=BF, device="cuda")[:, :k]
+    at = torch.tensor([0, 5, 1023, 2 ** 30, k - 2000, k - 1025, k - 1024, k - 9, k - 2, k - 1], device="cuda")
+    x[0, at], x[1, at[::2]] = 1.0, 2.0
+    w[0, at], w[1, at[-1]], w[2, at[1:]] = 1.0, 3.0, 1.0
+    y = empty((2, 3))
+    za.zero_linear_forward(x, w, y)
+    assert y.tolist() == [[10.0, 3.0, 9.0], [10.0, 0.0, 8.0]]

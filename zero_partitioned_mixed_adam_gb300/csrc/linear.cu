@@ -1378,9 +1378,10 @@ struct FewArgs {
   Epilogue e;
 };
 
-// 8 elements from p[j] on; those from n on are 0.
+// 8 elements from p[j] on; those from n on are 0.  (Columns are counted without a
+// sign: n may be 2^31 - 2, and a warp's place passes it by up to a round of the block.)
 template <bool VEC, bool STREAM>
-__device__ __forceinline__ uint4 few_load(const uint16_t* p, int j, int n) {
+__device__ __forceinline__ uint4 few_load(const uint16_t* p, uint32_t j, uint32_t n) {
   if (VEC && j + 8 <= n) {
     uint4 v;
     if (STREAM)
@@ -1428,19 +1429,20 @@ __global__ void __launch_bounds__(32 * kFewWarps, U == 2 ? 5 : 3)
     const uint16_t* x[NT];  // rows past the end: row 0's, in sums that are not stored
 #pragma unroll
     for (int n = 0; n < NT; ++n) x[n] = a.x + (8 * n + g < a.rows ? 8 * n + g : 0) * a.ldx;
-    for (int k0 = kSpan * mine; k0 < a.depth; k0 += kSpan * share) {
-      const int j = k0 + 8 * t;
+    const uint32_t depth = a.depth;
+    for (uint32_t k0 = kSpan * mine; k0 < depth; k0 += kSpan * share) {
+      const uint32_t j = k0 + 8 * t;
       uint4 u[U], v[U];
 #pragma unroll
       for (int q = 0; q < U; ++q) {
-        u[q] = few_load<VEC, true>(w0, j + 32 * q, a.depth);
-        v[q] = few_load<VEC, true>(w1, j + 32 * q, a.depth);
+        u[q] = few_load<VEC, true>(w0, j + 32 * q, depth);
+        v[q] = few_load<VEC, true>(w1, j + 32 * q, depth);
       }
 #pragma unroll
       for (int q = 0; q < U; ++q) {
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-          const uint4 y = few_load<VEC, false>(x[n], j + 32 * q, a.depth);
+          const uint4 y = few_load<VEC, false>(x[n], j + 32 * q, depth);
           warp_mma(acc[n], u[q].x, v[q].x, u[q].y, v[q].y, y.x, y.y);
           warp_mma(acc[n], u[q].z, v[q].z, u[q].w, v[q].w, y.z, y.w);
         }
