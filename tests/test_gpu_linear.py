@@ -473,3 +473,30 @@ def test_few_rows_of_the_greatest_width():
     y = empty((2, 3))
     za.zero_linear_forward(x, w, y)
     assert y.tolist() == [[10.0, 3.0, 9.0], [10.0, 0.0, 8.0]]
+
+
+@pytest.mark.parametrize("handle", [False, True])
+def test_a_call_on_another_stream_leaves_freed_memory_alone(handle):
+    """Memory that the current stream has freed but not yet done with is not the workspace of
+    a call on another stream, which may run long before."""
+    m, k, n = 300, 520, 264
+    x, w, dy, pre = (normal(s, 1.0, i) for i, s in enumerate([(m, k), (n, k), (m, n), (m, n)]))
+    dx, dw = empty((m, k)), empty((n, k), F32)
+    need = za.zero_linear_workspace(m, k, n, True)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    # of the sizes that a workspace may have, in one block or in parts of one
+    temporaries = [torch.full((size,), 77, dtype=torch.uint8, device="cuda") for size in (need, need, 20 << 20)]
+    seen = [torch.empty_like(t) for t in temporaries]
+    torch.cuda.synchronize()
+    torch.cuda._sleep(200_000_000)
+    for t, s in zip(temporaries, seen):
+        s.copy_(t)
+    del temporaries, t
+    for _ in range(4):
+        za.zero_linear_backward(dy, x, w, dx=dx, dw=dw, act=3, pre=pre,
+                                stream=side.cuda_stream if handle else side)
+    side.synchronize()
+    torch.cuda.synchronize()
+    assert all(bool((s == 77).all()) for s in seen)

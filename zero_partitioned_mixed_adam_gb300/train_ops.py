@@ -76,9 +76,10 @@ def _vector(name, t, n, dtypes=_BF16):
 
 
 def _linear_workspace(shape, flags, bases, pitches, workspace, device, stream):
-    """The caller's workspace, or one from PyTorch's allocator that is kept from reuse
-    until `stream` is past the call; and its bytes.  bases, pitches: those of the matrices
-    (and the bias) that the products read, or-ed together."""
+    """The caller's workspace, or one from PyTorch's allocator; and its bytes.  The allocator
+    hands memory out, and takes it back, in the order of the stream that is current when it
+    is asked, so it is asked on `stream`.  bases, pitches: those of the matrices (and the
+    bias) that the products read, or-ed together."""
     if workspace is not None:
         return workspace, workspace.numel() * workspace.element_size()
     if bases % 16 == 0 and pitches % 8 == 0:
@@ -88,11 +89,12 @@ def _linear_workspace(shape, flags, bases, pitches, workspace, device, stream):
         raise ZeroError(need, "zero_linear_workspace")
     if need == 0:
         return None, 0
-    workspace = torch.empty(need, dtype=torch.uint8, device=device)
-    if stream is not None:
-        workspace.record_stream(stream if not isinstance(stream, int)
-                                else torch.cuda.ExternalStream(stream, device))
-    return workspace, need
+    if stream is None:
+        return torch.empty(need, dtype=torch.uint8, device=device), need
+    if isinstance(stream, int):
+        stream = torch.cuda.ExternalStream(stream, device)
+    with torch.cuda.stream(stream):
+        return torch.empty(need, dtype=torch.uint8, device=device), need
 
 
 def zero_linear_workspace(rows: int, width_in: int, width_out: int, backward: bool = False,
