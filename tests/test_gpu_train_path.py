@@ -114,3 +114,19 @@ def test_example_learns(eight):
     losses = mod.train(steps=60, eight_bit=eight)
     assert losses[-1] < 0.5 * losses[0]
     assert za.device_status() == za.ZERO_OK
+
+
+@pytest.mark.parametrize("eight", [False, True])
+def test_a_replaced_parameter_is_the_one_stepped(eight):
+    """p.data = ... between two steps with the same gradient buffers: the new storage gets the
+    weights, the old one is left alone."""
+    params = [leaf(70, 33, seed=1).detach(), leaf(33, seed=2).detach()]
+    grads = [leaf(70, 33, seed=3).detach(), leaf(33, seed=4).detach()]
+    opt = TensorAdamW(params, lr=1e-2, eight_bit=eight, grads=grads)
+    opt.step()
+    old, before = params[0].data, params[0].clone()
+    params[0].data = torch.zeros_like(old)
+    opt.step()
+    assert torch.equal(old, before)
+    for p, w in zip(params, opt.master):
+        assert torch.equal(p, w.bfloat16())

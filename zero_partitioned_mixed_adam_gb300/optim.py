@@ -125,18 +125,20 @@ class TensorAdamW:
             self.v_scale = [torch.zeros(b, dtype=torch.float32, device=dev) for b in blocks]
         self.norm = torch.zeros(2, dtype=torch.float32, device=dev)  # of the last step, and its clip
         self._workspace = grad_norm_workspace(dev)
-        self._list = None
+        self._list = self._at = None
 
     def _tensors(self):
         grads = self.grads if self.grads is not None else [p.grad for p in self.params]
         if any(g is None for g in grads):
             raise ValueError("a parameter has no gradient")
-        known = self._list
-        if known is None or any(a is not b or a.data_ptr() != p for a, b, p in
-                                zip(grads, known.grads.buffers, known.grads.ptrs)):
+        columns = (grads, self.params, self.master, self.m, self.v, self.m_scale or (),
+                   self.v_scale or ())
+        at = [t.data_ptr() for c in columns for t in c] + [g.dtype for g in grads]
+        if self._list is None or at != self._at:  # marshalled anew once anything has moved
             self._list = adamw_tensors(grads, self.master, self.m, self.v, params=self.params,
                                        m_scale=self.m_scale, v_scale=self.v_scale,
                                        weight_decay=self.decay)
+            self._at = at
         return self._list
 
     def step(self, stream=None):
