@@ -130,3 +130,18 @@ def test_a_replaced_parameter_is_the_one_stepped(eight):
     assert torch.equal(old, before)
     for p, w in zip(params, opt.master):
         assert torch.equal(p, w.bfloat16())
+
+
+def test_moments_between_steps():
+    """The values of 8-bit moments with the gradients set to None, and before the first step."""
+    params = [leaf(70, 33, seed=1).detach(), leaf(33, seed=2).detach()]
+    opt = TensorAdamW(params, lr=1e-2, eight_bit=True)
+    assert not any(x.any() for xs in opt.moments() for x in xs)
+    for p in params:
+        p.grad = torch.ones_like(p)
+    opt.step()
+    for p in params:
+        p.grad = None
+    m, v = opt.moments()
+    for x, want in ((m, 0.1), (v, 1e-3)):      # 3 bits after the first, rounded either way
+        assert all(((t / want - 1.0).abs() <= 2.0 ** -3).all() for t in x)

@@ -49,3 +49,19 @@ def test_replaced_storage_is_noticed(eight, own_grads):
         opt.grads = grads + [torch.zeros(3)]
         with pytest.raises(ValueError):              # one gradient too many
             opt._tensors()
+
+
+def test_moments_need_no_gradients(monkeypatch):
+    """A checkpoint is taken between steps, where gradients are usually None."""
+    opt, calls = optimizer(eight=True), []
+    monkeypatch.setattr(optim, "zero_adamw_state_f32", lambda lst, m, v: calls.append((lst, m, v)))
+    for p in opt.params:
+        p.grad = None
+    m, v = opt.moments()
+    (lst, *outs), = calls
+    assert outs[0] is m and outs[1] is v and lst.flags & za.ZERO_STATE_8BIT
+    for i, p in enumerate(opt.params):
+        assert m[i].shape == v[i].shape == p.shape and lst.arr[i].numel == p.numel()
+        assert lst.arr[i].m == opt.m[i].data_ptr() and lst.arr[i].v_scale == opt.v_scale[i].data_ptr()
+    with pytest.raises(ValueError):
+        opt._tensors()                               # a step does need them

@@ -165,7 +165,10 @@ class TensorAdamW:
             return self.m, self.v
         out = [[torch.empty(p.shape, dtype=torch.float32, device=p.device) for p in self.params]
                for _ in range(2)]
-        zero_adamw_state_f32(self._tensors(), *out)
+        # (the parameters in place of gradients, which may be None: only their sizes are used)
+        codes = adamw_tensors(self.params, self.master, self.m, self.v, m_scale=self.m_scale,
+                              v_scale=self.v_scale)
+        zero_adamw_state_f32(codes, *out)
         return out[0], out[1]
 
     def state_bytes(self):
