@@ -65,3 +65,15 @@ def test_moments_need_no_gradients(monkeypatch):
         assert lst.arr[i].m == opt.m[i].data_ptr() and lst.arr[i].v_scale == opt.v_scale[i].data_ptr()
     with pytest.raises(ValueError):
         opt._tensors()                               # a step does need them
+
+
+def test_a_grad_scale_of_another_type_is_refused():
+    """The step reads 4 bytes of it as fp32, whatever they are."""
+    opt = optimizer()
+    for bad in (torch.tensor([0.5]).bfloat16(), torch.tensor([0.5], dtype=torch.float64), torch.tensor([1]),
+                torch.zeros(0)):
+        with pytest.raises(ValueError):
+            za.zero_adamw_step(opt._tensors(), lr=1e-3, t=1, grad_scale=bad)
+    none = za.adamw_tensors([], [], [], [])
+    for good in (None, torch.tensor(0.5), torch.tensor([0.5]), torch.ones(2)[1:], 1 << 40):
+        za.zero_adamw_step(none, lr=1e-3, t=1, grad_scale=good)     # nothing to step: no launch

@@ -293,6 +293,8 @@ def zero_adamw_step(tensors: AdamwTensors, *, lr: float, beta1: float = 0.9, bet
 
     grad_scale: one fp32 on the device that multiplies every gradient, or None;
     seed: of the stochastic rounding of 8-bit moments, a new one every step."""
+    if hasattr(grad_scale, "dtype") and (grad_scale.dtype != torch.float32 or grad_scale.numel() < 1):
+        raise ValueError(f"grad_scale: expected one fp32, got {tuple(grad_scale.shape)} {grad_scale.dtype}")
     rc = _lib.zero_adamw_step(len(tensors), tensors.arr, tensors.flags, lr, beta1, beta2, eps, t,
                               _addr(grad_scale), seed & 0xFFFFFFFF, _stream_handle(stream))
     if rc != ZERO_OK:
