@@ -62,14 +62,14 @@ extern "C" {
 #define ZERO_E_RANK (-4)    /* rank not in [0, world) and not ZERO_ALL_RANKS        */
 #define ZERO_E_STEP (-5)    /* t < 1 (t is the 1-based step count after increment)  */
 #define ZERO_E_ALIGN (-6)   /* bf16 pointer odd, or fp32 pointer not 4-byte aligned */
-#define ZERO_E_HPARAM (-7)  /* lr/eps negative or not finite; beta not in [0, 1)    */
-#define ZERO_E_LAYOUT (-8)  /* unknown layout, or a shard layout with ALL_RANKS     */
+#define ZERO_E_HPARAM (-7)  /* lr/eps (weight_decay, max_norm) < 0 or not finite; beta not in [0, 1) */
+#define ZERO_E_LAYOUT (-8)  /* unknown layout, activation or flag, or a shard layout with ALL_RANKS */
 #define ZERO_E_PLAN (-9)    /* the plan's fields are not those zero_plan computes   */
 #define ZERO_E_ALIAS (-10)  /* an output buffer overlaps another buffer             */
 #define ZERO_E_LAUNCH (-11) /* the CUDA launch failed; see zero_strerror            */
 #define ZERO_E_DEVICE (-12) /* no usable CUDA device                                */
 #define ZERO_E_RANGE (-13)  /* zero_adam_step_range: begin < 0 or end < begin       */
-#define ZERO_E_SHAPE (-14)  /* zero3_unit_gather_rows: bad tensor count or shape    */
+#define ZERO_E_SHAPE (-14)  /* a tensor count, size or pitch is out of the call's range */
 #define ZERO_E_TIMEOUT (-15) /* a kernel gave up a bounded wait (zero_device_status) */
 #define ZERO_E_HOOK (-16)    /* a test hook was called without ZEROADAM_TEST_HOOKS=1 */
 #define ZERO_E_WORKSPACE (-17) /* the workspace is NULL, misaligned or too small     */

@@ -201,3 +201,10 @@ def test_side_by_side_columns_are_no_overlap():
     # the residual as another pair of columns: only the overlapping one is refused
     assert LIB.zero_linear_forward(ctypes.byref(s), at(1), at(2), None, 0, None, None,
                                    at(1) + 2 * 16, at(9), GIB, None) == CODES["ZERO_E_ALIAS"]
+
+
+def test_messages_name_what_these_calls_refuse():
+    """The statuses are shared with the ZeRO step and the gathers; so are their messages."""
+    for code, words in (("ZERO_E_SHAPE", ("pitch", "count", "size")), ("ZERO_E_HPARAM", ("weight_decay", "max_norm", "betas")),
+                        ("ZERO_E_LAYOUT", ("activation", "flag", "layout"))):
+        assert all(w in za.strerror(CODES[code]) for w in words)

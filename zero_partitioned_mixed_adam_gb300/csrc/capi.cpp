@@ -430,8 +430,10 @@ const char* zero_strerror(int status) {
     case ZERO_E_RANK: return "rank must be in [0, world) or ZERO_ALL_RANKS";
     case ZERO_E_STEP: return "t must be >= 1 (1-based step count)";
     case ZERO_E_ALIGN: return "bf16 pointers must be 2-byte and fp32 pointers 4-byte aligned";
-    case ZERO_E_HPARAM: return "lr and eps must be finite and >= 0, betas in [0, 1)";
-    case ZERO_E_LAYOUT: return "unknown layout, or a shard layout with ZERO_ALL_RANKS";
+    case ZERO_E_HPARAM: return "lr, eps, weight_decay and max_norm must be finite and >= 0, "
+                               "betas in [0, 1)";
+    case ZERO_E_LAYOUT: return "unknown layout, activation or flag, or a shard layout with "
+                               "ZERO_ALL_RANKS";
     case ZERO_E_PLAN: return "plan fields differ from zero_plan(numel, world)";
     case ZERO_E_ALIAS: return "an output buffer overlaps another buffer";
     case ZERO_E_DEVICE:
@@ -439,7 +441,8 @@ const char* zero_strerror(int status) {
               cudaGetErrorString(t_last_cuda == cudaSuccess ? cudaErrorNoDevice : t_last_cuda);
       return t_msg.c_str();
     case ZERO_E_RANGE: return "the window must satisfy 0 <= begin <= end";
-    case ZERO_E_SHAPE: return "ntensors in [1, ZERO_MAX_UNIT_TENSORS] and sizes >= 1 required";
+    case ZERO_E_SHAPE: return "a tensor count or a size is out of its call's range, "
+                              "or a pitch is below its matrix's width";
     case ZERO_E_TIMEOUT: return "a kernel gave up a bounded wait; that step's outputs are incomplete";
     case ZERO_E_HOOK: return "test hooks are off: they need ZEROADAM_TEST_HOOKS=1 in the environment";
     case ZERO_E_WORKSPACE: return "the workspace is NULL, not 16-byte aligned or too small";
