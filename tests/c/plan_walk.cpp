@@ -1,8 +1,10 @@
 // Walks the items that a grid's units take of a linear map's backward products, as the
 // kernels do, for `shapes` drawn sizes and the SM counts given, and prints how many
 // shapes leave an item out or take one twice.  Arguments: shapes, SM counts...
+// With "turns rows in out": how often dw's early items go round.
 #include <cstdio>
 #include <cstdlib>
+#include <cstring>
 #include <cmath>
 #include <random>
 #include <vector>
@@ -25,6 +27,12 @@ static bool every_item_once(const Plan& p, int sms) {
 }
 
 int main(int argc, char** argv) {
+  if (std::strcmp(argv[1], "turns") == 0) {
+    const Plan dw = plan_backward({std::atoll(argv[2]), std::atoll(argv[3]), std::atoll(argv[4]), 0, 0, 0, 0,
+                                   0, 0, 0, 0}, true, true).dw;
+    std::printf("%d\n", dw.early_units > 0 ? dw.early_tiles / dw.early_units : 0);
+    return 0;
+  }
   std::mt19937 rng(1);
   std::uniform_real_distribution<double> d(0.0, 1.0);
   const auto draw = [&](double low, double high) {

@@ -500,3 +500,34 @@ def test_a_call_on_another_stream_leaves_freed_memory_alone(handle):
     side.synchronize()
     torch.cuda.synchronize()
     assert all(bool((s == 77).all()) for s in seen)
+
+
+@pytest.mark.parametrize("shape", o.SHARED_ROUNDS)
+@pytest.mark.parametrize("act,act_in,dtype,add", [("none", "silu", F32, True), ("silu", "none", BF, False)])
+def test_shared_rounds_of_dx_and_dw(shape, act, act_in, dtype, add):
+    """dw's tiles go round several times among the units that dx's last round leaves idle."""
+    test_backward(shape, act, act_in, dtype, add)
+
+
+@pytest.mark.parametrize("shape", [(130, 200, 136), (300, 775, 1031), (777, 768, 2304), (1003, 71, 2311)])
+@pytest.mark.parametrize("act", ["relu", "gelu", "silu"])
+def test_backward_against_the_rounded_dz(shape, act):
+    """dx and dw are products of dz = bf16(dy act'(pre)): held to an fp32 product's error of
+    those, which is far below what the rounding itself may do.  The slope is good to 2^-17, so
+    an element of dz that lies that near to a rounding boundary may be its other neighbour."""
+    m, k, n = shape
+    x, w, dy = normal((m, k), 1.0, 1), normal((n, k), 1.0 / math.sqrt(k), 2), normal((m, n), 1.0, 3)
+    pre = normal((m, n), 1.0, 4)
+    dx, dw = empty((m, k)), empty((n, k), F32)
+    za.zero_linear_backward(dy, x, w, dx=dx, dw=dw, act=o.ACTS[act], pre=pre)
+    exact = host(dy) * o.slope(host(pre), act)
+    # what 2^-17 of a slope near 0 is to dz is not relative to dz itself
+    near = 2.0 ** -17 * (np.abs(exact) + np.abs(host(dy)))
+    low, dz, high = (o.round_bf16((exact + d).astype(np.float32)).astype(np.float64) for d in (-near, 0.0, near))
+    edz = torch.from_numpy(high - low).cuda()
+    dz = torch.from_numpy(dz).cuda()
+    want = host(dz @ w.double())
+    tol = product_error(dz, w, n) + host(edz @ w.double().abs()) + 2.0 ** -8 * np.abs(want) + 1e-30
+    check(dx, want, tol, "dx")
+    want = host(dz.t() @ x.double())
+    check(dw, want, product_error(dz.t(), x, m) + host(edz.t() @ x.double().abs()) + 1e-30, "dw")

@@ -145,3 +145,38 @@ def test_moments_between_steps():
     m, v = opt.moments()
     for x, want in ((m, 0.1), (v, 1e-3)):      # 3 bits after the first, rounded either way
         assert all(((t / want - 1.0).abs() <= 2.0 ** -3).all() for t in x)
+
+
+def test_8bit_optimizer_step_by_step():
+    """With 8-bit moments each step is AdamW in 64 bits on the moments' values before it, to
+    binary32's roundings (16 operations of 2^-22, on the magnitudes that m is a sum of), as the
+    weights take the new moments before they are encoded; and the new values are within one
+    step of their codes of the exact ones: 1/8, or the least step of the block."""
+    params = [leaf(70, 33, sigma=0.1, seed=1).detach(), leaf(33, sigma=0.1, seed=2).detach()]
+    opt = TensorAdamW(params, lr=1e-2, betas=(0.9, 0.95), weight_decay=0.1, max_norm=0.5, eight_bit=True)
+    for t in range(1, 6):
+        for i, p in enumerate(params):
+            p.grad = leaf(*p.shape, sigma=0.1, seed=10 * t + i).detach()
+        before = [[x.double().cpu().numpy() for x in xs] for xs in (*opt.moments(), opt.master)]
+        opt.step()
+        c = float(opt.norm[1])
+        assert 0.0 < c < 1.0
+        after = [[x.double().cpu().numpy() for x in xs] for xs in (*opt.moments(), opt.master)]
+        for i, p in enumerate(params):
+            m, v, w = (x[i] for x in before)
+            g = c * p.grad.double().cpu().numpy()
+            size = 0.9 * np.abs(m) + 0.1 * np.abs(g)
+            m, v = 0.9 * m + 0.1 * g, 0.95 * v + 0.05 * g * g
+            decay = 0.1 if i == 0 else 0.0
+            want = o.update(w, m, v, 1e-2, decay, 0.9, 0.95, 1e-8, t)
+            most = np.abs(o.update(np.zeros_like(w), size, v, 1e-2, 0.0, 0.9, 0.95, 1e-8, t))
+            got = after[2][i]
+            assert (np.abs(got - want) <= 16 * 2.0 ** -22 * most + 2.0 ** -23 * (np.abs(w) + np.abs(want))).all()
+            # a first step is about lr in size; an untouched weight would be that far off
+            assert (np.abs(got - w) > 1e-4).mean() > 0.8
+            for x, exact, least in ((after[0][i], m, 2.0 ** -17), (after[1][i], v, 2.0 ** -33)):
+                x, exact = x.ravel(), exact.ravel()
+                scale = np.repeat([np.abs(exact[b:b + o.BLOCK]).max() * 17 / 16 for b in range(0, len(exact), o.BLOCK)],
+                                  o.BLOCK)[:len(exact)]
+                step = np.maximum(2.0 ** -3 * np.abs(exact), least * scale)
+                assert (np.abs(x - exact) <= step * (1 + 2.0 ** -16)).all()

@@ -5,6 +5,8 @@ import subprocess
 
 import pytest
 
+from train_oracle import SHARED_ROUNDS
+
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
 
@@ -24,3 +26,10 @@ def test_every_item_is_taken_once(walk):
     got = dict(line.split() for line in r.stdout.splitlines())
     assert int(got.pop("turns")) > 100      # the drawn sizes do reach the shared rounds
     assert got == {n: "0" for n in sms}
+
+
+def test_the_shapes_of_shared_rounds_have_them(walk):
+    """The sizes that the GPU tests name so: dw's early tiles go round more than once."""
+    for shape in SHARED_ROUNDS:
+        r = subprocess.run([walk, "turns", *map(str, shape)], capture_output=True, text=True, check=True)
+        assert int(r.stdout) >= 2, shape

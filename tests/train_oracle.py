@@ -8,6 +8,8 @@ BLOCK = 256
 ACTS = {"none": 0, "relu": 1, "gelu": 2, "silu": 3}
 # the largest |act'| over all z, and |act(z)| <= |z|
 SLOPE = {"none": 1.0, "relu": 1.0, "gelu": 1.13, "silu": 1.1}
+# (rows, in, out) whose backward has several of dw's tiles on each unit that dx's last round leaves idle
+SHARED_ROUNDS = [(300, 2304, 768), (256, 4096, 1000), (600, 1024, 2048), (512, 2048, 2048), (300, 4096, 2312)]
 
 
 def act(z, name):
