@@ -531,3 +531,36 @@ def test_backward_against_the_rounded_dz(shape, act):
     check(dx, want, tol, "dx")
     want = host(dz.t() @ x.double())
     check(dw, want, product_error(dz.t(), x, m) + host(edz.t() @ x.double().abs()) + 1e-30, "dw")
+
+
+@pytest.mark.parametrize("m", [1, 16, 40, 300])
+@pytest.mark.parametrize("d", [256, 515, 1024])
+def test_one_calls_output_is_the_nexts_input(m, d):
+    """Layers in a row on one stream, each adding to its input in place and the next reading
+    that, called without a pause (a kernel begins while the one before ends): the bits of the
+    same calls with the GPU waited for after each."""
+    ws = [normal((d, d), 0.3 / math.sqrt(d), i) for i in range(4)]
+    x0, space = normal((m, d), 1.0, 9), torch.empty(za.zero_linear_workspace(m, d, d, True) + 16, dtype=torch.uint8, device="cuda")
+    dy0 = normal((m, d), 1.0, 10)
+
+    def layers(wait):
+        x, mid, dy, dw = x0.clone(), empty((m, d)), dy0.clone(), empty((d, d), F32)
+        for _ in range(10):
+            for w in ws:
+                za.zero_linear_forward(x, w, mid, act=3, workspace=space)
+                wait()
+                za.zero_linear_forward(mid, w, x, residual=x, workspace=space)
+                wait()
+                za.zero_linear_backward(dy, x, w, dx=mid, dw=dw, act=3, pre=x, workspace=space, accumulate=True)
+                wait()
+                za.zero_linear_forward(mid, w, dy, residual=dy, workspace=space)
+                wait()
+                x.mul_(0.7)
+                dy.mul_(0.7)
+        torch.cuda.synchronize()
+        return x, dy, dw
+
+    want = layers(torch.cuda.synchronize)
+    assert all(bool(t.isfinite().all()) for t in want)
+    for _ in range(3):
+        assert all(torch.equal(a, b) for a, b in zip(layers(lambda: None), want))
