@@ -161,23 +161,23 @@ __device__ __noinline__ void epilogue_scalar(const Epilogue& e, const float* min
 }
 
 // 32 columns of fp32 as they are, in the room of both slots: no send() may
-  // follow (fp32 outputs have none, and split tiles are a unit's last).
-  __device__ __forceinline__ void send_sums(const CUtensorMap* map, uint8_t* staging,
-                                            const float v[32], int x, int y, int z, bool sum,
-                                            int lane) {
-    if (lane == 0) bulk_wait_read<0>();
-    __syncwarp();
+// follow (fp32 outputs have none, and split tiles are a unit's last).
+__device__ __forceinline__ void send_sums(const CUtensorMap* map, uint8_t* staging,
+                                          const float v[32], int x, int y, int z, bool sum,
+                                          int lane) {
+  if (lane == 0) bulk_wait_read<0>();
+  __syncwarp();
 #pragma unroll
-    for (int q = 0; q < 8; ++q)
-      *reinterpret_cast<float4*>(staging + 4 * staged(lane, q)) =
-          make_float4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
-    fence_async_shared();
-    __syncwarp();
-    if (lane == 0) {
-      tile_store(map, staging, x, y, z, sum);
-      bulk_commit();
-    }
+  for (int q = 0; q < 8; ++q)
+    *reinterpret_cast<float4*>(staging + 4 * staged(lane, q)) =
+        make_float4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
+  fence_async_shared();
+  __syncwarp();
+  if (lane == 0) {
+    tile_store(map, staging, x, y, z, sum);
+    bulk_commit();
   }
+}
 
 // A 32 x 32 part, a row a lane, through shared memory and out by TMA, which takes
 // the addresses and the edges off the lanes and adds fp32 gradients to what is
