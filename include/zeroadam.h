@@ -107,6 +107,14 @@ extern "C" {
 #define ZERO_LINEAR_ALIGNED 2
 #define ZERO_LINEAR_PLAIN 4
 
+/* flag: token ids and targets are int32 (default: int64) */
+#define ZERO_IDS_I32 0x100
+
+/* kinds of norm of zero_block_norm_* */
+#define ZERO_NORM_NONE 0
+#define ZERO_NORM_RMS 1   /* x / sqrt(mean(x^2) + eps) * weight                      */
+#define ZERO_NORM_LAYER 2 /* (x - mean(x)) / sqrt(var(x) + eps) * weight + bias      */
+
 /* zero_adamw_step */
 #define ZERO_STATE_8BIT 0x80   /* flag: m and v are held as 8-bit codes with block scales */
 #define ZERO_MOMENT_BLOCK 256  /* elements that share one scale of an 8-bit moment        */
@@ -483,6 +491,163 @@ int zero_adamw_step(int32_t ntensors, const zero_adamw_tensor_t* tensors, int32_
  */
 int zero_adamw_state_f32(int32_t ntensors, const zero_adamw_tensor_t* tensors,
                          float* const* m_out, float* const* v_out, void* stream);
+
+/* ------------------------------------------- the two ends of a model, and norms */
+
+/*
+ * Sizes of a table of `vocab` rows of `width` elements looked up by `rows` ids,
+ * and the pitches (elements) of the table (or of its gradient) and of the rows
+ * looked up (or of their gradient).  1 <= width, vocab; 0 <= rows; all below 2^31.
+ */
+typedef struct {
+  int64_t rows, width, vocab;
+  int64_t ldt, ldy;
+} zero_embedding_t;
+
+/*
+ * Embedding: y[i] = bf16(scale * table[ids[i]]), the product in fp32.
+ *   table, y    bf16, any pitch and 2-byte address.
+ *   ids         int64, or int32 with ZERO_IDS_I32.  A row whose id is not in
+ *               [0, vocab) is NaN: nothing is read for it.
+ *   flags       ZERO_IDS_I32.
+ * Errors: ZERO_E_NULLPTR, ZERO_E_SHAPE, ZERO_E_LAYOUT (unknown flags),
+ * ZERO_E_HPARAM (scale not finite), ZERO_E_ALIGN, ZERO_E_ALIAS, ZERO_E_LAUNCH,
+ * ZERO_E_DEVICE.
+ */
+int zero_embedding_forward(const zero_embedding_t* shape, const void* table, const void* ids,
+                           int32_t flags, double scale, void* y, void* stream);
+
+/*
+ * Its gradient: dtable[v] = scale * (sum of dy[i] over the rows i with id v), in
+ * fp32 in an order that follows from the ids alone, and rounded once.  Rows of no
+ * token are set to zero; with ZERO_GRAD_ACCUMULATE sums are added to what is there
+ * and rows of no token are left alone.
+ *   dy          bf16.
+ *   padding     an id whose rows have no gradient (-1: none).  Rows whose id is
+ *               not in [0, vocab) have none either.
+ *   dtable      bf16, or fp32 with ZERO_GRAD_F32.
+ *   flags       ZERO_IDS_I32, ZERO_GRAD_F32, ZERO_GRAD_ACCUMULATE.
+ * No workspace.  Errors: as zero_embedding_forward.
+ */
+int zero_embedding_backward(const zero_embedding_t* shape, const void* dy, const void* ids,
+                            int32_t flags, double scale, int64_t padding, void* dtable,
+                            void* stream);
+
+/*
+ * Sizes of a linear map of `rows` tokens from `width` features onto a vocabulary,
+ * and the pitches (elements) of x, w and their gradients.  1 <= width, vocab;
+ * 0 <= rows; all below 2^31 - 1.
+ */
+typedef struct {
+  int64_t rows, width, vocab;
+  int64_t ldx, ldw, lddx, lddw;
+} zero_cross_entropy_t;
+
+/*
+ * Softmax cross entropy of z = x W^T against a target each row, and its gradient,
+ * without keeping z:
+ *   losses[i] = log(sum over j of exp(z[i][j])) - z[i][targets[i]]
+ *   total     = sum over i of c[i] * losses[i]
+ *   dz[i][j]  = c[i] * (exp(z[i][j] - log(sum ...)) - (j == targets[i]))
+ *   dx = bf16(dz W),   dw = dz^T x  (added to dw with ZERO_GRAD_ACCUMULATE).
+ * c[i] is scale[i], or without scale 1 / (number of rows that are not ignored): the
+ * mean.  An ignored row's loss and dx are 0 and it adds nothing to total and dw,
+ * whatever is in its x; if every row is ignored total and all gradients are 0.
+ *
+ *   x, w        bf16, read; any pitch and 2-byte address.
+ *   targets     int64, or int32 with ZERO_IDS_I32.  Rows whose target is
+ *               ignore_index are ignored.  Any other target that is not in
+ *               [0, vocab) is an error of the data: its row's loss is NaN, and so
+ *               are then total and the gradients.
+ *   scale       device, fp32, one a row; or NULL.
+ *   losses      fp32, one a row, written, or NULL.
+ *   total       fp32, one, written, or NULL.
+ *   dx, dw      written, or NULL to skip (both NULL: the loss alone, a third of the
+ *               work).  dw is bf16, or fp32 with ZERO_GRAD_F32.
+ *   flags       ZERO_IDS_I32, ZERO_GRAD_F32, ZERO_GRAD_ACCUMULATE.
+ *   workspace   zero_linear_cross_entropy_workspace bytes, 16-byte aligned.
+ * Sums are fp32.  dz is rounded to bf16 (the tensor cores' operand type) before
+ * the products, from exponentials that are held in 16 bits of fixed point, good to
+ * 2^-11; probabilities below exp(-32) of the target's (of the largest, in a row
+ * whose loss is above 30) are 0 in dz.  Rows go in pieces whose 16-bit values take
+ * at most 1 GiB of the workspace.  Results do not depend on the run.
+ * rows = 0: total is 0, and dw is too (or is left, accumulating).
+ * Errors: ZERO_E_NULLPTR, ZERO_E_SHAPE, ZERO_E_LAYOUT, ZERO_E_ALIGN, ZERO_E_ALIAS
+ * (an output overlaps another buffer), ZERO_E_WORKSPACE, ZERO_E_LAUNCH, ZERO_E_DEVICE.
+ */
+int zero_linear_cross_entropy(const zero_cross_entropy_t* shape, const void* x, const void* w,
+                              const void* targets, int64_t ignore_index, const float* scale,
+                              float* losses, float* total, void* dx, void* dw, int32_t flags,
+                              void* workspace, int64_t workspace_bytes, void* stream);
+
+/* Bytes of workspace that suffice for zero_linear_cross_entropy of this shape;
+ * flags: ZERO_LINEAR_BACKWARD if dx or dw is wanted, ZERO_GRAD_F32 if dw is fp32,
+ * ZERO_LINEAR_ALIGNED if w's base is on a 16-byte boundary and its pitch a multiple
+ * of 8 (else it is laid out anew).  Negative: the ZERO_E_* code.  Host only. */
+int64_t zero_linear_cross_entropy_workspace(const zero_cross_entropy_t* shape, int32_t flags);
+
+/*
+ * The norms before and after a block, its gate and its residual scale: a model's
+ * residual stream r takes the output h of a block, and the next block gets y,
+ *   s = r + alpha * gate * P(h),   y = N(s)
+ * with P of kind `post` (NONE: h itself) and N of kind `kind` (RMS or LAYER), each
+ * row by itself.  Pitches in elements; ldg = 0: gate is one vector for all rows.
+ * 1 <= width <= ZERO_MAX_NORM_WIDTH; 0 <= rows < 2^31.
+ */
+#define ZERO_MAX_NORM_WIDTH 32768
+typedef struct {
+  int64_t rows, width;
+  int32_t post, kind;
+  double alpha, eps;
+  int64_t ldr, ldh, ldg, lds, ldy;        /* r, h, gate, s, y              */
+  int64_t lddy, ldds, lddr, lddh, lddg;   /* dy, ds, dr, dh, dgate         */
+} zero_block_norm_t;
+
+/*
+ * Forward.  Everything is bf16 in memory and fp32 within: y takes s unrounded.
+ *   r           read.
+ *   h           read, or NULL: no block yet, s = r (post is NONE, gate NULL).
+ *   post_weight, post_bias   `width` elements each, or NULL for 1 and 0 (post_bias
+ *               is LAYER's alone); weight, bias likewise for N.
+ *   gate        a vector (ldg = 0), a matrix of rows x width, or NULL for 1.
+ *   s           written, or NULL; it may be r itself (same pitch): in place.
+ *   y           written.
+ * Errors: ZERO_E_NULLPTR, ZERO_E_SHAPE, ZERO_E_LAYOUT (unknown kind, or a weight,
+ * bias or gate that its kind or h does not have), ZERO_E_HPARAM (alpha not finite,
+ * eps < 0 or not finite), ZERO_E_ALIGN, ZERO_E_ALIAS, ZERO_E_LAUNCH, ZERO_E_DEVICE.
+ */
+int zero_block_norm_forward(const zero_block_norm_t* shape, const void* r, const void* h,
+                            const void* post_weight, const void* post_bias, const void* gate,
+                            const void* weight, const void* bias, void* s, void* y, void* stream);
+
+/*
+ * Backward: from dy and the gradient ds that reaches s from elsewhere (NULL: 0),
+ *   dr = ds + N's gradient of dy,   dh, dgate, and the weights' and biases' sums.
+ * Statistics are computed anew from s and h as they are here.
+ *   dy, s       read.   h: read, or NULL as in the forward.
+ *   dr          written, or NULL; it may be ds itself (same pitch).
+ *   dh          written, or NULL.  With post NONE, no gate and alpha 1 it is dr.
+ *   dgate       NULL, or with ldg = 0 a vector, its sum over rows, else (lddg) a
+ *               matrix, bf16.
+ *   dpost_weight, dpost_bias, dweight, dbias   sums over rows; NULL to skip.  They
+ *               and a vector dgate are bf16, or fp32 with ZERO_GRAD_F32, and added
+ *               to what is there with ZERO_GRAD_ACCUMULATE.
+ *   workspace   zero_block_norm_workspace bytes, 16-byte aligned; free again once
+ *               the call's work has run.
+ * Sums are fp32 in an order that follows from the sizes alone.  rows = 0 writes zeros
+ * to the sums (or leaves them, accumulating).
+ * Errors: as the forward, and ZERO_E_WORKSPACE.
+ */
+int zero_block_norm_backward(const zero_block_norm_t* shape, const void* dy, const void* ds,
+                             const void* s, const void* h, const void* post_weight,
+                             const void* post_bias, const void* gate, const void* weight,
+                             void* dr, void* dh, void* dgate, void* dpost_weight,
+                             void* dpost_bias, void* dweight, void* dbias, int32_t flags,
+                             void* workspace, int64_t workspace_bytes, void* stream);
+
+/* Bytes of workspace that suffice for zero_block_norm_backward.  Negative: the
+ * ZERO_E_* code of a bad shape.  Host only. */
+int64_t zero_block_norm_workspace(const zero_block_norm_t* shape);
 
 /* ------------------------------------------------------------------ misc */
 

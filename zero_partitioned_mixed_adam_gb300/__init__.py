@@ -10,7 +10,9 @@ and the parameters" (AI infra handbooks), "Implementing ZeRO's Adam from
 scratch" (ZeroAdam) and "ZeRO-3 and FSDP" (unit all-gather).  Around it, the rest
 of a training step (train_ops.py): zero_linear_forward and zero_linear_backward (a
 unit's linear maps), zero_grad_norm, and zero_adamw_step (AdamW over a list of
-tensors, with moments in 32 or 8 bits).
+tensors, with moments in 32 or 8 bits); and the two ends of a model (model_ops.py):
+zero_embedding_forward and _backward, zero_linear_cross_entropy, and
+zero_block_norm_forward and _backward (the norms around a block).
 """
 from __future__ import annotations
 
@@ -29,6 +31,9 @@ ZERO_GRAD_ACCUMULATE, ZERO_STATE_8BIT = 0x40, 0x80
 ZERO_PARAM_FULL, ZERO_PARAM_SHARD = 0, 1
 ZERO_ACT_NONE, ZERO_ACT_RELU, ZERO_ACT_GELU, ZERO_ACT_SILU = 0, 1, 2, 3
 ZERO_LINEAR_BACKWARD, ZERO_LINEAR_ALIGNED, ZERO_LINEAR_PLAIN = 1, 2, 4
+ZERO_IDS_I32 = 0x100
+ZERO_NORM_NONE, ZERO_NORM_RMS, ZERO_NORM_LAYER = 0, 1, 2
+ZERO_MAX_NORM_WIDTH = 32768
 ZERO_MOMENT_BLOCK = 256
 ZERO_MAX_LIST = 65536
 ZERO_MAX_WORLD = 1024
@@ -48,7 +53,9 @@ EXPORTS = ("zero_plan", "zero_adam_step", "zero_adam_step_range", "zero3_unit_ga
            "zero_test_withhold_copies", "zero_strerror", "zero_version",
            "zero_linear_forward", "zero_linear_backward", "zero_linear_workspace",
            "zero_grad_norm", "zero_grad_norm_workspace", "zero_adamw_step",
-           "zero_adamw_state_f32")
+           "zero_adamw_state_f32", "zero_embedding_forward", "zero_embedding_backward",
+           "zero_linear_cross_entropy", "zero_linear_cross_entropy_workspace",
+           "zero_block_norm_forward", "zero_block_norm_backward", "zero_block_norm_workspace")
 
 
 class ZeroError(RuntimeError):
@@ -310,6 +317,8 @@ def raw_lib() -> ctypes.CDLL:
 
 from . import train_ops  # noqa: E402  (it takes the loaded library from here)
 from .train_ops import *  # noqa: E402,F401,F403
+from . import model_ops  # noqa: E402
+from .model_ops import *  # noqa: E402,F401,F403
 
 __all__ = ["zero_plan", "zero_adam_step", "zero_adam_step_range", "zero3_unit_gather",
            "zero3_unit_gather_rows", "pointer_array", "PointerArray", "zero3_unit_step", "rows_layout", "device_status",
@@ -320,4 +329,5 @@ __all__ = ["zero_plan", "zero_adam_step", "zero_adam_step_range", "zero3_unit_ga
            "ZERO_MAX_UNIT_TENSORS", "EXPORTS", "LIB_PATH", "ZERO_GRAD_ACCUMULATE",
            "ZERO_STATE_8BIT", "ZERO_ACT_NONE", "ZERO_ACT_RELU", "ZERO_ACT_GELU", "ZERO_ACT_SILU",
            "ZERO_LINEAR_BACKWARD", "ZERO_LINEAR_ALIGNED", "ZERO_LINEAR_PLAIN", "ZERO_MOMENT_BLOCK",
-           "ZERO_MAX_LIST"] + train_ops.__all__
+           "ZERO_MAX_LIST", "ZERO_IDS_I32", "ZERO_NORM_NONE", "ZERO_NORM_RMS", "ZERO_NORM_LAYER",
+           "ZERO_MAX_NORM_WIDTH"] + train_ops.__all__ + model_ops.__all__

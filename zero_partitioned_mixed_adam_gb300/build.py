@@ -16,7 +16,7 @@ CSRC = os.path.join(HERE, "csrc")
 OUT = os.path.join(HERE, "libzeroadam.so")
 OBJ_DIR = os.path.join(ROOT, "_build", "zeroadam")
 SOURCES = ["capi.cpp", "capi_train.cpp", "adam_step.cu", "unit_gather.cu", "adamw_tensors.cu",
-           "linear.cu"]
+           "linear.cu", "cross_entropy.cu", "embedding.cu", "block_norm.cu"]
 HEADERS = ([os.path.join(CSRC, h) for h in sorted(os.listdir(CSRC))
             if h.endswith((".h", ".hpp", ".cuh"))]
            + [os.path.join(ROOT, "include", "zeroadam.h")])

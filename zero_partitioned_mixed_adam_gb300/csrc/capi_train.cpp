@@ -1,7 +1,9 @@
-// capi_train.cpp -- the extern "C" entry points of the linear maps, the gradient
-// norm and AdamW over a list of tensors: argument checks, scalars, dispatch.
+// capi_train.cpp -- the extern "C" entry points of a training step around the ZeRO step
+// (linear maps, the gradient norm, AdamW over a list of tensors, embedding, cross
+// entropy, block norms): argument checks, scalars, dispatch.
 #include <cuda_runtime.h>
 
+#include <cfloat>
 #include <cmath>
 #include <cstdint>
 
@@ -82,6 +84,50 @@ int check_step_scalars(double lr, double beta1, double beta2, double eps, int64_
 }
 
 constexpr int64_t kMostNumel = int64_t{1} << 40;
+
+int check_sides(int64_t rows, int64_t width, int64_t vocab) {
+  if (rows < 0 || width < 1 || vocab < 1 || rows >= kMostSide || width >= kMostSide ||
+      vocab >= kMostSide)
+    return ZERO_E_SHAPE;
+  return ZERO_OK;
+}
+
+// A list of ids, as a row.
+Matrix ids_row(const void* ids, int64_t rows, int32_t flags) {
+  return Matrix{ids, 1, rows, rows, (flags & ZERO_IDS_I32) ? 4 : 8};
+}
+
+int check_embedding(const zero_embedding_t* s, const Matrix& from, const Matrix& ids, const Matrix& to,
+                    double scale) {
+  if (!std::isfinite(scale) || std::fabs(scale) > FLT_MAX) return ZERO_E_HPARAM;
+  for (const Matrix* m : {&from, &ids, &to}) {
+    const int rc = check_matrix(*m);
+    if (rc != ZERO_OK) return rc;
+  }
+  return share(to, from) || share(to, ids) ? ZERO_E_ALIAS : ZERO_OK;
+}
+
+bool norm_kind(int32_t kind) { return kind == ZERO_NORM_RMS || kind == ZERO_NORM_LAYER; }
+
+// What the two directions of the block norms share.
+int check_block_norm(const zero_block_norm_t* s) {
+  if (s == nullptr) return ZERO_E_NULLPTR;
+  if (s->rows < 0 || s->rows >= kMostSide || s->width < 1 || s->width > ZERO_MAX_NORM_WIDTH)
+    return ZERO_E_SHAPE;
+  return ZERO_OK;
+}
+int check_block_norm_inputs(const zero_block_norm_t& s, const void* h, const void* post_weight,
+                            const void* post_bias, const void* gate, const void* bias) {
+  if (!norm_kind(s.kind) || (s.post != ZERO_NORM_NONE && !norm_kind(s.post))) return ZERO_E_LAYOUT;
+  if (h == nullptr && s.rows > 0 && (s.post != ZERO_NORM_NONE || gate != nullptr)) return ZERO_E_LAYOUT;
+  if (s.post == ZERO_NORM_NONE && post_weight != nullptr) return ZERO_E_LAYOUT;
+  if (s.post != ZERO_NORM_LAYER && post_bias != nullptr) return ZERO_E_LAYOUT;
+  if (s.kind != ZERO_NORM_LAYER && bias != nullptr) return ZERO_E_LAYOUT;
+  if (!std::isfinite(s.alpha) || std::fabs(s.alpha) > FLT_MAX || !std::isfinite(s.eps) || s.eps < 0.0 ||
+      s.eps > FLT_MAX)
+    return ZERO_E_HPARAM;
+  return ZERO_OK;
+}
 
 }  // namespace
 }  // namespace zeroadam
@@ -318,6 +364,229 @@ int zero_adamw_state_f32(int32_t ntensors, const zero_adamw_tensor_t* tensors,
   L.v_out = v_out;
   L.stream = static_cast<cudaStream_t>(stream);
   return launch_status(launch_adamw_moments(L));
+}
+
+int zero_embedding_forward(const zero_embedding_t* shape, const void* table, const void* ids,
+                           int32_t flags, double scale, void* y, void* stream) {
+  Trace trace("zero_embedding_forward");
+  if (shape == nullptr) return ZERO_E_NULLPTR;
+  const zero_embedding_t& s = *shape;
+  int rc = check_sides(s.rows, s.width, s.vocab);
+  if (rc != ZERO_OK) return rc;
+  if ((flags & ~ZERO_IDS_I32) != 0) return ZERO_E_LAYOUT;
+  if (table == nullptr || (s.rows > 0 && (ids == nullptr || y == nullptr))) return ZERO_E_NULLPTR;
+  const Matrix mt{table, s.vocab, s.width, s.ldt, 2}, my{y, s.rows, s.width, s.ldy, 2};
+  if ((rc = check_embedding(shape, mt, ids_row(ids, s.rows, flags), my, scale)) != ZERO_OK) return rc;
+  if (s.rows == 0) return ZERO_OK;
+  EmbeddingLaunch L{};
+  L.s = s;
+  L.from = static_cast<const uint16_t*>(table);
+  L.ids = ids;
+  L.ids_i32 = (flags & ZERO_IDS_I32) ? 1 : 0;
+  L.scale = static_cast<float>(scale);
+  L.to = y;
+  L.stream = static_cast<cudaStream_t>(stream);
+  return launch_status(launch_embedding_forward(L));
+}
+
+int zero_embedding_backward(const zero_embedding_t* shape, const void* dy, const void* ids,
+                            int32_t flags, double scale, int64_t padding, void* dtable,
+                            void* stream) {
+  Trace trace("zero_embedding_backward");
+  if (shape == nullptr) return ZERO_E_NULLPTR;
+  const zero_embedding_t& s = *shape;
+  int rc = check_sides(s.rows, s.width, s.vocab);
+  if (rc != ZERO_OK) return rc;
+  if ((flags & ~(ZERO_IDS_I32 | ZERO_GRAD_F32 | ZERO_GRAD_ACCUMULATE)) != 0) return ZERO_E_LAYOUT;
+  if (dtable == nullptr || (s.rows > 0 && (ids == nullptr || dy == nullptr))) return ZERO_E_NULLPTR;
+  const Matrix md{dy, s.rows, s.width, s.ldy, 2},
+      mt{dtable, s.vocab, s.width, s.ldt, (flags & ZERO_GRAD_F32) ? 4 : 2};
+  if ((rc = check_embedding(shape, md, ids_row(ids, s.rows, flags), mt, scale)) != ZERO_OK) return rc;
+  if (s.rows == 0 && (flags & ZERO_GRAD_ACCUMULATE) != 0) return ZERO_OK;
+  EmbeddingLaunch L{};
+  L.s = s;
+  L.from = static_cast<const uint16_t*>(dy);
+  L.ids = ids;
+  L.ids_i32 = (flags & ZERO_IDS_I32) ? 1 : 0;
+  L.scale = static_cast<float>(scale);
+  L.padding = padding;
+  L.to = dtable;
+  L.grad_f32 = (flags & ZERO_GRAD_F32) ? 1 : 0;
+  L.accumulate = (flags & ZERO_GRAD_ACCUMULATE) ? 1 : 0;
+  L.stream = static_cast<cudaStream_t>(stream);
+  return launch_status(launch_embedding_backward(L));
+}
+
+int64_t zero_linear_cross_entropy_workspace(const zero_cross_entropy_t* shape, int32_t flags) {
+  if (shape == nullptr) return ZERO_E_NULLPTR;
+  const int rc = check_sides(shape->rows, shape->width, shape->vocab);
+  if (rc != ZERO_OK) return rc;
+  if ((flags & ~(ZERO_LINEAR_BACKWARD | ZERO_LINEAR_ALIGNED | ZERO_GRAD_F32)) != 0) return ZERO_E_LAYOUT;
+  return cross_entropy_workspace(*shape, flags);
+}
+
+int zero_linear_cross_entropy(const zero_cross_entropy_t* shape, const void* x, const void* w,
+                              const void* targets, int64_t ignore_index, const float* scale,
+                              float* losses, float* total, void* dx, void* dw, int32_t flags,
+                              void* workspace, int64_t workspace_bytes, void* stream) {
+  Trace trace("zero_linear_cross_entropy");
+  if (shape == nullptr) return ZERO_E_NULLPTR;
+  const zero_cross_entropy_t& s = *shape;
+  int rc = check_sides(s.rows, s.width, s.vocab);
+  if (rc != ZERO_OK) return rc;
+  if ((flags & ~(ZERO_IDS_I32 | ZERO_GRAD_F32 | ZERO_GRAD_ACCUMULATE)) != 0) return ZERO_E_LAYOUT;
+  if (w == nullptr || (s.rows > 0 && (x == nullptr || targets == nullptr))) return ZERO_E_NULLPTR;
+  const int gsize = (flags & ZERO_GRAD_F32) ? 4 : 2;
+  const Matrix mx{x, s.rows, s.width, s.ldx, 2}, mw{w, s.vocab, s.width, s.ldw, 2},
+      mt = ids_row(targets, s.rows, flags), ms{scale, 1, s.rows, s.rows, 4},
+      ml{losses, 1, s.rows, s.rows, 4}, mo{total, 1, 1, 1, 4}, mdx{dx, s.rows, s.width, s.lddx, 2},
+      mdw{dw, s.vocab, s.width, s.lddw, gsize};
+  for (const Matrix* m : {&mx, &mw, &mt, &ms, &ml, &mo, &mdx, &mdw})
+    if ((rc = check_matrix(*m)) != ZERO_OK) return rc;
+  const Matrix* const in[] = {&mx, &mw, &mt, &ms};
+  const Matrix* const out[] = {&ml, &mo, &mdx, &mdw};
+  for (int i = 0; i < 4; ++i) {
+    for (const Matrix* m : in)
+      if (share(*out[i], *m)) return ZERO_E_ALIAS;
+    for (int j = 0; j < i; ++j)
+      if (share(*out[i], *out[j])) return ZERO_E_ALIAS;
+  }
+  const int64_t need = cross_entropy_workspace(
+      s, (dx != nullptr || dw != nullptr ? ZERO_LINEAR_BACKWARD : 0) | (in_place(mw) ? ZERO_LINEAR_ALIGNED : 0) |
+             (flags & ZERO_GRAD_F32));
+  if ((rc = check_workspace(workspace, workspace_bytes, need)) != ZERO_OK) return rc;
+  const Matrix mws{workspace, 1, need, need, 1};
+  for (int i = 0; i < 4; ++i)
+    if (share(mws, *in[i]) || share(mws, *out[i])) return ZERO_E_ALIAS;
+  CrossEntropyLaunch L{};
+  L.s = s;
+  L.x = static_cast<const uint16_t*>(x);
+  L.w = static_cast<const uint16_t*>(w);
+  L.targets = targets;
+  L.ids_i32 = (flags & ZERO_IDS_I32) ? 1 : 0;
+  L.ignore = ignore_index;
+  L.scale = scale;
+  L.losses = losses;
+  L.total = total;
+  L.dx = static_cast<uint16_t*>(dx);
+  L.dw = dw;
+  L.grad_f32 = (flags & ZERO_GRAD_F32) ? 1 : 0;
+  L.accumulate = (flags & ZERO_GRAD_ACCUMULATE) ? 1 : 0;
+  L.workspace = workspace;
+  L.stream = static_cast<cudaStream_t>(stream);
+  L.withhold = withhold_copies();
+  return launch_status(launch_cross_entropy(L));
+}
+
+int64_t zero_block_norm_workspace(const zero_block_norm_t* shape) {
+  const int rc = check_block_norm(shape);
+  return rc != ZERO_OK ? rc : block_norm_workspace(*shape);
+}
+
+int zero_block_norm_forward(const zero_block_norm_t* shape, const void* r, const void* h,
+                            const void* post_weight, const void* post_bias, const void* gate,
+                            const void* weight, const void* bias, void* s, void* y, void* stream) {
+  Trace trace("zero_block_norm_forward");
+  int rc = check_block_norm(shape);
+  if (rc != ZERO_OK) return rc;
+  const zero_block_norm_t& z = *shape;
+  if ((rc = check_block_norm_inputs(z, h, post_weight, post_bias, gate, bias)) != ZERO_OK) return rc;
+  if (z.rows > 0 && (r == nullptr || y == nullptr)) return ZERO_E_NULLPTR;
+  const bool one = z.ldg == 0;  // gate for all rows
+  const int64_t rows = z.rows, d = z.width;
+  const Matrix mr{r, rows, d, z.ldr, 2}, mh{h, rows, d, z.ldh, 2}, ms{s, rows, d, z.lds, 2},
+      my{y, rows, d, z.ldy, 2}, mg{gate, one ? 1 : rows, d, one ? d : z.ldg, 2}, mpw{post_weight, 1, d, d, 2},
+      mpb{post_bias, 1, d, d, 2}, mw{weight, 1, d, d, 2}, mb{bias, 1, d, d, 2};
+  for (const Matrix* m : {&mr, &mh, &ms, &my, &mg, &mpw, &mpb, &mw, &mb})
+    if ((rc = check_matrix(*m)) != ZERO_OK) return rc;
+  for (const Matrix* m : {&mh, &mg, &mpw, &mpb, &mw, &mb})
+    if (share(ms, *m) || share(my, *m)) return ZERO_E_ALIAS;
+  if (share(my, mr) || share(my, ms) || (!(s == r && z.lds == z.ldr) && share(ms, mr))) return ZERO_E_ALIAS;
+  if (rows == 0) return ZERO_OK;
+  BlockNormLaunch L{};
+  L.s = z;
+  L.r = static_cast<const uint16_t*>(r);
+  L.h = static_cast<const uint16_t*>(h);
+  L.post_weight = static_cast<const uint16_t*>(post_weight);
+  L.post_bias = static_cast<const uint16_t*>(post_bias);
+  L.gate = static_cast<const uint16_t*>(gate);
+  L.weight = static_cast<const uint16_t*>(weight);
+  L.bias = static_cast<const uint16_t*>(bias);
+  L.s_out = static_cast<uint16_t*>(s);
+  L.y = static_cast<uint16_t*>(y);
+  L.stream = static_cast<cudaStream_t>(stream);
+  return launch_status(launch_block_norm_forward(L));
+}
+
+int zero_block_norm_backward(const zero_block_norm_t* shape, const void* dy, const void* ds,
+                             const void* s, const void* h, const void* post_weight,
+                             const void* post_bias, const void* gate, const void* weight,
+                             void* dr, void* dh, void* dgate, void* dpost_weight,
+                             void* dpost_bias, void* dweight, void* dbias, int32_t flags,
+                             void* workspace, int64_t workspace_bytes, void* stream) {
+  Trace trace("zero_block_norm_backward");
+  int rc = check_block_norm(shape);
+  if (rc != ZERO_OK) return rc;
+  const zero_block_norm_t& z = *shape;
+  if ((rc = check_block_norm_inputs(z, h, post_weight, post_bias, gate, nullptr)) != ZERO_OK) return rc;
+  if ((flags & ~(ZERO_GRAD_F32 | ZERO_GRAD_ACCUMULATE)) != 0) return ZERO_E_LAYOUT;
+  if ((z.rows > 0 && h == nullptr && dh != nullptr) || (gate == nullptr && dgate != nullptr) ||
+      (z.post == ZERO_NORM_NONE && dpost_weight != nullptr) ||
+      (z.post != ZERO_NORM_LAYER && dpost_bias != nullptr) ||
+      (z.kind != ZERO_NORM_LAYER && dbias != nullptr))
+    return ZERO_E_LAYOUT;
+  if (z.rows > 0 && (dy == nullptr || s == nullptr)) return ZERO_E_NULLPTR;
+  const bool one = z.ldg == 0;
+  const int gsize = (flags & ZERO_GRAD_F32) ? 4 : 2;
+  const int64_t rows = z.rows, d = z.width;
+  const Matrix mdy{dy, rows, d, z.lddy, 2}, mds{ds, rows, d, z.ldds, 2}, ms{s, rows, d, z.lds, 2},
+      mh{h, rows, d, z.ldh, 2}, mg{gate, one ? 1 : rows, d, one ? d : z.ldg, 2}, mpw{post_weight, 1, d, d, 2},
+      mpb{post_bias, 1, d, d, 2}, mw{weight, 1, d, d, 2}, mdr{dr, rows, d, z.lddr, 2}, mdh{dh, rows, d, z.lddh, 2},
+      mdg{dgate, one ? 1 : rows, d, one ? d : z.lddg, one ? gsize : 2}, mdpw{dpost_weight, 1, d, d, gsize},
+      mdpb{dpost_bias, 1, d, d, gsize}, mdw{dweight, 1, d, d, gsize}, mdb{dbias, 1, d, d, gsize};
+  const Matrix* const in[] = {&mdy, &mds, &ms, &mh, &mg, &mpw, &mpb, &mw};
+  const Matrix* const out[] = {&mdr, &mdh, &mdg, &mdpw, &mdpb, &mdw, &mdb};
+  for (const Matrix* m : in)
+    if ((rc = check_matrix(*m)) != ZERO_OK) return rc;
+  for (const Matrix* m : out)
+    if ((rc = check_matrix(*m)) != ZERO_OK) return rc;
+  for (const Matrix* o : out) {
+    for (const Matrix* m : in)
+      if (!(o == &mdr && m == &mds && dr == ds && z.lddr == z.ldds) && share(*o, *m)) return ZERO_E_ALIAS;
+    for (const Matrix* other : out) {
+      if (other == o) break;
+      if (share(*o, *other)) return ZERO_E_ALIAS;
+    }
+  }
+  const int64_t need = block_norm_workspace(z);
+  if ((rc = check_workspace(workspace, workspace_bytes, need)) != ZERO_OK) return rc;
+  const Matrix mws{need > 0 ? workspace : nullptr, 1, need, need, 1};
+  for (const Matrix* m : in)
+    if (share(mws, *m)) return ZERO_E_ALIAS;
+  for (const Matrix* m : out)
+    if (share(mws, *m)) return ZERO_E_ALIAS;
+  BlockNormLaunch L{};
+  L.s = z;
+  L.dy = static_cast<const uint16_t*>(dy);
+  L.ds = static_cast<const uint16_t*>(ds);
+  L.sum = static_cast<const uint16_t*>(s);
+  L.h = static_cast<const uint16_t*>(h);
+  L.post_weight = static_cast<const uint16_t*>(post_weight);
+  L.post_bias = static_cast<const uint16_t*>(post_bias);
+  L.gate = static_cast<const uint16_t*>(gate);
+  L.weight = static_cast<const uint16_t*>(weight);
+  L.dr = static_cast<uint16_t*>(dr);
+  L.dh = static_cast<uint16_t*>(dh);
+  L.dgate = dgate;
+  L.dpost_weight = dpost_weight;
+  L.dpost_bias = dpost_bias;
+  L.dweight = dweight;
+  L.dbias = dbias;
+  L.grad_f32 = (flags & ZERO_GRAD_F32) ? 1 : 0;
+  L.accumulate = (flags & ZERO_GRAD_ACCUMULATE) ? 1 : 0;
+  L.workspace = workspace;
+  L.stream = static_cast<cudaStream_t>(stream);
+  return launch_status(launch_block_norm_backward(L));
 }
 
 }  // extern "C"

@@ -10,6 +10,7 @@
 #include <mutex>
 #include <type_traits>
 
+#include "chain.cuh"
 #include "internal.h"
 #include "linear_epilogue.cuh"
 #include "linear_plan.hpp"
@@ -42,6 +43,7 @@ struct ProductArgs {
   int32_t late;          // its inputs were there before its predecessor began
   int32_t early_units;   // units that the predecessor leaves idle in its last round,
   int32_t early_tiles;   // and tiles they do meanwhile
+  ExponentOf x;          // of kExponent
 };
 
 struct Tile {
@@ -85,6 +87,7 @@ enum Kind {
   kForward,   // bias, pre, activation, residual; bf16
   kGradient,  // times an activation's slope, or added to what is there; bf16
   kFloat,     // fp32, alone or added to what is there
+  kExponent,  // exponentials less each row's reference: their sums, and 16 bits each
 };
 
 // A warp's 32 x 32 part of D from shared memory, where row r's 16-byte piece q
@@ -473,6 +476,80 @@ struct RowsPart {
   }
 };
 
+// 32 columns of logits z, a row a lane, less the row's reference r: d = z - r goes out
+// as 16 bits of fixed point, in 2^-10 (below -32: as -32, which stands for nothing), by
+// TMA as bf16 does; exp(d) is added up, and the largest z is kept, over the columns of
+// the vocabulary but the target's.  d itself is what is held because it costs no
+// exponent's bits: exp(d) is then good to 2^-11, where bf16 would leave it 2^-9 and the
+// pass that makes dz of it round a second time.
+// Some 5 instructions an element, half of them two elements at a time, and one of the
+// special-function unit: 1,300 cycles of a tile's epilogue where its products take 8 for
+// each step of the reduction, so it is hidden from 256 steps on.
+struct ExponentPart {
+  float r;      // the row's reference
+  int32_t t;    // its target
+  Pair sum;
+  float top;
+  int slot = 0;
+
+  __device__ __forceinline__ void begin(float ref, int32_t target) {
+    r = ref;
+    t = target;
+    sum = pair(0.0f, 0.0f);
+    top = -INFINITY;
+  }
+  __device__ __forceinline__ void put(const ProductArgs& a, uint8_t* staging, float x[32], int row,
+                                      int64_t col, int64_t cols, int lane) {
+    if (col + 32 > cols) {
+#pragma unroll
+      for (int q = 0; q < 32; ++q)
+        if (col + q >= cols) x[q] = -INFINITY;
+    }
+    const int64_t at = t - col;
+    if (__any_sync(0xffffffffu, at >= 0 && at < 32)) {
+#pragma unroll
+      for (int q = 0; q < 32; ++q)
+        if (at == q) x[q] = -INFINITY;
+    }
+#pragma unroll
+    for (int q = 0; q < 32; ++q) top = fmaxf(top, x[q]);
+    const bool keep = a.e.out != nullptr;
+    constexpr float kMagic = 12582912.0f;  // 3 2^22: the sum's low bits are a whole number
+    uint32_t w[16];
+#pragma unroll
+    for (int q = 0; q < 32; q += 2) {
+      const Pair d = pair(x[q], x[q + 1]) + pair(-r, -r);
+      float u, v;
+      split(d * pair(kLog2e, kLog2e), u, v);
+      sum = sum + pair(fast_exp2(u), fast_exp2(v));
+      split(fma2(d, pair(1024.0f, 1024.0f), pair(kMagic, kMagic)), u, v);
+      u = fmaxf(u, kMagic - 32768.0f);
+      v = fmaxf(v, kMagic - 32768.0f);
+      w[q / 2] = __byte_perm(__float_as_uint(u), __float_as_uint(v), 0x5410);
+    }
+    if (!keep || col >= cols) return;
+    if (lane == 0) bulk_wait_read<1>();  // the copy before the last has left this slot
+    __syncwarp();
+    uint8_t* to = staging + 2048 * slot;
+    slot ^= 1;
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+      *reinterpret_cast<uint4*>(to + lane * 64 + ((q ^ ((lane >> 1) & 3)) * 16)) =
+          make_uint4(w[4 * q], w[4 * q + 1], w[4 * q + 2], w[4 * q + 3]);
+    fence_async_shared();
+    __syncwarp();
+    if (lane == 0) {
+      tile_store(&a.out, to, static_cast<int>(col), row, 0, false);
+      bulk_commit();
+    }
+  }
+  __device__ __forceinline__ float2 end() const {
+    float lo, hi;
+    split(sum, lo, hi);
+    return make_float2(lo + hi, top);
+  }
+};
+
 // Place in the ring of stages: the stage, and the parity of its barriers' phase.
 struct Place {
   int stages;
@@ -551,7 +628,7 @@ __global__ void __launch_bounds__(kProductThreads, 1)
   const uint32_t rank = CG == 2 ? cluster_rank() : 0u;
   const int unit = blockIdx.x / CG;
   const Turns turns{a.early_units, a.early_tiles, static_cast<int>(gridDim.x) / CG};
-  const int tiles = a.whole + (a.tiles_m * a.tiles_n - a.whole) * a.splits;
+  int tiles = a.whole + (a.tiles_m * a.tiles_n - a.whole) * a.splits;
 
   if (threadIdx.x == 0) {
     *failed = 0;
@@ -572,6 +649,8 @@ __global__ void __launch_bounds__(kProductThreads, 1)
   if (warp == 1) tmem_alloc<CG>(tmem_at, Shape::kColumns);
   if (!a.late) wait_for_predecessor();
   launch_dependents();
+  if constexpr (KIND == kExponent)
+    if (a.x.only_if != nullptr && __ldcg(a.x.only_if) == 0) tiles = 0;
   tc_fence_before();
   __syncthreads();
   if constexpr (CG == 2) cluster_sync();
@@ -720,6 +799,7 @@ __global__ void __launch_bounds__(kProductThreads, 1)
     };
     int n = 0;
     bool ok = true;
+    ExponentPart exponents;  // of kExponent
     for (int t = turns.first(unit); t < tiles && ok; t = turns.after(t)) {
       const Tile tile = tile_of<BM>(a, t);
       const int64_t row0 = tile.row + rank * kBlockRows + quarter * 32;
@@ -783,7 +863,32 @@ __global__ void __launch_bounds__(kProductThreads, 1)
           __syncwarp();
         }
       };
-      if constexpr (KIND == kFloat) {
+      if constexpr (KIND == kExponent) {
+        const int b = n & 1;
+        exponents.begin(mine_in ? __ldcg(a.x.ref + row0 + lane) : 0.0f,
+                        mine_in ? __ldcg(a.x.target + row0 + lane) : -1);
+        ok = wait_for_chain(&done[b], static_cast<uint32_t>((n / 2) & 1), tile.last - tile.first);
+        ++n;
+        if (!ok) break;
+        tc_fence_after();
+        const uint32_t from = lanes + b * Shape::kMaxCols;
+        uint32_t bits[32];
+        if (c_first < c_end) tmem_load32(from + c_first, bits);
+        else release(b);
+#pragma unroll 1
+        for (int c = c_first; c < c_end; c += c_step) {
+          float x[32];
+          tmem_load_wait();
+#pragma unroll
+          for (int q = 0; q < 32; ++q) x[q] = __uint_as_float(bits[q]);
+          if (c + c_step < c_end) tmem_load32(from + c + c_step, bits);
+          else release(b);
+          if (any) exponents.put(a, reinterpret_cast<uint8_t*>(mine), x, static_cast<int>(row0),
+                                 tile.col + c, cols, lane);
+        }
+        if (mine_in)
+          a.x.sums[(row0 + lane) * a.x.sum_pitch + tile.col / bn * 2 + half] = exponents.end();
+      } else if constexpr (KIND == kFloat) {
         constexpr int kParts = Shape::kMaxCols / 64;
         float sum[kParts][32];
         for (int step = tile.first; step < tile.last; step += kChain<KIND>, ++n) {
@@ -972,8 +1077,6 @@ __global__ void __launch_bounds__(256) linear_join_kernel(const __grid_constant_
 
 // ------------------------------------------------------------------ layouts
 
-bool aligned(const void* p, uintptr_t k) { return (reinterpret_cast<uintptr_t>(p) & (k - 1)) == 0; }
-
 // A bf16 matrix as it lies in memory.  A single row has no pitch.
 struct Stored {
   const uint16_t* p;
@@ -1099,48 +1202,6 @@ __global__ void __launch_bounds__(256) linear_prepare_kernel(const __grid_consta
   else add_dbias(a.dbias);
 }
 
-// Takes pieces of the workspace in order.
-struct Space {
-  char* at;
-  void* take(int64_t bytes) {
-    void* p = at;
-    at += round_up(bytes, 256);
-    return p;
-  }
-};
-
-// The kernels of one call, launched as programmatic dependents: they begin while
-// their predecessor ends, and wait for it (wait_for_predecessor) before they read
-// what it wrote; the first one so after whatever the stream held before.
-struct Chain {
-  cudaStream_t stream;
-  bool begun = false;
-
-  template <typename... Params, typename... Args>
-  cudaError_t launch(void (*kernel)(Params...), dim3 grid, int threads, int smem, int cluster,
-                     Args&&... args) {
-    cudaLaunchConfig_t config = {};
-    config.gridDim = grid;
-    config.blockDim = dim3(threads);
-    config.dynamicSmemBytes = smem;
-    config.stream = stream;
-    cudaLaunchAttribute attr[2];
-    config.attrs = attr;
-    if (cluster > 1) {
-      cudaLaunchAttribute& a = attr[config.numAttrs++];
-      a.id = cudaLaunchAttributeClusterDimension;
-      a.val.clusterDim.x = cluster;
-      a.val.clusterDim.y = 1;
-      a.val.clusterDim.z = 1;
-    }
-    cudaLaunchAttribute& a = attr[config.numAttrs++];
-    a.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    a.val.programmaticStreamSerializationAllowed = 1;
-    begun = true;
-    return cudaLaunchKernelEx(&config, kernel, static_cast<Params>(args)...);
-  }
-};
-
 // Lays the matrices that TMA cannot read where they are out anew.
 cudaError_t lay_out(Stored* const* matrices, int count, Space* space, Chain* chain) {
   PrepareArgs all{};
@@ -1225,6 +1286,11 @@ cudaError_t make_out_map(CUtensorMap* map, const void* p, int64_t rows, int64_t 
 }
 
 // ----------------------------------------------------------------- products
+
+// Exponentials of a product's rows (kExponent).
+Plan plan_exponents(int64_t rows, int64_t vocab, int64_t width) {
+  return plan_product(rows, vocab, width, false, false, nullptr, true, 1);
+}
 
 // D[rows, cols] over `depth`; a_mn / b_mn: the operand is stored [depth, rows]
 // ([depth, cols]) instead of [rows, depth] ([cols, depth]).
@@ -1628,6 +1694,55 @@ int read_and_clear_linear_status(int* status) {
   if (cudaMemcpyFromSymbol(&v, g_linear_status_taken, sizeof(int)) != cudaSuccess) return -1;
   *status = v;
   return 0;
+}
+
+bool tileable_matrix(const uint16_t* p, int64_t rows, int64_t cols, int64_t ld) {
+  return tileable(Stored(p, rows, cols, ld));
+}
+int64_t laid_out_pitch(int64_t cols) { return copy_pitch(cols); }
+
+cudaError_t launch_lay_out(const uint16_t* p, int64_t rows, int64_t cols, int64_t ld, uint16_t* to,
+                           cudaStream_t stream) {
+  Stored m(p, rows, cols, ld);
+  Stored* const all[1] = {&m};
+  Space space{reinterpret_cast<char*>(to)};
+  Chain chain{stream};
+  return lay_out(all, 1, &space, &chain);
+}
+
+int64_t exponent_parts(int64_t rows, int64_t vocab, int64_t width) {
+  const int bn = plan_exponents(rows, vocab, width).bn;
+  return (vocab + bn - 1) / bn * 2;
+}
+
+cudaError_t launch_exponents(const ExponentLaunch& L) {
+  (void)cudaGetLastError();
+  Product p{};
+  p.a = {L.x, L.rows, L.width, L.ldx};
+  p.b = {L.w, L.vocab, L.width, L.ldw};
+  p.rows = L.rows;
+  p.cols = L.vocab;
+  p.depth = L.width;
+  p.e.out = L.out;
+  p.e.ldo = L.ldo;
+  Pending w{};
+  w.plan = plan_exponents(L.rows, L.vocab, L.width);
+  ProductArgs& a = w.a;
+  a.e = p.e;
+  a.e.vec = 1;
+  a.rows = p.rows;
+  a.cols = p.cols;
+  a.steps = static_cast<int32_t>((p.depth + kStep - 1) / kStep);
+  a.withhold = L.withhold;
+  a.x = L.of;
+  if (L.out != nullptr) {
+    const int64_t ld = L.rows > 1 ? L.ldo : round_up(L.vocab, 8);
+    const cudaError_t e = make_out_map(&a.out, L.out, L.rows, L.vocab, ld, 1, L.rows * ld, false);
+    if (e != cudaSuccess) return e;
+  }
+  Chain chain{L.stream};
+  return w.plan.cg == 2 ? launch_shape<2, false, false, kExponent, false>(p, &w, &chain)
+                        : launch_shape<1, false, false, kExponent, false>(p, &w, &chain);
 }
 
 int64_t linear_workspace(const zero_linear_t& s, int32_t flags) {

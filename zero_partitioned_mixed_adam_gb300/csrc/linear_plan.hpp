@@ -105,9 +105,9 @@ struct Plan {
 // first, so that this one's tiles fill its last round: units without a tile there
 // take theirs early, as many as they can do meanwhile (the first blocks of a grid
 // get the first units that are free).  split: whether tiles past the last whole
-// round may be.
+// round may be.  most_parts: of a tile's reduction.
 inline Plan plan_product(int64_t rows, int64_t cols, int64_t depth, bool a_mn, bool b_mn,
-                  const Plan* follows = nullptr, bool split = true) {
+                  const Plan* follows = nullptr, bool split = true, int most_parts = 16) {
   Plan best{2, 256, 0, 1, 0, false, 0, 0, 0.0, 0.0, 0};
   if (rows < 1 || cols < 1) return best;
   const int steps = static_cast<int>((depth + kStep - 1) / kStep);
@@ -145,7 +145,7 @@ inline Plan plan_product(int64_t rows, int64_t cols, int64_t depth, bool a_mn, b
         const double rounds_us = (whole - early) / units * tile;
         const double late_us = begin + rounds_us, early_us = turn * tile + rounds_us;
         const double all_us = late_us > early_us ? late_us : early_us;
-        for (int parts = 1; parts <= 16; ++parts) {
+        for (int parts = 1; parts <= most_parts; ++parts) {
           // (past two rounds of parts nothing was ever gained)
           if (parts > 1 && (rest == 0 || parts * 2 > steps || rest * parts > 2 * units ||
                             (!split && whole > 0)))

@@ -83,6 +83,92 @@ struct LinearBackwardLaunch {
   int32_t withhold;
 };
 
+// ------------------------------------------- exponentials of a linear map's rows
+
+// What becomes of z = x W^T in place of an epilogue: with d = z - ref of its row, the
+// sum of exp(d) and the largest z over each part of the columns, the target's left out
+// (target < 0: none is); and d in 16 bits where it is wanted.
+struct ExponentOf {
+  const float* ref;       // [rows]
+  const int32_t* target;  // [rows]
+  float2* sums;           // [rows][sum_pitch], exponent_parts of them written
+  int64_t sum_pitch;
+  const int32_t* only_if; // nothing is done where this is 0; NULL: always
+};
+struct ExponentLaunch {
+  int64_t rows, width, vocab;
+  const uint16_t *x, *w;  // where TMA can read them
+  int64_t ldx, ldw;
+  ExponentOf of;
+  uint16_t* out;          // [rows][ldo], in 2^-10, -32 and below as -32768; NULL: not wanted
+  int64_t ldo;
+  cudaStream_t stream;
+  int32_t withhold;
+};
+int64_t exponent_parts(int64_t rows, int64_t vocab, int64_t width);
+cudaError_t launch_exponents(const ExponentLaunch& L);
+
+// Whether TMA can read a matrix in place; else the pitch of a copy that it can read,
+// and the copy.
+bool tileable_matrix(const uint16_t* p, int64_t rows, int64_t cols, int64_t ld);
+int64_t laid_out_pitch(int64_t cols);
+cudaError_t launch_lay_out(const uint16_t* p, int64_t rows, int64_t cols, int64_t ld, uint16_t* to,
+                           cudaStream_t stream);
+
+// ------------------------------------------------------------------ cross entropy
+
+struct CrossEntropyLaunch {
+  zero_cross_entropy_t s;
+  const uint16_t *x, *w;
+  const void* targets;
+  int32_t ids_i32;
+  int64_t ignore;
+  const float* scale;
+  float *losses, *total;
+  uint16_t* dx;
+  void* dw;
+  int32_t grad_f32, accumulate;
+  void* workspace;
+  cudaStream_t stream;
+  int32_t withhold;
+};
+// flags: ZERO_LINEAR_BACKWARD, ZERO_LINEAR_ALIGNED, ZERO_GRAD_F32
+int64_t cross_entropy_workspace(const zero_cross_entropy_t& s, int32_t flags);
+cudaError_t launch_cross_entropy(const CrossEntropyLaunch& L);
+
+// ---------------------------------------------------------------------- embedding
+
+struct EmbeddingLaunch {
+  zero_embedding_t s;
+  const uint16_t* from;   // the table, or dy
+  const void* ids;
+  int32_t ids_i32;
+  float scale;
+  int64_t padding;        // backward
+  void* to;               // y, or dtable
+  int32_t grad_f32, accumulate;
+  cudaStream_t stream;
+};
+cudaError_t launch_embedding_forward(const EmbeddingLaunch& L);
+cudaError_t launch_embedding_backward(const EmbeddingLaunch& L);
+
+// -------------------------------------------------------------------- block norms
+
+struct BlockNormLaunch {
+  zero_block_norm_t s;
+  const uint16_t *r, *h, *post_weight, *post_bias, *gate, *weight, *bias;
+  const uint16_t *dy, *ds, *sum;   // backward: `sum` is s
+  uint16_t *s_out, *y;             // forward
+  uint16_t *dr, *dh;               // backward
+  void *dgate, *dpost_weight, *dpost_bias, *dweight, *dbias;
+  int32_t grad_f32, accumulate;
+  void* workspace;
+  cudaStream_t stream;
+};
+cudaError_t launch_block_norm_forward(const BlockNormLaunch& L);
+cudaError_t launch_block_norm_backward(const BlockNormLaunch& L);
+int64_t block_norm_workspace(const zero_block_norm_t& s);
+
 // flags: ZERO_LINEAR_*
 int64_t linear_workspace(const zero_linear_t& s, int32_t flags);
 cudaError_t launch_linear_forward(const LinearForwardLaunch& L);

@@ -1,0 +1,297 @@
+"""Binding of the two ends of a model and what stands between its blocks: the embedding of
+token ids and its gradient, softmax cross entropy of a linear map onto a vocabulary with its
+gradients, and the norms before and after a block with its gate and residual scale.
+
+Like the rest of the binding it marshals arguments only; everything here is reached through
+the package itself (zero_embedding_forward, zero_linear_cross_entropy, ...).  Unlike the
+optimizer's calls these take tensors of the current CUDA device only.
+"""
+from __future__ import annotations
+
+import ctypes
+
+import torch
+
+from . import (ZERO_GRAD_ACCUMULATE, ZERO_GRAD_F32, ZERO_IDS_I32, ZERO_LINEAR_ALIGNED,
+               ZERO_LINEAR_BACKWARD, ZERO_NORM_LAYER, ZERO_NORM_NONE, ZERO_NORM_RMS, ZERO_OK,
+               ZeroError, _addr, _lib, _stream_handle)
+from .train_ops import _BF16, _GRADS, _matrix, _vector
+
+
+class ZeroEmbedding(ctypes.Structure):
+    """zero_embedding_t: sizes and row pitches of a table and the rows looked up in it."""
+
+    _fields_ = [(n, ctypes.c_int64) for n in ("rows", "width", "vocab", "ldt", "ldy")]
+
+
+class ZeroCrossEntropy(ctypes.Structure):
+    """zero_cross_entropy_t: sizes and row pitches of a linear map onto a vocabulary."""
+
+    _fields_ = [(n, ctypes.c_int64) for n in ("rows", "width", "vocab", "ldx", "ldw", "lddx", "lddw")]
+
+
+class ZeroBlockNorm(ctypes.Structure):
+    """zero_block_norm_t: sizes, kinds, scalars and row pitches of a block's norms."""
+
+    _fields_ = [("rows", ctypes.c_int64), ("width", ctypes.c_int64), ("post", ctypes.c_int32),
+                ("kind", ctypes.c_int32), ("alpha", ctypes.c_double), ("eps", ctypes.c_double)] + [
+        (n, ctypes.c_int64) for n in ("ldr", "ldh", "ldg", "lds", "ldy", "lddy", "ldds", "lddr",
+                                      "lddh", "lddg")]
+
+
+def _declare(lib) -> None:
+    vp, i32, i64, dbl = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_double
+    emb, ce, bn = (ctypes.POINTER(t) for t in (ZeroEmbedding, ZeroCrossEntropy, ZeroBlockNorm))
+    lib.zero_embedding_forward.argtypes = [emb, vp, vp, i32, dbl, vp, vp]
+    lib.zero_embedding_backward.argtypes = [emb, vp, vp, i32, dbl, i64, vp, vp]
+    lib.zero_linear_cross_entropy.argtypes = [ce, vp, vp, vp, i64, vp, vp, vp, vp, vp, i32, vp, i64, vp]
+    lib.zero_linear_cross_entropy_workspace.argtypes = [ce, i32]
+    lib.zero_block_norm_forward.argtypes = [bn] + [vp] * 10
+    lib.zero_block_norm_backward.argtypes = [bn] + [vp] * 15 + [i32, vp, i64, vp]
+    lib.zero_block_norm_workspace.argtypes = [bn]
+    for name in ("zero_embedding_forward", "zero_embedding_backward", "zero_linear_cross_entropy",
+                 "zero_block_norm_forward", "zero_block_norm_backward"):
+        getattr(lib, name).restype = ctypes.c_int
+    for name in ("zero_linear_cross_entropy_workspace", "zero_block_norm_workspace"):
+        getattr(lib, name).restype = i64
+
+
+_declare(_lib)
+
+_IDS = (torch.int64, torch.int32)
+
+
+def _here(stream, *tensors):
+    """Refuses tensors and streams that are not of the current CUDA device, on which the
+    library launches."""
+    device = None
+    for t in tensors:
+        if t is None:
+            continue
+        if device is None:
+            device = t.device
+        if t.device != device or t.device.type != "cuda":
+            raise ValueError(f"expected tensors of one CUDA device, got {device} and {t.device}")
+    if device is not None and device.index != torch.cuda.current_device():
+        raise ValueError(f"the tensors are on {device}, the current device is "
+                         f"cuda:{torch.cuda.current_device()}")
+    of = getattr(stream, "device", None)
+    if device is not None and of is not None and of != device:
+        raise ValueError(f"the tensors are on {device}, the stream on {of}")
+
+
+def _workspace(need, what, workspace, device, stream):
+    """The caller's workspace, or one from PyTorch's allocator, which is asked while the call's
+    stream is current: it hands memory out in that stream's order."""
+    if need < 0:
+        raise ZeroError(need, what)
+    if workspace is not None:
+        return workspace, workspace.numel() * workspace.element_size()
+    if need == 0:
+        return None, 0
+    if stream is None:
+        return torch.empty(need, dtype=torch.uint8, device=device), need
+    if isinstance(stream, int):
+        stream = torch.cuda.ExternalStream(stream, device)
+    with torch.cuda.stream(stream):
+        return torch.empty(need, dtype=torch.uint8, device=device), need
+
+
+def _check(rc, what):
+    if rc != ZERO_OK:
+        raise ZeroError(rc, what)
+
+
+# ---------------------------------------------------------------------- embedding
+
+def _embedding(ids, table, rows, name, kinds):
+    if ids.dim() != 1 or ids.dtype not in _IDS or (ids.numel() > 1 and ids.stride(0) != 1):
+        raise ValueError(f"ids: expected contiguous int64 or int32, got {tuple(ids.shape)} {ids.dtype}")
+    if table.dim() != 2:
+        raise ValueError(f"{name} is a matrix")
+    vocab, width = table.shape
+    s = ZeroEmbedding(ids.numel(), width, vocab, _matrix(name, table, vocab, width, kinds),
+                      _matrix("the rows", rows, ids.numel(), width))
+    return s, ZERO_IDS_I32 if ids.dtype == torch.int32 else 0
+
+
+def zero_embedding_forward(ids, table, y, *, scale: float = 1.0, stream=None) -> None:
+    """y[i] = scale * table[ids[i]] for ids [rows] (int64 or int32), table [vocab, width] and
+    y [rows, width], bf16 with contiguous columns.  Ids outside the table give rows of NaN."""
+    s, flags = _embedding(ids, table, y, "table", _BF16)
+    _here(stream, ids, table, y)
+    _check(_lib.zero_embedding_forward(ctypes.byref(s), _addr(table), _addr(ids), flags, scale, _addr(y),
+                                       _stream_handle(stream)), "zero_embedding_forward")
+
+
+def zero_embedding_backward(dy, ids, dtable, *, scale: float = 1.0, padding=None,
+                            accumulate: bool = False, stream=None) -> None:
+    """dtable[v] = scale * (sum of the rows of dy whose id is v), zeros where there are none; or
+    with accumulate=True added to dtable.  dy bf16, dtable bf16 or fp32.  Rows whose id is
+    `padding`, or outside the table, have no gradient."""
+    s, flags = _embedding(ids, dtable, dy, "dtable", _GRADS)
+    flags |= ZERO_GRAD_F32 if dtable.dtype == torch.float32 else 0
+    flags |= ZERO_GRAD_ACCUMULATE if accumulate else 0
+    _here(stream, dy, ids, dtable)
+    _check(_lib.zero_embedding_backward(ctypes.byref(s), _addr(dy), _addr(ids), flags, scale,
+                                        -1 if padding is None else padding, _addr(dtable),
+                                        _stream_handle(stream)), "zero_embedding_backward")
+
+
+# ------------------------------------------------------------------ cross entropy
+
+def zero_linear_cross_entropy_workspace(rows: int, width: int, vocab: int, gradients: bool = True,
+                                        f32: bool = False, aligned: bool = False) -> int:
+    """Bytes of workspace that suffice for a cross entropy of these sizes; gradients: dx or dw
+    is wanted; f32: dw is fp32; aligned: w starts on a 16-byte boundary and its pitch is a
+    multiple of 8."""
+    flags = (ZERO_LINEAR_BACKWARD if gradients else 0) | (ZERO_LINEAR_ALIGNED if aligned else 0) | \
+        (ZERO_GRAD_F32 if f32 else 0)
+    need = _lib.zero_linear_cross_entropy_workspace(ctypes.byref(ZeroCrossEntropy(rows, width, vocab)), flags)
+    if need < 0:
+        raise ZeroError(need, "zero_linear_cross_entropy_workspace")
+    return need
+
+
+def zero_linear_cross_entropy(x, w, targets, losses=None, total=None, *, dx=None, dw=None,
+                              ignore_index: int = -100, scale=None, accumulate: bool = False,
+                              workspace=None, stream=None) -> None:
+    """Softmax cross entropy of z = x w^T against targets, without keeping z:
+    losses[i] = logsumexp(z[i]) - z[i, targets[i]], total = sum of c[i] losses[i], and total's
+    gradients dx and dw (dw added to with accumulate=True), each where it is given.
+
+    x [rows, width], w [vocab, width], dx: bf16; targets [rows]: int64 or int32; dw bf16 or
+    fp32; losses [rows], total [1], scale [rows]: fp32.  c is scale, or 1 / (rows that are not
+    ignored).  Rows whose target is ignore_index are ignored: 0 everywhere.  Other targets
+    outside [0, vocab) make their loss NaN.  Without a workspace tensor
+    (zero_linear_cross_entropy_workspace bytes) one is taken from PyTorch's allocator."""
+    if x.dim() != 2 or w.dim() != 2:
+        raise ValueError("x and w are matrices")
+    (rows, width), vocab = x.shape, w.shape[0]
+    if targets.shape != (rows,) or targets.dtype not in _IDS or (rows > 1 and targets.stride(0) != 1):
+        raise ValueError(f"targets: expected {rows} contiguous int64 or int32, got "
+                         f"{tuple(targets.shape)} {targets.dtype}")
+    s = ZeroCrossEntropy(rows, width, vocab, _matrix("x", x, rows, width), _matrix("w", w, vocab, width))
+    f32 = (torch.float32,)
+    for name, t, n in (("losses", losses, rows), ("total", total, 1), ("scale", scale, rows)):
+        if t is not None:
+            _vector(name, t, n, f32)
+    flags = ZERO_IDS_I32 if targets.dtype == torch.int32 else 0
+    if dx is not None:
+        s.lddx = _matrix("dx", dx, rows, width)
+    if dw is not None:
+        s.lddw = _matrix("dw", dw, vocab, width, _GRADS)
+        flags |= ZERO_GRAD_F32 if dw.dtype == torch.float32 else 0
+    flags |= ZERO_GRAD_ACCUMULATE if accumulate else 0
+    _here(stream, x, w, targets, losses, total, scale, dx, dw, workspace)
+    need = 0
+    if workspace is None:
+        kind = (ZERO_LINEAR_BACKWARD if dx is not None or dw is not None else 0) | (flags & ZERO_GRAD_F32)
+        if w.data_ptr() % 16 == 0 and (vocab == 1 or s.ldw % 8 == 0):
+            kind |= ZERO_LINEAR_ALIGNED
+        need = _lib.zero_linear_cross_entropy_workspace(ctypes.byref(s), kind)
+    workspace, nbytes = _workspace(need, "zero_linear_cross_entropy_workspace", workspace, x.device, stream)
+    _check(_lib.zero_linear_cross_entropy(ctypes.byref(s), _addr(x), _addr(w), _addr(targets), ignore_index,
+                                          _addr(scale), _addr(losses), _addr(total), _addr(dx), _addr(dw),
+                                          flags, _addr(workspace), nbytes, _stream_handle(stream)),
+           "zero_linear_cross_entropy")
+
+
+# -------------------------------------------------------------------- block norms
+
+def _block_norm(rows, width, post, kind, alpha, eps, h, gate, vectors):
+    s = ZeroBlockNorm(rows, width, post, kind, alpha, eps)
+    if h is not None:
+        s.ldh = _matrix("h", h, rows, width)
+    if gate is not None:
+        if gate.dim() == 1:
+            _vector("gate", gate, width)
+        else:
+            s.ldg = max(_matrix("gate", gate, rows, width), width)
+    for name, t in vectors.items():
+        if t is not None:
+            _vector(name, t, width)
+    return s
+
+
+def zero_block_norm_forward(r, y, *, h=None, s=None, post: int = ZERO_NORM_NONE, post_weight=None,
+                            post_bias=None, gate=None, alpha: float = 1.0, kind: int = ZERO_NORM_RMS,
+                            weight=None, bias=None, eps: float = 1e-5, stream=None) -> None:
+    """s = r + alpha * gate * P(h) and y = N(s), each row by itself, all bf16.
+
+    r, y, h, s [rows, width] with contiguous columns; h None: s is r.  P: the norm `post`
+    (ZERO_NORM_NONE, _RMS, _LAYER) with post_weight and post_bias; N: `kind` (RMS or LAYER) with
+    weight and bias (vectors; None: 1 and 0).  gate: a vector [width] or a matrix [rows, width].
+    s may be r itself, or None where only y is wanted."""
+    if r.dim() != 2:
+        raise ValueError("r is a matrix")
+    rows, width = r.shape
+    z = _block_norm(rows, width, post, kind, alpha, eps, h, gate,
+                    {"post_weight": post_weight, "post_bias": post_bias, "weight": weight, "bias": bias})
+    z.ldr = _matrix("r", r, rows, width)
+    z.ldy = _matrix("y", y, rows, width)
+    if s is not None:
+        z.lds = _matrix("s", s, rows, width)
+    _here(stream, r, y, h, s, post_weight, post_bias, gate, weight, bias)
+    _check(_lib.zero_block_norm_forward(ctypes.byref(z), _addr(r), _addr(h), _addr(post_weight),
+                                        _addr(post_bias), _addr(gate), _addr(weight), _addr(bias), _addr(s),
+                                        _addr(y), _stream_handle(stream)), "zero_block_norm_forward")
+
+
+def zero_block_norm_workspace(rows: int, width: int) -> int:
+    """Bytes of workspace that suffice for zero_block_norm_backward."""
+    need = _lib.zero_block_norm_workspace(ctypes.byref(ZeroBlockNorm(rows, width)))
+    if need < 0:
+        raise ZeroError(need, "zero_block_norm_workspace")
+    return need
+
+
+def zero_block_norm_backward(dy, s, *, ds=None, h=None, post: int = ZERO_NORM_NONE, post_weight=None,
+                             post_bias=None, gate=None, alpha: float = 1.0, kind: int = ZERO_NORM_RMS,
+                             weight=None, eps: float = 1e-5, dr=None, dh=None, dgate=None,
+                             dpost_weight=None, dpost_bias=None, dweight=None, dbias=None,
+                             accumulate: bool = False, workspace=None, stream=None) -> None:
+    """Gradients of zero_block_norm_forward, from dy and the gradient ds that reaches s from
+    elsewhere (None: 0); each output that is given is written.
+
+    dr, dh and a matrix dgate are bf16; dpost_weight, dpost_bias, dweight, dbias and a vector
+    dgate are bf16 or fp32, all alike, and added to with accumulate=True.  dr may be ds itself."""
+    if dy.dim() != 2:
+        raise ValueError("dy is a matrix")
+    rows, width = dy.shape
+    z = _block_norm(rows, width, post, kind, alpha, eps, h, gate,
+                    {"post_weight": post_weight, "post_bias": post_bias, "weight": weight})
+    z.lddy = _matrix("dy", dy, rows, width)
+    z.lds = _matrix("s", s, rows, width)
+    for name, t in (("ds", ds), ("dr", dr), ("dh", dh)):
+        if t is not None:
+            setattr(z, "ld" + name, _matrix(name, t, rows, width))
+    sums = {"dpost_weight": dpost_weight, "dpost_bias": dpost_bias, "dweight": dweight, "dbias": dbias}
+    if dgate is not None:
+        if gate is None or dgate.dim() != gate.dim():
+            raise ValueError("dgate is of gate's shape")
+        if gate.dim() == 1:
+            sums["dgate"] = dgate
+        else:
+            z.lddg = max(_matrix("dgate", dgate, rows, width), width)
+    kinds = {t.dtype for t in sums.values() if t is not None}
+    if len(kinds) > 1:
+        raise ValueError("the gradients of vectors are bf16 or fp32, all alike")
+    for name, t in sums.items():
+        if t is not None:
+            _vector(name, t, width, _GRADS)
+    flags = (ZERO_GRAD_F32 if kinds == {torch.float32} else 0) | (ZERO_GRAD_ACCUMULATE if accumulate else 0)
+    _here(stream, dy, s, ds, h, post_weight, post_bias, gate, weight, dr, dh, dgate, dpost_weight,
+          dpost_bias, dweight, dbias, workspace)
+    need = _lib.zero_block_norm_workspace(ctypes.byref(z)) if workspace is None else 0
+    workspace, nbytes = _workspace(need, "zero_block_norm_workspace", workspace, dy.device, stream)
+    _check(_lib.zero_block_norm_backward(
+        ctypes.byref(z), _addr(dy), _addr(ds), _addr(s), _addr(h), _addr(post_weight), _addr(post_bias),
+        _addr(gate), _addr(weight), _addr(dr), _addr(dh), _addr(dgate), _addr(dpost_weight),
+        _addr(dpost_bias), _addr(dweight), _addr(dbias), flags, _addr(workspace), nbytes,
+        _stream_handle(stream)), "zero_block_norm_backward")
+
+
+__all__ = ["zero_embedding_forward", "zero_embedding_backward", "zero_linear_cross_entropy",
+           "zero_linear_cross_entropy_workspace", "zero_block_norm_forward", "zero_block_norm_backward",
+           "zero_block_norm_workspace", "ZeroEmbedding", "ZeroCrossEntropy", "ZeroBlockNorm"]
