@@ -220,7 +220,7 @@ int zero_linear_backward(const zero_linear_t* shape, const void* dy, const void*
   const Matrix ms{need > 0 ? workspace : nullptr, 1, need, need, 1};
   for (const Matrix* m : {&mdy, &mx, &mw, &mp, &mi, &mdx, &mdw, &mdb})
     if (share(ms, *m)) return ZERO_E_ALIAS;
-  LinearBackwardLaunch L;
+  LinearBackwardLaunch L{};
   L.s = s;
   L.dy = static_cast<const uint16_t*>(dy);
   L.x = static_cast<const uint16_t*>(x);

@@ -36,6 +36,7 @@ struct Words {
   int32_t again;   // some row of this piece wants another reference
   int32_t ticket;  // blocks of the last kernel that are done
   int32_t valid;   // rows that are not ignored, of all pieces
+  float share;     // 1 / valid: c of the mean (0 where there is none)
 };
 
 struct LossArgs {
@@ -81,7 +82,7 @@ __global__ void __launch_bounds__(1024) loss_count_kernel(const __grid_constant_
   __syncthreads();
   if (threadIdx.x < 32) {
     n = __reduce_add_sync(0xffffffffu, part[threadIdx.x]);
-    if (threadIdx.x == 0) *a.words = Words{0, 0, n};
+    if (threadIdx.x == 0) *a.words = Words{0, 0, n, n > 0 ? 1.0f / static_cast<float>(n) : 0.0f};
   }
 }
 
@@ -95,7 +96,9 @@ __device__ __forceinline__ float warp_sum(float x) {
 // (its x may hold anything, and 0 times an infinity would reach dw).
 template <bool VEC>
 __global__ void __launch_bounds__(256) loss_rows_kernel(const __grid_constant__ LossArgs a) {
-  wait_for_predecessor();
+  // The first piece's rows do not wait for the count, whose kernel let this one begin when
+  // all that came before was complete.
+  if (a.first > 0) wait_for_predecessor();
   launch_dependents();
   const int lane = threadIdx.x % 32;
   for (int64_t i = static_cast<int64_t>(blockIdx.x) * 8 + threadIdx.x / 32; i < a.rows;
@@ -140,29 +143,28 @@ __global__ void __launch_bounds__(256) loss_rows_kernel(const __grid_constant__ 
       a.column[i] = column ? static_cast<int32_t>(t) : ignored ? -1 : -2;
     }
   }
+  if (a.first == 0) wait_for_predecessor();
 }
 
 constexpr int kFinishThreads = 256, kFinishWarps = kFinishThreads / 32;
 
-// A block a row: the row's sums in the order of its parts, its loss, and dz.  AGAIN: the
-// second time, where the first has asked for it; its last block adds up the losses.
-// Bound by HBM: 4 bytes an element (8192 x 50257).
+// A block a row: the row's sums in the order of its parts, its loss, and dz.  With c alike
+// for all rows (the mean) dz is p less the target's 1, whose rounding is nothing where p is
+// small, and c multiplies the products' sums; a scale of each row's own is in its dz.
+// AGAIN: the second time, where the first has asked for it.  The last block adds up the
+// losses.  Bound by HBM: 4 bytes an element (8192 x 50257: 1.65 GB).
 template <bool AGAIN>
 __global__ void __launch_bounds__(kFinishThreads) loss_finish_kernel(const __grid_constant__ LossArgs a) {
-  __shared__ float part[kFinishWarps];
-  __shared__ float top_part[kFinishWarps];
+  __shared__ float2 part[kFinishWarps];
   __shared__ double sum_part[kFinishWarps];
   __shared__ int32_t last;
   wait_for_predecessor();
   launch_dependents();
+  if (AGAIN && __ldcg(&a.words->again) == 0) return;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  const int32_t valid = __ldcg(&a.words->valid);
-  const auto share_of = [&](int64_t i) {  // c of row i
-    return a.scale != nullptr ? __ldg(a.scale + i) : 1.0f / static_cast<float>(valid);
-  };
-  const bool run = !AGAIN || __ldcg(&a.words->again) != 0;
-  for (int64_t i = blockIdx.x; run && i < a.rows; i += gridDim.x) {
+  for (int64_t i = blockIdx.x; i < a.rows; i += gridDim.x) {
     const int32_t t = __ldcg(a.column + i);
+    const float zt = __ldcg(a.zt + i), ref = __ldcg(a.ref + i);
     float sum = 0.0f, top = -INFINITY;
     if (t != -1) {
       for (int k = threadIdx.x; k < a.parts; k += kFinishThreads) {
@@ -175,24 +177,20 @@ __global__ void __launch_bounds__(kFinishThreads) loss_finish_kernel(const __gri
 #pragma unroll
     for (int k = 16; k > 0; k /= 2) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, k));
     __syncthreads();  // the row before is done with these
-    if (lane == 0) {
-      part[warp] = sum;
-      top_part[warp] = top;
-    }
+    if (lane == 0) part[warp] = make_float2(sum, top);
     __syncthreads();
     sum = 0.0f;
 #pragma unroll
     for (int k = 0; k < kFinishWarps; ++k) {
-      sum += part[k];
-      top = fmaxf(top, top_part[k]);
+      sum += part[k].x;
+      top = fmaxf(top, part[k].y);
     }
-    const float zt = __ldcg(a.zt + i), ref = __ldcg(a.ref + i);
     const bool own = zt == ref;
     const float et = own ? 1.0f : expf(zt - ref);
     const float whole = sum + et;
     float loss = own ? log1pf(sum) : (ref - zt) + logf(whole);
     // a NaN is no column's, or of the inputs'; an infinite logit leaves no gradient
-    float f = share_of(a.first + i) / whole;
+    float f = (a.scale != nullptr ? __ldg(a.scale + a.first + i) : 1.0f) / whole;
     if (!isfinite(whole)) f = NAN;
     if (t == -1) loss = f = 0.0f;
     if (t == -2) loss = f = NAN;
@@ -204,46 +202,78 @@ __global__ void __launch_bounds__(kFinishThreads) loss_finish_kernel(const __gri
       }
     }
     if (a.held == nullptr) continue;
+    // (the pitch has room for whole vectors; an ignored row's are not read)
     uint16_t* row = a.held + i * a.ldz;
-    constexpr float kStep2 = kLog2e / 1024.0f;
-    for (int64_t j = 8 * threadIdx.x; j < a.vocab; j += 8 * kFinishThreads) {
-      // (the pitch has room for whole vectors)
-      uint4* at = reinterpret_cast<uint4*>(row + j);
-      float y[8] = {};
-      if (t != -1) {
-        const uint4 v = __ldcs(at);
-        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    constexpr int kSpan = 8 * kFinishThreads, U = 2;
+    for (int64_t j0 = 8 * threadIdx.x; j0 < a.vocab; j0 += U * kSpan) {
+      uint4 v[U];
 #pragma unroll
-        for (int c = 0; c < 8; ++c) {
-          const int16_t d = static_cast<int16_t>(c % 2 ? w[c / 2] >> 16 : w[c / 2] & 0xffffu);
-          const float e = d == INT16_MIN ? 0.0f : fast_exp2(static_cast<float>(d) * kStep2);
-          y[c] = j + c == t ? -(f * sum) : f * e;
+      for (int u = 0; u < U; ++u)
+        if (t != -1 && j0 + u * kSpan < a.vocab)
+          v[u] = __ldcs(reinterpret_cast<const uint4*>(row + j0 + u * kSpan));
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int64_t j = j0 + u * kSpan;
+        if (j >= a.vocab) break;
+        float y[8] = {};
+        if (t != -1) {
+          const uint32_t w[4] = {v[u].x, v[u].y, v[u].z, v[u].w};
+#pragma unroll
+          for (int c = 0; c < 8; ++c) {
+            const int16_t d = static_cast<int16_t>(c % 2 ? w[c / 2] >> 16 : w[c / 2] & 0xffffu);
+            const float e = fast_exp2(static_cast<float>(d) * (kLog2e / 1024.0f));
+            y[c] = d == INT16_MIN ? f * 0.0f : f * e;
+          }
+          if (t - j >= 0 && t - j < 8) {
+#pragma unroll
+            for (int c = 0; c < 8; ++c)
+              if (j + c == t) y[c] = -(f * sum);
+          }
         }
+        *reinterpret_cast<uint4*>(row + j) = to_bf16x8(y);
       }
-      *at = to_bf16x8(y);
     }
   }
-  if constexpr (AGAIN) {
-    if (a.total == nullptr) return;
-    __threadfence();
-    __syncthreads();
-    if (threadIdx.x == 0) last = atomicAdd(&a.words->ticket, 1) == static_cast<int32_t>(gridDim.x) - 1;
-    __syncthreads();
-    if (!last) return;
-    __threadfence();
-    double total = 0.0;
-    for (int64_t i = threadIdx.x; i < a.all_rows; i += kFinishThreads)
-      if (target_of(a, i) != a.ignore)
-        total += static_cast<double>(share_of(i)) * static_cast<double>(__ldcg(a.losses + i));
-#pragma unroll
-    for (int k = 16; k > 0; k /= 2) total += __shfl_xor_sync(0xffffffffu, total, k);
-    if (lane == 0) sum_part[warp] = total;
-    __syncthreads();
-    if (threadIdx.x != 0) return;
-    total = 0.0;
-    for (int k = 0; k < kFinishWarps; ++k) total += sum_part[k];
-    *a.total = static_cast<float>(total);
+  if (a.total == nullptr) return;
+  __threadfence();
+  __syncthreads();
+  if (threadIdx.x == 0) last = atomicAdd(&a.words->ticket, 1) == static_cast<int32_t>(gridDim.x) - 1;
+  __syncthreads();
+  if (!last) return;
+  __threadfence();
+  if (!AGAIN) {
+    if (threadIdx.x == 0) a.words->ticket = 0;
+    if (__ldcg(&a.words->again) != 0) return;  // there are other losses to come
   }
+  // in 64 bits, a thread's own in chains of 8
+  double total = 0.0;
+  constexpr int U = 8;
+  for (int64_t i0 = threadIdx.x; i0 < a.all_rows; i0 += U * kFinishThreads) {
+    float x[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int64_t i = i0 + u * kFinishThreads;
+      x[u] = i < a.all_rows ? __ldcg(a.losses + i) : 0.0f;
+      if (a.scale != nullptr && i < a.all_rows && target_of(a, i) != a.ignore)
+        total += static_cast<double>(__ldg(a.scale + i)) * static_cast<double>(x[u]);
+    }
+    if (a.scale == nullptr) {
+#pragma unroll
+      for (int u = 0; u < U; ++u) total += static_cast<double>(x[u]);
+    }
+  }
+#pragma unroll
+  for (int k = 16; k > 0; k /= 2) total += __shfl_xor_sync(0xffffffffu, total, k);
+  if (lane == 0) sum_part[warp] = total;
+  __syncthreads();
+  if (threadIdx.x != 0) return;
+  total = 0.0;
+  for (int k = 0; k < kFinishWarps; ++k) total += sum_part[k];
+  if (a.scale == nullptr) {
+    const int32_t valid = __ldcg(&a.words->valid);
+    total = valid > 0 ? total / valid : 0.0;
+  }
+  *a.total = static_cast<float>(total);
 }
 
 // The next piece of rows asks anew.
@@ -416,7 +446,8 @@ cudaError_t launch_cross_entropy(const CrossEntropyLaunch& L) {
     if (e == cudaSuccess) e = chain.launch(loss_finish_kernel<false>, grid, kFinishThreads, 0, 1, a);
     x.of.only_if = &a.words->again;
     if (e == cudaSuccess) e = launch_exponents(x);
-    if (e == cudaSuccess) e = chain.launch(loss_finish_kernel<true>, grid, kFinishThreads, 0, 1, a);
+    if (e == cudaSuccess)
+      e = chain.launch(loss_finish_kernel<true>, blocks_of(a.rows, 2 * kSms), kFinishThreads, 0, 1, a);
     if (e != cudaSuccess || !grads) continue;
     LinearBackwardLaunch b{};
     b.s = linear_of(s, a.rows);
@@ -429,6 +460,7 @@ cudaError_t launch_cross_entropy(const CrossEntropyLaunch& L) {
     if (joined) b.s.lddw = round_up(s.width, 4);
     b.grad_f32 = L.grad_f32 || joined;
     b.accumulate = first > 0 || (L.accumulate && !joined);
+    b.scale = L.scale == nullptr ? &a.words->share : nullptr;
     b.workspace = base + l.linear;
     b.stream = L.stream;
     b.withhold = L.withhold;

@@ -628,8 +628,13 @@ __global__ void __launch_bounds__(kProductThreads, 1)
   const uint32_t rank = CG == 2 ? cluster_rank() : 0u;
   const int unit = blockIdx.x / CG;
   const Turns turns{a.early_units, a.early_tiles, static_cast<int>(gridDim.x) / CG};
-  int tiles = a.whole + (a.tiles_m * a.tiles_n - a.whole) * a.splits;
+  const int tiles = a.whole + (a.tiles_m * a.tiles_n - a.whole) * a.splits;
 
+  if constexpr (KIND == kExponent)
+    if (a.x.only_if != nullptr) {  // alike for every thread of the grid
+      wait_for_predecessor();
+      if (__ldcg(a.x.only_if) == 0) return;
+    }
   if (threadIdx.x == 0) {
     *failed = 0;
     for (int s = 0; s < stages; ++s) {
@@ -649,8 +654,6 @@ __global__ void __launch_bounds__(kProductThreads, 1)
   if (warp == 1) tmem_alloc<CG>(tmem_at, Shape::kColumns);
   if (!a.late) wait_for_predecessor();
   launch_dependents();
-  if constexpr (KIND == kExponent)
-    if (a.x.only_if != nullptr && __ldcg(a.x.only_if) == 0) tiles = 0;
   tc_fence_before();
   __syncthreads();
   if constexpr (CG == 2) cluster_sync();
@@ -800,6 +803,8 @@ __global__ void __launch_bounds__(kProductThreads, 1)
     int n = 0;
     bool ok = true;
     ExponentPart exponents;  // of kExponent
+    const bool scaled = KIND != kForward && KIND != kExponent && a.e.scale != nullptr;
+    const float scale = scaled ? __ldcg(a.e.scale) : 1.0f;
     for (int t = turns.first(unit); t < tiles && ok; t = turns.after(t)) {
       const Tile tile = tile_of<BM>(a, t);
       const int64_t row0 = tile.row + rank * kBlockRows + quarter * 32;
@@ -819,6 +824,10 @@ __global__ void __launch_bounds__(kProductThreads, 1)
       // 32 columns from c on are summed up: on their way.
       const auto finish = [&](float x[32], int c) {
         const int64_t col0 = tile.col + c;
+        if (scaled) {
+#pragma unroll
+          for (int q = 0; q < 32; ++q) x[q] *= scale;
+        }
         if constexpr (GATHER) {
           float* to = reinterpret_cast<float*>(ring) + (c / 32 * 4 + quarter) * 32 * 32;
 #pragma unroll
@@ -1880,6 +1889,7 @@ cudaError_t launch_linear_backward(const LinearBackwardLaunch& L) {
     p.e.lds = s.ldpi;
     p.e.out = L.dx;
     p.e.ldo = s.lddx;
+    p.e.scale = L.scale;
     // dbias's kernel has waited for all that this one reads before it let it begin
     e = launch_product(p, plan.dx, L.dbias != nullptr, &space, L.withhold, &chain, &dx);
     if (e != cudaSuccess) return e;
@@ -1895,6 +1905,7 @@ cudaError_t launch_linear_backward(const LinearBackwardLaunch& L) {
     p.depth = s.rows;
     p.e.out = L.dw;
     p.e.ldo = s.lddw;
+    p.e.scale = L.scale;
     p.e.out_f32 = L.grad_f32;
     p.e.accumulate = L.accumulate;
     // (and so have dx's product, or what came before that)

@@ -147,6 +147,7 @@ struct Epilogue {
   void* out;                 // bf16, or fp32
   int64_t ldo;
   int32_t out_f32, accumulate;
+  const float* scale;        // gradients: multiplies the sum first, one number on the device
   int32_t vec;               // every matrix's base and pitch are multiples of 16 bytes
 };
 

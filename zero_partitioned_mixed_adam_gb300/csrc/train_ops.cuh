@@ -81,6 +81,7 @@ struct LinearBackwardLaunch {
   void* workspace;
   cudaStream_t stream;
   int32_t withhold;
+  const float* scale;  // of dx and dw, one number on the device; NULL: 1
 };
 
 // ------------------------------------------- exponentials of a linear map's rows

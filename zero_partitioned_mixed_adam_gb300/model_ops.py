@@ -64,20 +64,13 @@ _IDS = (torch.int64, torch.int32)
 def _here(stream, *tensors):
     """Refuses tensors and streams that are not of the current CUDA device, on which the
     library launches."""
-    device = None
+    here = torch.cuda.current_device() if torch.cuda.is_initialized() else 0
     for t in tensors:
-        if t is None:
-            continue
-        if device is None:
-            device = t.device
-        if t.device != device or t.device.type != "cuda":
-            raise ValueError(f"expected tensors of one CUDA device, got {device} and {t.device}")
-    if device is not None and device.index != torch.cuda.current_device():
-        raise ValueError(f"the tensors are on {device}, the current device is "
-                         f"cuda:{torch.cuda.current_device()}")
+        if t is not None and t.get_device() != here:
+            raise ValueError(f"expected tensors of the current device, cuda:{here}, not of {t.device}")
     of = getattr(stream, "device", None)
-    if device is not None and of is not None and of != device:
-        raise ValueError(f"the tensors are on {device}, the stream on {of}")
+    if of is not None and of.index != here:
+        raise ValueError(f"the tensors are on cuda:{here}, the stream on {of}")
 
 
 def _workspace(need, what, workspace, device, stream):
