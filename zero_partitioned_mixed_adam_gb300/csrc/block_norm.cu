@@ -15,10 +15,10 @@ namespace {
 constexpr int kMostThreads = 512, kMostWarps = kMostThreads / 32, kMostCluster = 8;
 constexpr int kStages = 4;  // rows under way
 
-// Who shares a row: a warp up to 1,024 columns (forward), a block up to 4,096, a cluster of
-// blocks beyond.  A thread's columns are few in every case, so that the backward pass has
-// room for the sums of each in registers.
-enum Share { kWarp, kBlock, kCluster };
+// Who shares a row: a block up to 4,096 columns, a cluster of blocks beyond.  A thread has 8
+// columns in every case, so that the backward pass has room for the sums of each in
+// registers, and the vectors are read once.
+enum Share { kBlock, kCluster };
 
 __device__ __forceinline__ uint32_t cluster_blocks() {
   uint32_t n;
@@ -65,86 +65,136 @@ __device__ __forceinline__ void copy_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-// Columns of a thread: 8 for each of V, a 16-byte vector (VEC), or 8 single ones spread
-// over the row.  (`lanes` threads share a row.)
-template <int V, bool VEC>
+// A thread's 8 columns of a row, in fp32, two to an operation: with one at a time the kernels
+// were bound by their instructions (500 a row and warp forward, 780 backward).
+struct Eight {
+  Pair p[4];
+};
+__device__ __forceinline__ Eight all_of(float x) {
+  Eight r;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) r.p[k] = pair(x, x);
+  return r;
+}
+__device__ __forceinline__ Eight eight_of(uint4 v) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  Eight r;
+#pragma unroll
+  for (int k = 0; k < 4; ++k)
+    r.p[k] = pair(__uint_as_float(w[k] << 16), __uint_as_float(w[k] & 0xffff0000u));
+  return r;
+}
+__device__ __forceinline__ uint4 bf16_of(const Eight& x) {
+  uint32_t w[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    float lo, hi;
+    split(x.p[k], lo, hi);
+    w[k] = bf16x2_bits(lo, hi);
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+__device__ __forceinline__ Eight operator*(const Eight& a, const Eight& b) {
+  Eight r;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) r.p[k] = a.p[k] * b.p[k];
+  return r;
+}
+__device__ __forceinline__ Eight operator*(const Eight& a, float b) { return a * all_of(b); }
+__device__ __forceinline__ Eight operator+(const Eight& a, const Eight& b) {
+  Eight r;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) r.p[k] = a.p[k] + b.p[k];
+  return r;
+}
+__device__ __forceinline__ Eight fma8(const Eight& a, const Eight& b, const Eight& c) {
+  Eight r;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) r.p[k] = fma2(a.p[k], b.p[k], c.p[k]);
+  return r;
+}
+__device__ __forceinline__ float total(Pair a, Pair b, Pair c, Pair d) {
+  float lo, hi;
+  split((a + b) + (c + d), lo, hi);
+  return lo + hi;
+}
+__device__ __forceinline__ float sum8(const Eight& a) { return total(a.p[0], a.p[1], a.p[2], a.p[3]); }
+__device__ __forceinline__ float dot8(const Eight& a, const Eight& b) {
+  float lo, hi;
+  split(fma2(a.p[0], b.p[0], a.p[1] * b.p[1]) + fma2(a.p[2], b.p[2], a.p[3] * b.p[3]), lo, hi);
+  return lo + hi;
+}
+
+// A thread's columns: a 16-byte vector (VEC), or 8 single ones spread over the row.
+template <bool VEC>
 struct Columns {
-  int at, lanes;
-  int width;
-  __device__ __forceinline__ int of(int k) const {  // k-th column, 0 to 8 V - 1
-    return VEC ? (k / 8 * lanes + at) * 8 + k % 8 : k * lanes + at;
-  }
+  int at, lanes, width;
+  bool whole;  // all 8 are the row's, and may go as a vector
+  __device__ __forceinline__ Columns(int at, int lanes, int width)
+      : at(at), lanes(lanes), width(width), whole(VEC && 8 * at + 8 <= width) {}
+  __device__ __forceinline__ int of(int k) const { return VEC ? 8 * at + k : k * lanes + at; }
   __device__ __forceinline__ bool in(int k) const { return of(k) < width; }
-  __device__ __forceinline__ bool whole(int v) const { return VEC && of(8 * v) + 8 <= width; }
-  // Elements of a row (0 past its end).
-  __device__ __forceinline__ void load(const uint16_t* p, float x[8 * V], bool vec = VEC) const {
+  // Elements one by one (0 past the row's end).
+  __device__ __forceinline__ Eight load_single(const uint16_t* p) const {
+    float x[8];
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-      if (vec && whole(v)) {
-        bf16x8(*reinterpret_cast<const uint4*>(p + of(8 * v)), x + 8 * v);
-      } else {
+    for (int k = 0; k < 8; ++k) x[k] = in(k) ? bf16_at(p + of(k)) : 0.0f;
+    Eight r;
 #pragma unroll
-        for (int c = 0; c < 8; ++c) x[8 * v + c] = in(8 * v + c) ? bf16_at(p + of(8 * v + c)) : 0.0f;
-      }
+    for (int k = 0; k < 4; ++k) r.p[k] = pair(x[2 * k], x[2 * k + 1]);
+    return r;
+  }
+  // A vector of the columns (NULL: `other`), which lies on 16 bytes or not.
+  __device__ __forceinline__ Eight load_vector(const uint16_t* p, float other, bool vec) const {
+    if (p == nullptr) return all_of(other);
+    if (vec && whole) return eight_of(__ldg(reinterpret_cast<const uint4*>(p + 8 * at)));
+    return load_single(p);
+  }
+  __device__ __forceinline__ void store(uint16_t* p, const Eight& x) const {
+    if (whole) {
+      *reinterpret_cast<uint4*>(p + 8 * at) = bf16_of(x);
+      return;
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      float lo, hi;
+      split(x.p[k], lo, hi);
+      if (in(2 * k)) p[of(2 * k)] = to_bf16(lo);
+      if (in(2 * k + 1)) p[of(2 * k + 1)] = to_bf16(hi);
     }
   }
-  __device__ __forceinline__ void store(uint16_t* p, const float x[8 * V]) const {
+  // Columns past the row's end set to 0 (a thread that has some).
+  __device__ __forceinline__ void clear(Eight& x) const {
+    if (whole) return;
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-      if (whole(v)) {
-        *reinterpret_cast<uint4*>(p + of(8 * v)) = to_bf16x8(x + 8 * v);
-      } else {
-#pragma unroll
-        for (int c = 0; c < 8; ++c)
-          if (in(8 * v + c)) p[of(8 * v + c)] = to_bf16(x[8 * v + c]);
-      }
+    for (int k = 0; k < 4; ++k) {
+      float lo, hi;
+      split(x.p[k], lo, hi);
+      x.p[k] = pair(in(2 * k) ? lo : 0.0f, in(2 * k + 1) ? hi : 0.0f);
     }
   }
 };
 
-// A vector of the columns, held in registers as bf16: 4 of them for 8 columns.
-template <int V>
-struct Held {
-  uint32_t p[4 * V];
-  template <bool VEC>
-  __device__ __forceinline__ Held(const Columns<V, VEC>& at, const uint16_t* from, float other, bool vec) {
-    float x[8 * V];
-    if (from != nullptr) at.load(from, x, vec);
-#pragma unroll
-    for (int k = 0; k < 4 * V; ++k)
-      p[k] = from != nullptr ? bf16x2_bits(x[2 * k], x[2 * k + 1]) : bf16x2_bits(other, other);
-  }
-  __device__ __forceinline__ float operator[](int k) const {
-    return __uint_as_float(k % 2 ? p[k / 2] & 0xffff0000u : p[k / 2] << 16);
-  }
-};
-
-// The rows that a thread reads, kStages ahead (RING): its own 16 bytes of each input, from
-// its own place in shared memory, so no thread waits for another's.  Rows that are not on
-// 16-byte boundaries, and those too wide for the ring, are read when they are wanted.
-template <int V, bool VEC, bool RING>
+// The rows that a thread reads, kStages ahead (VEC): its own 16 bytes of each input, from its
+// own place in shared memory, so no thread waits for another's.  Rows that are not on 16-byte
+// boundaries are read when they are wanted.
+template <bool VEC>
 struct Rows {
   const NormArgs& a;
-  const Columns<V, VEC>& at;
+  const Columns<VEC>& at;
   uint8_t* ring;      // of this thread
-  int32_t threads;    // of the block
+  int32_t pitch;      // of a place in a stage
   int64_t next;       // the row that is asked for next
   int64_t step;
   int put = 0, got = 0;
 
-  __device__ __forceinline__ uint8_t* slot(int stage, int q, int v) const {
-    return ring + ((stage * a.inputs + a.place[q]) * V + v) * threads * 16;
-  }
   __device__ __forceinline__ void ask() {
-    if constexpr (RING) {
-      if (next < a.rows) {
+    if constexpr (VEC) {
+      if (next < a.rows && at.whole) {
+        uint8_t* to = ring + put * a.inputs * pitch;
 #pragma unroll
-        for (int q = 0; q < kInputs; ++q) {
-          if (a.in[q] == nullptr) continue;
-#pragma unroll
-          for (int v = 0; v < V; ++v)
-            if (at.whole(v)) copy16(slot(put, q, v), a.in[q] + next * a.ld[q] + at.of(8 * v));
-        }
+        for (int q = 0; q < kInputs; ++q)
+          if (a.in[q] != nullptr) copy16(to + a.place[q] * pitch, a.in[q] + next * a.ld[q] + 8 * at.at);
       }
       next += step;
       put = put + 1 == kStages ? 0 : put + 1;
@@ -155,81 +205,80 @@ struct Rows {
 #pragma unroll
     for (int k = 1; k < kStages; ++k) ask();
   }
-  // The row after the last can be read.
+  // The next row can be read.
   __device__ __forceinline__ void arrive() {
-    if constexpr (RING) {
-      ask();
-      copy_wait<kStages - 1>();
-    }
+    ask();
+    if constexpr (VEC) copy_wait<kStages - 1>();
   }
-  __device__ __forceinline__ void read(int q, int64_t i, float x[8 * V]) const {
-    if constexpr (RING) {
-#pragma unroll
-      for (int v = 0; v < V; ++v) {
-        if (at.whole(v)) {
-          bf16x8(*reinterpret_cast<const uint4*>(slot(got, q, v)), x + 8 * v);
-        } else {
-          const uint16_t* p = a.in[q] + i * a.ld[q];
-#pragma unroll
-          for (int c = 0; c < 8; ++c) x[8 * v + c] = at.in(8 * v + c) ? bf16_at(p + at.of(8 * v + c)) : 0.0f;
-        }
-      }
-    } else {
-      at.load(a.in[q] + i * a.ld[q], x);
-    }
+  __device__ __forceinline__ Eight read(int q, int64_t i) const {
+    if (VEC && at.whole)
+      return eight_of(*reinterpret_cast<const uint4*>(ring + (got * a.inputs + a.place[q]) * pitch));
+    return at.load_single(a.in[q] + i * a.ld[q]);
   }
   __device__ __forceinline__ void done() { got = got + 1 == kStages ? 0 : got + 1; }
 };
 
-// Sums over the threads of a row, in the same order for each of them.  The warps' parts go
+// N sums over the threads of a row, in the same order for each of them.  The warps' parts go
 // through shared memory, every block's to all blocks of the cluster, in two places taken in
 // turn, so that one barrier is enough: a place is written again only after the barrier
 // that follows its reading.
 template <Share SHARE>
 struct RowSum {
-  static constexpr int kParts = SHARE == kWarp ? 1 : SHARE == kBlock ? kMostWarps : kMostCluster * kMostWarps;
-  float4 (*part)[kParts];
+  static constexpr int kParts = SHARE == kBlock ? 32 : kMostCluster * kMostWarps;
+  float4 (*part)[kParts];  // kBlock: places past the block's warps are 0
   int place = 0;
-  __device__ __forceinline__ float3 operator()(float x, float y = 0.0f, float z = 0.0f) {
-    const auto add_lanes = [&] {
+  template <int N>
+  __device__ __forceinline__ void lanes(float (&x)[N], int width) {
 #pragma unroll
-      for (int k = 16; k > 0; k /= 2) {
-        x += __shfl_xor_sync(0xffffffffu, x, k);
-        y += __shfl_xor_sync(0xffffffffu, y, k);
-        z += __shfl_xor_sync(0xffffffffu, z, k);
+    for (int k = 16; k > 0; k /= 2)
+      if (k < width) {
+#pragma unroll
+        for (int n = 0; n < N; ++n) x[n] += __shfl_xor_sync(0xffffffffu, x[n], k);
       }
-    };
-    add_lanes();
+  }
+  template <int N>
+  __device__ __forceinline__ void put(float4* to, const float (&x)[N]) {
+    if constexpr (N == 1) to->x = x[0];
+    else *to = make_float4(x[0], x[1], N > 2 ? x[2] : 0.0f, 0.0f);
+  }
+  template <int N>
+  __device__ __forceinline__ void get(const float4* from, float (&x)[N]) {
+    if constexpr (N == 1) {
+      x[0] += from->x;
+    } else {
+      const float4 p = *from;
+      x[0] += p.x;
+      x[1] += p.y;
+      if (N > 2) x[2] += p.z;
+    }
+  }
+  template <int N>
+  __device__ __forceinline__ void operator()(float (&x)[N]) {
+    static_assert(N >= 1 && N <= 3, "a part has room for 3");
+    lanes(x, 32);
     const int warps = blockDim.x / 32, warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     if constexpr (SHARE == kBlock) {
-      if (lane == 0) part[place][warp] = make_float4(x, y, z, 0.0f);
+      if (warps == 1) return;
+      if (lane == 0) put(&part[place][warp], x);
       __syncthreads();
-      x = y = z = 0.0f;
-#pragma unroll 4
-      for (int w = 0; w < warps; ++w) {
-        const float4 p = part[place][w];
-        x += p.x;
-        y += p.y;
-        z += p.z;
-      }
-      place ^= 1;
-    } else if constexpr (SHARE == kCluster) {
+#pragma unroll
+      for (int n = 0; n < N; ++n) x[n] = 0.0f;
+      get(&part[place][lane % kMostWarps], x);
+      lanes(x, kMostWarps);
+    } else {
       const int blocks = static_cast<int>(cluster_blocks());
       if (lane < blocks)
         peer_store(peer_addr(&part[place][static_cast<int>(cluster_rank()) * warps + warp], lane),
-                   make_float4(x, y, z, 0.0f));
+                   make_float4(x[0], N > 1 ? x[N > 1 ? 1 : 0] : 0.0f, N > 2 ? x[N > 2 ? 2 : 0] : 0.0f, 0.0f));
+      __syncwarp();
       cluster_sync_writes();
-      x = y = z = 0.0f;
-      for (int w = lane; w < blocks * warps; w += 32) {
-        const float4 p = part[place][w];
-        x += p.x;
-        y += p.y;
-        z += p.z;
-      }
-      add_lanes();
-      place ^= 1;
+#pragma unroll
+      for (int n = 0; n < N; ++n) x[n] = 0.0f;
+      for (int w = lane; w < blocks * warps; w += 32) get(&part[place][w], x);
+      __syncwarp();
+      lanes(x, 32);
     }
-    return make_float3(x, y, z);
+    place ^= 1;
   }
 };
 
@@ -239,103 +288,85 @@ struct RowOwner {
   int at, lanes;        // this thread's place among the row's
   int64_t first, step;  // rows
   __device__ __forceinline__ RowOwner() {
-    if constexpr (SHARE == kWarp) {
-      at = threadIdx.x % 32;
-      lanes = 32;
-      first = static_cast<int64_t>(blockIdx.x) * 8 + threadIdx.x / 32;
-      step = static_cast<int64_t>(gridDim.x) * 8;
-    } else if constexpr (SHARE == kBlock) {
-      at = threadIdx.x;
-      lanes = blockDim.x;
-      first = blockIdx.x;
-      step = gridDim.x;
-    } else {
-      const int blocks = static_cast<int>(cluster_blocks());
-      at = static_cast<int>(cluster_rank() * blockDim.x + threadIdx.x);
-      lanes = blocks * blockDim.x;
-      first = blockIdx.x / blocks;
-      step = gridDim.x / blocks;
-    }
+    const int blocks = SHARE == kBlock ? 1 : static_cast<int>(cluster_blocks());
+    at = SHARE == kBlock ? threadIdx.x : cluster_rank() * blockDim.x + threadIdx.x;
+    lanes = blocks * blockDim.x;
+    first = blockIdx.x / blocks;
+    step = gridDim.x / blocks;
   }
 };
 
-// x to (x - mean) / root, mean 0 for RMS; columns past the end stay 0.
-template <int V, bool VEC, Share SHARE>
-__device__ __forceinline__ void standardize(const Columns<V, VEC>& at, float x[8 * V], bool layer, float eps,
-                                            float inv_width, RowSum<SHARE>& row_sum) {
-  if (layer) {
-    float m = 0.0f;
-#pragma unroll
-    for (int k = 0; k < 8 * V; ++k) m += x[k];
-    m = row_sum(m).x * inv_width;
-#pragma unroll
-    for (int k = 0; k < 8 * V; ++k) x[k] = at.in(k) ? x[k] - m : 0.0f;
+// Before the first sum: the parts past the block's warps, and with a cluster its blocks there.
+template <Share SHARE>
+__device__ __forceinline__ void begin_sums(float4 (*part)[RowSum<SHARE>::kParts]) {
+  if constexpr (SHARE == kBlock) {
+    if (threadIdx.x < 64) part[threadIdx.x / 32][threadIdx.x % 32] = make_float4(0, 0, 0, 0);
+    if (blockDim.x < 64 && threadIdx.x < 32) part[1][threadIdx.x] = make_float4(0, 0, 0, 0);
+    __syncthreads();
+  } else {
+    cluster_sync();
   }
-  float q = 0.0f;
-#pragma unroll
-  for (int k = 0; k < 8 * V; ++k) q = fmaf(x[k], x[k], q);
-  const float inverse = rsqrtf(fmaf(row_sum(q).x, inv_width, eps));
-#pragma unroll
-  for (int k = 0; k < 8 * V; ++k) x[k] *= inverse;
 }
 
-template <int V, bool VEC, Share SHARE, bool RING>
-__global__ void __launch_bounds__(SHARE == kWarp ? 256 : kMostThreads)
+// BIAS: there are biases.
+template <bool VEC, Share SHARE, bool BIAS>
+__global__ void __launch_bounds__(kMostThreads, 2)
     block_norm_forward_kernel(const __grid_constant__ NormArgs a) {
   __shared__ float4 part[2][RowSum<SHARE>::kParts];
   extern __shared__ uint8_t ring[];
   wait_for_predecessor();
   launch_dependents();
-  constexpr int N = 8 * V;
   const RowOwner<SHARE> own;
-  const Columns<V, VEC> at{own.at, own.lanes, static_cast<int>(a.width)};
+  const Columns<VEC> at(own.at, own.lanes, static_cast<int>(a.width));
+  Rows<VEC> rows{a, at, ring + threadIdx.x * 16, static_cast<int32_t>(blockDim.x * 16), own.first, own.step};
+  rows.begin();
+  const bool wvec = a.wvec != 0, has_h = a.in[kInH] != nullptr, matrix = a.in[kInGate] != nullptr;
+  const bool layer = a.kind == ZERO_NORM_LAYER, post_layer = a.post == ZERO_NORM_LAYER;
+  // s = r + (h standardized * scale1 + bias1) [* gate's row]
+  Eight scale1 = at.load_vector(a.gate, 1.0f, wvec) * a.alpha, bias1 = all_of(0.0f);
+  if constexpr (BIAS) bias1 = at.load_vector(a.b1, 0.0f, wvec) * scale1;
+  scale1 = scale1 * at.load_vector(a.w1, 1.0f, wvec);
+  const Eight w = at.load_vector(a.w, 1.0f, wvec), b = BIAS ? at.load_vector(a.b, 0.0f, wvec) : all_of(0.0f);
+  begin_sums<SHARE>(part);
   RowSum<SHARE> row_sum{part};
   const float inv_width = 1.0f / static_cast<float>(a.width);
-  const bool wvec = a.wvec != 0;
-  Rows<V, VEC, RING> rows{a, at, ring + threadIdx.x * 16, static_cast<int32_t>(blockDim.x), own.first, own.step};
-  rows.begin();
+  const auto center = [&](Eight& x) {
+    float m[1] = {sum8(x)};
+    row_sum(m);
+    x = x + all_of(-m[0] * inv_width);
+    at.clear(x);
+  };
+  const auto inverse_of = [&](const Eight& x) {
+    float q[1] = {dot8(x, x)};
+    row_sum(q);
+    return rsqrtf(fmaf(q[0], inv_width, a.eps));
+  };
   for (int64_t i = own.first; i < a.rows; i += own.step, rows.done()) {
-    float s[N], t[N];
     rows.arrive();
-    rows.read(kInR, i, s);
-    if (a.in[kInH] != nullptr) {
-      float p[N];
-      rows.read(kInH, i, p);
+    Eight s = rows.read(kInR, i);
+    if (has_h) {
+      Eight h = rows.read(kInH, i);
       if (a.post != ZERO_NORM_NONE) {
-        standardize(at, p, a.post == ZERO_NORM_LAYER, a.eps, inv_width, row_sum);
-        if (a.w1 != nullptr) {
-          at.load(a.w1, t, wvec);
-#pragma unroll
-          for (int k = 0; k < N; ++k) p[k] *= t[k];
-        }
-        if (a.b1 != nullptr) {
-          at.load(a.b1, t, wvec);
-#pragma unroll
-          for (int k = 0; k < N; ++k) p[k] += t[k];
-        }
+        if (post_layer) center(h);
+        h = h * inverse_of(h);
       }
-      const bool matrix = a.in[kInGate] != nullptr;
-      if (matrix || a.gate != nullptr) {
-        if (matrix) rows.read(kInGate, i, t);
-        else at.load(a.gate, t, wvec);
-#pragma unroll
-        for (int k = 0; k < N; ++k) p[k] *= t[k];
+      if (matrix) {
+        Eight p = h * scale1;
+        if constexpr (BIAS) p = p + bias1;
+        s = fma8(p, rows.read(kInGate, i), s);
+      } else {
+        if constexpr (BIAS) s = s + bias1;
+        s = fma8(h, scale1, s);
       }
-#pragma unroll
-      for (int k = 0; k < N; ++k) s[k] = fmaf(a.alpha, p[k], s[k]);
     }
     if (a.s_out != nullptr) at.store(a.s_out + i * a.lds, s);
-    standardize(at, s, a.kind == ZERO_NORM_LAYER, a.eps, inv_width, row_sum);
-    if (a.w != nullptr) {
-      at.load(a.w, t, wvec);
-#pragma unroll
-      for (int k = 0; k < N; ++k) s[k] *= t[k];
+    if (layer) {
+      at.clear(s);
+      center(s);
     }
-    if (a.b != nullptr) {
-      at.load(a.b, t, wvec);
-#pragma unroll
-      for (int k = 0; k < N; ++k) s[k] += t[k];
-    }
+    s = s * inverse_of(s);
+    if constexpr (BIAS) s = fma8(s, w, b);
+    else s = s * w;
     at.store(a.y + i * a.ldy, s);
   }
   if constexpr (SHARE == kCluster) cluster_sync();  // no block ends while others write to it
@@ -345,7 +376,8 @@ __global__ void __launch_bounds__(SHARE == kWarp ? 256 : kMostThreads)
 // columns of each, whose sums over the rows stay in their registers until the end.  With xh
 // the standardized row, u what reaches it and m its means,
 //   x's gradient = (u - m(u) [LAYER] - xh m(u xh)) / root.
-// FULL: there is a norm after the block, or a gate: h is read.  BIAS: sums of biases.
+// FULL: there is a norm after the block, or a gate: h is read.  BIAS: sums of biases, or
+// a bias under a gate.
 template <bool VEC, Share SHARE, bool FULL, bool BIAS>
 __global__ void __launch_bounds__(kMostThreads)
     block_norm_backward_kernel(const __grid_constant__ NormArgs a) {
@@ -353,131 +385,102 @@ __global__ void __launch_bounds__(kMostThreads)
   extern __shared__ uint8_t ring[];
   wait_for_predecessor();
   launch_dependents();
-  constexpr int N = 8, M = FULL ? N : 1;
   const RowOwner<SHARE> own;
-  const Columns<1, VEC> at{own.at, own.lanes, static_cast<int>(a.width)};
-  RowSum<SHARE> row_sum{part};
-  const float inv_width = 1.0f / static_cast<float>(a.width);
-  const bool wvec = a.wvec != 0;
+  const Columns<VEC> at(own.at, own.lanes, static_cast<int>(a.width));
+  Rows<VEC> rows{a, at, ring + threadIdx.x * 16, static_cast<int32_t>(blockDim.x * 16), own.first, own.step};
+  rows.begin();
+  const bool wvec = a.wvec != 0, matrix = a.in[kInGate] != nullptr, gated = matrix || a.gate != nullptr;
   const bool layer = a.kind == ZERO_NORM_LAYER, post_layer = a.post == ZERO_NORM_LAYER;
   const bool post = a.post != ZERO_NORM_NONE;
-  const Held<1> w(at, a.w, 1.0f, wvec);
-  float dw[N] = {}, db[BIAS ? N : 1] = {}, dg[M] = {}, dw1[M] = {}, db1[BIAS ? M : 1] = {};
-  Rows<1, VEC, VEC> rows{a, at, ring + threadIdx.x * 16, static_cast<int32_t>(blockDim.x), own.first, own.step};
-  rows.begin();
+  const Eight w = at.load_vector(a.w, 1.0f, wvec);
+  Eight w1, g, dg, dw1;
+  if constexpr (FULL) {
+    w1 = at.load_vector(a.w1, 1.0f, wvec);
+    g = at.load_vector(a.gate, 1.0f, wvec);
+    dg = dw1 = all_of(0.0f);
+  }
+  Eight dw = all_of(0.0f), db = dw, db1 = dw;
+  begin_sums<SHARE>(part);
+  RowSum<SHARE> row_sum{part};
+  const float inv_width = 1.0f / static_cast<float>(a.width);
   for (int64_t i = own.first; i < a.rows; i += own.step, rows.done()) {
-    float x[N], u[N], h[M];
     rows.arrive();
-    rows.read(kInR, i, x);
-    rows.read(kInDy, i, u);
-    if constexpr (FULL) rows.read(kInH, i, h);
+    Eight x = rows.read(kInR, i), u = rows.read(kInDy, i), h;
+    if constexpr (FULL) h = rows.read(kInH, i);
     if (layer || (FULL && post_layer)) {  // means, then what is left
-      float m = 0.0f, m1 = 0.0f;
-#pragma unroll
-      for (int k = 0; k < N; ++k) {
-        m += x[k];
-        if constexpr (FULL) m1 += h[k];
-      }
-      const float3 means = row_sum(m, m1);
+      float m[2] = {sum8(x), FULL ? sum8(h) : 0.0f};
+      row_sum(m);
       if (layer) {
-#pragma unroll
-        for (int k = 0; k < N; ++k) x[k] = at.in(k) ? x[k] - means.x * inv_width : 0.0f;
+        x = x + all_of(-m[0] * inv_width);
+        at.clear(x);
       }
       if constexpr (FULL)
         if (post_layer) {
-#pragma unroll
-          for (int k = 0; k < N; ++k) h[k] = at.in(k) ? h[k] - means.y * inv_width : 0.0f;
+          h = h + all_of(-m[1] * inv_width);
+          at.clear(h);
         }
     }
-    float xx = 0.0f, ux = 0.0f, hh = 0.0f, mean = 0.0f;
-#pragma unroll
-    for (int k = 0; k < N; ++k) {
-      xx = fmaf(x[k], x[k], xx);
-      ux = fmaf(u[k] * w[k], x[k], ux);
-      if constexpr (FULL) hh = fmaf(h[k], h[k], hh);
-    }
+    const Eight uw = u * w;
+    float q[3] = {dot8(x, x), dot8(uw, x), FULL ? dot8(h, h) : 0.0f};
+    float mean[1] = {0.0f};
     if (layer) {
-#pragma unroll
-      for (int k = 0; k < N; ++k) mean = fmaf(u[k], w[k], mean);
-      mean = row_sum(mean).x * inv_width;
+      mean[0] = sum8(uw);
+      row_sum(mean);
     }
-    const float3 q = row_sum(xx, ux, hh);
-    const float inverse = rsqrtf(fmaf(q.x, inv_width, a.eps));
-    const float along = q.y * inverse * inv_width;
-    const float inverse1 = FULL && post ? rsqrtf(fmaf(q.z, inv_width, a.eps)) : 1.0f;
-#pragma unroll
-    for (int k = 0; k < N; ++k) {
-      const float xh = x[k] * inverse;
-      dw[k] = fmaf(u[k], xh, dw[k]);
-      if constexpr (BIAS) db[k] += u[k];
-      x[k] = at.in(k) ? inverse * (u[k] * w[k] - mean - xh * along) : 0.0f;
-    }
-    if (a.in[kInDs] != nullptr) {
-      rows.read(kInDs, i, u);
-#pragma unroll
-      for (int k = 0; k < N; ++k) x[k] += u[k];
-    }
+    row_sum(q);
+    const float inverse = rsqrtf(fmaf(q[0], inv_width, a.eps));
+    const float along = q[1] * inverse * inv_width;
+    x = x * inverse;  // standardized
+    dw = fma8(u, x, dw);
+    if constexpr (BIAS) db = db + u;
+    x = fma8(x, all_of(-along), uw);
+    if (layer) x = x + all_of(-mean[0] * inv_width);
+    if (a.in[kInDs] != nullptr) x = fma8(x, all_of(inverse), rows.read(kInDs, i));
+    else x = x * inverse;
+    at.clear(x);
     if (a.dr != nullptr) at.store(a.dr + i * a.lddr, x);
-#pragma unroll
-    for (int k = 0; k < N; ++k) x[k] *= a.alpha;  // the gradient of gate P(h)
-    if constexpr (!FULL) {
-      if (a.dh != nullptr) at.store(a.dh + i * a.lddh, x);
-    } else {
-      float w1[N], g[N];
-      if (post) {
-#pragma unroll
-        for (int k = 0; k < N; ++k) h[k] *= inverse1;  // standardized
-      }
-      if (a.w1 != nullptr) {
-        at.load(a.w1, w1, wvec);
-      } else {
-#pragma unroll
-        for (int k = 0; k < N; ++k) w1[k] = 1.0f;
-      }
-      const bool matrix = a.in[kInGate] != nullptr;
-      if (matrix || a.gate != nullptr) {
-        if (a.b1 != nullptr) {
-          at.load(a.b1, u, wvec);
+    x = x * a.alpha;  // the gradient of gate P(h)
+    if constexpr (FULL) {
+      const float inverse1 = post ? rsqrtf(fmaf(q[2], inv_width, a.eps)) : 1.0f;
+      h = h * inverse1;
+      if (gated) {
+        Eight t = h * w1;
+        if constexpr (BIAS) t = t + at.load_vector(a.b1, 0.0f, wvec);
+        if (matrix) {
+          g = rows.read(kInGate, i);
+          if (a.dgate_rows != nullptr) at.store(a.dgate_rows + i * a.lddg, x * t);
         } else {
-#pragma unroll
-          for (int k = 0; k < N; ++k) u[k] = 0.0f;
+          dg = fma8(x, t, dg);
         }
-        if (matrix) rows.read(kInGate, i, g);
-        else at.load(a.gate, g, wvec);
-#pragma unroll
-        for (int k = 0; k < N; ++k) {
-          u[k] = x[k] * fmaf(h[k], w1[k], u[k]);
-          dg[k] += u[k];
-          x[k] *= g[k];
-        }
-        if (a.dgate_rows != nullptr) at.store(a.dgate_rows + i * a.lddg, u);
+        x = x * g;
       }
       if (post) {
-        float vh = 0.0f, v = 0.0f;
-#pragma unroll
-        for (int k = 0; k < N; ++k) {
-          dw1[k] = fmaf(x[k], h[k], dw1[k]);
-          if constexpr (BIAS) db1[k] += x[k];
-          x[k] *= w1[k];
-          vh = fmaf(x[k], h[k], vh);
-          v += x[k];
-        }
+        dw1 = fma8(x, h, dw1);
+        if constexpr (BIAS) db1 = db1 + x;
         if (a.dh != nullptr) {  // (alike for every thread)
-          const float3 m = row_sum(vh, v);
-          const float along1 = m.x * inv_width, mean1 = post_layer ? m.y * inv_width : 0.0f;
-#pragma unroll
-          for (int k = 0; k < N; ++k) x[k] = inverse1 * (x[k] - mean1 - h[k] * along1);
+          x = x * w1;
+          at.clear(x);
+          float m[2] = {dot8(x, h), 0.0f};
+          if (post_layer) m[1] = sum8(x);
+          row_sum(m);
+          x = fma8(h, all_of(-m[0] * inv_width), x);
+          if (post_layer) x = x + all_of(-m[1] * inv_width);
+          x = x * inverse1;
         }
       }
-      if (a.dh != nullptr) at.store(a.dh + i * a.lddh, x);
     }
+    if (a.dh != nullptr) at.store(a.dh + i * a.lddh, x);
   }
-  const auto put = [&](int q, const float* x) {
+  const auto put = [&](int q, const Eight& x) {
     if ((a.wanted >> q & 1) == 0) return;
     float* to = a.sums + (static_cast<int64_t>(q) * a.blocks + own.first) * a.width;
 #pragma unroll
-    for (int k = 0; k < N; ++k)
-      if (at.in(k)) to[at.of(k)] = x[k];
+    for (int k = 0; k < 4; ++k) {
+      float lo, hi;
+      split(x.p[k], lo, hi);
+      if (at.in(2 * k)) to[at.of(2 * k)] = lo;
+      if (at.in(2 * k + 1)) to[at.of(2 * k + 1)] = hi;
+    }
   };
   put(kDw, dw);
   if constexpr (BIAS) put(kDb, db);
@@ -540,11 +543,11 @@ RowShape row_shape(int64_t width) {
 static_assert(ZERO_MAX_NORM_WIDTH == 8 * kMostThreads * kMostCluster, "the widest row's cluster");
 
 // Blocks (clusters) of the backward pass: 4 rows each at least, and as many as are there at
-// one time (768 threads an SM).
+// one time (512 threads an SM).
 int64_t backward_blocks(int64_t rows, int64_t width) {
   const RowShape r = row_shape(width);
   const int64_t n = (rows + 3) / 4;
-  const int64_t most = kSms / r.cluster * (r.threads < 64 ? 12 : 768 / r.threads);
+  const int64_t most = kSms / r.cluster * (kMostThreads / r.threads);
   return n < most ? n : most;
 }
 
@@ -580,12 +583,10 @@ NormArgs args_of(const BlockNormLaunch& L) {
   return a;
 }
 
-// Bytes of the ring, for each thread 16 of each vector of each input.
+// Bytes of the ring, for each thread 16 of each input.
 constexpr int kMostRing = kStages * kInputs * kMostThreads * 16;
 static_assert(kMostRing + 8192 <= kSmem, "the ring and the parts of the sums");
-int ring_bytes(const NormArgs& a, int vectors, int threads) {
-  return kStages * a.inputs * vectors * threads * 16;
-}
+int ring_bytes(const NormArgs& a, int threads) { return kStages * a.inputs * threads * 16; }
 
 // Whether rows of every matrix lie on 16-byte boundaries; and the inputs' places.
 struct Rows16 {
@@ -621,35 +622,21 @@ cudaError_t launch_backward(const NormArgs& a, bool vec, Chain* chain) {
                                             : block_norm_backward_kernel<true, kCluster, FULL, BIAS>)
                           : (r.cluster == 1 ? block_norm_backward_kernel<false, kBlock, FULL, BIAS>
                                             : block_norm_backward_kernel<false, kCluster, FULL, BIAS>);
-  return launch_ring(kernel, a.blocks, r.threads, vec ? ring_bytes(a, 1, r.threads) : 0, r.cluster, a, chain);
+  return launch_ring(kernel, a.blocks, r.threads, vec ? ring_bytes(a, r.threads) : 0, r.cluster, a, chain);
 }
 
+template <bool BIAS>
 cudaError_t launch_forward(const NormArgs& a, bool vec, Chain* chain) {
-  const int64_t eights = (a.width + 7) / 8;
-  if (eights <= 128 && a.rows >= 8 * kSms) {  // (of fewer rows each is made by more threads)
-    const int v = static_cast<int>((eights + 31) / 32);
-    const int64_t blocks = (a.rows + 7) / 8;
-    const int smem = ring_bytes(a, v, 256);
-    if (vec && v <= 2)
-      return launch_ring(v == 1 ? block_norm_forward_kernel<1, true, kWarp, true>
-                                : block_norm_forward_kernel<2, true, kWarp, true>,
-                         blocks < 4 * kSms ? blocks : 4 * kSms, 256, smem, 1, a, chain);
-    const auto kernel = vec ? (v == 3 ? block_norm_forward_kernel<3, true, kWarp, false>
-                                      : block_norm_forward_kernel<4, true, kWarp, false>)
-                            : (v <= 2 ? block_norm_forward_kernel<2, false, kWarp, false>
-                                      : block_norm_forward_kernel<4, false, kWarp, false>);
-    return launch_ring(kernel, blocks < 65536 ? blocks : 65536, 256, 0, 1, a, chain);
-  }
   const RowShape r = row_shape(a.width);
-  const int smem = vec ? ring_bytes(a, 1, r.threads) : 0;
-  int64_t each = 2048 / r.threads;  // blocks an SM
-  if (each > 16) each = 16;
-  if (each > kSmem / (smem + 1536)) each = kSmem / (smem + 1536);
+  const int smem = vec ? ring_bytes(a, r.threads) : 0;
+  int64_t each = 1024 / r.threads;  // blocks an SM
+  if (each > 24) each = 24;
+  if (each > kSmem / (smem + 2560)) each = kSmem / (smem + 2560);
   const int64_t most = each * kSms / r.cluster;
-  const auto kernel = vec ? (r.cluster == 1 ? block_norm_forward_kernel<1, true, kBlock, true>
-                                            : block_norm_forward_kernel<1, true, kCluster, true>)
-                          : (r.cluster == 1 ? block_norm_forward_kernel<1, false, kBlock, false>
-                                            : block_norm_forward_kernel<1, false, kCluster, false>);
+  const auto kernel = vec ? (r.cluster == 1 ? block_norm_forward_kernel<true, kBlock, BIAS>
+                                            : block_norm_forward_kernel<true, kCluster, BIAS>)
+                          : (r.cluster == 1 ? block_norm_forward_kernel<false, kBlock, BIAS>
+                                            : block_norm_forward_kernel<false, kCluster, BIAS>);
   return launch_ring(kernel, a.rows < most ? a.rows : most, r.threads, smem, r.cluster, a, chain);
 }
 
@@ -668,7 +655,8 @@ cudaError_t launch_block_norm_forward(const BlockNormLaunch& L) {
   vec(a.s_out, a.lds);
   vec(a.y, a.ldy);
   Chain chain{L.stream};
-  return launch_forward(a, vec.all, &chain);
+  return a.b1 != nullptr || a.b != nullptr ? launch_forward<true>(a, vec.all, &chain)
+                                           : launch_forward<false>(a, vec.all, &chain);
 }
 
 cudaError_t launch_block_norm_backward(const BlockNormLaunch& L) {
@@ -700,7 +688,7 @@ cudaError_t launch_block_norm_backward(const BlockNormLaunch& L) {
     vec(a.dgate_rows, a.lddg);
     a.sums = static_cast<float*>(L.workspace);
     a.blocks = static_cast<int32_t>(backward_blocks(a.rows, a.width));
-    const bool bias = L.dbias != nullptr || L.dpost_bias != nullptr;
+    const bool bias = L.dbias != nullptr || L.dpost_bias != nullptr || a.b1 != nullptr;
     e = full ? (bias ? launch_backward<true, true>(a, vec.all, &chain)
                      : launch_backward<true, false>(a, vec.all, &chain))
              : (bias ? launch_backward<false, true>(a, vec.all, &chain)

@@ -14,6 +14,18 @@ __device__ __forceinline__ int64_t id_at(const void* ids, int32_t i32, int64_t i
              : __ldg(static_cast<const long long*>(ids) + i);
 }
 
+// 16 bytes, or zeros: a predicate and no branch, so that several are under way together
+// (loads behind branches came one after the other: 4 us for 8 of them instead of 1).
+__device__ __forceinline__ uint4 load16_if(bool p, const void* from) {
+  uint4 v;
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %5, 0;\n mov.b32 %0, 0;\n mov.b32 %1, 0;\n mov.b32 %2, 0;\n"
+      " mov.b32 %3, 0;\n @p ld.global.nc.v4.b32 {%0, %1, %2, %3}, [%4];\n}\n"
+      : "=&r"(v.x), "=&r"(v.y), "=&r"(v.z), "=&r"(v.w)
+      : "l"(from), "r"(static_cast<int>(p)));
+  return v;
+}
+
 // ------------------------------------------------------------------------ forward
 
 struct LookupArgs {
@@ -49,8 +61,7 @@ __global__ void __launch_bounds__(256) embedding_lookup_kernel(const __grid_cons
 #pragma unroll
       for (int k = 0; k < kVectors; ++k) {
         const int64_t j = j0 + 256 * k + 8 * lane;
-        v[k] = known && j + 8 <= a.width ? __ldg(reinterpret_cast<const uint4*>(from + j))
-                                         : make_uint4(0, 0, 0, 0);
+        v[k] = load16_if(known && j + 8 <= a.width, from + j);
       }
 #pragma unroll
       for (int k = 0; k < kVectors; ++k) {
@@ -82,16 +93,26 @@ __global__ void __launch_bounds__(256) embedding_lookup_kernel(const __grid_cons
 // lie together in most vocabularies, fall to different ones; and the columns to slices of
 // 256.  A block takes one class and one slice, and needs nothing of any other: it finds
 // its class's rows among the ids (which all blocks read, from L2), sorts them by token,
-// keeping the rows' order, sums each token's rows in registers, and writes every row of
-// its class, zeros where no token was.  Neither sums nor places go through atomics on
-// floats or other blocks, so the result follows from the ids alone.
+// keeping the rows' order, sums each token's rows in registers, and writes them; the rows
+// of the table of no token are zeros, which a warp of its own gives to the TMA engine
+// meanwhile.  Neither sums nor places go through atomics on floats or other blocks, so the
+// result follows from the ids alone.
+// Bound by the writes: 206 MB of zeros and sums at 8192 x 2048 of 50257.  (Clusters whose
+// blocks look through a share of the ids each found their rows in half the time, but took
+// 15 us longer from one call to the next.)
 
 constexpr int kSumThreads = 256, kSumWarps = kSumThreads / 32;
+constexpr int kScatterThreads = kSumThreads + 32;  // and the warp of the zeros
 constexpr int kSlice = 256;      // columns: 8 a lane
 constexpr int kWindow = 4096;    // tokens of a class that are sorted at one time
 constexpr int kMostRows = 6144;  // rows that are sorted at one time
-constexpr int kEachRows = kMostRows / kSumWarps;
+constexpr int kEachRows = kMostRows / kSumWarps;  // of them, those that one warp finds
 constexpr int kOneWarp = 48;     // rows of a token that one warp sums by itself
+
+// The summing warps.
+__device__ __forceinline__ void sum_sync() {
+  asm volatile("barrier.sync.aligned 1, %0;" ::"n"(kSumThreads) : "memory");
+}
 
 struct ScatterArgs {
   const uint16_t* dy;
@@ -99,20 +120,29 @@ struct ScatterArgs {
   void* dtable;
   int64_t rows, width, vocab, ldy, ldt, padding;
   int32_t ids_i32, grad_f32, accumulate;
-  int32_t classes;
+  int32_t classes, slices;
+  uint64_t inverse;   // 2^64 / classes, rounded up: its high product with an id is the quotient
+  int32_t bulk;       // a row of dtable is whole 16-byte vectors: zeros go by the TMA engine
   float scale;
 };
 
+constexpr int kZeros = 4096;  // bytes of zeros
+
 struct ScatterShared {
+  alignas(128) uint8_t zeros[kZeros];
   int32_t offset[kWindow + 1];  // counts; then where a token's rows begin; then where they end
   int32_t row[kMostRows];       // the class's rows in their order, kEachRows for each warp
   uint16_t token[kMostRows];    // and their tokens, within the window
+  int32_t next;                 // share of the sums that is taken next
+  int32_t full;                 // a warp has found more rows than there is room for
   int32_t sorted[kMostRows];    // rows by token
-  uint16_t some[kWindow];       // tokens that have rows
+  uint16_t sorted_token[kMostRows];
   float part[kSumWarps][kSlice];
-  int32_t found[kSumWarps];     // rows of each warp
-  int32_t scan[2][kSumWarps];
-  int32_t next_sum, next_zero;  // items taken
+  int32_t found[kSumWarps];     // rows that each warp has found
+  int32_t scan[kSumWarps];
+  uint16_t common[kMostRows / kOneWarp];  // tokens of more than kOneWarp rows
+  int32_t commons;
+  uint32_t empty[kWindow / 32]; // tokens of no row, a bit each
 };
 
 // The sum of a run of rows: 8 columns a lane, in the order of the rows, eight rows' loads
@@ -123,51 +153,61 @@ struct SliceSum {
   float run[8] = {}, sum[8] = {};
   int chain = 0;
 
+  // Rows rows[0], ..., rows[U - 1], those whose bit of `here` is set; after(u) follows the u-th.
+  template <int U, typename After>
+  __device__ __forceinline__ void walk(const ScatterArgs& a, const int32_t* rows, uint32_t here, int64_t col,
+                                       int lane, After after) {
+    if constexpr (VEC) {
+      uint4 v[U];
+      const bool in = col + 8 * lane + 8 <= a.width, some = col + 8 * lane < a.width;
+      const uint16_t* from = a.dy + col + 8 * lane;
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const bool take = here >> u & 1;
+        v[u] = load16_if(take && in, from + (take ? rows[u] : 0) * a.ldy);
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        if ((here >> u & 1) == 0) continue;
+        float x[8];
+        bf16x8(v[u], x);
+        if (!in && some) {
+#pragma unroll
+          for (int c = 0; c < 8; ++c)
+            if (col + 8 * lane + c < a.width) x[c] = bf16_at(from + rows[u] * a.ldy + c);
+        }
+#pragma unroll
+        for (int c = 0; c < 8; ++c) run[c] += x[c];
+        after(u);
+      }
+    } else {
+#pragma unroll
+      for (int h = 0; h < U; h += 2) {
+        float x[2][8];
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+          for (int c = 0; c < 8; ++c) {
+            const int64_t j = col + lane + 32 * c;
+            x[u][c] = (here >> (h + u) & 1) && j < a.width ? bf16_at(a.dy + rows[h + u] * a.ldy + j) : 0.0f;
+          }
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          if ((here >> (h + u) & 1) == 0) continue;
+#pragma unroll
+          for (int c = 0; c < 8; ++c) run[c] += x[u][c];
+          after(h + u);
+        }
+      }
+    }
+  }
   __device__ __forceinline__ void add(const ScatterArgs& a, const int32_t* rows, int n, int64_t col,
                                       int lane) {
     constexpr int U = 8;
 #pragma unroll 1
     for (int k = 0; k < n; k += U) {
-      if constexpr (VEC) {
-        uint4 v[U];
-        const bool in = col + 8 * lane + 8 <= a.width;
-        const uint16_t* from = a.dy + col + 8 * lane;
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-          v[u] = make_uint4(0, 0, 0, 0);
-          if (k + u < n && in) v[u] = __ldg(reinterpret_cast<const uint4*>(from + rows[k + u] * a.ldy));
-        }
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-          float x[8];
-          bf16x8(v[u], x);
-#pragma unroll
-          for (int c = 0; c < 8; ++c) run[c] += x[c];
-        }
-        if (!in && col + 8 * lane < a.width) {
-#pragma unroll 1
-          for (int u = 0; u < U && k + u < n; ++u)
-#pragma unroll
-            for (int c = 0; c < 8; ++c)
-              if (col + 8 * lane + c < a.width) run[c] += bf16_at(from + rows[k + u] * a.ldy + c);
-        }
-      } else {
-#pragma unroll
-        for (int h = 0; h < U; h += 2) {
-          float x[2][8];
-#pragma unroll
-          for (int u = 0; u < 2; ++u)
-#pragma unroll
-            for (int c = 0; c < 8; ++c) {
-              const int64_t j = col + lane + 32 * c;
-              x[u][c] = k + h + u < n && j < a.width ? bf16_at(a.dy + rows[k + h + u] * a.ldy + j) : 0.0f;
-            }
-#pragma unroll
-          for (int u = 0; u < 2; ++u)
-#pragma unroll
-            for (int c = 0; c < 8; ++c) run[c] += x[u][c];
-        }
-      }
+      const uint32_t here = n - k >= U ? (1u << U) - 1u : (1u << (n - k)) - 1u;
+      walk<U>(a, rows + k, here, col, lane, [](int) {});
       if ((chain += U) >= 64) join();
     }
   }
@@ -181,6 +221,12 @@ struct SliceSum {
   }
 };
 
+__device__ __forceinline__ void add_vector(float* to, const float* x) {
+  asm volatile("red.global.add.v4.f32 [%0], {%1, %2, %3, %4};" ::"l"(to), "f"(x[0]), "f"(x[1]), "f"(x[2]),
+               "f"(x[3])
+               : "memory");
+}
+
 // A lane's 8 columns of one row of the table's gradient.
 template <bool VEC>
 __device__ __forceinline__ void put_slice(const ScatterArgs& a, int64_t v, int64_t col, const float x[8],
@@ -188,14 +234,16 @@ __device__ __forceinline__ void put_slice(const ScatterArgs& a, int64_t v, int64
   const int64_t at = v * a.ldt + col;
   if (VEC && col + 8 * lane + 8 <= a.width) {
     if (a.grad_f32) {
-      float4* o = reinterpret_cast<float4*>(static_cast<float*>(a.dtable) + at + 8 * lane);
-      float4 p = make_float4(0, 0, 0, 0), q = p;
+      float* o = static_cast<float*>(a.dtable) + at + 8 * lane;
       if (a.accumulate) {
-        p = o[0];
-        q = o[1];
+        // One addition an element and call, in L2: nothing waits for what was there, and
+        // there is no order to depend on.  (What comes to below 2^-126 is 0 there.)
+        add_vector(o, x);
+        add_vector(o + 4, x + 4);
+      } else {
+        reinterpret_cast<float4*>(o)[0] = make_float4(x[0], x[1], x[2], x[3]);
+        reinterpret_cast<float4*>(o)[1] = make_float4(x[4], x[5], x[6], x[7]);
       }
-      o[0] = make_float4(p.x + x[0], p.y + x[1], p.z + x[2], p.w + x[3]);
-      o[1] = make_float4(q.x + x[4], q.y + x[5], q.z + x[6], q.w + x[7]);
     } else {
       uint4* o = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.dtable) + at + 8 * lane);
       float y[8] = {};
@@ -225,10 +273,11 @@ struct ScatterPlace {
   int64_t col, w0;
   uint32_t mine, classes;
   int window;
-  // row i's token within the window, or -1
-  __device__ __forceinline__ int token_of(const ScatterArgs& a, int64_t i) const {
-    const int64_t id = id_at(a.ids, a.ids_i32, i);
-    const uint32_t k = static_cast<uint32_t>(id) / classes;
+  // an id's token within the window, or -1
+  __device__ __forceinline__ int token_of(const ScatterArgs& a, int64_t id) const {
+    const uint32_t k =
+        classes == 1 ? static_cast<uint32_t>(id)
+                     : static_cast<uint32_t>(__umul64hi(static_cast<uint32_t>(id), a.inverse));
     const int64_t t = static_cast<int64_t>(k) - w0;
     const bool good = id >= 0 && id < a.vocab && id != a.padding &&
                       static_cast<uint32_t>(id) - k * classes == mine && t >= 0 && t < window;
@@ -254,14 +303,14 @@ __device__ __forceinline__ void finish_token_together(const ScatterArgs& a, cons
   s.join();
 #pragma unroll
   for (int c = 0; c < 8; ++c) sh.part[warp][32 * c + lane] = s.sum[c];
-  __syncthreads();
+  sum_sync();
   if (warp == 0) {
     for (int k = 1; k < kSumWarps; ++k)
 #pragma unroll
       for (int c = 0; c < 8; ++c) s.sum[c] += sh.part[k][32 * c + lane];
     finish_token(a, p, s, t, lane);
   }
-  __syncthreads();
+  sum_sync();
 }
 template <bool VEC>
 __device__ __forceinline__ void add_share(const ScatterArgs& a, const ScatterPlace& p, SliceSum<VEC>& s,
@@ -272,35 +321,44 @@ __device__ __forceinline__ void add_share(const ScatterArgs& a, const ScatterPla
 }
 
 // Rows [i0, i1) of tokens [t0, t1) in their order, each warp's own run of rows in its own
-// part of the list; whether all have room.  (All threads; found[] can be read after it.)
-__device__ __forceinline__ bool list_rows(const ScatterArgs& a, const ScatterPlace& p, ScatterShared& sh,
-                                          int64_t i0, int64_t i1, int t0, int t1, bool count) {
+// part of the list (the first kEachRows of them); count: adds up offset[] too.  The list, found[]
+// and full can be read after it.
+__device__ __forceinline__ void list_rows(const ScatterArgs& a, const ScatterPlace& p, ScatterShared& sh, int64_t i0,
+                                          int64_t i1, int t0, int t1, bool count) {
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int64_t each = (i1 - i0 + kSumThreads - 1) / kSumThreads * 32;
   const int64_t from = i0 + warp * each, to = from + each < i1 ? from + each : i1;
   int n = 0;
-  constexpr int U = 8;
+  constexpr int U = 8;  // loads under way: what bounds this is their latency
   for (int64_t i = from; i < to; i += 32 * U) {
-    int t[U];
-#pragma unroll
-    for (int u = 0; u < U; ++u) t[u] = i + 32 * u + lane < to ? p.token_of(a, i + 32 * u + lane) : -1;
+    int64_t id[U];  // (past the end: the last one, which does not count)
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const bool has = t[u] >= t0 && t[u] < t1;
+      const int64_t k = i + 32 * u + lane;
+      id[u] = id_at(a.ids, a.ids_i32, k < to ? k : to - 1);
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int64_t k = i + 32 * u + lane;
+      const int t = p.token_of(a, id[u]);
+      const bool has = k < to && t >= t0 && t < t1;
       const uint32_t all = __ballot_sync(0xffffffffu, has);
       if (has) {
         const int at = n + __popc(all & ((1u << lane) - 1u));
         if (at < kEachRows) {
-          sh.row[warp * kEachRows + at] = static_cast<int32_t>(i + 32 * u + lane);
-          sh.token[warp * kEachRows + at] = static_cast<uint16_t>(t[u]);
+          sh.row[warp * kEachRows + at] = static_cast<int32_t>(k);
+          sh.token[warp * kEachRows + at] = static_cast<uint16_t>(t);
         }
-        if (count) atomicAdd(&sh.offset[t[u]], 1);
+        if (count) atomicAdd(&sh.offset[t], 1);
       }
       n += __popc(all);
     }
   }
-  if (lane == 0) sh.found[warp] = n;
-  return __syncthreads_and(n <= kEachRows) != 0;
+  if (lane == 0) {
+    sh.found[warp] = n;
+    if (n > kEachRows) sh.full = 1;
+  }
+  sum_sync();
 }
 
 // The listed rows by token, each token's in the order of the list: a warp takes every 8th
@@ -309,212 +367,230 @@ __device__ __forceinline__ void sort_rows(ScatterShared& sh, int start) {
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   for (int w = 0; w < kSumWarps; ++w) {
     const int n = sh.found[w];
-    for (int k = 0; k < n; k += 32) {
-      const int t = k + lane < n ? sh.token[w * kEachRows + k + lane] : -1;
+    for (int k = w * kEachRows; k < w * kEachRows + n; k += 32) {
+      const int t = k + lane < w * kEachRows + n ? sh.token[k + lane] : -1;
       const bool take = t >= 0 && t % kSumWarps == warp;
       const uint32_t takers = __ballot_sync(0xffffffffu, take);
       if (take) {
         const uint32_t same = __match_any_sync(takers, t);
         const int before = __popc(same & ((1u << lane) - 1u));
         const int at = sh.offset[t];
-        sh.sorted[at - start + before] = sh.row[w * kEachRows + k + lane];
+        sh.sorted[at - start + before] = sh.row[k + lane];
+        sh.sorted_token[at - start + before] = static_cast<uint16_t>(t);
         __syncwarp(takers);
         if (before == 0) sh.offset[t] = at + __popc(same);
       }
       __syncwarp();
     }
   }
-  __syncthreads();
+  sum_sync();
 }
 
-// The next item of a kind, for a warp.
-__device__ __forceinline__ int take_item(int32_t* next, int lane) {
-  int k = 0;
-  if (lane == 0) k = atomicAdd(next, 1);
-  return __shfl_sync(0xffffffffu, k, 0);
+// The tokens of the n sorted rows, one after the other: a warp takes the next 16 rows that no
+// other has taken, of them the tokens whose first row is there, and has eight rows' loads
+// under way at a time whatever tokens they are of.  Tokens of more than kOneWarp rows are
+// left out.  (Which warp sums a token does not change its sum.)
+template <bool VEC>
+__device__ __forceinline__ void sum_tokens(const ScatterArgs& a, const ScatterPlace& p, ScatterShared& sh, int start,
+                                           int n, int t_first, int lane) {
+  constexpr int U = 8, kTaken = 16;
+  const auto begin_of = [&](int t) { return (t == t_first ? start : sh.offset[t - 1]) - start; };
+  const auto end_of = [&](int t) { return sh.offset[t] - start; };
+  const auto next_first = [&](int k) {  // the first row at or after k that is a token's first
+    if (k >= n) return n;
+    const int t = sh.sorted_token[k];
+    return begin_of(t) == k ? k : end_of(t);
+  };
+  for (;;) {
+    int share = 0;
+    if (lane == 0) share = atomicAdd(&sh.next, 1);
+    share = __shfl_sync(0xffffffffu, share, 0) * kTaken;
+    if (share >= n) return;
+    const int end = next_first(share + kTaken);
+    SliceSum<VEC> s;
+    for (int k = next_first(share); k < end;) {
+      const int t = sh.sorted_token[k];
+      if (end_of(t) - begin_of(t) > kOneWarp) {
+        k = end_of(t);
+        continue;
+      }
+      const int m = end - k < U ? end - k : U;
+      int token = -1, after = -2;
+      if (lane < m) {
+        token = sh.sorted_token[k + lane];
+        after = k + lane + 1 < n ? sh.sorted_token[k + lane + 1] : -2;
+      }
+      // rows that count, and those that end a token
+      const bool counts = lane < m && end_of(token) - begin_of(token) <= kOneWarp;
+      const uint32_t here = __ballot_sync(0xffffffffu, counts);
+      const uint32_t last = __ballot_sync(0xffffffffu, counts && token != after);
+      s.template walk<U>(a, sh.sorted + k, here, p.col, lane, [&](int u) {
+        if ((last >> u & 1) == 0) return;
+        finish_token(a, p, s, sh.sorted_token[k + u], lane);
+        s = SliceSum<VEC>();
+      });
+      k += m;
+    }
+  }
+}
+
+// Rows of the table of no token: zeros, a token a lane (a warp's work).  A class's blocks share
+// them out by rows, whole ones.
+__device__ __forceinline__ void write_zeros(const ScatterArgs& a, const ScatterPlace& p, const ScatterShared& sh,
+                                            int slice, int slices, int lane) {
+  const int size = a.grad_f32 ? 4 : 2;
+  const int64_t bytes = a.width * size;
+  for (int t0 = slice; t0 < p.window; t0 += 32 * slices) {
+    const int t = t0 + slices * lane;
+    const bool none = t < p.window && (sh.empty[t / 32] >> (t % 32) & 1) != 0;
+    char* row = static_cast<char*>(a.dtable) + ((p.w0 + t) * p.classes + p.mine) * a.ldt * size;
+    if (a.bulk) {
+      if (none) {
+        for (int64_t b = 0; b < bytes; b += kZeros)
+          bulk_store(row + b, sh.zeros, static_cast<uint32_t>(bytes - b < kZeros ? bytes - b : kZeros));
+      }
+      bulk_commit();
+    } else {
+      uint32_t left = __ballot_sync(0xffffffffu, none);
+      while (left != 0) {
+        const int u = __ffs(left) - 1;
+        left &= left - 1;
+        uint16_t* o = reinterpret_cast<uint16_t*>(__shfl_sync(0xffffffffu, reinterpret_cast<uintptr_t>(row), u));
+        for (int64_t j = lane; j < bytes / 2; j += 32) o[j] = 0;
+      }
+    }
+  }
 }
 
 template <bool VEC>
-__global__ void __launch_bounds__(kSumThreads, 2)
+__global__ void __launch_bounds__(kScatterThreads, 2)
     embedding_scatter_kernel(const __grid_constant__ ScatterArgs a) {
   extern __shared__ uint8_t raw[];
-  ScatterShared& sh = *reinterpret_cast<ScatterShared*>(raw);
+  ScatterShared& sh = *reinterpret_cast<ScatterShared*>(raw + ((128u - (smem_addr(raw) & 127u)) & 127u));
+  if (a.bulk && threadIdx.x < kZeros / 16) {
+    *reinterpret_cast<uint4*>(sh.zeros + 16 * threadIdx.x) = make_uint4(0, 0, 0, 0);
+    fence_async_shared();
+  }
   wait_for_predecessor();
   launch_dependents();
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int slices = a.slices, slice = static_cast<int>(blockIdx.x / static_cast<uint32_t>(a.classes));
   ScatterPlace p;
-  p.col = static_cast<int64_t>(blockIdx.y) * kSlice;
-  p.mine = blockIdx.x;
+  p.col = static_cast<int64_t>(slice) * kSlice;
+  p.mine = blockIdx.x % static_cast<uint32_t>(a.classes);
   p.classes = a.classes;
   const int64_t tokens = (a.vocab - p.mine + p.classes - 1) / p.classes;  // of this class
 
   for (p.w0 = 0; p.w0 < tokens; p.w0 += kWindow) {
     const int window = tokens - p.w0 < kWindow ? static_cast<int>(tokens - p.w0) : kWindow;
     p.window = window;
-    for (int t = threadIdx.x; t <= window; t += kSumThreads) sh.offset[t] = 0;
-    if (threadIdx.x == 0) sh.next_sum = sh.next_zero = 0;
+    for (int t = threadIdx.x; t <= window; t += kScatterThreads) sh.offset[t] = 0;
+    if (threadIdx.x < kWindow / 32) sh.empty[threadIdx.x] = 0;
+    if (threadIdx.x == 0) sh.full = 0;
     __syncthreads();
-    const bool room = list_rows(a, p, sh, 0, a.rows, 0, window, true);
-    // counts to offsets, and the tokens that have rows: a thread takes a run of tokens
-    int some = 0;
+    if (warp == kSumWarps) {
+      __syncthreads();  // the tokens of no row are known
+      if (!a.accumulate) write_zeros(a, p, sh, slice, slices, lane);
+      __syncthreads();  // the window is done
+      continue;
+    }
+    list_rows(a, p, sh, 0, a.rows, 0, window, true);
+    const bool room = sh.full == 0;
+    // counts to offsets: a thread takes a run of tokens
     {
       const int per = (window + kSumThreads - 1) / kSumThreads;
       const int t0 = threadIdx.x * per < window ? threadIdx.x * per : window;
       const int t1 = t0 + per < window ? t0 + per : window;
       int rows = 0;
       for (int t = t0; t < t1; ++t) {
-        rows += sh.offset[t];
-        some += sh.offset[t] > 0;
+        const int n = sh.offset[t];
+        rows += n;
+        if (n == 0) atomicOr(&sh.empty[t / 32], 1u << (t % 32));
       }
-      int x = rows, y = some;
+      int x = rows;
 #pragma unroll
       for (int k = 1; k < 32; k *= 2) {
-        const int u = __shfl_up_sync(0xffffffffu, x, k), v = __shfl_up_sync(0xffffffffu, y, k);
-        if (lane >= k) {
-          x += u;
-          y += v;
-        }
+        const int u = __shfl_up_sync(0xffffffffu, x, k);
+        if (lane >= k) x += u;
       }
-      if (lane == 31) {
-        sh.scan[0][warp] = x;
-        sh.scan[1][warp] = y;
-      }
-      __syncthreads();
-      int before = x - rows, at = y - some, all = 0;
-      some = 0;
+      if (lane == 31) sh.scan[warp] = x;
+      __syncthreads();  // (the zeros may begin)
+      int before = x - rows;
 #pragma unroll
-      for (int w = 0; w < kSumWarps; ++w) {
-        if (w < warp) {
-          before += sh.scan[0][w];
-          at += sh.scan[1][w];
-        }
-        all += sh.scan[0][w];
-        some += sh.scan[1][w];
-      }
+      for (int w = 0; w < kSumWarps; ++w)
+        if (w < warp) before += sh.scan[w];
       for (int t = t0; t < t1; ++t) {
         const int n = sh.offset[t];
         sh.offset[t] = before;
         before += n;
-        if (n > 0) sh.some[at++] = static_cast<uint16_t>(t);
       }
-      if (threadIdx.x == 0) sh.offset[window] = all;
-      __syncthreads();
+      if (threadIdx.x == kSumThreads - 1) sh.offset[window] = before;
+      sum_sync();
     }
-    // tokens of no row: zeros
-    const int zeros = a.accumulate ? 0 : (window + 31) / 32;
-    const auto zero_item = [&](int k, bool sorted) {
-      const int t = 32 * k + lane;
-      bool none = false;
-      if (t < window)
-        none = sorted ? (t == 0 ? 0 : sh.offset[t - 1]) == sh.offset[t] : sh.offset[t] == sh.offset[t + 1];
-      uint32_t left = __ballot_sync(0xffffffffu, none);
-      const float zero[8] = {};
-      while (left != 0) {
-        const int u = __ffs(left) - 1;
-        left &= left - 1;
-        put_slice<VEC>(a, (p.w0 + 32 * k + u) * p.classes + p.mine, p.col, zero, lane);
-      }
-    };
-    if (room) {
-      sort_rows(sh, 0);
-      const auto begin_of = [&](int t) { return t == 0 ? 0 : sh.offset[t - 1]; };
-      // Half of the warps begin with the zeros, which fill the way to memory, half with
-      // the sums, which wait for it.
-      const auto sums = [&] {
-        for (int k; (k = take_item(&sh.next_sum, lane)) < some;) {
-          const int t = sh.some[k], first = begin_of(t), n = sh.offset[t] - first;
-          if (n > kOneWarp) continue;
-          SliceSum<VEC> s;
-          s.add(a, sh.sorted + first, n, p.col, lane);
-          finish_token(a, p, s, t, lane);
-        }
-      };
-      if (warp % 2 == 0) sums();
-      for (int k; (k = take_item(&sh.next_zero, lane)) < zeros;) zero_item(k, true);
-      if (warp % 2 != 0) sums();
-      for (int k0 = 0; k0 < some; k0 += 32) {
-        const int k = k0 + lane, mine = k < some ? sh.some[k] : 0;
-        uint32_t left = __ballot_sync(0xffffffffu, k < some && sh.offset[mine] - begin_of(mine) > kOneWarp);
-        while (left != 0) {  // alike in every warp
-          const int t = __shfl_sync(0xffffffffu, mine, __ffs(left) - 1);
-          left &= left - 1;
-          const int first = begin_of(t);
-          SliceSum<VEC> s;
-          add_share(a, p, s, sh.sorted + first, sh.offset[t] - first);
-          finish_token_together(a, p, sh, s, t);
-        }
-      }
-      __syncthreads();
-      continue;
-    }
-    // More rows than there is room for: tokens from t0 up to t1, as many as fit however
-    // they lie; a token of more rows than that goes alone, its rows in runs.  The ids are
-    // read once more for each.
-    for (int k = warp; k < zeros; k += kSumWarps) zero_item(k, false);
-    __syncthreads();
+    // Tokens from t0 up to t1: all, if their rows have room; else as many as fit however
+    // they lie, and a token of more rows than that alone, its rows in runs.  The ids are read
+    // once more for each.
     for (int t0 = 0; t0 < window;) {
       const int start = sh.offset[t0];
-      int lo = t0 + 1, hi = window;  // the last t1 whose rows have room, or t0 + 1
-      while (lo < hi) {
-        const int mid = (lo + hi + 1) / 2;
-        if (sh.offset[mid] - start <= kEachRows) lo = mid;
-        else hi = mid - 1;
+      int t1 = window;
+      if (!room) {
+        int lo = t0 + 1, hi = window;  // the last t1 whose rows have room, or t0 + 1
+        while (lo < hi) {
+          const int mid = (lo + hi + 1) / 2;
+          if (sh.offset[mid] - start <= kEachRows) lo = mid;
+          else hi = mid - 1;
+        }
+        t1 = lo;
       }
-      const int t1 = lo, count = sh.offset[t1] - start;
-      __syncthreads();
-      if (count > kEachRows) {
+      const int count = sh.offset[t1] - start;
+      sum_sync();  // (all have read what is set anew here)
+      if (threadIdx.x == 0) sh.commons = sh.next = 0;
+      sum_sync();
+      if (!room && count > kEachRows) {
         SliceSum<VEC> s;
-        for (int64_t i0 = 0; i0 < a.rows; i0 += kMostRows) {
-          const int64_t i1 = i0 + kMostRows < a.rows ? i0 + kMostRows : a.rows;
-          list_rows(a, p, sh, i0, i1, t0, t1, false);  // (a warp looks at kEachRows rows)
+        for (int64_t i = 0; i < a.rows; i += kMostRows) {
+          const int64_t end = i + kMostRows < a.rows ? i + kMostRows : a.rows;
+          list_rows(a, p, sh, i, end, t0, t1, false);  // (a warp looks at kEachRows rows)
           s.add(a, sh.row + warp * kEachRows, sh.found[warp], p.col, lane);
-          __syncthreads();
+          sum_sync();
         }
         finish_token_together(a, p, sh, s, t0);
       } else if (count > 0) {
-        list_rows(a, p, sh, 0, a.rows, t0, t1, false);
+        if (!room) list_rows(a, p, sh, 0, a.rows, t0, t1, false);
         sort_rows(sh, start);
-        for (int t = t0; t < t1; ++t) {
-          const int first = (t == t0 ? start : sh.offset[t - 1]), n = sh.offset[t] - first;
-          if (n == 0 || (n <= kOneWarp && t % kSumWarps != warp)) continue;
+        const auto begin_of = [&](int t) { return t == t0 ? start : sh.offset[t - 1]; };
+        for (int t = t0 + static_cast<int>(threadIdx.x); t < t1; t += kSumThreads)
+          if (sh.offset[t] - begin_of(t) > kOneWarp)
+            sh.common[atomicAdd(&sh.commons, 1)] = static_cast<uint16_t>(t);
+        sum_tokens<VEC>(a, p, sh, start, count, t0, lane);
+        sum_sync();
+        // tokens of many rows, by all warps (in any order: each is written by itself)
+        for (int k = 0; k < sh.commons; ++k) {
+          const int t = sh.common[k], first = begin_of(t);
           SliceSum<VEC> s;
-          if (n <= kOneWarp) {
-            s.add(a, sh.sorted + first - start, n, p.col, lane);
-            finish_token(a, p, s, t, lane);
-          } else {
-            add_share(a, p, s, sh.sorted + first - start, n);
-            finish_token_together(a, p, sh, s, t);
-          }
+          add_share(a, p, s, sh.sorted + first - start, sh.offset[t] - first);
+          finish_token_together(a, p, sh, s, t);
         }
-        __syncthreads();
       }
       t0 = t1;
     }
+    __syncthreads();
   }
+  if (a.bulk) bulk_wait_all();
 }
 
 template <bool VEC>
 cudaError_t launch_scatter(const ScatterArgs& a, Chain* chain) {
-  constexpr int smem = static_cast<int>(sizeof(ScatterShared));
+  constexpr int smem = static_cast<int>(sizeof(ScatterShared)) + 128;
   static_assert(smem <= 113 * 1024, "two blocks an SM");
   const auto kernel = embedding_scatter_kernel<VEC>;
   // (a property of the kernel on the current device, set alike by every call)
   const cudaError_t e =
       cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  const int64_t slices = (a.width + kSlice - 1) / kSlice;
-  for (int64_t k = 0; k < slices; k += 65535) {  // the grid's y side ends there
-    ScatterArgs part = a;
-    part.dy += k * kSlice;
-    part.dtable = a.grad_f32 ? static_cast<void*>(static_cast<float*>(a.dtable) + k * kSlice)
-                             : static_cast<void*>(static_cast<uint16_t*>(a.dtable) + k * kSlice);
-    part.width -= k * kSlice;
-    const int64_t high = slices - k < 65535 ? slices - k : 65535;
-    const cudaError_t e2 = chain->launch(kernel, dim3(a.classes, static_cast<unsigned>(high)),
-                                         kSumThreads, smem, 1, part);
-    if (e2 != cudaSuccess) return e2;
-  }
-  return cudaSuccess;
+  const int64_t blocks = int64_t{a.classes} * a.slices;
+  if (blocks > INT32_MAX) return cudaErrorInvalidValue;
+  return chain->launch(kernel, dim3(static_cast<unsigned>(blocks)), kScatterThreads, smem, 1, a);
 }
 
 }  // namespace
@@ -559,15 +635,19 @@ cudaError_t launch_embedding_backward(const EmbeddingLaunch& L) {
   a.grad_f32 = L.grad_f32;
   a.accumulate = L.accumulate;
   a.scale = L.scale;
-  // two blocks an SM in all; more where a class would have over half of the rows that a
-  // block has room for
+  // Two blocks an SM in all; more where a class would have over half of the rows that a block
+  // has room for.
   const int64_t slices = (s.width + kSlice - 1) / kSlice;
+  a.slices = static_cast<int32_t>(slices);
   int64_t classes = 2 * kSms / slices;
   const int64_t least = s.rows / (kMostRows / 2) + 1;
   if (classes < least) classes = least;
   a.classes = static_cast<int32_t>(classes < s.vocab ? classes : s.vocab);
+  a.inverse = a.classes > 1 ? ~uint64_t{0} / static_cast<uint64_t>(a.classes) + 1 : 0;
   const bool vec = aligned(L.from, 16) && aligned(L.to, 16) && (s.rows == 1 || s.ldy % 8 == 0) &&
                    (s.vocab == 1 || s.ldt % (L.grad_f32 ? 4 : 8) == 0);
+  a.bulk = aligned(L.to, 16) && (s.vocab == 1 || s.ldt * (L.grad_f32 ? 4 : 2) % 16 == 0) &&
+           s.width * (L.grad_f32 ? 4 : 2) % 16 == 0;
   Chain chain{L.stream};
   return vec ? launch_scatter<true>(a, &chain) : launch_scatter<false>(a, &chain);
 }
