@@ -591,8 +591,8 @@ int64_t zero_linear_cross_entropy_workspace(const zero_cross_entropy_t* shape, i
  * residual stream r takes the output h of a block, and the next block gets y,
  *   s = r + alpha * gate * P(h),   y = N(s)
  * with P of kind `post` (NONE: h itself) and N of kind `kind` (RMS or LAYER), each
- * row by itself.  Pitches in elements; ldg = 0: gate is one vector for all rows.
- * 1 <= width <= ZERO_MAX_NORM_WIDTH; 0 <= rows < 2^31.
+ * row by itself.  Pitches in elements, below 2^31; ldg = 0: gate is one vector for all
+ * rows.  1 <= width <= ZERO_MAX_NORM_WIDTH; 0 <= rows < 2^31 - 1.
  */
 #define ZERO_MAX_NORM_WIDTH 32768
 typedef struct {

@@ -25,27 +25,25 @@ __device__ __forceinline__ uint32_t cluster_blocks() {
   asm volatile("mov.u32 %0, %%cluster_nctaid.x;" : "=r"(n));
   return n;
 }
-__device__ __forceinline__ void peer_store(uint32_t addr, float4 v) {
-  asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "f"(v.x), "f"(v.y), "f"(v.z),
-               "f"(v.w)
-               : "memory");
+__device__ __forceinline__ void peer_store(uint32_t addr, float v) {
+  asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
 }
 
 // What a row is read from.
-enum Input { kInR, kInH, kInGate, kInDy, kInDs, kInputs };
+// (the backward pass's s is kInR; it always has that and kInDy, the forward kInR)
+enum Input { kInDy, kInR, kInDs, kInH, kInGate, kInputs };
 
 struct NormArgs {
   int64_t rows, width;
   int32_t post, kind;
   float alpha, eps;
   const uint16_t* in[kInputs];  // NULL: not there (kInR is the backward pass's s)
-  int64_t ld[kInputs];
-  int32_t place[kInputs];       // in a stage of the ring
-  int32_t inputs;
+  uint32_t pitch[kInputs];      // bytes
+  int32_t inputs;               // how many are there
   const uint16_t *gate, *w1, *b1, *w, *b;  // vectors (gate: or NULL, kInGate is a matrix)
   uint16_t *s_out, *y;
   uint16_t *dr, *dh, *dgate_rows;          // dgate_rows: a matrix
-  int64_t lds, ldy, lddr, lddh, lddg;
+  uint32_t pitch_s, pitch_y, pitch_dr, pitch_dh, pitch_dg;  // bytes
   int32_t wvec;    // the vectors are read 16 bytes at a time
   // backward: sums of each block's rows, [kSums][blocks][width], where wanted
   float* sums;
@@ -56,8 +54,16 @@ struct NormArgs {
 // The sums over rows.
 enum { kDw, kDgate, kDw1, kDb, kDb1, kSums };
 
-__device__ __forceinline__ void copy16(void* to, const void* from) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_addr(to)), "l"(from) : "memory");
+__device__ __forceinline__ void copy16(uint32_t to, const void* from) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
+}
+__device__ __forceinline__ uint4 shared16(uint32_t from) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(from)
+               : "memory");
+  return v;
 }
 __device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
@@ -175,110 +181,170 @@ struct Columns {
   }
 };
 
+// Values that stay in registers: without this the compiler works out flags, pitches and places
+// anew from the kernel's arguments for every row, 150 instructions of it.
+__device__ __forceinline__ void keep(uint32_t& x) { asm volatile("" : "+r"(x)); }
+__device__ __forceinline__ void keep(const uint16_t*& p) { asm volatile("" : "+l"(p)); }
+
+// Row i of a matrix, from its first row's place for this thread.
+__device__ __forceinline__ const uint16_t* row_at(const uint16_t* base, uint32_t i, uint32_t pitch) {
+  return reinterpret_cast<const uint16_t*>(reinterpret_cast<const char*>(base) +
+                                           static_cast<uint64_t>(i) * pitch);
+}
+
 // The rows that a thread reads, kStages ahead (VEC): its own 16 bytes of each input, from its
 // own place in shared memory, so no thread waits for another's.  Rows that are not on 16-byte
-// boundaries are read when they are wanted.
-template <bool VEC>
+// boundaries are read when they are wanted.  FIRST to LAST: the inputs there may be.
+template <bool VEC, int FIRST, int LAST>
 struct Rows {
   const NormArgs& a;
   const Columns<VEC>& at;
-  uint8_t* ring;      // of this thread
-  int32_t pitch;      // of a place in a stage
-  int64_t next;       // the row that is asked for next
-  int64_t step;
-  int put = 0, got = 0;
+  const uint16_t* base[kInputs];
+  uint32_t there;                 // bit q: input q
+  uint32_t place;                 // of the first input, in the first stage
+  uint32_t stage, end;            // bytes of a stage, and of all
+  uint32_t each;                  // bytes of an input in a stage
+  uint32_t put = 0, got = 0;      // the stage asked into, and that read
+  uint32_t next, step, rows;
 
-  __device__ __forceinline__ void ask() {
-    if constexpr (VEC) {
-      if (next < a.rows && at.whole) {
-        uint8_t* to = ring + put * a.inputs * pitch;
+  __device__ __forceinline__ Rows(const NormArgs& a, const Columns<VEC>& at, uint8_t* ring, uint32_t first,
+                                  uint32_t step)
+      : a(a), at(at), there(0), each(blockDim.x * 16), next(first), step(step),
+        rows(static_cast<uint32_t>(a.rows)) {
+    place = smem_addr(ring) + threadIdx.x * 16;
+    stage = a.inputs * each;
+    end = kStages * stage;
 #pragma unroll
-        for (int q = 0; q < kInputs; ++q)
-          if (a.in[q] != nullptr) copy16(to + a.place[q] * pitch, a.in[q] + next * a.ld[q] + 8 * at.at);
-      }
-      next += step;
-      put = put + 1 == kStages ? 0 : put + 1;
-      copy_commit();
+    for (int q = FIRST; q <= LAST; ++q) {
+      there |= (a.in[q] != nullptr ? 1u : 0u) << q;
+      base[q] = a.in[q] + (VEC ? 8 * at.at : 0);
+      keep(base[q]);
     }
+    keep(there);
+    keep(stage);
+    keep(end);
+    keep(each);
+  }
+  __device__ __forceinline__ bool has(int q) const { return (there >> q & 1u) != 0; }
+  __device__ __forceinline__ void ask() {
+    if (next < rows && at.whole) {
+      uint32_t to = place + put;  // the inputs that are there, one after the other
+#pragma unroll
+      for (int q = FIRST; q <= LAST; ++q)
+        if (has(q)) {
+          copy16(to, row_at(base[q], next, a.pitch[q]));
+          to += each;
+        }
+    }
+    next += step;
+    put = put + stage == end ? 0 : put + stage;
+    copy_commit();
   }
   __device__ __forceinline__ void begin() {
+    if constexpr (VEC) {
 #pragma unroll
-    for (int k = 1; k < kStages; ++k) ask();
+      for (int k = 1; k < kStages; ++k) ask();
+    }
   }
   // The next row can be read.
   __device__ __forceinline__ void arrive() {
-    ask();
-    if constexpr (VEC) copy_wait<kStages - 1>();
+    if constexpr (VEC) {
+      ask();
+      copy_wait<kStages - 1>();
+    }
   }
-  __device__ __forceinline__ Eight read(int q, int64_t i) const {
-    if (VEC && at.whole)
-      return eight_of(*reinterpret_cast<const uint4*>(ring + (got * a.inputs + a.place[q]) * pitch));
-    return at.load_single(a.in[q] + i * a.ld[q]);
+  // Input q of row i, that is the `nth` of the inputs that are there.
+  __device__ __forceinline__ Eight read(int q, uint32_t i, uint32_t nth) const {
+    if constexpr (VEC) {
+      if (at.whole) return eight_of(shared16(place + got + nth * each));
+      return at.load_single(row_at(base[q] - 8 * at.at, i, a.pitch[q]));
+    } else {
+      return at.load_single(row_at(base[q], i, a.pitch[q]));
+    }
   }
-  __device__ __forceinline__ void done() { got = got + 1 == kStages ? 0 : got + 1; }
+  __device__ __forceinline__ void done() {
+    if constexpr (VEC) got = got + stage == end ? 0 : got + stage;
+  }
 };
 
-// N sums over the threads of a row, in the same order for each of them.  The warps' parts go
-// through shared memory, every block's to all blocks of the cluster, in two places taken in
-// turn, so that one barrier is enough: a place is written again only after the barrier
-// that follows its reading.
+// A matrix that is written by rows.
+template <bool VEC>
+struct Output {
+  const uint16_t* base;
+  uint32_t pitch;
+  __device__ __forceinline__ Output(uint16_t* p, uint32_t pitch) : base(p), pitch(pitch) { keep(base); }
+  __device__ __forceinline__ void put(const Columns<VEC>& at, uint32_t i, const Eight& x) const {
+    if (base != nullptr) at.store(const_cast<uint16_t*>(row_at(base, i, pitch)), x);
+  }
+};
+
+// N sums over the threads of a row, alike for each of them.  A warp adds up its lanes' by
+// halves: where there are several sums, each step passes on half of them, so 4 sums take 6
+// exchanges and not 20.  The warps' parts go through shared memory, every block's to all
+// blocks of the cluster, in two places taken in turn, so that one barrier is enough: a
+// place is written again only after the barrier that follows its reading.
 template <Share SHARE>
 struct RowSum {
   static constexpr int kParts = SHARE == kBlock ? 32 : kMostCluster * kMostWarps;
-  float4 (*part)[kParts];  // kBlock: places past the block's warps are 0
+  float (*part)[kParts][4];  // kBlock: parts past the block's warps are 0
   int place = 0;
+  __device__ __forceinline__ static float from(float x, int k) { return __shfl_xor_sync(0xffffffffu, x, k); }
+  // The sum of x[lane % N] over the lanes (N 1, 2 or 4).
   template <int N>
-  __device__ __forceinline__ void lanes(float (&x)[N], int width) {
-#pragma unroll
-    for (int k = 16; k > 0; k /= 2)
-      if (k < width) {
-#pragma unroll
-        for (int n = 0; n < N; ++n) x[n] += __shfl_xor_sync(0xffffffffu, x[n], k);
-      }
-  }
-  template <int N>
-  __device__ __forceinline__ void put(float4* to, const float (&x)[N]) {
-    if constexpr (N == 1) to->x = x[0];
-    else *to = make_float4(x[0], x[1], N > 2 ? x[2] : 0.0f, 0.0f);
-  }
-  template <int N>
-  __device__ __forceinline__ void get(const float4* from, float (&x)[N]) {
+  __device__ __forceinline__ static float over_lanes(const float (&x)[N], int lane) {
+    float v;
     if constexpr (N == 1) {
-      x[0] += from->x;
+      v = x[0] + from(x[0], 1);
+      v += from(v, 2);
+    } else if constexpr (N == 2) {
+      const bool odd = lane & 1;
+      v = (odd ? x[1] : x[0]) + from(odd ? x[0] : x[1], 1);
+      v += from(v, 2);
     } else {
-      const float4 p = *from;
-      x[0] += p.x;
-      x[1] += p.y;
-      if (N > 2) x[2] += p.z;
+      const bool odd = lane & 1, high = lane & 2;
+      const float lo = (odd ? x[1] : x[0]) + from(odd ? x[0] : x[1], 1);
+      const float hi = (odd ? x[3] : x[2]) + from(odd ? x[2] : x[3], 1);
+      v = (high ? hi : lo) + from(high ? lo : hi, 2);
     }
+    v += from(v, 4);
+    v += from(v, 8);
+    v += from(v, 16);
+    return v;
   }
   template <int N>
   __device__ __forceinline__ void operator()(float (&x)[N]) {
-    static_assert(N >= 1 && N <= 3, "a part has room for 3");
-    lanes(x, 32);
     const int warps = blockDim.x / 32, warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    float v = over_lanes(x, lane);
     if constexpr (SHARE == kBlock) {
-      if (warps == 1) return;
-      if (lane == 0) put(&part[place][warp], x);
-      __syncthreads();
-#pragma unroll
-      for (int n = 0; n < N; ++n) x[n] = 0.0f;
-      get(&part[place][lane % kMostWarps], x);
-      lanes(x, kMostWarps);
+      if (warps > 1) {
+        if (lane < N) part[place][warp][lane] = v;
+        __syncthreads();
+        // lane l: part l / 4 (and 8 further), sum l % 4
+        v = part[place][lane / 4][lane % 4];
+        if (warps > 8) v += part[place][lane / 4 + 8][lane % 4];
+        v += from(v, 4);
+        v += from(v, 8);
+        v += from(v, 16);
+        place ^= 1;
+      }
     } else {
       const int blocks = static_cast<int>(cluster_blocks());
-      if (lane < blocks)
-        peer_store(peer_addr(&part[place][static_cast<int>(cluster_rank()) * warps + warp], lane),
-                   make_float4(x[0], N > 1 ? x[N > 1 ? 1 : 0] : 0.0f, N > 2 ? x[N > 2 ? 2 : 0] : 0.0f, 0.0f));
+      if (lane < 4 * blocks) {  // lanes 4 b to 4 b + 3: to block b
+        const uint32_t to = peer_addr(&part[place][static_cast<int>(cluster_rank()) * warps + warp][lane % 4], lane / 4);
+        peer_store(to, v);
+      }
       __syncwarp();
       cluster_sync_writes();
-#pragma unroll
-      for (int n = 0; n < N; ++n) x[n] = 0.0f;
-      for (int w = lane; w < blocks * warps; w += 32) get(&part[place][w], x);
+      v = 0.0f;
+      for (int w = lane / 4; w < blocks * warps; w += 8) v += part[place][w][lane % 4];
       __syncwarp();
-      lanes(x, 32);
+      v += from(v, 4);
+      v += from(v, 8);
+      v += from(v, 16);
+      place ^= 1;
     }
-    place ^= 1;
+#pragma unroll
+    for (int n = 0; n < N; ++n) x[n] = N == 1 && SHARE == kBlock && warps == 1 ? v : __shfl_sync(0xffffffffu, v, n);
   }
 };
 
@@ -286,7 +352,7 @@ struct RowSum {
 template <Share SHARE>
 struct RowOwner {
   int at, lanes;        // this thread's place among the row's
-  int64_t first, step;  // rows
+  uint32_t first, step;  // rows
   __device__ __forceinline__ RowOwner() {
     const int blocks = SHARE == kBlock ? 1 : static_cast<int>(cluster_blocks());
     at = SHARE == kBlock ? threadIdx.x : cluster_rank() * blockDim.x + threadIdx.x;
@@ -296,32 +362,44 @@ struct RowOwner {
   }
 };
 
-// Before the first sum: the parts past the block's warps, and with a cluster its blocks there.
+// Before the first sum: parts that no warp writes, and with a cluster its blocks there.
 template <Share SHARE>
-__device__ __forceinline__ void begin_sums(float4 (*part)[RowSum<SHARE>::kParts]) {
-  if constexpr (SHARE == kBlock) {
-    if (threadIdx.x < 64) part[threadIdx.x / 32][threadIdx.x % 32] = make_float4(0, 0, 0, 0);
-    if (blockDim.x < 64 && threadIdx.x < 32) part[1][threadIdx.x] = make_float4(0, 0, 0, 0);
-    __syncthreads();
-  } else {
-    cluster_sync();
-  }
+__device__ __forceinline__ void begin_sums(float (*part)[RowSum<SHARE>::kParts][4]) {
+  for (int k = threadIdx.x; k < 2 * RowSum<SHARE>::kParts * 4; k += blockDim.x)
+    (&part[0][0][0])[k] = 0.0f;
+  __syncthreads();
+  if constexpr (SHARE == kCluster) cluster_sync();
 }
+
+// What norms and gate there are, in one register.
+struct Kinds {
+  uint32_t bits;
+  __device__ __forceinline__ explicit Kinds(const NormArgs& a)
+      : bits((a.kind == ZERO_NORM_LAYER ? 1u : 0u) | (a.post == ZERO_NORM_LAYER ? 2u : 0u) |
+             (a.post != ZERO_NORM_NONE ? 4u : 0u) | (a.gate != nullptr ? 8u : 0u)) {
+    keep(bits);
+  }
+  __device__ __forceinline__ bool layer() const { return (bits & 1u) != 0; }
+  __device__ __forceinline__ bool post_layer() const { return (bits & 2u) != 0; }
+  __device__ __forceinline__ bool post() const { return (bits & 4u) != 0; }
+  __device__ __forceinline__ bool gated() const { return (bits & 8u) != 0; }  // by a vector
+};
 
 // BIAS: there are biases.
 template <bool VEC, Share SHARE, bool BIAS>
 __global__ void __launch_bounds__(kMostThreads, 2)
     block_norm_forward_kernel(const __grid_constant__ NormArgs a) {
-  __shared__ float4 part[2][RowSum<SHARE>::kParts];
+  __shared__ float part[2][RowSum<SHARE>::kParts][4];
   extern __shared__ uint8_t ring[];
   wait_for_predecessor();
   launch_dependents();
   const RowOwner<SHARE> own;
   const Columns<VEC> at(own.at, own.lanes, static_cast<int>(a.width));
-  Rows<VEC> rows{a, at, ring + threadIdx.x * 16, static_cast<int32_t>(blockDim.x * 16), own.first, own.step};
+  Rows<VEC, kInR, kInGate> rows(a, at, ring, own.first, own.step);
   rows.begin();
-  const bool wvec = a.wvec != 0, has_h = a.in[kInH] != nullptr, matrix = a.in[kInGate] != nullptr;
-  const bool layer = a.kind == ZERO_NORM_LAYER, post_layer = a.post == ZERO_NORM_LAYER;
+  const Output<VEC> s_out(a.s_out, a.pitch_s), y_out(a.y, a.pitch_y);
+  const bool wvec = a.wvec != 0;
+  const Kinds kinds(a);
   // s = r + (h standardized * scale1 + bias1) [* gate's row]
   Eight scale1 = at.load_vector(a.gate, 1.0f, wvec) * a.alpha, bias1 = all_of(0.0f);
   if constexpr (BIAS) bias1 = at.load_vector(a.b1, 0.0f, wvec) * scale1;
@@ -341,33 +419,33 @@ __global__ void __launch_bounds__(kMostThreads, 2)
     row_sum(q);
     return rsqrtf(fmaf(q[0], inv_width, a.eps));
   };
-  for (int64_t i = own.first; i < a.rows; i += own.step, rows.done()) {
+  for (uint32_t i = own.first; i < rows.rows; i += own.step, rows.done()) {
     rows.arrive();
-    Eight s = rows.read(kInR, i);
-    if (has_h) {
-      Eight h = rows.read(kInH, i);
-      if (a.post != ZERO_NORM_NONE) {
-        if (post_layer) center(h);
+    Eight s = rows.read(kInR, i, 0);
+    if (rows.has(kInH)) {
+      Eight h = rows.read(kInH, i, 1);
+      if (kinds.post()) {
+        if (kinds.post_layer()) center(h);
         h = h * inverse_of(h);
       }
-      if (matrix) {
+      if (rows.has(kInGate)) {
         Eight p = h * scale1;
         if constexpr (BIAS) p = p + bias1;
-        s = fma8(p, rows.read(kInGate, i), s);
+        s = fma8(p, rows.read(kInGate, i, 2), s);
       } else {
         if constexpr (BIAS) s = s + bias1;
         s = fma8(h, scale1, s);
       }
     }
-    if (a.s_out != nullptr) at.store(a.s_out + i * a.lds, s);
-    if (layer) {
+    s_out.put(at, i, s);
+    if (kinds.layer()) {
       at.clear(s);
       center(s);
     }
     s = s * inverse_of(s);
     if constexpr (BIAS) s = fma8(s, w, b);
     else s = s * w;
-    at.store(a.y + i * a.ldy, s);
+    y_out.put(at, i, s);
   }
   if constexpr (SHARE == kCluster) cluster_sync();  // no block ends while others write to it
 }
@@ -381,17 +459,17 @@ __global__ void __launch_bounds__(kMostThreads, 2)
 template <bool VEC, Share SHARE, bool FULL, bool BIAS>
 __global__ void __launch_bounds__(kMostThreads)
     block_norm_backward_kernel(const __grid_constant__ NormArgs a) {
-  __shared__ float4 part[2][RowSum<SHARE>::kParts];
+  __shared__ float part[2][RowSum<SHARE>::kParts][4];
   extern __shared__ uint8_t ring[];
   wait_for_predecessor();
   launch_dependents();
   const RowOwner<SHARE> own;
   const Columns<VEC> at(own.at, own.lanes, static_cast<int>(a.width));
-  Rows<VEC> rows{a, at, ring + threadIdx.x * 16, static_cast<int32_t>(blockDim.x * 16), own.first, own.step};
+  Rows<VEC, kInDy, kInGate> rows(a, at, ring, own.first, own.step);
   rows.begin();
-  const bool wvec = a.wvec != 0, matrix = a.in[kInGate] != nullptr, gated = matrix || a.gate != nullptr;
-  const bool layer = a.kind == ZERO_NORM_LAYER, post_layer = a.post == ZERO_NORM_LAYER;
-  const bool post = a.post != ZERO_NORM_NONE;
+  const Output<VEC> dr_out(a.dr, a.pitch_dr), dh_out(a.dh, a.pitch_dh), dgate_out(a.dgate_rows, a.pitch_dg);
+  const bool wvec = a.wvec != 0;
+  const Kinds kinds(a);
   const Eight w = at.load_vector(a.w, 1.0f, wvec);
   Eight w1, g, dg, dw1;
   if constexpr (FULL) {
@@ -403,10 +481,12 @@ __global__ void __launch_bounds__(kMostThreads)
   begin_sums<SHARE>(part);
   RowSum<SHARE> row_sum{part};
   const float inv_width = 1.0f / static_cast<float>(a.width);
-  for (int64_t i = own.first; i < a.rows; i += own.step, rows.done()) {
+  for (uint32_t i = own.first; i < rows.rows; i += own.step, rows.done()) {
     rows.arrive();
-    Eight x = rows.read(kInR, i), u = rows.read(kInDy, i), h;
-    if constexpr (FULL) h = rows.read(kInH, i);
+    const bool layer = kinds.layer(), post_layer = kinds.post_layer(), post = kinds.post();
+    const uint32_t has_ds = rows.has(kInDs) ? 1u : 0u;
+    Eight x = rows.read(kInR, i, 1), u = rows.read(kInDy, i, 0), h;
+    if constexpr (FULL) h = rows.read(kInH, i, 2 + has_ds);
     if (layer || (FULL && post_layer)) {  // means, then what is left
       float m[2] = {sum8(x), FULL ? sum8(h) : 0.0f};
       row_sum(m);
@@ -421,12 +501,8 @@ __global__ void __launch_bounds__(kMostThreads)
         }
     }
     const Eight uw = u * w;
-    float q[3] = {dot8(x, x), dot8(uw, x), FULL ? dot8(h, h) : 0.0f};
-    float mean[1] = {0.0f};
-    if (layer) {
-      mean[0] = sum8(uw);
-      row_sum(mean);
-    }
+    // x x, u w x, u w [LAYER], h h
+    float q[4] = {dot8(x, x), dot8(uw, x), layer ? sum8(uw) : 0.0f, FULL ? dot8(h, h) : 0.0f};
     row_sum(q);
     const float inverse = rsqrtf(fmaf(q[0], inv_width, a.eps));
     const float along = q[1] * inverse * inv_width;
@@ -434,21 +510,22 @@ __global__ void __launch_bounds__(kMostThreads)
     dw = fma8(u, x, dw);
     if constexpr (BIAS) db = db + u;
     x = fma8(x, all_of(-along), uw);
-    if (layer) x = x + all_of(-mean[0] * inv_width);
-    if (a.in[kInDs] != nullptr) x = fma8(x, all_of(inverse), rows.read(kInDs, i));
+    if (layer) x = x + all_of(-q[2] * inv_width);
+    if (has_ds) x = fma8(x, all_of(inverse), rows.read(kInDs, i, 2));
     else x = x * inverse;
     at.clear(x);
-    if (a.dr != nullptr) at.store(a.dr + i * a.lddr, x);
+    dr_out.put(at, i, x);
     x = x * a.alpha;  // the gradient of gate P(h)
     if constexpr (FULL) {
-      const float inverse1 = post ? rsqrtf(fmaf(q[2], inv_width, a.eps)) : 1.0f;
+      const float inverse1 = post ? rsqrtf(fmaf(q[3], inv_width, a.eps)) : 1.0f;
       h = h * inverse1;
-      if (gated) {
+      const bool matrix = rows.has(kInGate);
+      if (matrix || kinds.gated()) {
         Eight t = h * w1;
         if constexpr (BIAS) t = t + at.load_vector(a.b1, 0.0f, wvec);
         if (matrix) {
-          g = rows.read(kInGate, i);
-          if (a.dgate_rows != nullptr) at.store(a.dgate_rows + i * a.lddg, x * t);
+          g = rows.read(kInGate, i, 3 + has_ds);
+          dgate_out.put(at, i, x * t);
         } else {
           dg = fma8(x, t, dg);
         }
@@ -457,7 +534,7 @@ __global__ void __launch_bounds__(kMostThreads)
       if (post) {
         dw1 = fma8(x, h, dw1);
         if constexpr (BIAS) db1 = db1 + x;
-        if (a.dh != nullptr) {  // (alike for every thread)
+        if (dh_out.base != nullptr) {  // (alike for every thread)
           x = x * w1;
           at.clear(x);
           float m[2] = {dot8(x, h), 0.0f};
@@ -469,7 +546,7 @@ __global__ void __launch_bounds__(kMostThreads)
         }
       }
     }
-    if (a.dh != nullptr) at.store(a.dh + i * a.lddh, x);
+    dh_out.put(at, i, x);
   }
   const auto put = [&](int q, const Eight& x) {
     if ((a.wanted >> q & 1) == 0) return;
@@ -551,6 +628,8 @@ int64_t backward_blocks(int64_t rows, int64_t width) {
   return n < most ? n : most;
 }
 
+uint32_t bytes_of(int64_t pitch) { return static_cast<uint32_t>(2 * pitch); }
+
 NormArgs args_of(const BlockNormLaunch& L) {
   const zero_block_norm_t& s = L.s;
   NormArgs a{};
@@ -565,18 +644,18 @@ NormArgs args_of(const BlockNormLaunch& L) {
   a.w = L.weight;
   a.b = L.bias;
   (s.ldg == 0 ? a.gate : a.in[kInGate]) = L.gate;
-  a.ld[kInGate] = s.ldg;
   a.in[kInH] = L.h;
-  a.ld[kInH] = s.ldh;
   a.s_out = L.s_out;
   a.y = L.y;
   a.dr = L.dr;
   a.dh = L.dh;
-  a.lds = s.lds;
-  a.ldy = s.ldy;
-  a.lddr = s.lddr;
-  a.lddh = s.lddh;
-  a.lddg = s.lddg;
+  a.pitch[kInGate] = bytes_of(s.ldg);
+  a.pitch[kInH] = bytes_of(s.ldh);
+  a.pitch_s = bytes_of(s.lds);
+  a.pitch_y = bytes_of(s.ldy);
+  a.pitch_dr = bytes_of(s.lddr);
+  a.pitch_dh = bytes_of(s.lddh);
+  a.pitch_dg = bytes_of(s.lddg);
   a.wvec = 1;
   for (const uint16_t* p : {a.w1, a.b1, a.w, a.b, a.gate})
     if (!aligned(p, 16)) a.wvec = 0;
@@ -588,17 +667,17 @@ constexpr int kMostRing = kStages * kInputs * kMostThreads * 16;
 static_assert(kMostRing + 8192 <= kSmem, "the ring and the parts of the sums");
 int ring_bytes(const NormArgs& a, int threads) { return kStages * a.inputs * threads * 16; }
 
-// Whether rows of every matrix lie on 16-byte boundaries; and the inputs' places.
+// Whether rows of every matrix lie on 16-byte boundaries; and how many inputs there are.
 struct Rows16 {
   int64_t rows;
   bool all = true;
-  void operator()(const void* p, int64_t ld) {
-    if (p != nullptr && (!aligned(p, 16) || (rows > 1 && ld % 8 != 0))) all = false;
+  void operator()(const void* p, uint32_t pitch) {
+    if (p != nullptr && (!aligned(p, 16) || (rows > 1 && pitch % 16 != 0))) all = false;
   }
   explicit Rows16(NormArgs* a) : rows(a->rows) {
     for (int q = 0; q < kInputs; ++q) {
-      (*this)(a->in[q], a->ld[q]);
-      if (a->in[q] != nullptr) a->place[q] = a->inputs++;
+      (*this)(a->in[q], a->pitch[q]);
+      if (a->in[q] != nullptr) ++a->inputs;
     }
   }
 };
@@ -650,10 +729,10 @@ cudaError_t launch_block_norm_forward(const BlockNormLaunch& L) {
   (void)cudaGetLastError();
   NormArgs a = args_of(L);
   a.in[kInR] = L.r;
-  a.ld[kInR] = L.s.ldr;
+  a.pitch[kInR] = bytes_of(L.s.ldr);
   Rows16 vec(&a);
-  vec(a.s_out, a.lds);
-  vec(a.y, a.ldy);
+  vec(a.s_out, a.pitch_s);
+  vec(a.y, a.pitch_y);
   Chain chain{L.stream};
   return a.b1 != nullptr || a.b != nullptr ? launch_forward<true>(a, vec.all, &chain)
                                            : launch_forward<false>(a, vec.all, &chain);
@@ -664,13 +743,13 @@ cudaError_t launch_block_norm_backward(const BlockNormLaunch& L) {
   NormArgs a = args_of(L);
   const bool one = L.s.ldg == 0;
   a.in[kInR] = L.sum;
-  a.ld[kInR] = L.s.lds;
+  a.pitch[kInR] = bytes_of(L.s.lds);
   a.in[kInDy] = L.dy;
-  a.ld[kInDy] = L.s.lddy;
+  a.pitch[kInDy] = bytes_of(L.s.lddy);
   a.in[kInDs] = L.ds;
-  a.ld[kInDs] = L.s.ldds;
+  a.pitch[kInDs] = bytes_of(L.s.ldds);
   const bool full = L.h != nullptr && (a.post != ZERO_NORM_NONE || L.gate != nullptr);
-  if (!full) a.in[kInH] = nullptr;  // (its values are not needed)
+  if (!full) a.in[kInH] = a.in[kInGate] = nullptr;  // (their values are not needed)
   NormJoinArgs j{};
   j.out[kDw] = L.dweight;
   j.out[kDb] = L.dbias;
@@ -683,9 +762,9 @@ cudaError_t launch_block_norm_backward(const BlockNormLaunch& L) {
   cudaError_t e = cudaSuccess;
   if (a.rows > 0) {
     Rows16 vec(&a);
-    vec(a.dr, a.lddr);
-    vec(a.dh, a.lddh);
-    vec(a.dgate_rows, a.lddg);
+    vec(a.dr, a.pitch_dr);
+    vec(a.dh, a.pitch_dh);
+    vec(a.dgate_rows, a.pitch_dg);
     a.sums = static_cast<float*>(L.workspace);
     a.blocks = static_cast<int32_t>(backward_blocks(a.rows, a.width));
     const bool bias = L.dbias != nullptr || L.dpost_bias != nullptr || a.b1 != nullptr;

@@ -107,6 +107,11 @@ int check_embedding(const zero_embedding_t* s, const Matrix& from, const Matrix&
   return share(to, from) || share(to, ids) ? ZERO_E_ALIAS : ZERO_OK;
 }
 
+// A matrix of the block norms, whose kernels count a row's bytes in 32 bits.
+int check_rows(const Matrix& m) {
+  return m.base != nullptr && m.ld > kMostSide ? ZERO_E_SHAPE : check_matrix(m);
+}
+
 bool norm_kind(int32_t kind) { return kind == ZERO_NORM_RMS || kind == ZERO_NORM_LAYER; }
 
 // What the two directions of the block norms share.
@@ -498,7 +503,7 @@ int zero_block_norm_forward(const zero_block_norm_t* shape, const void* r, const
       my{y, rows, d, z.ldy, 2}, mg{gate, one ? 1 : rows, d, one ? d : z.ldg, 2}, mpw{post_weight, 1, d, d, 2},
       mpb{post_bias, 1, d, d, 2}, mw{weight, 1, d, d, 2}, mb{bias, 1, d, d, 2};
   for (const Matrix* m : {&mr, &mh, &ms, &my, &mg, &mpw, &mpb, &mw, &mb})
-    if ((rc = check_matrix(*m)) != ZERO_OK) return rc;
+    if ((rc = check_rows(*m)) != ZERO_OK) return rc;
   for (const Matrix* m : {&mh, &mg, &mpw, &mpb, &mw, &mb})
     if (share(ms, *m) || share(my, *m)) return ZERO_E_ALIAS;
   if (share(my, mr) || share(my, ms) || (!(s == r && z.lds == z.ldr) && share(ms, mr))) return ZERO_E_ALIAS;
@@ -547,9 +552,9 @@ int zero_block_norm_backward(const zero_block_norm_t* shape, const void* dy, con
   const Matrix* const in[] = {&mdy, &mds, &ms, &mh, &mg, &mpw, &mpb, &mw};
   const Matrix* const out[] = {&mdr, &mdh, &mdg, &mdpw, &mdpb, &mdw, &mdb};
   for (const Matrix* m : in)
-    if ((rc = check_matrix(*m)) != ZERO_OK) return rc;
+    if ((rc = check_rows(*m)) != ZERO_OK) return rc;
   for (const Matrix* m : out)
-    if ((rc = check_matrix(*m)) != ZERO_OK) return rc;
+    if ((rc = check_rows(*m)) != ZERO_OK) return rc;
   for (const Matrix* o : out) {
     for (const Matrix* m : in)
       if (!(o == &mdr && m == &mds && dr == ds && z.lddr == z.ldds) && share(*o, *m)) return ZERO_E_ALIAS;
