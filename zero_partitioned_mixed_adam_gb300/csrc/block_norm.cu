@@ -3,6 +3,8 @@
 //   s = r + alpha * gate * P(h),   y = N(s),
 // a row at a time, in registers between its loads and its stores, so that each matrix is
 // read or written once.  Bound by HBM: 8 bytes an element forward, 12 backward.
+#include <type_traits>
+
 #include "chain.cuh"
 #include "internal.h"
 #include "linear_epilogue.cuh"
@@ -14,6 +16,7 @@ namespace {
 
 constexpr int kMostThreads = 512, kMostWarps = kMostThreads / 32, kMostCluster = 8;
 constexpr int kStages = 4;  // rows under way
+constexpr int kSumsAtOnce = 8;
 
 // Who shares a row: a block up to 4,096 columns, a cluster of blocks beyond.  A thread has 8
 // columns in every case, so that the backward pass has room for the sums of each in
@@ -181,6 +184,15 @@ struct Columns {
   }
 };
 
+// A vector of the columns in bf16, 4 registers instead of 8 (NULL: ones).
+struct Held {
+  uint4 v;
+  template <bool VEC>
+  __device__ __forceinline__ Held(const Columns<VEC>& at, const uint16_t* p, bool vec)
+      : v(bf16_of(at.load_vector(p, 1.0f, vec))) {}
+  __device__ __forceinline__ Eight get() const { return eight_of(v); }
+};
+
 // Values that stay in registers: without this the compiler works out flags, pitches and places
 // anew from the kernel's arguments for every row, 150 instructions of it.
 __device__ __forceinline__ void keep(uint32_t& x) { asm volatile("" : "+r"(x)); }
@@ -246,24 +258,37 @@ struct Rows {
       for (int k = 1; k < kStages; ++k) ask();
     }
   }
-  // The next row can be read.
-  __device__ __forceinline__ void arrive() {
+  // The next R rows can be read.
+  __device__ __forceinline__ void arrive(int R = 1) {
     if constexpr (VEC) {
       ask();
-      copy_wait<kStages - 1>();
+      if (R > 1) {
+        copy_wait<kStages - 2>();  // (all but the last two)
+      } else {
+        copy_wait<kStages - 1>();
+      }
     }
   }
-  // Input q of row i, that is the `nth` of the inputs that are there.
-  __device__ __forceinline__ Eight read(int q, uint32_t i, uint32_t nth) const {
+  // Input q of row i, that is the `nth` of the inputs that are there, `ahead` of the rows read.
+  __device__ __forceinline__ Eight read(int q, uint32_t i, uint32_t nth, int ahead = 0) const {
     if constexpr (VEC) {
-      if (at.whole) return eight_of(shared16(place + got + nth * each));
+      uint32_t from = got;
+      if (ahead > 0) from = from + stage == end ? 0 : from + stage;
+      if (at.whole) return eight_of(shared16(place + from + nth * each));
       return at.load_single(row_at(base[q] - 8 * at.at, i, a.pitch[q]));
     } else {
       return at.load_single(row_at(base[q], i, a.pitch[q]));
     }
   }
-  __device__ __forceinline__ void done() {
-    if constexpr (VEC) got = got + stage == end ? 0 : got + stage;
+  // R rows have been read (another may be asked for in the place of each but the last).
+  __device__ __forceinline__ void done(int R = 1) {
+    if constexpr (VEC) {
+      got = got + stage == end ? 0 : got + stage;
+      if (R > 1) {
+        ask();
+        got = got + stage == end ? 0 : got + stage;
+      }
+    }
   }
 };
 
@@ -278,18 +303,18 @@ struct Output {
   }
 };
 
-// N sums over the threads of a row, alike for each of them.  A warp adds up its lanes' by
-// halves: where there are several sums, each step passes on half of them, so 4 sums take 6
-// exchanges and not 20.  The warps' parts go through shared memory, every block's to all
+// N sums over the threads of a row (or of two), alike for each of them.  A warp adds up its
+// lanes' by halves: where there are several sums, each step passes on half of them, so 4 sums
+// take 6 exchanges and not 20.  The warps' parts go through shared memory, every block's to all
 // blocks of the cluster, in two places taken in turn, so that one barrier is enough: a
 // place is written again only after the barrier that follows its reading.
 template <Share SHARE>
 struct RowSum {
   static constexpr int kParts = SHARE == kBlock ? 32 : kMostCluster * kMostWarps;
-  float (*part)[kParts][4];  // kBlock: parts past the block's warps are 0
+  float (*part)[kParts][kSumsAtOnce];  // kBlock: parts past the block's warps are 0
   int place = 0;
   __device__ __forceinline__ static float from(float x, int k) { return __shfl_xor_sync(0xffffffffu, x, k); }
-  // The sum of x[lane % N] over the lanes (N 1, 2 or 4).
+  // The sum of x[lane % N] over the lanes (N 1, 2, 4 or 8).
   template <int N>
   __device__ __forceinline__ static float over_lanes(const float (&x)[N], int lane) {
     float v;
@@ -302,11 +327,21 @@ struct RowSum {
       v += from(v, 2);
     } else {
       const bool odd = lane & 1, high = lane & 2;
-      const float lo = (odd ? x[1] : x[0]) + from(odd ? x[0] : x[1], 1);
-      const float hi = (odd ? x[3] : x[2]) + from(odd ? x[2] : x[3], 1);
-      v = (high ? hi : lo) + from(high ? lo : hi, 2);
+      float y[N / 4];
+#pragma unroll
+      for (int k = 0; k < N / 4; ++k) {
+        const float* z = x + 4 * k;
+        const float lo = (odd ? z[1] : z[0]) + from(odd ? z[0] : z[1], 1);
+        const float hi = (odd ? z[3] : z[2]) + from(odd ? z[2] : z[3], 1);
+        y[k] = (high ? hi : lo) + from(high ? lo : hi, 2);
+      }
+      v = y[0];
+      if constexpr (N == 8) {
+        const bool top = lane & 4;
+        v = (top ? y[1] : y[0]) + from(top ? y[0] : y[1], 4);
+      }
     }
-    v += from(v, 4);
+    if constexpr (N != 8) v += from(v, 4);
     v += from(v, 8);
     v += from(v, 16);
     return v;
@@ -314,37 +349,38 @@ struct RowSum {
   template <int N>
   __device__ __forceinline__ void operator()(float (&x)[N]) {
     const int warps = blockDim.x / 32, warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    constexpr int W = N == 8 ? 8 : 4;  // of a part, N of them in use; lane l takes sum l % W of
+                                       // the parts l / W, l / W + 32 / W, ...
     float v = over_lanes(x, lane);
-    if constexpr (SHARE == kBlock) {
-      if (warps > 1) {
-        if (lane < N) part[place][warp][lane] = v;
+    if (SHARE == kCluster || warps > 1) {
+      int parts = kMostWarps;
+      if constexpr (SHARE == kBlock) {
+        if (lane < W) part[place][warp][lane] = v;
         __syncthreads();
-        // lane l: part l / 4 (and 8 further), sum l % 4
-        v = part[place][lane / 4][lane % 4];
-        if (warps > 8) v += part[place][lane / 4 + 8][lane % 4];
-        v += from(v, 4);
-        v += from(v, 8);
-        v += from(v, 16);
-        place ^= 1;
+      } else {
+        const int blocks = static_cast<int>(cluster_blocks());
+        for (int k = lane; k < W * blocks; k += 32)  // to block k / W (the lanes' sums repeat every W)
+          peer_store(peer_addr(&part[place][static_cast<int>(cluster_rank()) * warps + warp][k % W], k / W), v);
+        __syncwarp();
+        cluster_sync_writes();
+        parts = blocks * warps;
       }
-    } else {
-      const int blocks = static_cast<int>(cluster_blocks());
-      if (lane < 4 * blocks) {  // lanes 4 b to 4 b + 3: to block b
-        const uint32_t to = peer_addr(&part[place][static_cast<int>(cluster_rank()) * warps + warp][lane % 4], lane / 4);
-        peer_store(to, v);
-      }
-      __syncwarp();
-      cluster_sync_writes();
       v = 0.0f;
-      for (int w = lane / 4; w < blocks * warps; w += 8) v += part[place][w][lane % 4];
-      __syncwarp();
-      v += from(v, 4);
+      if constexpr (SHARE == kBlock) {
+#pragma unroll
+        for (int w = 0; w < kMostWarps; w += 32 / W)
+          if (w < warps) v += part[place][lane / W + w][lane % W];
+      } else {
+        for (int w = lane / W; w < parts; w += 32 / W) v += part[place][w][lane % W];
+        __syncwarp();
+      }
+      if constexpr (W == 4) v += from(v, 4);
       v += from(v, 8);
       v += from(v, 16);
       place ^= 1;
     }
 #pragma unroll
-    for (int n = 0; n < N; ++n) x[n] = N == 1 && SHARE == kBlock && warps == 1 ? v : __shfl_sync(0xffffffffu, v, n);
+    for (int n = 0; n < N; ++n) x[n] = __shfl_sync(0xffffffffu, v, n);
   }
 };
 
@@ -364,8 +400,8 @@ struct RowOwner {
 
 // Before the first sum: parts that no warp writes, and with a cluster its blocks there.
 template <Share SHARE>
-__device__ __forceinline__ void begin_sums(float (*part)[RowSum<SHARE>::kParts][4]) {
-  for (int k = threadIdx.x; k < 2 * RowSum<SHARE>::kParts * 4; k += blockDim.x)
+__device__ __forceinline__ void begin_sums(float (*part)[RowSum<SHARE>::kParts][kSumsAtOnce]) {
+  for (int k = threadIdx.x; k < 2 * RowSum<SHARE>::kParts * kSumsAtOnce; k += blockDim.x)
     (&part[0][0][0])[k] = 0.0f;
   __syncthreads();
   if constexpr (SHARE == kCluster) cluster_sync();
@@ -389,7 +425,7 @@ struct Kinds {
 template <bool VEC, Share SHARE, bool BIAS>
 __global__ void __launch_bounds__(kMostThreads, 2)
     block_norm_forward_kernel(const __grid_constant__ NormArgs a) {
-  __shared__ float part[2][RowSum<SHARE>::kParts][4];
+  __shared__ float part[2][RowSum<SHARE>::kParts][kSumsAtOnce];
   extern __shared__ uint8_t ring[];
   wait_for_predecessor();
   launch_dependents();
@@ -459,7 +495,7 @@ __global__ void __launch_bounds__(kMostThreads, 2)
 template <bool VEC, Share SHARE, bool FULL, bool BIAS>
 __global__ void __launch_bounds__(kMostThreads)
     block_norm_backward_kernel(const __grid_constant__ NormArgs a) {
-  __shared__ float part[2][RowSum<SHARE>::kParts][4];
+  __shared__ float part[2][RowSum<SHARE>::kParts][kSumsAtOnce];
   extern __shared__ uint8_t ring[];
   wait_for_predecessor();
   launch_dependents();
@@ -470,84 +506,113 @@ __global__ void __launch_bounds__(kMostThreads)
   const Output<VEC> dr_out(a.dr, a.pitch_dr), dh_out(a.dh, a.pitch_dh), dgate_out(a.dgate_rows, a.pitch_dg);
   const bool wvec = a.wvec != 0;
   const Kinds kinds(a);
-  const Eight w = at.load_vector(a.w, 1.0f, wvec);
-  Eight w1, g, dg, dw1;
-  if constexpr (FULL) {
-    w1 = at.load_vector(a.w1, 1.0f, wvec);
-    g = at.load_vector(a.gate, 1.0f, wvec);
-    dg = dw1 = all_of(0.0f);
-  }
-  Eight dw = all_of(0.0f), db = dw, db1 = dw;
+  const Held w(at, a.w, wvec), w1(at, FULL ? a.w1 : nullptr, wvec), g(at, FULL ? a.gate : nullptr, wvec);
+  Eight dw = all_of(0.0f), db = dw, dg = dw, dw1 = dw, db1 = dw;
   begin_sums<SHARE>(part);
   RowSum<SHARE> row_sum{part};
   const float inv_width = 1.0f / static_cast<float>(a.width);
-  for (uint32_t i = own.first; i < rows.rows; i += own.step, rows.done()) {
-    rows.arrive();
+  // R rows, i and i + step: what they wait for, they wait for together.
+  const auto make = [&](auto how_many, uint32_t i0) {
+    constexpr int R = decltype(how_many)::value;
     const bool layer = kinds.layer(), post_layer = kinds.post_layer(), post = kinds.post();
     const uint32_t has_ds = rows.has(kInDs) ? 1u : 0u;
-    Eight x = rows.read(kInR, i, 1), u = rows.read(kInDy, i, 0), h;
-    if constexpr (FULL) h = rows.read(kInH, i, 2 + has_ds);
+    Eight x[R], u[R], h[R];
+    float q[4 * R], m[2 * R];
+    const auto each = [&](auto f) {
+#pragma unroll
+      for (int r = 0; r < R; ++r) f(r, i0 + r * own.step);
+    };
+    if constexpr (VEC) rows.arrive(R);
+    each([&](int r, uint32_t i) {
+      x[r] = rows.read(kInR, i, 1, r);
+      u[r] = rows.read(kInDy, i, 0, r);
+      if constexpr (FULL) h[r] = rows.read(kInH, i, 2 + has_ds, r);
+    });
     if (layer || (FULL && post_layer)) {  // means, then what is left
-      float m[2] = {sum8(x), FULL ? sum8(h) : 0.0f};
+      each([&](int r, uint32_t) {
+        m[2 * r] = sum8(x[r]);
+        m[2 * r + 1] = FULL ? sum8(h[r]) : 0.0f;
+      });
       row_sum(m);
-      if (layer) {
-        x = x + all_of(-m[0] * inv_width);
-        at.clear(x);
-      }
-      if constexpr (FULL)
-        if (post_layer) {
-          h = h + all_of(-m[1] * inv_width);
-          at.clear(h);
+      each([&](int r, uint32_t) {
+        if (layer) {
+          x[r] = x[r] + all_of(-m[2 * r] * inv_width);
+          at.clear(x[r]);
         }
+        if constexpr (FULL)
+          if (post_layer) {
+            h[r] = h[r] + all_of(-m[2 * r + 1] * inv_width);
+            at.clear(h[r]);
+          }
+      });
     }
-    const Eight uw = u * w;
-    // x x, u w x, u w [LAYER], h h
-    float q[4] = {dot8(x, x), dot8(uw, x), layer ? sum8(uw) : 0.0f, FULL ? dot8(h, h) : 0.0f};
+    each([&](int r, uint32_t) {  // x x, u w x, u w [LAYER], h h
+      const Eight uw = u[r] * w.get();
+      q[4 * r] = dot8(x[r], x[r]);
+      q[4 * r + 1] = dot8(uw, x[r]);
+      q[4 * r + 2] = layer ? sum8(uw) : 0.0f;
+      q[4 * r + 3] = FULL ? dot8(h[r], h[r]) : 0.0f;
+    });
     row_sum(q);
-    const float inverse = rsqrtf(fmaf(q[0], inv_width, a.eps));
-    const float along = q[1] * inverse * inv_width;
-    x = x * inverse;  // standardized
-    dw = fma8(u, x, dw);
-    if constexpr (BIAS) db = db + u;
-    x = fma8(x, all_of(-along), uw);
-    if (layer) x = x + all_of(-q[2] * inv_width);
-    if (has_ds) x = fma8(x, all_of(inverse), rows.read(kInDs, i, 2));
-    else x = x * inverse;
-    at.clear(x);
-    dr_out.put(at, i, x);
-    x = x * a.alpha;  // the gradient of gate P(h)
-    if constexpr (FULL) {
-      const float inverse1 = post ? rsqrtf(fmaf(q[3], inv_width, a.eps)) : 1.0f;
-      h = h * inverse1;
-      const bool matrix = rows.has(kInGate);
-      if (matrix || kinds.gated()) {
-        Eight t = h * w1;
-        if constexpr (BIAS) t = t + at.load_vector(a.b1, 0.0f, wvec);
-        if (matrix) {
-          g = rows.read(kInGate, i, 3 + has_ds);
-          dgate_out.put(at, i, x * t);
-        } else {
-          dg = fma8(x, t, dg);
+    each([&](int r, uint32_t i) {
+      const float inverse = rsqrtf(fmaf(q[4 * r], inv_width, a.eps));
+      const float along = q[4 * r + 1] * inverse * inv_width;
+      x[r] = x[r] * inverse;  // standardized
+      dw = fma8(u[r], x[r], dw);
+      if constexpr (BIAS) db = db + u[r];
+      x[r] = fma8(x[r], all_of(-along), u[r] * w.get());
+      if (layer) x[r] = x[r] + all_of(-q[4 * r + 2] * inv_width);
+      if (has_ds) x[r] = fma8(x[r], all_of(inverse), rows.read(kInDs, i, 2, r));
+      else x[r] = x[r] * inverse;
+      at.clear(x[r]);
+      dr_out.put(at, i, x[r]);
+      x[r] = x[r] * a.alpha;  // the gradient of gate P(h)
+      if constexpr (FULL) {
+        const float inverse1 = post ? rsqrtf(fmaf(q[4 * r + 3], inv_width, a.eps)) : 1.0f;
+        q[4 * r + 3] = inverse1;
+        h[r] = h[r] * inverse1;
+        const bool matrix = rows.has(kInGate);
+        if (matrix || kinds.gated()) {
+          Eight t = h[r] * w1.get();
+          if constexpr (BIAS) t = t + at.load_vector(a.b1, 0.0f, wvec);
+          if (matrix) {
+            dgate_out.put(at, i, x[r] * t);
+            x[r] = x[r] * rows.read(kInGate, i, 3 + has_ds, r);
+          } else {
+            dg = fma8(x[r], t, dg);
+            x[r] = x[r] * g.get();
+          }
         }
-        x = x * g;
-      }
-      if (post) {
-        dw1 = fma8(x, h, dw1);
-        if constexpr (BIAS) db1 = db1 + x;
-        if (dh_out.base != nullptr) {  // (alike for every thread)
-          x = x * w1;
-          at.clear(x);
-          float m[2] = {dot8(x, h), 0.0f};
-          if (post_layer) m[1] = sum8(x);
-          row_sum(m);
-          x = fma8(h, all_of(-m[0] * inv_width), x);
-          if (post_layer) x = x + all_of(-m[1] * inv_width);
-          x = x * inverse1;
+        if (post) {
+          dw1 = fma8(x[r], h[r], dw1);
+          if constexpr (BIAS) db1 = db1 + x[r];
+          x[r] = x[r] * w1.get();
+          at.clear(x[r]);
+          m[2 * r] = dot8(x[r], h[r]);
+          m[2 * r + 1] = post_layer ? sum8(x[r]) : 0.0f;
         }
       }
+    });
+    if (dh_out.base != nullptr) {  // (alike for every thread)
+      if (FULL && post) row_sum(m);
+      each([&](int r, uint32_t i) {
+        if (FULL && post) {
+          x[r] = fma8(h[r], all_of(-m[2 * r] * inv_width), x[r]);
+          if (post_layer) x[r] = x[r] + all_of(-m[2 * r + 1] * inv_width);
+          x[r] = x[r] * q[4 * r + 3];
+        }
+        dh_out.put(at, i, x[r]);
+      });
     }
-    dh_out.put(at, i, x);
-  }
+    if constexpr (VEC) rows.done(R);
+  };
+  // Two rows at a time where there is room for them in registers (8192 x 2048 without a norm
+  // after the block 41 -> 28 us; with one, sums spilt, 58 -> 66), or a barrier is a cluster's
+  // (4096 x 8192 177 -> 135).
+  uint32_t i = own.first;
+  if constexpr (!FULL || SHARE == kCluster)
+    for (; i + own.step < rows.rows; i += 2 * own.step) make(std::integral_constant<int, 2>(), i);
+  for (; i < rows.rows; i += own.step) make(std::integral_constant<int, 1>(), i);
   const auto put = [&](int q, const Eight& x) {
     if ((a.wanted >> q & 1) == 0) return;
     float* to = a.sums + (static_cast<int64_t>(q) * a.blocks + own.first) * a.width;
@@ -577,10 +642,11 @@ struct NormJoinArgs {
   int32_t out_f32, accumulate;
 };
 
-// The blocks' sums in their order: 32 columns a block, 8 runs of blocks, which are added
+// The blocks' sums in their order: 32 columns a block, 32 runs of blocks, which are added
 // up in their order too.
-__global__ void __launch_bounds__(256) block_norm_join_kernel(const __grid_constant__ NormJoinArgs a) {
-  __shared__ float part[8][33];
+constexpr int kRuns = 32;
+__global__ void __launch_bounds__(32 * kRuns) block_norm_join_kernel(const __grid_constant__ NormJoinArgs a) {
+  __shared__ float part[kRuns][33];
   wait_for_predecessor();
   launch_dependents();
   void* out = a.out[blockIdx.y];
@@ -591,13 +657,13 @@ __global__ void __launch_bounds__(256) block_norm_join_kernel(const __grid_const
   if (j < a.width) {
     const float* p = a.sums + static_cast<int64_t>(blockIdx.y) * a.blocks * a.width + j;
 #pragma unroll 8
-    for (int k = r; k < a.blocks; k += 8) sum += __ldcg(p + k * a.width);
+    for (int k = r; k < a.blocks; k += kRuns) sum += __ldcg(p + k * a.width);
   }
   part[r][c] = sum;
   __syncthreads();
   if (r != 0 || j >= a.width) return;
 #pragma unroll
-  for (int k = 1; k < 8; ++k) sum += part[k][c];
+  for (int k = 1; k < kRuns; ++k) sum += part[k][c];
   if (a.out_f32) {
     float* o = static_cast<float*>(out) + j;
     *o = a.accumulate ? *o + sum : sum;
@@ -781,8 +847,8 @@ cudaError_t launch_block_norm_backward(const BlockNormLaunch& L) {
   j.accumulate = L.accumulate;
   // the sums of biases are the last ones
   const unsigned kinds = L.dbias != nullptr || L.dpost_bias != nullptr ? kSums : kDb;
-  return chain.launch(block_norm_join_kernel, dim3(static_cast<unsigned>((a.width + 31) / 32), kinds), 256, 0, 1,
-                      j);
+  return chain.launch(block_norm_join_kernel, dim3(static_cast<unsigned>((a.width + 31) / 32), kinds),
+                      32 * kRuns, 0, 1, j);
 }
 
 }  // namespace zeroadam
