@@ -753,8 +753,7 @@ template <typename Kernel>
 cudaError_t launch_ring(Kernel kernel, int64_t blocks, int threads, int smem, int cluster, const NormArgs& a,
                         Chain* chain) {
   if (smem > 40 * 1024) {
-    // (a property of the kernel on the current device, set alike by every call)
-    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMostRing);
+    const cudaError_t e = allow_shared(reinterpret_cast<const void*>(kernel), kMostRing);
     if (e != cudaSuccess) return e;
   }
   return chain->launch(kernel, dim3(static_cast<unsigned>(blocks * cluster)), threads, smem, cluster, a);

@@ -15,6 +15,46 @@ inline bool aligned(const void* p, uintptr_t k) {
   return (reinterpret_cast<uintptr_t>(p) & (k - 1)) == 0;
 }
 
+// The value that a function of the sizes has, from the last few that this thread asked for:
+// what it takes to work one out is host time of every call.
+template <typename Key, typename Value>
+struct Memo {
+  static constexpr int kKept = 8;
+  Key keys[kKept];
+  Value values[kKept];
+  int used = 0, next = 0;
+  template <typename F>
+  const Value& get(const Key& key, F f) {
+    for (int k = 0; k < used; ++k)
+      if (keys[k] == key) return values[k];
+    const int at = next;
+    next = (next + 1) % kKept;
+    if (used < kKept) ++used;
+    keys[at] = key;
+    values[at] = f();
+    return values[at];
+  }
+};
+
+// Lets a kernel use `bytes` of dynamic shared memory on the current device, once a thread.
+inline cudaError_t allow_shared(const void* kernel, int bytes) {
+  struct Allowed {
+    const void* kernel;
+    int device, bytes;
+  };
+  constexpr int kMost = 64;
+  static thread_local Allowed known[kMost];
+  static thread_local int count = 0;
+  int device = 0;
+  cudaError_t e = cudaGetDevice(&device);
+  if (e != cudaSuccess) return e;
+  for (int k = 0; k < count; ++k)
+    if (known[k].kernel == kernel && known[k].device == device && known[k].bytes >= bytes) return cudaSuccess;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess && count < kMost) known[count++] = {kernel, device, bytes};
+  return e;
+}
+
 // Takes pieces of the workspace in order.
 struct Space {
   char* at;

@@ -323,7 +323,15 @@ zero_linear_t linear_of(const zero_cross_entropy_t& s, int64_t rows) {
   return l;
 }
 
-Layout layout_of(const zero_cross_entropy_t& s, int32_t flags) {
+struct LayoutKey {
+  int64_t rows, width, vocab;
+  int32_t flags;
+  bool operator==(const LayoutKey& o) const {
+    return rows == o.rows && width == o.width && vocab == o.vocab && flags == o.flags;
+  }
+};
+
+Layout make_layout(const zero_cross_entropy_t& s, int32_t flags) {
   const bool grads = (flags & ZERO_LINEAR_BACKWARD) != 0;
   Layout l{};
   l.piece = piece_rows(s, grads);
@@ -356,6 +364,11 @@ Layout layout_of(const zero_cross_entropy_t& s, int32_t flags) {
   }
   l.bytes = at;
   return l;
+}
+
+Layout layout_of(const zero_cross_entropy_t& s, int32_t flags) {
+  static thread_local Memo<LayoutKey, Layout> memo;
+  return memo.get({s.rows, s.width, s.vocab, flags}, [&] { return make_layout(s, flags); });
 }
 
 }  // namespace

@@ -584,9 +584,7 @@ cudaError_t launch_scatter(const ScatterArgs& a, Chain* chain) {
   constexpr int smem = static_cast<int>(sizeof(ScatterShared)) + 128;
   static_assert(smem <= 113 * 1024, "two blocks an SM");
   const auto kernel = embedding_scatter_kernel<VEC>;
-  // (a property of the kernel on the current device, set alike by every call)
-  const cudaError_t e =
-      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  const cudaError_t e = allow_shared(reinterpret_cast<const void*>(kernel), smem);
   if (e != cudaSuccess) return e;
   const int64_t blocks = int64_t{a.classes} * a.slices;
   if (blocks > INT32_MAX) return cudaErrorInvalidValue;

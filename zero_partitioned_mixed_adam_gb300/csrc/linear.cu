@@ -1297,8 +1297,25 @@ cudaError_t make_out_map(CUtensorMap* map, const void* p, int64_t rows, int64_t 
 // ----------------------------------------------------------------- products
 
 // Exponentials of a product's rows (kExponent).
+struct SizesKey {
+  int64_t rows, in, out;
+  int32_t which;
+  bool operator==(const SizesKey& o) const {
+    return rows == o.rows && in == o.in && out == o.out && which == o.which;
+  }
+};
 Plan plan_exponents(int64_t rows, int64_t vocab, int64_t width) {
-  return plan_product(rows, vocab, width, false, false, nullptr, true, 1);
+  static thread_local Memo<SizesKey, Plan> memo;
+  return memo.get({rows, width, vocab, 0},
+                  [&] { return plan_product(rows, vocab, width, false, false, nullptr, true, 1); });
+}
+BackwardPlan known_plan_backward(const zero_linear_t& s, bool dx, bool dw) {
+  static thread_local Memo<SizesKey, BackwardPlan> memo;
+  return memo.get({s.rows, s.in, s.out, (dx ? 1 : 0) | (dw ? 2 : 0)}, [&] { return plan_backward(s, dx, dw); });
+}
+Plan known_plan_forward(const zero_linear_t& s) {
+  static thread_local Memo<SizesKey, Plan> memo;
+  return memo.get({s.rows, s.in, s.out, 0}, [&] { return plan_forward(s); });
 }
 
 // D[rows, cols] over `depth`; a_mn / b_mn: the operand is stored [depth, rows]
@@ -1760,11 +1777,11 @@ int64_t linear_workspace(const zero_linear_t& s, int32_t flags) {
   const int64_t w = in_place ? 0 : copy_bytes(Stored(nullptr, s.out, s.in, 0));
   const int64_t bias = in_place ? 0 : copy_bytes(Stored(nullptr, 1, s.out, 0));
   if ((flags & ZERO_LINEAR_BACKWARD) == 0)
-    return s.rows <= kFewRows ? 0 : x + w + bias + round_up(plan_forward(s).part_bytes(), 256);
+    return s.rows <= kFewRows ? 0 : x + w + bias + round_up(known_plan_forward(s).part_bytes(), 256);
   const bool dz = !in_place || (flags & ZERO_LINEAR_PLAIN) == 0;
   // the two products' parts, side by side; either may be wanted alone
-  const BackwardPlan both = plan_backward(s, true, true), one = plan_backward(s, true, false),
-                     two = plan_backward(s, false, true);
+  const BackwardPlan both = known_plan_backward(s, true, true), one = known_plan_backward(s, true, false),
+                     two = known_plan_backward(s, false, true);
   auto most = [](int64_t x, int64_t y) { return x > y ? x : y; };
   return (dz ? copy_bytes(Stored(nullptr, s.rows, s.out, 0)) : 0) + w + x +
          round_up(slope_blocks(s.rows, s.out) * round_up4(s.out) * 4, 256) +
@@ -1800,7 +1817,7 @@ cudaError_t launch_linear_forward(const LinearForwardLaunch& L) {
   p.e.bias = bias.p;
   Pending w;
   if (e == cudaSuccess)
-    e = launch_product(p, plan_forward(s), false, &space, L.withhold, &chain, &w);
+    e = launch_product(p, known_plan_forward(s), false, &space, L.withhold, &chain, &w);
   return e == cudaSuccess ? launch_join(w, &chain) : e;
 }
 
@@ -1873,7 +1890,7 @@ cudaError_t launch_linear_backward(const LinearBackwardLaunch& L) {
     if (e == cudaSuccess && L.dbias != nullptr) e = launch_dbias(dbias, &chain);
     if (e != cudaSuccess) return e;
   }
-  const BackwardPlan plan = plan_backward(s, L.dx != nullptr, L.dw != nullptr);
+  const BackwardPlan plan = known_plan_backward(s, L.dx != nullptr, L.dw != nullptr);
   Pending dx{}, dw{};
   dx.plan.splits = dw.plan.splits = 1;
   if (L.dx != nullptr) {

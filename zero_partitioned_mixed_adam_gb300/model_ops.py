@@ -17,6 +17,8 @@ from . import (ZERO_GRAD_ACCUMULATE, ZERO_GRAD_F32, ZERO_IDS_I32, ZERO_LINEAR_AL
                ZeroError, _addr, _lib, _stream_handle)
 from .train_ops import _BF16, _GRADS, _matrix, _vector
 
+_B = torch.bfloat16
+
 
 class ZeroEmbedding(ctypes.Structure):
     """zero_embedding_t: sizes and row pitches of a table and the rows looked up in it."""
@@ -61,16 +63,37 @@ _declare(_lib)
 _IDS = (torch.int64, torch.int32)
 
 
-def _here(stream, *tensors):
+def _current_device() -> int:
+    """The current device's number, without initializing CUDA."""
+    return torch._C._cuda_getDevice() if torch.cuda.is_initialized() else 0
+
+
+def _here(stream, tensors):
     """Refuses tensors and streams that are not of the current CUDA device, on which the
     library launches."""
-    here = torch.cuda.current_device() if torch.cuda.is_initialized() else 0
+    here = _current_device()
     for t in tensors:
         if t is not None and t.get_device() != here:
             raise ValueError(f"expected tensors of the current device, cuda:{here}, not of {t.device}")
-    of = getattr(stream, "device", None)
-    if of is not None and of.index != here:
-        raise ValueError(f"the tensors are on cuda:{here}, the stream on {of}")
+    if stream is not None and not isinstance(stream, int) and stream.device.index != here:
+        raise ValueError(f"the tensors are on cuda:{here}, the stream on {stream.device}")
+
+
+def _rows(name, t, shape):
+    """_matrix for bf16, of a shape."""
+    if t.shape != shape or t.dtype is not _B:
+        _matrix(name, t, *shape)  # (says what is wrong)
+    pitch, step = t.stride()
+    rows, cols = shape
+    if step != 1 and cols > 1:
+        _matrix(name, t, rows, cols)
+    return pitch if rows > 1 else max(cols, pitch)
+
+
+def _columns(name, t, shape):
+    """_vector for bf16, of a shape."""
+    if t.shape != shape or t.dtype is not _B or not t.is_contiguous():
+        _vector(name, t, shape[0])
 
 
 def _workspace(need, what, workspace, device, stream):
@@ -112,7 +135,7 @@ def zero_embedding_forward(ids, table, y, *, scale: float = 1.0, stream=None) ->
     """y[i] = scale * table[ids[i]] for ids [rows] (int64 or int32), table [vocab, width] and
     y [rows, width], bf16 with contiguous columns.  Ids outside the table give rows of NaN."""
     s, flags = _embedding(ids, table, y, "table", _BF16)
-    _here(stream, ids, table, y)
+    _here(stream, (ids, table, y))
     _check(_lib.zero_embedding_forward(ctypes.byref(s), _addr(table), _addr(ids), flags, scale, _addr(y),
                                        _stream_handle(stream)), "zero_embedding_forward")
 
@@ -125,7 +148,7 @@ def zero_embedding_backward(dy, ids, dtable, *, scale: float = 1.0, padding=None
     s, flags = _embedding(ids, dtable, dy, "dtable", _GRADS)
     flags |= ZERO_GRAD_F32 if dtable.dtype == torch.float32 else 0
     flags |= ZERO_GRAD_ACCUMULATE if accumulate else 0
-    _here(stream, dy, ids, dtable)
+    _here(stream, (dy, ids, dtable))
     _check(_lib.zero_embedding_backward(ctypes.byref(s), _addr(dy), _addr(ids), flags, scale,
                                         -1 if padding is None else padding, _addr(dtable),
                                         _stream_handle(stream)), "zero_embedding_backward")
@@ -176,7 +199,7 @@ def zero_linear_cross_entropy(x, w, targets, losses=None, total=None, *, dx=None
         s.lddw = _matrix("dw", dw, vocab, width, _GRADS)
         flags |= ZERO_GRAD_F32 if dw.dtype == torch.float32 else 0
     flags |= ZERO_GRAD_ACCUMULATE if accumulate else 0
-    _here(stream, x, w, targets, losses, total, scale, dx, dw, workspace)
+    _here(stream, (x, w, targets, losses, total, scale, dx, dw, workspace))
     need = 0
     if workspace is None:
         kind = (ZERO_LINEAR_BACKWARD if dx is not None or dw is not None else 0) | (flags & ZERO_GRAD_F32)
@@ -192,18 +215,28 @@ def zero_linear_cross_entropy(x, w, targets, losses=None, total=None, *, dx=None
 
 # -------------------------------------------------------------------- block norms
 
-def _block_norm(rows, width, post, kind, alpha, eps, h, gate, vectors):
+def _pointer(t):
+    return None if t is None else t.data_ptr()
+
+
+def _block_norm(shape, post, kind, alpha, eps, h, gate, w1, b1, w):
+    """The sizes with the pitches of h and gate; the vectors checked."""
+    rows, width = shape
     s = ZeroBlockNorm(rows, width, post, kind, alpha, eps)
     if h is not None:
-        s.ldh = _matrix("h", h, rows, width)
+        s.ldh = _rows("h", h, shape)
+    one = (width,)
     if gate is not None:
         if gate.dim() == 1:
-            _vector("gate", gate, width)
+            _columns("gate", gate, one)
         else:
-            s.ldg = max(_matrix("gate", gate, rows, width), width)
-    for name, t in vectors.items():
-        if t is not None:
-            _vector(name, t, width)
+            s.ldg = max(_rows("gate", gate, shape), width)
+    if w1 is not None:
+        _columns("post_weight", w1, one)
+    if b1 is not None:
+        _columns("post_bias", b1, one)
+    if w is not None:
+        _columns("weight", w, one)
     return s
 
 
@@ -218,17 +251,19 @@ def zero_block_norm_forward(r, y, *, h=None, s=None, post: int = ZERO_NORM_NONE,
     s may be r itself, or None where only y is wanted."""
     if r.dim() != 2:
         raise ValueError("r is a matrix")
-    rows, width = r.shape
-    z = _block_norm(rows, width, post, kind, alpha, eps, h, gate,
-                    {"post_weight": post_weight, "post_bias": post_bias, "weight": weight, "bias": bias})
-    z.ldr = _matrix("r", r, rows, width)
-    z.ldy = _matrix("y", y, rows, width)
+    shape = r.shape
+    z = _block_norm(shape, post, kind, alpha, eps, h, gate, post_weight, post_bias, weight)
+    if bias is not None:
+        _columns("bias", bias, (shape[1],))
+    z.ldr = _rows("r", r, shape)
+    z.ldy = _rows("y", y, shape)
     if s is not None:
-        z.lds = _matrix("s", s, rows, width)
-    _here(stream, r, y, h, s, post_weight, post_bias, gate, weight, bias)
-    _check(_lib.zero_block_norm_forward(ctypes.byref(z), _addr(r), _addr(h), _addr(post_weight),
-                                        _addr(post_bias), _addr(gate), _addr(weight), _addr(bias), _addr(s),
-                                        _addr(y), _stream_handle(stream)), "zero_block_norm_forward")
+        z.lds = _rows("s", s, shape)
+    _here(stream, (r, y, h, s, post_weight, post_bias, gate, weight, bias))
+    _check(_lib.zero_block_norm_forward(ctypes.byref(z), _pointer(r), _pointer(h), _pointer(post_weight),
+                                        _pointer(post_bias), _pointer(gate), _pointer(weight), _pointer(bias),
+                                        _pointer(s), _pointer(y), _stream_handle(stream)),
+           "zero_block_norm_forward")
 
 
 def zero_block_norm_workspace(rows: int, width: int) -> int:
@@ -251,37 +286,42 @@ def zero_block_norm_backward(dy, s, *, ds=None, h=None, post: int = ZERO_NORM_NO
     dgate are bf16 or fp32, all alike, and added to with accumulate=True.  dr may be ds itself."""
     if dy.dim() != 2:
         raise ValueError("dy is a matrix")
-    rows, width = dy.shape
-    z = _block_norm(rows, width, post, kind, alpha, eps, h, gate,
-                    {"post_weight": post_weight, "post_bias": post_bias, "weight": weight})
-    z.lddy = _matrix("dy", dy, rows, width)
-    z.lds = _matrix("s", s, rows, width)
-    for name, t in (("ds", ds), ("dr", dr), ("dh", dh)):
-        if t is not None:
-            setattr(z, "ld" + name, _matrix(name, t, rows, width))
-    sums = {"dpost_weight": dpost_weight, "dpost_bias": dpost_bias, "dweight": dweight, "dbias": dbias}
+    shape = dy.shape
+    z = _block_norm(shape, post, kind, alpha, eps, h, gate, post_weight, post_bias, weight)
+    z.lddy = _rows("dy", dy, shape)
+    z.lds = _rows("s", s, shape)
+    if ds is not None:
+        z.ldds = _rows("ds", ds, shape)
+    if dr is not None:
+        z.lddr = _rows("dr", dr, shape)
+    if dh is not None:
+        z.lddh = _rows("dh", dh, shape)
+    vectors = (dpost_weight, dpost_bias, dweight, dbias, dgate)
     if dgate is not None:
         if gate is None or dgate.dim() != gate.dim():
             raise ValueError("dgate is of gate's shape")
-        if gate.dim() == 1:
-            sums["dgate"] = dgate
-        else:
-            z.lddg = max(_matrix("dgate", dgate, rows, width), width)
-    kinds = {t.dtype for t in sums.values() if t is not None}
-    if len(kinds) > 1:
-        raise ValueError("the gradients of vectors are bf16 or fp32, all alike")
-    for name, t in sums.items():
-        if t is not None:
-            _vector(name, t, width, _GRADS)
-    flags = (ZERO_GRAD_F32 if kinds == {torch.float32} else 0) | (ZERO_GRAD_ACCUMULATE if accumulate else 0)
-    _here(stream, dy, s, ds, h, post_weight, post_bias, gate, weight, dr, dh, dgate, dpost_weight,
-          dpost_bias, dweight, dbias, workspace)
-    need = _lib.zero_block_norm_workspace(ctypes.byref(z)) if workspace is None else 0
+        if gate.dim() == 2:
+            z.lddg = max(_rows("dgate", dgate, shape), shape[1])
+            vectors = vectors[:4]
+    kind_of = None
+    for t in vectors:
+        if t is None:
+            continue
+        if t.shape != (shape[1],) or t.dtype not in _GRADS or not t.is_contiguous():
+            _vector("a vector's gradient", t, shape[1], _GRADS)
+        if kind_of is not None and t.dtype is not kind_of:
+            raise ValueError("the gradients of vectors are bf16 or fp32, all alike")
+        kind_of = t.dtype
+    flags = (ZERO_GRAD_F32 if kind_of is torch.float32 else 0) | (ZERO_GRAD_ACCUMULATE if accumulate else 0)
+    _here(stream, (dy, s, ds, h, post_weight, post_bias, gate, weight, dr, dh, dgate, dpost_weight,
+                   dpost_bias, dweight, dbias, workspace))
+    at = ctypes.byref(z)
+    need = _lib.zero_block_norm_workspace(at) if workspace is None else 0
     workspace, nbytes = _workspace(need, "zero_block_norm_workspace", workspace, dy.device, stream)
     _check(_lib.zero_block_norm_backward(
-        ctypes.byref(z), _addr(dy), _addr(ds), _addr(s), _addr(h), _addr(post_weight), _addr(post_bias),
-        _addr(gate), _addr(weight), _addr(dr), _addr(dh), _addr(dgate), _addr(dpost_weight),
-        _addr(dpost_bias), _addr(dweight), _addr(dbias), flags, _addr(workspace), nbytes,
+        at, _pointer(dy), _pointer(ds), _pointer(s), _pointer(h), _pointer(post_weight), _pointer(post_bias),
+        _pointer(gate), _pointer(weight), _pointer(dr), _pointer(dh), _pointer(dgate), _pointer(dpost_weight),
+        _pointer(dpost_bias), _pointer(dweight), _pointer(dbias), flags, _pointer(workspace), nbytes,
         _stream_handle(stream)), "zero_block_norm_backward")
 
 
