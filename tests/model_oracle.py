@@ -35,10 +35,10 @@ def embedding_grad(dy, ids, vocab, scale=1.0, padding=None):
 
 
 def standardized(x, kind, eps):
-    """(x standardized, its root)."""
+    """(x standardized along its last dimension, the root)."""
     if kind == "layer":
-        x = x - x.mean(1, keepdim=True)
-    root = (x.square().mean(1, keepdim=True) + eps).sqrt()
+        x = x - x.mean(-1, keepdim=True)
+    root = (x.square().mean(-1, keepdim=True) + eps).sqrt()
     return x / root, root
 
 

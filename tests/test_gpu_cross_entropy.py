@@ -79,7 +79,18 @@ def check(x, w, t, *, scale=None, dtype=BF, add=False, dx=None, dw=None, ignore=
     half = 2.0 ** -8 if dw.dtype == BF else 2.0 ** -23
     near(dw, want, tol_dw + half * (want.abs() + tol_dw) + 1e-30, "dw")
     assert za.device_status() == za.ZERO_OK
+    check_alone(x, w, t, ref, scale=scale, ignore_index=ignore)
     return losses, total, dx, dw, ref
+
+
+def check_alone(x, w, t, ref, **kw):
+    """The loss without gradients, which other kernels compute: each exponential once less the
+    largest logit and once more less the target's, so twice the error of the sum."""
+    losses, total = torch.full(t.shape, 7.0, device="cuda"), torch.full((1,), 7.0, device="cuda")
+    za.zero_linear_cross_entropy(x, w, t, losses, total, **kw)
+    tol = tolerances(x, w, ref)[0] + 2.0 ** -17 * -torch.expm1(-ref[0])
+    near(losses, ref[0], tol, "losses alone")
+    near(total, ref[1], (tol * ref[6].abs()).sum() + 2.0 ** -22 * (ref[6] * ref[0]).abs().sum(), "total alone")
 
 
 @pytest.mark.parametrize("shape", SHAPES)
@@ -119,13 +130,16 @@ def test_parts_alone():
     m, k, v = 150, 96, 700
     x, w, t = matrix(m, k, 1.0, 1), matrix(v, k, 0.2, 2), targets_of(m, v, 3, 0.1)
     losses, total, dx, dw, _ = check(x, w, t)
-    for name, want in (("losses", losses), ("total", total), ("dx", dx), ("dw", dw)):
+    for name, want in (("dx", dx), ("dw", dw)):
         got = torch.full_like(want, 7.0)
         za.zero_linear_cross_entropy(x, w, t, **{name: got})
         assert torch.equal(got, want), name
     alone = [torch.full_like(losses, 7.0), torch.full_like(total, 7.0)]
     za.zero_linear_cross_entropy(x, w, t, *alone)     # no gradients
-    assert torch.equal(alone[0], losses) and torch.equal(alone[1], total)
+    for name, want in (("losses", alone[0]), ("total", alone[1])):
+        got = torch.full_like(want, 7.0)
+        za.zero_linear_cross_entropy(x, w, t, **{name: got})
+        assert torch.equal(got, want), name
 
 
 @pytest.mark.parametrize("rows", [3, 140])
@@ -171,8 +185,12 @@ def test_every_row_ignored():
     x = torch.full((m, k), float("nan"), device="cuda", dtype=BF)
     losses, total, dx, dw = (torch.full(s, 7.0, device="cuda") for s in ((m,), (1,), (m, k), (v, k)))
     dx = dx.to(BF)
-    za.zero_linear_cross_entropy(x, matrix(v, k, 1.0, 2), t, losses, total, dx=dx, dw=dw, ignore_index=5)
+    w = matrix(v, k, 1.0, 2)
+    za.zero_linear_cross_entropy(x, w, t, losses, total, dx=dx, dw=dw, ignore_index=5)
     assert not any(a.any() for a in (losses, total, dx, dw))
+    losses.fill_(7.0), total.fill_(7.0)
+    za.zero_linear_cross_entropy(x, w, t, losses, total, ignore_index=5)
+    assert not losses.any() and not total.any()
 
 
 def test_no_rows():
@@ -196,6 +214,9 @@ def test_targets_that_are_no_column(bad):
     assert losses[7].isnan() and total.isnan().all() and dx[7].isnan().all()
     others = torch.arange(m, device="cuda") != 7
     assert ((losses - want).abs() < 1e-4)[others].all() and torch.isfinite(dx[others]).all()
+    losses.fill_(7.0), total.fill_(7.0)
+    za.zero_linear_cross_entropy(x, w, t, losses, total)
+    assert losses[7].isnan() and total.isnan().all() and ((losses - want).abs() < 1e-4)[others].all()
 
 
 @pytest.mark.parametrize("value", [float("inf"), float("-inf"), float("nan")])
@@ -208,6 +229,9 @@ def test_rows_that_are_not_finite(value):
     others = torch.arange(m, device="cuda") != 5
     assert not torch.isfinite(losses[5]) and not torch.isfinite(dx[5]).any()
     assert torch.isfinite(losses[others]).all() and torch.isfinite(dx[others]).all()
+    alone = torch.zeros(m, device="cuda")
+    za.zero_linear_cross_entropy(x, w, t, alone)
+    assert not torch.isfinite(alone[5]) and torch.isfinite(alone[others]).all()
 
 
 @pytest.mark.parametrize("dtype,add", [(BF, False), (BF, True), (F32, True)])
@@ -242,9 +266,10 @@ def test_streams_and_graphs():
     za.zero_linear_cross_entropy(x, w, t, out[0], out[1], dx=out[2], dw=out[3], workspace=ws, stream=side)
     torch.cuda.current_stream().wait_stream(side)
     assert all(torch.equal(a, b) for a, b in zip(out, want))
-    graph = torch.cuda.CUDAGraph()
+    graph, alone = torch.cuda.CUDAGraph(), torch.zeros(m, device="cuda")
     with torch.cuda.graph(graph):
         za.zero_linear_cross_entropy(x, w, t, out[0], out[1], dx=out[2], dw=out[3])
+        za.zero_linear_cross_entropy(x, w, t, alone)
     x.copy_(matrix(m, k, 4.0, 11))          # among them rows that need another reference
     w.copy_(matrix(v, k, 1.0, 12))
     t.copy_(targets_of(m, v, 13, 0.3))
@@ -252,6 +277,9 @@ def test_streams_and_graphs():
     graph.replay()
     want = check(x, w, t)[:4]
     assert all(torch.equal(a, b) for a, b in zip(out, want))
+    again = torch.zeros_like(alone)
+    za.zero_linear_cross_entropy(x, w, t, again)
+    assert torch.equal(alone, again)
 
 
 def test_withheld_copies_are_reported():

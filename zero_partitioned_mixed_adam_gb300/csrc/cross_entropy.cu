@@ -19,6 +19,10 @@
 //   product   (linear.cu) exponentials
 //   finish    losses, dz;  product and finish again, where some row needs it
 //   products  (linear.cu) dx = dz W, dw = dz^T x
+// The loss alone needs neither reference nor x laid out: its product takes the exponentials
+// less the largest logit so far, and a warp a row ends it.  The target's logit is a dot
+// product of its own there too, rounded to nearest: the tensor cores cut off, and what
+// that takes from one logit of 12 is 10 times the loss's other errors.
 #include "chain.cuh"
 #include "internal.h"
 #include "linear_epilogue.cuh"
@@ -33,10 +37,9 @@ constexpr float kOneMore = 17592186044416.0f;    // 2^44: a sum that asks for an
 
 // Words of the workspace that a call's kernels share.
 struct Words {
+  int32_t ticket;  // blocks of a kernel that are done
   int32_t again;   // some row of this piece wants another reference
-  int32_t ticket;  // blocks of the last kernel that are done
-  int32_t valid;   // rows that are not ignored, of all pieces
-  float share;     // 1 / valid: c of the mean (0 where there is none)
+  float share;     // 1 / rows that are not ignored: c of the mean (0 where there is none)
 };
 
 struct LossArgs {
@@ -57,8 +60,8 @@ struct LossArgs {
   int32_t parts;
   const float* scale;     // [all_rows] or NULL
   float* losses;          // [all_rows]
-  float* total;           // NULL: not wanted, or not the last piece
-  uint16_t* held;         // [rows][ldz]: 16 bits, then dz; NULL: no gradients
+  float* total;           // NULL: not wanted, or this is not the last piece
+  uint16_t* held;         // [rows][ldz]: 16 bits, then dz
   int64_t ldz;
   int32_t vec;            // x and w are read in vectors
 };
@@ -68,72 +71,65 @@ __device__ __forceinline__ int64_t target_of(const LossArgs& a, int64_t i) {
                    : static_cast<const int64_t*>(a.targets)[i];
 }
 
-// Counts the rows that are not ignored, and sets the words.  One block: it runs beside
-// the rows' kernel (8,192 targets take it 3 us).
-__global__ void __launch_bounds__(1024) loss_count_kernel(const __grid_constant__ LossArgs a) {
-  __shared__ int32_t part[32];
-  wait_for_predecessor();
-  launch_dependents();
-  int32_t n = 0;
-  if (a.scale == nullptr)
-    for (int64_t i = threadIdx.x; i < a.all_rows; i += 1024) n += target_of(a, i) != a.ignore;
-  n = __reduce_add_sync(0xffffffffu, n);
-  if (threadIdx.x % 32 == 0) part[threadIdx.x / 32] = n;
-  __syncthreads();
-  if (threadIdx.x < 32) {
-    n = __reduce_add_sync(0xffffffffu, part[threadIdx.x]);
-    if (threadIdx.x == 0) *a.words = Words{0, 0, n, n > 0 ? 1.0f / static_cast<float>(n) : 0.0f};
-  }
-}
-
 __device__ __forceinline__ float warp_sum(float x) {
 #pragma unroll
   for (int k = 16; k > 0; k /= 2) x += __shfl_xor_sync(0xffffffffu, x, k);
   return x;
 }
 
+// A lane's part of the product of two rows of bf16; f(j, v) is given x's vectors or elements.
+template <bool VEC, typename F>
+__device__ __forceinline__ float dot_part(const uint16_t* x, const uint16_t* w, int64_t width, int lane, F f) {
+  float sum = 0.0f;
+  if constexpr (VEC) {
+    for (int64_t j = 8 * lane; j < width; j += 256) {
+      if (j + 8 <= width) {
+        const uint4 v = __ldg(reinterpret_cast<const uint4*>(x + j));
+        float p[8], q[8];
+        bf16x8(v, p);
+        bf16x8(__ldg(reinterpret_cast<const uint4*>(w + j)), q);
+#pragma unroll
+        for (int c = 0; c < 8; ++c) sum = fmaf(p[c], q[c], sum);
+        f(j, v);
+      } else {
+        for (int64_t k = j; k < width; ++k) {
+          sum = fmaf(bf16_at(x + k), bf16_at(w + k), sum);
+          f(k, x[k]);
+        }
+      }
+    }
+  } else {
+    for (int64_t j = lane; j < width; j += 32) {
+      sum = fmaf(bf16_at(x + j), bf16_at(w + j), sum);
+      f(j, x[j]);
+    }
+  }
+  return sum;
+}
+
 // A warp a row: the target's logit, and x laid out for TMA, an ignored row's as zeros
 // (its x may hold anything, and 0 times an infinity would reach dw).
 template <bool VEC>
 __global__ void __launch_bounds__(256) loss_rows_kernel(const __grid_constant__ LossArgs a) {
-  // The first piece's rows do not wait for the count, whose kernel let this one begin when
-  // all that came before was complete.
-  if (a.first > 0) wait_for_predecessor();
+  wait_for_predecessor();
   launch_dependents();
+  if (blockIdx.x == 0 && threadIdx.x == 0) *a.words = Words{0, 0, 0.0f};
   const int lane = threadIdx.x % 32;
   for (int64_t i = static_cast<int64_t>(blockIdx.x) * 8 + threadIdx.x / 32; i < a.rows;
        i += static_cast<int64_t>(gridDim.x) * 8) {
     const int64_t t = target_of(a, a.first + i);
     const bool ignored = t == a.ignore, column = !ignored && t >= 0 && t < a.vocab;
-    const uint16_t* x = a.x + (a.first + i) * a.ldx;
-    const uint16_t* w = a.w + (column ? t : 0) * a.ldw;
     uint16_t* to = a.xc + i * a.ldxc;
     float sum = 0.0f;
-    if constexpr (VEC) {
-      for (int64_t j = 8 * lane; j < a.width; j += 256) {
-        uint4 v = make_uint4(0, 0, 0, 0);
-        if (j + 8 <= a.width) {
-          if (!ignored) v = *reinterpret_cast<const uint4*>(x + j);
-          if (column) {
-            float p[8], q[8];
-            bf16x8(v, p);
-            bf16x8(__ldg(reinterpret_cast<const uint4*>(w + j)), q);
-#pragma unroll
-            for (int c = 0; c < 8; ++c) sum = fmaf(p[c], q[c], sum);
-          }
-          *reinterpret_cast<uint4*>(to + j) = v;
-        } else {
-          for (int64_t k = j; k < a.width; ++k) {
-            to[k] = ignored ? 0 : x[k];
-            if (column) sum = fmaf(bf16_at(x + k), bf16_at(w + k), sum);
-          }
-        }
-      }
+    if (ignored) {  // (the pitch has room for whole vectors)
+      for (int64_t j = 8 * lane; j < a.width; j += 256) *reinterpret_cast<uint4*>(to + j) = make_uint4(0, 0, 0, 0);
     } else {
-      for (int64_t j = lane; j < a.width; j += 32) {
-        to[j] = ignored ? 0 : x[j];
-        if (column) sum = fmaf(bf16_at(x + j), bf16_at(w + j), sum);
-      }
+      struct Put {
+        uint16_t* to;
+        __device__ __forceinline__ void operator()(int64_t j, uint4 v) const { *reinterpret_cast<uint4*>(to + j) = v; }
+        __device__ __forceinline__ void operator()(int64_t j, uint16_t v) const { to[j] = v; }
+      };
+      sum = dot_part<VEC>(a.x + (a.first + i) * a.ldx, a.w + (column ? t : 0) * a.ldw, a.width, lane, Put{to});
     }
     sum = warp_sum(sum);
     if (lane == 0) {
@@ -143,10 +139,104 @@ __global__ void __launch_bounds__(256) loss_rows_kernel(const __grid_constant__ 
       a.column[i] = column ? static_cast<int32_t>(t) : ignored ? -1 : -2;
     }
   }
-  if (a.first == 0) wait_for_predecessor();
 }
 
 constexpr int kFinishThreads = 256, kFinishWarps = kFinishThreads / 32;
+
+// Whether this is the last of the grid's blocks; all that the others wrote can be read then.
+__device__ __forceinline__ bool last_block(Words* words, int32_t* shared) {
+  __threadfence();
+  __syncthreads();
+  if (threadIdx.x == 0) *shared = atomicAdd(&words->ticket, 1) == static_cast<int32_t>(gridDim.x) - 1;
+  __syncthreads();
+  __threadfence();
+  return *shared != 0;
+}
+
+// The rows that count, and with `sums` their losses' sum, of all pieces: in 64 bits, in an order
+// that follows from the sizes.  A whole block.
+__device__ __forceinline__ void total_losses(const LossArgs& a, bool sums) {
+  __shared__ double sum_part[kFinishWarps];
+  __shared__ int32_t count_part[kFinishWarps];
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  double total = 0.0;
+  int32_t valid = 0;
+  constexpr int U = 8;
+  for (int64_t i0 = threadIdx.x; i0 < a.all_rows; i0 += U * kFinishThreads) {
+    float x[U], c[U];
+    int64_t t[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int64_t i = i0 + u * kFinishThreads < a.all_rows ? i0 + u * kFinishThreads : i0;
+      t[u] = target_of(a, i);
+      x[u] = sums ? __ldcg(a.losses + i) : 0.0f;
+      c[u] = a.scale != nullptr ? __ldg(a.scale + i) : 1.0f;
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (i0 + u * kFinishThreads < a.all_rows && t[u] != a.ignore) {
+        ++valid;
+        total += static_cast<double>(c[u]) * static_cast<double>(x[u]);
+      }
+  }
+#pragma unroll
+  for (int k = 16; k > 0; k /= 2) total += __shfl_xor_sync(0xffffffffu, total, k);
+  valid = __reduce_add_sync(0xffffffffu, valid);
+  if (lane == 0) {
+    sum_part[warp] = total;
+    count_part[warp] = valid;
+  }
+  __syncthreads();
+  if (threadIdx.x != 0) return;
+  total = 0.0;
+  valid = 0;
+  for (int k = 0; k < kFinishWarps; ++k) {
+    total += sum_part[k];
+    valid += count_part[k];
+  }
+  a.words->share = valid > 0 ? 1.0f / static_cast<float>(valid) : 0.0f;
+  if (a.scale == nullptr) total = valid > 0 ? total / valid : 0.0;
+  if (sums) *a.total = static_cast<float>(total);
+}
+
+// The loss alone, a warp a row: of parts less their own largest logit.
+template <bool VEC>
+__global__ void __launch_bounds__(kFinishThreads) loss_alone_kernel(const __grid_constant__ LossArgs a) {
+  __shared__ int32_t last;
+  wait_for_predecessor();
+  launch_dependents();
+  const int lane = threadIdx.x % 32;
+  for (int64_t i = static_cast<int64_t>(blockIdx.x) * kFinishWarps + threadIdx.x / 32; i < a.rows;
+       i += static_cast<int64_t>(gridDim.x) * kFinishWarps) {
+    const int64_t t = target_of(a, a.first + i);
+    const bool column = t >= 0 && t < a.vocab;
+    if (t == a.ignore || !column) {
+      if (lane == 0) a.losses[a.first + i] = t == a.ignore ? 0.0f : NAN;
+      continue;
+    }
+    struct Nothing {
+      __device__ __forceinline__ void operator()(int64_t, uint4) const {}
+      __device__ __forceinline__ void operator()(int64_t, uint16_t) const {}
+    };
+    const float zt = warp_sum(dot_part<VEC>(a.x + (a.first + i) * a.ldx, a.w + t * a.ldw, a.width, lane, Nothing{}));
+    const float2* parts = a.sums + i * a.parts;
+    float top = zt;
+    for (int k = lane; k < a.parts; k += 32) top = fmaxf(top, __ldcg(parts + k).y);
+#pragma unroll
+    for (int k = 16; k > 0; k /= 2) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, k));
+    // less the target's logit, where that leaves fp32's range alone
+    const bool own = top - zt < 80.0f;
+    const float ref = own ? zt : top;
+    float sum = 0.0f;
+    for (int k = lane; k < a.parts; k += 32) {
+      const float2 s = __ldcg(parts + k);
+      if (s.x != 0.0f) sum += s.x * expf(s.y - ref);
+    }
+    sum = warp_sum(sum);
+    if (lane == 0) a.losses[a.first + i] = own ? log1pf(sum) : (ref - zt) + logf(sum + expf(zt - ref));
+  }
+  if (a.total != nullptr && last_block(a.words, &last)) total_losses(a, true);
+}
 
 // A block a row: the row's sums in the order of its parts, its loss, and dz.  With c alike
 // for all rows (the mean) dz is p less the target's 1, whose rounding is nothing where p is
@@ -156,7 +246,6 @@ constexpr int kFinishThreads = 256, kFinishWarps = kFinishThreads / 32;
 template <bool AGAIN>
 __global__ void __launch_bounds__(kFinishThreads) loss_finish_kernel(const __grid_constant__ LossArgs a) {
   __shared__ float2 part[kFinishWarps];
-  __shared__ double sum_part[kFinishWarps];
   __shared__ int32_t last;
   wait_for_predecessor();
   launch_dependents();
@@ -201,7 +290,6 @@ __global__ void __launch_bounds__(kFinishThreads) loss_finish_kernel(const __gri
         a.words->again = 1;
       }
     }
-    if (a.held == nullptr) continue;
     // (the pitch has room for whole vectors; an ignored row's are not read)
     uint16_t* row = a.held + i * a.ldz;
     constexpr int kSpan = 8 * kFinishThreads, U = 2;
@@ -234,53 +322,10 @@ __global__ void __launch_bounds__(kFinishThreads) loss_finish_kernel(const __gri
       }
     }
   }
-  if (a.total == nullptr) return;
-  __threadfence();
-  __syncthreads();
-  if (threadIdx.x == 0) last = atomicAdd(&a.words->ticket, 1) == static_cast<int32_t>(gridDim.x) - 1;
-  __syncthreads();
-  if (!last) return;
-  __threadfence();
-  if (!AGAIN) {
-    if (threadIdx.x == 0) a.words->ticket = 0;
-    if (__ldcg(&a.words->again) != 0) return;  // there are other losses to come
-  }
-  // in 64 bits, a thread's own in chains of 8
-  double total = 0.0;
-  constexpr int U = 8;
-  for (int64_t i0 = threadIdx.x; i0 < a.all_rows; i0 += U * kFinishThreads) {
-    float x[U];
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int64_t i = i0 + u * kFinishThreads;
-      x[u] = i < a.all_rows ? __ldcg(a.losses + i) : 0.0f;
-      if (a.scale != nullptr && i < a.all_rows && target_of(a, i) != a.ignore)
-        total += static_cast<double>(__ldg(a.scale + i)) * static_cast<double>(x[u]);
-    }
-    if (a.scale == nullptr) {
-#pragma unroll
-      for (int u = 0; u < U; ++u) total += static_cast<double>(x[u]);
-    }
-  }
-#pragma unroll
-  for (int k = 16; k > 0; k /= 2) total += __shfl_xor_sync(0xffffffffu, total, k);
-  if (lane == 0) sum_part[warp] = total;
-  __syncthreads();
-  if (threadIdx.x != 0) return;
-  total = 0.0;
-  for (int k = 0; k < kFinishWarps; ++k) total += sum_part[k];
-  if (a.scale == nullptr) {
-    const int32_t valid = __ldcg(&a.words->valid);
-    total = valid > 0 ? total / valid : 0.0;
-  }
-  *a.total = static_cast<float>(total);
-}
-
-// The next piece of rows asks anew.
-__global__ void loss_next_kernel(Words* words) {
-  wait_for_predecessor();
-  launch_dependents();
-  words->again = 0;
+  if (!last_block(a.words, &last)) return;
+  if (!AGAIN && threadIdx.x == 0) a.words->ticket = 0;
+  // (the losses are complete after the second time, where there is one)
+  total_losses(a, a.total != nullptr && (AGAIN || __ldcg(&a.words->again) == 0));
 }
 
 // dw (bf16) from the pieces' fp32 sums.
@@ -299,7 +344,7 @@ __global__ void __launch_bounds__(256) loss_round_kernel(const float* from, int6
 
 // Rows of a piece.
 int64_t piece_rows(const zero_cross_entropy_t& s, bool grads) {
-  const int64_t row = grads ? 2 * laid_out_pitch(s.vocab) : 16;
+  const int64_t row = grads ? 2 * laid_out_pitch(s.vocab) : 16 * ((s.vocab + 127) / 128);
   int64_t n = kMostHeld / row / 256 * 256;
   if (n < 256) n = 256;
   return s.rows < n ? s.rows : n;
@@ -348,6 +393,7 @@ Layout make_layout(const zero_cross_entropy_t& s, int32_t flags) {
     return p;
   };
   l.w = take((flags & ZERO_LINEAR_ALIGNED) ? 0 : 2 * s.vocab * laid_out_pitch(s.width));
+  // (the loss alone reads x in place, if it lies so; what it lies like is not known here)
   l.x = take(2 * l.piece * laid_out_pitch(s.width));
   l.zt = take(12 * l.piece);  // zt, ref, column
   l.held = take(grads ? 2 * l.piece * laid_out_pitch(s.vocab) : 0);
@@ -412,7 +458,7 @@ cudaError_t launch_cross_entropy(const CrossEntropyLaunch& L) {
   a.sums = reinterpret_cast<const float2*>(base + l.sums);
   a.scale = L.scale;
   a.losses = L.losses != nullptr ? L.losses : reinterpret_cast<float*>(base + l.losses);
-  a.held = grads ? reinterpret_cast<uint16_t*>(base + l.held) : nullptr;
+  a.held = reinterpret_cast<uint16_t*>(base + l.held);
   a.ldz = laid_out_pitch(s.vocab);
   a.vec = aligned(L.x, 16) && aligned(L.w, 16) && (s.rows == 1 || s.ldx % 8 == 0) &&
           (s.vocab == 1 || s.ldw % 8 == 0);
@@ -425,7 +471,6 @@ cudaError_t launch_cross_entropy(const CrossEntropyLaunch& L) {
     w = copy;
     ldw = laid_out_pitch(s.width);
   }
-  if (e == cudaSuccess) e = chain.launch(loss_count_kernel, dim3(1), 1024, 0, 1, a);
   const bool joined = L.dw != nullptr && s.rows > l.piece && !L.grad_f32;  // sums of pieces in fp32
   float* acc = reinterpret_cast<float*>(base + l.acc);
   const auto blocks_of = [](int64_t n, int64_t most) {
@@ -437,23 +482,42 @@ cudaError_t launch_cross_entropy(const CrossEntropyLaunch& L) {
     const bool last = first + a.rows == s.rows;
     a.parts = static_cast<int32_t>(exponent_parts(a.rows, s.vocab, s.width));
     a.total = last ? L.total : nullptr;
-    if (first > 0) e = chain.launch(loss_next_kernel, dim3(1), 1, 0, 1, a.words);
-    if (e == cudaSuccess)
-      e = chain.launch(a.vec ? loss_rows_kernel<true> : loss_rows_kernel<false>,
-                       blocks_of((a.rows + 7) / 8, 16 * kSms), 256, 0, 1, a);
     ExponentLaunch x{};
     x.rows = a.rows;
     x.width = s.width;
     x.vocab = s.vocab;
-    x.x = a.xc;
-    x.ldx = a.ldxc;
     x.w = w;
     x.ldw = ldw;
-    x.of = {a.ref, a.column, const_cast<float2*>(a.sums), a.parts, nullptr};
-    x.out = a.held;
-    x.ldo = a.ldz;
     x.stream = L.stream;
     x.withhold = L.withhold;
+    x.of.sums = const_cast<float2*>(a.sums);
+    x.of.sum_pitch = a.parts;
+    if (!grads) {
+      x.x = L.x + first * s.ldx;
+      x.ldx = s.ldx;
+      if (!tileable_matrix(x.x, a.rows, s.width, s.ldx)) {
+        e = launch_lay_out(x.x, a.rows, s.width, s.ldx, a.xc, L.stream);
+        x.x = a.xc;
+        x.ldx = a.ldxc;
+      }
+      x.of.targets = static_cast<const char*>(L.targets) + first * (L.ids_i32 ? 4 : 8);
+      x.of.ids_i32 = L.ids_i32;
+      x.of.ignore = L.ignore;
+      x.of.ticket = &a.words->ticket;
+      if (e == cudaSuccess) e = launch_exponents(x);
+      if (e == cudaSuccess)
+        e = chain.launch(a.vec ? loss_alone_kernel<true> : loss_alone_kernel<false>, blocks_of((a.rows + kFinishWarps - 1) / kFinishWarps, 8 * kSms),
+                         kFinishThreads, 0, 1, a);
+      continue;
+    }
+    e = chain.launch(a.vec ? loss_rows_kernel<true> : loss_rows_kernel<false>,
+                     blocks_of((a.rows + 7) / 8, 16 * kSms), 256, 0, 1, a);
+    x.x = a.xc;
+    x.ldx = a.ldxc;
+    x.of.ref = a.ref;
+    x.of.target = a.column;
+    x.out = a.held;
+    x.ldo = a.ldz;
     if (e == cudaSuccess) e = launch_exponents(x);
     const dim3 grid = blocks_of(a.rows, 8 * kSms);
     if (e == cudaSuccess) e = chain.launch(loss_finish_kernel<false>, grid, kFinishThreads, 0, 1, a);
@@ -461,7 +525,7 @@ cudaError_t launch_cross_entropy(const CrossEntropyLaunch& L) {
     if (e == cudaSuccess) e = launch_exponents(x);
     if (e == cudaSuccess)
       e = chain.launch(loss_finish_kernel<true>, blocks_of(a.rows, 2 * kSms), kFinishThreads, 0, 1, a);
-    if (e != cudaSuccess || !grads) continue;
+    if (e != cudaSuccess) return e;
     LinearBackwardLaunch b{};
     b.s = linear_of(s, a.rows);
     b.s.ldw = ldw;

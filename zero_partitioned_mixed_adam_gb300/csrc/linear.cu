@@ -88,6 +88,7 @@ enum Kind {
   kGradient,  // times an activation's slope, or added to what is there; bf16
   kFloat,     // fp32, alone or added to what is there
   kExponent,  // exponentials less each row's reference: their sums, and 16 bits each
+  kLogSum,    // exponentials less the largest: their sums alone
 };
 
 // A warp's 32 x 32 part of D from shared memory, where row r's 16-byte piece q
@@ -550,6 +551,63 @@ struct ExponentPart {
   }
 };
 
+// The same where nothing is to be made of the exponentials but their sum: less the largest
+// logit so far, so that no reference is needed beforehand.
+struct LogSumPart {
+  int32_t t;
+  Pair sum;
+  float top;
+
+  __device__ __forceinline__ void begin(int32_t target) {
+    t = target;
+    sum = pair(0.0f, 0.0f);
+    top = -INFINITY;
+  }
+  __device__ __forceinline__ void put(float x[32], int64_t col, int64_t cols) {
+    if (col + 32 > cols) {
+#pragma unroll
+      for (int q = 0; q < 32; ++q)
+        if (col + q >= cols) x[q] = -INFINITY;
+    }
+    const int64_t at = t - col;
+    if (__any_sync(0xffffffffu, at >= 0 && at < 32)) {
+#pragma unroll
+      for (int q = 0; q < 32; ++q)
+        if (at == q) x[q] = -INFINITY;
+    }
+    float most[8];
+#pragma unroll
+    for (int q = 0; q < 8; ++q) most[q] = fmaxf(fmaxf(x[q], x[q + 8]), fmaxf(x[q + 16], x[q + 24]));
+#pragma unroll
+    for (int k = 4; k > 0; k /= 2)
+#pragma unroll
+      for (int q = 0; q < k; ++q) most[q] = fmaxf(most[q], most[q + k]);
+    // (-inf: nothing here counts, and a reference of 0 leaves the exponentials 0)
+    const float now = fmaxf(top, most[0]), ref = now == -INFINITY ? 0.0f : now;
+    const float less = fast_exp2((top - ref) * kLog2e);
+    sum = sum * pair(less, less);
+    top = now;
+#pragma unroll
+    for (int q = 0; q < 32; q += 2) {
+      float u, v;
+      split((pair(x[q], x[q + 1]) + pair(-ref, -ref)) * pair(kLog2e, kLog2e), u, v);
+      sum = sum + pair(fast_exp2(u), fast_exp2(v));
+    }
+  }
+  __device__ __forceinline__ float2 end() const {
+    float lo, hi;
+    split(sum, lo, hi);
+    return make_float2(lo + hi, top);
+  }
+};
+
+// A target as a column, or -1.
+__device__ __forceinline__ int32_t column_of(const ExponentOf& x, int64_t row, int64_t cols) {
+  const int64_t t = x.ids_i32 ? static_cast<const int32_t*>(x.targets)[row]
+                              : static_cast<const int64_t*>(x.targets)[row];
+  return t >= 0 && t < cols && t != x.ignore ? static_cast<int32_t>(t) : -1;
+}
+
 // Place in the ring of stages: the stage, and the parity of its barriers' phase.
 struct Place {
   int stages;
@@ -654,6 +712,8 @@ __global__ void __launch_bounds__(kProductThreads, 1)
   if (warp == 1) tmem_alloc<CG>(tmem_at, Shape::kColumns);
   if (!a.late) wait_for_predecessor();
   launch_dependents();
+  if constexpr (KIND == kLogSum)
+    if (blockIdx.x == 0 && threadIdx.x == 0) *a.x.ticket = 0;
   tc_fence_before();
   __syncthreads();
   if constexpr (CG == 2) cluster_sync();
@@ -803,7 +863,8 @@ __global__ void __launch_bounds__(kProductThreads, 1)
     int n = 0;
     bool ok = true;
     ExponentPart exponents;  // of kExponent
-    const bool scaled = KIND != kForward && KIND != kExponent && a.e.scale != nullptr;
+    LogSumPart log_sum;      // of kLogSum
+    const bool scaled = (KIND == kGradient || KIND == kFloat) && a.e.scale != nullptr;
     const float scale = scaled ? __ldcg(a.e.scale) : 1.0f;
     for (int t = turns.first(unit); t < tiles && ok; t = turns.after(t)) {
       const Tile tile = tile_of<BM>(a, t);
@@ -872,10 +933,14 @@ __global__ void __launch_bounds__(kProductThreads, 1)
           __syncwarp();
         }
       };
-      if constexpr (KIND == kExponent) {
+      if constexpr (KIND == kExponent || KIND == kLogSum) {
         const int b = n & 1;
-        exponents.begin(mine_in ? __ldcg(a.x.ref + row0 + lane) : 0.0f,
-                        mine_in ? __ldcg(a.x.target + row0 + lane) : -1);
+        if constexpr (KIND == kExponent) {
+          exponents.begin(mine_in ? __ldcg(a.x.ref + row0 + lane) : 0.0f,
+                          mine_in ? __ldcg(a.x.target + row0 + lane) : -1);
+        } else {
+          log_sum.begin(mine_in ? column_of(a.x, row0 + lane, cols) : -1);
+        }
         ok = wait_for_chain(&done[b], static_cast<uint32_t>((n / 2) & 1), tile.last - tile.first);
         ++n;
         if (!ok) break;
@@ -892,11 +957,17 @@ __global__ void __launch_bounds__(kProductThreads, 1)
           for (int q = 0; q < 32; ++q) x[q] = __uint_as_float(bits[q]);
           if (c + c_step < c_end) tmem_load32(from + c + c_step, bits);
           else release(b);
-          if (any) exponents.put(a, reinterpret_cast<uint8_t*>(mine), x, static_cast<int>(row0),
-                                 tile.col + c, cols, lane);
+          if (!any) continue;
+          if constexpr (KIND == kExponent)
+            exponents.put(a, reinterpret_cast<uint8_t*>(mine), x, static_cast<int>(row0), tile.col + c, cols, lane);
+          else
+            log_sum.put(x, tile.col + c, cols);
         }
-        if (mine_in)
-          a.x.sums[(row0 + lane) * a.x.sum_pitch + tile.col / bn * 2 + half] = exponents.end();
+        if (mine_in) {
+          float2* to = a.x.sums + (row0 + lane) * a.x.sum_pitch + tile.col / bn * 2 + half;
+          if constexpr (KIND == kExponent) *to = exponents.end();
+          else *to = log_sum.end();
+        }
       } else if constexpr (KIND == kFloat) {
         constexpr int kParts = Shape::kMaxCols / 64;
         float sum[kParts][32];
@@ -1767,6 +1838,9 @@ cudaError_t launch_exponents(const ExponentLaunch& L) {
     if (e != cudaSuccess) return e;
   }
   Chain chain{L.stream};
+  if (L.of.targets != nullptr)
+    return w.plan.cg == 2 ? launch_shape<2, false, false, kLogSum, false>(p, &w, &chain)
+                          : launch_shape<1, false, false, kLogSum, false>(p, &w, &chain);
   return w.plan.cg == 2 ? launch_shape<2, false, false, kExponent, false>(p, &w, &chain)
                         : launch_shape<1, false, false, kExponent, false>(p, &w, &chain);
 }

@@ -86,22 +86,27 @@ struct LinearBackwardLaunch {
 
 // ------------------------------------------- exponentials of a linear map's rows
 
-// What becomes of z = x W^T in place of an epilogue: with d = z - ref of its row, the
-// sum of exp(d) and the largest z over each part of the columns, the target's left out
-// (target < 0: none is); and d in 16 bits where it is wanted.
+// What becomes of z = x W^T in place of an epilogue: over each part of the columns, the
+// target's left out, the sum of exp(d) and the largest z.
+//   with ref      d = z - ref of its row; d is written too, in 16 bits
+//   with targets  d = z less the largest z
 struct ExponentOf {
-  const float* ref;       // [rows]
-  const int32_t* target;  // [rows]
   float2* sums;           // [rows][sum_pitch], exponent_parts of them written
   int64_t sum_pitch;
+  const float* ref;       // [rows]
+  const int32_t* target;  // [rows], -1: none
   const int32_t* only_if; // nothing is done where this is 0; NULL: always
+  const void* targets;    // [rows], as the caller gives them
+  int32_t ids_i32;
+  int64_t ignore;
+  int32_t* ticket;        // set to 0
 };
 struct ExponentLaunch {
   int64_t rows, width, vocab;
   const uint16_t *x, *w;  // where TMA can read them
   int64_t ldx, ldw;
   ExponentOf of;
-  uint16_t* out;          // [rows][ldo], in 2^-10, -32 and below as -32768; NULL: not wanted
+  uint16_t* out;          // [rows][ldo], in 2^-10, -32 and below as -32768
   int64_t ldo;
   cudaStream_t stream;
   int32_t withhold;
