@@ -142,11 +142,11 @@ def test_parts_alone():
         assert torch.equal(got, want), name
 
 
-@pytest.mark.parametrize("rows", [3, 140])
-def test_far_targets(rows):
-    """Targets far below the largest logit (losses of 40 to 400: another reference is taken), far
-    above all others, and both among ordinary rows."""
-    k, v = 64, 1000
+@pytest.mark.parametrize("rows,k,v", [(3, 64, 1000), (140, 64, 1000), (40, 75, 333), (300, 256, 4099)])
+def test_far_targets(rows, k, v):
+    """Targets far below the largest logit (losses of 40 to 400: another reference is taken, by the
+    rows' own blocks up to 2^28 products and by a second run of the product beyond), far above
+    all others, and both among ordinary rows."""
     x, w = matrix(rows, k, 1.0, 1), matrix(v, k, 1.0, 2)
     t = targets_of(rows, v, 3)
     z = x.float() @ w.float().t()

@@ -606,9 +606,9 @@ __global__ void __launch_bounds__(kMostThreads)
     }
     if constexpr (VEC) rows.done(R);
   };
-  // Two rows at a time where there is room for them in registers (8192 x 2048 without a norm
-  // after the block 41 -> 28 us; with one, sums spilt, 58 -> 66), or a barrier is a cluster's
-  // (4096 x 8192 177 -> 135).
+  // Two rows at a time, unless the registers of that are the sums' (8192 x 2048 without a norm
+  // after the block 41 -> 28 us, with one 58 -> 66; 4096 x 8192, where a barrier is a cluster's,
+  // 177 -> 140).
   uint32_t i = own.first;
   if constexpr (!FULL || SHARE == kCluster)
     for (; i + own.step < rows.rows; i += 2 * own.step) make(std::integral_constant<int, 2>(), i);

@@ -64,6 +64,7 @@ struct LossArgs {
   uint16_t* held;         // [rows][ldz]: 16 bits, then dz
   int64_t ldz;
   int32_t vec;            // x and w are read in vectors
+  int32_t alone;          // rows that want another reference are made anew by their block
 };
 
 __device__ __forceinline__ int64_t target_of(const LossArgs& a, int64_t i) {
@@ -106,6 +107,11 @@ __device__ __forceinline__ float dot_part(const uint16_t* x, const uint16_t* w, 
   }
   return sum;
 }
+
+struct Nothing {
+  __device__ __forceinline__ void operator()(int64_t, uint4) const {}
+  __device__ __forceinline__ void operator()(int64_t, uint16_t) const {}
+};
 
 // A warp a row: the target's logit, and x laid out for TMA, an ignored row's as zeros
 // (its x may hold anything, and 0 times an infinity would reach dw).
@@ -214,28 +220,86 @@ __global__ void __launch_bounds__(kFinishThreads) loss_alone_kernel(const __grid
       if (lane == 0) a.losses[a.first + i] = t == a.ignore ? 0.0f : NAN;
       continue;
     }
-    struct Nothing {
-      __device__ __forceinline__ void operator()(int64_t, uint4) const {}
-      __device__ __forceinline__ void operator()(int64_t, uint16_t) const {}
-    };
     const float zt = warp_sum(dot_part<VEC>(a.x + (a.first + i) * a.ldx, a.w + t * a.ldw, a.width, lane, Nothing{}));
     const float2* parts = a.sums + i * a.parts;
-    float top = zt;
-    for (int k = lane; k < a.parts; k += 32) top = fmaxf(top, __ldcg(parts + k).y);
+    // a lane's parts, less the largest logit of them so far
+    float top = -INFINITY, sum = 0.0f;
+    constexpr int U = 4;
+    for (int k0 = lane; k0 < a.parts; k0 += 32 * U) {
+      float2 v[U];
 #pragma unroll
-    for (int k = 16; k > 0; k /= 2) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, k));
-    // less the target's logit, where that leaves fp32's range alone
-    const bool own = top - zt < 80.0f;
-    const float ref = own ? zt : top;
-    float sum = 0.0f;
-    for (int k = lane; k < a.parts; k += 32) {
-      const float2 s = __ldcg(parts + k);
-      if (s.x != 0.0f) sum += s.x * expf(s.y - ref);
+      for (int u = 0; u < U; ++u)
+        v[u] = k0 + 32 * u < a.parts ? __ldcg(parts + k0 + 32 * u) : make_float2(0.0f, -INFINITY);
+      float now = top;
+#pragma unroll
+      for (int u = 0; u < U; ++u) now = fmaxf(now, v[u].y);
+      if (sum != 0.0f) sum *= expf(top - now);
+      top = now;
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        if (v[u].x != 0.0f) sum += v[u].x * expf(v[u].y - now);
     }
+    float most = fmaxf(top, zt);
+#pragma unroll
+    for (int k = 16; k > 0; k /= 2) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, k));
+    // less the target's logit, where that leaves fp32's range alone
+    const bool own = most - zt < 80.0f;
+    const float ref = own ? zt : most;
+    if (sum != 0.0f) sum *= expf(top - ref);
     sum = warp_sum(sum);
     if (lane == 0) a.losses[a.first + i] = own ? log1pf(sum) : (ref - zt) + logf(sum + expf(zt - ref));
   }
   if (a.total != nullptr && last_block(a.words, &last)) total_losses(a, true);
+}
+
+// Row i's exponentials less `ref`, as the product's epilogue makes them; this warp's part of
+// their sum.  Four columns at a time.
+template <bool VEC>
+__device__ __noinline__ float row_again(const LossArgs& a, int64_t i, int32_t t, float ref) {
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const uint16_t* x = a.xc + i * a.ldxc;
+  constexpr int U = 4;
+  float sum = 0.0f;
+  for (int64_t j = U * warp; j < a.vocab; j += U * kFinishWarps) {
+    const uint16_t* w[U];
+    float z[U] = {};
+#pragma unroll
+    for (int u = 0; u < U; ++u) w[u] = a.w + (j + u < a.vocab ? j + u : j) * a.ldw;
+    if constexpr (VEC) {
+      int64_t k = 8 * lane;
+      for (; k + 8 <= a.width; k += 256) {
+        float p[8];
+        bf16x8(__ldg(reinterpret_cast<const uint4*>(x + k)), p);
+        uint4 v[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) v[u] = __ldg(reinterpret_cast<const uint4*>(w[u] + k));
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          float q[8];
+          bf16x8(v[u], q);
+#pragma unroll
+          for (int c = 0; c < 8; ++c) z[u] = fmaf(p[c], q[c], z[u]);
+        }
+      }
+      for (; k < a.width; ++k)  // (one lane's: what is left of a vector)
+#pragma unroll
+        for (int u = 0; u < U; ++u) z[u] = fmaf(bf16_at(x + k), bf16_at(w[u] + k), z[u]);
+    } else {
+      for (int64_t k = lane; k < a.width; k += 32)
+#pragma unroll
+        for (int u = 0; u < U; ++u) z[u] = fmaf(bf16_at(x + k), bf16_at(w[u] + k), z[u]);
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      z[u] = warp_sum(z[u]);
+      if (j + u >= a.vocab) continue;
+      const float d = j + u == t ? -INFINITY : z[u] - ref;
+      sum += expf(d);
+      if (lane == 0)
+        a.held[i * a.ldz + j + u] = static_cast<uint16_t>(static_cast<int16_t>(fmaxf(rintf(d * 1024.0f), -32768.0f)));
+    }
+  }
+  return sum;
 }
 
 // A block a row: the row's sums in the order of its parts, its loss, and dz.  With c alike
@@ -243,6 +307,11 @@ __global__ void __launch_bounds__(kFinishThreads) loss_alone_kernel(const __grid
 // small, and c multiplies the products' sums; a scale of each row's own is in its dz.
 // AGAIN: the second time, where the first has asked for it.  The last block adds up the
 // losses.  Bound by HBM: 4 bytes an element (8192 x 50257: 1.65 GB).
+// Where the whole product is small, a row that wants another reference is made anew here, by
+// dot products, which saves the two launches that else do it (37 x 256 -> 515: 5 us of 37; were
+// every row of 2^28 multiplications such a one, they would take some 30 us).
+constexpr int64_t kFewProducts = int64_t{1} << 28;
+
 template <bool AGAIN>
 __global__ void __launch_bounds__(kFinishThreads) loss_finish_kernel(const __grid_constant__ LossArgs a) {
   __shared__ float2 part[kFinishWarps];
@@ -253,8 +322,8 @@ __global__ void __launch_bounds__(kFinishThreads) loss_finish_kernel(const __gri
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   for (int64_t i = blockIdx.x; i < a.rows; i += gridDim.x) {
     const int32_t t = __ldcg(a.column + i);
-    const float zt = __ldcg(a.zt + i), ref = __ldcg(a.ref + i);
-    float sum = 0.0f, top = -INFINITY;
+    const float zt = __ldcg(a.zt + i);
+    float ref = __ldcg(a.ref + i), sum = 0.0f, top = -INFINITY;
     if (t != -1) {
       for (int k = threadIdx.x; k < a.parts; k += kFinishThreads) {
         const float2 s = __ldcg(a.sums + i * a.parts + k);
@@ -274,6 +343,21 @@ __global__ void __launch_bounds__(kFinishThreads) loss_finish_kernel(const __gri
       sum += part[k].x;
       top = fmaxf(top, part[k].y);
     }
+    if (!AGAIN && t >= 0 && sum > kOneMore && isfinite(top)) {
+      if (a.alone) {
+        ref = top;
+        sum = a.vec ? row_again<true>(a, i, t, ref) : row_again<false>(a, i, t, ref);
+        __syncthreads();  // part[] and the row are written
+        if (lane == 0) part[warp].x = sum;
+        __syncthreads();
+        sum = 0.0f;
+#pragma unroll
+        for (int k = 0; k < kFinishWarps; ++k) sum += part[k].x;
+      } else if (threadIdx.x == 0) {
+        a.ref[i] = top;
+        a.words->again = 1;
+      }
+    }
     const bool own = zt == ref;
     const float et = own ? 1.0f : expf(zt - ref);
     const float whole = sum + et;
@@ -283,13 +367,7 @@ __global__ void __launch_bounds__(kFinishThreads) loss_finish_kernel(const __gri
     if (!isfinite(whole)) f = NAN;
     if (t == -1) loss = f = 0.0f;
     if (t == -2) loss = f = NAN;
-    if (threadIdx.x == 0) {
-      a.losses[a.first + i] = loss;
-      if (!AGAIN && t >= 0 && sum > kOneMore && isfinite(top)) {
-        a.ref[i] = top;
-        a.words->again = 1;
-      }
-    }
+    if (threadIdx.x == 0) a.losses[a.first + i] = loss;
     // (the pitch has room for whole vectors; an ignored row's are not read)
     uint16_t* row = a.held + i * a.ldz;
     constexpr int kSpan = 8 * kFinishThreads, U = 2;
@@ -480,6 +558,7 @@ cudaError_t launch_cross_entropy(const CrossEntropyLaunch& L) {
     a.first = first;
     a.rows = s.rows - first < l.piece ? s.rows - first : l.piece;
     const bool last = first + a.rows == s.rows;
+    a.alone = a.rows * s.vocab <= kFewProducts / s.width;
     a.parts = static_cast<int32_t>(exponent_parts(a.rows, s.vocab, s.width));
     a.total = last ? L.total : nullptr;
     ExponentLaunch x{};
@@ -522,8 +601,8 @@ cudaError_t launch_cross_entropy(const CrossEntropyLaunch& L) {
     const dim3 grid = blocks_of(a.rows, 8 * kSms);
     if (e == cudaSuccess) e = chain.launch(loss_finish_kernel<false>, grid, kFinishThreads, 0, 1, a);
     x.of.only_if = &a.words->again;
-    if (e == cudaSuccess) e = launch_exponents(x);
-    if (e == cudaSuccess)
+    if (e == cudaSuccess && !a.alone) e = launch_exponents(x);
+    if (e == cudaSuccess && !a.alone)
       e = chain.launch(loss_finish_kernel<true>, blocks_of(a.rows, 2 * kSms), kFinishThreads, 0, 1, a);
     if (e != cudaSuccess) return e;
     LinearBackwardLaunch b{};
