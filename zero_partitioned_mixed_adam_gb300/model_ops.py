@@ -9,12 +9,13 @@ optimizer's calls these take tensors of the current CUDA device only.
 from __future__ import annotations
 
 import ctypes
+import functools
 
 import torch
 
 from . import (ZERO_GRAD_ACCUMULATE, ZERO_GRAD_F32, ZERO_IDS_I32, ZERO_LINEAR_ALIGNED,
                ZERO_LINEAR_BACKWARD, ZERO_NORM_LAYER, ZERO_NORM_NONE, ZERO_NORM_RMS, ZERO_OK,
-               ZeroError, _addr, _lib, _stream_handle)
+               ZeroError, _lib, _stream_handle)
 from .train_ops import _BF16, _GRADS, _matrix, _vector
 
 _B = torch.bfloat16
@@ -90,27 +91,40 @@ def _rows(name, t, shape):
     return pitch if rows > 1 else max(cols, pitch)
 
 
+def _floats(name, t, n):
+    """_vector for fp32."""
+    if t.shape != (n,) or t.dtype is not torch.float32 or not t.is_contiguous():
+        _vector(name, t, n, (torch.float32,))
+
+
+def _pointer(t):
+    return None if t is None else t.data_ptr()
+
+
 def _columns(name, t, shape):
     """_vector for bf16, of a shape."""
     if t.shape != shape or t.dtype is not _B or not t.is_contiguous():
         _vector(name, t, shape[0])
 
 
-def _workspace(need, what, workspace, device, stream):
-    """The caller's workspace, or one from PyTorch's allocator, which is asked while the call's
-    stream is current: it hands memory out in that stream's order."""
+@functools.lru_cache(maxsize=256)
+def _bytes(call, sizes, *flags):
+    """Bytes of workspace, which follow from the sizes."""
+    need = getattr(_lib, call)(ctypes.byref(sizes[0](*sizes[1:])), *flags)
     if need < 0:
-        raise ZeroError(need, what)
-    if workspace is not None:
-        return workspace, workspace.numel() * workspace.element_size()
-    if need == 0:
-        return None, 0
+        raise ZeroError(need, call)
+    return need
+
+
+def _workspace(need, device, stream):
+    """Memory from PyTorch's allocator, which is asked while the call's stream is current: it
+    hands memory out in that stream's order."""
     if stream is None:
-        return torch.empty(need, dtype=torch.uint8, device=device), need
+        return torch.empty(need, dtype=torch.uint8, device=device)
     if isinstance(stream, int):
         stream = torch.cuda.ExternalStream(stream, device)
     with torch.cuda.stream(stream):
-        return torch.empty(need, dtype=torch.uint8, device=device), need
+        return torch.empty(need, dtype=torch.uint8, device=device)
 
 
 def _check(rc, what):
@@ -121,14 +135,14 @@ def _check(rc, what):
 # ---------------------------------------------------------------------- embedding
 
 def _embedding(ids, table, rows, name, kinds):
-    if ids.dim() != 1 or ids.dtype not in _IDS or (ids.numel() > 1 and ids.stride(0) != 1):
+    if ids.dim() != 1 or ids.dtype not in _IDS or not ids.is_contiguous():
         raise ValueError(f"ids: expected contiguous int64 or int32, got {tuple(ids.shape)} {ids.dtype}")
     if table.dim() != 2:
         raise ValueError(f"{name} is a matrix")
     vocab, width = table.shape
-    s = ZeroEmbedding(ids.numel(), width, vocab, _matrix(name, table, vocab, width, kinds),
-                      _matrix("the rows", rows, ids.numel(), width))
-    return s, ZERO_IDS_I32 if ids.dtype == torch.int32 else 0
+    n = ids.numel()
+    s = ZeroEmbedding(n, width, vocab, _matrix(name, table, vocab, width, kinds), _rows("the rows", rows, (n, width)))
+    return s, ZERO_IDS_I32 if ids.dtype is torch.int32 else 0
 
 
 def zero_embedding_forward(ids, table, y, *, scale: float = 1.0, stream=None) -> None:
@@ -136,7 +150,7 @@ def zero_embedding_forward(ids, table, y, *, scale: float = 1.0, stream=None) ->
     y [rows, width], bf16 with contiguous columns.  Ids outside the table give rows of NaN."""
     s, flags = _embedding(ids, table, y, "table", _BF16)
     _here(stream, (ids, table, y))
-    _check(_lib.zero_embedding_forward(ctypes.byref(s), _addr(table), _addr(ids), flags, scale, _addr(y),
+    _check(_lib.zero_embedding_forward(ctypes.byref(s), table.data_ptr(), ids.data_ptr(), flags, scale, y.data_ptr(),
                                        _stream_handle(stream)), "zero_embedding_forward")
 
 
@@ -149,8 +163,8 @@ def zero_embedding_backward(dy, ids, dtable, *, scale: float = 1.0, padding=None
     flags |= ZERO_GRAD_F32 if dtable.dtype == torch.float32 else 0
     flags |= ZERO_GRAD_ACCUMULATE if accumulate else 0
     _here(stream, (dy, ids, dtable))
-    _check(_lib.zero_embedding_backward(ctypes.byref(s), _addr(dy), _addr(ids), flags, scale,
-                                        -1 if padding is None else padding, _addr(dtable),
+    _check(_lib.zero_embedding_backward(ctypes.byref(s), dy.data_ptr(), ids.data_ptr(), flags, scale,
+                                        -1 if padding is None else padding, dtable.data_ptr(),
                                         _stream_handle(stream)), "zero_embedding_backward")
 
 
@@ -163,10 +177,7 @@ def zero_linear_cross_entropy_workspace(rows: int, width: int, vocab: int, gradi
     multiple of 8."""
     flags = (ZERO_LINEAR_BACKWARD if gradients else 0) | (ZERO_LINEAR_ALIGNED if aligned else 0) | \
         (ZERO_GRAD_F32 if f32 else 0)
-    need = _lib.zero_linear_cross_entropy_workspace(ctypes.byref(ZeroCrossEntropy(rows, width, vocab)), flags)
-    if need < 0:
-        raise ZeroError(need, "zero_linear_cross_entropy_workspace")
-    return need
+    return _bytes("zero_linear_cross_entropy_workspace", (ZeroCrossEntropy, rows, width, vocab), flags)
 
 
 def zero_linear_cross_entropy(x, w, targets, losses=None, total=None, *, dx=None, dw=None,
@@ -183,41 +194,44 @@ def zero_linear_cross_entropy(x, w, targets, losses=None, total=None, *, dx=None
     (zero_linear_cross_entropy_workspace bytes) one is taken from PyTorch's allocator."""
     if x.dim() != 2 or w.dim() != 2:
         raise ValueError("x and w are matrices")
-    (rows, width), vocab = x.shape, w.shape[0]
-    if targets.shape != (rows,) or targets.dtype not in _IDS or (rows > 1 and targets.stride(0) != 1):
+    shape, table = x.shape, w.shape
+    rows, width = shape
+    vocab = table[0]
+    if targets.shape != (rows,) or targets.dtype not in _IDS or not targets.is_contiguous():
         raise ValueError(f"targets: expected {rows} contiguous int64 or int32, got "
                          f"{tuple(targets.shape)} {targets.dtype}")
-    s = ZeroCrossEntropy(rows, width, vocab, _matrix("x", x, rows, width), _matrix("w", w, vocab, width))
-    f32 = (torch.float32,)
-    for name, t, n in (("losses", losses, rows), ("total", total, 1), ("scale", scale, rows)):
-        if t is not None:
-            _vector(name, t, n, f32)
-    flags = ZERO_IDS_I32 if targets.dtype == torch.int32 else 0
+    s = ZeroCrossEntropy(rows, width, vocab, _rows("x", x, shape), _rows("w", w, (vocab, width)))
+    if losses is not None:
+        _floats("losses", losses, rows)
+    if total is not None:
+        _floats("total", total, 1)
+    if scale is not None:
+        _floats("scale", scale, rows)
+    flags = ZERO_IDS_I32 if targets.dtype is torch.int32 else 0
     if dx is not None:
-        s.lddx = _matrix("dx", dx, rows, width)
+        s.lddx = _rows("dx", dx, shape)
     if dw is not None:
         s.lddw = _matrix("dw", dw, vocab, width, _GRADS)
-        flags |= ZERO_GRAD_F32 if dw.dtype == torch.float32 else 0
-    flags |= ZERO_GRAD_ACCUMULATE if accumulate else 0
+        if dw.dtype is torch.float32:
+            flags |= ZERO_GRAD_F32
+    if accumulate:
+        flags |= ZERO_GRAD_ACCUMULATE
     _here(stream, (x, w, targets, losses, total, scale, dx, dw, workspace))
-    need = 0
+    at = w.data_ptr()
     if workspace is None:
         kind = (ZERO_LINEAR_BACKWARD if dx is not None or dw is not None else 0) | (flags & ZERO_GRAD_F32)
-        if w.data_ptr() % 16 == 0 and (vocab == 1 or s.ldw % 8 == 0):
+        if at % 16 == 0 and (vocab == 1 or s.ldw % 8 == 0):
             kind |= ZERO_LINEAR_ALIGNED
-        need = _lib.zero_linear_cross_entropy_workspace(ctypes.byref(s), kind)
-    workspace, nbytes = _workspace(need, "zero_linear_cross_entropy_workspace", workspace, x.device, stream)
-    _check(_lib.zero_linear_cross_entropy(ctypes.byref(s), _addr(x), _addr(w), _addr(targets), ignore_index,
-                                          _addr(scale), _addr(losses), _addr(total), _addr(dx), _addr(dw),
-                                          flags, _addr(workspace), nbytes, _stream_handle(stream)),
+        workspace = _workspace(_bytes("zero_linear_cross_entropy_workspace", (ZeroCrossEntropy, rows, width, vocab), kind),
+                               x.device, stream)
+    _check(_lib.zero_linear_cross_entropy(ctypes.byref(s), x.data_ptr(), at, targets.data_ptr(), ignore_index,
+                                          _pointer(scale), _pointer(losses), _pointer(total), _pointer(dx),
+                                          _pointer(dw), flags, workspace.data_ptr(),
+                                          workspace.numel() * workspace.element_size(), _stream_handle(stream)),
            "zero_linear_cross_entropy")
 
 
 # -------------------------------------------------------------------- block norms
-
-def _pointer(t):
-    return None if t is None else t.data_ptr()
-
 
 def _block_norm(shape, post, kind, alpha, eps, h, gate, w1, b1, w):
     """The sizes with the pitches of h and gate; the vectors checked."""
@@ -268,10 +282,7 @@ def zero_block_norm_forward(r, y, *, h=None, s=None, post: int = ZERO_NORM_NONE,
 
 def zero_block_norm_workspace(rows: int, width: int) -> int:
     """Bytes of workspace that suffice for zero_block_norm_backward."""
-    need = _lib.zero_block_norm_workspace(ctypes.byref(ZeroBlockNorm(rows, width)))
-    if need < 0:
-        raise ZeroError(need, "zero_block_norm_workspace")
-    return need
+    return _bytes("zero_block_norm_workspace", (ZeroBlockNorm, rows, width))
 
 
 def zero_block_norm_backward(dy, s, *, ds=None, h=None, post: int = ZERO_NORM_NONE, post_weight=None,
@@ -315,14 +326,13 @@ def zero_block_norm_backward(dy, s, *, ds=None, h=None, post: int = ZERO_NORM_NO
     flags = (ZERO_GRAD_F32 if kind_of is torch.float32 else 0) | (ZERO_GRAD_ACCUMULATE if accumulate else 0)
     _here(stream, (dy, s, ds, h, post_weight, post_bias, gate, weight, dr, dh, dgate, dpost_weight,
                    dpost_bias, dweight, dbias, workspace))
-    at = ctypes.byref(z)
-    need = _lib.zero_block_norm_workspace(at) if workspace is None else 0
-    workspace, nbytes = _workspace(need, "zero_block_norm_workspace", workspace, dy.device, stream)
+    if workspace is None:
+        workspace = _workspace(_bytes("zero_block_norm_workspace", (ZeroBlockNorm, *shape)), dy.device, stream)
     _check(_lib.zero_block_norm_backward(
-        at, _pointer(dy), _pointer(ds), _pointer(s), _pointer(h), _pointer(post_weight), _pointer(post_bias),
-        _pointer(gate), _pointer(weight), _pointer(dr), _pointer(dh), _pointer(dgate), _pointer(dpost_weight),
-        _pointer(dpost_bias), _pointer(dweight), _pointer(dbias), flags, _pointer(workspace), nbytes,
-        _stream_handle(stream)), "zero_block_norm_backward")
+        ctypes.byref(z), dy.data_ptr(), _pointer(ds), s.data_ptr(), _pointer(h), _pointer(post_weight),
+        _pointer(post_bias), _pointer(gate), _pointer(weight), _pointer(dr), _pointer(dh), _pointer(dgate),
+        _pointer(dpost_weight), _pointer(dpost_bias), _pointer(dweight), _pointer(dbias), flags, workspace.data_ptr(),
+        workspace.numel() * workspace.element_size(), _stream_handle(stream)), "zero_block_norm_backward")
 
 
 __all__ = ["zero_embedding_forward", "zero_embedding_backward", "zero_linear_cross_entropy",
