@@ -193,6 +193,34 @@ def test_every_row_ignored():
     assert not losses.any() and not total.any()
 
 
+@pytest.mark.parametrize("count", [0, 1, 5, 128, 129, 700, 1023, 1024])
+@pytest.mark.parametrize("k,pitch", [(256, 0), (263, 5)])
+def test_rows_that_count_are_done_alone(count, k, pitch):
+    """Beyond 2^28 products ignored rows are left out of them: as many as there are, wherever they
+    lie, whatever they hold, to the bits of a call without them."""
+    m, v = 1024, 2000
+    assert m * k * v > 2 ** 28
+    gen = torch.Generator("cuda").manual_seed(count)
+    t = targets_of(m, v, 3)
+    t[torch.randperm(m, device="cuda", generator=gen)[count:]] = -100
+    x, w = matrix(m, k, 1.0, 1, pitch), matrix(v, k, 0.2, 2)
+    x[t == -100] = float("nan")
+    if count == 0:
+        out = [torch.full(s, 7.0, device="cuda") for s in ((m,), (1,), (m, k), (v, k))]
+        out[2] = out[2].to(BF)
+        za.zero_linear_cross_entropy(x, w, t, out[0], out[1], dx=out[2], dw=out[3])
+        assert not any(a.any() for a in out)
+        return
+    losses, total, dx, dw, _ = check(x, w, t, dx=blank(m, k, pitch=pitch))
+    assert (losses[t == -100] == 0).all() and (dx[t == -100] == 0).all()
+    scale = torch.linspace(-1.0, 2.0, m, device="cuda")
+    scale[t == -100] = float("inf")
+    check(x, w, t, scale=torch.where(t == -100, 0.0, scale), dtype=F32, add=True, dw=matrix(v, k, 0.1, 5).float())
+    again = torch.zeros(m, device="cuda")
+    za.zero_linear_cross_entropy(x, w, t, again, total, dx=dx, scale=scale)
+    assert torch.isfinite(total).all() and torch.isfinite(dx).all()
+
+
 def test_no_rows():
     w = matrix(9, 16, 1.0, 1)
     x, t = w[:0], torch.empty(0, dtype=torch.int64, device="cuda")

@@ -15,10 +15,13 @@
 // pass run once more; the launches that do so end at once where no row needs them.
 //
 // Kernels of one piece of rows:
+//   places    which rows are not ignored: only they take part in what follows
 //   rows      z_t, the reference, the target as a column, x where TMA can read it
 //   product   (linear.cu) exponentials
 //   finish    losses, dz;  product and finish again, where some row needs it
 //   products  (linear.cu) dx = dz W, dw = dz^T x
+//   spread    dx where the caller's rows are
+// Small problems leave out places and spread, as their launches are worth more than the rows.
 // The loss alone needs neither reference nor x laid out: its product takes the exponentials
 // less the largest logit so far, and a warp a row ends it.  The target's logit is a dot
 // product of its own there too, rounded to nearest: the tensor cores cut off, and what
@@ -39,6 +42,7 @@ constexpr float kOneMore = 17592186044416.0f;    // 2^44: a sum that asks for an
 struct Words {
   int32_t ticket;  // blocks of a kernel that are done
   int32_t again;   // some row of this piece wants another reference
+  int32_t rows;    // that are not ignored, of this piece
   float share;     // 1 / rows that are not ignored: c of the mean (0 where there is none)
 };
 
@@ -64,8 +68,29 @@ struct LossArgs {
   uint16_t* held;         // [rows][ldz]: 16 bits, then dz
   int64_t ldz;
   int32_t vec;            // x and w are read in vectors
-  int32_t alone;          // rows that want another reference are made anew by their block
+  int32_t alone;          // rows that want another reference are made anew by their block (kOnce)
+  // Rows that are not ignored, one after the other (NULL: all rows as they are):
+  int32_t* place;         // [rows]: the piece's row that the k-th is
+  int32_t* slot;          // [rows]: and the k that a row is, -1: ignored
+  int64_t fill;           // rows that are 0 behind them at least, from the first on
+  uint16_t* dxc;          // [rows][lddxc]: their dx
+  int64_t lddxc;
+  uint16_t* dx;           // the piece's
+  int64_t lddx;
+  int32_t dx_vec;
+  int32_t direct;         // dx is written where it belongs if no row is ignored
 };
+
+// The rows of a piece that the kernels look at: those there are, and those that are 0.
+__device__ __forceinline__ int64_t rows_of(const LossArgs& a) {
+  return a.place != nullptr ? __ldcg(&a.words->rows) : a.rows;
+}
+__device__ __forceinline__ int64_t filled_rows(const LossArgs& a, int64_t n) {
+  if (a.place == nullptr) return a.rows;
+  int64_t m = (n + 127) / 128 * 128;
+  m = m > a.fill ? m : a.fill;
+  return m < a.rows ? m : a.rows;
+}
 
 __device__ __forceinline__ int64_t target_of(const LossArgs& a, int64_t i) {
   return a.ids_i32 ? static_cast<const int32_t*>(a.targets)[i]
@@ -78,26 +103,90 @@ __device__ __forceinline__ float warp_sum(float x) {
   return x;
 }
 
+// Where the rows that are not ignored go: one after the other, so that the products have no
+// others to do.  One block: a warp looks through a run of rows, once to count and once to
+// write (8,192 rows: 4 us).
+constexpr int kPlaceWarps = 32;
+__global__ void __launch_bounds__(32 * kPlaceWarps) loss_places_kernel(const __grid_constant__ LossArgs a) {
+  __shared__ int32_t found[kPlaceWarps];
+  wait_for_predecessor();
+  launch_dependents();
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int64_t each = (a.rows + 32 * kPlaceWarps - 1) / (32 * kPlaceWarps) * 32;
+  const int64_t from = warp * each < a.rows ? warp * each : a.rows, to = from + each < a.rows ? from + each : a.rows;
+  constexpr int U = 8;
+  const auto look = [&](auto f) {
+    for (int64_t i0 = from; i0 < to; i0 += 32 * U) {
+      int64_t t[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int64_t i = i0 + 32 * u + lane;
+        t[u] = target_of(a, a.first + (i < to ? i : to - 1));
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int64_t i = i0 + 32 * u + lane;
+        f(i, i < to && t[u] != a.ignore);
+      }
+    }
+  };
+  int n = 0;
+  look([&](int64_t, bool has) { n += __popc(__ballot_sync(0xffffffffu, has)); });
+  if (lane == 0) found[warp] = n;
+  __syncthreads();
+  int at = 0, all = 0;
+  for (int w = 0; w < kPlaceWarps; ++w) {
+    if (w < warp) at += found[w];
+    all += found[w];
+  }
+  look([&](int64_t i, bool has) {
+    const uint32_t those = __ballot_sync(0xffffffffu, has);
+    const int k = at + __popc(those & ((1u << lane) - 1u));
+    if (i < to) {
+      a.slot[i] = has ? k : -1;
+      if (has) a.place[k] = static_cast<int32_t>(i);
+      else a.losses[a.first + i] = 0.0f;
+    }
+    at += __popc(those);
+  });
+  if (threadIdx.x == 0) *a.words = Words{0, 0, all, 0.0f};
+}
+
 // A lane's part of the product of two rows of bf16; f(j, v) is given x's vectors or elements.
 template <bool VEC, typename F>
 __device__ __forceinline__ float dot_part(const uint16_t* x, const uint16_t* w, int64_t width, int lane, F f) {
   float sum = 0.0f;
   if constexpr (VEC) {
-    for (int64_t j = 8 * lane; j < width; j += 256) {
-      if (j + 8 <= width) {
-        const uint4 v = __ldg(reinterpret_cast<const uint4*>(x + j));
-        float p[8], q[8];
-        bf16x8(v, p);
-        bf16x8(__ldg(reinterpret_cast<const uint4*>(w + j)), q);
+    int64_t j = 8 * lane;
+    const auto add = [&](uint4 v, uint4 u) {
+      float p[8], q[8];
+      bf16x8(v, p);
+      bf16x8(u, q);
 #pragma unroll
-        for (int c = 0; c < 8; ++c) sum = fmaf(p[c], q[c], sum);
-        f(j, v);
-      } else {
-        for (int64_t k = j; k < width; ++k) {
-          sum = fmaf(bf16_at(x + k), bf16_at(w + k), sum);
-          f(k, x[k]);
-        }
+      for (int c = 0; c < 8; ++c) sum = fmaf(p[c], q[c], sum);
+    };
+    constexpr int U = 4;  // of each row's loads under way
+    for (; j + 256 * (U - 1) + 8 <= width; j += 256 * U) {
+      uint4 v[U], u[U];
+#pragma unroll
+      for (int k = 0; k < U; ++k) {
+        v[k] = __ldg(reinterpret_cast<const uint4*>(x + j + 256 * k));
+        u[k] = __ldg(reinterpret_cast<const uint4*>(w + j + 256 * k));
       }
+#pragma unroll
+      for (int k = 0; k < U; ++k) {
+        add(v[k], u[k]);
+        f(j + 256 * k, v[k]);
+      }
+    }
+    for (; j + 8 <= width; j += 256) {
+      const uint4 v = __ldg(reinterpret_cast<const uint4*>(x + j));
+      add(v, __ldg(reinterpret_cast<const uint4*>(w + j)));
+      f(j, v);
+    }
+    for (; j < width; ++j) {  // (one lane's: what is left of a vector)
+      sum = fmaf(bf16_at(x + j), bf16_at(w + j), sum);
+      f(j, x[j]);
     }
   } else {
     for (int64_t j = lane; j < width; j += 32) {
@@ -119,13 +208,15 @@ template <bool VEC>
 __global__ void __launch_bounds__(256) loss_rows_kernel(const __grid_constant__ LossArgs a) {
   wait_for_predecessor();
   launch_dependents();
-  if (blockIdx.x == 0 && threadIdx.x == 0) *a.words = Words{0, 0, 0.0f};
+  if (a.place == nullptr && blockIdx.x == 0 && threadIdx.x == 0) *a.words = Words{0, 0, 0, 0.0f};
   const int lane = threadIdx.x % 32;
-  for (int64_t i = static_cast<int64_t>(blockIdx.x) * 8 + threadIdx.x / 32; i < a.rows;
-       i += static_cast<int64_t>(gridDim.x) * 8) {
-    const int64_t t = target_of(a, a.first + i);
-    const bool ignored = t == a.ignore, column = !ignored && t >= 0 && t < a.vocab;
-    uint16_t* to = a.xc + i * a.ldxc;
+  const int64_t n = rows_of(a), filled = filled_rows(a, n);
+  for (int64_t k = static_cast<int64_t>(blockIdx.x) * 8 + threadIdx.x / 32; k < filled;
+       k += static_cast<int64_t>(gridDim.x) * 8) {
+    const int64_t i = a.first + (a.place == nullptr ? k : k < n ? __ldcg(a.place + k) : 0);
+    const int64_t t = target_of(a, i);
+    const bool ignored = k >= n || t == a.ignore, column = !ignored && t >= 0 && t < a.vocab;
+    uint16_t* to = a.xc + k * a.ldxc;
     float sum = 0.0f;
     if (ignored) {  // (the pitch has room for whole vectors)
       for (int64_t j = 8 * lane; j < a.width; j += 256) *reinterpret_cast<uint4*>(to + j) = make_uint4(0, 0, 0, 0);
@@ -135,14 +226,14 @@ __global__ void __launch_bounds__(256) loss_rows_kernel(const __grid_constant__ 
         __device__ __forceinline__ void operator()(int64_t j, uint4 v) const { *reinterpret_cast<uint4*>(to + j) = v; }
         __device__ __forceinline__ void operator()(int64_t j, uint16_t v) const { to[j] = v; }
       };
-      sum = dot_part<VEC>(a.x + (a.first + i) * a.ldx, a.w + (column ? t : 0) * a.ldw, a.width, lane, Put{to});
+      sum = dot_part<VEC>(a.x + i * a.ldx, a.w + (column ? t : 0) * a.ldw, a.width, lane, Put{to});
     }
     sum = warp_sum(sum);
     if (lane == 0) {
       const float zt = column || ignored ? sum : NAN;
-      a.zt[i] = zt;
-      a.ref[i] = isfinite(zt) ? zt : 0.0f;
-      a.column[i] = column ? static_cast<int32_t>(t) : ignored ? -1 : -2;
+      a.zt[k] = zt;
+      a.ref[k] = isfinite(zt) ? zt : 0.0f;
+      a.column[k] = column ? static_cast<int32_t>(t) : ignored ? -1 : -2;
     }
   }
 }
@@ -305,23 +396,30 @@ __device__ __noinline__ float row_again(const LossArgs& a, int64_t i, int32_t t,
 // A block a row: the row's sums in the order of its parts, its loss, and dz.  With c alike
 // for all rows (the mean) dz is p less the target's 1, whose rounding is nothing where p is
 // small, and c multiplies the products' sums; a scale of each row's own is in its dz.
-// AGAIN: the second time, where the first has asked for it.  The last block adds up the
+// kAgain: the second time, where the first has asked for it.  The last block adds up the
 // losses.  Bound by HBM: 4 bytes an element (8192 x 50257: 1.65 GB).
 // Where the whole product is small, a row that wants another reference is made anew here, by
 // dot products, which saves the two launches that else do it (37 x 256 -> 515: 5 us of 37; were
 // every row of 2^28 multiplications such a one, they would take some 30 us).
 constexpr int64_t kFewProducts = int64_t{1} << 28;
 
-template <bool AGAIN>
-__global__ void __launch_bounds__(kFinishThreads) loss_finish_kernel(const __grid_constant__ LossArgs a) {
+// (kOnce has registers of its own for that; the other two are 4 blocks an SM, with 6 vectors of
+// a row under way in each thread.)
+enum Time { kFirst, kAgain, kOnce };
+constexpr int kFinishBlocks = 4;
+
+template <Time TIME>
+__global__ void __launch_bounds__(kFinishThreads, TIME == kOnce ? 2 : kFinishBlocks) loss_finish_kernel(const __grid_constant__ LossArgs a) {
   __shared__ float2 part[kFinishWarps];
   __shared__ int32_t last;
   wait_for_predecessor();
   launch_dependents();
-  if (AGAIN && __ldcg(&a.words->again) == 0) return;
+  if (TIME == kAgain && __ldcg(&a.words->again) == 0) return;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  for (int64_t i = blockIdx.x; i < a.rows; i += gridDim.x) {
+  const int64_t n = rows_of(a), filled = filled_rows(a, n);
+  for (int64_t i = blockIdx.x; i < filled; i += gridDim.x) {
     const int32_t t = __ldcg(a.column + i);
+    const int64_t from = a.first + (a.place == nullptr ? i : i < n ? __ldcg(a.place + i) : 0);  // the caller's row
     const float zt = __ldcg(a.zt + i);
     float ref = __ldcg(a.ref + i), sum = 0.0f, top = -INFINITY;
     if (t != -1) {
@@ -343,8 +441,8 @@ __global__ void __launch_bounds__(kFinishThreads) loss_finish_kernel(const __gri
       sum += part[k].x;
       top = fmaxf(top, part[k].y);
     }
-    if (!AGAIN && t >= 0 && sum > kOneMore && isfinite(top)) {
-      if (a.alone) {
+    if (TIME != kAgain && t >= 0 && sum > kOneMore && isfinite(top)) {
+      if constexpr (TIME == kOnce) {
         ref = top;
         sum = a.vec ? row_again<true>(a, i, t, ref) : row_again<false>(a, i, t, ref);
         __syncthreads();  // part[] and the row are written
@@ -363,47 +461,74 @@ __global__ void __launch_bounds__(kFinishThreads) loss_finish_kernel(const __gri
     const float whole = sum + et;
     float loss = own ? log1pf(sum) : (ref - zt) + logf(whole);
     // a NaN is no column's, or of the inputs'; an infinite logit leaves no gradient
-    float f = (a.scale != nullptr ? __ldg(a.scale + a.first + i) : 1.0f) / whole;
+    float f = (a.scale != nullptr ? __ldg(a.scale + from) : 1.0f) / whole;
     if (!isfinite(whole)) f = NAN;
     if (t == -1) loss = f = 0.0f;
     if (t == -2) loss = f = NAN;
-    if (threadIdx.x == 0) a.losses[a.first + i] = loss;
+    if (threadIdx.x == 0 && i < n) a.losses[from] = loss;
     // (the pitch has room for whole vectors; an ignored row's are not read)
-    uint16_t* row = a.held + i * a.ldz;
-    constexpr int kSpan = 8 * kFinishThreads, U = 2;
-    for (int64_t j0 = 8 * threadIdx.x; j0 < a.vocab; j0 += U * kSpan) {
+    uint4* row = reinterpret_cast<uint4*>(a.held + i * a.ldz);
+    constexpr int U = TIME == kOnce ? 2 : 6;  // (2, 4, 6: 309, 280, 272 us; at 6 blocks an SM 281, 283, 379)
+    const uint32_t vectors = static_cast<uint32_t>((a.vocab + 7) / 8);
+    for (uint32_t j0 = threadIdx.x; j0 < vectors; j0 += U * kFinishThreads) {
       uint4 v[U];
 #pragma unroll
       for (int u = 0; u < U; ++u)
-        if (t != -1 && j0 + u * kSpan < a.vocab)
-          v[u] = __ldcs(reinterpret_cast<const uint4*>(row + j0 + u * kSpan));
+        if (t != -1 && j0 + u * kFinishThreads < vectors) v[u] = __ldcs(row + j0 + u * kFinishThreads);
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        const int64_t j = j0 + u * kSpan;
-        if (j >= a.vocab) break;
-        float y[8] = {};
+        const uint32_t j = j0 + u * kFinishThreads;
+        if (j >= vectors) break;
+        uint4 y = make_uint4(0, 0, 0, 0);
         if (t != -1) {
           const uint32_t w[4] = {v[u].x, v[u].y, v[u].z, v[u].w};
+          float x[8];
 #pragma unroll
           for (int c = 0; c < 8; ++c) {
             const int16_t d = static_cast<int16_t>(c % 2 ? w[c / 2] >> 16 : w[c / 2] & 0xffffu);
             const float e = fast_exp2(static_cast<float>(d) * (kLog2e / 1024.0f));
-            y[c] = d == INT16_MIN ? f * 0.0f : f * e;
+            x[c] = f * (d == INT16_MIN ? 0.0f : e);
           }
-          if (t - j >= 0 && t - j < 8) {
+          const uint32_t at = static_cast<uint32_t>(t) - 8 * j;
+          if (at < 8) {
 #pragma unroll
             for (int c = 0; c < 8; ++c)
-              if (j + c == t) y[c] = -(f * sum);
+              if (at == c) x[c] = -(f * sum);
           }
+          y = to_bf16x8(x);
         }
-        *reinterpret_cast<uint4*>(row + j) = to_bf16x8(y);
+        row[j] = y;
       }
     }
   }
   if (!last_block(a.words, &last)) return;
-  if (!AGAIN && threadIdx.x == 0) a.words->ticket = 0;
+  if (TIME == kFirst && threadIdx.x == 0) a.words->ticket = 0;
   // (the losses are complete after the second time, where there is one)
-  total_losses(a, a.total != nullptr && (AGAIN || __ldcg(&a.words->again) == 0));
+  total_losses(a, a.total != nullptr && (TIME != kFirst || __ldcg(&a.words->again) == 0));
+}
+
+// dx of every row of the piece from those that are not ignored; the others' is 0.  A warp a row.
+__global__ void __launch_bounds__(256) loss_spread_kernel(const __grid_constant__ LossArgs a) {
+  wait_for_predecessor();
+  launch_dependents();
+  if (a.direct && __ldcg(&a.words->rows) == a.rows) return;
+  const int lane = threadIdx.x % 32;
+  for (int64_t i = static_cast<int64_t>(blockIdx.x) * 8 + threadIdx.x / 32; i < a.rows;
+       i += static_cast<int64_t>(gridDim.x) * 8) {
+    const int32_t k = __ldcg(a.slot + i);
+    const uint16_t* from = a.dxc + (k < 0 ? 0 : k) * a.lddxc;
+    uint16_t* to = a.dx + i * a.lddx;
+    if (a.dx_vec) {
+#pragma unroll 4
+      for (int64_t j = 8 * lane; j + 8 <= a.width; j += 256)
+        *reinterpret_cast<uint4*>(to + j) =
+            k < 0 ? make_uint4(0, 0, 0, 0) : __ldcs(reinterpret_cast<const uint4*>(from + j));
+      for (int64_t j = a.width / 8 * 8 + lane; j < a.width; j += 32) to[j] = k < 0 ? 0 : from[j];
+    } else {
+#pragma unroll 4
+      for (int64_t j = lane; j < a.width; j += 32) to[j] = k < 0 ? 0 : from[j];
+    }
+  }
 }
 
 // dw (bf16) from the pieces' fp32 sums.
@@ -431,7 +556,7 @@ int64_t piece_rows(const zero_cross_entropy_t& s, bool grads) {
 // Where a call's arrays lie in its workspace.
 struct Layout {
   int64_t piece, parts;  // rows of a piece, and parts of the vocabulary at most
-  int64_t w, x, zt, held, sums, losses, acc, linear, bytes;
+  int64_t w, x, zt, held, sums, losses, acc, dxc, linear, bytes;
 };
 
 zero_linear_t linear_of(const zero_cross_entropy_t& s, int64_t rows) {
@@ -473,12 +598,13 @@ Layout make_layout(const zero_cross_entropy_t& s, int32_t flags) {
   l.w = take((flags & ZERO_LINEAR_ALIGNED) ? 0 : 2 * s.vocab * laid_out_pitch(s.width));
   // (the loss alone reads x in place, if it lies so; what it lies like is not known here)
   l.x = take(2 * l.piece * laid_out_pitch(s.width));
-  l.zt = take(12 * l.piece);  // zt, ref, column
+  l.zt = take(20 * l.piece);  // zt, ref, column, place, slot
   l.held = take(grads ? 2 * l.piece * laid_out_pitch(s.vocab) : 0);
   l.sums = take(8 * l.piece * l.parts);
   l.losses = take(4 * s.rows);
   const bool sums32 = grads && s.rows > l.piece && (flags & ZERO_GRAD_F32) == 0;
   l.acc = take(sums32 ? 4 * s.vocab * round_up(s.width, 4) : 0);
+  l.dxc = take(grads ? 2 * l.piece * laid_out_pitch(s.width) : 0);
   l.linear = at;
   if (grads && s.rows > 0) {
     constexpr int32_t kind = ZERO_LINEAR_BACKWARD | ZERO_LINEAR_ALIGNED | ZERO_LINEAR_PLAIN;
@@ -531,6 +657,12 @@ cudaError_t launch_cross_entropy(const CrossEntropyLaunch& L) {
   a.zt = reinterpret_cast<float*>(base + l.zt);
   a.ref = a.zt + l.piece;
   a.column = reinterpret_cast<int32_t*>(a.ref + l.piece);
+  int32_t* const place = a.column + l.piece;
+  a.slot = place + l.piece;
+  a.dxc = reinterpret_cast<uint16_t*>(base + l.dxc);
+  a.lddxc = laid_out_pitch(s.width);
+  a.lddx = s.lddx;
+  a.dx_vec = aligned(L.dx, 16) && s.lddx % 8 == 0;
   a.xc = reinterpret_cast<uint16_t*>(base + l.x);
   a.ldxc = laid_out_pitch(s.width);
   a.sums = reinterpret_cast<const float2*>(base + l.sums);
@@ -589,7 +721,13 @@ cudaError_t launch_cross_entropy(const CrossEntropyLaunch& L) {
                          kFinishThreads, 0, 1, a);
       continue;
     }
-    e = chain.launch(a.vec ? loss_rows_kernel<true> : loss_rows_kernel<false>,
+    a.place = a.alone ? nullptr : place;
+    zero_linear_t b_shape = linear_of(s, a.rows);
+    a.fill = L.dw != nullptr ? least_rows(b_shape, L.dx != nullptr) : 0;
+    a.dx = L.dx != nullptr ? L.dx + first * s.lddx : nullptr;
+    if (!a.alone) e = chain.launch(loss_places_kernel, dim3(1), 32 * kPlaceWarps, 0, 1, a);
+    if (e == cudaSuccess)
+      e = chain.launch(a.vec ? loss_rows_kernel<true> : loss_rows_kernel<false>,
                      blocks_of((a.rows + 7) / 8, 16 * kSms), 256, 0, 1, a);
     x.x = a.xc;
     x.ldx = a.ldxc;
@@ -597,21 +735,33 @@ cudaError_t launch_cross_entropy(const CrossEntropyLaunch& L) {
     x.of.target = a.column;
     x.out = a.held;
     x.ldo = a.ldz;
+    x.rows_now = a.alone ? nullptr : &a.words->rows;
     if (e == cudaSuccess) e = launch_exponents(x);
-    const dim3 grid = blocks_of(a.rows, 8 * kSms);
-    if (e == cudaSuccess) e = chain.launch(loss_finish_kernel<false>, grid, kFinishThreads, 0, 1, a);
+    const dim3 grid = blocks_of(a.rows, (a.alone ? 2 : kFinishBlocks) * kSms);
+    if (e == cudaSuccess)
+      e = chain.launch(a.alone ? loss_finish_kernel<kOnce> : loss_finish_kernel<kFirst>, grid, kFinishThreads, 0, 1, a);
     x.of.only_if = &a.words->again;
     if (e == cudaSuccess && !a.alone) e = launch_exponents(x);
     if (e == cudaSuccess && !a.alone)
-      e = chain.launch(loss_finish_kernel<true>, blocks_of(a.rows, 2 * kSms), kFinishThreads, 0, 1, a);
+      e = chain.launch(loss_finish_kernel<kAgain>, blocks_of(a.rows, 2 * kSms), kFinishThreads, 0, 1, a);
     if (e != cudaSuccess) return e;
     LinearBackwardLaunch b{};
-    b.s = linear_of(s, a.rows);
+    b.s = b_shape;
     b.s.ldw = ldw;
     b.dy = a.held;
     b.x = a.xc;
     b.w = w;
-    b.dx = L.dx != nullptr ? L.dx + first * s.lddx : nullptr;
+    b.dx = a.dx;
+    if (a.dx != nullptr && !a.alone) {
+      a.direct = a.dx_vec && a.rows > 1 && whole_in_place(b.s, L.dw != nullptr);
+      if (a.direct) {
+        b.dx_all = a.dx;
+        b.ld_all = s.lddx;
+      }
+      b.dx = a.dxc;
+      b.s.lddx = a.lddxc;
+    }
+    b.rows_now = x.rows_now;
     b.dw = joined ? acc : L.dw;
     if (joined) b.s.lddw = round_up(s.width, 4);
     b.grad_f32 = L.grad_f32 || joined;
@@ -621,6 +771,8 @@ cudaError_t launch_cross_entropy(const CrossEntropyLaunch& L) {
     b.stream = L.stream;
     b.withhold = L.withhold;
     e = launch_linear_backward(b);
+    if (e == cudaSuccess && a.dx != nullptr && !a.alone)
+      e = chain.launch(loss_spread_kernel, blocks_of((a.rows + 7) / 8, 16 * kSms), 256, 0, 1, a);
   }
   if (e == cudaSuccess && joined)
     e = chain.launch(loss_round_kernel, blocks_of(s.vocab, 16 * kSms), 256, 0, 1, acc,

@@ -44,6 +44,34 @@ struct ProductArgs {
   int32_t early_units;   // units that the predecessor leaves idle in its last round,
   int32_t early_tiles;   // and tiles they do meanwhile
   ExponentOf x;          // of kExponent
+  CUtensorMap all;          // D if all rows are there, where that is another place
+  int32_t elsewhere;        // it is
+  const int32_t* rows_now;  // how many rows there are (a_mn: of the reduction), at most those
+                            // planned for; NULL: all
+  int32_t least_steps;      // of the reduction, whatever rows_now says: its parts have some
+};
+
+// What of a plan there is to do: rows, rows of tiles and stages, and the items of those.
+template <int BM, bool A_MN>
+struct Extent {
+  int64_t rows;
+  int tiles_m, steps, items;
+  __device__ __forceinline__ explicit Extent(const ProductArgs& a)
+      : rows(a.rows), tiles_m(a.tiles_m), steps(a.steps) {
+    if (a.rows_now != nullptr) {
+      const int n = __ldcg(a.rows_now);
+      if constexpr (A_MN) {
+        const int need = (n + kStep - 1) / kStep;
+        steps = need > a.least_steps ? need : a.least_steps;
+        steps = steps < a.steps ? steps : a.steps;
+      } else {
+        rows = n;
+        tiles_m = (n + BM - 1) / BM;
+      }
+    }
+    const int tiles = tiles_m * a.tiles_n;
+    items = tiles <= a.whole ? tiles : a.whole + (tiles - a.whole) * a.splits;
+  }
 };
 
 struct Tile {
@@ -56,26 +84,26 @@ struct Tile {
 // tiles in flight at one time share their operands in L2; after the first
 // `whole` of them each tile is `splits` items, one for each part of the
 // reduction, so that the last round of tiles keeps every SM busy.
-__device__ __forceinline__ void part_of(const ProductArgs& a, int t, Tile& r) {
+__device__ __forceinline__ void part_of(const ProductArgs& a, int steps, int t, Tile& r) {
   r.part = -1;
   r.first = 0;
-  r.last = a.steps;
+  r.last = steps;
   if (t >= a.whole && a.splits > 1) {
     r.part = t - a.whole;
     const int part = r.part % a.splits;
-    r.first = static_cast<int>(static_cast<int64_t>(a.steps) * part / a.splits);
-    r.last = static_cast<int>(static_cast<int64_t>(a.steps) * (part + 1) / a.splits);
+    r.first = static_cast<int>(static_cast<int64_t>(steps) * part / a.splits);
+    r.last = static_cast<int>(static_cast<int64_t>(steps) * (part + 1) / a.splits);
   }
 }
 template <int BM>
-__device__ __forceinline__ Tile tile_of(const ProductArgs& a, int t) {
+__device__ __forceinline__ Tile tile_of(const ProductArgs& a, int tiles_m, int steps, int t) {
   constexpr int kGroup = 8;
   Tile r;
-  part_of(a, t, r);
+  part_of(a, steps, t, r);
   if (t >= a.whole) t = a.whole + (t - a.whole) / a.splits;
   const int group = t / (kGroup * a.tiles_n);
   const int m0 = group * kGroup;
-  const int height = a.tiles_m - m0 < kGroup ? a.tiles_m - m0 : kGroup;
+  const int height = tiles_m - m0 < kGroup ? tiles_m - m0 : kGroup;
   const int in = t - group * kGroup * a.tiles_n;
   r.row = static_cast<int64_t>(m0 + in % height) * BM;
   r.col = static_cast<int64_t>(in / height) * a.bn;
@@ -202,6 +230,7 @@ struct EpiloguePart {
   bool pre, add;     // pre is written; what is read is added
   int slot = 0;
   uint4 in[4], bias[4];
+  const CUtensorMap* out = nullptr;  // NULL: ProductArgs' own
 
   __device__ __forceinline__ explicit EpiloguePart(const Epilogue& e)
       : from(nullptr), bias_from(nullptr), from_pitch(0), act(ZERO_ACT_NONE), pre(false), add(true) {
@@ -295,7 +324,7 @@ struct EpiloguePart {
         else if (act == ZERO_ACT_SILU) times_slope<ZERO_ACT_SILU>(v);
         else if (act == ZERO_ACT_RELU) times_slope<ZERO_ACT_RELU>(v);
       }
-      send(&a.out, staging, v, col, row, lane);
+      send(out != nullptr ? out : &a.out, staging, v, col, row, lane);
     }
   }
 };
@@ -686,7 +715,6 @@ __global__ void __launch_bounds__(kProductThreads, 1)
   const uint32_t rank = CG == 2 ? cluster_rank() : 0u;
   const int unit = blockIdx.x / CG;
   const Turns turns{a.early_units, a.early_tiles, static_cast<int>(gridDim.x) / CG};
-  const int tiles = a.whole + (a.tiles_m * a.tiles_n - a.whole) * a.splits;
 
   if constexpr (KIND == kExponent)
     if (a.x.only_if != nullptr) {  // alike for every thread of the grid
@@ -719,13 +747,18 @@ __global__ void __launch_bounds__(kProductThreads, 1)
   if constexpr (CG == 2) cluster_sync();
   tc_fence_after();
   const uint32_t tmem = *tmem_at;
+  // (what rows_now says was there before this kernel's predecessor began)
+  const Extent<BM, A_MN> extent(a);
+  const int tiles = extent.items;
+  const auto tile_at = [&](int t) { return tile_of<BM>(a, extent.tiles_m, extent.steps, t); };
 
   if (warp == 0) {
     if (lane == 0) {
       Place at(stages);
       int issued = 0;  // stages, up to the ring's
       bool ok = true;
-      Tile next = tile_of<BM>(a, turns.first(unit));
+      Tile next{};
+      if (turns.first(unit) < tiles) next = tile_at(turns.first(unit));
       for (int t = turns.first(unit); t < tiles && ok; t = turns.after(t)) {
         const Tile tile = next;
         const int ra = static_cast<int>(tile.row) + rank * kBlockRows;
@@ -740,7 +773,7 @@ __global__ void __launch_bounds__(kProductThreads, 1)
             ++issued;
           }
           if (a.withhold) {
-            if (step == tile.first && turns.after(t) < tiles) next = tile_of<BM>(a, turns.after(t));
+            if (step == tile.first && turns.after(t) < tiles) next = tile_at(turns.after(t));
             continue;
           }
           const uint32_t bar = CG == 2 ? peer_addr(&full[at.s], 0) : smem_addr(&full[at.s]);
@@ -765,7 +798,7 @@ __global__ void __launch_bounds__(kProductThreads, 1)
             }
           }
           // (off the path from one tile's last loads to the next one's first)
-          if (step == tile.first && turns.after(t) < tiles) next = tile_of<BM>(a, turns.after(t));
+          if (step == tile.first && turns.after(t) < tiles) next = tile_at(turns.after(t));
         }
       }
       if (!ok) atomicExch(&g_linear_status, 1);
@@ -795,7 +828,7 @@ __global__ void __launch_bounds__(kProductThreads, 1)
       bool ok = true;
       for (int t = turns.first(unit); t < tiles && ok; t = turns.after(t)) {
         Tile tile;
-        part_of(a, t, tile);
+        part_of(a, extent.steps, t, tile);
         for (int step = tile.first; step < tile.last && ok; ++n) {
           const int first = step;
           const int last = tile.last - step > kChain<KIND> ? step + kChain<KIND> : tile.last;
@@ -839,6 +872,8 @@ __global__ void __launch_bounds__(kProductThreads, 1)
     const int quarter = warp % 4, half = (warp - 2) / 4;
     float* mine = staging + (warp - 2) * 32 * 32;
     std::conditional_t<ROWS, RowsPart<KIND>, EpiloguePart<KIND>> part(a.e);
+    if constexpr (KIND == kGradient && !A_MN && !ROWS)
+      if (a.elsewhere && extent.rows == a.rows) part.out = &a.all;
     const bool vec = a.e.vec != 0;
     const int bn = a.bn;
     // The columns of a tile that are this warp's, 32 at a time: every other 32, or half
@@ -849,7 +884,7 @@ __global__ void __launch_bounds__(kProductThreads, 1)
     const int c_first = 32 * half * (kBeside ? (bn / 32 + 1) / 2 : 1);
     const int c_end = kBeside && half == 0 ? (bn / 32 + 1) / 2 * 32 : bn;
     constexpr int c_step = kBeside ? 32 : 64;
-    const int64_t rows = a.rows, cols = a.cols;
+    const int64_t rows = extent.rows, cols = a.cols;
     const uint32_t lanes = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
     // This half of tensor memory has been read by the warp and may be written again.
     const auto release = [&](int b) {
@@ -867,7 +902,7 @@ __global__ void __launch_bounds__(kProductThreads, 1)
     const bool scaled = (KIND == kGradient || KIND == kFloat) && a.e.scale != nullptr;
     const float scale = scaled ? __ldcg(a.e.scale) : 1.0f;
     for (int t = turns.first(unit); t < tiles && ok; t = turns.after(t)) {
-      const Tile tile = tile_of<BM>(a, t);
+      const Tile tile = tile_at(t);
       const int64_t row0 = tile.row + rank * kBlockRows + quarter * 32;
       // (rows past the end are left out by the copy)
       const bool any = row0 < rows;
@@ -1044,17 +1079,19 @@ __global__ void __launch_bounds__(kProductThreads, 1)
       bool ok = true;
       for (int s = 0; s < a.splits; ++s)
         ok = ok && peer_load_u32(peer_addr(failed, s)) == 0;
-      const Tile tile = tile_of<BM>(a, unit);
+      Tile tile{};
+      if (unit < tiles) tile = tile_at(unit);
+      ok = ok && unit < tiles;
       const int64_t row0 = tile.row + quarter * 32;
       std::conditional_t<ROWS, RowsPart<KIND>, EpiloguePart<KIND>> part(a.e);
       for (int c = 32 * (mine_of + a.splits * half); c < a.bn; c += 64 * a.splits) {
         const int64_t col0 = tile.col + c;
-        if (!ok || row0 >= a.rows || col0 >= a.cols) break;
+        if (!ok || row0 >= extent.rows || col0 >= a.cols) break;
         const int64_t end = a.cols < col0 + 32 ? a.cols : col0 + 32;
         const bool whole = ROWS ? end - col0 >= 8 : a.e.vec && col0 + 32 <= a.cols;
         if (whole) {
-          if constexpr (ROWS) part.ask(row0 + lane, col0, row0 + lane < a.rows, col0, end, lane);
-          else part.ask(row0 + lane, col0, row0 + lane < a.rows);
+          if constexpr (ROWS) part.ask(row0 + lane, col0, row0 + lane < extent.rows, col0, end, lane);
+          else part.ask(row0 + lane, col0, row0 + lane < extent.rows);
         }
         const float* from = reinterpret_cast<const float*>(ring) + (c / 32 * 4 + quarter) * 32 * 32;
         // A load takes 4 whole rows, two parts at a time (16 bytes of 32 rows, a row a
@@ -1087,12 +1124,12 @@ __global__ void __launch_bounds__(kProductThreads, 1)
           }
           __syncwarp();
           if constexpr (ROWS)
-            part.put(mine, x, row0, a.rows, col0, col0, end, lane);
+            part.put(mine, x, row0, extent.rows, col0, col0, end, lane);
           else
             part.put(a, reinterpret_cast<uint8_t*>(mine), x, static_cast<int>(row0),
                      static_cast<int>(col0), lane);
         } else {
-          epilogue_scalar<KIND>(a.e, mine, row0, col0, a.rows, a.cols, lane);
+          epilogue_scalar<KIND>(a.e, mine, row0, col0, extent.rows, a.cols, lane);
           __syncwarp();
         }
       }
@@ -1109,18 +1146,20 @@ __global__ void __launch_bounds__(kProductThreads, 1)
 
 // The parts of the tiles whose reduction was split, added in their order, and the
 // epilogue: 8 columns a thread.
-template <int BM>
+template <int BM, bool A_MN>
 __global__ void __launch_bounds__(256) linear_join_kernel(const __grid_constant__ ProductArgs a,
                                                           const float* parts) {
   const int per_row = a.bn / 8;
   const int u = blockIdx.y;  // of the tiles split
-  const Tile tile = tile_of<BM>(a, a.whole + u * a.splits);
+  const Extent<BM, A_MN> extent(a);
+  Tile tile{extent.rows, 0, 0, 0, 0};
+  if (a.whole + u * a.splits < extent.items) tile = tile_of<BM>(a, extent.tiles_m, extent.steps, a.whole + u * a.splits);
   const int in = blockIdx.x * 256 + threadIdx.x;
   const int r = in / per_row, c = in % per_row * 8;
   const int64_t i = tile.row + r, j = tile.col + c;
   wait_for_predecessor();
   launch_dependents();
-  if (r >= BM || i >= a.rows || j >= a.cols) return;
+  if (r >= BM || i >= extent.rows || j >= a.cols) return;
   const Epilogue& e = a.e;
   const bool vec = e.vec && j + 8 <= a.cols;
   float x[8] = {};
@@ -1396,7 +1435,13 @@ struct Product {
   bool a_mn, b_mn;
   int64_t rows, cols, depth;
   Epilogue e;
+  const int32_t* rows_now;  // as in ProductArgs
+  uint16_t* all;            // D if all rows are there; NULL: e.out anyhow
+  int64_t ld_all;
 };
+
+// Stages that leave each part of a tile's reduction two.
+int32_t least_steps(const Plan& plan) { return plan.splits > 1 ? 2 * plan.splits : 1; }
 
 // A product under way: what its join needs, where its reduction is split.
 struct Pending {
@@ -1404,6 +1449,7 @@ struct Pending {
   Plan plan;
   int64_t rows;
   float* parts;
+  bool a_mn;
 };
 
 template <int CG, bool A_MN, bool B_MN, Kind KIND, bool ROWS, bool GATHER = false>
@@ -1455,8 +1501,11 @@ cudaError_t launch_join(const Pending& w, Chain* chain) {
   if (w.plan.splits == 1 || w.plan.gather) return cudaSuccess;
   const int64_t high = w.rows < w.plan.cg * kBlockRows ? w.rows : w.plan.cg * kBlockRows;
   const dim3 grid(static_cast<unsigned>((high * (w.plan.bn / 8) + 255) / 256), w.plan.tail);
-  return w.plan.cg == 2 ? chain->launch(linear_join_kernel<256>, grid, 256, 0, 1, w.a, w.parts)
-                        : chain->launch(linear_join_kernel<128>, grid, 256, 0, 1, w.a, w.parts);
+  if (w.a_mn)
+    return w.plan.cg == 2 ? chain->launch(linear_join_kernel<256, true>, grid, 256, 0, 1, w.a, w.parts)
+                          : chain->launch(linear_join_kernel<128, true>, grid, 256, 0, 1, w.a, w.parts);
+  return w.plan.cg == 2 ? chain->launch(linear_join_kernel<256, false>, grid, 256, 0, 1, w.a, w.parts)
+                        : chain->launch(linear_join_kernel<128, false>, grid, 256, 0, 1, w.a, w.parts);
 }
 
 template <bool A_MN, bool B_MN, Kind KIND>
@@ -1489,6 +1538,7 @@ cudaError_t launch_product(Product p, const Plan& plan, bool late, Space* space,
   *w = Pending{};
   w->plan = plan;
   w->rows = p.rows;
+  w->a_mn = p.a_mn;
   w->parts = static_cast<float*>(space->take(plan.part_bytes()));
   ProductArgs& a = w->a;
   a.e = p.e;
@@ -1497,6 +1547,8 @@ cudaError_t launch_product(Product p, const Plan& plan, bool late, Space* space,
   a.steps = static_cast<int32_t>((p.depth + kStep - 1) / kStep);
   a.withhold = withhold;
   a.late = late;
+  a.rows_now = p.rows_now;
+  a.least_steps = least_steps(plan);
   const bool f32 = a.e.out_f32 != 0;
   if (a.e.vec) {
     // a matrix of one row has any pitch
@@ -1507,6 +1559,11 @@ cudaError_t launch_product(Product p, const Plan& plan, bool late, Space* space,
     if (e == cudaSuccess && a.e.pre != nullptr)
       e = make_out_map(&a.pre, a.e.pre, p.rows, p.cols, p.rows > 1 ? a.e.ldp : one, 1, stride, false);
     if (e != cudaSuccess) return e;
+  }
+  if (p.all != nullptr) {
+    const cudaError_t e = make_out_map(&a.all, p.all, p.rows, p.cols, p.ld_all, 1, p.rows * p.ld_all, false);
+    if (e != cudaSuccess) return e;
+    a.elsewhere = 1;
   }
   if (p.a_mn)
     return f32 ? launch_kind<true, true, kFloat>(p, w, chain)
@@ -1807,6 +1864,16 @@ cudaError_t launch_lay_out(const uint16_t* p, int64_t rows, int64_t cols, int64_
   return lay_out(all, 1, &space, &chain);
 }
 
+int64_t least_rows(const zero_linear_t& s, bool dx) {
+  return int64_t{kStep} * least_steps(known_plan_backward(s, dx, true).dw);
+}
+
+bool whole_in_place(const zero_linear_t& s, bool dw) {
+  // (no tile's edge is written element by element, and none joined by another kernel)
+  const Plan plan = known_plan_backward(s, true, dw).dx;
+  return s.in % 32 == 0 && plan.splits == 1;
+}
+
 int64_t exponent_parts(int64_t rows, int64_t vocab, int64_t width) {
   const int bn = plan_exponents(rows, vocab, width).bn;
   return (vocab + bn - 1) / bn * 2;
@@ -1832,6 +1899,7 @@ cudaError_t launch_exponents(const ExponentLaunch& L) {
   a.steps = static_cast<int32_t>((p.depth + kStep - 1) / kStep);
   a.withhold = L.withhold;
   a.x = L.of;
+  a.rows_now = L.rows_now;
   if (L.out != nullptr) {
     const int64_t ld = L.rows > 1 ? L.ldo : round_up(L.vocab, 8);
     const cudaError_t e = make_out_map(&a.out, L.out, L.rows, L.vocab, ld, 1, L.rows * ld, false);
@@ -1981,6 +2049,9 @@ cudaError_t launch_linear_backward(const LinearBackwardLaunch& L) {
     p.e.out = L.dx;
     p.e.ldo = s.lddx;
     p.e.scale = L.scale;
+    p.rows_now = L.rows_now;
+    p.all = L.dx_all;
+    p.ld_all = L.ld_all;
     // dbias's kernel has waited for all that this one reads before it let it begin
     e = launch_product(p, plan.dx, L.dbias != nullptr, &space, L.withhold, &chain, &dx);
     if (e != cudaSuccess) return e;
@@ -1997,6 +2068,7 @@ cudaError_t launch_linear_backward(const LinearBackwardLaunch& L) {
     p.e.out = L.dw;
     p.e.ldo = s.lddw;
     p.e.scale = L.scale;
+    p.rows_now = L.rows_now;
     p.e.out_f32 = L.grad_f32;
     p.e.accumulate = L.accumulate;
     // (and so have dx's product, or what came before that)

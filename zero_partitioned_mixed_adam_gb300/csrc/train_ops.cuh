@@ -82,7 +82,15 @@ struct LinearBackwardLaunch {
   cudaStream_t stream;
   int32_t withhold;
   const float* scale;  // of dx and dw, one number on the device; NULL: 1
+  // How many of the rows there are, on the device; NULL: all.  What lies behind them in dx is
+  // left anyhow; in dy and x rows up to the next multiple of 128, and least_rows, are 0.
+  const int32_t* rows_now;
+  uint16_t* dx_all;    // dx in its place if all rows are there; NULL: it goes to dx anyhow
+  int64_t ld_all;
 };
+int64_t least_rows(const zero_linear_t& s, bool dx);
+// Whether dx_all may be given, for a dx_all that TMA can write.
+bool whole_in_place(const zero_linear_t& s, bool dw);
 
 // ------------------------------------------- exponentials of a linear map's rows
 
@@ -108,6 +116,7 @@ struct ExponentLaunch {
   ExponentOf of;
   uint16_t* out;          // [rows][ldo], in 2^-10, -32 and below as -32768
   int64_t ldo;
+  const int32_t* rows_now;  // how many of the rows there are, on the device; NULL: all
   cudaStream_t stream;
   int32_t withhold;
 };
