@@ -407,7 +407,8 @@ __device__ __forceinline__ void begin_sums(float (*part)[RowSum<SHARE>::kParts][
   if constexpr (SHARE == kCluster) cluster_sync();
 }
 
-// What norms and gate there are, in one register.
+// What norms and gate there are, in one register.  LAYER: there may be norms of that kind.
+template <bool LAYER>
 struct Kinds {
   uint32_t bits;
   __device__ __forceinline__ explicit Kinds(const NormArgs& a)
@@ -415,14 +416,14 @@ struct Kinds {
              (a.post != ZERO_NORM_NONE ? 4u : 0u) | (a.gate != nullptr ? 8u : 0u)) {
     keep(bits);
   }
-  __device__ __forceinline__ bool layer() const { return (bits & 1u) != 0; }
-  __device__ __forceinline__ bool post_layer() const { return (bits & 2u) != 0; }
+  __device__ __forceinline__ bool layer() const { return LAYER && (bits & 1u) != 0; }
+  __device__ __forceinline__ bool post_layer() const { return LAYER && (bits & 2u) != 0; }
   __device__ __forceinline__ bool post() const { return (bits & 4u) != 0; }
   __device__ __forceinline__ bool gated() const { return (bits & 8u) != 0; }  // by a vector
 };
 
-// BIAS: there are biases.
-template <bool VEC, Share SHARE, bool BIAS>
+// LAYER: there are norms of that kind, or biases, which are theirs.
+template <bool VEC, Share SHARE, bool LAYER>
 __global__ void __launch_bounds__(kMostThreads, 2)
     block_norm_forward_kernel(const __grid_constant__ NormArgs a) {
   __shared__ float part[2][RowSum<SHARE>::kParts][kSumsAtOnce];
@@ -435,12 +436,12 @@ __global__ void __launch_bounds__(kMostThreads, 2)
   rows.begin();
   const Output<VEC> s_out(a.s_out, a.pitch_s), y_out(a.y, a.pitch_y);
   const bool wvec = a.wvec != 0;
-  const Kinds kinds(a);
+  const Kinds<LAYER> kinds(a);
   // s = r + (h standardized * scale1 + bias1) [* gate's row]
   Eight scale1 = at.load_vector(a.gate, 1.0f, wvec) * a.alpha, bias1 = all_of(0.0f);
-  if constexpr (BIAS) bias1 = at.load_vector(a.b1, 0.0f, wvec) * scale1;
+  if constexpr (LAYER) bias1 = at.load_vector(a.b1, 0.0f, wvec) * scale1;
   scale1 = scale1 * at.load_vector(a.w1, 1.0f, wvec);
-  const Eight w = at.load_vector(a.w, 1.0f, wvec), b = BIAS ? at.load_vector(a.b, 0.0f, wvec) : all_of(0.0f);
+  const Eight w = at.load_vector(a.w, 1.0f, wvec), b = LAYER ? at.load_vector(a.b, 0.0f, wvec) : all_of(0.0f);
   begin_sums<SHARE>(part);
   RowSum<SHARE> row_sum{part};
   const float inv_width = 1.0f / static_cast<float>(a.width);
@@ -466,10 +467,10 @@ __global__ void __launch_bounds__(kMostThreads, 2)
       }
       if (rows.has(kInGate)) {
         Eight p = h * scale1;
-        if constexpr (BIAS) p = p + bias1;
+        if constexpr (LAYER) p = p + bias1;
         s = fma8(p, rows.read(kInGate, i, 2), s);
       } else {
-        if constexpr (BIAS) s = s + bias1;
+        if constexpr (LAYER) s = s + bias1;
         s = fma8(h, scale1, s);
       }
     }
@@ -479,7 +480,7 @@ __global__ void __launch_bounds__(kMostThreads, 2)
       center(s);
     }
     s = s * inverse_of(s);
-    if constexpr (BIAS) s = fma8(s, w, b);
+    if constexpr (LAYER) s = fma8(s, w, b);
     else s = s * w;
     y_out.put(at, i, s);
   }
@@ -490,9 +491,8 @@ __global__ void __launch_bounds__(kMostThreads, 2)
 // columns of each, whose sums over the rows stay in their registers until the end.  With xh
 // the standardized row, u what reaches it and m its means,
 //   x's gradient = (u - m(u) [LAYER] - xh m(u xh)) / root.
-// FULL: there is a norm after the block, or a gate: h is read.  BIAS: sums of biases, or
-// a bias under a gate.
-template <bool VEC, Share SHARE, bool FULL, bool BIAS>
+// FULL: there is a norm after the block, or a gate: h is read.
+template <bool VEC, Share SHARE, bool FULL, bool LAYER>
 __global__ void __launch_bounds__(kMostThreads)
     block_norm_backward_kernel(const __grid_constant__ NormArgs a) {
   __shared__ float part[2][RowSum<SHARE>::kParts][kSumsAtOnce];
@@ -505,7 +505,7 @@ __global__ void __launch_bounds__(kMostThreads)
   rows.begin();
   const Output<VEC> dr_out(a.dr, a.pitch_dr), dh_out(a.dh, a.pitch_dh), dgate_out(a.dgate_rows, a.pitch_dg);
   const bool wvec = a.wvec != 0;
-  const Kinds kinds(a);
+  const Kinds<LAYER> kinds(a);
   const Held w(at, a.w, wvec), w1(at, FULL ? a.w1 : nullptr, wvec), g(at, FULL ? a.gate : nullptr, wvec);
   Eight dw = all_of(0.0f), db = dw, dg = dw, dw1 = dw, db1 = dw;
   begin_sums<SHARE>(part);
@@ -559,7 +559,7 @@ __global__ void __launch_bounds__(kMostThreads)
       const float along = q[4 * r + 1] * inverse * inv_width;
       x[r] = x[r] * inverse;  // standardized
       dw = fma8(u[r], x[r], dw);
-      if constexpr (BIAS) db = db + u[r];
+      if constexpr (LAYER) db = db + u[r];
       x[r] = fma8(x[r], all_of(-along), u[r] * w.get());
       if (layer) x[r] = x[r] + all_of(-q[4 * r + 2] * inv_width);
       if (has_ds) x[r] = fma8(x[r], all_of(inverse), rows.read(kInDs, i, 2, r));
@@ -574,7 +574,7 @@ __global__ void __launch_bounds__(kMostThreads)
         const bool matrix = rows.has(kInGate);
         if (matrix || kinds.gated()) {
           Eight t = h[r] * w1.get();
-          if constexpr (BIAS) t = t + at.load_vector(a.b1, 0.0f, wvec);
+          if constexpr (LAYER) t = t + at.load_vector(a.b1, 0.0f, wvec);
           if (matrix) {
             dgate_out.put(at, i, x[r] * t);
             x[r] = x[r] * rows.read(kInGate, i, 3 + has_ds, r);
@@ -585,7 +585,7 @@ __global__ void __launch_bounds__(kMostThreads)
         }
         if (post) {
           dw1 = fma8(x[r], h[r], dw1);
-          if constexpr (BIAS) db1 = db1 + x[r];
+          if constexpr (LAYER) db1 = db1 + x[r];
           x[r] = x[r] * w1.get();
           at.clear(x[r]);
           m[2 * r] = dot8(x[r], h[r]);
@@ -625,11 +625,11 @@ __global__ void __launch_bounds__(kMostThreads)
     }
   };
   put(kDw, dw);
-  if constexpr (BIAS) put(kDb, db);
+  if constexpr (LAYER) put(kDb, db);
   if constexpr (FULL) {
     put(kDgate, dg);
     put(kDw1, dw1);
-    if constexpr (BIAS) put(kDb1, db1);
+    if constexpr (LAYER) put(kDb1, db1);
   }
   if constexpr (SHARE == kCluster) cluster_sync();  // no block ends while others write to it
 }
@@ -733,6 +733,9 @@ constexpr int kMostRing = kStages * kInputs * kMostThreads * 16;
 static_assert(kMostRing + 8192 <= kSmem, "the ring and the parts of the sums");
 int ring_bytes(const NormArgs& a, int threads) { return kStages * a.inputs * threads * 16; }
 
+// (Biases are LAYER's.)
+bool has_layer(const NormArgs& a) { return a.kind == ZERO_NORM_LAYER || a.post == ZERO_NORM_LAYER; }
+
 // Whether rows of every matrix lie on 16-byte boundaries; and how many inputs there are.
 struct Rows16 {
   int64_t rows;
@@ -759,17 +762,17 @@ cudaError_t launch_ring(Kernel kernel, int64_t blocks, int threads, int smem, in
   return chain->launch(kernel, dim3(static_cast<unsigned>(blocks * cluster)), threads, smem, cluster, a);
 }
 
-template <bool FULL, bool BIAS>
+template <bool FULL, bool LAYER>
 cudaError_t launch_backward(const NormArgs& a, bool vec, Chain* chain) {
   const RowShape r = row_shape(a.width);
-  const auto kernel = vec ? (r.cluster == 1 ? block_norm_backward_kernel<true, kBlock, FULL, BIAS>
-                                            : block_norm_backward_kernel<true, kCluster, FULL, BIAS>)
-                          : (r.cluster == 1 ? block_norm_backward_kernel<false, kBlock, FULL, BIAS>
-                                            : block_norm_backward_kernel<false, kCluster, FULL, BIAS>);
+  const auto kernel = vec ? (r.cluster == 1 ? block_norm_backward_kernel<true, kBlock, FULL, LAYER>
+                                            : block_norm_backward_kernel<true, kCluster, FULL, LAYER>)
+                          : (r.cluster == 1 ? block_norm_backward_kernel<false, kBlock, FULL, LAYER>
+                                            : block_norm_backward_kernel<false, kCluster, FULL, LAYER>);
   return launch_ring(kernel, a.blocks, r.threads, vec ? ring_bytes(a, r.threads) : 0, r.cluster, a, chain);
 }
 
-template <bool BIAS>
+template <bool LAYER>
 cudaError_t launch_forward(const NormArgs& a, bool vec, Chain* chain) {
   const RowShape r = row_shape(a.width);
   const int smem = vec ? ring_bytes(a, r.threads) : 0;
@@ -777,10 +780,10 @@ cudaError_t launch_forward(const NormArgs& a, bool vec, Chain* chain) {
   if (each > 24) each = 24;
   if (each > kSmem / (smem + 2560)) each = kSmem / (smem + 2560);
   const int64_t most = each * kSms / r.cluster;
-  const auto kernel = vec ? (r.cluster == 1 ? block_norm_forward_kernel<true, kBlock, BIAS>
-                                            : block_norm_forward_kernel<true, kCluster, BIAS>)
-                          : (r.cluster == 1 ? block_norm_forward_kernel<false, kBlock, BIAS>
-                                            : block_norm_forward_kernel<false, kCluster, BIAS>);
+  const auto kernel = vec ? (r.cluster == 1 ? block_norm_forward_kernel<true, kBlock, LAYER>
+                                            : block_norm_forward_kernel<true, kCluster, LAYER>)
+                          : (r.cluster == 1 ? block_norm_forward_kernel<false, kBlock, LAYER>
+                                            : block_norm_forward_kernel<false, kCluster, LAYER>);
   return launch_ring(kernel, a.rows < most ? a.rows : most, r.threads, smem, r.cluster, a, chain);
 }
 
@@ -799,8 +802,7 @@ cudaError_t launch_block_norm_forward(const BlockNormLaunch& L) {
   vec(a.s_out, a.pitch_s);
   vec(a.y, a.pitch_y);
   Chain chain{L.stream};
-  return a.b1 != nullptr || a.b != nullptr ? launch_forward<true>(a, vec.all, &chain)
-                                           : launch_forward<false>(a, vec.all, &chain);
+  return has_layer(a) ? launch_forward<true>(a, vec.all, &chain) : launch_forward<false>(a, vec.all, &chain);
 }
 
 cudaError_t launch_block_norm_backward(const BlockNormLaunch& L) {
@@ -832,10 +834,10 @@ cudaError_t launch_block_norm_backward(const BlockNormLaunch& L) {
     vec(a.dgate_rows, a.pitch_dg);
     a.sums = static_cast<float*>(L.workspace);
     a.blocks = static_cast<int32_t>(backward_blocks(a.rows, a.width));
-    const bool bias = L.dbias != nullptr || L.dpost_bias != nullptr || a.b1 != nullptr;
-    e = full ? (bias ? launch_backward<true, true>(a, vec.all, &chain)
+    const bool layer = has_layer(a);
+    e = full ? (layer ? launch_backward<true, true>(a, vec.all, &chain)
                      : launch_backward<true, false>(a, vec.all, &chain))
-             : (bias ? launch_backward<false, true>(a, vec.all, &chain)
+             : (layer ? launch_backward<false, true>(a, vec.all, &chain)
                      : launch_backward<false, false>(a, vec.all, &chain));
   }
   if (e != cudaSuccess || a.wanted == 0 || (a.rows == 0 && L.accumulate)) return e;

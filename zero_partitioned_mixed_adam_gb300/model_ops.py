@@ -64,18 +64,18 @@ _declare(_lib)
 _IDS = (torch.int64, torch.int32)
 
 
-def _current_device() -> int:
-    """The current device's number, without initializing CUDA."""
-    return torch._C._cuda_getDevice() if torch.cuda.is_initialized() else 0
+_current_device = torch._C._cuda_getDevice  # (of a process that has tensors there)
 
 
 def _here(stream, tensors):
     """Refuses tensors and streams that are not of the current CUDA device, on which the
     library launches."""
-    here = _current_device()
+    here = tensors[0].get_device()
+    if here < 0 or here != _current_device():
+        raise ValueError(f"expected tensors of the current CUDA device, not of {tensors[0].device}")
     for t in tensors:
         if t is not None and t.get_device() != here:
-            raise ValueError(f"expected tensors of the current device, cuda:{here}, not of {t.device}")
+            raise ValueError(f"expected tensors of one device, not of cuda:{here} and {t.device}")
     if stream is not None and not isinstance(stream, int) and stream.device.index != here:
         raise ValueError(f"the tensors are on cuda:{here}, the stream on {stream.device}")
 
