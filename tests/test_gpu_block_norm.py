@@ -178,8 +178,8 @@ def check_backward(b, *, dtype=BF, add=False, has_ds=True, in_place=False, want=
             ((("dgate", grads["gate"], mags["gate"]),) if gate_rows else ()):
         if name in out:
             near(out[name], exact, e * mag + half * (exact.abs() + e * mag) + 1e-30, name)
-    # sums over rows: up to m/304 + 1 a block (or 4), 304 blocks in 8 runs
-    es = e + (m / 304 + 4 + 304 / 8 + 8) * 2.0 ** -24
+    # sums over rows: up to m/152 + 2 a block, up to 2,432 blocks in 32 runs
+    es = e + (m / 152 + 2 + 2432 / 32 + 32) * 2.0 ** -24
     half = 2.0 ** -8 if dtype == BF else 2.0 ** -23
     for name, of in vectors.items():
         if name in out:
