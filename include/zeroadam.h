@@ -566,11 +566,14 @@ typedef struct {
  *               work).  dw is bf16, or fp32 with ZERO_GRAD_F32.
  *   flags       ZERO_IDS_I32, ZERO_GRAD_F32, ZERO_GRAD_ACCUMULATE.
  *   workspace   zero_linear_cross_entropy_workspace bytes, 16-byte aligned.
- * Sums are fp32.  dz is rounded to bf16 (the tensor cores' operand type) before
- * the products, from exponentials that are held in 16 bits of fixed point, good to
- * 2^-11; probabilities below exp(-32) of the target's (of the largest, in a row
- * whose loss is above 30) are 0 in dz.  Rows go in pieces whose 16-bit values take
- * at most 1 GiB of the workspace.  Results do not depend on the run.
+ * Sums are fp32.  The products' operands are bf16 (the tensor cores' type): the
+ * exponentials, and then dz, each rounded once; of more than 2^25 values (rows *
+ * vocab) the exponentials alone, and x times its row's factor for dw, whose rounding
+ * averages out over the rows.  Exponentials below exp(-87) of the target's (of the
+ * largest, in a row whose loss is above 44) are 0 in dz.  Rows that are ignored are
+ * left out of the products.  The loss alone takes other kernels than the loss with
+ * gradients, and may differ from it in its last bits.  Rows go in pieces whose
+ * exponentials take at most 1 GiB of the workspace.  Results do not depend on the run.
  * rows = 0: total is 0, and dw is too (or is left, accumulating).
  * Errors: ZERO_E_NULLPTR, ZERO_E_SHAPE, ZERO_E_LAYOUT, ZERO_E_ALIGN, ZERO_E_ALIAS
  * (an output overlaps another buffer), ZERO_E_WORKSPACE, ZERO_E_LAUNCH, ZERO_E_DEVICE.

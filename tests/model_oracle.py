@@ -13,14 +13,18 @@ def cross_entropy(x, w, targets, ignore=-100, scale=None):
     x = torch.where(keep[:, None], x, torch.zeros_like(x))   # an ignored row's x does not count
     at = torch.where(good, targets, torch.zeros_like(targets)).long()[:, None]
     z = x @ w.t()
-    top = z.amax(1, keepdim=True)
-    norm = top + (z - top).exp().sum(1, keepdim=True).log()
-    losses = torch.where(good, (norm - z.gather(1, at))[:, 0], torch.full_like(norm[:, 0], float("nan")))
+    # less the target's logit or the largest: 1 - p of the target loses nothing however small it is
+    d = z - z.gather(1, at)
+    top = d.amax(1, keepdim=True).clamp(min=0.0)
+    others = (d - top).exp().scatter(1, at, 0.0)
+    rest = others.sum(1, keepdim=True)
+    whole = rest + (-top).exp()
+    losses = torch.where(top > 0, top + whole.log(), rest.log1p())[:, 0]
+    losses = torch.where(good, losses, torch.full_like(losses, float("nan")))
     losses = torch.where(keep, losses, torch.zeros_like(losses))
     c = scale.to(F64) if scale is not None else torch.ones_like(losses) / keep.sum()
     c = torch.where(good, c, torch.where(keep, torch.full_like(c, float("nan")), torch.zeros_like(c)))
-    dz = (z - norm).exp()
-    dz.scatter_add_(1, at, -torch.ones_like(at, dtype=F64))
+    dz = others.scatter(1, at, -rest) / whole
     dz = torch.where(keep[:, None], dz * c[:, None], torch.zeros_like(dz))
     total = torch.where(keep, c * losses, torch.zeros_like(c)).sum()
     return losses, total, dz @ w, dz.t() @ x, dz, z, c

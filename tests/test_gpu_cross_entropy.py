@@ -39,9 +39,11 @@ def tolerances(x, w, ref):
 
     z: sums of 16 products or more at a time, each of the width/16 + 2 additions good to 2^-22
     of the sum of magnitudes so far, and the reference's alike.  The sum of exponentials: each
-    within its argument's error, 2^-19 of argument times 2^-24 and 2 ulp (arguments up to 30),
-    100 additions of 2^-24: 2^-17 in all.  dz: the sum's error, half of 2^-10 of fixed point,
-    2^-8 for its rounding to bf16, nothing below exp(-32).  Products: as z."""
+    within its argument's error, 2^-19 of argument times 2^-24 and 2 ulp (arguments up to 45),
+    100 additions of 2^-24: 2^-17 in all.  dz: the sum's error, 2^-8 for an exponential's rounding to
+    bf16, and 2^-8 more: dz's own rounding, or the target's, which the row's factor takes over.  What
+    is below exp(-87) of the reference's is nothing.  dw of more than 2^25 values: 2^-8 for x times the
+    factor, in bf16, and there the target's dz is exact.  Products: as z."""
     losses, _, _, _, dz, z, c = ref
     keep = (c != 0)[:, None]
     ax, aw = torch.where(keep, x.to(F64).abs(), 0.0), w.to(F64).abs()
@@ -49,10 +51,12 @@ def tolerances(x, w, ref):
     ez = 2 * ((width / 16 + 2) * 2.0 ** -22 * (ax @ aw.t())).amax(1)
     rel = 2 * ez + 2.0 ** -17
     tol_loss = rel * -torch.expm1(-losses) + 2.0 ** -22 * losses.abs() + 1e-12 + ez * (losses > 30)
-    ddz = dz.abs() * (2.0 ** -8 + 2.0 ** -11 + rel[:, None]) * 1.01 + math.exp(-32) * c[:, None].abs()
+    ddz = dz.abs() * (torch.where(dz * c[:, None] > 0, 2.0 ** -7, 2.0 ** -8) + rel[:, None]) * 1.01
+    ddz = ddz + math.exp(-87) * c[:, None].abs()
+    fdw = 2.0 ** -8 if rows * vocab > 2 ** 25 else 0.0
     adz = dz.abs() + ddz
     tol_dx = ddz @ aw + (vocab / 16 + 2) * 2.0 ** -22 * (adz @ aw)
-    tol_dw = ddz.t() @ ax + (rows / 16 + 2) * 2.0 ** -22 * (adz.t() @ ax)
+    tol_dw = (ddz + fdw * adz).t() @ ax + (rows / 16 + 2) * 2.0 ** -22 * (adz.t() @ ax)
     return tol_loss, tol_dx, tol_dw
 
 
@@ -269,6 +273,56 @@ def test_rows_in_pieces(dtype, add):
     assert 2 * m * v > 2 ** 30
     dw = matrix(v, k, 1e-4, 5).to(dtype)
     check(matrix(m, k, 1.0, 1), matrix(v, k, 0.3, 2), targets_of(m, v, 3, 0.1), dtype=dtype, add=add, dw=dw)
+
+
+# more than 2^25 values: the exponentials stay as they are, and x and dx take the rows' factors
+MANY = [(1100, 40, 32003), (2100, 264, 16411), (700, 75, 50257)]
+
+
+@pytest.mark.parametrize("m,k,v", MANY)
+@pytest.mark.parametrize("ignored,pitch", [(0.0, 0), (0.4, 3)])
+def test_many_values(m, k, v, ignored, pitch):
+    t = targets_of(m, v, 3, ignored)
+    x, w = matrix(m, k, 1.0, 1, pitch), matrix(v, k, 2.0 / math.sqrt(k), 2, pitch)
+    x[t == -100] = float("nan")
+    check(x, w, t, dx=blank(m, k, pitch=pitch), dw=blank(v, k, pitch=pitch))
+    scale = torch.linspace(-1.0, 2.0, m, device="cuda")
+    first = check(x, w, t, scale=scale, dtype=F32, add=True, dw=matrix(v, k, 0.1, 5).float())
+    for name, at in (("dx", 2), ("dw", 3)):          # each alone, to the same bits
+        got = matrix(v, k, 0.1, 5).float() if name == "dw" else torch.full_like(first[2], 7.0)
+        za.zero_linear_cross_entropy(x, w, t, scale=scale, accumulate=name == "dw", **{name: got})
+        assert torch.equal(got, first[at]), name
+
+
+@pytest.mark.parametrize("m,k,v", MANY[::2])
+def test_many_values_far_targets(m, k, v):
+    """Rows that take the largest logit for their reference beside ordinary and certain ones, then
+    most rows of the first kind."""
+    x, w = matrix(m, k, 1.0, 1), matrix(v, k, 1.0, 2)
+    t = targets_of(m, v, 3, 0.1)
+    z = x.float() @ w.float().t()
+    t[0], t[1] = z[0].argmin(), z[1].argmax()
+    x[0] *= 16.0
+    x[1] *= 16.0
+    losses, *_ = check(x, w, t)
+    assert losses[0] > 100 and losses[1] < 1e-3
+    check(x * 8.0, w, t)
+
+
+def test_many_values_that_are_not_good():
+    """A target that is no column and a row that is not finite spoil their own losses and dx."""
+    m, k, v = MANY[0]
+    x, w, t = matrix(m, k, 1.0, 1), matrix(v, k, 0.2, 2), targets_of(m, v, 3, 0.1)
+    t[4] = t[7] = t[9] = 1
+    want = o.cross_entropy(x, w, t)[0]
+    t[4], x[7, 3], x[9, 5] = v, float("inf"), float("nan")
+    losses, total, dx, dw = torch.zeros(m, device="cuda"), torch.zeros(1, device="cuda"), blank(m, k), blank(v, k)
+    za.zero_linear_cross_entropy(x, w, t, losses, total, dx=dx, dw=dw)
+    others = torch.ones(m, dtype=torch.bool, device="cuda")
+    others[torch.tensor([4, 7, 9], device="cuda")] = False
+    assert not torch.isfinite(losses[~others]).any() and not torch.isfinite(dx[~others]).any()
+    assert ((losses - want).abs() < 1e-4)[others].all() and torch.isfinite(dx[others]).all()
+    assert not torch.isfinite(total).any() and not torch.isfinite(dw).any()
 
 
 def test_the_same_bits_every_time():

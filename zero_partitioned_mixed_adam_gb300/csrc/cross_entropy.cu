@@ -5,27 +5,37 @@
 // A row's exponentials are taken less a reference r that is there before the product:
 // the target's logit z_t itself, one dot product a row.  Then, S' the sum over j != t,
 //   loss = log(1 + S'),   p_j = exp(z_j - z_t) / (1 + S'),   1 - p_t = S' / (1 + S'),
-// where nothing is lost to cancellation however sure the model is.  The gradient
-// dz_j = c (p_j - [j = t]) wants the row's whole sum first, so the product's epilogue
-// writes z_j - z_t in 16 bits, and one pass over them makes dz of them in place once the
-// sums are there: three products for the loss and both gradients, where computing z
-// again would be a fourth (8192 x 2048 -> 50257: 0.9 ms; the pass 0.25).
-// A row whose S' passes 2^44 (the target 30 below the largest logit) leaves that range:
-// its reference becomes the largest logit, which the first product found, and product and
-// pass run once more; the launches that do so end at once where no row needs them.
+// where nothing is lost to cancellation however sure the model is.  The gradient of z is
+// dz_j = c (p_j - [j = t]) = f e_j with one f = c / (1 + S') a row, e_j = exp(z_j - z_t), and
+// e_t = -S'.  The product's epilogue writes e in bf16, whose exponent has room for all of it, and
+// adds up S'; then dx_i = f_i sum over j of e_ij W_j takes f in its epilogue, and
+// dw_j = sum over i of e_ij (f_i x_i) takes x with f in it, rounded to bf16.  So nothing passes over
+// the [rows][vocab] values between the products, which read them as they were written (with a
+// pass that makes dz of them in place 8192 x 2048 -> 50257 took 3,400 us instead of 3,090, and
+// 4096 x 768 -> 50257 709 instead of 611).  The price is one more rounding in dw, of f x: over
+// thousands of rows it averages out (these two cases' dw is 1.05 times as far from the exact one
+// as its own rounding puts it), over few it does not (37 x 256 -> 515: 1.5 times).  So where
+// the values stay in L2, up to 2^25 of them, that pass is made: dz is rounded to bf16 there, and
+// dw of few rows is as near as dx (1.2 times).
+// A row whose S' passes 2^64 (the target 44 below the largest logit) leaves the range where
+// products with 1 / S' lose nothing: its reference becomes the largest logit, which the first
+// product found, and product and ends run once more; the launches that do so end at once
+// where no row needs them.
 //
 // Kernels of one piece of rows:
 //   places    which rows are not ignored: only they take part in what follows
 //   rows      z_t, the reference, the target as a column, x where TMA can read it
-//   product   (linear.cu) exponentials
-//   finish    losses, dz;  product and finish again, where some row needs it
-//   products  (linear.cu) dx = dz W, dw = dz^T x
+//   product   (linear.cu) e and its sums
+//   ends      losses, e_t, f, f x (or dz);  product and ends again, where some row needs it
+//   products  (linear.cu) dx, dw
 //   spread    dx where the caller's rows are
 // Small problems leave out places and spread, as their launches are worth more than the rows.
 // The loss alone needs neither reference nor x laid out: its product takes the exponentials
 // less the largest logit so far, and a warp a row ends it.  The target's logit is a dot
 // product of its own there too, rounded to nearest: the tensor cores cut off, and what
 // that takes from one logit of 12 is 10 times the loss's other errors.
+#include <type_traits>
+
 #include "chain.cuh"
 #include "internal.h"
 #include "linear_epilogue.cuh"
@@ -35,8 +45,8 @@
 namespace zeroadam {
 namespace {
 
-constexpr int64_t kMostHeld = int64_t{1} << 30;  // bytes of 16-bit values of one piece
-constexpr float kOneMore = 17592186044416.0f;    // 2^44: a sum that asks for another reference
+constexpr int64_t kMostHeld = int64_t{1} << 30;  // bytes of e of one piece
+constexpr float kOneMore = 18446744073709551616.0f;  // 2^64: a sum that asks for another reference
 
 // Words of the workspace that a call's kernels share.
 struct Words {
@@ -65,7 +75,9 @@ struct LossArgs {
   const float* scale;     // [all_rows] or NULL
   float* losses;          // [all_rows]
   float* total;           // NULL: not wanted, or this is not the last piece
-  uint16_t* held;         // [rows][ldz]: 16 bits, then dz
+  uint16_t* held;         // [rows][ldz]: e, or dz made of it
+  uint16_t* xs;           // [rows][ldxc]: f x; NULL: not wanted (never where dz is made)
+  float* factor;          // [rows]: f
   int64_t ldz;
   int32_t vec;            // x and w are read in vectors
   int32_t alone;          // rows that want another reference are made anew by their block (kOnce)
@@ -386,72 +398,79 @@ __device__ __noinline__ float row_again(const LossArgs& a, int64_t i, int32_t t,
       if (j + u >= a.vocab) continue;
       const float d = j + u == t ? -INFINITY : z[u] - ref;
       sum += expf(d);
-      if (lane == 0)
-        a.held[i * a.ldz + j + u] = static_cast<uint16_t>(static_cast<int16_t>(fmaxf(rintf(d * 1024.0f), -32768.0f)));
+      if (lane == 0) a.held[i * a.ldz + j + u] = to_bf16(expf(d));
     }
   }
   return sum;
 }
 
-// A block a row: the row's sums in the order of its parts, its loss, and dz.  With c alike
-// for all rows (the mean) dz is p less the target's 1, whose rounding is nothing where p is
-// small, and c multiplies the products' sums; a scale of each row's own is in its dz.
-// kAgain: the second time, where the first has asked for it.  The last block adds up the
-// losses.  Bound by HBM: 4 bytes an element (8192 x 50257: 1.65 GB).
+// A row's sums in the order of its parts, its loss, e of the target, and f: with DZ f times e in
+// place, a block a row, without it f times x, a warp a row.  The last block adds up the losses.  With
+// c alike for all rows (the mean) c is left to the products' sums, and dz is p less the target's 1,
+// whose rounding is nothing where p is small.
+// Without DZ bound by HBM: the sums, x twice (8192 x 2048 -> 50257: 100 MB).
 // Where the whole product is small, a row that wants another reference is made anew here, by
-// dot products, which saves the two launches that else do it (37 x 256 -> 515: 5 us of 37; were
-// every row of 2^28 multiplications such a one, they would take some 30 us).
-constexpr int64_t kFewProducts = int64_t{1} << 28;
+// dot products, which saves the two launches that else do it (37 x 256 -> 515: 5 us of 37); such
+// a row takes its block some 30 us at most.
+constexpr int64_t kFewProducts = int64_t{1} << 28, kFewWeights = int64_t{1} << 21;
+constexpr int64_t kFewValues = int64_t{1} << 25;
 
-// (kOnce has registers of its own for that; the other two are 4 blocks an SM, with 6 vectors of
-// a row under way in each thread.)
 enum Time { kFirst, kAgain, kOnce };
-constexpr int kFinishBlocks = 4;
 
-template <Time TIME>
-__global__ void __launch_bounds__(kFinishThreads, TIME == kOnce ? 2 : kFinishBlocks) loss_finish_kernel(const __grid_constant__ LossArgs a) {
+template <Time TIME, bool DZ>
+__global__ void __launch_bounds__(kFinishThreads) loss_ends_kernel(const __grid_constant__ LossArgs a) {
+  static_assert(TIME != kOnce || DZ);
   __shared__ float2 part[kFinishWarps];
   __shared__ int32_t last;
   wait_for_predecessor();
   launch_dependents();
   if (TIME == kAgain && __ldcg(&a.words->again) == 0) return;
-  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  constexpr int kWarps = DZ ? kFinishWarps : 1, kThreads = 32 * kWarps;  // of a row
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, thread = threadIdx.x % kThreads;
   const int64_t n = rows_of(a), filled = filled_rows(a, n);
-  for (int64_t i = blockIdx.x; i < filled; i += gridDim.x) {
+  constexpr int kRows = kFinishWarps / kWarps;  // of a block at one time
+  for (int64_t i = static_cast<int64_t>(blockIdx.x) * kRows + threadIdx.x / kThreads; i < filled;
+       i += static_cast<int64_t>(gridDim.x) * kRows) {
     const int32_t t = __ldcg(a.column + i);
     const int64_t from = a.first + (a.place == nullptr ? i : i < n ? __ldcg(a.place + i) : 0);  // the caller's row
     const float zt = __ldcg(a.zt + i);
     float ref = __ldcg(a.ref + i), sum = 0.0f, top = -INFINITY;
     if (t != -1) {
-      for (int k = threadIdx.x; k < a.parts; k += kFinishThreads) {
-        const float2 s = __ldcg(a.sums + i * a.parts + k);
-        sum += s.x;
-        top = fmaxf(top, s.y);
+      constexpr int U = 8;
+      for (int k0 = thread; k0 < a.parts; k0 += U * kThreads) {
+        float2 s[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+          s[u] = k0 + u * kThreads < a.parts ? __ldcg(a.sums + i * a.parts + k0 + u * kThreads)
+                                             : make_float2(0.0f, -INFINITY);
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          sum += s[u].x;
+          top = fmaxf(top, s[u].y);
+        }
       }
     }
     sum = warp_sum(sum);
 #pragma unroll
     for (int k = 16; k > 0; k /= 2) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, k));
-    __syncthreads();  // the row before is done with these
-    if (lane == 0) part[warp] = make_float2(sum, top);
-    __syncthreads();
-    sum = 0.0f;
+    const auto of_block = [&] {  // (the warps' sums in their order)
+      __syncthreads();  // the row before is done with part[]; what row_again wrote is there
+      if (lane == 0) part[warp] = make_float2(sum, top);
+      __syncthreads();
+      sum = 0.0f;
 #pragma unroll
-    for (int k = 0; k < kFinishWarps; ++k) {
-      sum += part[k].x;
-      top = fmaxf(top, part[k].y);
-    }
+      for (int k = 0; k < kFinishWarps; ++k) {
+        sum += part[k].x;
+        top = fmaxf(top, part[k].y);
+      }
+    };
+    if constexpr (kWarps > 1) of_block();
     if (TIME != kAgain && t >= 0 && sum > kOneMore && isfinite(top)) {
       if constexpr (TIME == kOnce) {
         ref = top;
         sum = a.vec ? row_again<true>(a, i, t, ref) : row_again<false>(a, i, t, ref);
-        __syncthreads();  // part[] and the row are written
-        if (lane == 0) part[warp].x = sum;
-        __syncthreads();
-        sum = 0.0f;
-#pragma unroll
-        for (int k = 0; k < kFinishWarps; ++k) sum += part[k].x;
-      } else if (threadIdx.x == 0) {
+        of_block();
+      } else if (lane == 0) {
         a.ref[i] = top;
         a.words->again = 1;
       }
@@ -465,39 +484,49 @@ __global__ void __launch_bounds__(kFinishThreads, TIME == kOnce ? 2 : kFinishBlo
     if (!isfinite(whole)) f = NAN;
     if (t == -1) loss = f = 0.0f;
     if (t == -2) loss = f = NAN;
-    if (threadIdx.x == 0 && i < n) a.losses[from] = loss;
-    // (the pitch has room for whole vectors; an ignored row's are not read)
-    uint4* row = reinterpret_cast<uint4*>(a.held + i * a.ldz);
-    constexpr int U = TIME == kOnce ? 2 : 6;  // (2, 4, 6: 309, 280, 272 us; at 6 blocks an SM 281, 283, 379)
-    const uint32_t vectors = static_cast<uint32_t>((a.vocab + 7) / 8);
-    for (uint32_t j0 = threadIdx.x; j0 < vectors; j0 += U * kFinishThreads) {
-      uint4 v[U];
+    if (thread == 0 && i < n) a.losses[from] = loss;
+    // (the pitches have room for whole vectors; an ignored row's e are not read)
+    uint4* e = reinterpret_cast<uint4*>(a.held + i * a.ldz);
+    if constexpr (DZ) {
+      constexpr int U = 4;
+      const uint32_t vectors = static_cast<uint32_t>((a.vocab + 7) / 8);
+      for (uint32_t j0 = thread; j0 < vectors; j0 += U * kThreads) {
+        uint4 v[U];
 #pragma unroll
-      for (int u = 0; u < U; ++u)
-        if (t != -1 && j0 + u * kFinishThreads < vectors) v[u] = __ldcs(row + j0 + u * kFinishThreads);
+        for (int u = 0; u < U; ++u)
+          if (t != -1 && j0 + u * kThreads < vectors) v[u] = __ldcg(e + j0 + u * kThreads);
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const uint32_t j = j0 + u * kFinishThreads;
-        if (j >= vectors) break;
-        uint4 y = make_uint4(0, 0, 0, 0);
-        if (t != -1) {
-          const uint32_t w[4] = {v[u].x, v[u].y, v[u].z, v[u].w};
-          float x[8];
+        for (int u = 0; u < U; ++u) {
+          const uint32_t j = j0 + u * kThreads, at = static_cast<uint32_t>(t) - 8 * j;
+          if (j >= vectors) break;
+          float x[8] = {};
+          if (t != -1) bf16x8(v[u], x);
 #pragma unroll
-          for (int c = 0; c < 8; ++c) {
-            const int16_t d = static_cast<int16_t>(c % 2 ? w[c / 2] >> 16 : w[c / 2] & 0xffffu);
-            const float e = fast_exp2(static_cast<float>(d) * (kLog2e / 1024.0f));
-            x[c] = f * (d == INT16_MIN ? 0.0f : e);
-          }
-          const uint32_t at = static_cast<uint32_t>(t) - 8 * j;
-          if (at < 8) {
-#pragma unroll
-            for (int c = 0; c < 8; ++c)
-              if (at == c) x[c] = -(f * sum);
-          }
-          y = to_bf16x8(x);
+          for (int c = 0; c < 8; ++c) x[c] = t == -1 ? 0.0f : f * (at == c ? -sum : x[c]);
+          e[j] = to_bf16x8(x);
         }
-        row[j] = y;
+      }
+    } else {
+      // f takes what e_t's rounding loses: f e_t is then exact, and the others, which weigh less
+      // together, are off by as much as one more rounding of theirs
+      const float rounded = __uint_as_float(static_cast<uint32_t>(to_bf16(sum)) << 16);
+      if (t >= 0 && rounded > 0.0f) f *= sum / rounded;
+      if (thread == 0) {
+        a.factor[i] = f;
+        if (t >= 0) a.held[i * a.ldz + t] = to_bf16(-sum);
+      }
+      if (t == -1)
+        for (int64_t j = thread; j < (a.vocab + 7) / 8; j += kThreads) e[j] = make_uint4(0, 0, 0, 0);
+      if (a.xs == nullptr) continue;
+      const uint16_t* x = a.xc + i * a.ldxc;
+      uint16_t* to = a.xs + i * a.ldxc;
+#pragma unroll 4
+      for (int64_t j = 8 * thread; j < a.width; j += 8 * kThreads) {
+        float p[8];
+        bf16x8(__ldcg(reinterpret_cast<const uint4*>(x + j)), p);
+#pragma unroll
+        for (int c = 0; c < 8; ++c) p[c] *= f;
+        *reinterpret_cast<uint4*>(to + j) = to_bf16x8(p);
       }
     }
   }
@@ -556,7 +585,7 @@ int64_t piece_rows(const zero_cross_entropy_t& s, bool grads) {
 // Where a call's arrays lie in its workspace.
 struct Layout {
   int64_t piece, parts;  // rows of a piece, and parts of the vocabulary at most
-  int64_t w, x, zt, held, sums, losses, acc, dxc, linear, bytes;
+  int64_t w, x, xs, zt, held, sums, losses, acc, dxc, linear, bytes;
 };
 
 zero_linear_t linear_of(const zero_cross_entropy_t& s, int64_t rows) {
@@ -598,7 +627,8 @@ Layout make_layout(const zero_cross_entropy_t& s, int32_t flags) {
   l.w = take((flags & ZERO_LINEAR_ALIGNED) ? 0 : 2 * s.vocab * laid_out_pitch(s.width));
   // (the loss alone reads x in place, if it lies so; what it lies like is not known here)
   l.x = take(2 * l.piece * laid_out_pitch(s.width));
-  l.zt = take(20 * l.piece);  // zt, ref, column, place, slot
+  l.xs = take(grads && l.piece * s.vocab > kFewValues ? 2 * l.piece * laid_out_pitch(s.width) : 0);
+  l.zt = take(24 * l.piece);  // zt, ref, column, place, slot, factor
   l.held = take(grads ? 2 * l.piece * laid_out_pitch(s.vocab) : 0);
   l.sums = take(8 * l.piece * l.parts);
   l.losses = take(4 * s.rows);
@@ -659,6 +689,7 @@ cudaError_t launch_cross_entropy(const CrossEntropyLaunch& L) {
   a.column = reinterpret_cast<int32_t*>(a.ref + l.piece);
   int32_t* const place = a.column + l.piece;
   a.slot = place + l.piece;
+  a.factor = reinterpret_cast<float*>(a.slot + l.piece);
   a.dxc = reinterpret_cast<uint16_t*>(base + l.dxc);
   a.lddxc = laid_out_pitch(s.width);
   a.lddx = s.lddx;
@@ -690,9 +721,11 @@ cudaError_t launch_cross_entropy(const CrossEntropyLaunch& L) {
     a.first = first;
     a.rows = s.rows - first < l.piece ? s.rows - first : l.piece;
     const bool last = first + a.rows == s.rows;
-    a.alone = a.rows * s.vocab <= kFewProducts / s.width;
+    a.alone = a.rows * s.vocab <= kFewProducts / s.width && s.vocab <= kFewWeights / s.width;
     a.parts = static_cast<int32_t>(exponent_parts(a.rows, s.vocab, s.width));
     a.total = last ? L.total : nullptr;
+    const bool make_dz = a.alone || a.rows * s.vocab <= kFewValues;
+    a.xs = L.dw != nullptr && !make_dz ? reinterpret_cast<uint16_t*>(base + l.xs) : nullptr;
     ExponentLaunch x{};
     x.rows = a.rows;
     x.width = s.width;
@@ -737,19 +770,27 @@ cudaError_t launch_cross_entropy(const CrossEntropyLaunch& L) {
     x.ldo = a.ldz;
     x.rows_now = a.alone ? nullptr : &a.words->rows;
     if (e == cudaSuccess) e = launch_exponents(x);
-    const dim3 grid = blocks_of(a.rows, (a.alone ? 2 : kFinishBlocks) * kSms);
-    if (e == cudaSuccess)
-      e = chain.launch(a.alone ? loss_finish_kernel<kOnce> : loss_finish_kernel<kFirst>, grid, kFinishThreads, 0, 1, a);
-    x.of.only_if = &a.words->again;
-    if (e == cudaSuccess && !a.alone) e = launch_exponents(x);
-    if (e == cudaSuccess && !a.alone)
-      e = chain.launch(loss_finish_kernel<kAgain>, blocks_of(a.rows, 2 * kSms), kFinishThreads, 0, 1, a);
+    const auto end = [&](auto dz, auto first_time) {
+      constexpr bool DZ = decltype(dz)::value;
+      constexpr Time TIME = decltype(first_time)::value ? kFirst : kAgain;
+      return chain.launch(loss_ends_kernel<TIME, DZ>, blocks_of(DZ ? a.rows : (a.rows + kFinishWarps - 1) / kFinishWarps, 8 * kSms),
+                          kFinishThreads, 0, 1, a);
+    };
+    using std::false_type, std::true_type;
+    if (e == cudaSuccess && a.alone)
+      e = chain.launch(loss_ends_kernel<kOnce, true>, blocks_of(a.rows, 4 * kSms), kFinishThreads, 0, 1, a);
+    if (!a.alone) {
+      if (e == cudaSuccess) e = make_dz ? end(true_type{}, true_type{}) : end(false_type{}, true_type{});
+      x.of.only_if = &a.words->again;
+      if (e == cudaSuccess) e = launch_exponents(x);
+      if (e == cudaSuccess) e = make_dz ? end(true_type{}, false_type{}) : end(false_type{}, false_type{});
+    }
     if (e != cudaSuccess) return e;
     LinearBackwardLaunch b{};
     b.s = b_shape;
     b.s.ldw = ldw;
     b.dy = a.held;
-    b.x = a.xc;
+    b.x = make_dz ? a.xc : a.xs;
     b.w = w;
     b.dx = a.dx;
     if (a.dx != nullptr && !a.alone) {
@@ -766,6 +807,7 @@ cudaError_t launch_cross_entropy(const CrossEntropyLaunch& L) {
     if (joined) b.s.lddw = round_up(s.width, 4);
     b.grad_f32 = L.grad_f32 || joined;
     b.accumulate = first > 0 || (L.accumulate && !joined);
+    b.row_scale = make_dz ? nullptr : a.factor;
     b.scale = L.scale == nullptr ? &a.words->share : nullptr;
     b.workspace = base + l.linear;
     b.stream = L.stream;

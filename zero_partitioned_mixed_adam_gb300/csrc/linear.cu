@@ -506,15 +506,12 @@ struct RowsPart {
   }
 };
 
-// 32 columns of logits z, a row a lane, less the row's reference r: d = z - r goes out
-// as 16 bits of fixed point, in 2^-10 (below -32: as -32, which stands for nothing), by
-// TMA as bf16 does; exp(d) is added up, and the largest z is kept, over the columns of
-// the vocabulary but the target's.  d itself is what is held because it costs no
-// exponent's bits: exp(d) is then good to 2^-11, where bf16 would leave it 2^-9 and the
-// pass that makes dz of it round a second time.
-// Some 5 instructions an element, half of them two elements at a time, and one of the
-// special-function unit: 1,300 cycles of a tile's epilogue where its products take 8 for
-// each step of the reduction, so it is hidden from 256 steps on.
+// 32 columns of logits z, a row a lane, less the row's reference r: exp(z - r) is added up and
+// goes out in bf16 by TMA, and the largest z is kept, over the columns of the vocabulary but the
+// target's, where 0 goes out.  What goes out is an operand of the gradients' products as it is:
+// a row's factor 1 / sum is not known yet, and goes to the other operand and to the sums.
+// Some 4 instructions an element, half of them two elements at a time, and one of the
+// special-function unit: hidden behind a tile's products from 256 steps of the reduction on.
 struct ExponentPart {
   float r;      // the row's reference
   int32_t t;    // its target
@@ -543,21 +540,18 @@ struct ExponentPart {
     }
 #pragma unroll
     for (int q = 0; q < 32; ++q) top = fmaxf(top, x[q]);
-    const bool keep = a.e.out != nullptr;
-    constexpr float kMagic = 12582912.0f;  // 3 2^22: the sum's low bits are a whole number
     uint32_t w[16];
 #pragma unroll
     for (int q = 0; q < 32; q += 2) {
       const Pair d = pair(x[q], x[q + 1]) + pair(-r, -r);
       float u, v;
       split(d * pair(kLog2e, kLog2e), u, v);
-      sum = sum + pair(fast_exp2(u), fast_exp2(v));
-      split(fma2(d, pair(1024.0f, 1024.0f), pair(kMagic, kMagic)), u, v);
-      u = fmaxf(u, kMagic - 32768.0f);
-      v = fmaxf(v, kMagic - 32768.0f);
-      w[q / 2] = __byte_perm(__float_as_uint(u), __float_as_uint(v), 0x5410);
+      u = fast_exp2(u);
+      v = fast_exp2(v);
+      sum = sum + pair(u, v);
+      w[q / 2] = bf16x2_bits(u, v);
     }
-    if (!keep || col >= cols) return;
+    if (col >= cols) return;
     if (lane == 0) bulk_wait_read<1>();  // the copy before the last has left this slot
     __syncwarp();
     uint8_t* to = staging + 2048 * slot;
@@ -899,8 +893,9 @@ __global__ void __launch_bounds__(kProductThreads, 1)
     bool ok = true;
     ExponentPart exponents;  // of kExponent
     LogSumPart log_sum;      // of kLogSum
-    const bool scaled = (KIND == kGradient || KIND == kFloat) && a.e.scale != nullptr;
-    const float scale = scaled ? __ldcg(a.e.scale) : 1.0f;
+    const bool by_row = KIND == kGradient && a.e.row_scale != nullptr;
+    const bool scaled = (KIND == kGradient || KIND == kFloat) && (a.e.scale != nullptr || by_row);
+    const float whole_scale = scaled && a.e.scale != nullptr ? __ldcg(a.e.scale) : 1.0f;
     for (int t = turns.first(unit); t < tiles && ok; t = turns.after(t)) {
       const Tile tile = tile_at(t);
       const int64_t row0 = tile.row + rank * kBlockRows + quarter * 32;
@@ -910,6 +905,7 @@ __global__ void __launch_bounds__(kProductThreads, 1)
       const bool fast = any && tile.part < 0 &&
                         (ROWS ? end - first >= 8 : vec && tile.col + bn <= cols);
       const bool mine_in = row0 + lane < rows;
+      const float scale = by_row && mine_in ? whole_scale * __ldcg(a.e.row_scale + row0 + lane) : whole_scale;
       const auto ask = [&](int c) {
         if constexpr (ROWS) {
           if (tile.col + c < end) part.ask(row0 + lane, tile.col + c, mine_in, first, end, lane);
@@ -2049,6 +2045,7 @@ cudaError_t launch_linear_backward(const LinearBackwardLaunch& L) {
     p.e.out = L.dx;
     p.e.ldo = s.lddx;
     p.e.scale = L.scale;
+    p.e.row_scale = L.row_scale;
     p.rows_now = L.rows_now;
     p.all = L.dx_all;
     p.ld_all = L.ld_all;

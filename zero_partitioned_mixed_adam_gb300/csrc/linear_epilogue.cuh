@@ -148,6 +148,7 @@ struct Epilogue {
   int64_t ldo;
   int32_t out_f32, accumulate;
   const float* scale;        // gradients: multiplies the sum first, one number on the device
+  const float* row_scale;    // and one for each row (bf16 alone)
   int32_t vec;               // every matrix's base and pitch are multiples of 16 bytes
 };
 

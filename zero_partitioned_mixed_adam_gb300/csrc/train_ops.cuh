@@ -82,6 +82,7 @@ struct LinearBackwardLaunch {
   cudaStream_t stream;
   int32_t withhold;
   const float* scale;  // of dx and dw, one number on the device; NULL: 1
+  const float* row_scale;  // of dx, a number a row; NULL: 1
   // How many of the rows there are, on the device; NULL: all.  What lies behind them in dx is
   // left anyhow; in dy and x rows up to the next multiple of 128, and least_rows, are 0.
   const int32_t* rows_now;
@@ -96,7 +97,7 @@ bool whole_in_place(const zero_linear_t& s, bool dw);
 
 // What becomes of z = x W^T in place of an epilogue: over each part of the columns, the
 // target's left out, the sum of exp(d) and the largest z.
-//   with ref      d = z - ref of its row; d is written too, in 16 bits
+//   with ref      d = z - ref of its row; exp(d) is written too, in bf16, 0 for the target
 //   with targets  d = z less the largest z
 struct ExponentOf {
   float2* sums;           // [rows][sum_pitch], exponent_parts of them written
@@ -114,7 +115,7 @@ struct ExponentLaunch {
   const uint16_t *x, *w;  // where TMA can read them
   int64_t ldx, ldw;
   ExponentOf of;
-  uint16_t* out;          // [rows][ldo], in 2^-10, -32 and below as -32768
+  uint16_t* out;          // [rows][ldo]
   int64_t ldo;
   const int32_t* rows_now;  // how many of the rows there are, on the device; NULL: all
   cudaStream_t stream;
