@@ -407,19 +407,18 @@ __device__ __forceinline__ void begin_sums(float (*part)[RowSum<SHARE>::kParts][
   if constexpr (SHARE == kCluster) cluster_sync();
 }
 
-// What norms and gate there are, in one register.  LAYER: there may be norms of that kind.
+// What norms there are, in one register.  LAYER: there may be norms of that kind.
 template <bool LAYER>
 struct Kinds {
   uint32_t bits;
   __device__ __forceinline__ explicit Kinds(const NormArgs& a)
       : bits((a.kind == ZERO_NORM_LAYER ? 1u : 0u) | (a.post == ZERO_NORM_LAYER ? 2u : 0u) |
-             (a.post != ZERO_NORM_NONE ? 4u : 0u) | (a.gate != nullptr ? 8u : 0u)) {
+             (a.post != ZERO_NORM_NONE ? 4u : 0u)) {
     keep(bits);
   }
   __device__ __forceinline__ bool layer() const { return LAYER && (bits & 1u) != 0; }
   __device__ __forceinline__ bool post_layer() const { return LAYER && (bits & 2u) != 0; }
   __device__ __forceinline__ bool post() const { return (bits & 4u) != 0; }
-  __device__ __forceinline__ bool gated() const { return (bits & 8u) != 0; }  // by a vector
 };
 
 // LAYER: there are norms of that kind, or biases, which are theirs.
@@ -506,18 +505,89 @@ __global__ void __launch_bounds__(kMostThreads)
   const Output<VEC> dr_out(a.dr, a.pitch_dr), dh_out(a.dh, a.pitch_dh), dgate_out(a.dgate_rows, a.pitch_dg);
   const bool wvec = a.wvec != 0;
   const Kinds<LAYER> kinds(a);
-  const Held w(at, a.w, wvec), w1(at, FULL ? a.w1 : nullptr, wvec), g(at, FULL ? a.gate : nullptr, wvec);
-  Eight dw = all_of(0.0f), db = dw, dg = dw, dw1 = dw, db1 = dw;
+  // With a = s's gradient (times the gate's row, where it is a matrix) and hh the standardized h,
+  // what reaches hh is a c, c = alpha w1 (times the gate, where it is a vector), and the sums of
+  // a hh and a over the rows give dw1, db1 and a vector's dgate.
+  const Eight w = at.load_vector(a.w, 1.0f, wvec);
+  const Held w1(at, FULL ? a.w1 : nullptr, wvec);  // (of a matrix gate's gradient alone)
+  Eight c = all_of(a.alpha);
+  if constexpr (FULL) c = (at.load_vector(a.gate, 1.0f, wvec) * a.alpha) * w1.get();
+  Eight dw = all_of(0.0f), db = dw, ah = dw, aa = dw;
   begin_sums<SHARE>(part);
   RowSum<SHARE> row_sum{part};
   const float inv_width = 1.0f / static_cast<float>(a.width);
+  const bool layer = kinds.layer(), post_layer = kinds.post_layer(), post = kinds.post();
+  const uint32_t has_ds = rows.has(kInDs) ? 1u : 0u;
+  // What is done with a row i, `ahead` of the rows read, between its sums.  First means are taken off:
+  const auto center = [&](Eight& x, Eight& h, const float* m) {
+    if (layer) {
+      x = x + all_of(-m[0] * inv_width);
+      at.clear(x);
+    }
+    if constexpr (FULL)
+      if (post_layer) {
+        h = h + all_of(-m[1] * inv_width);
+        at.clear(h);
+      }
+  };
+  // then x x, u w x, h h, u w [LAYER]
+  constexpr int Q = LAYER ? 4 : FULL ? 3 : 2, M = LAYER ? 2 : 1;
+  const auto products = [&](const Eight& x, const Eight& u, const Eight& h, float* q) {
+    const Eight uw = u * w;
+    q[0] = dot8(x, x);
+    q[1] = dot8(uw, x);
+    if constexpr (Q > 2) q[2] = FULL ? dot8(h, h) : 0.0f;
+    if constexpr (LAYER) q[3] = layer ? sum8(uw) : 0.0f;
+  };
+  // then dr; x becomes what reaches h's norm, h standardized, m their sums; h's 1 / root
+  const auto through = [&](uint32_t i, int ahead, Eight& x, const Eight& u, Eight& h, const float* q, float* m) {
+    const float inverse = rsqrtf(fmaf(q[0], inv_width, a.eps));
+    const float along = q[1] * inverse * inv_width;
+    float inverse1 = 1.0f;
+    x = x * inverse;  // standardized
+    dw = fma8(u, x, dw);
+    if constexpr (LAYER) db = db + u;
+    x = fma8(x, all_of(-along), u * w);
+    if constexpr (LAYER)
+      if (layer) x = x + all_of(-q[3] * inv_width);
+    if (has_ds) x = fma8(x, all_of(inverse), rows.read(kInDs, i, 2, ahead));
+    else x = x * inverse;
+    if constexpr (LAYER) at.clear(x);  // (else they are 0 already)
+    dr_out.put(at, i, x);
+    if constexpr (FULL) {
+      if (post) inverse1 = rsqrtf(fmaf(q[2], inv_width, a.eps));
+      h = h * inverse1;
+      if (rows.has(kInGate)) {
+        Eight t = h * w1.get();
+        if constexpr (LAYER) t = t + at.load_vector(a.b1, 0.0f, wvec);
+        dgate_out.put(at, i, (x * a.alpha) * t);
+        x = x * rows.read(kInGate, i, 3 + has_ds, ahead);
+      }
+      ah = fma8(x, h, ah);
+      if constexpr (LAYER) aa = aa + x;
+    }
+    x = x * c;
+    if constexpr (FULL) {
+      m[0] = dot8(x, h);
+      if constexpr (LAYER) m[1] = post_layer ? sum8(x) : 0.0f;
+    }
+    return inverse1;
+  };
+  // and dh.
+  const auto end = [&](uint32_t i, Eight& x, const Eight& h, const float* m, float inverse1) {
+    if (FULL && post) {
+      x = fma8(h, all_of(-m[0] * inv_width), x);
+      if constexpr (LAYER)
+        if (post_layer) x = x + all_of(-m[1] * inv_width);
+      x = x * inverse1;
+    }
+    dh_out.put(at, i, x);
+  };
   // R rows, i and i + step: what they wait for, they wait for together.
   const auto make = [&](auto how_many, uint32_t i0) {
-    constexpr int R = decltype(how_many)::value;
-    const bool layer = kinds.layer(), post_layer = kinds.post_layer(), post = kinds.post();
-    const uint32_t has_ds = rows.has(kInDs) ? 1u : 0u;
+    constexpr int R = decltype(how_many)::value, QR = Q == 3 ? 4 : Q;
     Eight x[R], u[R], h[R];
-    float q[4 * R], m[2 * R];
+    float q[QR * R] = {}, m[2 * R], inverse1[R];
     const auto each = [&](auto f) {
 #pragma unroll
       for (int r = 0; r < R; ++r) f(r, i0 + r * own.step);
@@ -528,91 +598,70 @@ __global__ void __launch_bounds__(kMostThreads)
       u[r] = rows.read(kInDy, i, 0, r);
       if constexpr (FULL) h[r] = rows.read(kInH, i, 2 + has_ds, r);
     });
-    if (layer || (FULL && post_layer)) {  // means, then what is left
+    if (layer || (FULL && post_layer)) {
       each([&](int r, uint32_t) {
         m[2 * r] = sum8(x[r]);
         m[2 * r + 1] = FULL ? sum8(h[r]) : 0.0f;
       });
       row_sum(m);
-      each([&](int r, uint32_t) {
-        if (layer) {
-          x[r] = x[r] + all_of(-m[2 * r] * inv_width);
-          at.clear(x[r]);
-        }
-        if constexpr (FULL)
-          if (post_layer) {
-            h[r] = h[r] + all_of(-m[2 * r + 1] * inv_width);
-            at.clear(h[r]);
-          }
-      });
+      each([&](int r, uint32_t) { center(x[r], h[r], m + 2 * r); });
     }
-    each([&](int r, uint32_t) {  // x x, u w x, u w [LAYER], h h
-      const Eight uw = u[r] * w.get();
-      q[4 * r] = dot8(x[r], x[r]);
-      q[4 * r + 1] = dot8(uw, x[r]);
-      q[4 * r + 2] = layer ? sum8(uw) : 0.0f;
-      q[4 * r + 3] = FULL ? dot8(h[r], h[r]) : 0.0f;
-    });
+    each([&](int r, uint32_t) { products(x[r], u[r], h[r], q + QR * r); });
     row_sum(q);
-    each([&](int r, uint32_t i) {
-      const float inverse = rsqrtf(fmaf(q[4 * r], inv_width, a.eps));
-      const float along = q[4 * r + 1] * inverse * inv_width;
-      x[r] = x[r] * inverse;  // standardized
-      dw = fma8(u[r], x[r], dw);
-      if constexpr (LAYER) db = db + u[r];
-      x[r] = fma8(x[r], all_of(-along), u[r] * w.get());
-      if (layer) x[r] = x[r] + all_of(-q[4 * r + 2] * inv_width);
-      if (has_ds) x[r] = fma8(x[r], all_of(inverse), rows.read(kInDs, i, 2, r));
-      else x[r] = x[r] * inverse;
-      at.clear(x[r]);
-      dr_out.put(at, i, x[r]);
-      x[r] = x[r] * a.alpha;  // the gradient of gate P(h)
-      if constexpr (FULL) {
-        const float inverse1 = post ? rsqrtf(fmaf(q[4 * r + 3], inv_width, a.eps)) : 1.0f;
-        q[4 * r + 3] = inverse1;
-        h[r] = h[r] * inverse1;
-        const bool matrix = rows.has(kInGate);
-        if (matrix || kinds.gated()) {
-          Eight t = h[r] * w1.get();
-          if constexpr (LAYER) t = t + at.load_vector(a.b1, 0.0f, wvec);
-          if (matrix) {
-            dgate_out.put(at, i, x[r] * t);
-            x[r] = x[r] * rows.read(kInGate, i, 3 + has_ds, r);
-          } else {
-            dg = fma8(x[r], t, dg);
-            x[r] = x[r] * g.get();
-          }
-        }
-        if (post) {
-          dw1 = fma8(x[r], h[r], dw1);
-          if constexpr (LAYER) db1 = db1 + x[r];
-          x[r] = x[r] * w1.get();
-          at.clear(x[r]);
-          m[2 * r] = dot8(x[r], h[r]);
-          m[2 * r + 1] = post_layer ? sum8(x[r]) : 0.0f;
-        }
-      }
-    });
+    each([&](int r, uint32_t i) { inverse1[r] = through(i, r, x[r], u[r], h[r], q + QR * r, m + M * r); });
     if (dh_out.base != nullptr) {  // (alike for every thread)
-      if (FULL && post) row_sum(m);
-      each([&](int r, uint32_t i) {
-        if (FULL && post) {
-          x[r] = fma8(h[r], all_of(-m[2 * r] * inv_width), x[r]);
-          if (post_layer) x[r] = x[r] + all_of(-m[2 * r + 1] * inv_width);
-          x[r] = x[r] * q[4 * r + 3];
-        }
-        dh_out.put(at, i, x[r]);
-      });
+      if (FULL && post) row_sum(reinterpret_cast<float(&)[M * R]>(m));
+      each([&](int r, uint32_t i) { end(i, x[r], h[r], m + M * r, inverse1[r]); });
     }
     if constexpr (VEC) rows.done(R);
   };
-  // Two rows at a time, unless the registers of that are the sums' (8192 x 2048 without a norm
-  // after the block 41 -> 28 us, with one 58 -> 66; 4096 x 8192, where a barrier is a cluster's,
-  // 177 -> 140).
-  uint32_t i = own.first;
-  if constexpr (!FULL || SHARE == kCluster)
-    for (; i + own.step < rows.rows; i += 2 * own.step) make(std::integral_constant<int, 2>(), i);
-  for (; i < rows.rows; i += own.step) make(std::integral_constant<int, 1>(), i);
+  // One row at a time, whose last sums are taken with the next row's first ones: as many waits a
+  // row as with two at a time, in fewer registers.
+  const auto in_turn = [&] {
+    Eight x, h;  // of the row before, until its dh
+    float m[2] = {}, inverse1 = 1.0f;
+    const bool late = post && dh_out.base != nullptr;
+    for (uint32_t i = own.first; ; i += own.step) {
+      const bool more = i < rows.rows, before = i != own.first;
+      if (!more && !(late && before)) break;
+      Eight nx, u, nh;
+      float q[LAYER ? 8 : 4] = {};
+      if (more) {
+        if constexpr (VEC) rows.arrive();
+        nx = rows.read(kInR, i, 1);
+        u = rows.read(kInDy, i, 0);
+        nh = rows.read(kInH, i, 2 + has_ds);
+        if (layer || post_layer) {
+          float mean[2] = {sum8(nx), sum8(nh)};
+          row_sum(mean);
+          center(nx, nh, mean);
+        }
+        products(nx, u, nh, q);
+      }
+#pragma unroll
+      for (int k = 0; k < M; ++k) q[Q + k] = m[k];
+      row_sum(q);
+      if (late && before) end(i - own.step, x, h, q + Q, inverse1);
+      if (!more) break;
+      x = nx;
+      h = nh;
+      inverse1 = through(i, 0, x, u, h, q, m);
+      if (!late && dh_out.base != nullptr) end(i, x, h, m, inverse1);
+      if constexpr (VEC) rows.done();
+    }
+  };
+  // With h, whose sums fill the registers, rows go in turn (8192 x 2048 45 us, one by one 47; 32768 x 2048 137 and 148); where
+  // they are not asked for ahead, one by one, as their loads are what counts (1003 x 775 15, in
+  // turn 20, two at a time 18).  Else two at a time (8192 x 2048 without a norm after the block 28 us,
+  // one by one 41; 4096 x 8192, where a barrier is a cluster's, 140 and 177).
+  if constexpr (FULL && VEC && SHARE == kBlock) {
+    in_turn();
+  } else {
+    uint32_t i = own.first;
+    if constexpr (!FULL || SHARE == kCluster)
+      for (; i + own.step < rows.rows; i += 2 * own.step) make(std::integral_constant<int, 2>(), i);
+    for (; i < rows.rows; i += own.step) make(std::integral_constant<int, 1>(), i);
+  }
   const auto put = [&](int q, const Eight& x) {
     if ((a.wanted >> q & 1) == 0) return;
     float* to = a.sums + (static_cast<int64_t>(q) * a.blocks + own.first) * a.width;
@@ -627,9 +676,14 @@ __global__ void __launch_bounds__(kMostThreads)
   put(kDw, dw);
   if constexpr (LAYER) put(kDb, db);
   if constexpr (FULL) {
-    put(kDgate, dg);
-    put(kDw1, dw1);
-    if constexpr (LAYER) put(kDb1, db1);
+    const Eight g = at.load_vector(a.gate, 1.0f, wvec) * a.alpha;
+    put(kDw1, ah * g);
+    Eight dg = ah * w1.get();
+    if constexpr (LAYER) {
+      put(kDb1, aa * g);
+      dg = fma8(aa, at.load_vector(a.b1, 0.0f, wvec), dg);
+    }
+    put(kDgate, dg * a.alpha);
   }
   if constexpr (SHARE == kCluster) cluster_sync();  // no block ends while others write to it
 }
