@@ -15,7 +15,10 @@ namespace zeroadam {
 namespace {
 
 constexpr int kMostThreads = 512, kMostWarps = kMostThreads / 32, kMostCluster = 8;
-constexpr int kStages = 4;  // rows under way
+// Rows under way.  More of them make the forward pass slower where HBM bounds it (32768 x 2048 with
+// 2, 3, 4: 83, 96, 98 us), fewer the backward pass, which its instructions bound (2, 3, 4 without a
+// norm after the block: 119, 110, 85 us).
+constexpr int kForwardStages = 2, kBackwardStages = 4;
 constexpr int kSumsAtOnce = 8;
 
 // Who shares a row: a block up to 4,096 columns, a cluster of blocks beyond.  A thread has 8
@@ -204,10 +207,10 @@ __device__ __forceinline__ const uint16_t* row_at(const uint16_t* base, uint32_t
                                            static_cast<uint64_t>(i) * pitch);
 }
 
-// The rows that a thread reads, kStages ahead (VEC): its own 16 bytes of each input, from its
+// The rows that a thread reads, STAGES under way (VEC): its own 16 bytes of each input, from its
 // own place in shared memory, so no thread waits for another's.  Rows that are not on 16-byte
 // boundaries are read when they are wanted.  FIRST to LAST: the inputs there may be.
-template <bool VEC, int FIRST, int LAST>
+template <bool VEC, int FIRST, int LAST, int STAGES>
 struct Rows {
   const NormArgs& a;
   const Columns<VEC>& at;
@@ -225,7 +228,7 @@ struct Rows {
         rows(static_cast<uint32_t>(a.rows)) {
     place = smem_addr(ring) + threadIdx.x * 16;
     stage = a.inputs * each;
-    end = kStages * stage;
+    end = STAGES * stage;
 #pragma unroll
     for (int q = FIRST; q <= LAST; ++q) {
       there |= (a.in[q] != nullptr ? 1u : 0u) << q;
@@ -255,7 +258,7 @@ struct Rows {
   __device__ __forceinline__ void begin() {
     if constexpr (VEC) {
 #pragma unroll
-      for (int k = 1; k < kStages; ++k) ask();
+      for (int k = 1; k < STAGES; ++k) ask();
     }
   }
   // The next R rows can be read.
@@ -263,9 +266,9 @@ struct Rows {
     if constexpr (VEC) {
       ask();
       if (R > 1) {
-        copy_wait<kStages - 2>();  // (all but the last two)
+        copy_wait<STAGES - 2>();  // (all but the last two)
       } else {
-        copy_wait<kStages - 1>();
+        copy_wait<STAGES - 1>();
       }
     }
   }
@@ -431,7 +434,7 @@ __global__ void __launch_bounds__(kMostThreads, 2)
   launch_dependents();
   const RowOwner<SHARE> own;
   const Columns<VEC> at(own.at, own.lanes, static_cast<int>(a.width));
-  Rows<VEC, kInR, kInGate> rows(a, at, ring, own.first, own.step);
+  Rows<VEC, kInR, kInGate, kForwardStages> rows(a, at, ring, own.first, own.step);
   rows.begin();
   const Output<VEC> s_out(a.s_out, a.pitch_s), y_out(a.y, a.pitch_y);
   const bool wvec = a.wvec != 0;
@@ -444,44 +447,88 @@ __global__ void __launch_bounds__(kMostThreads, 2)
   begin_sums<SHARE>(part);
   RowSum<SHARE> row_sum{part};
   const float inv_width = 1.0f / static_cast<float>(a.width);
-  const auto center = [&](Eight& x) {
-    float m[1] = {sum8(x)};
-    row_sum(m);
-    x = x + all_of(-m[0] * inv_width);
+  const bool layer = kinds.layer(), post_layer = kinds.post_layer();
+  const auto center = [&](Eight& x, float sum) {
+    x = x + all_of(-sum * inv_width);
     at.clear(x);
   };
-  const auto inverse_of = [&](const Eight& x) {
-    float q[1] = {dot8(x, x)};
-    row_sum(q);
-    return rsqrtf(fmaf(q[0], inv_width, a.eps));
-  };
-  for (uint32_t i = own.first; i < rows.rows; i += own.step, rows.done()) {
-    rows.arrive();
-    Eight s = rows.read(kInR, i, 0);
-    if (rows.has(kInH)) {
-      Eight h = rows.read(kInH, i, 1);
-      if (kinds.post()) {
-        if (kinds.post_layer()) center(h);
-        h = h * inverse_of(h);
-      }
-      if (rows.has(kInGate)) {
-        Eight p = h * scale1;
-        if constexpr (LAYER) p = p + bias1;
-        s = fma8(p, rows.read(kInGate, i, 2), s);
-      } else {
-        if constexpr (LAYER) s = s + bias1;
-        s = fma8(h, scale1, s);
-      }
+  const auto inverse_of = [&](float squares) { return rsqrtf(fmaf(squares, inv_width, a.eps)); };
+  // s of row i, from r and h standardized
+  const auto add = [&](uint32_t i, Eight s, const Eight& h) {
+    if (rows.has(kInGate)) {
+      Eight p = h * scale1;
+      if constexpr (LAYER) p = p + bias1;
+      s = fma8(p, rows.read(kInGate, i, 2), s);
+    } else {
+      if constexpr (LAYER) s = s + bias1;
+      s = fma8(h, scale1, s);
     }
     s_out.put(at, i, s);
-    if (kinds.layer()) {
-      at.clear(s);
-      center(s);
-    }
-    s = s * inverse_of(s);
+    if constexpr (LAYER)
+      if (layer) at.clear(s);
+    return s;
+  };
+  const auto end = [&](uint32_t i, Eight& s, float squares) {
+    s = s * inverse_of(squares);
     if constexpr (LAYER) s = fma8(s, w, b);
     else s = s * w;
     y_out.put(at, i, s);
+  };
+  if (VEC && kinds.post()) {
+    // The sums of a row's s are taken with those of the next row's h: one wait a row, not two
+    // (8192 x 2048 26 -> 23 us, 4096 x 8192 in clusters 93 -> 66).  Rows that are not asked for ahead
+    // are better one by one, r beside h (1003 x 775 9 us, in turn 15).
+    Eight s = all_of(0.0f);
+    for (uint32_t i = own.first;; i += own.step) {
+      const bool more = i < rows.rows, before = i != own.first;
+      if (!more && !before) break;
+      Eight h = all_of(0.0f);
+      if (more) {
+        rows.arrive();
+        h = rows.read(kInH, i, 1);
+      }
+      if (layer || post_layer) {
+        float m[2] = {sum8(h), sum8(s)};
+        row_sum(m);
+        if (post_layer) center(h, m[0]);
+        if (layer) center(s, m[1]);
+      }
+      float q[2] = {dot8(h, h), dot8(s, s)};
+      row_sum(q);
+      if (before) end(i - own.step, s, q[1]);
+      if (!more) break;
+      s = add(i, rows.read(kInR, i, 0), h * inverse_of(q[0]));
+      rows.done();
+    }
+  } else {
+    for (uint32_t i = own.first; i < rows.rows; i += own.step, rows.done()) {
+      rows.arrive();
+      Eight s = rows.read(kInR, i, 0);
+      if (rows.has(kInH)) {
+        Eight h = rows.read(kInH, i, 1);
+        if (!VEC && kinds.post()) {
+          if (post_layer) {
+            float m[1] = {sum8(h)};
+            row_sum(m);
+            center(h, m[0]);
+          }
+          float q[1] = {dot8(h, h)};
+          row_sum(q);
+          h = h * inverse_of(q[0]);
+        }
+        s = add(i, s, h);
+      } else {
+        s_out.put(at, i, s);
+      }
+      if (layer) {
+        float m[1] = {sum8(s)};
+        row_sum(m);
+        center(s, m[0]);
+      }
+      float q[1] = {dot8(s, s)};
+      row_sum(q);
+      end(i, s, q[0]);
+    }
   }
   if constexpr (SHARE == kCluster) cluster_sync();  // no block ends while others write to it
 }
@@ -500,7 +547,7 @@ __global__ void __launch_bounds__(kMostThreads)
   launch_dependents();
   const RowOwner<SHARE> own;
   const Columns<VEC> at(own.at, own.lanes, static_cast<int>(a.width));
-  Rows<VEC, kInDy, kInGate> rows(a, at, ring, own.first, own.step);
+  Rows<VEC, kInDy, kInGate, kBackwardStages> rows(a, at, ring, own.first, own.step);
   rows.begin();
   const Output<VEC> dr_out(a.dr, a.pitch_dr), dh_out(a.dh, a.pitch_dh), dgate_out(a.dgate_rows, a.pitch_dg);
   const bool wvec = a.wvec != 0;
@@ -650,10 +697,11 @@ __global__ void __launch_bounds__(kMostThreads)
       if constexpr (VEC) rows.done();
     }
   };
-  // With h, whose sums fill the registers, rows go in turn (8192 x 2048 45 us, one by one 47; 32768 x 2048 137 and 148); where
-  // they are not asked for ahead, one by one, as their loads are what counts (1003 x 775 15, in
-  // turn 20, two at a time 18).  Else two at a time (8192 x 2048 without a norm after the block 28 us,
-  // one by one 41; 4096 x 8192, where a barrier is a cluster's, 140 and 177).
+  // With h, whose sums fill the registers, rows go in turn (8192 x 2048 45 us, one by one 47; 32768 x
+  // 2048 137 and 148); where they are not asked for ahead, one by one, as their loads are what
+  // counts (1003 x 775 15, in turn 20, two at a time 18).  Else two at a time (8192 x 2048 without
+  // a norm after the block 28 us, one by one 41; 4096 x 8192, where a barrier is a cluster's, 125
+  // and 177).
   if constexpr (FULL && VEC && SHARE == kBlock) {
     in_turn();
   } else {
@@ -784,9 +832,9 @@ NormArgs args_of(const BlockNormLaunch& L) {
 }
 
 // Bytes of the ring, for each thread 16 of each input.
-constexpr int kMostRing = kStages * kInputs * kMostThreads * 16;
+constexpr int kMostRing = kBackwardStages * kInputs * kMostThreads * 16;
 static_assert(kMostRing + 8192 <= kSmem, "the ring and the parts of the sums");
-int ring_bytes(const NormArgs& a, int threads) { return kStages * a.inputs * threads * 16; }
+int ring_bytes(const NormArgs& a, int threads, int stages) { return stages * a.inputs * threads * 16; }
 
 // (Biases are LAYER's.)
 bool has_layer(const NormArgs& a) { return a.kind == ZERO_NORM_LAYER || a.post == ZERO_NORM_LAYER; }
@@ -824,13 +872,13 @@ cudaError_t launch_backward(const NormArgs& a, bool vec, Chain* chain) {
                                             : block_norm_backward_kernel<true, kCluster, FULL, LAYER>)
                           : (r.cluster == 1 ? block_norm_backward_kernel<false, kBlock, FULL, LAYER>
                                             : block_norm_backward_kernel<false, kCluster, FULL, LAYER>);
-  return launch_ring(kernel, a.blocks, r.threads, vec ? ring_bytes(a, r.threads) : 0, r.cluster, a, chain);
+  return launch_ring(kernel, a.blocks, r.threads, vec ? ring_bytes(a, r.threads, kBackwardStages) : 0, r.cluster, a, chain);
 }
 
 template <bool LAYER>
 cudaError_t launch_forward(const NormArgs& a, bool vec, Chain* chain) {
   const RowShape r = row_shape(a.width);
-  const int smem = vec ? ring_bytes(a, r.threads) : 0;
+  const int smem = vec ? ring_bytes(a, r.threads, kForwardStages) : 0;
   int64_t each = 1024 / r.threads;  // blocks an SM
   if (each > 24) each = 24;
   if (each > kSmem / (smem + 2560)) each = kSmem / (smem + 2560);
