@@ -270,8 +270,23 @@ __device__ __forceinline__ void total_losses(const LossArgs& a, bool sums) {
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   double total = 0.0;
   int32_t valid = 0;
+  // Where the rows that count are counted, and c is alike for all: the losses alone, an ignored
+  // row's being 0.
+  const bool counted = a.place != nullptr && a.rows == a.all_rows && a.scale == nullptr;
+  if (counted) {
+    constexpr int U = 16;
+    valid = threadIdx.x == 0 ? __ldcg(&a.words->rows) : 0;
+    for (int64_t i0 = threadIdx.x; sums && i0 < a.all_rows; i0 += U * kFinishThreads) {
+      float x[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        x[u] = i0 + u * kFinishThreads < a.all_rows ? __ldcg(a.losses + i0 + u * kFinishThreads) : 0.0f;
+#pragma unroll
+      for (int u = 0; u < U; ++u) total += static_cast<double>(x[u]);
+    }
+  }
   constexpr int U = 8;
-  for (int64_t i0 = threadIdx.x; i0 < a.all_rows; i0 += U * kFinishThreads) {
+  for (int64_t i0 = threadIdx.x; !counted && i0 < a.all_rows; i0 += U * kFinishThreads) {
     float x[U], c[U];
     int64_t t[U];
 #pragma unroll
@@ -428,6 +443,12 @@ __global__ void __launch_bounds__(kFinishThreads) loss_ends_kernel(const __grid_
   constexpr int kWarps = DZ ? kFinishWarps : 1, kThreads = 32 * kWarps;  // of a row
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, thread = threadIdx.x % kThreads;
   const int64_t n = rows_of(a), filled = filled_rows(a, n);
+  if constexpr (!DZ) {  // e of the rows behind the last: zeros, by the whole grid (43 rows of 50257 columns, a warp a row: 5 us)
+    const int64_t vectors = (a.vocab + 7) / 8;
+    for (int64_t i = n; i < filled; ++i)
+      for (int64_t j = blockIdx.x * kFinishThreads + threadIdx.x; j < vectors; j += gridDim.x * kFinishThreads)
+        reinterpret_cast<uint4*>(a.held + i * a.ldz)[j] = make_uint4(0, 0, 0, 0);
+  }
   constexpr int kRows = kFinishWarps / kWarps;  // of a block at one time
   for (int64_t i = static_cast<int64_t>(blockIdx.x) * kRows + threadIdx.x / kThreads; i < filled;
        i += static_cast<int64_t>(gridDim.x) * kRows) {
@@ -435,7 +456,7 @@ __global__ void __launch_bounds__(kFinishThreads) loss_ends_kernel(const __grid_
     const int64_t from = a.first + (a.place == nullptr ? i : i < n ? __ldcg(a.place + i) : 0);  // the caller's row
     const float zt = __ldcg(a.zt + i);
     float ref = __ldcg(a.ref + i), sum = 0.0f, top = -INFINITY;
-    if (t != -1) {
+    if (a.place != nullptr ? i < n : t != -1) {  // (the same; with i nothing waits for t)
       constexpr int U = 8;
       for (int k0 = thread; k0 < a.parts; k0 += U * kThreads) {
         float2 s[U];
@@ -485,9 +506,9 @@ __global__ void __launch_bounds__(kFinishThreads) loss_ends_kernel(const __grid_
     if (t == -1) loss = f = 0.0f;
     if (t == -2) loss = f = NAN;
     if (thread == 0 && i < n) a.losses[from] = loss;
-    // (the pitches have room for whole vectors; an ignored row's e are not read)
-    uint4* e = reinterpret_cast<uint4*>(a.held + i * a.ldz);
     if constexpr (DZ) {
+      // (the pitch has room for whole vectors; an ignored row's e are not read)
+      uint4* e = reinterpret_cast<uint4*>(a.held + i * a.ldz);
       constexpr int U = 4;
       const uint32_t vectors = static_cast<uint32_t>((a.vocab + 7) / 8);
       for (uint32_t j0 = thread; j0 < vectors; j0 += U * kThreads) {
@@ -515,8 +536,6 @@ __global__ void __launch_bounds__(kFinishThreads) loss_ends_kernel(const __grid_
         a.factor[i] = f;
         if (t >= 0) a.held[i * a.ldz + t] = to_bf16(-sum);
       }
-      if (t == -1)
-        for (int64_t j = thread; j < (a.vocab + 7) / 8; j += kThreads) e[j] = make_uint4(0, 0, 0, 0);
       if (a.xs == nullptr) continue;
       const uint16_t* x = a.xc + i * a.ldxc;
       uint16_t* to = a.xs + i * a.ldxc;
