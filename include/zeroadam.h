@@ -62,8 +62,10 @@ extern "C" {
 #define ZERO_E_RANK (-4)    /* rank not in [0, world) and not ZERO_ALL_RANKS        */
 #define ZERO_E_STEP (-5)    /* t < 1 (t is the 1-based step count after increment)  */
 #define ZERO_E_ALIGN (-6)   /* bf16 pointer odd, or fp32 pointer not 4-byte aligned */
-#define ZERO_E_HPARAM (-7)  /* lr/eps (weight_decay, max_norm) < 0 or not finite; beta not in [0, 1) */
-#define ZERO_E_LAYOUT (-8)  /* unknown layout, activation or flag, or a shard layout with ALL_RANKS */
+#define ZERO_E_HPARAM (-7)  /* lr/eps (weight_decay, max_norm) < 0 or not finite; beta not in [0, 1);
+                               scale, alpha not finite */
+#define ZERO_E_LAYOUT (-8)  /* unknown layout, activation, norm or flag, a shard layout with ALL_RANKS,
+                               or a tensor that the norm's kind does not have */
 #define ZERO_E_PLAN (-9)    /* the plan's fields are not those zero_plan computes   */
 #define ZERO_E_ALIAS (-10)  /* an output buffer overlaps another buffer             */
 #define ZERO_E_LAUNCH (-11) /* the CUDA launch failed; see zero_strerror            */
@@ -90,7 +92,7 @@ extern "C" {
 #define ZERO_GRAD_LAYOUT_MASK 0x0f
 #define ZERO_GRAD_F32 0x10 /* flag: gradient buffers hold fp32 (default: bf16) */
 #define ZERO_ACC_BF16 0x20 /* flag: round the running sum over ranks to bf16 after every addition */
-#define ZERO_GRAD_ACCUMULATE 0x40 /* zero_linear_backward: add to dw and dbias instead of writing them */
+#define ZERO_GRAD_ACCUMULATE 0x40 /* gradients of weights (dw, dbias, dtable, ...): add to them instead of writing */
 
 /* param_layout */
 #define ZERO_PARAM_FULL 0  /* param_bf16: the whole flat parameter buffer (>= numel elements) */
@@ -525,7 +527,8 @@ int zero_embedding_forward(const zero_embedding_t* shape, const void* table, con
  *   dy          bf16.
  *   padding     an id whose rows have no gradient (-1: none).  Rows whose id is
  *               not in [0, vocab) have none either.
- *   dtable      bf16, or fp32 with ZERO_GRAD_F32.
+ *   dtable      bf16, or fp32 with ZERO_GRAD_F32.  Added to fp32 what comes to
+ *               less than 2^-126 may be held as 0.
  *   flags       ZERO_IDS_I32, ZERO_GRAD_F32, ZERO_GRAD_ACCUMULATE.
  * No workspace.  Errors: as zero_embedding_forward.
  */
@@ -569,7 +572,7 @@ typedef struct {
  * Sums are fp32.  The products' operands are bf16 (the tensor cores' type): the
  * exponentials, and then dz, each rounded once; of more than 2^25 values (rows *
  * vocab) the exponentials alone, and x times its row's factor for dw, whose rounding
- * averages out over the rows.  Exponentials below exp(-87) of the target's (of the
+ * averages out over a token's rows.  Exponentials below exp(-87) of the target's (of the
  * largest, in a row whose loss is above 44) are 0 in dz.  Rows that are ignored are
  * left out of the products.  The loss alone takes other kernels than the loss with
  * gradients, and may differ from it in its last bits.  Rows go in pieces whose
@@ -680,8 +683,8 @@ int zero_device_status(void);
  * stepped range's first element), every zero3_unit_gather or
  * zero3_unit_gather_rows that uses the TMA copy (see those calls), every
  * zero3_unit_step that runs as a single launch, and every product of
- * zero_linear_forward (more than 16 rows) and zero_linear_backward tells its
- * producers to issue no copies.  Every wait then runs out after its limit (about one second),
+ * zero_linear_forward (more than 16 rows), zero_linear_backward and
+ * zero_linear_cross_entropy tells its producers to issue no copies.  Every wait then runs out after its limit (about one second),
  * the outputs of the parts that wait are not written (at world <= 4 the
  * unit step's step part reads its gradients without staging and completes),
  * and zero_device_status reports ZERO_E_TIMEOUT; the device and its context

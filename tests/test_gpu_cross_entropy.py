@@ -163,6 +163,23 @@ def test_far_targets(rows, k, v):
     check((x * 4.0), w, t)                       # most rows
 
 
+@pytest.mark.parametrize("rows,k,v", [(1, 64, 50257), (2, 2048, 4099), (7, 775, 9001), (130, 520, 5003)])
+def test_few_rows_of_many_columns(rows, k, v):
+    """More weights than one block reads again for a row: another reference is a second run of the
+    product for few rows too, and dz is made in place."""
+    assert rows * v <= 2 ** 25 and k * v > 2 ** 21
+    x, w = matrix(rows, k, 1.0, 1), matrix(v, k, 2.0 / math.sqrt(k), 2)
+    t = targets_of(rows, v, 3)
+    check(x, w, t)
+    x[0] *= 32.0
+    t[0] = (x[0].float() @ w.float().t()).argmin()
+    if rows > 2:
+        t[1] = -100
+        x[1] = float("nan")
+    losses, *_ = check(x, w, t)
+    assert losses[0] > 60
+
+
 def test_certain_rows():
     """A model that is sure of its target: 1 - p_t as small as 1e-9 comes out to its last bits."""
     k, v = 32, 300

@@ -431,9 +431,9 @@ const char* zero_strerror(int status) {
     case ZERO_E_STEP: return "t must be >= 1 (1-based step count)";
     case ZERO_E_ALIGN: return "bf16 pointers must be 2-byte and fp32 pointers 4-byte aligned";
     case ZERO_E_HPARAM: return "lr, eps, weight_decay and max_norm must be finite and >= 0, "
-                               "betas in [0, 1)";
-    case ZERO_E_LAYOUT: return "unknown layout, activation or flag, or a shard layout with "
-                               "ZERO_ALL_RANKS";
+                               "betas in [0, 1), scale and alpha finite";
+    case ZERO_E_LAYOUT: return "unknown layout, activation, norm or flag, a shard layout with "
+                               "ZERO_ALL_RANKS, or a tensor that the norm's kind does not have";
     case ZERO_E_PLAN: return "plan fields differ from zero_plan(numel, world)";
     case ZERO_E_ALIAS: return "an output buffer overlaps another buffer";
     case ZERO_E_DEVICE:

@@ -11,12 +11,12 @@
 // adds up S'; then dx_i = f_i sum over j of e_ij W_j takes f in its epilogue, and
 // dw_j = sum over i of e_ij (f_i x_i) takes x with f in it, rounded to bf16.  So nothing passes over
 // the [rows][vocab] values between the products, which read them as they were written (with a
-// pass that makes dz of them in place 8192 x 2048 -> 50257 took 3,400 us instead of 3,090, and
-// 4096 x 768 -> 50257 709 instead of 611).  The price is one more rounding in dw, of f x: over
-// thousands of rows it averages out (these two cases' dw is 1.05 times as far from the exact one
-// as its own rounding puts it), over few it does not (37 x 256 -> 515: 1.5 times).  So where
-// the values stay in L2, up to 2^25 of them, that pass is made: dz is rounded to bf16 there, and
-// dw of few rows is as near as dx (1.2 times).
+// pass that makes dz of them in place 8192 x 2048 -> 50257 took 3,400 us instead of 3,100, and
+// 4096 x 768 -> 50257 709 instead of 600).  The price is one more rounding in dw, of f x: for a
+// token that is the target of many rows it averages out (these two cases' dw is 1.05 times as
+// far from the exact one as its own rounding puts it), for those of one row it does not (1.4
+// times).  So where the values stay in L2, up to 2^25 of them, that pass is made, and dz is
+// rounded to bf16 there (1.0 to 1.3 times).
 // A row whose S' passes 2^64 (the target 44 below the largest logit) leaves the range where
 // products with 1 / S' lose nothing: its reference becomes the largest logit, which the first
 // product found, and product and ends run once more; the launches that do so end at once
