@@ -67,6 +67,44 @@ def check(dy, ids, dtable, *, scale=1.0, padding=None, add=False, **kw):
     assert (got == before)[(count == 0).expand_as(got)].all()      # rows of no token, to the bit
 
 
+# few tokens, whose rows several blocks share: around the runs of rows and what is added at a time;
+# tokens of no row; and as many tokens as there are blocks of their own for, and one more
+FEW = [(9000, 64, 2), (5000, 775, 3), (20000, 260, 1), (3000, 2048, 19), (511, 8, 304), (513, 8, 305), (4097, 100, 608),
+       (4097, 100, 609), (8192, 16, 5)]
+
+
+@pytest.mark.parametrize("shape", FEW)
+@pytest.mark.parametrize("dtype,add,ids,pitch,offset", [
+    (BF, False, torch.int64, 0, 0), (F32, True, torch.int32, 8, 8), (BF, True, torch.int64, 1, 3),
+    (F32, False, torch.int32, 5, 1)])
+def test_gradient_of_few_tokens(shape, dtype, add, ids, pitch, offset):
+    m, d, v = shape
+    dy, i = matrix(m, d, 1.0, 1, pitch, offset), ids_of(m, v, 2, ids)
+    for padding in (None, 0, v // 2):
+        dtable = matrix(v, d, 1.0, 3, pitch, offset, dtype) if add else blank(v, d, dtype, pitch, offset)
+        check(dy, i, dtable, scale=1.5, add=add, padding=padding)
+        again = matrix(v, d, 1.0, 3, pitch, offset, dtype) if add else blank(v, d, dtype, pitch, offset)
+        za.zero_embedding_backward(dy, i, again, scale=1.5, padding=padding, accumulate=add)
+        assert torch.equal(again, dtable)
+        if not add:
+            untouched(dtable)
+    i[m // 3:] = v                # ids outside the table, and of the rest all one token
+    i[:m // 3] = v - 1
+    dtable = matrix(v, d, 1.0, 3, pitch, offset, dtype) if add else blank(v, d, dtype, pitch, offset)
+    check(dy, i, dtable, scale=1.5, add=add)
+
+
+@pytest.mark.parametrize("width", [1, 7, 8, 100, 255, 256, 257, 263, 513])
+@pytest.mark.parametrize("offset", [0, 1, 2, 3, 4, 5, 6, 7])
+def test_gradients_rows_at_every_address(width, offset):
+    """Rows that begin at every 2-byte place of a 16-byte vector, among values that are not theirs."""
+    flat = torch.full((40 * (width + 3) + 16,), float("nan"), dtype=BF, device="cuda")
+    for v in (2, 400):
+        dy = flat[offset:offset + 40 * (width + 3)].view(40, width + 3)[:, :width]
+        dy.copy_(matrix(40, width, 1.0, 1))
+        check(dy, ids_of(40, v, 2), blank(v, width))
+
+
 @pytest.mark.parametrize("shape", SHAPES)
 @pytest.mark.parametrize("dtype,add,ids,pitch,offset", [
     (BF, False, torch.int64, 0, 0), (F32, False, torch.int32, 0, 0), (F32, True, torch.int64, 8, 8),

@@ -121,7 +121,9 @@ struct ScatterArgs {
   int64_t rows, width, vocab, ldy, ldt, padding;
   int32_t ids_i32, grad_f32, accumulate;
   int32_t classes, slices;
+  int32_t blocks;     // that share a token's rows (few tokens)
   uint64_t inverse;   // 2^64 / classes, rounded up: its high product with an id is the quotient
+  int32_t out_vec;    // rows of dtable are on 16 bytes
   int32_t bulk;       // a row of dtable is whole 16-byte vectors: zeros go by the TMA engine
   float scale;
 };
@@ -145,8 +147,31 @@ struct ScatterShared {
   uint32_t empty[kWindow / 32]; // tokens of no row, a bit each
 };
 
+// The 8 elements from the s-th on of a lane's aligned vector and the next lane's (lane 31's: `edge`);
+// s is alike for the warp.
+__device__ __forceinline__ uint4 from_column(uint4 v, uint4 edge, int s, int lane) {
+  uint32_t w[8] = {v.x, v.y, v.z, v.w};
+  const uint32_t e[4] = {edge.x, edge.y, edge.z, edge.w};
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const uint32_t next = __shfl_down_sync(0xffffffffu, w[k], 1);
+    w[4 + k] = lane == 31 ? e[k] : next;
+  }
+  if (s & 4)
+#pragma unroll
+    for (int k = 0; k < 6; ++k) w[k] = w[k + 2];
+  if (s & 2)
+#pragma unroll
+    for (int k = 0; k < 5; ++k) w[k] = w[k + 1];
+  if (s & 1)
+#pragma unroll
+    for (int k = 0; k < 4; ++k) w[k] = __funnelshift_r(w[k], w[k + 1], 16);
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
 // The sum of a run of rows: 8 columns a lane, in the order of the rows, eight rows' loads
-// under way at a time.  A chain ends after 64 rows, so that its error does not grow with
+// under way at a time.  Rows that are not on 16 bytes (VEC: all are) come in aligned vectors too,
+// shifted between lanes.  A chain ends after 64 rows, so that its error does not grow with
 // a common token's count.
 template <bool VEC>
 struct SliceSum {
@@ -154,51 +179,36 @@ struct SliceSum {
   int chain = 0;
 
   // Rows rows[0], ..., rows[U - 1], those whose bit of `here` is set; after(u) follows the u-th.
+  // A lane's vector may end past the row: what is there goes into columns that no one writes.
   template <int U, typename After>
   __device__ __forceinline__ void walk(const ScatterArgs& a, const int32_t* rows, uint32_t here, int64_t col,
                                        int lane, After after) {
-    if constexpr (VEC) {
-      uint4 v[U];
-      const bool in = col + 8 * lane + 8 <= a.width, some = col + 8 * lane < a.width;
-      const uint16_t* from = a.dy + col + 8 * lane;
+    uint4 v[U], edge[VEC ? 1 : U];
+    const uint16_t* const first = a.dy + col;
+    const int64_t n = a.width - col;  // (lanes from there on have nothing)
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const bool take = here >> u & 1;
-        v[u] = load16_if(take && in, from + (take ? rows[u] : 0) * a.ldy);
+    for (int u = 0; u < U; ++u) {
+      const bool take = here >> u & 1;
+      const uint16_t* from = first + (take ? rows[u] : 0) * a.ldy;
+      if constexpr (VEC) {
+        v[u] = load16_if(take && 8 * lane < n, from + 8 * lane);
+      } else {
+        // the aligned vector that a lane's first column lies in; the next one is the next lane's
+        const int s = static_cast<int>(reinterpret_cast<uintptr_t>(from) % 16 / 2);
+        v[u] = load16_if(take && 8 * lane - s < n, from + 8 * lane - s);
+        edge[u] = load16_if(take && lane == 31 && s > 0 && 256 - s < n, from + 256 - s);
       }
+    }
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        if ((here >> u & 1) == 0) continue;
-        float x[8];
-        bf16x8(v[u], x);
-        if (!in && some) {
+    for (int u = 0; u < U; ++u) {
+      if ((here >> u & 1) == 0) continue;
+      if constexpr (!VEC)
+        v[u] = from_column(v[u], edge[u], static_cast<int>(reinterpret_cast<uintptr_t>(first + rows[u] * a.ldy) % 16 / 2), lane);
+      float x[8];
+      bf16x8(v[u], x);
 #pragma unroll
-          for (int c = 0; c < 8; ++c)
-            if (col + 8 * lane + c < a.width) x[c] = bf16_at(from + rows[u] * a.ldy + c);
-        }
-#pragma unroll
-        for (int c = 0; c < 8; ++c) run[c] += x[c];
-        after(u);
-      }
-    } else {
-#pragma unroll
-      for (int h = 0; h < U; h += 2) {
-        float x[2][8];
-#pragma unroll
-        for (int u = 0; u < 2; ++u)
-#pragma unroll
-          for (int c = 0; c < 8; ++c) {
-            const int64_t j = col + lane + 32 * c;
-            x[u][c] = (here >> (h + u) & 1) && j < a.width ? bf16_at(a.dy + rows[h + u] * a.ldy + j) : 0.0f;
-          }
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          if ((here >> (h + u) & 1) == 0) continue;
-#pragma unroll
-          for (int c = 0; c < 8; ++c) run[c] += x[u][c];
-          after(h + u);
-        }
-      }
+      for (int c = 0; c < 8; ++c) run[c] += x[c];
+      after(u);
     }
   }
   __device__ __forceinline__ void add(const ScatterArgs& a, const int32_t* rows, int n, int64_t col,
@@ -228,11 +238,10 @@ __device__ __forceinline__ void add_vector(float* to, const float* x) {
 }
 
 // A lane's 8 columns of one row of the table's gradient.
-template <bool VEC>
 __device__ __forceinline__ void put_slice(const ScatterArgs& a, int64_t v, int64_t col, const float x[8],
                                           int lane) {
   const int64_t at = v * a.ldt + col;
-  if (VEC && col + 8 * lane + 8 <= a.width) {
+  if (a.out_vec && col + 8 * lane + 8 <= a.width) {
     if (a.grad_f32) {
       float* o = static_cast<float*>(a.dtable) + at + 8 * lane;
       if (a.accumulate) {
@@ -256,7 +265,7 @@ __device__ __forceinline__ void put_slice(const ScatterArgs& a, int64_t v, int64
   }
 #pragma unroll
   for (int c = 0; c < 8; ++c) {
-    const int64_t j = VEC ? 8 * lane + c : lane + 32 * c;
+    const int64_t j = 8 * lane + c;
     if (col + j >= a.width) continue;
     if (a.grad_f32) {
       float* o = static_cast<float*>(a.dtable) + at + j;
@@ -292,7 +301,7 @@ __device__ __forceinline__ void finish_token(const ScatterArgs& a, const Scatter
   s.join();
 #pragma unroll
   for (int c = 0; c < 8; ++c) s.sum[c] *= a.scale;
-  put_slice<VEC>(a, (p.w0 + t) * p.classes + p.mine, p.col, s.sum, lane);
+  put_slice(a, (p.w0 + t) * p.classes + p.mine, p.col, s.sum, lane);
 }
 
 // n rows by the whole block: a run of them a warp, the warps' sums added in their order.
@@ -579,6 +588,87 @@ __global__ void __launch_bounds__(kScatterThreads, 2)
   if (a.bulk) bulk_wait_all();
 }
 
+// Few tokens: a cluster of up to 8 blocks takes one token and one slice, its blocks a run of the
+// rows each and their warps a run of those.  Nothing is sorted: a warp lists the rows of its run
+// that are the token's, and adds them up 64 or more at a time.  The warps' sums are added in
+// their order, and the blocks'.  What bounds it is the latency of the rows' loads (16384 x 2048 of
+// 2 tokens: 18 us; by the kernel above, where a token's rows are one block's, 123).
+constexpr int kFewWarps = 16, kFewThreads = 32 * kFewWarps, kFewCluster = 8;
+constexpr int kFewItems = 2 * kSms, kManyRows = 4096;
+constexpr int kFewListed = 64, kFewAsked = 4;  // rows that are added up; loads of 32 ids under way
+
+template <bool VEC>
+__global__ void __launch_bounds__(kFewThreads, 1)
+    embedding_few_tokens_kernel(const __grid_constant__ ScatterArgs a) {
+  __shared__ alignas(16) float part[kFewWarps][kSlice];
+  __shared__ alignas(16) float sum[kSlice];
+  __shared__ int32_t list[kFewWarps][kFewListed + 32 * kFewAsked];
+  __shared__ int32_t found[kFewWarps], all;
+  wait_for_predecessor();
+  launch_dependents();
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, blocks = a.blocks;
+  const int rank = static_cast<int>(blockIdx.x) % blocks, item = static_cast<int>(blockIdx.x) / blocks;
+  const int64_t token = item % a.vocab, col = static_cast<int64_t>(item / static_cast<int>(a.vocab)) * kSlice;
+  const int64_t run = rank * kFewWarps + warp, runs = static_cast<int64_t>(blocks) * kFewWarps;
+  const int64_t from = a.rows * run / runs, to = a.rows * (run + 1) / runs;
+  SliceSum<VEC> s;
+  int n = 0, rows = 0;
+  for (int64_t i = from; token != a.padding && i < to; i += 32 * kFewAsked) {
+    int64_t id[kFewAsked];
+#pragma unroll
+    for (int u = 0; u < kFewAsked; ++u) {
+      const int64_t k = i + 32 * u + lane;
+      id[u] = id_at(a.ids, a.ids_i32, k < to ? k : to - 1);
+    }
+#pragma unroll
+    for (int u = 0; u < kFewAsked; ++u) {
+      const int64_t k = i + 32 * u + lane;
+      const bool has = k < to && id[u] == token;
+      const uint32_t those = __ballot_sync(0xffffffffu, has);
+      if (has) list[warp][n + __popc(those & ((1u << lane) - 1u))] = static_cast<int32_t>(k);
+      n += __popc(those);
+    }
+    if (n < kFewListed && i + 32 * kFewAsked < to) continue;
+    __syncwarp();
+    s.add(a, list[warp], n, col, lane);
+    __syncwarp();
+    rows += n;
+    n = 0;
+  }
+  s.join();
+  *reinterpret_cast<float4*>(&part[warp][8 * lane]) = make_float4(s.sum[0], s.sum[1], s.sum[2], s.sum[3]);
+  *reinterpret_cast<float4*>(&part[warp][8 * lane + 4]) = make_float4(s.sum[4], s.sum[5], s.sum[6], s.sum[7]);
+  if (lane == 0) found[warp] = rows;
+  __syncthreads();
+  if (threadIdx.x < kSlice) {
+    float x = 0.0f;
+#pragma unroll
+    for (int w = 0; w < kFewWarps; ++w) x += part[w][threadIdx.x];
+    sum[threadIdx.x] = x;
+  }
+  if (threadIdx.x == 0) {
+    int x = 0;
+    for (int w = 0; w < kFewWarps; ++w) x += found[w];
+    all = x;
+  }
+  if (blocks > 1) cluster_sync_writes();
+  else __syncthreads();
+  if (rank == 0 && warp == 0) {
+    float x[8] = {};
+    uint32_t any = 0;
+    for (int r = 0; r < blocks; ++r) {
+      const float4 lo = peer_load(peer_addr(&sum[8 * lane], r)), hi = peer_load(peer_addr(&sum[8 * lane + 4], r));
+      x[0] += lo.x; x[1] += lo.y; x[2] += lo.z; x[3] += lo.w;
+      x[4] += hi.x; x[5] += hi.y; x[6] += hi.z; x[7] += hi.w;
+      any |= peer_load_u32(peer_addr(&all, r));
+    }
+#pragma unroll
+    for (int c = 0; c < 8; ++c) x[c] *= a.scale;
+    if (any != 0 || !a.accumulate) put_slice(a, token, col, x, lane);  // (of no rows: 0, or as it was)
+  }
+  if (blocks > 1) cluster_sync();  // no block ends while another reads from it
+}
+
 template <bool VEC>
 cudaError_t launch_scatter(const ScatterArgs& a, Chain* chain) {
   constexpr int smem = static_cast<int>(sizeof(ScatterShared)) + 128;
@@ -633,20 +723,29 @@ cudaError_t launch_embedding_backward(const EmbeddingLaunch& L) {
   a.grad_f32 = L.grad_f32;
   a.accumulate = L.accumulate;
   a.scale = L.scale;
+  const int64_t slices = (s.width + kSlice - 1) / kSlice;
+  const bool vec = aligned(L.from, 16) && (s.rows == 1 || s.ldy % 8 == 0);
+  a.out_vec = aligned(L.to, 16) && (s.vocab == 1 || s.ldt % (L.grad_f32 ? 4 : 8) == 0);
+  Chain chain{L.stream};
+  // Few tokens: up to two blocks an SM with their slices, four where there are many rows (300 tokens
+  // of 256 columns, 600 rows 5.4 us, by the other kernel 9.1; 600 tokens 9.2 and 8.1, but with
+  // 8192 rows 15 and 23).  Clusters as large as the SMs have room for, and as leave every block 256
+  // rows.
+  if (s.vocab * slices <= (s.rows < kManyRows ? 1 : 2) * kFewItems) {
+    a.blocks = 1;
+    while (a.blocks < kFewCluster && 2 * a.blocks * s.vocab * slices <= kSms && s.rows >= 512 * a.blocks) a.blocks *= 2;
+    return chain.launch(vec ? embedding_few_tokens_kernel<true> : embedding_few_tokens_kernel<false>,
+                        dim3(static_cast<unsigned>(a.blocks * s.vocab * slices)), kFewThreads, 0, a.blocks, a);
+  }
   // Two blocks an SM in all; more where a class would have over half of the rows that a block
   // has room for.
-  const int64_t slices = (s.width + kSlice - 1) / kSlice;
   a.slices = static_cast<int32_t>(slices);
   int64_t classes = 2 * kSms / slices;
   const int64_t least = s.rows / (kMostRows / 2) + 1;
   if (classes < least) classes = least;
   a.classes = static_cast<int32_t>(classes < s.vocab ? classes : s.vocab);
   a.inverse = a.classes > 1 ? ~uint64_t{0} / static_cast<uint64_t>(a.classes) + 1 : 0;
-  const bool vec = aligned(L.from, 16) && aligned(L.to, 16) && (s.rows == 1 || s.ldy % 8 == 0) &&
-                   (s.vocab == 1 || s.ldt % (L.grad_f32 ? 4 : 8) == 0);
-  a.bulk = aligned(L.to, 16) && (s.vocab == 1 || s.ldt * (L.grad_f32 ? 4 : 2) % 16 == 0) &&
-           s.width * (L.grad_f32 ? 4 : 2) % 16 == 0;
-  Chain chain{L.stream};
+  a.bulk = a.out_vec && s.width * (L.grad_f32 ? 4 : 2) % 16 == 0;
   return vec ? launch_scatter<true>(a, &chain) : launch_scatter<false>(a, &chain);
 }
 
