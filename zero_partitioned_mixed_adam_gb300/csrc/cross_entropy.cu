@@ -370,15 +370,15 @@ __global__ void __launch_bounds__(kFinishThreads) loss_alone_kernel(const __grid
   if (a.total != nullptr && last_block(a.words, &last)) total_losses(a, true);
 }
 
-// Row i's exponentials less `ref`, as the product's epilogue makes them; this warp's part of
-// their sum.  Four columns at a time.
-template <bool VEC>
+// Row i's exponentials less `ref`, as the product's epilogue makes them, by WARPS warps; this warp's
+// part of their sum.  Four columns at a time.
+template <bool VEC, int WARPS>
 __device__ __noinline__ float row_again(const LossArgs& a, int64_t i, int32_t t, float ref) {
-  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int warp = threadIdx.x / 32 % WARPS, lane = threadIdx.x % 32;
   const uint16_t* x = a.xc + i * a.ldxc;
   constexpr int U = 4;
   float sum = 0.0f;
-  for (int64_t j = U * warp; j < a.vocab; j += U * kFinishWarps) {
+  for (int64_t j = U * warp; j < a.vocab; j += U * WARPS) {
     const uint16_t* w[U];
     float z[U] = {};
 #pragma unroll
@@ -429,10 +429,13 @@ __device__ __noinline__ float row_again(const LossArgs& a, int64_t i, int32_t t,
 // a row takes its block some 30 us at most.
 constexpr int64_t kFewProducts = int64_t{1} << 28, kFewWeights = int64_t{1} << 21;
 constexpr int64_t kFewValues = int64_t{1} << 25;
+// (Warps instead of blocks: 8192 x 256 -> 100 77 -> 47 us, 4096 x 768 -> 4000 103 -> 90, 700 x 512 -> 4000 50.5
+// and 50.8.)
+constexpr int64_t kWarpRows = 600, kWarpVocab = 4096;
 
 enum Time { kFirst, kAgain, kOnce };
 
-template <Time TIME, bool DZ>
+template <Time TIME, bool DZ, int WARPS>
 __global__ void __launch_bounds__(kFinishThreads) loss_ends_kernel(const __grid_constant__ LossArgs a) {
   static_assert(TIME != kOnce || DZ);
   __shared__ float2 part[kFinishWarps];
@@ -440,7 +443,7 @@ __global__ void __launch_bounds__(kFinishThreads) loss_ends_kernel(const __grid_
   wait_for_predecessor();
   launch_dependents();
   if (TIME == kAgain && __ldcg(&a.words->again) == 0) return;
-  constexpr int kWarps = DZ ? kFinishWarps : 1, kThreads = 32 * kWarps;  // of a row
+  constexpr int kThreads = 32 * WARPS;  // of a row
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, thread = threadIdx.x % kThreads;
   const int64_t n = rows_of(a), filled = filled_rows(a, n);
   if constexpr (!DZ) {  // e of the rows behind the last: zeros, by the whole grid (43 rows of 50257 columns, a warp a row: 5 us)
@@ -449,7 +452,7 @@ __global__ void __launch_bounds__(kFinishThreads) loss_ends_kernel(const __grid_
       for (int64_t j = blockIdx.x * kFinishThreads + threadIdx.x; j < vectors; j += gridDim.x * kFinishThreads)
         reinterpret_cast<uint4*>(a.held + i * a.ldz)[j] = make_uint4(0, 0, 0, 0);
   }
-  constexpr int kRows = kFinishWarps / kWarps;  // of a block at one time
+  constexpr int kRows = kFinishWarps / WARPS;  // of a block at one time
   for (int64_t i = static_cast<int64_t>(blockIdx.x) * kRows + threadIdx.x / kThreads; i < filled;
        i += static_cast<int64_t>(gridDim.x) * kRows) {
     const int32_t t = __ldcg(a.column + i);
@@ -485,12 +488,13 @@ __global__ void __launch_bounds__(kFinishThreads) loss_ends_kernel(const __grid_
         top = fmaxf(top, part[k].y);
       }
     };
-    if constexpr (kWarps > 1) of_block();
+    if constexpr (WARPS > 1) of_block();
     if (TIME != kAgain && t >= 0 && sum > kOneMore && isfinite(top)) {
       if constexpr (TIME == kOnce) {
         ref = top;
-        sum = a.vec ? row_again<true>(a, i, t, ref) : row_again<false>(a, i, t, ref);
-        of_block();
+        sum = a.vec ? row_again<true, WARPS>(a, i, t, ref) : row_again<false, WARPS>(a, i, t, ref);
+        if constexpr (WARPS > 1) of_block();
+        else __syncwarp();  // (the row is written)
       } else if (lane == 0) {
         a.ref[i] = top;
         a.words->again = 1;
@@ -789,20 +793,23 @@ cudaError_t launch_cross_entropy(const CrossEntropyLaunch& L) {
     x.ldo = a.ldz;
     x.rows_now = a.alone ? nullptr : &a.words->rows;
     if (e == cudaSuccess) e = launch_exponents(x);
-    const auto end = [&](auto dz, auto first_time) {
-      constexpr bool DZ = decltype(dz)::value;
+    const bool warps = !make_dz || (a.rows > kWarpRows && s.vocab <= kWarpVocab);  // a warp a row
+    const dim3 grid = blocks_of(warps ? (a.rows + kFinishWarps - 1) / kFinishWarps : a.rows, 8 * kSms);
+    const auto end = [&](auto first_time) {
       constexpr Time TIME = decltype(first_time)::value ? kFirst : kAgain;
-      return chain.launch(loss_ends_kernel<TIME, DZ>, blocks_of(DZ ? a.rows : (a.rows + kFinishWarps - 1) / kFinishWarps, 8 * kSms),
-                          kFinishThreads, 0, 1, a);
+      return chain.launch(!make_dz ? loss_ends_kernel<TIME, false, 1>
+                          : warps  ? loss_ends_kernel<TIME, true, 1>
+                                   : loss_ends_kernel<TIME, true, kFinishWarps>,
+                          grid, kFinishThreads, 0, 1, a);
     };
-    using std::false_type, std::true_type;
     if (e == cudaSuccess && a.alone)
-      e = chain.launch(loss_ends_kernel<kOnce, true>, blocks_of(a.rows, 4 * kSms), kFinishThreads, 0, 1, a);
+      e = chain.launch(warps ? loss_ends_kernel<kOnce, true, 1> : loss_ends_kernel<kOnce, true, kFinishWarps>, grid,
+                       kFinishThreads, 0, 1, a);
     if (!a.alone) {
-      if (e == cudaSuccess) e = make_dz ? end(true_type{}, true_type{}) : end(false_type{}, true_type{});
+      if (e == cudaSuccess) e = end(std::true_type{});
       x.of.only_if = &a.words->again;
       if (e == cudaSuccess) e = launch_exponents(x);
-      if (e == cudaSuccess) e = make_dz ? end(true_type{}, false_type{}) : end(false_type{}, false_type{});
+      if (e == cudaSuccess) e = end(std::false_type{});
     }
     if (e != cudaSuccess) return e;
     LinearBackwardLaunch b{};
