@@ -464,8 +464,13 @@ __device__ __forceinline__ void write_zeros(const ScatterArgs& a, const ScatterP
       while (left != 0) {
         const int u = __ffs(left) - 1;
         left &= left - 1;
-        uint16_t* o = reinterpret_cast<uint16_t*>(__shfl_sync(0xffffffffu, reinterpret_cast<uintptr_t>(row), u));
-        for (int64_t j = lane; j < bytes / 2; j += 32) o[j] = 0;
+        // up to a 16-byte boundary, vectors, and what is left
+        char* o = reinterpret_cast<char*>(__shfl_sync(0xffffffffu, reinterpret_cast<uintptr_t>(row), u));
+        const int64_t up = static_cast<int64_t>(-reinterpret_cast<uintptr_t>(o) & 15u);
+        const int64_t head = up < bytes ? up : bytes, body = (bytes - head) / 16 * 16;
+        if (2 * lane < head) *reinterpret_cast<uint16_t*>(o + 2 * lane) = 0;
+        for (int64_t j = 16 * lane; j < body; j += 512) *reinterpret_cast<uint4*>(o + head + j) = make_uint4(0, 0, 0, 0);
+        if (2 * lane < bytes - head - body) *reinterpret_cast<uint16_t*>(o + head + body + 2 * lane) = 0;
       }
     }
   }
