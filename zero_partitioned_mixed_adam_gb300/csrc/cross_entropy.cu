@@ -16,7 +16,7 @@
 // token that is the target of many rows it averages out (these two cases' dw is 1.05 times as
 // far from the exact one as its own rounding puts it), for those of one row it does not (1.4
 // times).  So where the values stay in L2, up to 2^25 of them, that pass is made, and dz is
-// rounded to bf16 there (1.0 to 1.3 times).
+// rounded to bf16 there (1.0 to 1.4 times, of 3 columns up to 1.7).
 // A row whose S' passes 2^64 (the target 44 below the largest logit) leaves the range where
 // products with 1 / S' lose nothing: its reference becomes the largest logit, which the first
 // product found, and product and ends run once more; the launches that do so end at once
@@ -431,7 +431,7 @@ constexpr int64_t kFewProducts = int64_t{1} << 28, kFewWeights = int64_t{1} << 2
 constexpr int64_t kFewValues = int64_t{1} << 25;
 // (Warps instead of blocks: 8192 x 256 -> 100 77 -> 47 us, 4096 x 768 -> 4000 103 -> 90, 700 x 512 -> 4000 50.5
 // and 50.8.)
-constexpr int64_t kWarpRows = 600, kWarpVocab = 4096;
+constexpr int64_t kWarpRows = 600, kWarpVocab = 4096, kFewColumns = 64;
 
 enum Time { kFirst, kAgain, kOnce };
 
@@ -515,6 +515,30 @@ __global__ void __launch_bounds__(kFinishThreads) loss_ends_kernel(const __grid_
       uint4* e = reinterpret_cast<uint4*>(a.held + i * a.ldz);
       constexpr int U = 4;
       const uint32_t vectors = static_cast<uint32_t>((a.vocab + 7) / 8);
+      // Where few columns share a row, e's roundings do not average out: the others' factor is
+      // what makes their sum, as rounded, S' again (dw of 100 rows, 2 columns: 1.4 times as far
+      // from the exact one as its own rounding puts it, without this 1.9; 8 columns 1.25, 1.3; 8192 x
+      // 64 -> 3 42 us instead of 40, but 4096 x 768 -> 4000 96 instead of 90, for nothing).
+      float others = f;
+      if (a.vocab <= kFewColumns) {
+        float held = 0.0f;
+        for (uint32_t j = thread; t >= 0 && j < vectors; j += kThreads) {
+          float x[8];
+          bf16x8(__ldcg(e + j), x);
+#pragma unroll
+          for (int c = 0; c < 8; ++c) held += 8 * j + c < a.vocab ? x[c] : 0.0f;
+        }
+        held = warp_sum(held);
+        if constexpr (WARPS > 1) {
+          __syncthreads();
+          if (lane == 0) part[warp].x = held;
+          __syncthreads();
+          held = 0.0f;
+#pragma unroll
+          for (int k = 0; k < kFinishWarps; ++k) held += part[k].x;
+        }
+        if (held > 0.0f) others = f * (sum / held);
+      }
       for (uint32_t j0 = thread; j0 < vectors; j0 += U * kThreads) {
         uint4 v[U];
 #pragma unroll
@@ -527,7 +551,7 @@ __global__ void __launch_bounds__(kFinishThreads) loss_ends_kernel(const __grid_
           float x[8] = {};
           if (t != -1) bf16x8(v[u], x);
 #pragma unroll
-          for (int c = 0; c < 8; ++c) x[c] = t == -1 ? 0.0f : f * (at == c ? -sum : x[c]);
+          for (int c = 0; c < 8; ++c) x[c] = t == -1 ? 0.0f : at == c ? -(f * sum) : others * x[c];
           e[j] = to_bf16x8(x);
         }
       }
