@@ -163,6 +163,17 @@ def test_far_targets(rows, k, v):
     check((x * 4.0), w, t)                       # most rows
 
 
+@pytest.mark.parametrize("rows,k,v", [(5, 64, 7), (700, 64, 40), (1300, 75, 3), (601, 16, 64), (601, 16, 65)])
+def test_far_targets_of_few_columns(rows, k, v):
+    """Rows of few columns, a warp's or a block's, most of them with another reference; some ignored."""
+    x, w = matrix(rows, k, 1.0, 1), matrix(v, k, 1.0, 2)
+    t = targets_of(rows, v, 3, 0.2)
+    t[0] = 0
+    check(x, w, t)
+    losses, *_ = check(x * 16.0, w, t)
+    assert (losses > 50).any()
+
+
 @pytest.mark.parametrize("rows,k,v", [(1, 64, 50257), (2, 2048, 4099), (7, 775, 9001), (130, 520, 5003)])
 def test_few_rows_of_many_columns(rows, k, v):
     """More weights than one block reads again for a row: another reference is a second run of the
