@@ -163,6 +163,22 @@ def test_far_targets(rows, k, v):
     check((x * 4.0), w, t)                       # most rows
 
 
+@pytest.mark.parametrize("v", [2, 515, 50257, 131072])
+def test_targets_below_a_plateau(v):
+    """All other logits alike and 30 to 100 above the target's: the exponentials' sum less the target's
+    passes fp32's range from a loss of 88.7 on, whatever its largest term is."""
+    depth = torch.arange(30.0, 100.5, 0.5, device="cuda")
+    x, w = blank(len(depth), 8), blank(v, 8)
+    x.zero_(), w.zero_()
+    x[:, 0], w[:, 0] = depth.to(BF), 1.0
+    at = min(7, v - 1)
+    w[at] = 0.0
+    t = torch.full((len(depth),), at, device="cuda")
+    losses, *_ = check(x, w, t)
+    assert losses.max() > 99
+    check(x, w, t, scale=torch.linspace(-1.0, 2.0, len(depth), device="cuda"), dtype=F32)
+
+
 @pytest.mark.parametrize("rows,k,v", [(5, 64, 7), (700, 64, 40), (1300, 75, 3), (601, 16, 64), (601, 16, 65)])
 def test_far_targets_of_few_columns(rows, k, v):
     """Rows of few columns, a warp's or a block's, most of them with another reference; some ignored."""

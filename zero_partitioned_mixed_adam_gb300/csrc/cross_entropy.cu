@@ -360,8 +360,9 @@ __global__ void __launch_bounds__(kFinishThreads) loss_alone_kernel(const __grid
     float most = fmaxf(top, zt);
 #pragma unroll
     for (int k = 16; k > 0; k /= 2) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, k));
-    // less the target's logit, where that leaves fp32's range alone
-    const bool own = most - zt < 80.0f;
+    // less the target's logit, where that leaves fp32's range alone: 2^31 columns of e^44 come to
+    // 3e28 (of e^80, 1e5 columns already pass 3.4e38)
+    const bool own = most - zt < 44.0f;
     const float ref = own ? zt : most;
     if (sum != 0.0f) sum *= expf(top - ref);
     sum = warp_sum(sum);
