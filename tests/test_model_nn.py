@@ -201,3 +201,24 @@ def test_linear_cross_entropy(lead, scaled):
             nn.linear_cross_entropy(*bad)
     with pytest.raises(ValueError):
         nn.linear_cross_entropy(x, w, t, scale=torch.ones(5))
+
+
+@pytest.mark.parametrize("mode", [torch.no_grad, torch.inference_mode])
+def test_linear_cross_entropy_without_gradients(mode, monkeypatch):
+    """Where nothing is recorded the library is asked for the loss alone, whatever requires gradients."""
+    asked = []
+
+    def recorded(*args, dx=None, dw=None, **kw):
+        asked.append((dx is not None, dw is not None))
+        loss(*args, dx=dx, dw=dw, **kw)
+
+    monkeypatch.setattr(nn, "zero_linear_cross_entropy", torch.no_grad()(recorded))
+    x, w, t = leaf(6, 8, seed=1), leaf(9, 8, seed=2), torch.tensor([0, 8, 3, -100, 3, 1])
+    with mode():
+        out = nn.linear_cross_entropy(x, w, t)
+    assert asked == [(False, False)] and not out.requires_grad
+    assert torch.equal(nn.linear_cross_entropy(x, w, t).detach(), out)
+    nn.linear_cross_entropy(x, w.detach(), t)
+    nn.linear_cross_entropy(x.detach(), w, t)
+    nn.linear_cross_entropy(x.detach(), w.detach(), t)
+    assert asked[1:] == [(True, True), (True, False), (False, True), (False, False)]

@@ -182,12 +182,14 @@ def block_norm(r, weight=None, bias=None, *, h=None, kind="rms", post=None, post
 
 class _LinearCrossEntropy(torch.autograd.Function):
     @staticmethod
-    def forward(ctx, x, weight, targets, ignore_index, scale):
+    def forward(ctx, x, weight, targets, ignore_index, scale, recorded):
         width = weight.shape[1]
         rows, w = _rows(x, width), _rows(weight, width)
         total = torch.empty(1, dtype=torch.float32, device=x.device)
-        dx = torch.empty(rows.shape, dtype=rows.dtype, device=x.device) if ctx.needs_input_grad[0] else None
-        dw = torch.empty(w.shape, dtype=w.dtype, device=x.device) if ctx.needs_input_grad[1] else None
+        # (needs_input_grad says what requires gradients, whether or not anything is recorded)
+        need_x, need_w = (recorded and need for need in ctx.needs_input_grad[:2])
+        dx = torch.empty(rows.shape, dtype=rows.dtype, device=x.device) if need_x else None
+        dw = torch.empty(w.shape, dtype=w.dtype, device=x.device) if need_w else None
         zero_linear_cross_entropy(rows, w, targets.reshape(-1).contiguous(), None, total, dx=dx, dw=dw,
                                   ignore_index=ignore_index,
                                   scale=None if scale is None else scale.reshape(-1).contiguous())
@@ -200,7 +202,7 @@ class _LinearCrossEntropy(torch.autograd.Function):
     def backward(ctx, grad):
         dx, dw = ctx.saved_tensors
         return (None if dx is None else (dx * grad).view(ctx.shape), None if dw is None else dw * grad, None, None,
-                None)
+                None, None)
 
 
 def linear_cross_entropy(x, weight, targets, ignore_index: int = -100, scale=None):
@@ -208,10 +210,12 @@ def linear_cross_entropy(x, weight, targets, ignore_index: int = -100, scale=Non
     rows whose target is not ignore_index, or with scale (fp32, of targets' shape) the sum of
     scale times each row's.  x [..., width], weight [vocab, width], bf16; targets of x's leading
     shape.  The logits are not kept: x's and weight's gradients are computed in the forward pass,
-    where they are wanted, and only multiplied by the loss's own in the backward pass."""
+    where they are wanted (not under torch.no_grad), and only multiplied by the loss's own in the
+    backward pass, which rounds them to bf16 once more unless that is a power of two."""
     if weight.dim() != 2 or x.shape[-1] != weight.shape[1] or targets.shape != x.shape[:-1]:
         raise ValueError(f"x {tuple(x.shape)}, weight {tuple(weight.shape)} and targets {tuple(targets.shape)} "
                          "do not match")
     if scale is not None and (scale.shape != targets.shape or scale.requires_grad):
         raise ValueError("scale is of targets' shape, and has no gradient")
-    return _LinearCrossEntropy.apply(x, weight, targets, ignore_index, scale)
+    # asked here: within an autograd function nothing is ever recorded
+    return _LinearCrossEntropy.apply(x, weight, targets, ignore_index, scale, torch.is_grad_enabled())
