@@ -222,3 +222,15 @@ def test_linear_cross_entropy_without_gradients(mode, monkeypatch):
     nn.linear_cross_entropy(x.detach(), w, t)
     nn.linear_cross_entropy(x.detach(), w.detach(), t)
     assert asked[1:] == [(True, True), (True, False), (False, True), (False, False)]
+
+
+def test_linear_cross_entropy_backward_twice():
+    """Each backward pass multiplies what the forward pass computed by its own factor."""
+    x, w, t = leaf(6, 8, seed=1), leaf(9, 8, seed=2), torch.tensor([0, 8, 3, -100, 3, 1])
+    ref = o.cross_entropy(x.detach(), w.detach(), t)
+    out = nn.linear_cross_entropy(x, w, t)
+    for factor in (3.0, 1.0, -0.25):
+        x.grad = w.grad = None
+        (factor * out).backward(retain_graph=True)
+        near(x.grad, factor * ref[2])
+        near(w.grad, factor * ref[3])
