@@ -3,6 +3,7 @@
 #include "chain.cuh"
 #include "internal.h"
 #include "linear_epilogue.cuh"
+#include "row_reads.hpp"
 #include "train_ops.cuh"
 #include "umma.cuh"
 
@@ -122,6 +123,7 @@ struct ScatterArgs {
   int32_t ids_i32, grad_f32, accumulate;
   int32_t classes, slices;
   int32_t blocks;     // that share a token's rows (few tokens)
+  WholeRows whole;    // rows of dy
   uint64_t inverse;   // 2^64 / classes, rounded up: its high product with an id is the quotient
   int32_t out_vec;    // rows of dtable are on 16 bytes
   int32_t bulk;       // a row of dtable is whole 16-byte vectors: zeros go by the TMA engine
@@ -169,23 +171,75 @@ __device__ __forceinline__ uint4 from_column(uint4 v, uint4 edge, int s, int lan
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
+// 16 bytes that may lie in part outside dy, or zeros.
+__device__ __forceinline__ uint4 vector_of(const Extents& in, bool has, uintptr_t p) {
+  if (!has) return make_uint4(0, 0, 0, 0);
+  if (in.whole(p)) return __ldg(reinterpret_cast<const uint4*>(p));
+  uint64_t w[2];
+  read_cut(p, in, w, [](uintptr_t q) { return __ldg(reinterpret_cast<const uint16_t*>(q)); });
+  return make_uint4(static_cast<uint32_t>(w[0]), static_cast<uint32_t>(w[0] >> 32), static_cast<uint32_t>(w[1]),
+                    static_cast<uint32_t>(w[1] >> 32));
+}
+
+// A lane's sums and 8 columns of a row whose vectors may lie in part outside dy.  (Not inlined: it
+// would cost the loop beside it registers.)
+struct Run {
+  float x[8];
+};
+__device__ __noinline__ Run careful_row(const ScatterArgs& a, const uint16_t* row, int64_t n, int lane, Run run) {
+  const uintptr_t begin = reinterpret_cast<uintptr_t>(a.dy), at = reinterpret_cast<uintptr_t>(row);
+  const Extents in{begin, begin + 2 * ((a.rows - 1) * a.ldy + a.width)};
+  const LaneReads r(at, n, lane);
+  const uint4 low = vector_of(in, r.has_first, r.first), next = vector_of(in, r.has_next, r.next);
+  float x[8];
+  bf16x8(from_column(low, next, LaneReads::shift(at), lane), x);
+#pragma unroll
+  for (int c = 0; c < 8; ++c) run.x[c] += x[c];
+  return run;
+}
+
+// How rows of dy lie.
+enum Lie {
+  kWhole,     // on 16 bytes, and whole vectors of them
+  kAligned,   // on 16 bytes
+  kAnywhere,
+};
+
 // The sum of a run of rows: 8 columns a lane, in the order of the rows, eight rows' loads
-// under way at a time.  Rows that are not on 16 bytes (VEC: all are) come in aligned vectors too,
-// shifted between lanes.  A chain ends after 64 rows, so that its error does not grow with
-// a common token's count.
-template <bool VEC>
+// under way at a time.  Rows that are not on 16 bytes come in aligned vectors too, shifted between
+// lanes.  A lane's vector may end past the row, or begin before it: what is there goes into
+// columns that no one writes.  Vectors that are not whole in dy's memory, of the first and last
+// rows, are read element by element: a group of rows with one of these goes row by row (8192 x
+// 2047 of 50257 83 us; with a look at each vector 99).  A chain ends after 64 rows, so that its
+// error does not grow with a common token's count.
+template <Lie LIE>
 struct SliceSum {
+  static constexpr bool VEC = LIE != kAnywhere, CUT = LIE != kWhole;
   float run[8] = {}, sum[8] = {};
   int chain = 0;
 
   // Rows rows[0], ..., rows[U - 1], those whose bit of `here` is set; after(u) follows the u-th.
-  // A lane's vector may end past the row: what is there goes into columns that no one writes.
+  // careful (alike for the warp): some of them may not be whole.
   template <int U, typename After>
   __device__ __forceinline__ void walk(const ScatterArgs& a, const int32_t* rows, uint32_t here, int64_t col,
-                                       int lane, After after) {
-    uint4 v[U], edge[VEC ? 1 : U];
+                                       int lane, bool careful, After after) {
     const uint16_t* const first = a.dy + col;
     const int64_t n = a.width - col;  // (lanes from there on have nothing)
+    if (CUT && careful) {
+#pragma unroll 1
+      for (int u = 0; u < U; ++u) {
+        if ((here >> u & 1) == 0) continue;
+        Run now;
+#pragma unroll
+        for (int c = 0; c < 8; ++c) now.x[c] = run[c];
+        now = careful_row(a, first + rows[u] * a.ldy, n, lane, now);
+#pragma unroll
+        for (int c = 0; c < 8; ++c) run[c] = now.x[c];
+        after(u);
+      }
+      return;
+    }
+    uint4 v[U], edge[VEC ? 1 : U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const bool take = here >> u & 1;
@@ -193,8 +247,8 @@ struct SliceSum {
       if constexpr (VEC) {
         v[u] = load16_if(take && 8 * lane < n, from + 8 * lane);
       } else {
-        // the aligned vector that a lane's first column lies in; the next one is the next lane's
-        const int s = static_cast<int>(reinterpret_cast<uintptr_t>(from) % 16 / 2);
+        // (as LaneReads has them)
+        const int s = LaneReads::shift(reinterpret_cast<uintptr_t>(from));
         v[u] = load16_if(take && 8 * lane - s < n, from + 8 * lane - s);
         edge[u] = load16_if(take && lane == 31 && s > 0 && 256 - s < n, from + 256 - s);
       }
@@ -203,7 +257,7 @@ struct SliceSum {
     for (int u = 0; u < U; ++u) {
       if ((here >> u & 1) == 0) continue;
       if constexpr (!VEC)
-        v[u] = from_column(v[u], edge[u], static_cast<int>(reinterpret_cast<uintptr_t>(first + rows[u] * a.ldy) % 16 / 2), lane);
+        v[u] = from_column(v[u], edge[u], LaneReads::shift(reinterpret_cast<uintptr_t>(first + rows[u] * a.ldy)), lane);
       float x[8];
       bf16x8(v[u], x);
 #pragma unroll
@@ -211,13 +265,16 @@ struct SliceSum {
       after(u);
     }
   }
+  // Rows in ascending order.  cut: there may be some among them that are not whole.
   __device__ __forceinline__ void add(const ScatterArgs& a, const int32_t* rows, int n, int64_t col,
-                                      int lane) {
+                                      int lane, bool cut) {
     constexpr int U = 8;
 #pragma unroll 1
     for (int k = 0; k < n; k += U) {
       const uint32_t here = n - k >= U ? (1u << U) - 1u : (1u << (n - k)) - 1u;
-      walk<U>(a, rows + k, here, col, lane, [](int) {});
+      const bool careful =
+          CUT && cut && (rows[k] < a.whole.first || rows[n - k >= U ? k + U - 1 : n - 1] >= a.whole.end);
+      walk<U>(a, rows + k, here, col, lane, careful, [](int) {});
       if ((chain += U) >= 64) join();
     }
   }
@@ -295,8 +352,8 @@ struct ScatterPlace {
 };
 
 // The sum of a token's rows, scaled and written.
-template <bool VEC>
-__device__ __forceinline__ void finish_token(const ScatterArgs& a, const ScatterPlace& p, SliceSum<VEC>& s,
+template <Lie LIE>
+__device__ __forceinline__ void finish_token(const ScatterArgs& a, const ScatterPlace& p, SliceSum<LIE>& s,
                                              int t, int lane) {
   s.join();
 #pragma unroll
@@ -305,9 +362,9 @@ __device__ __forceinline__ void finish_token(const ScatterArgs& a, const Scatter
 }
 
 // n rows by the whole block: a run of them a warp, the warps' sums added in their order.
-template <bool VEC>
+template <Lie LIE>
 __device__ __forceinline__ void finish_token_together(const ScatterArgs& a, const ScatterPlace& p,
-                                                      ScatterShared& sh, SliceSum<VEC>& s, int t) {
+                                                      ScatterShared& sh, SliceSum<LIE>& s, int t) {
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   s.join();
 #pragma unroll
@@ -321,12 +378,12 @@ __device__ __forceinline__ void finish_token_together(const ScatterArgs& a, cons
   }
   sum_sync();
 }
-template <bool VEC>
-__device__ __forceinline__ void add_share(const ScatterArgs& a, const ScatterPlace& p, SliceSum<VEC>& s,
+template <Lie LIE>
+__device__ __forceinline__ void add_share(const ScatterArgs& a, const ScatterPlace& p, SliceSum<LIE>& s,
                                           const int32_t* rows, int n) {
   const int warp = threadIdx.x / 32, per = (n + kSumWarps - 1) / kSumWarps;
   const int first = warp * per < n ? warp * per : n, end = first + per < n ? first + per : n;
-  s.add(a, rows + first, end - first, p.col, threadIdx.x % 32);
+  s.add(a, rows + first, end - first, p.col, threadIdx.x % 32, true);
 }
 
 // Rows [i0, i1) of tokens [t0, t1) in their order, each warp's own run of rows in its own
@@ -399,7 +456,7 @@ __device__ __forceinline__ void sort_rows(ScatterShared& sh, int start) {
 // other has taken, of them the tokens whose first row is there, and has eight rows' loads
 // under way at a time whatever tokens they are of.  Tokens of more than kOneWarp rows are
 // left out.  (Which warp sums a token does not change its sum.)
-template <bool VEC>
+template <Lie LIE>
 __device__ __forceinline__ void sum_tokens(const ScatterArgs& a, const ScatterPlace& p, ScatterShared& sh, int start,
                                            int n, int t_first, int lane) {
   constexpr int U = 8, kTaken = 16;
@@ -416,7 +473,7 @@ __device__ __forceinline__ void sum_tokens(const ScatterArgs& a, const ScatterPl
     share = __shfl_sync(0xffffffffu, share, 0) * kTaken;
     if (share >= n) return;
     const int end = next_first(share + kTaken);
-    SliceSum<VEC> s;
+    SliceSum<LIE> s;
     for (int k = next_first(share); k < end;) {
       const int t = sh.sorted_token[k];
       if (end_of(t) - begin_of(t) > kOneWarp) {
@@ -433,10 +490,12 @@ __device__ __forceinline__ void sum_tokens(const ScatterArgs& a, const ScatterPl
       const bool counts = lane < m && end_of(token) - begin_of(token) <= kOneWarp;
       const uint32_t here = __ballot_sync(0xffffffffu, counts);
       const uint32_t last = __ballot_sync(0xffffffffu, counts && token != after);
-      s.template walk<U>(a, sh.sorted + k, here, p.col, lane, [&](int u) {
+      const bool careful =
+          SliceSum<LIE>::CUT && __any_sync(0xffffffffu, counts && !a.whole.has(sh.sorted[k + lane]));
+      s.template walk<U>(a, sh.sorted + k, here, p.col, lane, careful, [&](int u) {
         if ((last >> u & 1) == 0) return;
         finish_token(a, p, s, sh.sorted_token[k + u], lane);
-        s = SliceSum<VEC>();
+        s = SliceSum<LIE>();
       });
       k += m;
     }
@@ -476,7 +535,7 @@ __device__ __forceinline__ void write_zeros(const ScatterArgs& a, const ScatterP
   }
 }
 
-template <bool VEC>
+template <Lie LIE>
 __global__ void __launch_bounds__(kScatterThreads, 2)
     embedding_scatter_kernel(const __grid_constant__ ScatterArgs a) {
   extern __shared__ uint8_t raw[];
@@ -561,11 +620,11 @@ __global__ void __launch_bounds__(kScatterThreads, 2)
       if (threadIdx.x == 0) sh.commons = sh.next = 0;
       sum_sync();
       if (!room && count > kEachRows) {
-        SliceSum<VEC> s;
+        SliceSum<LIE> s;
         for (int64_t i = 0; i < a.rows; i += kMostRows) {
           const int64_t end = i + kMostRows < a.rows ? i + kMostRows : a.rows;
           list_rows(a, p, sh, i, end, t0, t1, false);  // (a warp looks at kEachRows rows)
-          s.add(a, sh.row + warp * kEachRows, sh.found[warp], p.col, lane);
+          s.add(a, sh.row + warp * kEachRows, sh.found[warp], p.col, lane, true);
           sum_sync();
         }
         finish_token_together(a, p, sh, s, t0);
@@ -576,12 +635,12 @@ __global__ void __launch_bounds__(kScatterThreads, 2)
         for (int t = t0 + static_cast<int>(threadIdx.x); t < t1; t += kSumThreads)
           if (sh.offset[t] - begin_of(t) > kOneWarp)
             sh.common[atomicAdd(&sh.commons, 1)] = static_cast<uint16_t>(t);
-        sum_tokens<VEC>(a, p, sh, start, count, t0, lane);
+        sum_tokens<LIE>(a, p, sh, start, count, t0, lane);
         sum_sync();
         // tokens of many rows, by all warps (in any order: each is written by itself)
         for (int k = 0; k < sh.commons; ++k) {
           const int t = sh.common[k], first = begin_of(t);
-          SliceSum<VEC> s;
+          SliceSum<LIE> s;
           add_share(a, p, s, sh.sorted + first - start, sh.offset[t] - first);
           finish_token_together(a, p, sh, s, t);
         }
@@ -602,7 +661,7 @@ constexpr int kFewWarps = 16, kFewThreads = 32 * kFewWarps, kFewCluster = 8;
 constexpr int kFewItems = 2 * kSms, kManyRows = 4096;
 constexpr int kFewListed = 64, kFewAsked = 4;  // rows that are added up; loads of 32 ids under way
 
-template <bool VEC>
+template <Lie LIE>
 __global__ void __launch_bounds__(kFewThreads, 1)
     embedding_few_tokens_kernel(const __grid_constant__ ScatterArgs a) {
   __shared__ alignas(16) float part[kFewWarps][kSlice];
@@ -616,7 +675,8 @@ __global__ void __launch_bounds__(kFewThreads, 1)
   const int64_t token = item % a.vocab, col = static_cast<int64_t>(item / static_cast<int>(a.vocab)) * kSlice;
   const int64_t run = rank * kFewWarps + warp, runs = static_cast<int64_t>(blocks) * kFewWarps;
   const int64_t from = a.rows * run / runs, to = a.rows * (run + 1) / runs;
-  SliceSum<VEC> s;
+  const bool cut = from < a.whole.first || to > a.whole.end;
+  SliceSum<LIE> s;
   int n = 0, rows = 0;
   for (int64_t i = from; token != a.padding && i < to; i += 32 * kFewAsked) {
     int64_t id[kFewAsked];
@@ -635,7 +695,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
     }
     if (n < kFewListed && i + 32 * kFewAsked < to) continue;
     __syncwarp();
-    s.add(a, list[warp], n, col, lane);
+    s.add(a, list[warp], n, col, lane, cut);
     __syncwarp();
     rows += n;
     n = 0;
@@ -674,11 +734,11 @@ __global__ void __launch_bounds__(kFewThreads, 1)
   if (blocks > 1) cluster_sync();  // no block ends while another reads from it
 }
 
-template <bool VEC>
+template <Lie LIE>
 cudaError_t launch_scatter(const ScatterArgs& a, Chain* chain) {
   constexpr int smem = static_cast<int>(sizeof(ScatterShared)) + 128;
   static_assert(smem <= 113 * 1024, "two blocks an SM");
-  const auto kernel = embedding_scatter_kernel<VEC>;
+  const auto kernel = embedding_scatter_kernel<LIE>;
   const cudaError_t e = allow_shared(reinterpret_cast<const void*>(kernel), smem);
   if (e != cudaSuccess) return e;
   const int64_t blocks = int64_t{a.classes} * a.slices;
@@ -714,7 +774,10 @@ cudaError_t launch_embedding_forward(const EmbeddingLaunch& L) {
 cudaError_t launch_embedding_backward(const EmbeddingLaunch& L) {
   (void)cudaGetLastError();
   const zero_embedding_t& s = L.s;
+  const bool vec = aligned(L.from, 16) && (s.rows == 1 || s.ldy % 8 == 0);
   ScatterArgs a{};
+  a.whole = WholeRows(s.rows, s.width, s.ldy, vec);
+  const Lie lie = !vec ? kAnywhere : a.whole.end < s.rows ? kAligned : kWhole;
   a.dy = L.from;
   a.ids = L.ids;
   a.dtable = L.to;
@@ -729,7 +792,6 @@ cudaError_t launch_embedding_backward(const EmbeddingLaunch& L) {
   a.accumulate = L.accumulate;
   a.scale = L.scale;
   const int64_t slices = (s.width + kSlice - 1) / kSlice;
-  const bool vec = aligned(L.from, 16) && (s.rows == 1 || s.ldy % 8 == 0);
   a.out_vec = aligned(L.to, 16) && (s.vocab == 1 || s.ldt % (L.grad_f32 ? 4 : 8) == 0);
   Chain chain{L.stream};
   // Few tokens: up to two blocks an SM with their slices, four where there are many rows (300 tokens
@@ -739,7 +801,9 @@ cudaError_t launch_embedding_backward(const EmbeddingLaunch& L) {
   if (s.vocab * slices <= (s.rows < kManyRows ? 1 : 2) * kFewItems) {
     a.blocks = 1;
     while (a.blocks < kFewCluster && 2 * a.blocks * s.vocab * slices <= kSms && s.rows >= 512 * a.blocks) a.blocks *= 2;
-    return chain.launch(vec ? embedding_few_tokens_kernel<true> : embedding_few_tokens_kernel<false>,
+    return chain.launch(lie == kWhole     ? embedding_few_tokens_kernel<kWhole>
+                        : lie == kAligned ? embedding_few_tokens_kernel<kAligned>
+                                          : embedding_few_tokens_kernel<kAnywhere>,
                         dim3(static_cast<unsigned>(a.blocks * s.vocab * slices)), kFewThreads, 0, a.blocks, a);
   }
   // Two blocks an SM in all; more where a class would have over half of the rows that a block
@@ -751,7 +815,9 @@ cudaError_t launch_embedding_backward(const EmbeddingLaunch& L) {
   a.classes = static_cast<int32_t>(classes < s.vocab ? classes : s.vocab);
   a.inverse = a.classes > 1 ? ~uint64_t{0} / static_cast<uint64_t>(a.classes) + 1 : 0;
   a.bulk = a.out_vec && s.width * (L.grad_f32 ? 4 : 2) % 16 == 0;
-  return vec ? launch_scatter<true>(a, &chain) : launch_scatter<false>(a, &chain);
+  return lie == kWhole     ? launch_scatter<kWhole>(a, &chain)
+         : lie == kAligned ? launch_scatter<kAligned>(a, &chain)
+                           : launch_scatter<kAnywhere>(a, &chain);
 }
 
 }  // namespace zeroadam
