@@ -245,3 +245,32 @@ def test_another_device_and_stream(monkeypatch):
     for stream, tensors in ((None, (Tensor(0), Tensor(1))), (None, (Tensor(-1),)), (Stream(), (Tensor(0),))):
         with pytest.raises(ValueError):
             model_ops._here(stream, tensors)
+
+
+def test_gates_whose_rows_overlap_are_refused(monkeypatch):
+    """A matrix gate or dgate of expanded or overlapping rows: as if its rows lay one after the
+    other, it would be read and written past its end."""
+    called = []
+
+    class Library:
+        def __getattr__(self, name):
+            return lambda *args: called.append(args[0]._obj) or 0
+
+    monkeypatch.setattr(model_ops, "_here", lambda *args: None)
+    monkeypatch.setattr(model_ops, "_stream_handle", lambda stream: None)
+    monkeypatch.setattr(model_ops, "_lib", Library())
+    m, workspace = bf(4, 8), torch.empty(1, dtype=torch.uint8)
+    expanded, overlapping = bf(8).expand(4, 8), bf(32).as_strided((4, 8), (5, 1))
+    for gate in (expanded, overlapping):
+        with pytest.raises(ValueError, match="gate"):
+            za.zero_block_norm_forward(m, m, h=m, gate=gate)
+        with pytest.raises(ValueError, match="gate"):
+            za.zero_block_norm_backward(m, m, h=m, gate=gate, dgate=m, workspace=workspace)
+        with pytest.raises(ValueError, match="dgate"):
+            za.zero_block_norm_backward(m, m, h=m, gate=m, dgate=gate, workspace=workspace)
+    assert not called
+    # one row has any pitch; columns of a wider matrix are read where they lie
+    za.zero_block_norm_forward(m[:1], m[:1], h=m[:1], gate=expanded[:1])
+    za.zero_block_norm_forward(m, m, h=m, gate=bf(4, 24)[:, 8:16])
+    za.zero_block_norm_backward(m, m, h=m, gate=m, dgate=bf(4, 24)[:, 8:16], workspace=workspace)
+    assert [s.ldg for s in called] == [8, 24, 8] and called[2].lddg == 24

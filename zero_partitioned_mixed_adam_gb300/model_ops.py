@@ -91,6 +91,14 @@ def _rows(name, t, shape):
     return pitch if rows > 1 else max(cols, pitch)
 
 
+def _gate_rows(name, t, shape):
+    """_rows, of a matrix that a pitch of 0 would make a vector."""
+    pitch = _rows(name, t, shape)
+    if pitch < shape[1]:
+        raise ValueError(f"{name}: its rows overlap (pitch {pitch}, {shape[1]} columns)")
+    return pitch
+
+
 def _floats(name, t, n):
     """_vector for fp32."""
     if t.shape != (n,) or t.dtype is not torch.float32 or not t.is_contiguous():
@@ -244,7 +252,7 @@ def _block_norm(shape, post, kind, alpha, eps, h, gate, w1, b1, w):
         if gate.dim() == 1:
             _columns("gate", gate, one)
         else:
-            s.ldg = max(_rows("gate", gate, shape), width)
+            s.ldg = _gate_rows("gate", gate, shape)
     if w1 is not None:
         _columns("post_weight", w1, one)
     if b1 is not None:
@@ -312,7 +320,7 @@ def zero_block_norm_backward(dy, s, *, ds=None, h=None, post: int = ZERO_NORM_NO
         if gate is None or dgate.dim() != gate.dim():
             raise ValueError("dgate is of gate's shape")
         if gate.dim() == 2:
-            z.lddg = max(_rows("dgate", dgate, shape), shape[1])
+            z.lddg = _gate_rows("dgate", dgate, shape)
             vectors = vectors[:4]
     kind_of = None
     for t in vectors:
