@@ -348,3 +348,26 @@ def test_gradients_against_differences():
             slope = (moved[0] - moved[1]) / (2 * step)
             # s was rounded to bf16 before the backward pass, and the result after it
             assert (grad[i, j].to(F64) - slope).abs() <= 2.0 ** -5 * grad[i].to(F64).abs().max()
+
+
+@pytest.mark.parametrize("post,kind", [("none", "rms"), ("rms", "rms"), ("layer", "layer")])
+def test_rows_of_clusters_do_not_meet(post, kind):
+    """Rows that several blocks share: a row of NaN leaves the others' outputs alone, and the same bits
+    come every time."""
+    m, d = 600, 8208
+    b = Block(m, d, post, "vector", kind)
+    dy = matrix(m, d, 1.0, 11)
+
+    def run():
+        s, y, dr, dh = (blank(m, d) for _ in range(4))
+        za.zero_block_norm_forward(b.r, y, s=s, bias=b.b, **b.args)
+        za.zero_block_norm_backward(dy, s, dr=dr, dh=dh, **b.args)
+        return s, y, dr, dh
+
+    first = run()
+    assert all(torch.isfinite(t).all() for t in first)
+    for _ in range(10):
+        assert all(torch.equal(a, t) for a, t in zip(run(), first))
+    b.h[77] = float("nan")
+    others = torch.arange(m, device="cuda") != 77
+    assert all(torch.equal(a[others], t[others]) and a[77].isnan().any() for a, t in zip(run(), first))

@@ -401,13 +401,17 @@ struct RowOwner {
   }
 };
 
-// Before the first sum: parts that no warp writes, and with a cluster its blocks there.
+// Before the first sum: a block's parts that no warp writes are 0; a cluster's blocks are there.  (A
+// cluster's parts are all written, by other blocks too: a 0 put here could come after those.)
 template <Share SHARE>
 __device__ __forceinline__ void begin_sums(float (*part)[RowSum<SHARE>::kParts][kSumsAtOnce]) {
-  for (int k = threadIdx.x; k < 2 * RowSum<SHARE>::kParts * kSumsAtOnce; k += blockDim.x)
-    (&part[0][0][0])[k] = 0.0f;
-  __syncthreads();
-  if constexpr (SHARE == kCluster) cluster_sync();
+  if constexpr (SHARE == kCluster) {
+    cluster_sync();
+  } else {
+    for (int k = threadIdx.x; k < 2 * RowSum<SHARE>::kParts * kSumsAtOnce; k += blockDim.x)
+      (&part[0][0][0])[k] = 0.0f;
+    __syncthreads();
+  }
 }
 
 // What norms there are, in one register.  LAYER: there may be norms of that kind.
