@@ -371,3 +371,30 @@ def test_rows_of_clusters_do_not_meet(post, kind):
     b.h[77] = float("nan")
     others = torch.arange(m, device="cuda") != 77
     assert all(torch.equal(a[others], t[others]) and a[77].isnan().any() for a, t in zip(run(), first))
+
+
+@pytest.mark.parametrize("shape", [(37, 256), (1003, 775), (4096, 2048), (700, 4100), (300, 8200), (64, 32768)])
+@pytest.mark.parametrize("kind", ["rms", "layer"])
+def test_sums_over_rows_in_fp32(shape, kind):
+    """dweight and dbias as near 64 bits as their additions allow, u = 2^-24 each.
+
+    A row's sum of squares: 4 additions of a thread's 8 columns, 5 of lanes, 16 parts of 128 and 3
+    of lanes: 28 u, and 2 u for the mean; half of it in the root, 2 ulp (4 u) for rsqrt, 1 u for the
+    product: 20 u of x standardized.  LAYER: the mean is off by 30 u of the mean magnitude.  Sums over
+    rows: those of a block, its runs of up to 2,432 blocks and 32 runs."""
+    m, d = shape
+    b = Block(m, d, "none", "none", kind)
+    s, dy = matrix(m, d, 2.0, 5, mean=0.5), matrix(m, d, 1.0, 11)
+    dw, db = (torch.full((d,), 7.0, device="cuda") for _ in range(2))
+    out = dict(dweight=dw, dbias=db) if kind == "layer" else dict(dweight=dw)
+    za.zero_block_norm_backward(dy, s, weight=b.w, kind=KINDS[kind], eps=EPS, **out)
+    s64, dy64, u = s.to(F64), dy.to(F64), 2.0 ** -24
+    standard, root = o.standardized(s64, kind, EPS)
+    rows = m / 152 + 2 + 2432 / 32 + 32
+    size = (dy64 * standard).abs().sum(0)
+    tol = (20 + rows) * u * size
+    if kind == "layer":
+        off = 30 * u * s64.abs().mean(1, keepdim=True) / root
+        tol = tol + (dy64.abs() * (off + u * s64.abs() / root)).sum(0)
+        near(db, dy64.sum(0), rows * u * dy64.abs().sum(0), "dbias")
+    near(dw, (dy64 * standard).sum(0), tol, "dweight")
