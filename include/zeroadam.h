@@ -499,7 +499,7 @@ int zero_adamw_state_f32(int32_t ntensors, const zero_adamw_tensor_t* tensors,
 /*
  * Sizes of a table of `vocab` rows of `width` elements looked up by `rows` ids,
  * and the pitches (elements) of the table (or of its gradient) and of the rows
- * looked up (or of their gradient).  1 <= width, vocab; 0 <= rows; all below 2^31.
+ * looked up (or of their gradient).  1 <= width, vocab; 0 <= rows; all below 2^31 - 1.
  */
 typedef struct {
   int64_t rows, width, vocab;

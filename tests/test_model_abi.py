@@ -274,3 +274,14 @@ def test_gates_whose_rows_overlap_are_refused(monkeypatch):
     za.zero_block_norm_forward(m, m, h=m, gate=bf(4, 24)[:, 8:16])
     za.zero_block_norm_backward(m, m, h=m, gate=m, dgate=bf(4, 24)[:, 8:16], workspace=workspace)
     assert [s.ldg for s in called] == [8, 24, 8] and called[2].lddg == 24
+
+
+def test_the_largest_sides():
+    """Sides below 2^31 - 1 are taken, and not 2^31 - 1 itself: as the header says."""
+    most = 2 ** 31 - 1
+    for kw in (dict(rows=most), dict(width=most), dict(vocab=most)):
+        assert lookup(s=embedding(**kw)) == scatter(s=embedding(**kw)) == loss(s=ce(**kw)) == CODES["ZERO_E_SHAPE"]
+    # (of no rows: checked and done, or refused for the workspace, before any CUDA call)
+    for kw in (dict(width=most - 1, vocab=1), dict(vocab=most - 1, width=1)):
+        assert lookup(s=embedding(rows=0, **kw)) == 0
+        assert loss(s=ce(rows=0, **kw), ws=None) == CODES["ZERO_E_WORKSPACE"]
