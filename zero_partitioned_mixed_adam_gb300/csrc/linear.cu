@@ -1402,7 +1402,7 @@ cudaError_t make_out_map(CUtensorMap* map, const void* p, int64_t rows, int64_t 
 
 // ----------------------------------------------------------------- products
 
-// Exponentials of a product's rows (kExponent).
+// What plans are remembered by.
 struct SizesKey {
   int64_t rows, in, out;
   int32_t which;
