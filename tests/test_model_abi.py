@@ -285,3 +285,16 @@ def test_the_largest_sides():
     for kw in (dict(width=most - 1, vocab=1), dict(vocab=most - 1, width=1)):
         assert lookup(s=embedding(rows=0, **kw)) == 0
         assert loss(s=ce(rows=0, **kw), ws=None) == CODES["ZERO_E_WORKSPACE"]
+
+
+def test_cross_entropy_workspace_of_more_than_memory_is_refused():
+    """Matrices of more elements than a call takes have no workspace, instead of one that wraps."""
+    most = 2 ** 31 - 2
+    for rows, width, vocab in ((64, most, most), (0, most, most), (most, most, 1), (64, 1 << 30, 1 << 30)):
+        for flags in (0, za.ZERO_LINEAR_BACKWARD, za.ZERO_LINEAR_BACKWARD | za.ZERO_GRAD_F32 | za.ZERO_LINEAR_ALIGNED):
+            s = ce(rows=rows, width=width, vocab=vocab)
+            assert LIB.zero_linear_cross_entropy_workspace(ctypes.byref(s), flags) == CODES["ZERO_E_SHAPE"]
+    for rows, width, vocab in ((64, 1 << 29, (1 << 30) - 1), (most, 1, most), (most, 1 << 28, 1)):
+        sizes = [za.zero_linear_cross_entropy_workspace(rows, width, vocab, f32=f32) for f32 in (True, False)]
+        # at least a copy of w and of a piece of rows
+        assert all(2 * (vocab * width + min(rows, 64) * width) <= n < 2 ** 62 for n in sizes)

@@ -427,6 +427,9 @@ int64_t zero_linear_cross_entropy_workspace(const zero_cross_entropy_t* shape, i
   const int rc = check_sides(shape->rows, shape->width, shape->vocab);
   if (rc != ZERO_OK) return rc;
   if ((flags & ~(ZERO_LINEAR_BACKWARD | ZERO_LINEAR_ALIGNED | ZERO_GRAD_F32)) != 0) return ZERO_E_LAYOUT;
+  // (as the call refuses them with their pitches, so that no size below wraps)
+  for (const int64_t n : {shape->rows, shape->vocab})
+    if (n > 0 && shape->width > kMostElements / n) return ZERO_E_SHAPE;
   return cross_entropy_workspace(*shape, flags);
 }
 
