@@ -436,3 +436,21 @@ def test_gradients_against_differences():
             slope = (moved[0] - moved[1]) / (2 * step)
             # step^2 of the third derivative, and the gradient's own rounding
             assert (grad[i, j].to(F64) - slope).abs() <= 1e-6 + 2.0 ** -6 * grad[i].to(F64).abs().max()
+
+
+@pytest.mark.parametrize("m,k,v", [(40, 64, 100), (5, 75, 33), (700, 64, 40), (300, 64, 50257), (1024, 256, 2000), (1100, 40, 32003)])
+@pytest.mark.parametrize("value", [float("inf"), float("nan")])
+def test_ignored_rows_beside_weights_that_are_not_finite(m, k, v, value):
+    """An ignored row's loss and dx are 0 whatever is in w too; with all rows ignored so are dw and total."""
+    x, w, t = matrix(m, k, 1.0, 1), matrix(v, k, 0.2, 2), targets_of(m, v, 3, 0.4)
+    t[0], t[1] = -100, 1
+    w[3, 5] = value
+    losses, total = torch.full((m,), 7.0, device="cuda"), torch.full((1,), 7.0, device="cuda")
+    dx, dw = blank(m, k), blank(v, k)
+    za.zero_linear_cross_entropy(x, w, t, losses, total, dx=dx, dw=dw)
+    ignored = t == -100
+    assert (losses[ignored] == 0).all() and (dx[ignored] == 0).all()
+    assert not torch.isfinite(dx[1]).all()     # (the weight's 0 or infinite share of a row that counts)
+    t.fill_(-100)
+    za.zero_linear_cross_entropy(x, w, t, losses, total, dx=dx, dw=dw)
+    assert not any(a.any() for a in (losses, total, dx, dw))

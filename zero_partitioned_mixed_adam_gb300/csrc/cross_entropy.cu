@@ -77,7 +77,7 @@ struct LossArgs {
   float* total;           // NULL: not wanted, or this is not the last piece
   uint16_t* held;         // [rows][ldz]: e, or dz made of it
   uint16_t* xs;           // [rows][ldxc]: f x; NULL: not wanted (never where dz is made)
-  float* factor;          // [rows]: f
+  float* factor;          // [rows]: f; where dz is made, 0 of an ignored row and else 1
   int64_t ldz;
   int32_t vec;            // x and w are read in vectors
   int32_t alone;          // rows that want another reference are made anew by their block (kOnce)
@@ -512,6 +512,8 @@ __global__ void __launch_bounds__(kFinishThreads) loss_ends_kernel(const __grid_
     if (t == -2) loss = f = NAN;
     if (thread == 0 && i < n) a.losses[from] = loss;
     if constexpr (DZ) {
+      // where ignored rows are not left out: 0 times an infinite weight would reach dx
+      if (thread == 0) a.factor[i] = t == -1 ? 0.0f : 1.0f;
       // (the pitch has room for whole vectors; an ignored row's e are not read)
       uint4* e = reinterpret_cast<uint4*>(a.held + i * a.ldz);
       constexpr int U = 4;
@@ -858,7 +860,7 @@ cudaError_t launch_cross_entropy(const CrossEntropyLaunch& L) {
     if (joined) b.s.lddw = round_up(s.width, 4);
     b.grad_f32 = L.grad_f32 || joined;
     b.accumulate = first > 0 || (L.accumulate && !joined);
-    b.row_scale = make_dz ? nullptr : a.factor;
+    b.row_scale = make_dz && !a.alone ? nullptr : a.factor;
     b.scale = L.scale == nullptr ? &a.words->share : nullptr;
     b.workspace = base + l.linear;
     b.stream = L.stream;

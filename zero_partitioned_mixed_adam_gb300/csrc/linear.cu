@@ -905,7 +905,8 @@ __global__ void __launch_bounds__(kProductThreads, 1)
       const bool fast = any && tile.part < 0 &&
                         (ROWS ? end - first >= 8 : vec && tile.col + bn <= cols);
       const bool mine_in = row0 + lane < rows;
-      const float scale = by_row && mine_in ? whole_scale * __ldcg(a.e.row_scale + row0 + lane) : whole_scale;
+      const float row_scale = by_row && mine_in ? __ldcg(a.e.row_scale + row0 + lane) : 1.0f;
+      const float scale = whole_scale * row_scale;
       const auto ask = [&](int c) {
         if constexpr (ROWS) {
           if (tile.col + c < end) part.ask(row0 + lane, tile.col + c, mine_in, first, end, lane);
@@ -919,6 +920,10 @@ __global__ void __launch_bounds__(kProductThreads, 1)
         if (scaled) {
 #pragma unroll
           for (int q = 0; q < 32; ++q) x[q] *= scale;
+          if (by_row && row_scale == 0.0f) {
+#pragma unroll
+            for (int q = 0; q < 32; ++q) x[q] = 0.0f;
+          }
         }
         if constexpr (GATHER) {
           float* to = reinterpret_cast<float*>(ring) + (c / 32 * 4 + quarter) * 32 * 32;

@@ -148,7 +148,7 @@ struct Epilogue {
   int64_t ldo;
   int32_t out_f32, accumulate;
   const float* scale;        // gradients: multiplies the sum first, one number on the device
-  const float* row_scale;    // and one for each row (bf16 alone)
+  const float* row_scale;    // and one for each row (bf16 alone); 0: the row is 0 whatever its sum is
   int32_t vec;               // every matrix's base and pitch are multiples of 16 bytes
 };
 

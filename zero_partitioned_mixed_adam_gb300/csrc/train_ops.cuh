@@ -82,7 +82,7 @@ struct LinearBackwardLaunch {
   cudaStream_t stream;
   int32_t withhold;
   const float* scale;  // of dx and dw, one number on the device; NULL: 1
-  const float* row_scale;  // of dx, a number a row; NULL: 1
+  const float* row_scale;  // of dx, a number a row (0: dx is 0, whatever is in w); NULL: 1
   // How many of the rows there are, on the device; NULL: all.  What lies behind them in dx is
   // left anyhow; in dy and x rows up to the next multiple of 128, and least_rows, are 0.
   const int32_t* rows_now;
