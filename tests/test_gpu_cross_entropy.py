@@ -454,3 +454,21 @@ def test_ignored_rows_beside_weights_that_are_not_finite(m, k, v, value):
     t.fill_(-100)
     za.zero_linear_cross_entropy(x, w, t, losses, total, dx=dx, dw=dw)
     assert not any(a.any() for a in (losses, total, dx, dw))
+
+
+@pytest.mark.parametrize("m,k,v", [(1024, 3776, 5003), (700, 4096, 4099), (300, 8200, 2051)])
+def test_wide_losses_are_fp32(m, k, v):
+    """The tensor cores cut off some 1e-9 of a sum at each step of the reduction, all one way, so that a
+    mean of many losses does not average it out.  Chains of 768 steps leave 768e-9 of the logits,
+    weighted as the loss weighs them; the loss itself is worth 2^-24 of its value, and its sum and
+    logarithm 3 times that."""
+    x, w, t = matrix(m, k, 1.0, 1), matrix(v, k, 0.02, 2), targets_of(m, v, 3)
+    ref = o.cross_entropy(x, w, t)
+    p = torch.softmax(ref[5], 1)
+    tol = 768e-9 * (p * ref[5]).sum(1).abs().mean() + 4 * 2.0 ** -24 * ref[1]
+    total = torch.zeros(1, device="cuda")
+    za.zero_linear_cross_entropy(x, w, t, None, total)
+    near(total, ref[1], tol, "alone")
+    za.zero_linear_cross_entropy(x, w, t, None, total, dx=torch.empty_like(x))
+    near(total, ref[1], tol, "with gradients")
+    check(x, w, t)

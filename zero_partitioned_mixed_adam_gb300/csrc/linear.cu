@@ -117,7 +117,14 @@ enum Kind {
   kFloat,     // fp32, alone or added to what is there
   kExponent,  // exponentials less each row's reference: their sums, and 16 bits each
   kLogSum,    // exponentials less the largest: their sums alone
+  kExponentLong, kLogSumLong,  // the same, of reductions in several chains
 };
+template <Kind KIND>
+constexpr bool kExponents = KIND == kExponent || KIND == kExponentLong;
+template <Kind KIND>
+constexpr bool kLogSums = KIND == kLogSum || KIND == kLogSumLong;
+template <Kind KIND>
+constexpr bool kChains = KIND == kFloat || KIND == kExponentLong || KIND == kLogSumLong;
 
 // A warp's 32 x 32 part of D from shared memory, where row r's 16-byte piece q
 // (columns 4q to 4q+3) lies at piece q ^ (r & 7): bank conflicts neither where a
@@ -648,12 +655,12 @@ struct Place {
 // Stages that are summed in tensor memory before the sum is taken over in fp32.
 // The tensor cores cut off what does not fit a sum's 24 bits, so a chain of
 // additions comes out too small by 1e-9 of itself for each step of the reduction
-// (1e-6 over 1,024 steps, 4e-6 over 4,096).  fp32 gradients are worth more than
-// that: their chains end after 768 steps, and the epilogue's warps add them up in
-// registers, rounding to nearest.  Results in bf16 keep one chain: its loss is
-// below a hundredth of their rounding up to 16,384 steps.
+// (1e-6 over 1,024 steps, 4e-6 over 4,096).  fp32 gradients and the logits of fp32
+// losses are worth more than that: their chains end after 768 steps, and the
+// epilogue's warps add them up in registers, rounding to nearest.  Results in bf16
+// keep one chain: its loss is below a hundredth of their rounding up to 16,384 steps.
 template <Kind KIND>
-constexpr int kChain = KIND == kFloat ? 768 / kStep : INT32_MAX;
+constexpr int kChain = kChains<KIND> ? 768 / kStep : INT32_MAX;
 
 // A wait for a chain, which may take `stages` stages: 1 s, and 10 us for each.
 __device__ __forceinline__ bool wait_for_chain(uint64_t* bar, uint32_t parity, int stages) {
@@ -710,7 +717,7 @@ __global__ void __launch_bounds__(kProductThreads, 1)
   const int unit = blockIdx.x / CG;
   const Turns turns{a.early_units, a.early_tiles, static_cast<int>(gridDim.x) / CG};
 
-  if constexpr (KIND == kExponent)
+  if constexpr (kExponents<KIND>)
     if (a.x.only_if != nullptr) {  // alike for every thread of the grid
       wait_for_predecessor();
       if (__ldcg(a.x.only_if) == 0) return;
@@ -734,7 +741,7 @@ __global__ void __launch_bounds__(kProductThreads, 1)
   if (warp == 1) tmem_alloc<CG>(tmem_at, Shape::kColumns);
   if (!a.late) wait_for_predecessor();
   launch_dependents();
-  if constexpr (KIND == kLogSum)
+  if constexpr (kLogSums<KIND>)
     if (blockIdx.x == 0 && threadIdx.x == 0) *a.x.ticket = 0;
   tc_fence_before();
   __syncthreads();
@@ -891,8 +898,8 @@ __global__ void __launch_bounds__(kProductThreads, 1)
     };
     int n = 0;
     bool ok = true;
-    ExponentPart exponents;  // of kExponent
-    LogSumPart log_sum;      // of kLogSum
+    ExponentPart exponent_part;
+    LogSumPart log_sum;
     const bool by_row = KIND == kGradient && a.e.row_scale != nullptr;
     const bool scaled = (KIND == kGradient || KIND == kFloat) && (a.e.scale != nullptr || by_row);
     const float whole_scale = scaled && a.e.scale != nullptr ? __ldcg(a.e.scale) : 1.0f;
@@ -969,44 +976,9 @@ __global__ void __launch_bounds__(kProductThreads, 1)
           __syncwarp();
         }
       };
-      if constexpr (KIND == kExponent || KIND == kLogSum) {
-        const int b = n & 1;
-        if constexpr (KIND == kExponent) {
-          exponents.begin(mine_in ? __ldcg(a.x.ref + row0 + lane) : 0.0f,
-                          mine_in ? __ldcg(a.x.target + row0 + lane) : -1);
-        } else {
-          log_sum.begin(mine_in ? column_of(a.x, row0 + lane, cols) : -1);
-        }
-        ok = wait_for_chain(&done[b], static_cast<uint32_t>((n / 2) & 1), tile.last - tile.first);
-        ++n;
-        if (!ok) break;
-        tc_fence_after();
-        const uint32_t from = lanes + b * Shape::kMaxCols;
-        uint32_t bits[32];
-        if (c_first < c_end) tmem_load32(from + c_first, bits);
-        else release(b);
-#pragma unroll 1
-        for (int c = c_first; c < c_end; c += c_step) {
-          float x[32];
-          tmem_load_wait();
-#pragma unroll
-          for (int q = 0; q < 32; ++q) x[q] = __uint_as_float(bits[q]);
-          if (c + c_step < c_end) tmem_load32(from + c + c_step, bits);
-          else release(b);
-          if (!any) continue;
-          if constexpr (KIND == kExponent)
-            exponents.put(a, reinterpret_cast<uint8_t*>(mine), x, static_cast<int>(row0), tile.col + c, cols, lane);
-          else
-            log_sum.put(x, tile.col + c, cols);
-        }
-        if (mine_in) {
-          float2* to = a.x.sums + (row0 + lane) * a.x.sum_pitch + tile.col / bn * 2 + half;
-          if constexpr (KIND == kExponent) *to = exponents.end();
-          else *to = log_sum.end();
-        }
-      } else if constexpr (KIND == kFloat) {
-        constexpr int kParts = Shape::kMaxCols / 64;
-        float sum[kParts][32];
+      // The tile's sums in registers, from chains of the reduction.
+      constexpr int kParts = Shape::kMaxCols / 64;
+      const auto add_chains = [&](float (&sum)[kParts][32]) {
         for (int step = tile.first; step < tile.last; step += kChain<KIND>, ++n) {
           const int b = n & 1;
           ok = wait_for_chain(&done[b], static_cast<uint32_t>((n / 2) & 1), kChain<KIND>);
@@ -1032,6 +1004,56 @@ __global__ void __launch_bounds__(kProductThreads, 1)
           }
           release(b);
         }
+      };
+      if constexpr (kExponents<KIND> || kLogSums<KIND>) {
+        if constexpr (kExponents<KIND>) {
+          exponent_part.begin(mine_in ? __ldcg(a.x.ref + row0 + lane) : 0.0f,
+                              mine_in ? __ldcg(a.x.target + row0 + lane) : -1);
+        } else {
+          log_sum.begin(mine_in ? column_of(a.x, row0 + lane, cols) : -1);
+        }
+        const auto put = [&](float (&x)[32], int c) {
+          if constexpr (kExponents<KIND>)
+            exponent_part.put(a, reinterpret_cast<uint8_t*>(mine), x, static_cast<int>(row0), tile.col + c, cols, lane);
+          else
+            log_sum.put(x, tile.col + c, cols);
+        };
+        if constexpr (kChains<KIND>) {
+          float sum[kParts][32];
+          add_chains(sum);
+          if (!ok) break;
+#pragma unroll
+          for (int i = 0; i < kParts; ++i)
+            if (any && c_first + c_step * i < c_end) put(sum[i], c_first + c_step * i);
+        } else {
+          const int b = n & 1;
+          ok = wait_for_chain(&done[b], static_cast<uint32_t>((n / 2) & 1), tile.last - tile.first);
+          ++n;
+          if (!ok) break;
+          tc_fence_after();
+          const uint32_t from = lanes + b * Shape::kMaxCols;
+          uint32_t bits[32];
+          if (c_first < c_end) tmem_load32(from + c_first, bits);
+          else release(b);
+#pragma unroll 1
+          for (int c = c_first; c < c_end; c += c_step) {
+            float x[32];
+            tmem_load_wait();
+#pragma unroll
+            for (int q = 0; q < 32; ++q) x[q] = __uint_as_float(bits[q]);
+            if (c + c_step < c_end) tmem_load32(from + c + c_step, bits);
+            else release(b);
+            if (any) put(x, c);
+          }
+        }
+        if (mine_in) {
+          float2* to = a.x.sums + (row0 + lane) * a.x.sum_pitch + tile.col / bn * 2 + half;
+          if constexpr (kExponents<KIND>) *to = exponent_part.end();
+          else *to = log_sum.end();
+        }
+      } else if constexpr (KIND == kFloat) {
+        float sum[kParts][32];
+        add_chains(sum);
         if (ok) {
 #pragma unroll
           for (int i = 0; i < kParts; ++i)
@@ -1875,6 +1897,23 @@ bool whole_in_place(const zero_linear_t& s, bool dw) {
   return s.in % 32 == 0 && plan.splits == 1;
 }
 
+namespace {
+// Features beyond which a logit's sum is taken in chains, as the loss is fp32: up to there one chain
+// takes less off it than an ulp (a mean loss of 5 from 64 bits, in one chain and in chains: 1024
+// features 3e-7, 2e-7; 2048 1.4e-6, 5e-7; 4096 5.4e-6, 6e-7; 8192 2.4e-5, 1.7e-6). The chains cost
+// 2048 x 1024 -> 50257 120 us instead of 119, 2048 x 4096 -> 20000 200 instead of 195.
+constexpr int64_t kWide = 1024;
+
+template <Kind EXPONENT, Kind LOG_SUM>
+cudaError_t launch_exponent_kind(const Product& p, bool alone, Pending* w, Chain* chain) {
+  if (alone)
+    return w->plan.cg == 2 ? launch_shape<2, false, false, LOG_SUM, false>(p, w, chain)
+                           : launch_shape<1, false, false, LOG_SUM, false>(p, w, chain);
+  return w->plan.cg == 2 ? launch_shape<2, false, false, EXPONENT, false>(p, w, chain)
+                         : launch_shape<1, false, false, EXPONENT, false>(p, w, chain);
+}
+}  // namespace
+
 int64_t exponent_parts(int64_t rows, int64_t vocab, int64_t width) {
   const int bn = plan_exponents(rows, vocab, width).bn;
   return (vocab + bn - 1) / bn * 2;
@@ -1907,11 +1946,9 @@ cudaError_t launch_exponents(const ExponentLaunch& L) {
     if (e != cudaSuccess) return e;
   }
   Chain chain{L.stream};
-  if (L.of.targets != nullptr)
-    return w.plan.cg == 2 ? launch_shape<2, false, false, kLogSum, false>(p, &w, &chain)
-                          : launch_shape<1, false, false, kLogSum, false>(p, &w, &chain);
-  return w.plan.cg == 2 ? launch_shape<2, false, false, kExponent, false>(p, &w, &chain)
-                        : launch_shape<1, false, false, kExponent, false>(p, &w, &chain);
+  const bool alone = L.of.targets != nullptr;
+  if (L.width > kWide) return launch_exponent_kind<kExponentLong, kLogSumLong>(p, alone, &w, &chain);
+  return launch_exponent_kind<kExponent, kLogSum>(p, alone, &w, &chain);
 }
 
 int64_t linear_workspace(const zero_linear_t& s, int32_t flags) {
