@@ -572,7 +572,8 @@ typedef struct {
  * Sums are fp32.  The products' operands are bf16 (the tensor cores' type): the
  * exponentials, and then dz, each rounded once; of more than 2^25 values (rows *
  * vocab) the exponentials alone, and x times its row's factor for dw, whose rounding
- * averages out over a token's rows.  Exponentials below exp(-87) of the target's (of the
+ * averages out over a token's rows (the factor is within 2^-9 of its value, so that
+ * the target's term is exact).  Exponentials below exp(-87) of the target's (of the
  * largest, in a row whose loss is above 44) are 0 in dz.  Rows that are ignored are
  * left out of the products.  The loss alone takes other kernels than the loss with
  * gradients, and may differ from it in its last bits.  Rows go in pieces whose

@@ -16,8 +16,8 @@ namespace {
 
 constexpr int kMostThreads = 512, kMostWarps = kMostThreads / 32, kMostCluster = 8;
 // Rows under way.  More of them make the forward pass slower where HBM bounds it (32768 x 2048 with
-// 2, 3, 4: 83, 96, 98 us), fewer the backward pass, which its instructions bound (2, 3, 4 without a
-// norm after the block: 119, 110, 85 us).
+// 2, 3, 4: 83, 96, 98 us), fewer the backward pass (2, 3, 4 without a norm after the block: 119, 110,
+// 85 us).
 constexpr int kForwardStages = 2, kBackwardStages = 4;
 constexpr int kSumsAtOnce = 8;
 
