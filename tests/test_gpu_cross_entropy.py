@@ -472,3 +472,22 @@ def test_wide_losses_are_fp32(m, k, v):
     za.zero_linear_cross_entropy(x, w, t, None, total, dx=torch.empty_like(x))
     near(total, ref[1], tol, "with gradients")
     check(x, w, t)
+
+
+@pytest.mark.parametrize("m,v", [(500, 2), (500, 3), (500, 5), (2000, 8), (900, 20), (2000, 64), (500, 65), (300, 200)])
+def test_each_gradient_of_a_logit(m, v):
+    """dz itself, which rows of the unit matrix in w hand on to dx: of the target within one rounding to bf16,
+    2^-8, of the others within two, theirs and their exponentials', however few columns share a row."""
+    gen = torch.Generator("cuda").manual_seed(v)
+    slope = torch.randn(v, device="cuda", generator=gen).to(BF)
+    x, w = blank(m, v + 1), blank(v, v + 1)
+    x.zero_()
+    x[:, 0] = torch.randn(m, device="cuda", generator=gen) * 3.0
+    w.copy_(torch.cat([slope[:, None], torch.eye(v, device="cuda", dtype=BF)], 1))
+    t = targets_of(m, v, 3)
+    dx = blank(m, v + 1)
+    za.zero_linear_cross_entropy(x, w, t, dx=dx, scale=torch.ones(m, device="cuda"))
+    dz = o.cross_entropy(x, w, t, scale=torch.ones(m, device="cuda"))[4]
+    half = torch.full_like(dz, 2.0 ** -7).scatter_(1, t[:, None], 2.0 ** -8)
+    # (the exponentials' own error is 2^-17, as in tolerances; twice that for the sum's)
+    near(dx[:, 1:], dz, (half * 1.01 + 3 * 2.0 ** -17) * dz.abs() + 1e-30, "dz")

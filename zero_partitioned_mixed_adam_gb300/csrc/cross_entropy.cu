@@ -115,6 +115,12 @@ __device__ __forceinline__ float warp_sum(float x) {
   return x;
 }
 
+__device__ __forceinline__ float warp_max(float x) {
+#pragma unroll
+  for (int k = 16; k > 0; k /= 2) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, k));
+  return x;
+}
+
 // Where the rows that are not ignored go: one after the other, so that the products have no
 // others to do.  One block: a warp looks through a run of rows, once to count and once to
 // write (8,192 rows: 4 us).
@@ -518,29 +524,40 @@ __global__ void __launch_bounds__(kFinishThreads) loss_ends_kernel(const __grid_
       uint4* e = reinterpret_cast<uint4*>(a.held + i * a.ldz);
       constexpr int U = 4;
       const uint32_t vectors = static_cast<uint32_t>((a.vocab + 7) / 8);
-      // Where few columns share a row, e's roundings do not average out: the others' factor is
-      // what makes their sum, as rounded, S' again (dw of 100 rows, 2 columns: 1.4 times as far
-      // from the exact one as its own rounding puts it, without this 1.9; 8 columns 1.25, 1.3; 8192 x
-      // 64 -> 3 42 us instead of 40, but 4096 x 768 -> 4000 96 instead of 90, for nothing).
-      float others = f;
+      // Where few columns share a row, e's roundings do not average out.  One of at least half of their
+      // sum takes what makes the sum, as rounded, S' again: that is at most another rounding of its own,
+      // as the others weigh no more than it; with a factor for all, small ones could be off by two
+      // more.  (100 rows, 2 columns: dx and dw 1.4 times as far from 64 bits as their own rounding puts
+      // them, without this 1.55; 12 x 2048 -> 2 1.25, at worst 1.8, and 1.5, 2.8.)
       if (a.vocab <= kFewColumns) {
-        float held = 0.0f;
-        for (uint32_t j = thread; t >= 0 && j < vectors; j += kThreads) {
-          float x[8];
-          bf16x8(__ldcg(e + j), x);
+        if (thread >= 32) continue;  // (its vectors are its first warp's lanes')
+        const uint32_t j = thread, at = static_cast<uint32_t>(t) - 8 * j;
+        float x[8] = {}, held = 0.0f, most = 0.0f;
+        if (t != -1 && j < vectors) bf16x8(__ldcg(e + j), x);
 #pragma unroll
-          for (int c = 0; c < 8; ++c) held += 8 * j + c < a.vocab ? x[c] : 0.0f;
+        for (int c = 0; c < 8; ++c) {
+          if (8 * j + c >= a.vocab) x[c] = 0.0f;  // (nothing was written there)
+          held += x[c];
+          most = fmaxf(most, x[c]);
         }
         held = warp_sum(held);
-        if constexpr (WARPS > 1) {
-          __syncthreads();
-          if (lane == 0) part[warp].x = held;
-          __syncthreads();
-          held = 0.0f;
+        const float top_e = warp_max(most);
+        const uint32_t those = __ballot_sync(0xffffffffu, most == top_e);
+        if (top_e > 0.0f && 2.0f * top_e >= held && __ffs(those) - 1 == lane) {
+          bool done = false;
 #pragma unroll
-          for (int k = 0; k < kFinishWarps; ++k) held += part[k].x;
+          for (int c = 0; c < 8; ++c)
+            if (!done && x[c] == top_e) {
+              x[c] += sum - held;
+              done = true;
+            }
         }
-        if (held > 0.0f) others = f * (sum / held);
+        if (j < vectors) {
+#pragma unroll
+          for (int c = 0; c < 8; ++c) x[c] = t == -1 ? 0.0f : at == c ? -(f * sum) : f * x[c];
+          e[j] = to_bf16x8(x);
+        }
+        continue;
       }
       for (uint32_t j0 = thread; j0 < vectors; j0 += U * kThreads) {
         uint4 v[U];
@@ -554,7 +571,7 @@ __global__ void __launch_bounds__(kFinishThreads) loss_ends_kernel(const __grid_
           float x[8] = {};
           if (t != -1) bf16x8(v[u], x);
 #pragma unroll
-          for (int c = 0; c < 8; ++c) x[c] = t == -1 ? 0.0f : at == c ? -(f * sum) : others * x[c];
+          for (int c = 0; c < 8; ++c) x[c] = t == -1 ? 0.0f : at == c ? -(f * sum) : f * x[c];
           e[j] = to_bf16x8(x);
         }
       }
