@@ -491,3 +491,17 @@ def test_each_gradient_of_a_logit(m, v):
     half = torch.full_like(dz, 2.0 ** -7).scatter_(1, t[:, None], 2.0 ** -8)
     # (the exponentials' own error is 2^-17, as in tolerances; twice that for the sum's)
     near(dx[:, 1:], dz, (half * 1.01 + 3 * 2.0 ** -17) * dz.abs() + 1e-30, "dz")
+
+
+def test_withheld_copies_of_wide_rows_are_reported():
+    """Waits for one of several chains run out too; the next call is right."""
+    m, k, v = 40, 1100, 515
+    x, w, t = matrix(m, k, 1.0, 1), matrix(v, k, 0.05, 2), targets_of(m, v, 3)
+    for kw in ({}, dict(dx=blank(m, k))):
+        za.test_withhold_copies(True)
+        try:
+            za.zero_linear_cross_entropy(x, w, t, torch.zeros(m, device="cuda"), **kw)
+            assert za.device_status() != za.ZERO_OK
+        finally:
+            za.test_withhold_copies(False)
+    check(x, w, t)
